@@ -380,6 +380,121 @@ tt_status tt_emb_forward_noalloc(int64_t num_embeddings, const int64_t p[3], con
                                  int64_t num_bags, const float* per_sample_weights_dev, tt_pool mode,
                                  float* out_dev, int32_t* err_dev, tt_stream stream);
 
+/*
+ * Vocabulary head: losses over the scores of rows against a whole table,
+ *     z[n][v] = sum_d hidden[n][d] weight[v][d],
+ * without an [N][V] array of them.  weight is any dense table: an output
+ * projection, or the rows of a TT table (tt_emb_forward with one bag per row, whose
+ * backward pass then takes the rows' gradient to the cores).  These calls need no
+ * handle; every buffer is the caller's, and every call is asynchronous on `stream`
+ * and allocates nothing (so it may be captured in a CUDA graph).
+ */
+typedef enum { TT_F32 = 0, TT_BF16 = 1, TT_F16 = 2 } tt_dtype;
+
+#define TT_HEAD_MAX_ROWS 16777216    /* rows N */
+#define TT_HEAD_MAX_VOCAB 1073741824 /* table rows V */
+#define TT_HEAD_MAX_DIM 65536        /* width D */
+#define TT_HEAD_MAX_TEACHER 1024     /* teacher entries per row */
+
+typedef struct {
+    const void* hidden_dev; /* [rows][dim], rows hidden_stride elements apart */
+    const void* weight_dev; /* [vocab][dim], rows weight_stride elements apart */
+    int64_t rows, vocab;
+    int64_t hidden_stride, weight_stride; /* >= dim; elements of a row are contiguous */
+    int32_t dim;
+    int32_t dtype; /* tt_dtype of hidden and weight and of their gradients */
+} tt_head;
+
+/*
+ * Bytes of workspace that a forward (backward = 0) or backward (1) call on `head`
+ * needs; teacher_k: entries per row of the distillation calls, 1 for cross entropy.
+ * The size depends on the shapes, the type, the device and on whether the rows are
+ * 16-byte aligned (rows that are not, and fp32 rows, are copied).  The workspace is
+ * 256-byte aligned and holds nothing between calls.  -1 for a head that the calls
+ * would refuse.
+ */
+int64_t tt_emb_head_workspace(const tt_head* head, int32_t teacher_k, int32_t backward);
+
+/*
+ * Softmax cross entropy.
+ *   targets_dev  int64 [rows]; a row whose target is ignore_index has loss 0 and
+ *                gives no gradient, whatever its hidden row and grad_loss hold
+ *   loss_dev     float [rows]: lse[n] - z[n][targets[n]]
+ *   lse_dev      float [rows]: log sum_v exp(z[n][v]), of every row
+ *   err_dev      int32 or NULL; the call ORs in 1 for a target that is neither
+ *                ignore_index nor in [0, vocab) (its row counts as ignored) and 4
+ *                for a device wait that gave up (results undefined); the caller
+ *                clears it
+ * Backward: with lse from the forward call and grad_loss_dev float [rows] the
+ * gradient of each row's loss,
+ *   dz[n][v] = grad_loss[n] (exp(z[n][v] - lse[n]) - [v = targets[n]]),
+ *   grad_hidden [rows][dim] = dz weight, grad_weight [vocab][dim] = dz^T hidden,
+ * both written whole, contiguous, of the head's type.  The sums are taken in fp32
+ * in an order that is fixed for given sizes: results repeat bit for bit.
+ * Returns TT_ERR_ARG (null pointers, unknown type, misaligned or short workspace),
+ * TT_ERR_SHAPE (limits above, stride < dim), TT_ERR_CUDA.
+ */
+tt_status tt_emb_xent_forward(const tt_head* head, const int64_t* targets_dev, int64_t ignore_index, float* loss_dev,
+                              float* lse_dev, int32_t* err_dev, void* ws_dev, size_t ws_bytes, tt_stream stream);
+tt_status tt_emb_xent_backward(const tt_head* head, const int64_t* targets_dev, int64_t ignore_index,
+                               const float* lse_dev, const float* grad_loss_dev, void* grad_hidden_dev,
+                               void* grad_weight_dev, int32_t* err_dev, void* ws_dev, size_t ws_bytes,
+                               tt_stream stream);
+
+/*
+ * Distillation from a teacher's top logits.  Each row has teacher_k entries
+ * (ids_dev int64 [rows][teacher_k], logits_dev float [rows][teacher_k]).  An entry
+ * whose id is negative does not count, whatever its logit holds, nor does one whose
+ * logit is -inf; an id >= vocab does not count and sets 1 in err_dev.  Over the
+ * entries that count, q = softmax(logit / T); with lse[n] = log sum_v exp(z[n][v] / T)
+ *   loss[n] = T^2 sum_k q[n][k] (log q[n][k] - z[n][id_k] / T + lse[n]),
+ * the Kullback-Leibler divergence of the student from the teacher's renormalised
+ * entries, scaled by T^2.  A row with no entry that counts has loss 0 and gives no
+ * gradient.  Entries of a row with the same id add up in the gradient; in the loss
+ * each keeps its own log q.  T in [1e-4, 1e4].  The teacher gets no gradient.
+ * Backward: dz[n][v] = grad_loss[n] T (exp(z[n][v] / T - lse[n]) - sum of q of the
+ * row's entries with id v), and the gradients as for cross entropy.  Errors as there.
+ */
+tt_status tt_emb_distill_forward(const tt_head* head, const int64_t* ids_dev, const float* logits_dev,
+                                 int32_t teacher_k, float temperature, float* loss_dev, float* lse_dev,
+                                 int32_t* err_dev, void* ws_dev, size_t ws_bytes, tt_stream stream);
+tt_status tt_emb_distill_backward(const tt_head* head, const int64_t* ids_dev, const float* logits_dev,
+                                  int32_t teacher_k, float temperature, const float* lse_dev,
+                                  const float* grad_loss_dev, void* grad_hidden_dev, void* grad_weight_dev,
+                                  int32_t* err_dev, void* ws_dev, size_t ws_bytes, tt_stream stream);
+
+/*
+ * Bound, in nanoseconds, of each wait inside the head's kernels (for their own
+ * copies and MMAs; default 2e9).  Process-wide, from the next call on; 0 makes a wait
+ * that is not already over give up (a test of that path).  A wait that gives up sets
+ * 4 in err_dev; the call then ends with undefined results and leaves nothing running.
+ */
+tt_status tt_emb_head_set_wait_limit(uint64_t ns);
+
+/*
+ * Scores against a table held in 4 bits (serving):
+ *   out[m][v] = sum_d scale[v][d / group] (code[v][d] - 8) x[m][d]
+ * packed_dev: two codes to a byte, the even column in the low half, a row of
+ * ceil(dim / 32) * 16 bytes (padding columns hold 8, which stands for 0), 16-byte
+ * aligned.  scales_dev: bf16 bits [vocab][ceil(dim / group)].  group: 32, 64 or 128.
+ *
+ * tt_emb_q4_quantize lays a dense table out so: per group scale = bf16(max |w| / 7),
+ *   code = round(w / scale) held within [-8, 7], plus 8; an all-zero group gets scale
+ *   0.  weight_dev [vocab][dim] of `dtype` (tt_dtype), rows weight_stride apart.
+ * tt_emb_q4_matvec: x_dev [rows][dim] of `dtype`, rows x_stride apart; out_dev float
+ *   [rows][vocab], written whole.  Every product is exact and sums are fp32.  Meant for
+ *   few rows: each 32 of them read the table once.
+ * Both are asynchronous on `stream` and allocate nothing.  Return TT_ERR_ARG (null or
+ * misaligned pointers, unknown type), TT_ERR_SHAPE (limits, group, stride), TT_ERR_CUDA.
+ */
+#define TT_Q4_MAX_ROWS 65536
+tt_status tt_emb_q4_quantize(const void* weight_dev, int64_t weight_stride, int64_t vocab, int32_t dim,
+                             int32_t dtype, int32_t group, uint8_t* packed_dev, uint16_t* scales_dev,
+                             tt_stream stream);
+tt_status tt_emb_q4_matvec(const void* x_dev, int64_t x_stride, int32_t rows, int32_t dtype,
+                           const uint8_t* packed_dev, const uint16_t* scales_dev, int64_t vocab, int32_t dim,
+                           int32_t group, float* out_dev, tt_stream stream);
+
 /* Static description of a status code; never NULL. */
 const char* tt_emb_status_string(tt_status s);
 

@@ -71,6 +71,17 @@ __all__ = [
     "EXPORTED_SYMBOLS",
     "TTEmbeddingBag",
     "TableBatchedTTEmbeddingBag",
+    "tt_emb_head_workspace",
+    "tt_emb_xent_forward",
+    "tt_emb_xent_backward",
+    "tt_emb_distill_forward",
+    "tt_emb_distill_backward",
+    "tt_emb_head_set_wait_limit",
+    "tt_emb_q4_quantize",
+    "tt_emb_q4_matvec",
+    "vocab_cross_entropy",
+    "vocab_distillation",
+    "Q4Table",
 ]
 
 TT_OK, TT_ERR_ARG, TT_ERR_SHAPE, TT_ERR_INDEX, TT_ERR_CUDA, TT_ERR_STATE, TT_ERR_TIMEOUT, TT_ERR_NOMEM, TT_ERR_BOUNDS = range(9)
@@ -105,6 +116,14 @@ EXPORTED_SYMBOLS = (
     "tt_emb_forward_noalloc",
     "tt_emb_apply_gradients",
     "tt_emb_set_wait_limit",
+    "tt_emb_head_workspace",
+    "tt_emb_xent_forward",
+    "tt_emb_xent_backward",
+    "tt_emb_distill_forward",
+    "tt_emb_distill_backward",
+    "tt_emb_head_set_wait_limit",
+    "tt_emb_q4_quantize",
+    "tt_emb_q4_matvec",
 )
 
 
@@ -179,6 +198,15 @@ def load_library():
                                                       vp, ctypes.c_int, vp, vp, vp]),
             "tt_emb_apply_gradients": (ctypes.c_int, [vp, i32, f32, f32, ctypes.POINTER(vp), ctypes.POINTER(vp), vp]),
             "tt_emb_set_wait_limit": (ctypes.c_int, [vp, ctypes.c_uint32]),
+            "tt_emb_head_workspace": (i64, [vp, i32, i32]),
+            "tt_emb_xent_forward": (ctypes.c_int, [vp, vp, i64, vp, vp, vp, vp, ctypes.c_size_t, vp]),
+            "tt_emb_xent_backward": (ctypes.c_int, [vp, vp, i64, vp, vp, vp, vp, vp, vp, ctypes.c_size_t, vp]),
+            "tt_emb_distill_forward": (ctypes.c_int, [vp, vp, vp, i32, f32, vp, vp, vp, vp, ctypes.c_size_t, vp]),
+            "tt_emb_distill_backward": (ctypes.c_int, [vp, vp, vp, i32, f32, vp, vp, vp, vp, vp, vp,
+                                                       ctypes.c_size_t, vp]),
+            "tt_emb_head_set_wait_limit": (ctypes.c_int, [ctypes.c_uint64]),
+            "tt_emb_q4_quantize": (ctypes.c_int, [vp, i64, i64, i32, i32, i32, vp, vp, vp]),
+            "tt_emb_q4_matvec": (ctypes.c_int, [vp, i64, i32, i32, vp, vp, i64, i32, i32, vp, vp]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)
@@ -781,3 +809,20 @@ class TableBatchedTTEmbeddingBag(_TTBase):
 
     def forward(self, input, offsets, per_sample_weights=None, mode: str = "sum", include_last_offset=True):
         return self._run(input, offsets, per_sample_weights, mode, include_last_offset)
+
+
+# ---------------------------------------------------------------- vocabulary head
+
+from .head import (  # noqa: E402  (uses the names above)
+    Q4Table,
+    tt_emb_distill_backward,
+    tt_emb_distill_forward,
+    tt_emb_head_set_wait_limit,
+    tt_emb_head_workspace,
+    tt_emb_q4_matvec,
+    tt_emb_q4_quantize,
+    tt_emb_xent_backward,
+    tt_emb_xent_forward,
+    vocab_cross_entropy,
+    vocab_distillation,
+)

@@ -1,0 +1,1219 @@
+// tt_head.cu -- the vocabulary head: softmax cross entropy and distillation from a
+// teacher's top logits over z[n, v] = <hidden[n], weight[v]>, forward and backward,
+// without an N x V array of logits.
+//
+//   lse[n]  = log sum_v exp(z[n, v] / T)
+//   xent    loss[n] = lse[n] - z[n, t_n]                                   (T = 1)
+//   distill q[n, k] = softmax over the row's entries of teacher_logit / T,
+//           loss[n] = T^2 sum_k q[n, k] (log q[n, k] - z[n, id_k] / T + lse[n])
+//   dz[n, v] = g_n T (exp(z[n, v] / T - lse[n]) - q[n, v])    (q: one-hot for xent)
+//   dhidden = dz weight,  dweight = dz^T hidden
+//
+// Forward: one product kernel keeps, per row, a running maximum and sum of the
+// exponentials of its column tiles and writes one pair per strip of tiles; a row
+// kernel joins them and takes the target scores as fp32 dot products.
+// Backward: the table is taken in pieces of the vocabulary.  For each, the scores
+// are formed again, dz of the piece is written in 16 bits (k_head_fix then writes
+// the entries that have a target), and two products read it: dweight of the piece
+// and the piece's share of dhidden.  The only array of N x (vocabulary piece) is
+// that dz (at most kDzBytes, or 1,024 columns).
+//
+// Types.  bf16 and f16 inputs go to the tensor cores as they are.  An fp32 input x
+// is split as x 2^e = hi + lo with hi, lo in f16 (e a power-of-two scale that puts
+// the largest magnitude near 2^14) and a product is taken as hi hi + hi lo + lo hi,
+// so 22 bits of each operand enter, with fp32 accumulation; lo lo (2^-22 of the
+// product and below) is dropped.  dz is rounded to the inputs' 16-bit type before
+// the two gradient products (relative 2^-9 or 2^-12 an entry, independent errors,
+// the size of the gradients' own final rounding), and split like an input for fp32.
+#include <math.h>
+#include <stdio.h>
+
+#include "tt_head.cuh"
+
+namespace ttemb {
+
+constexpr int kGemmThreads = 384;  // warp 0: TMA, 1: MMA, 2: tensor memory, 4..11: epilogue
+constexpr int kEpiWarps = 8;
+constexpr int kBK = 64;            // K depth of a stage: one 128-byte swizzled row
+constexpr int64_t kDzBytes = 256ll << 20;  // dz of one vocabulary piece
+constexpr int kMaxTeacher = TT_HEAD_MAX_TEACHER;
+
+enum Epi { kEpiStats = 0, kEpiDz = 1, kEpiOut = 2 };
+
+struct GemmArgs {
+    int64_t M, N;      // valid rows and columns of the product
+    int mtiles, ntiles;
+    int strip;         // column tiles per unit (kEpiStats), else 1
+    int nstrips;
+    int splits;        // K ranges (kEpiOut), else 1
+    int chunks;        // K chunks of 64
+    int nseg;          // 1, or 3: hi hi, hi lo, lo hi
+    int64_t units;
+    int fmt;           // 16-bit type of the operands: 0 f16, 1 bf16
+    uint64_t wait_ns;
+    int* err;
+    // scales: exponents of the operands' power-of-two scales come from these bits
+    const uint32_t* amax_a;
+    const uint32_t* amax_b;
+    const int* row_exp;  // per-row exponent of A (forward), else null
+    float ctemp;         // log2(e) / T
+    // kEpiStats
+    float2* part;        // [M][2 nstrips] (maximum in log2 units, sum)
+    // kEpiDz
+    const float* lse2;
+    const float* rowscale;
+    uint16_t* dz;        // [pieces][M][dz_pitch]
+    int64_t dz_pitch, dz_piece;
+    int dz_split;
+    // kEpiOut
+    void* out;           // [M][ldo] of out_type, or null: partial sums
+    int64_t ldo;
+    int out_type;        // tt_dtype
+    int vec;             // rows of out are 16-byte aligned
+    float* partial;      // [splits][M][pp]
+    int64_t pp;
+    int accumulate;
+};
+
+__device__ __forceinline__ int amax_exp(const uint32_t* p) { return p ? scale_exp(*p) : 0; }
+
+template <int BN>
+struct GemmShape {
+    static constexpr int kStages = BN == 256 ? 4 : (BN == 128 ? 6 : 8);
+    static constexpr uint32_t kA = 128 * 128, kB = BN * 128;
+    static constexpr uint32_t kStage = kA + kB;
+    static constexpr size_t kSmem = (size_t)kStages * kStage + 1024;
+};
+
+__device__ __forceinline__ void store_vec(void* out, int64_t at, const float* v, int type) {
+    // 8 consecutive elements, 16-byte aligned
+    if (type == TT_F32) {
+        float4* o = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
+        o[0] = make_float4(v[0], v[1], v[2], v[3]);
+        o[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+        const int fmt = type == TT_BF16;
+        uint4 u;
+        u.x = pack16(v[0], v[1], fmt);
+        u.y = pack16(v[2], v[3], fmt);
+        u.z = pack16(v[4], v[5], fmt);
+        u.w = pack16(v[6], v[7], fmt);
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at) = u;
+    }
+}
+__device__ __forceinline__ void store_one(void* out, int64_t at, float v, int type) {
+    if (type == TT_F32)
+        static_cast<float*>(out)[at] = v;
+    else if (type == TT_BF16)
+        static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(v);
+    else
+        static_cast<__half*>(out)[at] = __float2half_rn(v);
+}
+
+// C[m, n] = sum_k A[m, k] B[n, k] by 128 x BN tiles, a persistent block per SM: one
+// thread feeds a ring of stages by TMA, one issues the MMAs into one of two
+// accumulators in tensor memory, eight warps read the other out (warps 4..7 the
+// left half of its columns, 8..11 the right half, a row per lane).
+template <int BN, bool AMN, bool BMN, int EPI>
+__global__ void __launch_bounds__(kGemmThreads, 1)
+    k_head_gemm(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
+                const __grid_constant__ GemmArgs a) {
+    using S = GemmShape<BN>;
+    extern __shared__ uint8_t raw[];
+    __shared__ uint64_t full[S::kStages], empty[S::kStages], accfull[2], accempty[2], drain;
+    __shared__ uint32_t tmem_slot;
+    __shared__ int gave_up_s;
+    volatile int* gave_up = &gave_up_s;
+    const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S::kStages; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&accfull[i], 1);
+            mbar_init(&accempty[i], kEpiWarps);
+        }
+        mbar_init(&drain, 1);
+        gave_up_s = 0;
+    }
+    if (warp == 2) tc_alloc(&tmem_slot, 2 * BN);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    uint32_t it = 0;  // stages fed (TMA thread) or consumed (MMA thread)
+    bool ok = true;
+
+    // unit -> row tile, first column tile, tiles, K range
+    auto unit = [&](int64_t u, int& m, int& n0, int& n1, int& kb, int& ke, int& split) {
+        if (EPI == kEpiOut) {  // column tiles fastest: blocks that run together share rows of A
+            const int64_t tiles = (int64_t)a.mtiles * a.ntiles;
+            split = (int)(u / tiles);
+            const int64_t t = u - split * tiles;
+            m = (int)(t / a.ntiles);
+            n0 = (int)(t - (int64_t)m * a.ntiles);
+            n1 = n0 + 1;
+            kb = (int)((int64_t)a.chunks * split / a.splits);
+            ke = (int)((int64_t)a.chunks * (split + 1) / a.splits);
+        } else {  // row tiles fastest: blocks that run together share rows of the table
+            const int s = (int)(u / a.mtiles);
+            m = (int)(u - (int64_t)s * a.mtiles);
+            n0 = s * a.strip;
+            n1 = min(n0 + a.strip, a.ntiles);
+            kb = 0;
+            ke = a.chunks;
+            split = s;
+        }
+    };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            for (int64_t u = blockIdx.x; ok && u < a.units; u += gridDim.x) {
+                int m, n0, n1, kb, ke, split;
+                unit(u, m, n0, n1, kb, ke, split);
+                for (int n = n0; ok && n < n1; ++n)
+                    for (int seg = 0; ok && seg < a.nseg; ++seg) {
+                        const int za = seg == 2, zb = seg == 1;
+                        for (int kc = kb; kc < ke; ++kc, ++it) {
+                            const uint32_t st = it % S::kStages;
+                            if (!head_wait(&empty[st], ((it / S::kStages) & 1) ^ 1, a.wait_ns, gave_up)) {
+                                ok = false;
+                                break;
+                            }
+                            const uint32_t sa = base + st * S::kStage, sb = sa + S::kA;
+                            bulk_expect(&full[st], S::kStage);
+                            if (AMN) {
+                                tma_load3(sa, &mapA, m * 128, kc * kBK, za, &full[st]);
+                                tma_load3(sa + 8192, &mapA, m * 128 + 64, kc * kBK, za, &full[st]);
+                            } else {
+                                tma_load3(sa, &mapA, kc * kBK, m * 128, za, &full[st]);
+                            }
+                            if (BMN) {
+#pragma unroll
+                                for (int j = 0; j < BN / 64; ++j)
+                                    tma_load3(sb + j * 8192, &mapB, n * BN + j * 64, kc * kBK, zb, &full[st]);
+                            } else {
+                                tma_load3(sb, &mapB, kc * kBK, n * BN, zb, &full[st]);
+                            }
+                        }
+                    }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            const uint32_t idesc = idesc_f16(128, BN, a.fmt, AMN, BMN);
+            uint32_t tile = 0;
+            for (int64_t u = blockIdx.x; ok && u < a.units; u += gridDim.x) {
+                int m, n0, n1, kb, ke, split;
+                unit(u, m, n0, n1, kb, ke, split);
+                for (int n = n0; ok && n < n1; ++n, ++tile) {
+                    const uint32_t buf = tile & 1;
+                    if (!head_wait(&accempty[buf], ((tile >> 1) & 1) ^ 1, a.wait_ns, gave_up)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t d = tmem + buf * BN;
+                    const int steps = (ke - kb) * a.nseg;
+                    for (int c = 0; c < steps; ++c, ++it) {
+                        const uint32_t st = it % S::kStages;
+                        if (!head_wait(&full[st], (it / S::kStages) & 1, a.wait_ns, gave_up)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t sa = base + st * S::kStage;
+                        const uint64_t da = desc_sw128(sa, AMN), db = desc_sw128(sa + S::kA, BMN);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mma_f16(d, da + (uint64_t)(k * (AMN ? 2048 : 32) >> 4),
+                                    db + (uint64_t)(k * (BMN ? 2048 : 32) >> 4), idesc, c > 0 || k > 0);
+                        tc_commit(&empty[st]);
+                    }
+                    if (ok) tc_commit(&accfull[buf]);
+                }
+            }
+        }
+    } else if (warp >= 4) {
+        const int half = warp >= 8, quad = warp & 3;
+        const int r = quad * 32 + lane;
+        float c = 0.f, s1 = 1.f, s2 = 1.f;
+        if (EPI == kEpiOut) {
+            s1 = exp2i(-amax_exp(a.amax_a));
+            s2 = exp2i(-amax_exp(a.amax_b));
+        } else {
+            c = a.ctemp * exp2i(-amax_exp(a.amax_a)) * exp2i(-amax_exp(a.amax_b));
+        }
+        uint32_t tile = 0;
+        for (int64_t u = blockIdx.x; ok && u < a.units; u += gridDim.x) {
+            int m, n0, n1, kb, ke, split;
+            unit(u, m, n0, n1, kb, ke, split);
+            const int64_t row = (int64_t)m * 128 + r;
+            const bool in = row < a.M;
+            float run_m = -INFINITY, run_s = 0.f, cr = c, l2 = 0.f, rs = 0.f;
+            if (EPI == kEpiStats && a.row_exp && in) cr = c * exp2i(-a.row_exp[row]);
+            if (EPI == kEpiDz && in) {
+                l2 = a.lse2[row];
+                rs = a.rowscale[row];
+            }
+            for (int n = n0; n < n1; ++n, ++tile) {
+                const uint32_t buf = tile & 1;
+                ok = __all_sync(0xffffffffu, head_wait(&accfull[buf], (tile >> 1) & 1, a.wait_ns, gave_up));
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t t0 = tmem + buf * BN + ((uint32_t)(quad * 32) << 16) + half * (BN / 2);
+                const int64_t col0 = (int64_t)n * BN + half * (BN / 2);
+#pragma unroll 1
+                for (int ch = 0; ch < BN / 64; ++ch) {
+                    float v[32];
+                    tc_ld32(t0 + ch * 32, v);
+                    const int64_t col = col0 + ch * 32;
+                    if (EPI == kEpiStats) {
+                        const int valid = (int)max((int64_t)0, min((int64_t)32, a.N - col));
+                        if (valid < 32) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                if (j >= valid) v[j] = -INFINITY;
+                        }
+                        float mx = v[0];
+#pragma unroll
+                        for (int j = 1; j < 32; ++j) mx = fmaxf(mx, v[j]);
+                        const float mn = fmaxf(run_m, mx);
+                        const float m2 = mn == -INFINITY ? 0.f : mn * cr;
+                        float s[4] = {run_s * ex2(fmaf(run_m, cr, -m2)), 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) s[j & 3] += ex2(fmaf(v[j], cr, -m2));
+                        run_s = (s[0] + s[1]) + (s[2] + s[3]);
+                        run_m = mn;
+                    } else if (EPI == kEpiDz) {
+                        if (in && col < a.dz_pitch) {
+                            float p[32];
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) p[j] = rs == 0.f ? 0.f : rs * ex2(fmaf(v[j], cr, -l2));
+                            uint4* o = reinterpret_cast<uint4*>(a.dz + row * a.dz_pitch + col);
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                uint32_t w[4];
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) w[i] = pack16(p[q * 8 + 2 * i], p[q * 8 + 2 * i + 1], a.fmt);
+                                o[q] = make_uint4(w[0], w[1], w[2], w[3]);
+                                if (a.dz_split) {
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i) {
+                                        const float2 h = unpack_f16(w[i]);
+                                        w[i] = pack16(p[q * 8 + 2 * i] - h.x, p[q * 8 + 2 * i + 1] - h.y, 0);
+                                    }
+                                    *(reinterpret_cast<uint4*>(a.dz + a.dz_piece + row * a.dz_pitch + col) + q) =
+                                        make_uint4(w[0], w[1], w[2], w[3]);
+                                }
+                            }
+                        }
+                    } else if (in && col < a.N) {
+                        if (a.out) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) v[j] = v[j] * s1 * s2;
+                            if (a.vec && col + 32 <= a.N) {
+#pragma unroll
+                                for (int q = 0; q < 4; ++q)
+                                    store_vec(a.out, row * a.ldo + col + q * 8, v + q * 8, a.out_type);
+                            } else {
+#pragma unroll
+                                for (int j = 0; j < 32; ++j)
+                                    if (col + j < a.N) store_one(a.out, row * a.ldo + col + j, v[j], a.out_type);
+                            }
+                        } else {  // pp is a multiple of 32: whole chunks, the columns past N hold zeros
+                            float4* o = reinterpret_cast<float4*>(a.partial + ((int64_t)split * a.M + row) * a.pp + col);
+#pragma unroll
+                            for (int q = 0; q < 8; ++q) {
+                                float4 x = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+                                if (a.accumulate) {
+                                    const float4 y = o[q];
+                                    x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+                                }
+                                o[q] = x;
+                            }
+                        }
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&accempty[buf]);
+            }
+            if (EPI == kEpiStats && ok && in)
+                a.part[row * (2 * a.nstrips) + 2 * split + half] =
+                    make_float2(run_m == -INFINITY ? -INFINITY : run_m * cr, run_s);
+        }
+    }
+    if (!ok) {
+        *gave_up = 1;
+        if (a.err) atomicOr(a.err, kErrTimeout);
+    }
+    __syncwarp();
+    __syncthreads();
+    if (*gave_up) {  // no copy and no MMA may still be running when the block ends
+        if (threadIdx.x == 0)
+            for (uint32_t i = it > S::kStages ? it - S::kStages : 0; i < it; ++i)
+                head_drain(&full[i % S::kStages], (i / S::kStages) & 1);
+        if (threadIdx.x == 32) {
+            tc_commit(&drain);
+            head_drain(&drain, 0);
+        }
+        __syncwarp();
+        __syncthreads();
+    }
+    tc_fence_after();
+    if (warp == 2) tc_dealloc(tmem, 2 * BN);
+}
+
+// ---------------------------------------------------------------- rows and copies
+
+struct HeadIn {
+    const void* h;
+    const void* w;
+    int64_t ldh, ldw;  // elements between rows
+    int64_t N, V;
+    int D, Dp;         // Dp: D rounded up to 8, the row pitch of packed copies
+    int vec;           // rows of h and w are 16-byte aligned and D is a multiple of 8
+};
+
+// What a row is trained towards.
+struct Target {
+    const int64_t* ids;    // [N][K]; xent: the targets, K = 1
+    const float* logits;   // [N][K] teacher logits; null: xent
+    int64_t ignore;        // xent: the id of rows that do not count
+    int K;
+    float T;
+};
+
+// Whether xent row n counts; ids that are neither `ignore` nor in [0, V) are
+// recorded and do not count.
+__device__ __forceinline__ int64_t xent_id(const Target& t, int64_t n, int64_t V, int* err) {
+    const int64_t id = t.ids[n];
+    if (id == t.ignore) return -1;
+    if (id < 0 || id >= V) {
+        if (err) atomicOr(err, kErrIndex);
+        return -1;
+    }
+    return id;
+}
+
+template <class T>
+__device__ __forceinline__ float warp_dot(const T* x, const T* y, int D, int vec, int lane) {
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+    constexpr int E = 16 / sizeof(T);
+    if (vec) {
+#pragma unroll 4
+        for (int i = lane * E; i < D; i += 32 * E) {
+            const uint4 a = *reinterpret_cast<const uint4*>(x + i), b = *reinterpret_cast<const uint4*>(y + i);
+            const T* pa = reinterpret_cast<const T*>(&a);
+            const T* pb = reinterpret_cast<const T*>(&b);
+#pragma unroll
+            for (int j = 0; j < E; ++j) s[j & 3] = fmaf(to_f32(pa[j]), to_f32(pb[j]), s[j & 3]);
+        }
+    } else {
+#pragma unroll 4
+        for (int i = lane; i < D; i += 32) s[0] = fmaf(to_f32(x[i]), to_f32(y[i]), s[0]);
+    }
+    float t = (s[0] + s[1]) + (s[2] + s[3]);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    return t;
+}
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// A warp's join of a row's (maximum, sum) pairs; natural-log sum in every lane.
+__device__ __forceinline__ float join_parts(const float2* p, int n, int lane) {
+    float m = -INFINITY, s = 0.f;
+    for (int i = lane; i < n; i += 32) {
+        const float2 x = p[i];
+        const float mn = fmaxf(m, x.x), b = mn == -INFINITY ? 0.f : mn;
+        s = s * ex2(m - b) + x.y * ex2(x.x - b);
+        m = mn;
+    }
+    const float mn = warp_max(m), b = mn == -INFINITY ? 0.f : mn;
+    s = warp_sum(s * ex2(m - b));
+    return (b + log2f(s)) * kLn2;
+}
+
+constexpr int kRowThreads = 128;
+
+// The teacher's distribution of one row, a block per row: q[k] and log q[k] in
+// shared memory, ids as int (-1: not counted).  An id below 0 marks an entry that
+// does not count, whatever its logit holds; one past the table is recorded and does
+// not count either; so does an entry whose logit is -inf.  Returns whether any counts.
+__device__ bool teacher_row(const Target& t, int64_t n, int64_t V, float* q, float* logq, int* ids, float* red, int* err) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    float mx = -INFINITY;
+    for (int k = tid; k < t.K; k += kRowThreads) {
+        const int64_t id = t.ids[n * t.K + k];
+        float x = -INFINITY;
+        int got = -1;
+        if (id >= V) {
+            if (err) atomicOr(err, kErrIndex);
+        } else if (id >= 0) {
+            x = t.logits[n * t.K + k];
+            got = x == -INFINITY ? -1 : (int)id;
+        }
+        logq[k] = x;
+        ids[k] = got;
+        if (got >= 0) mx = (mx != mx || x != x) ? NAN : fmaxf(mx, x);
+    }
+    // a NaN logit makes the whole row NaN, as a softmax does
+    const bool nan = __syncthreads_or(mx != mx);
+    mx = warp_max(mx);
+    if (lane == 0) red[warp] = mx;
+    __syncthreads();
+    mx = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+    if (nan) mx = NAN;
+    float s = 0.f;
+    for (int k = tid; k < t.K; k += kRowThreads)
+        if (ids[k] >= 0) s += expf((logq[k] - mx) / t.T);
+    s = warp_sum(s);
+    if (lane == 0) red[4 + warp] = s;
+    const bool any = __syncthreads_or(mx != -INFINITY);
+    s = (red[4] + red[5]) + (red[6] + red[7]);
+    const float ls = logf(s), inv = 1.f / s;
+    for (int k = tid; k < t.K; k += kRowThreads) {
+        const float d = (logq[k] - mx) / t.T;
+        q[k] = ids[k] >= 0 ? expf(d) * inv : 0.f;
+        logq[k] = ids[k] >= 0 ? d - ls : 0.f;
+    }
+    __syncthreads();
+    return any;
+}
+
+// lse and loss of every row: the strips' pairs joined, the target scores as dot
+// products.  xent: a warp per row; distill: a block per row, a warp per entry.
+template <class T, bool DISTILL>
+__global__ void __launch_bounds__(kRowThreads) k_head_finish(HeadIn in, Target t, const float2* part, int nparts,
+                                                             float* loss, float* lse, int* err) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const T* h = static_cast<const T*>(in.h);
+    const T* w = static_cast<const T*>(in.w);
+    if (!DISTILL) {
+        const int64_t n = (int64_t)blockIdx.x * 4 + warp;
+        if (n >= in.N) return;
+        const int64_t id = xent_id(t, n, in.V, lane == 0 ? err : nullptr);
+        const float z = id >= 0 ? warp_dot(h + n * in.ldh, w + id * in.ldw, in.D, in.vec, lane) : 0.f;
+        const float l = join_parts(part + n * nparts, nparts, lane);
+        if (lane == 0) {
+            lse[n] = l;
+            loss[n] = id >= 0 ? l - z : 0.f;
+        }
+    } else {
+        extern __shared__ float sm[];
+        float* q = sm;
+        float* lq = sm + t.K;
+        int* ids = reinterpret_cast<int*>(sm + 2 * t.K);
+        __shared__ float red[8];
+        __shared__ float ls;
+        const int64_t n = blockIdx.x;
+        const bool any = teacher_row(t, n, in.V, q, lq, ids, red, err);
+        if (warp == 0) {
+            const float l = join_parts(part + n * nparts, nparts, lane);
+            if (lane == 0) ls = l;
+        }
+        __syncthreads();
+        const float l = ls;
+        float acc = 0.f;
+        for (int k = warp; k < t.K; k += 4) {
+            if (q[k] == 0.f) continue;
+            const float z = warp_dot(h + n * in.ldh, w + (int64_t)ids[k] * in.ldw, in.D, in.vec, lane);
+            acc += q[k] * (lq[k] - z / t.T + l);
+        }
+        __syncthreads();
+        if (lane == 0) red[warp] = acc;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            lse[n] = l;
+            loss[n] = any ? t.T * t.T * ((red[0] + red[1]) + (red[2] + red[3])) : 0.f;
+        }
+    }
+}
+
+// What the backward pass needs of every row, a block per row: its scale (g T, 0 for
+// a row that does not count), its lse in log2 units, dz of its target entries, and
+// its packed copy (zeros for a row that does not count, so that nothing such a row
+// holds, infinities and NaN included, reaches dweight).  Entries of one row with the
+// same id hold the same value, of their summed q.
+template <class T, bool DISTILL>
+__global__ void __launch_bounds__(kRowThreads)
+    k_head_rows(HeadIn in, Target t, const float* lse, const float* grad, const uint32_t* amax, float* rowscale,
+                float* lse2, int* ids_out, float* dzt, uint16_t* hp, int* err) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t n = blockIdx.x;
+    const T* h = static_cast<const T*>(in.h) + n * in.ldh;
+    const T* w = static_cast<const T*>(in.w);
+    const float l = lse[n];
+    bool any;
+    extern __shared__ float sm[];
+    __shared__ float red[8];
+    float* q = sm;
+    int* ids = reinterpret_cast<int*>(sm + 2 * t.K);
+    int64_t xid = -1;
+    if (DISTILL) {
+        any = teacher_row(t, n, in.V, q, sm + t.K, ids, red, err);
+    } else {
+        xid = xent_id(t, n, in.V, threadIdx.x == 0 ? err : nullptr);
+        any = xid >= 0;
+    }
+    const int ez = amax ? scale_exp(amax[2]) : 0, eh = amax ? scale_exp(amax[0]) : 0;
+    const float rs = any ? grad[n] * t.T * exp2i(ez) : 0.f;
+    if (threadIdx.x == 0) {
+        rowscale[n] = rs;
+        lse2[n] = l * kLog2e;
+    }
+    for (int k = warp; k < t.K; k += 4) {
+        const int64_t id = DISTILL ? (q[k] == 0.f ? -1 : ids[k]) : xid;
+        float d = 0.f;
+        if (id >= 0) {
+            float qs = 1.f;
+            if (DISTILL) {
+                qs = 0.f;
+                for (int j = lane; j < t.K; j += 32)
+                    if (ids[j] == id) qs += q[j];
+                qs = warp_sum(qs);
+            }
+            const float z = warp_dot(h, w + id * in.ldw, in.D, in.vec, lane);
+            d = (expf(z / t.T - l) - qs) * rs;
+        }
+        if (lane == 0) {
+            ids_out[n * t.K + k] = (int)id;
+            dzt[n * t.K + k] = d;
+        }
+    }
+    const int64_t piece = in.N * in.Dp;
+    for (int i = threadIdx.x; i < in.Dp; i += kRowThreads) {
+        const int64_t at = n * in.Dp + i;
+        if (sizeof(T) == 4) {
+            const float x = any && i < in.D ? to_f32(h[i]) * exp2i(eh) : 0.f;
+            const __half hi = __float2half_rn(x);
+            hp[at] = __half_as_ushort(hi);
+            hp[piece + at] = __half_as_ushort(__float2half_rn(x - __half2float(hi)));
+        } else {
+            hp[at] = any && i < in.D ? reinterpret_cast<const uint16_t*>(h)[i] : (uint16_t)0;
+        }
+    }
+}
+
+// Target entries of dz in columns [v0, v0 + P) of the current piece.
+__global__ void k_head_fix(const int* ids, const float* dzt, int64_t total, int K, int v0, int P, uint16_t* dz,
+                           int64_t pitch, int64_t piece, int fmt, int split) {
+    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    if (i >= total) return;
+    const int id = ids[i];
+    if (id < v0 || id >= v0 + P) return;
+    const int64_t at = (i / K) * pitch + (id - v0);
+    const uint32_t w = pack16(dzt[i], 0.f, fmt);
+    dz[at] = (uint16_t)w;
+    if (split) dz[piece + at] = (uint16_t)pack16(dzt[i] - unpack_f16(w).x, 0.f, 0);
+}
+
+// Largest finite magnitudes: blockIdx.y = 0: |weight| -> amax[1]; 1: |hidden| over
+// the rows that count -> amax[0]; 2: |grad| T over the same rows -> amax[2].
+// A largest value is the same in whatever order the atomics arrive.
+__global__ void __launch_bounds__(256) k_head_absmax(HeadIn in, Target t, const float* grad, int distill, uint32_t* amax) {
+    const int what = blockIdx.y == 0 ? 1 : (blockIdx.y == 1 ? 0 : 2);
+    const int lane = threadIdx.x & 31;
+    const int64_t warp0 = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5), warps = (int64_t)gridDim.x * 8;
+    uint32_t m = 0;
+    auto take = [&](float x) {
+        const uint32_t b = __float_as_uint(x) & 0x7FFFFFFFu;
+        if (b < 0x7F800000u) m = max(m, b);
+    };
+    auto counts = [&](int64_t n) {
+        if (!distill) return t.ids[n] != t.ignore;
+        for (int k = 0; k < t.K; ++k)
+            if (t.ids[n * t.K + k] >= 0) return true;
+        return false;
+    };
+    if (what == 2) {
+        for (int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x; n < in.N; n += (int64_t)gridDim.x * 256)
+            if (counts(n)) take(grad[n] * t.T);
+    } else {
+        const float* x = static_cast<const float*>(what == 1 ? in.w : in.h);
+        const int64_t rows = what == 1 ? in.V : in.N, ld = what == 1 ? in.ldw : in.ldh;
+        if (what == 1 && in.vec && ld == in.D) {
+            const float4* x4 = reinterpret_cast<const float4*>(x);
+            const int64_t n4 = rows * in.D / 4, step = (int64_t)gridDim.x * 256;
+#pragma unroll 4
+            for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n4; i += step) {
+                const float4 v = x4[i];
+                take(v.x);
+                take(v.y);
+                take(v.z);
+                take(v.w);
+            }
+        } else {
+            for (int64_t n = warp0; n < rows; n += warps) {
+                if (what == 0 && !counts(n)) continue;
+                for (int i = lane; i < in.D; i += 32) take(x[n * ld + i]);
+            }
+        }
+    }
+    m = __reduce_max_sync(0xffffffffu, m);
+    if (lane == 0 && m) atomicMax(&amax[what], m);
+}
+
+// Packed copies with rows of Dp 16-bit elements: blockIdx.y = 0: the table (fp32:
+// hi and lo pieces under one scale for the whole table); 1: the hidden rows, a warp
+// per row (fp32: a scale of each row's own, its exponent in row_exp).
+template <class T>
+__global__ void __launch_bounds__(256) k_head_pack(HeadIn in, const uint32_t* amax, uint16_t* wp, uint16_t* hp, int* row_exp) {
+    if (blockIdx.y == 0) {
+        if (!wp) return;
+        const T* w = static_cast<const T*>(in.w);
+        const int g = in.Dp / 8;  // 8-element groups of a row
+        const int64_t total = in.V * g, piece = in.V * in.Dp;
+        const float sc = sizeof(T) == 4 ? exp2i(scale_exp(amax[1])) : 1.f;
+        for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+            const int64_t r = i / g;
+            const int c = (int)(i - r * g) * 8;
+            const T* src = w + r * in.ldw + c;
+            if (sizeof(T) == 4) {
+                float x[8];
+                if (in.vec) {
+                    *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(src);
+                    *reinterpret_cast<float4*>(x + 4) = *(reinterpret_cast<const float4*>(src) + 1);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) x[j] = c + j < in.D ? to_f32(src[j]) : 0.f;
+                }
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float a = x[2 * j] * sc, b = x[2 * j + 1] * sc;
+                    hi[j] = pack16(a, b, 0);
+                    const float2 h = unpack_f16(hi[j]);
+                    lo[j] = pack16(a - h.x, b - h.y, 0);
+                }
+                *reinterpret_cast<uint4*>(wp + i * 8) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *reinterpret_cast<uint4*>(wp + piece + i * 8) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            } else {
+                const uint16_t* s = reinterpret_cast<const uint16_t*>(src);
+                uint16_t x[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] = c + j < in.D ? s[j] : (uint16_t)0;
+                *reinterpret_cast<uint4*>(wp + i * 8) = *reinterpret_cast<uint4*>(x);
+            }
+        }
+    } else {
+        if (!hp) return;
+        const int lane = threadIdx.x & 31;
+        const int64_t piece = in.N * in.Dp;
+        for (int64_t n = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); n < in.N; n += (int64_t)gridDim.x * 8) {
+            const T* h = static_cast<const T*>(in.h) + n * in.ldh;
+            if (sizeof(T) == 4) {
+                uint32_t m = 0;
+                for (int i = lane; i < in.D; i += 32) {
+                    const uint32_t b = __float_as_uint(to_f32(h[i])) & 0x7FFFFFFFu;
+                    if (b < 0x7F800000u) m = max(m, b);
+                }
+                const int e = scale_exp(__reduce_max_sync(0xffffffffu, m));
+                if (lane == 0) row_exp[n] = e;
+                for (int i = lane; i < in.Dp; i += 32) {
+                    const float x = i < in.D ? to_f32(h[i]) * exp2i(e) : 0.f;
+                    const __half hi = __float2half_rn(x);
+                    hp[n * in.Dp + i] = __half_as_ushort(hi);
+                    hp[piece + n * in.Dp + i] = __half_as_ushort(__float2half_rn(x - __half2float(hi)));
+                }
+            } else {
+                const uint16_t* s = reinterpret_cast<const uint16_t*>(h);
+                for (int i = lane; i < in.Dp; i += 32) hp[n * in.Dp + i] = i < in.D ? s[i] : (uint16_t)0;
+            }
+        }
+    }
+}
+
+// out[m, n] = the splits' partial sums, in split order, unscaled and rounded once.
+__global__ void __launch_bounds__(256) k_head_reduce(const float* partial, int splits, int64_t M, int64_t N, int64_t pp, void* out,
+                                                     int64_t ldo, int type, const uint32_t* amax_a, const uint32_t* amax_b) {
+    const float s1 = exp2i(-amax_exp(amax_a)), s2 = exp2i(-amax_exp(amax_b));
+    const int64_t total = M * N;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+        const int64_t m = i / N, n = i - m * N;
+        float s = 0.f;
+        for (int k = 0; k < splits; ++k) s += partial[((int64_t)k * M + m) * pp + n];
+        store_one(out, m * ldo + n, s * s1 * s2, type);
+    }
+}
+
+// ---------------------------------------------------------------- host
+
+namespace {
+
+uint64_t g_head_wait_ns = kHeadWaitNs;
+
+typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled() {
+    static EncodeTiled fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+            r != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            p = nullptr;
+        }
+        return reinterpret_cast<EncodeTiled>(p);
+    }();
+    return fn;
+}
+
+// A [pieces][rows][cols] array of 16-bit elements, rows `pitch` elements apart, read
+// in boxes of 64 columns x box_rows rows; elements outside read as 0.
+bool make_map(CUtensorMap* m, const void* p, int fmt, int64_t cols, int64_t rows, int pieces, int64_t pitch, int64_t piece, int box_rows) {
+    EncodeTiled enc = encode_tiled();
+    if (!enc) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)pieces};
+    const cuuint64_t strides[2] = {(cuuint64_t)pitch * 2, (cuuint64_t)(pieces > 1 ? piece : pitch * rows) * 2};
+    const cuuint32_t box[3] = {kBK, (cuuint32_t)box_rows, 1}, one[3] = {1, 1, 1};
+    return enc(m, fmt ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(p), dims, strides, box, one,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+constexpr int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+int sm_count() {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    return n;
+}
+
+// Workspace cut into 256-byte aligned blocks; with a null base only the size counts.
+struct Arena {
+    uint8_t* base;
+    size_t used = 0;
+    explicit Arena(void* p) : base(static_cast<uint8_t*>(p)) {}
+    template <class T>
+    T* get(int64_t n) {
+        T* p = base ? reinterpret_cast<T*>(base + used) : nullptr;
+        used += ((size_t)n * sizeof(T) + 255) / 256 * 256;
+        return p;
+    }
+};
+
+struct Operand {  // a 16-bit matrix the products read
+    const uint16_t* p;
+    int64_t rows, cols, pitch, piece;
+};
+
+template <int BN, bool AMN, bool BMN, int EPI>
+bool run_gemm(const Operand& A, const Operand& B, GemmArgs a, int sms, cudaStream_t st) {
+    CUtensorMap ma, mb;
+    const int pieces = a.nseg > 1 ? 2 : 1;
+    if (!make_map(&ma, A.p, a.fmt, A.cols, A.rows, pieces, A.pitch, A.piece, AMN ? 64 : 128)) return false;
+    if (!make_map(&mb, B.p, a.fmt, B.cols, B.rows, pieces, B.pitch, B.piece, BMN ? 64 : BN)) return false;
+    a.mtiles = (int)cdiv(a.M, 128);
+    a.ntiles = (int)cdiv(a.N, BN);
+    a.nstrips = (int)cdiv(a.ntiles, a.strip);
+    a.units = EPI == kEpiOut ? (int64_t)a.mtiles * a.ntiles * a.splits : (int64_t)a.mtiles * a.nstrips;
+    a.wait_ns = g_head_wait_ns;
+    auto k = k_head_gemm<BN, AMN, BMN, EPI>;
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)GemmShape<BN>::kSmem) != cudaSuccess) return false;
+    k<<<(unsigned)(a.units < sms ? a.units : sms), kGemmThreads, GemmShape<BN>::kSmem, st>>>(ma, mb, a);
+    return cudaGetLastError() == cudaSuccess;
+}
+
+// Column tiles per strip: the fewest rounds of tiles over the blocks, and among the
+// strips within 3% of that the longest (fewer pairs to join).
+int choose_strip(int64_t mtiles, int64_t ntiles, int sms) {
+    const int64_t g0 = cdiv(ntiles, 2048);
+    auto rounds = [&](int64_t g) { return (double)cdiv(mtiles * cdiv(ntiles, g), sms) * g; };
+    double least = 1e30;
+    for (int64_t g = g0; g < g0 + 64 && g <= ntiles; ++g) least = fmin(least, rounds(g));
+    int64_t best = g0;
+    for (int64_t g = g0; g < g0 + 64 && g <= ntiles; ++g)
+        if (rounds(g) <= 1.03 * least) best = g;
+    return (int)best;
+}
+
+// K ranges of a product of `tiles` tiles and `chunks` K chunks: the shortest
+// schedule, a unit counted as its chunks and 4 for its start and read-out.
+int choose_splits(int64_t tiles, int64_t chunks, int sms) {
+    int best = 1;
+    double bestc = 1e30;
+    for (int s = 1; s <= 64 && s <= chunks; ++s) {
+        const double c = (double)cdiv(tiles * s, sms) * (cdiv(chunks, s) + 4) + (s > 1 ? 2.0 * s : 0.0);
+        if (c < bestc) bestc = c, best = s;
+    }
+    return best;
+}
+
+struct Plan {
+    HeadIn in;
+    int type, fmt, split;    // split: fp32 operands in hi and lo pieces
+    int esize, sms;
+    bool pack_h, pack_w;
+    int bn_s;                // column tile of the score products
+    int strip;
+    int64_t nparts;
+    int64_t P;               // vocabulary piece (backward)
+    int64_t pitch;           // its row pitch in dz
+    int bn_d;                // column tile of the gradient products
+    int dh_splits, dw_splits;
+    bool dh_direct;
+    int64_t pp;              // row pitch of partial sums
+};
+
+bool aligned_rows(const void* p, int64_t ld, int esize) { return ((uintptr_t)p % 16 == 0) && (ld * esize % 16 == 0); }
+
+tt_status make_plan(const tt_head* hd, int K, Plan* p) {
+    if (!hd) return TT_ERR_ARG;
+    if (hd->dtype != TT_F32 && hd->dtype != TT_BF16 && hd->dtype != TT_F16) return TT_ERR_ARG;
+    if (hd->rows < 0 || hd->dim < 1 || hd->vocab < 1 || K < 1 || K > kMaxTeacher) return TT_ERR_SHAPE;
+    if (hd->rows > TT_HEAD_MAX_ROWS || hd->vocab > TT_HEAD_MAX_VOCAB || hd->dim > TT_HEAD_MAX_DIM) return TT_ERR_SHAPE;
+    if (hd->hidden_stride < hd->dim || hd->weight_stride < hd->dim) return TT_ERR_SHAPE;
+    p->type = hd->dtype;
+    p->fmt = hd->dtype == TT_BF16;
+    p->split = hd->dtype == TT_F32;
+    p->esize = hd->dtype == TT_F32 ? 4 : 2;
+    p->sms = sm_count();
+    if (p->sms <= 0) return TT_ERR_CUDA;
+    if (((uintptr_t)hd->hidden_dev | (uintptr_t)hd->weight_dev) % p->esize) return TT_ERR_ARG;
+    HeadIn& in = p->in;
+    in.h = hd->hidden_dev;
+    in.w = hd->weight_dev;
+    in.ldh = hd->hidden_stride;
+    in.ldw = hd->weight_stride;
+    in.N = hd->rows;
+    in.V = hd->vocab;
+    in.D = hd->dim;
+    in.Dp = (in.D + 7) / 8 * 8;
+    const bool ah = aligned_rows(in.h, in.ldh, p->esize), aw = aligned_rows(in.w, in.ldw, p->esize);
+    in.vec = ah && aw && in.D % 8 == 0;
+    p->pack_h = p->split || !ah;
+    p->pack_w = p->split || !aw;
+    const int64_t mt = cdiv(in.N, 128);
+    // 256-column tiles read each operand row less often; 128-column tiles when the
+    // wide ones would leave blocks without work
+    p->bn_s = mt * cdiv(in.V, 256) >= 2 * p->sms ? 256 : 128;
+    p->strip = choose_strip(mt, cdiv(in.V, p->bn_s), p->sms);
+    p->nparts = 2 * cdiv(cdiv(in.V, p->bn_s), p->strip);
+    // backward
+    const int64_t vcap = cdiv(in.V, 64) * 64;
+    int64_t P = in.N > 0 ? kDzBytes / (2 * (p->split ? 2 : 1) * in.N) : vcap;
+    P = P / 1024 * 1024;
+    if (P < 1024) P = 1024;
+    if (P >= vcap) {
+        P = vcap;
+    } else {
+        P = cdiv(cdiv(in.V, cdiv(in.V, P)), 256) * 256;  // pieces of near-equal size
+    }
+    p->P = P;
+    p->pitch = P;
+    p->bn_d = in.D <= 64 ? 64 : (in.D <= 128 ? 128 : 256);
+    const int64_t nt = cdiv(in.D, p->bn_d);
+    p->dh_splits = choose_splits(mt * nt, cdiv(P, kBK) * (p->split ? 3 : 1), p->sms);
+    if (p->dh_splits > cdiv(P, kBK)) p->dh_splits = (int)cdiv(P, kBK);
+    const int64_t lastP = in.V - (cdiv(in.V, P) - 1) * P;
+    if (p->dh_splits > cdiv(lastP, kBK)) p->dh_splits = (int)cdiv(lastP, kBK);
+    p->dh_direct = p->dh_splits == 1 && in.V <= P;
+    p->dw_splits = choose_splits(cdiv(P, 128) * nt, cdiv(in.N, kBK) * (p->split ? 3 : 1), p->sms);
+    if (p->dw_splits > cdiv(in.N, kBK)) p->dw_splits = (int)(in.N > 0 ? cdiv(in.N, kBK) : 1);
+    p->pp = cdiv(in.D, 32) * 32;
+    return TT_OK;
+}
+
+struct FwdWs {
+    float2* part;
+    uint16_t *hp, *wp;
+    int* row_exp;
+    uint32_t* amax;
+};
+size_t fwd_ws(const Plan& p, void* base, FwdWs* w) {
+    Arena a(base);
+    const int64_t pc = p.split ? 2 : 1;
+    w->amax = a.get<uint32_t>(4);
+    w->part = a.get<float2>(p.in.N * p.nparts);
+    w->row_exp = a.get<int>(p.split ? p.in.N : 0);
+    w->hp = a.get<uint16_t>(p.pack_h ? pc * p.in.N * p.in.Dp : 0);
+    w->wp = a.get<uint16_t>(p.pack_w ? pc * p.in.V * p.in.Dp : 0);
+    return a.used;
+}
+
+struct BwdWs {
+    uint32_t* amax;
+    float *rowscale, *lse2, *dzt, *dh_part, *dw_part;
+    int* ids;
+    uint16_t *hp, *wp, *dz;
+};
+size_t bwd_ws(const Plan& p, int K, void* base, BwdWs* w) {
+    Arena a(base);
+    const int64_t pc = p.split ? 2 : 1;
+    w->amax = a.get<uint32_t>(4);
+    w->rowscale = a.get<float>(p.in.N);
+    w->lse2 = a.get<float>(p.in.N);
+    w->ids = a.get<int>(p.in.N * K);
+    w->dzt = a.get<float>(p.in.N * K);
+    w->hp = a.get<uint16_t>(pc * p.in.N * p.in.Dp);
+    w->wp = a.get<uint16_t>(p.pack_w ? pc * p.in.V * p.in.Dp : 0);
+    w->dz = a.get<uint16_t>(pc * p.in.N * p.pitch);
+    w->dh_part = a.get<float>(p.dh_direct ? 0 : (int64_t)p.dh_splits * p.in.N * p.pp);
+    w->dw_part = a.get<float>(p.dw_splits > 1 ? (int64_t)p.dw_splits * p.P * p.pp : 0);
+    return a.used;
+}
+
+unsigned grid_of(int64_t items, int per_block, int sms, int per_sm) {
+    const int64_t b = cdiv(items, per_block);
+    return (unsigned)(b < 1 ? 1 : (b > (int64_t)sms * per_sm ? (int64_t)sms * per_sm : b));
+}
+
+bool launch_ok() { return cudaGetLastError() == cudaSuccess; }
+
+GemmArgs gemm_args(const Plan& p, int* err) {
+    GemmArgs a{};
+    a.strip = 1;
+    a.splits = 1;
+    a.nseg = p.split ? 3 : 1;
+    a.fmt = p.fmt;
+    a.err = err;
+    return a;
+}
+
+template <class T>
+tt_status head_forward(const Plan& p, const Target& t, float* loss, float* lse, int* err, void* ws, size_t ws_bytes, cudaStream_t st) {
+    const HeadIn& in = p.in;
+    FwdWs w;
+    if (fwd_ws(p, ws, &w) > ws_bytes) return TT_ERR_ARG;
+    if (in.N == 0) return TT_OK;
+    const bool distill = t.logits != nullptr;
+    if (p.split) {
+        if (cudaMemsetAsync(w.amax, 0, 16, st) != cudaSuccess) return TT_ERR_CUDA;
+        k_head_absmax<<<dim3(grid_of(in.V * in.D, 4096, p.sms, 8), 1), 256, 0, st>>>(in, t, nullptr, distill, w.amax);
+        if (!launch_ok()) return TT_ERR_CUDA;
+    }
+    if (p.pack_h || p.pack_w) {
+        k_head_pack<T><<<dim3(grid_of(p.pack_w ? in.V * (in.Dp / 8) : in.N * 32, 256, p.sms, 8), 2), 256, 0, st>>>(
+            in, w.amax, p.pack_w ? w.wp : nullptr, p.pack_h ? w.hp : nullptr, w.row_exp);
+        if (!launch_ok()) return TT_ERR_CUDA;
+    }
+    GemmArgs a = gemm_args(p, err);
+    a.M = in.N;
+    a.N = in.V;
+    a.strip = p.strip;
+    a.chunks = (int)cdiv(in.D, kBK);
+    a.amax_b = p.split ? w.amax + 1 : nullptr;
+    a.row_exp = p.split ? w.row_exp : nullptr;
+    a.ctemp = kLog2e / t.T;
+    a.part = w.part;
+    const Operand H{p.pack_h ? w.hp : static_cast<const uint16_t*>(in.h), in.N, in.D, p.pack_h ? in.Dp : in.ldh, in.N * in.Dp};
+    const Operand W{p.pack_w ? w.wp : static_cast<const uint16_t*>(in.w), in.V, in.D, p.pack_w ? in.Dp : in.ldw, in.V * in.Dp};
+    const bool ok = p.bn_s == 256 ? run_gemm<256, false, false, kEpiStats>(H, W, a, p.sms, st)
+                                  : run_gemm<128, false, false, kEpiStats>(H, W, a, p.sms, st);
+    if (!ok) return TT_ERR_CUDA;
+    if (distill)
+        k_head_finish<T, true><<<(unsigned)in.N, kRowThreads, (size_t)t.K * 12, st>>>(in, t, w.part, (int)p.nparts, loss, lse, err);
+    else
+        k_head_finish<T, false><<<(unsigned)cdiv(in.N, 4), kRowThreads, 0, st>>>(in, t, w.part, (int)p.nparts, loss, lse, err);
+    return launch_ok() ? TT_OK : TT_ERR_CUDA;
+}
+
+template <bool AMN>
+bool out_gemm(int bn, const Operand& A, const Operand& B, const GemmArgs& a, int sms, cudaStream_t st) {
+    if (bn == 64) return run_gemm<64, AMN, true, kEpiOut>(A, B, a, sms, st);
+    if (bn == 128) return run_gemm<128, AMN, true, kEpiOut>(A, B, a, sms, st);
+    return run_gemm<256, AMN, true, kEpiOut>(A, B, a, sms, st);
+}
+
+template <class T>
+tt_status head_backward(const Plan& p, const Target& t, const float* lse, const float* grad, void* dh, void* dw, int* err, void* ws,
+                        size_t ws_bytes, cudaStream_t st) {
+    const HeadIn& in = p.in;
+    BwdWs w;
+    if (bwd_ws(p, t.K, ws, &w) > ws_bytes) return TT_ERR_ARG;
+    if (in.N == 0) return cudaMemsetAsync(dw, 0, (size_t)in.V * in.D * p.esize, st) == cudaSuccess ? TT_OK : TT_ERR_CUDA;
+    const bool distill = t.logits != nullptr;
+    const uint32_t* amax = p.fmt ? nullptr : w.amax;  // bf16 has fp32's range: dz needs no scale
+    if (amax) {
+        if (cudaMemsetAsync(w.amax, 0, 16, st) != cudaSuccess) return TT_ERR_CUDA;
+        // f16 inputs are taken as they are: only dz is scaled (blockIdx.y = 2)
+        if (p.split) {
+            k_head_absmax<<<dim3(grid_of(in.V * in.D, 4096, p.sms, 8), 3), 256, 0, st>>>(in, t, grad, distill, w.amax);
+        } else {
+            HeadIn none = in;
+            none.V = 0;
+            none.D = 0;
+            k_head_absmax<<<dim3(grid_of(in.N, 256, p.sms, 1), 3), 256, 0, st>>>(none, t, grad, distill, w.amax);
+        }
+        if (!launch_ok()) return TT_ERR_CUDA;
+    }
+    if (p.pack_w) {
+        k_head_pack<T><<<dim3(grid_of(in.V * (in.Dp / 8), 256, p.sms, 16), 1), 256, 0, st>>>(in, w.amax, w.wp, nullptr, nullptr);
+        if (!launch_ok()) return TT_ERR_CUDA;
+    }
+    if (distill)
+        k_head_rows<T, true><<<(unsigned)in.N, kRowThreads, (size_t)t.K * 12, st>>>(in, t, lse, grad, amax, w.rowscale, w.lse2, w.ids,
+                                                                                  w.dzt, w.hp, err);
+    else
+        k_head_rows<T, false><<<(unsigned)in.N, kRowThreads, 12, st>>>(in, t, lse, grad, amax, w.rowscale, w.lse2, w.ids, w.dzt, w.hp, err);
+    if (!launch_ok()) return TT_ERR_CUDA;
+    const uint32_t *ah = amax, *aw = amax ? amax + 1 : nullptr, *az = amax ? amax + 2 : nullptr;
+    const int64_t npieces = cdiv(in.V, p.P), dz_piece = in.N * p.pitch;
+    for (int64_t i = 0; i < npieces; ++i) {
+        const int64_t v0 = i * p.P, P = in.V - v0 < p.P ? in.V - v0 : p.P;
+        const int64_t wpitch = p.pack_w ? in.Dp : in.ldw;
+        const Operand H{w.hp, in.N, in.D, in.Dp, in.N * in.Dp};
+        const Operand W{(p.pack_w ? w.wp : static_cast<const uint16_t*>(in.w)) + v0 * wpitch, P, in.D, wpitch, in.V * in.Dp};
+        const Operand Z{w.dz, in.N, P, p.pitch, dz_piece};
+        GemmArgs a = gemm_args(p, err);
+        a.M = in.N;
+        a.N = P;
+        a.chunks = (int)cdiv(in.D, kBK);
+        a.amax_a = ah;
+        a.amax_b = aw;
+        a.ctemp = kLog2e / t.T;
+        a.lse2 = w.lse2;
+        a.rowscale = w.rowscale;
+        a.dz = w.dz;
+        a.dz_pitch = p.pitch;
+        a.dz_piece = dz_piece;
+        a.dz_split = p.split;
+        bool ok = p.bn_s == 256 ? run_gemm<256, false, false, kEpiDz>(H, W, a, p.sms, st) : run_gemm<128, false, false, kEpiDz>(H, W, a, p.sms, st);
+        if (!ok) return TT_ERR_CUDA;
+        k_head_fix<<<(unsigned)cdiv(in.N * t.K, 256), 256, 0, st>>>(w.ids, w.dzt, in.N * t.K, t.K, (int)v0, (int)P, w.dz, p.pitch, dz_piece,
+                                                                p.fmt, p.split);
+        if (!launch_ok()) return TT_ERR_CUDA;
+
+        GemmArgs b = gemm_args(p, err);  // dweight of the piece: [P][D] = dz^T H
+        b.M = P;
+        b.N = in.D;
+        b.chunks = (int)cdiv(in.N, kBK);
+        b.splits = p.dw_splits;
+        b.amax_a = az;
+        b.amax_b = ah;
+        void* dwp = static_cast<uint8_t*>(dw) + (size_t)v0 * in.D * p.esize;
+        b.out = p.dw_splits > 1 ? nullptr : dwp;
+        b.ldo = in.D;
+        b.out_type = p.type;
+        b.vec = ((uintptr_t)dwp % 16 == 0) && ((int64_t)in.D * p.esize % 16 == 0);
+        b.partial = w.dw_part;
+        b.pp = p.pp;
+        if (!out_gemm<true>(p.bn_d, Z, H, b, p.sms, st)) return TT_ERR_CUDA;
+        if (p.dw_splits > 1) {
+            k_head_reduce<<<grid_of(P * in.D, 256, p.sms, 8), 256, 0, st>>>(w.dw_part, p.dw_splits, P, in.D, p.pp, dwp, in.D, p.type, az, ah);
+            if (!launch_ok()) return TT_ERR_CUDA;
+        }
+
+        GemmArgs c = gemm_args(p, err);  // the piece's share of dhidden: [N][D] += dz W
+        c.M = in.N;
+        c.N = in.D;
+        c.chunks = (int)cdiv(P, kBK);
+        c.splits = p.dh_splits;
+        c.amax_a = az;
+        c.amax_b = aw;
+        c.out = p.dh_direct ? dh : nullptr;
+        c.ldo = in.D;
+        c.out_type = p.type;
+        c.vec = ((uintptr_t)dh % 16 == 0) && ((int64_t)in.D * p.esize % 16 == 0);
+        c.partial = w.dh_part;
+        c.pp = p.pp;
+        c.accumulate = i > 0;
+        if (!out_gemm<false>(p.bn_d, Z, W, c, p.sms, st)) return TT_ERR_CUDA;
+    }
+    if (!p.dh_direct) {
+        k_head_reduce<<<grid_of(in.N * in.D, 256, p.sms, 8), 256, 0, st>>>(w.dh_part, p.dh_splits, in.N, in.D, p.pp, dh, in.D, p.type, az, aw);
+        if (!launch_ok()) return TT_ERR_CUDA;
+    }
+    return TT_OK;
+}
+
+tt_status forward_any(const tt_head* hd, const Target& t, float* loss, float* lse, int* err, void* ws, size_t n, tt_stream s) {
+    Plan p;
+    const tt_status st = make_plan(hd, t.K, &p);
+    if (st != TT_OK) return st;
+    if (hd->rows > 0 && (!hd->hidden_dev || !t.ids || !loss || !lse)) return TT_ERR_ARG;
+    if (!hd->weight_dev || !ws || (uintptr_t)ws % 256) return TT_ERR_ARG;
+    cudaStream_t cs = reinterpret_cast<cudaStream_t>(s);
+    if (p.type == TT_F32) return head_forward<float>(p, t, loss, lse, err, ws, n, cs);
+    if (p.type == TT_BF16) return head_forward<__nv_bfloat16>(p, t, loss, lse, err, ws, n, cs);
+    return head_forward<__half>(p, t, loss, lse, err, ws, n, cs);
+}
+
+tt_status backward_any(const tt_head* hd, const Target& t, const float* lse, const float* grad, void* dh, void* dw, int* err, void* ws,
+                       size_t n, tt_stream s) {
+    Plan p;
+    const tt_status st = make_plan(hd, t.K, &p);
+    if (st != TT_OK) return st;
+    if (hd->rows > 0 && (!hd->hidden_dev || !t.ids || !lse || !grad || !dh)) return TT_ERR_ARG;
+    if (!hd->weight_dev || !dw || !ws || (uintptr_t)ws % 256) return TT_ERR_ARG;
+    if (((uintptr_t)dh | (uintptr_t)dw) % p.esize) return TT_ERR_ARG;
+    cudaStream_t cs = reinterpret_cast<cudaStream_t>(s);
+    if (p.type == TT_F32) return head_backward<float>(p, t, lse, grad, dh, dw, err, ws, n, cs);
+    if (p.type == TT_BF16) return head_backward<__nv_bfloat16>(p, t, lse, grad, dh, dw, err, ws, n, cs);
+    return head_backward<__half>(p, t, lse, grad, dh, dw, err, ws, n, cs);
+}
+
+bool good_temp(float T) { return T > 0.f && T <= 1e4f && T >= 1e-4f; }
+
+}  // namespace
+}  // namespace ttemb
+
+using namespace ttemb;
+
+extern "C" {
+
+int64_t tt_emb_head_workspace(const tt_head* head, int32_t teacher_k, int32_t backward) {
+    Plan p;
+    if (make_plan(head, teacher_k, &p) != TT_OK) return -1;
+    if (backward) {
+        BwdWs w;
+        return (int64_t)bwd_ws(p, teacher_k, nullptr, &w);
+    }
+    FwdWs w;
+    return (int64_t)fwd_ws(p, nullptr, &w);
+}
+
+tt_status tt_emb_xent_forward(const tt_head* head, const int64_t* targets_dev, int64_t ignore_index, float* loss_dev, float* lse_dev,
+                              int32_t* err_dev, void* ws_dev, size_t ws_bytes, tt_stream stream) {
+    const Target t{targets_dev, nullptr, ignore_index, 1, 1.f};
+    return forward_any(head, t, loss_dev, lse_dev, err_dev, ws_dev, ws_bytes, stream);
+}
+
+tt_status tt_emb_xent_backward(const tt_head* head, const int64_t* targets_dev, int64_t ignore_index, const float* lse_dev,
+                               const float* grad_loss_dev, void* grad_hidden_dev, void* grad_weight_dev, int32_t* err_dev, void* ws_dev,
+                               size_t ws_bytes, tt_stream stream) {
+    const Target t{targets_dev, nullptr, ignore_index, 1, 1.f};
+    return backward_any(head, t, lse_dev, grad_loss_dev, grad_hidden_dev, grad_weight_dev, err_dev, ws_dev, ws_bytes, stream);
+}
+
+tt_status tt_emb_distill_forward(const tt_head* head, const int64_t* ids_dev, const float* logits_dev, int32_t teacher_k, float temperature,
+                                 float* loss_dev, float* lse_dev, int32_t* err_dev, void* ws_dev, size_t ws_bytes, tt_stream stream) {
+    if (!good_temp(temperature) || (head && head->rows > 0 && !logits_dev)) return TT_ERR_ARG;
+    const Target t{ids_dev, logits_dev, -1, teacher_k, temperature};
+    return forward_any(head, t, loss_dev, lse_dev, err_dev, ws_dev, ws_bytes, stream);
+}
+
+tt_status tt_emb_distill_backward(const tt_head* head, const int64_t* ids_dev, const float* logits_dev, int32_t teacher_k,
+                                  float temperature, const float* lse_dev, const float* grad_loss_dev, void* grad_hidden_dev,
+                                  void* grad_weight_dev, int32_t* err_dev, void* ws_dev, size_t ws_bytes, tt_stream stream) {
+    if (!good_temp(temperature) || (head && head->rows > 0 && !logits_dev)) return TT_ERR_ARG;
+    const Target t{ids_dev, logits_dev, -1, teacher_k, temperature};
+    return backward_any(head, t, lse_dev, grad_loss_dev, grad_hidden_dev, grad_weight_dev, err_dev, ws_dev, ws_bytes, stream);
+}
+
+tt_status tt_emb_head_set_wait_limit(uint64_t ns) {
+    g_head_wait_ns = ns;
+    return TT_OK;
+}
+
+}  // extern "C"

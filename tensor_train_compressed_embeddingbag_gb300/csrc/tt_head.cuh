@@ -1,0 +1,135 @@
+// tt_head.cuh -- device code shared by the vocabulary-head kernels (tt_head.cu):
+// TMA loads, 128-byte-swizzled tensor-core operands, bounded waits.
+//
+// Operand tiles are 16-bit (both bf16 or both f16) and arrive by TMA with the
+// 128-byte swizzle, 64 deep along K.  A tile whose matrix is contiguous along K
+// ("K-major") is rows x 128 bytes: 8-row groups 1,024 bytes apart (the stride
+// byte offset), one MMA's K = 16 is 32 bytes further along the row.  A tile whose
+// matrix is contiguous along its M or N index ("MN-major", read transposed by the
+// MMA) is made of blocks of 64 indices x 64 K rows of 128 bytes: 8-K groups 1,024
+// bytes apart (stride byte offset), blocks 8,192 bytes apart (leading byte
+// offset), one MMA's K = 16 is 2,048 bytes further.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "tt_tc.cuh"
+
+namespace ttemb {
+
+constexpr uint64_t kHeadWaitNs = 2000000000ull;  // default bound of a device wait (2 s)
+
+__device__ __forceinline__ uint64_t global_ns() {
+    uint64_t t;
+    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+    return t;
+}
+
+__device__ __forceinline__ bool mbar_try(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+// Wait for the phase of the given parity for at most `ns` nanoseconds, or until
+// another role of the block gave up; false if the phase did not complete.
+__device__ __forceinline__ bool head_wait(uint64_t* bar, uint32_t parity, uint64_t ns, volatile int* gave_up) {
+    if (mbar_try(bar, parity)) return true;
+    const uint64_t t0 = global_ns();
+    while (!mbar_try(bar, parity)) {
+        if (*gave_up || global_ns() - t0 >= ns) return false;
+    }
+    return true;
+}
+
+// The same wait without the early way out, for copies and MMAs in flight.
+__device__ __forceinline__ void head_drain(uint64_t* bar, uint32_t parity) {
+    const uint64_t t0 = global_ns();
+    while (!mbar_try(bar, parity)) {
+        if (global_ns() - t0 >= kHeadWaitNs) return;
+    }
+}
+
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
+// One box of a 3-D tensor map into shared memory.  x: innermost coordinate, a
+// multiple of 8 elements (16 bytes).
+__device__ __forceinline__ void tma_load3(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
+        : "memory");
+}
+
+// Shared-memory matrix descriptor of a 128-byte-swizzled operand.
+__device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, bool mn_major) {
+    const uint64_t lbo = mn_major ? (8192u >> 4) : 1u;
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (lbo << 16) | ((uint64_t)(1024u >> 4) << 32) | ((uint64_t)1 << 46) |
+           ((uint64_t)2 << 61);
+}
+
+// Instruction descriptor of kind::f16, fp32 accumulator; fmt 0: f16, 1: bf16.
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int fmt, bool a_mn, bool b_mn) {
+    return (1u << 4) | ((uint32_t)fmt << 7) | ((uint32_t)fmt << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
+           ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                        bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+template <class T>
+__device__ __forceinline__ float to_f32(T x);
+template <>
+__device__ __forceinline__ float to_f32<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <>
+__device__ __forceinline__ float to_f32<__half>(__half x) { return __half2float(x); }
+
+// Two floats rounded to nearest and packed, the first in the low half; fmt 0: f16, 1: bf16.
+__device__ __forceinline__ uint32_t pack16(float a, float b, int fmt) {
+    uint32_t r;
+    if (fmt)
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    else
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    return r;
+}
+__device__ __forceinline__ float2 unpack_f16(uint32_t v) { return __half22float2(*reinterpret_cast<__half2*>(&v)); }
+
+// Power of two that brings a tensor whose largest magnitude has these fp32 bits
+// just below 2^14 (the largest f16 is 65,504).  An all-zero tensor and one that
+// holds an infinity or a NaN are left alone.  |exponent| <= 60, so the product of
+// two such factors is a normal fp32 number.
+__device__ __forceinline__ int scale_exp(uint32_t absmax_bits) {
+    if (absmax_bits == 0 || absmax_bits >= 0x7F800000u) return 0;
+    const int e = 13 - ((int)(absmax_bits >> 23) - 127);
+    return e < -60 ? -60 : (e > 60 ? 60 : e);
+}
+__device__ __forceinline__ float exp2i(int e) { return __int_as_float((e + 127) << 23); }
+
+}  // namespace ttemb
