@@ -394,7 +394,7 @@ typedef enum { TT_F32 = 0, TT_BF16 = 1, TT_F16 = 2 } tt_dtype;
 #define TT_HEAD_MAX_ROWS 16777216    /* rows N */
 #define TT_HEAD_MAX_VOCAB 1073741824 /* table rows V */
 #define TT_HEAD_MAX_DIM 65536        /* width D */
-#define TT_HEAD_MAX_TEACHER 1024     /* teacher entries per row */
+#define TT_HEAD_MAX_TEACHER 1024     /* teacher entries per row; rows x entries < 2^31 */
 
 typedef struct {
     const void* hidden_dev; /* [rows][dim], rows hidden_stride elements apart */

@@ -12,11 +12,12 @@
 // Forward: one product kernel keeps, per row, a running maximum and sum of the
 // exponentials of its column tiles and writes one pair per strip of tiles; a row
 // kernel joins them and takes the target scores as fp32 dot products.
-// Backward: the table is taken in pieces of the vocabulary.  For each, the scores
-// are formed again, dz of the piece is written in 16 bits (k_head_fix then writes
-// the entries that have a target), and two products read it: dweight of the piece
-// and the piece's share of dhidden.  The only array of N x (vocabulary piece) is
-// that dz (at most kDzBytes, or 1,024 columns).
+// Backward, D <= 128: one kernel per gradient, each forming the scores again and
+// keeping dz on the chip (tt_head_fused.cuh).  Wider: the table is taken in pieces of
+// the vocabulary.  For each, the scores are formed again, dz of the piece is written
+// in 16 bits (k_head_fix then writes the entries that have a target), and two products
+// read it: dweight of the piece and the piece's share of dhidden.  The only array of
+// N x (vocabulary piece) is that dz (at most kDzBytes, or 1,024 columns).
 //
 // Types.  bf16 and f16 inputs go to the tensor cores as they are.  An fp32 input x
 // is split as x 2^e = hi + lo with hi, lo in f16 (e a power-of-two scale that puts
@@ -29,344 +30,14 @@
 #include <stdio.h>
 
 #include "tt_head.cuh"
+#include "tt_head_fused.cuh"
+#include "tt_head_gemm.cuh"
 
 namespace ttemb {
 
-constexpr int kGemmThreads = 384;  // warp 0: TMA, 1: MMA, 2: tensor memory, 4..11: epilogue
-constexpr int kEpiWarps = 8;
-constexpr int kBK = 64;            // K depth of a stage: one 128-byte swizzled row
 constexpr int64_t kDzBytes = 256ll << 20;  // dz of one vocabulary piece
+constexpr int64_t kMaxBlocks = 1ll << 28;    // 32 x 32 blocks of targets (1 GB of list heads)
 constexpr int kMaxTeacher = TT_HEAD_MAX_TEACHER;
-
-enum Epi { kEpiStats = 0, kEpiDz = 1, kEpiOut = 2 };
-
-struct GemmArgs {
-    int64_t M, N;      // valid rows and columns of the product
-    int mtiles, ntiles;
-    int strip;         // column tiles per unit (kEpiStats), else 1
-    int nstrips;
-    int splits;        // K ranges (kEpiOut), else 1
-    int chunks;        // K chunks of 64
-    int nseg;          // 1, or 3: hi hi, hi lo, lo hi
-    int64_t units;
-    int fmt;           // 16-bit type of the operands: 0 f16, 1 bf16
-    uint64_t wait_ns;
-    int* err;
-    // scales: exponents of the operands' power-of-two scales come from these bits
-    const uint32_t* amax_a;
-    const uint32_t* amax_b;
-    const int* row_exp;  // per-row exponent of A (forward), else null
-    float ctemp;         // log2(e) / T
-    // kEpiStats
-    float2* part;        // [M][2 nstrips] (maximum in log2 units, sum)
-    // kEpiDz
-    const float* lse2;
-    const float* rowscale;
-    uint16_t* dz;        // [pieces][M][dz_pitch]
-    int64_t dz_pitch, dz_piece;
-    int dz_split;
-    // kEpiOut
-    void* out;           // [M][ldo] of out_type, or null: partial sums
-    int64_t ldo;
-    int out_type;        // tt_dtype
-    int vec;             // rows of out are 16-byte aligned
-    float* partial;      // [splits][M][pp]
-    int64_t pp;
-    int accumulate;
-};
-
-__device__ __forceinline__ int amax_exp(const uint32_t* p) { return p ? scale_exp(*p) : 0; }
-
-template <int BN>
-struct GemmShape {
-    static constexpr int kStages = BN == 256 ? 4 : (BN == 128 ? 6 : 8);
-    static constexpr uint32_t kA = 128 * 128, kB = BN * 128;
-    static constexpr uint32_t kStage = kA + kB;
-    static constexpr size_t kSmem = (size_t)kStages * kStage + 1024;
-};
-
-__device__ __forceinline__ void store_vec(void* out, int64_t at, const float* v, int type) {
-    // 8 consecutive elements, 16-byte aligned
-    if (type == TT_F32) {
-        float4* o = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
-        o[0] = make_float4(v[0], v[1], v[2], v[3]);
-        o[1] = make_float4(v[4], v[5], v[6], v[7]);
-    } else {
-        const int fmt = type == TT_BF16;
-        uint4 u;
-        u.x = pack16(v[0], v[1], fmt);
-        u.y = pack16(v[2], v[3], fmt);
-        u.z = pack16(v[4], v[5], fmt);
-        u.w = pack16(v[6], v[7], fmt);
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at) = u;
-    }
-}
-__device__ __forceinline__ void store_one(void* out, int64_t at, float v, int type) {
-    if (type == TT_F32)
-        static_cast<float*>(out)[at] = v;
-    else if (type == TT_BF16)
-        static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(v);
-    else
-        static_cast<__half*>(out)[at] = __float2half_rn(v);
-}
-
-// C[m, n] = sum_k A[m, k] B[n, k] by 128 x BN tiles, a persistent block per SM: one
-// thread feeds a ring of stages by TMA, one issues the MMAs into one of two
-// accumulators in tensor memory, eight warps read the other out (warps 4..7 the
-// left half of its columns, 8..11 the right half, a row per lane).
-template <int BN, bool AMN, bool BMN, int EPI>
-__global__ void __launch_bounds__(kGemmThreads, 1)
-    k_head_gemm(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
-                const __grid_constant__ GemmArgs a) {
-    using S = GemmShape<BN>;
-    extern __shared__ uint8_t raw[];
-    __shared__ uint64_t full[S::kStages], empty[S::kStages], accfull[2], accempty[2], drain;
-    __shared__ uint32_t tmem_slot;
-    __shared__ int gave_up_s;
-    volatile int* gave_up = &gave_up_s;
-    const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < S::kStages; ++i) {
-            mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 1);
-        }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&accfull[i], 1);
-            mbar_init(&accempty[i], kEpiWarps);
-        }
-        mbar_init(&drain, 1);
-        gave_up_s = 0;
-    }
-    if (warp == 2) tc_alloc(&tmem_slot, 2 * BN);
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = tmem_slot;
-    uint32_t it = 0;  // stages fed (TMA thread) or consumed (MMA thread)
-    bool ok = true;
-
-    // unit -> row tile, first column tile, tiles, K range
-    auto unit = [&](int64_t u, int& m, int& n0, int& n1, int& kb, int& ke, int& split) {
-        if (EPI == kEpiOut) {  // column tiles fastest: blocks that run together share rows of A
-            const int64_t tiles = (int64_t)a.mtiles * a.ntiles;
-            split = (int)(u / tiles);
-            const int64_t t = u - split * tiles;
-            m = (int)(t / a.ntiles);
-            n0 = (int)(t - (int64_t)m * a.ntiles);
-            n1 = n0 + 1;
-            kb = (int)((int64_t)a.chunks * split / a.splits);
-            ke = (int)((int64_t)a.chunks * (split + 1) / a.splits);
-        } else {  // row tiles fastest: blocks that run together share rows of the table
-            const int s = (int)(u / a.mtiles);
-            m = (int)(u - (int64_t)s * a.mtiles);
-            n0 = s * a.strip;
-            n1 = min(n0 + a.strip, a.ntiles);
-            kb = 0;
-            ke = a.chunks;
-            split = s;
-        }
-    };
-
-    if (warp == 0) {
-        if (lane == 0) {
-            for (int64_t u = blockIdx.x; ok && u < a.units; u += gridDim.x) {
-                int m, n0, n1, kb, ke, split;
-                unit(u, m, n0, n1, kb, ke, split);
-                for (int n = n0; ok && n < n1; ++n)
-                    for (int seg = 0; ok && seg < a.nseg; ++seg) {
-                        const int za = seg == 2, zb = seg == 1;
-                        for (int kc = kb; kc < ke; ++kc, ++it) {
-                            const uint32_t st = it % S::kStages;
-                            if (!head_wait(&empty[st], ((it / S::kStages) & 1) ^ 1, a.wait_ns, gave_up)) {
-                                ok = false;
-                                break;
-                            }
-                            const uint32_t sa = base + st * S::kStage, sb = sa + S::kA;
-                            bulk_expect(&full[st], S::kStage);
-                            if (AMN) {
-                                tma_load3(sa, &mapA, m * 128, kc * kBK, za, &full[st]);
-                                tma_load3(sa + 8192, &mapA, m * 128 + 64, kc * kBK, za, &full[st]);
-                            } else {
-                                tma_load3(sa, &mapA, kc * kBK, m * 128, za, &full[st]);
-                            }
-                            if (BMN) {
-#pragma unroll
-                                for (int j = 0; j < BN / 64; ++j)
-                                    tma_load3(sb + j * 8192, &mapB, n * BN + j * 64, kc * kBK, zb, &full[st]);
-                            } else {
-                                tma_load3(sb, &mapB, kc * kBK, n * BN, zb, &full[st]);
-                            }
-                        }
-                    }
-            }
-        }
-    } else if (warp == 1) {
-        if (lane == 0) {
-            const uint32_t idesc = idesc_f16(128, BN, a.fmt, AMN, BMN);
-            uint32_t tile = 0;
-            for (int64_t u = blockIdx.x; ok && u < a.units; u += gridDim.x) {
-                int m, n0, n1, kb, ke, split;
-                unit(u, m, n0, n1, kb, ke, split);
-                for (int n = n0; ok && n < n1; ++n, ++tile) {
-                    const uint32_t buf = tile & 1;
-                    if (!head_wait(&accempty[buf], ((tile >> 1) & 1) ^ 1, a.wait_ns, gave_up)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t d = tmem + buf * BN;
-                    const int steps = (ke - kb) * a.nseg;
-                    for (int c = 0; c < steps; ++c, ++it) {
-                        const uint32_t st = it % S::kStages;
-                        if (!head_wait(&full[st], (it / S::kStages) & 1, a.wait_ns, gave_up)) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-                        const uint32_t sa = base + st * S::kStage;
-                        const uint64_t da = desc_sw128(sa, AMN), db = desc_sw128(sa + S::kA, BMN);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            mma_f16(d, da + (uint64_t)(k * (AMN ? 2048 : 32) >> 4),
-                                    db + (uint64_t)(k * (BMN ? 2048 : 32) >> 4), idesc, c > 0 || k > 0);
-                        tc_commit(&empty[st]);
-                    }
-                    if (ok) tc_commit(&accfull[buf]);
-                }
-            }
-        }
-    } else if (warp >= 4) {
-        const int half = warp >= 8, quad = warp & 3;
-        const int r = quad * 32 + lane;
-        float c = 0.f, s1 = 1.f, s2 = 1.f;
-        if (EPI == kEpiOut) {
-            s1 = exp2i(-amax_exp(a.amax_a));
-            s2 = exp2i(-amax_exp(a.amax_b));
-        } else {
-            c = a.ctemp * exp2i(-amax_exp(a.amax_a)) * exp2i(-amax_exp(a.amax_b));
-        }
-        uint32_t tile = 0;
-        for (int64_t u = blockIdx.x; ok && u < a.units; u += gridDim.x) {
-            int m, n0, n1, kb, ke, split;
-            unit(u, m, n0, n1, kb, ke, split);
-            const int64_t row = (int64_t)m * 128 + r;
-            const bool in = row < a.M;
-            float run_m = -INFINITY, run_s = 0.f, cr = c, l2 = 0.f, rs = 0.f;
-            if (EPI == kEpiStats && a.row_exp && in) cr = c * exp2i(-a.row_exp[row]);
-            if (EPI == kEpiDz && in) {
-                l2 = a.lse2[row];
-                rs = a.rowscale[row];
-            }
-            for (int n = n0; n < n1; ++n, ++tile) {
-                const uint32_t buf = tile & 1;
-                ok = __all_sync(0xffffffffu, head_wait(&accfull[buf], (tile >> 1) & 1, a.wait_ns, gave_up));
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t t0 = tmem + buf * BN + ((uint32_t)(quad * 32) << 16) + half * (BN / 2);
-                const int64_t col0 = (int64_t)n * BN + half * (BN / 2);
-#pragma unroll 1
-                for (int ch = 0; ch < BN / 64; ++ch) {
-                    float v[32];
-                    tc_ld32(t0 + ch * 32, v);
-                    const int64_t col = col0 + ch * 32;
-                    if (EPI == kEpiStats) {
-                        const int valid = (int)max((int64_t)0, min((int64_t)32, a.N - col));
-                        if (valid < 32) {
-#pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                if (j >= valid) v[j] = -INFINITY;
-                        }
-                        float mx = v[0];
-#pragma unroll
-                        for (int j = 1; j < 32; ++j) mx = fmaxf(mx, v[j]);
-                        const float mn = fmaxf(run_m, mx);
-                        const float m2 = mn == -INFINITY ? 0.f : mn * cr;
-                        float s[4] = {run_s * ex2(fmaf(run_m, cr, -m2)), 0.f, 0.f, 0.f};
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) s[j & 3] += ex2(fmaf(v[j], cr, -m2));
-                        run_s = (s[0] + s[1]) + (s[2] + s[3]);
-                        run_m = mn;
-                    } else if (EPI == kEpiDz) {
-                        if (in && col < a.dz_pitch) {
-                            float p[32];
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) p[j] = rs == 0.f ? 0.f : rs * ex2(fmaf(v[j], cr, -l2));
-                            uint4* o = reinterpret_cast<uint4*>(a.dz + row * a.dz_pitch + col);
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                uint32_t w[4];
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) w[i] = pack16(p[q * 8 + 2 * i], p[q * 8 + 2 * i + 1], a.fmt);
-                                o[q] = make_uint4(w[0], w[1], w[2], w[3]);
-                                if (a.dz_split) {
-#pragma unroll
-                                    for (int i = 0; i < 4; ++i) {
-                                        const float2 h = unpack_f16(w[i]);
-                                        w[i] = pack16(p[q * 8 + 2 * i] - h.x, p[q * 8 + 2 * i + 1] - h.y, 0);
-                                    }
-                                    *(reinterpret_cast<uint4*>(a.dz + a.dz_piece + row * a.dz_pitch + col) + q) =
-                                        make_uint4(w[0], w[1], w[2], w[3]);
-                                }
-                            }
-                        }
-                    } else if (in && col < a.N) {
-                        if (a.out) {
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) v[j] = v[j] * s1 * s2;
-                            if (a.vec && col + 32 <= a.N) {
-#pragma unroll
-                                for (int q = 0; q < 4; ++q)
-                                    store_vec(a.out, row * a.ldo + col + q * 8, v + q * 8, a.out_type);
-                            } else {
-#pragma unroll
-                                for (int j = 0; j < 32; ++j)
-                                    if (col + j < a.N) store_one(a.out, row * a.ldo + col + j, v[j], a.out_type);
-                            }
-                        } else {  // pp is a multiple of 32: whole chunks, the columns past N hold zeros
-                            float4* o = reinterpret_cast<float4*>(a.partial + ((int64_t)split * a.M + row) * a.pp + col);
-#pragma unroll
-                            for (int q = 0; q < 8; ++q) {
-                                float4 x = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-                                if (a.accumulate) {
-                                    const float4 y = o[q];
-                                    x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
-                                }
-                                o[q] = x;
-                            }
-                        }
-                    }
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&accempty[buf]);
-            }
-            if (EPI == kEpiStats && ok && in)
-                a.part[row * (2 * a.nstrips) + 2 * split + half] =
-                    make_float2(run_m == -INFINITY ? -INFINITY : run_m * cr, run_s);
-        }
-    }
-    if (!ok) {
-        *gave_up = 1;
-        if (a.err) atomicOr(a.err, kErrTimeout);
-    }
-    __syncwarp();
-    __syncthreads();
-    if (*gave_up) {  // no copy and no MMA may still be running when the block ends
-        if (threadIdx.x == 0)
-            for (uint32_t i = it > S::kStages ? it - S::kStages : 0; i < it; ++i)
-                head_drain(&full[i % S::kStages], (i / S::kStages) & 1);
-        if (threadIdx.x == 32) {
-            tc_commit(&drain);
-            head_drain(&drain, 0);
-        }
-        __syncwarp();
-        __syncthreads();
-    }
-    tc_fence_after();
-    if (warp == 2) tc_dealloc(tmem, 2 * BN);
-}
 
 // ---------------------------------------------------------------- rows and copies
 
@@ -548,11 +219,12 @@ __global__ void __launch_bounds__(kRowThreads) k_head_finish(HeadIn in, Target t
 // a row that does not count), its lse in log2 units, dz of its target entries, and
 // its packed copy (zeros for a row that does not count, so that nothing such a row
 // holds, infinities and NaN included, reaches dweight).  Entries of one row with the
-// same id hold the same value, of their summed q.
+// same id hold the same value, of their summed q.  Target entries go to an array
+// (ids_out, dzt; k_head_fix) or, ents given, into lists by 32 x 32 block (k_head_fused).
 template <class T, bool DISTILL>
 __global__ void __launch_bounds__(kRowThreads)
-    k_head_rows(HeadIn in, Target t, const float* lse, const float* grad, const uint32_t* amax, float* rowscale,
-                float* lse2, int* ids_out, float* dzt, uint16_t* hp, int* err) {
+    k_head_rows(HeadIn in, Target t, const float* lse, const float* grad, const uint32_t* amax, float2* rowc, int* ids_out,
+                float* dzt, int* heads, int nblocks, TargetEntry* ents, uint16_t* hp, int* err) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t n = blockIdx.x;
     const T* h = static_cast<const T*>(in.h) + n * in.ldh;
@@ -573,8 +245,7 @@ __global__ void __launch_bounds__(kRowThreads)
     const int ez = amax ? scale_exp(amax[2]) : 0, eh = amax ? scale_exp(amax[0]) : 0;
     const float rs = any ? grad[n] * t.T * exp2i(ez) : 0.f;
     if (threadIdx.x == 0) {
-        rowscale[n] = rs;
-        lse2[n] = l * kLog2e;
+        rowc[n] = any ? make_float2(l * kLog2e, rs) : make_float2(0.f, 0.f);
     }
     for (int k = warp; k < t.K; k += 4) {
         const int64_t id = DISTILL ? (q[k] == 0.f ? -1 : ids[k]) : xid;
@@ -591,8 +262,19 @@ __global__ void __launch_bounds__(kRowThreads)
             d = (expf(z / t.T - l) - qs) * rs;
         }
         if (lane == 0) {
-            ids_out[n * t.K + k] = (int)id;
-            dzt[n * t.K + k] = d;
+            const int64_t e = n * t.K + k;
+            if (!ents) {
+                ids_out[e] = (int)id;
+                dzt[e] = d;
+            } else if (id >= 0) {
+                // an element's entries all hold its value: their order in the list does not matter
+                TargetEntry x;
+                x.at = (int)(n & 31) | (int)(id & 31) << 5;
+                x.val = d;
+                x.pad = 0;
+                x.next = atomicExch(&heads[(id >> 5) * nblocks + (n >> 5)], (int)e);
+                ents[e] = x;
+            }
         }
     }
     const int64_t piece = in.N * in.Dp;
@@ -817,10 +499,10 @@ struct Operand {  // a 16-bit matrix the products read
     int64_t rows, cols, pitch, piece;
 };
 
-template <int BN, bool AMN, bool BMN, int EPI>
+template <int BN, bool AMN, bool BMN, int EPI, bool SPLIT>
 bool run_gemm(const Operand& A, const Operand& B, GemmArgs a, int sms, cudaStream_t st) {
     CUtensorMap ma, mb;
-    const int pieces = a.nseg > 1 ? 2 : 1;
+    const int pieces = SPLIT ? 2 : 1;
     if (!make_map(&ma, A.p, a.fmt, A.cols, A.rows, pieces, A.pitch, A.piece, AMN ? 64 : 128)) return false;
     if (!make_map(&mb, B.p, a.fmt, B.cols, B.rows, pieces, B.pitch, B.piece, BMN ? 64 : BN)) return false;
     a.mtiles = (int)cdiv(a.M, 128);
@@ -828,10 +510,49 @@ bool run_gemm(const Operand& A, const Operand& B, GemmArgs a, int sms, cudaStrea
     a.nstrips = (int)cdiv(a.ntiles, a.strip);
     a.units = EPI == kEpiOut ? (int64_t)a.mtiles * a.ntiles * a.splits : (int64_t)a.mtiles * a.nstrips;
     a.wait_ns = g_head_wait_ns;
-    auto k = k_head_gemm<BN, AMN, BMN, EPI>;
+    auto k = k_head_gemm<BN, AMN, BMN, EPI, SPLIT>;
     if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)GemmShape<BN>::kSmem) != cudaSuccess) return false;
     k<<<(unsigned)(a.units < sms ? a.units : sms), kGemmThreads, GemmShape<BN>::kSmem, st>>>(ma, mb, a);
     return cudaGetLastError() == cudaSuccess;
+}
+
+// Scores: 128-column tiles for fp32 (the ranges' sums stay in registers).
+template <int EPI>
+bool score_gemm(int bn, bool split, const Operand& A, const Operand& B, const GemmArgs& a, int sms, cudaStream_t st) {
+    if (split) return run_gemm<128, false, false, EPI, true>(A, B, a, sms, st);
+    if (bn == 128) return run_gemm<128, false, false, EPI, false>(A, B, a, sms, st);
+    return run_gemm<256, false, false, EPI, false>(A, B, a, sms, st);
+}
+
+// Gradient products.  AMN: dweight = dz^T hidden; else dhidden = dz weight.
+template <bool AMN>
+bool out_gemm(bool split, const Operand& A, const Operand& B, const GemmArgs& a, int sms, cudaStream_t st) {
+    if (split) return run_gemm<128, AMN, true, kEpiOut, true>(A, B, a, sms, st);
+    return run_gemm<256, AMN, true, kEpiOut, false>(A, B, a, sms, st);
+}
+
+template <int DT, bool SPLIT, bool COLS>
+bool run_fused(const Operand& X, const Operand& Y, FusedArgs a, int sms, cudaStream_t st) {
+    using S = FusedShape<DT, SPLIT>;
+    CUtensorMap mx, my;
+    if (!make_map(&mx, X.p, a.fmt, X.cols, X.rows, S::PC, X.pitch, X.piece, 128)) return false;
+    if (!make_map(&my, Y.p, a.fmt, Y.cols, Y.rows, S::PC, Y.pitch, Y.piece, S::BY)) return false;
+    a.X = X.rows;
+    a.Y = Y.rows;
+    a.xtiles = (int)cdiv(X.rows, 128);
+    a.ytiles = (int)cdiv(Y.rows, S::BY);
+    a.units = (int64_t)a.xtiles * a.splits;
+    a.wait_ns = g_head_wait_ns;
+    auto k = k_head_fused<DT, SPLIT, COLS>;
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem) != cudaSuccess) return false;
+    k<<<(unsigned)(a.units < sms ? a.units : sms), kFusedThreads, S::kSmem, st>>>(mx, my, a);
+    return cudaGetLastError() == cudaSuccess;
+}
+
+template <bool COLS>
+bool fused(bool split, const Operand& X, const Operand& Y, const FusedArgs& a, int sms, cudaStream_t st) {
+    if (a.D <= 64) return split ? run_fused<64, true, COLS>(X, Y, a, sms, st) : run_fused<64, false, COLS>(X, Y, a, sms, st);
+    return split ? run_fused<128, true, COLS>(X, Y, a, sms, st) : run_fused<128, false, COLS>(X, Y, a, sms, st);
 }
 
 // Column tiles per strip: the fewest rounds of tiles over the blocks, and among the
@@ -852,7 +573,7 @@ int choose_strip(int64_t mtiles, int64_t ntiles, int sms) {
 int choose_splits(int64_t tiles, int64_t chunks, int sms) {
     int best = 1;
     double bestc = 1e30;
-    for (int s = 1; s <= 64 && s <= chunks; ++s) {
+    for (int s = 1; s <= sms && s <= chunks; ++s) {
         const double c = (double)cdiv(tiles * s, sms) * (cdiv(chunks, s) + 4) + (s > 1 ? 2.0 * s : 0.0);
         if (c < bestc) bestc = c, best = s;
     }
@@ -867,9 +588,10 @@ struct Plan {
     int bn_s;                // column tile of the score products
     int strip;
     int64_t nparts;
-    int64_t P;               // vocabulary piece (backward)
+    bool fused;              // backward: dz stays on the chip (k_head_fused)
+    int64_t nblocks, vblocks;  // its 32 x 32 blocks
+    int64_t P;               // else: vocabulary piece
     int64_t pitch;           // its row pitch in dz
-    int bn_d;                // column tile of the gradient products
     int dh_splits, dw_splits;
     bool dh_direct;
     int64_t pp;              // row pitch of partial sums
@@ -882,6 +604,7 @@ tt_status make_plan(const tt_head* hd, int K, Plan* p) {
     if (hd->dtype != TT_F32 && hd->dtype != TT_BF16 && hd->dtype != TT_F16) return TT_ERR_ARG;
     if (hd->rows < 0 || hd->dim < 1 || hd->vocab < 1 || K < 1 || K > kMaxTeacher) return TT_ERR_SHAPE;
     if (hd->rows > TT_HEAD_MAX_ROWS || hd->vocab > TT_HEAD_MAX_VOCAB || hd->dim > TT_HEAD_MAX_DIM) return TT_ERR_SHAPE;
+    if (hd->rows * K > 2147483647ll) return TT_ERR_SHAPE;
     if (hd->hidden_stride < hd->dim || hd->weight_stride < hd->dim) return TT_ERR_SHAPE;
     p->type = hd->dtype;
     p->fmt = hd->dtype == TT_BF16;
@@ -906,30 +629,38 @@ tt_status make_plan(const tt_head* hd, int K, Plan* p) {
     const int64_t mt = cdiv(in.N, 128);
     // 256-column tiles read each operand row less often; 128-column tiles when the
     // wide ones would leave blocks without work
-    p->bn_s = mt * cdiv(in.V, 256) >= 2 * p->sms ? 256 : 128;
+    p->bn_s = !p->split && mt * cdiv(in.V, 256) >= 2 * p->sms ? 256 : 128;
     p->strip = choose_strip(mt, cdiv(in.V, p->bn_s), p->sms);
     p->nparts = 2 * cdiv(cdiv(in.V, p->bn_s), p->strip);
     // backward
-    const int64_t vcap = cdiv(in.V, 64) * 64;
-    int64_t P = in.N > 0 ? kDzBytes / (2 * (p->split ? 2 : 1) * in.N) : vcap;
-    P = P / 1024 * 1024;
-    if (P < 1024) P = 1024;
-    if (P >= vcap) {
-        P = vcap;
+    p->nblocks = cdiv(in.N, 32);
+    p->vblocks = cdiv(in.V, 32);
+    p->fused = in.D <= 128 && p->nblocks * p->vblocks <= kMaxBlocks;
+    if (p->fused) {
+        const int by = p->split && in.D > 64 ? 64 : 128;
+        p->dh_splits = choose_splits(mt, cdiv(in.V, by), p->sms);
+        p->dw_splits = choose_splits(cdiv(in.V, 128), cdiv(in.N, by), p->sms);
+        p->dh_direct = p->dh_splits == 1;
+        p->P = in.V;
+        p->pitch = 0;
     } else {
-        P = cdiv(cdiv(in.V, cdiv(in.V, P)), 256) * 256;  // pieces of near-equal size
+        const int64_t vcap = cdiv(in.V, 64) * 64;
+        int64_t P = in.N > 0 ? kDzBytes / (2 * (p->split ? 2 : 1) * in.N) : vcap;
+        P = P / 1024 * 1024;
+        if (P < 1024) P = 1024;
+        if (P >= vcap) {
+            P = vcap;
+        } else {
+            P = cdiv(cdiv(in.V, cdiv(in.V, P)), 256) * 256;  // pieces of near-equal size
+        }
+        p->P = P;
+        p->pitch = P;
+        const int bn = p->split ? 128 : 256;
+        const int64_t nt = cdiv(in.D, bn), lastP = in.V - (cdiv(in.V, P) - 1) * P;
+        p->dh_splits = choose_splits(mt * nt, cdiv(lastP, kBK), p->sms);
+        p->dh_direct = p->dh_splits == 1 && in.V <= P;
+        p->dw_splits = choose_splits(cdiv(P, 128) * nt, cdiv(in.N, kBK), p->sms);
     }
-    p->P = P;
-    p->pitch = P;
-    p->bn_d = in.D <= 64 ? 64 : (in.D <= 128 ? 128 : 256);
-    const int64_t nt = cdiv(in.D, p->bn_d);
-    p->dh_splits = choose_splits(mt * nt, cdiv(P, kBK) * (p->split ? 3 : 1), p->sms);
-    if (p->dh_splits > cdiv(P, kBK)) p->dh_splits = (int)cdiv(P, kBK);
-    const int64_t lastP = in.V - (cdiv(in.V, P) - 1) * P;
-    if (p->dh_splits > cdiv(lastP, kBK)) p->dh_splits = (int)cdiv(lastP, kBK);
-    p->dh_direct = p->dh_splits == 1 && in.V <= P;
-    p->dw_splits = choose_splits(cdiv(P, 128) * nt, cdiv(in.N, kBK) * (p->split ? 3 : 1), p->sms);
-    if (p->dw_splits > cdiv(in.N, kBK)) p->dw_splits = (int)(in.N > 0 ? cdiv(in.N, kBK) : 1);
     p->pp = cdiv(in.D, 32) * 32;
     return TT_OK;
 }
@@ -953,18 +684,21 @@ size_t fwd_ws(const Plan& p, void* base, FwdWs* w) {
 
 struct BwdWs {
     uint32_t* amax;
-    float *rowscale, *lse2, *dzt, *dh_part, *dw_part;
-    int* ids;
+    float2* rowc;
+    float *dzt, *dh_part, *dw_part;
+    int *ids, *heads;
+    TargetEntry* ents;
     uint16_t *hp, *wp, *dz;
 };
 size_t bwd_ws(const Plan& p, int K, void* base, BwdWs* w) {
     Arena a(base);
-    const int64_t pc = p.split ? 2 : 1;
+    const int64_t pc = p.split ? 2 : 1, nk = p.in.N * K;
     w->amax = a.get<uint32_t>(4);
-    w->rowscale = a.get<float>(p.in.N);
-    w->lse2 = a.get<float>(p.in.N);
-    w->ids = a.get<int>(p.in.N * K);
-    w->dzt = a.get<float>(p.in.N * K);
+    w->rowc = a.get<float2>(p.in.N);
+    w->ids = a.get<int>(p.fused ? 0 : nk);
+    w->dzt = a.get<float>(p.fused ? 0 : nk);
+    w->heads = a.get<int>(p.fused ? p.nblocks * p.vblocks : 0);
+    w->ents = a.get<TargetEntry>(p.fused ? nk : 0);
     w->hp = a.get<uint16_t>(pc * p.in.N * p.in.Dp);
     w->wp = a.get<uint16_t>(p.pack_w ? pc * p.in.V * p.in.Dp : 0);
     w->dz = a.get<uint16_t>(pc * p.in.N * p.pitch);
@@ -984,7 +718,6 @@ GemmArgs gemm_args(const Plan& p, int* err) {
     GemmArgs a{};
     a.strip = 1;
     a.splits = 1;
-    a.nseg = p.split ? 3 : 1;
     a.fmt = p.fmt;
     a.err = err;
     return a;
@@ -1018,21 +751,12 @@ tt_status head_forward(const Plan& p, const Target& t, float* loss, float* lse, 
     a.part = w.part;
     const Operand H{p.pack_h ? w.hp : static_cast<const uint16_t*>(in.h), in.N, in.D, p.pack_h ? in.Dp : in.ldh, in.N * in.Dp};
     const Operand W{p.pack_w ? w.wp : static_cast<const uint16_t*>(in.w), in.V, in.D, p.pack_w ? in.Dp : in.ldw, in.V * in.Dp};
-    const bool ok = p.bn_s == 256 ? run_gemm<256, false, false, kEpiStats>(H, W, a, p.sms, st)
-                                  : run_gemm<128, false, false, kEpiStats>(H, W, a, p.sms, st);
-    if (!ok) return TT_ERR_CUDA;
+    if (!score_gemm<kEpiStats>(p.bn_s, p.split, H, W, a, p.sms, st)) return TT_ERR_CUDA;
     if (distill)
         k_head_finish<T, true><<<(unsigned)in.N, kRowThreads, (size_t)t.K * 12, st>>>(in, t, w.part, (int)p.nparts, loss, lse, err);
     else
         k_head_finish<T, false><<<(unsigned)cdiv(in.N, 4), kRowThreads, 0, st>>>(in, t, w.part, (int)p.nparts, loss, lse, err);
     return launch_ok() ? TT_OK : TT_ERR_CUDA;
-}
-
-template <bool AMN>
-bool out_gemm(int bn, const Operand& A, const Operand& B, const GemmArgs& a, int sms, cudaStream_t st) {
-    if (bn == 64) return run_gemm<64, AMN, true, kEpiOut>(A, B, a, sms, st);
-    if (bn == 128) return run_gemm<128, AMN, true, kEpiOut>(A, B, a, sms, st);
-    return run_gemm<256, AMN, true, kEpiOut>(A, B, a, sms, st);
 }
 
 template <class T>
@@ -1061,19 +785,62 @@ tt_status head_backward(const Plan& p, const Target& t, const float* lse, const 
         k_head_pack<T><<<dim3(grid_of(in.V * (in.Dp / 8), 256, p.sms, 16), 1), 256, 0, st>>>(in, w.amax, w.wp, nullptr, nullptr);
         if (!launch_ok()) return TT_ERR_CUDA;
     }
+    TargetEntry* ents = p.fused ? w.ents : nullptr;
+    if (ents && cudaMemsetAsync(w.heads, 0xFF, (size_t)(p.nblocks * p.vblocks) * sizeof(int), st) != cudaSuccess) return TT_ERR_CUDA;
     if (distill)
-        k_head_rows<T, true><<<(unsigned)in.N, kRowThreads, (size_t)t.K * 12, st>>>(in, t, lse, grad, amax, w.rowscale, w.lse2, w.ids,
-                                                                                  w.dzt, w.hp, err);
+        k_head_rows<T, true><<<(unsigned)in.N, kRowThreads, (size_t)t.K * 12, st>>>(in, t, lse, grad, amax, w.rowc, w.ids, w.dzt, w.heads,
+                                                                                  (int)p.nblocks, ents, w.hp, err);
     else
-        k_head_rows<T, false><<<(unsigned)in.N, kRowThreads, 12, st>>>(in, t, lse, grad, amax, w.rowscale, w.lse2, w.ids, w.dzt, w.hp, err);
+        k_head_rows<T, false><<<(unsigned)in.N, kRowThreads, 12, st>>>(in, t, lse, grad, amax, w.rowc, w.ids, w.dzt, w.heads, (int)p.nblocks,
+                                                                     ents, w.hp, err);
     if (!launch_ok()) return TT_ERR_CUDA;
     const uint32_t *ah = amax, *aw = amax ? amax + 1 : nullptr, *az = amax ? amax + 2 : nullptr;
+    const int64_t wpitch = p.pack_w ? in.Dp : in.ldw;
+    const uint16_t* w0 = p.pack_w ? w.wp : static_cast<const uint16_t*>(in.w);
+    const Operand H{w.hp, in.N, in.D, in.Dp, in.N * in.Dp};
+    const auto dest = [&](void* out, float* partial) {
+        OutArgs o{};
+        o.out = out;
+        o.ldo = in.D;
+        o.type = p.type;
+        o.vec = ((uintptr_t)out % 16 == 0) && ((int64_t)in.D * p.esize % 16 == 0);
+        o.partial = partial;
+        o.pp = p.pp;
+        return o;
+    };
+    const auto reduce = [&](const float* partial, int splits, int64_t rows, void* out, const uint32_t* ay) {
+        k_head_reduce<<<grid_of(rows * in.D, 256, p.sms, 8), 256, 0, st>>>(partial, splits, rows, in.D, p.pp, out, in.D, p.type, az, ay);
+        return launch_ok();
+    };
+    if (p.fused) {
+        const Operand W{w0, in.V, in.D, wpitch, in.V * in.Dp};
+        FusedArgs a{};
+        a.D = in.D;
+        a.fmt = p.fmt;
+        a.err = err;
+        a.amax_h = ah;
+        a.amax_w = aw;
+        a.amax_z = az;
+        a.ctemp = kLog2e / t.T;
+        a.rowc = w.rowc;
+        a.heads = w.heads;
+        a.ents = w.ents;
+        a.nblocks = (int)p.nblocks;
+        a.vblocks = (int)p.vblocks;
+        a.splits = p.dw_splits;
+        a.to = dest(p.dw_splits > 1 ? nullptr : dw, w.dw_part);
+        if (!fused<true>(p.split, W, H, a, p.sms, st)) return TT_ERR_CUDA;
+        if (p.dw_splits > 1 && !reduce(w.dw_part, p.dw_splits, in.V, dw, ah)) return TT_ERR_CUDA;
+        a.splits = p.dh_splits;
+        a.to = dest(p.dh_direct ? dh : nullptr, w.dh_part);
+        if (!fused<false>(p.split, H, W, a, p.sms, st)) return TT_ERR_CUDA;
+        if (!p.dh_direct && !reduce(w.dh_part, p.dh_splits, in.N, dh, aw)) return TT_ERR_CUDA;
+        return TT_OK;
+    }
     const int64_t npieces = cdiv(in.V, p.P), dz_piece = in.N * p.pitch;
     for (int64_t i = 0; i < npieces; ++i) {
         const int64_t v0 = i * p.P, P = in.V - v0 < p.P ? in.V - v0 : p.P;
-        const int64_t wpitch = p.pack_w ? in.Dp : in.ldw;
-        const Operand H{w.hp, in.N, in.D, in.Dp, in.N * in.Dp};
-        const Operand W{(p.pack_w ? w.wp : static_cast<const uint16_t*>(in.w)) + v0 * wpitch, P, in.D, wpitch, in.V * in.Dp};
+        const Operand W{w0 + v0 * wpitch, P, in.D, wpitch, in.V * in.Dp};
         const Operand Z{w.dz, in.N, P, p.pitch, dz_piece};
         GemmArgs a = gemm_args(p, err);
         a.M = in.N;
@@ -1082,14 +849,11 @@ tt_status head_backward(const Plan& p, const Target& t, const float* lse, const 
         a.amax_a = ah;
         a.amax_b = aw;
         a.ctemp = kLog2e / t.T;
-        a.lse2 = w.lse2;
-        a.rowscale = w.rowscale;
+        a.rowc = w.rowc;
         a.dz = w.dz;
         a.dz_pitch = p.pitch;
         a.dz_piece = dz_piece;
-        a.dz_split = p.split;
-        bool ok = p.bn_s == 256 ? run_gemm<256, false, false, kEpiDz>(H, W, a, p.sms, st) : run_gemm<128, false, false, kEpiDz>(H, W, a, p.sms, st);
-        if (!ok) return TT_ERR_CUDA;
+        if (!score_gemm<kEpiDz>(p.bn_s, p.split, H, W, a, p.sms, st)) return TT_ERR_CUDA;
         k_head_fix<<<(unsigned)cdiv(in.N * t.K, 256), 256, 0, st>>>(w.ids, w.dzt, in.N * t.K, t.K, (int)v0, (int)P, w.dz, p.pitch, dz_piece,
                                                                 p.fmt, p.split);
         if (!launch_ok()) return TT_ERR_CUDA;
@@ -1102,17 +866,9 @@ tt_status head_backward(const Plan& p, const Target& t, const float* lse, const 
         b.amax_a = az;
         b.amax_b = ah;
         void* dwp = static_cast<uint8_t*>(dw) + (size_t)v0 * in.D * p.esize;
-        b.out = p.dw_splits > 1 ? nullptr : dwp;
-        b.ldo = in.D;
-        b.out_type = p.type;
-        b.vec = ((uintptr_t)dwp % 16 == 0) && ((int64_t)in.D * p.esize % 16 == 0);
-        b.partial = w.dw_part;
-        b.pp = p.pp;
-        if (!out_gemm<true>(p.bn_d, Z, H, b, p.sms, st)) return TT_ERR_CUDA;
-        if (p.dw_splits > 1) {
-            k_head_reduce<<<grid_of(P * in.D, 256, p.sms, 8), 256, 0, st>>>(w.dw_part, p.dw_splits, P, in.D, p.pp, dwp, in.D, p.type, az, ah);
-            if (!launch_ok()) return TT_ERR_CUDA;
-        }
+        b.to = dest(p.dw_splits > 1 ? nullptr : dwp, w.dw_part);
+        if (!out_gemm<true>(p.split, Z, H, b, p.sms, st)) return TT_ERR_CUDA;
+        if (p.dw_splits > 1 && !reduce(w.dw_part, p.dw_splits, P, dwp, ah)) return TT_ERR_CUDA;
 
         GemmArgs c = gemm_args(p, err);  // the piece's share of dhidden: [N][D] += dz W
         c.M = in.N;
@@ -1121,19 +877,11 @@ tt_status head_backward(const Plan& p, const Target& t, const float* lse, const 
         c.splits = p.dh_splits;
         c.amax_a = az;
         c.amax_b = aw;
-        c.out = p.dh_direct ? dh : nullptr;
-        c.ldo = in.D;
-        c.out_type = p.type;
-        c.vec = ((uintptr_t)dh % 16 == 0) && ((int64_t)in.D * p.esize % 16 == 0);
-        c.partial = w.dh_part;
-        c.pp = p.pp;
-        c.accumulate = i > 0;
-        if (!out_gemm<false>(p.bn_d, Z, W, c, p.sms, st)) return TT_ERR_CUDA;
+        c.to = dest(p.dh_direct ? dh : nullptr, w.dh_part);
+        c.to.accumulate = i > 0;
+        if (!out_gemm<false>(p.split, Z, W, c, p.sms, st)) return TT_ERR_CUDA;
     }
-    if (!p.dh_direct) {
-        k_head_reduce<<<grid_of(in.N * in.D, 256, p.sms, 8), 256, 0, st>>>(w.dh_part, p.dh_splits, in.N, in.D, p.pp, dh, in.D, p.type, az, aw);
-        if (!launch_ok()) return TT_ERR_CUDA;
-    }
+    if (!p.dh_direct && !reduce(w.dh_part, p.dh_splits, in.N, dh, aw)) return TT_ERR_CUDA;
     return TT_OK;
 }
 

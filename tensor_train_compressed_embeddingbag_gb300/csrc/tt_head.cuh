@@ -70,11 +70,11 @@ __device__ __forceinline__ void tma_load3(uint32_t dst, const CUtensorMap* map, 
         : "memory");
 }
 
-// Shared-memory matrix descriptor of a 128-byte-swizzled operand.
-__device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, bool mn_major) {
-    const uint64_t lbo = mn_major ? (8192u >> 4) : 1u;
-    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (lbo << 16) | ((uint64_t)(1024u >> 4) << 32) | ((uint64_t)1 << 46) |
-           ((uint64_t)2 << 61);
+// Shared-memory matrix descriptor of a 128-byte-swizzled operand; lbo: bytes between
+// the 64-index blocks of an MN-major operand.
+__device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, bool mn_major, uint32_t lbo) {
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(mn_major ? lbo >> 4 : 1u) << 16) | ((uint64_t)(1024u >> 4) << 32) |
+           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
 // Instruction descriptor of kind::f16, fp32 accumulator; fmt 0: f16, 1: bf16.
@@ -91,6 +91,49 @@ __device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t a_desc, uint64
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate)
         : "memory");
 }
+
+// The same with A in tensor memory (K-major: a row per lane, two 16-bit elements per column).
+__device__ __forceinline__ void mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate)
+        : "memory");
+}
+
+// Start reading 32 consecutive fp32 columns of this warp's 32 lanes (lane i gets its
+// row); the values may be used after tm_wait_ld on the same array.
+__device__ __forceinline__ void tm_ld32(uint32_t taddr, float (&v)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]),
+          "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]),
+          "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]),
+          "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+        : "r"(taddr));
+}
+// All reads started so far are done.  The array passes through the statement, so
+// nothing that uses it can be moved above the wait.
+__device__ __forceinline__ void tm_wait_ld(float (&v)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]),
+                   "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]), "+f"(v[18]),
+                   "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]),
+                   "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31])
+                 :
+                 : "memory");
+}
+// Write 16 columns of this warp's 32 lanes (32 16-bit elements of an A operand's row);
+// tm_wait_st makes all such writes done.
+__device__ __forceinline__ void tm_st16(uint32_t taddr, const uint32_t (&w)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]), "r"(w[8]), "r"(w[9]), "r"(w[10]), "r"(w[11]),
+        "r"(w[12]), "r"(w[13]), "r"(w[14]), "r"(w[15])
+        : "memory");
+}
+__device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -131,5 +174,72 @@ __device__ __forceinline__ int scale_exp(uint32_t absmax_bits) {
     return e < -60 ? -60 : (e > 60 ? 60 : e);
 }
 __device__ __forceinline__ float exp2i(int e) { return __int_as_float((e + 127) << 23); }
+
+__device__ __forceinline__ int amax_exp(const uint32_t* p) { return p ? scale_exp(*p) : 0; }
+
+// Where a product goes: converted rows of `out`, or (out null) fp32 partial sums, one
+// array per K range.
+struct OutArgs {
+    void* out;       // [M][ldo] of `type`
+    int64_t ldo;
+    int type;        // tt_dtype
+    int vec;         // rows of out are 16-byte aligned
+    float* partial;  // [splits][M][pp], pp a multiple of 32
+    int64_t pp;
+    int accumulate;  // add to what partial holds
+};
+
+__device__ __forceinline__ void store_vec(void* out, int64_t at, const float* v, int type) {
+    // 8 consecutive elements, 16-byte aligned
+    if (type == TT_F32) {
+        float4* o = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
+        o[0] = make_float4(v[0], v[1], v[2], v[3]);
+        o[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+        const int fmt = type == TT_BF16;
+        uint4 u;
+        u.x = pack16(v[0], v[1], fmt);
+        u.y = pack16(v[2], v[3], fmt);
+        u.z = pack16(v[4], v[5], fmt);
+        u.w = pack16(v[6], v[7], fmt);
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at) = u;
+    }
+}
+__device__ __forceinline__ void store_one(void* out, int64_t at, float v, int type) {
+    if (type == TT_F32)
+        static_cast<float*>(out)[at] = v;
+    else if (type == TT_BF16)
+        static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(v);
+    else
+        static_cast<__half*>(out)[at] = __float2half_rn(v);
+}
+
+// 32 consecutive columns [col, col + 32) of row `row`; col < N.
+__device__ __forceinline__ void store_out(const OutArgs& o, int split, int64_t row, int64_t col, int64_t M, int64_t N, float (&v)[32],
+                                          float s1, float s2) {
+    if (o.out) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = v[j] * s1 * s2;
+        if (o.vec && col + 32 <= N) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) store_vec(o.out, row * o.ldo + col + q * 8, v + q * 8, o.type);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (col + j < N) store_one(o.out, row * o.ldo + col + j, v[j], o.type);
+        }
+    } else {  // whole chunks: the columns past N hold zeros
+        float4* p = reinterpret_cast<float4*>(o.partial + ((int64_t)split * M + row) * o.pp + col);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            float4 x = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+            if (o.accumulate) {
+                const float4 y = p[q];
+                x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+            }
+            p[q] = x;
+        }
+    }
+}
 
 }  // namespace ttemb

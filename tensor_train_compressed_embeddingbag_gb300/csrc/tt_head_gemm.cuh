@@ -1,0 +1,319 @@
+// tt_head_gemm.cuh -- the vocabulary head's products of large matrices: scores with a
+// softmax epilogue, dz of a piece of the vocabulary, and the two gradient products.
+#pragma once
+
+#include "tt_head.cuh"
+
+namespace ttemb {
+
+constexpr int kGemmThreads = 384;  // warp 0: TMA, 1: MMA, 2: tensor memory, 4..11: epilogue
+constexpr int kEpiWarps = 8;
+constexpr int kBK = 64;            // K depth of a stage: one 128-byte swizzled row
+
+enum Epi { kEpiStats = 0, kEpiDz = 1, kEpiOut = 2 };
+
+struct GemmArgs {
+    int64_t M, N;      // valid rows and columns of the product
+    int mtiles, ntiles;
+    int strip;         // column tiles per unit (kEpiStats), else 1
+    int nstrips;
+    int splits;        // K ranges (kEpiOut), else 1
+    int chunks;        // K chunks of 64
+    int64_t units;
+    int fmt;           // 16-bit type of the operands: 0 f16, 1 bf16
+    uint64_t wait_ns;
+    int* err;
+    // scales: exponents of the operands' power-of-two scales come from these bits
+    const uint32_t* amax_a;
+    const uint32_t* amax_b;
+    const int* row_exp;  // per-row exponent of A (forward), else null
+    float ctemp;         // log2(e) / T
+    // kEpiStats
+    float2* part;        // [M][2 nstrips] (maximum in log2 units, sum)
+    // kEpiDz
+    const float2* rowc;  // per row (lse in log2 units, scale)
+    uint16_t* dz;        // [pieces][M][dz_pitch]
+    int64_t dz_pitch, dz_piece;
+    // kEpiOut
+    OutArgs to;
+};
+
+template <int BN>
+struct GemmShape {
+    static constexpr int kStages = BN == 256 ? 4 : (BN == 128 ? 6 : 8);
+    static constexpr uint32_t kA = 128 * 128, kB = BN * 128;
+    static constexpr uint32_t kStage = kA + kB;
+    static constexpr size_t kSmem = (size_t)kStages * kStage + 1024;
+};
+
+// C[m, n] = sum_k A[m, k] B[n, k] by 128 x BN tiles, a persistent block per SM: one
+// thread feeds a ring of stages by TMA, one issues the MMAs into one of two
+// accumulators in tensor memory, eight warps read the other out (warps 4..7 the
+// left half of its columns, 8..11 the right half, a row per lane).
+//
+// SPLIT (fp32 operands in two pieces).  The tensor core's fp32 accumulation cuts off
+// the bits below its accumulator instead of rounding them, so the error of a long sum
+// grows with its length and always in one direction.  An accumulator therefore holds
+// kRange K chunks only, its small products (lo hi, hi lo) first, and the epilogue adds
+// the ranges up in registers, rounding to nearest.
+template <int BN, bool AMN, bool BMN, int EPI, bool SPLIT>
+__global__ void __launch_bounds__(kGemmThreads, 1)
+    k_head_gemm(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
+                const __grid_constant__ GemmArgs a) {
+    using S = GemmShape<BN>;
+    static_assert(!SPLIT || BN <= 128, "the ranges' sums stay in registers");
+    constexpr int kSegs = SPLIT ? 3 : 1, kRange = 4;
+    extern __shared__ uint8_t raw[];
+    __shared__ uint64_t full[S::kStages], empty[S::kStages], accfull[2], accempty[2], drain;
+    __shared__ uint32_t tmem_slot;
+    __shared__ int gave_up_s;
+    volatile int* gave_up = &gave_up_s;
+    const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S::kStages; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&accfull[i], 1);
+            mbar_init(&accempty[i], kEpiWarps);
+        }
+        mbar_init(&drain, 1);
+        gave_up_s = 0;
+    }
+    if (warp == 2) tc_alloc(&tmem_slot, 2 * BN);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    uint32_t it = 0;   // stages fed (TMA thread) or consumed (MMA thread)
+    uint32_t acc = 0;  // accumulators filled (MMA thread) or read (epilogue)
+    bool ok = true;
+
+    // unit -> row tile, column tiles, K range, and which split or strip it is
+    auto unit = [&](int64_t u, int& m, int& n0, int& n1, int& kb, int& ke, int& split) {
+        if (EPI == kEpiOut) {  // column tiles fastest: blocks that run together share rows of A
+            const int64_t tiles = (int64_t)a.mtiles * a.ntiles;
+            split = (int)(u / tiles);
+            const int64_t t = u - split * tiles;
+            m = (int)(t / a.ntiles);
+            n0 = (int)(t - (int64_t)m * a.ntiles);
+            n1 = n0 + 1;
+            kb = (int)((int64_t)a.chunks * split / a.splits);
+            ke = (int)((int64_t)a.chunks * (split + 1) / a.splits);
+        } else {  // row tiles fastest: blocks that run together share rows of the table
+            const int s = (int)(u / a.mtiles);
+            m = (int)(u - (int64_t)s * a.mtiles);
+            n0 = s * a.strip;
+            n1 = min(n0 + a.strip, a.ntiles);
+            kb = 0;
+            ke = a.chunks;
+            split = s;
+        }
+    };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            for (int64_t u = blockIdx.x; ok && u < a.units; u += gridDim.x) {
+                int m, n0, n1, kb, ke, split;
+                unit(u, m, n0, n1, kb, ke, split);
+                for (int n = n0; ok && n < n1; ++n)
+                    for (int r0 = kb; ok && r0 < ke; r0 += SPLIT ? kRange : ke - kb) {
+                        const int r1 = SPLIT ? min(r0 + kRange, ke) : ke;
+                        for (int seg = 0; ok && seg < kSegs; ++seg) {
+                            const int za = SPLIT && seg == 0, zb = SPLIT && seg == 1;
+                            for (int kc = r0; kc < r1; ++kc, ++it) {
+                                const uint32_t st = it % S::kStages;
+                                ok = head_wait(&empty[st], ((it / S::kStages) & 1) ^ 1, a.wait_ns, gave_up);
+                                if (!ok) break;
+                                const uint32_t sa = base + st * S::kStage, sb = sa + S::kA;
+                                bulk_expect(&full[st], S::kStage);
+                                if (AMN) {
+                                    tma_load3(sa, &mapA, m * 128, kc * kBK, za, &full[st]);
+                                    tma_load3(sa + 8192, &mapA, m * 128 + 64, kc * kBK, za, &full[st]);
+                                } else {
+                                    tma_load3(sa, &mapA, kc * kBK, m * 128, za, &full[st]);
+                                }
+                                if (BMN) {
+#pragma unroll
+                                    for (int j = 0; j < BN / 64; ++j)
+                                        tma_load3(sb + j * 8192, &mapB, n * BN + j * 64, kc * kBK, zb, &full[st]);
+                                } else {
+                                    tma_load3(sb, &mapB, kc * kBK, n * BN, zb, &full[st]);
+                                }
+                            }
+                        }
+                    }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            const uint32_t idesc = idesc_f16(128, BN, a.fmt, AMN, BMN);
+            for (int64_t u = blockIdx.x; ok && u < a.units; u += gridDim.x) {
+                int m, n0, n1, kb, ke, split;
+                unit(u, m, n0, n1, kb, ke, split);
+                for (int n = n0; ok && n < n1; ++n)
+                    for (int r0 = kb; ok && r0 < ke; r0 += SPLIT ? kRange : ke - kb, ++acc) {
+                        const int steps = (SPLIT ? min(kRange, ke - r0) : ke - kb) * kSegs;
+                        const uint32_t buf = acc & 1, d = tmem + buf * BN;
+                        ok = head_wait(&accempty[buf], ((acc >> 1) & 1) ^ 1, a.wait_ns, gave_up);
+                        if (!ok) break;
+                        tc_fence_after();
+                        for (int c = 0; c < steps; ++c, ++it) {
+                            const uint32_t st = it % S::kStages;
+                            ok = head_wait(&full[st], (it / S::kStages) & 1, a.wait_ns, gave_up);
+                            if (!ok) break;
+                            tc_fence_after();
+                            const uint32_t sa = base + st * S::kStage;
+                            const uint64_t da = desc_sw128(sa, AMN, 8192), db = desc_sw128(sa + S::kA, BMN, 8192);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                mma_f16(d, da + (uint64_t)(k * (AMN ? 2048 : 32) >> 4), db + (uint64_t)(k * (BMN ? 2048 : 32) >> 4),
+                                        idesc, c > 0 || k > 0);
+                            tc_commit(&empty[st]);
+                        }
+                        if (ok) tc_commit(&accfull[buf]);
+                    }
+            }
+        }
+    } else if (warp >= 4) {
+        const int half = warp >= 8, quad = warp & 3;
+        const int r = quad * 32 + lane;
+        float c = 0.f, s1 = 1.f, s2 = 1.f;
+        if (EPI == kEpiOut) {
+            s1 = exp2i(-amax_exp(a.amax_a));
+            s2 = exp2i(-amax_exp(a.amax_b));
+        } else {
+            c = a.ctemp * exp2i(-amax_exp(a.amax_a)) * exp2i(-amax_exp(a.amax_b));
+        }
+        for (int64_t u = blockIdx.x; ok && u < a.units; u += gridDim.x) {
+            int m, n0, n1, kb, ke, split;
+            unit(u, m, n0, n1, kb, ke, split);
+            const int64_t row = (int64_t)m * 128 + r;
+            const bool in = row < a.M;
+            float run_m = -INFINITY, run_s = 0.f, cr = c;
+            float2 rc = make_float2(0.f, 0.f);
+            if (EPI == kEpiStats && a.row_exp && in) cr = c * exp2i(-a.row_exp[row]);
+            if (EPI == kEpiDz && in) rc = a.rowc[row];
+            for (int n = n0; ok && n < n1; ++n) {
+                const int64_t col0 = (int64_t)n * BN + half * (BN / 2);
+                // 32 finished columns of this thread's row, the first of them `col`
+                auto finish = [&](float (&v)[32], int64_t col) {
+                    if (EPI == kEpiStats) {
+                        const int valid = (int)max((int64_t)0, min((int64_t)32, a.N - col));
+                        if (valid < 32) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                if (j >= valid) v[j] = -INFINITY;
+                        }
+                        float mx = v[0];
+#pragma unroll
+                        for (int j = 1; j < 32; ++j) mx = fmaxf(mx, v[j]);
+                        const float mn = fmaxf(run_m, mx);
+                        const float m2 = mn == -INFINITY ? 0.f : mn * cr;
+                        float s[4] = {run_s * ex2(fmaf(run_m, cr, -m2)), 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) s[j & 3] += ex2(fmaf(v[j], cr, -m2));
+                        run_s = (s[0] + s[1]) + (s[2] + s[3]);
+                        run_m = mn;
+                    } else if (EPI == kEpiDz) {
+                        if (in && col < a.dz_pitch) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) v[j] = rc.y == 0.f ? 0.f : rc.y * ex2(fmaf(v[j], cr, -rc.x));
+                            uint4* o = reinterpret_cast<uint4*>(a.dz + row * a.dz_pitch + col);
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                uint32_t w[4];
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) w[i] = pack16(v[q * 8 + 2 * i], v[q * 8 + 2 * i + 1], a.fmt);
+                                o[q] = make_uint4(w[0], w[1], w[2], w[3]);
+                                if (SPLIT) {
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i) {
+                                        const float2 h = unpack_f16(w[i]);
+                                        w[i] = pack16(v[q * 8 + 2 * i] - h.x, v[q * 8 + 2 * i + 1] - h.y, 0);
+                                    }
+                                    *(reinterpret_cast<uint4*>(a.dz + a.dz_piece + row * a.dz_pitch + col) + q) =
+                                        make_uint4(w[0], w[1], w[2], w[3]);
+                                }
+                            }
+                        }
+                    } else if (in && col < a.N) {
+                        store_out(a.to, split, row, col, a.M, a.N, v, s1, s2);
+                    }
+                };
+                if (SPLIT) {
+                    float sum[BN / 64][32];
+                    for (int r0 = kb; ok && r0 < ke; r0 += kRange, ++acc) {
+                        const uint32_t buf = acc & 1;
+                        ok = __all_sync(0xffffffffu, head_wait(&accfull[buf], (acc >> 1) & 1, a.wait_ns, gave_up));
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t t0 = tmem + buf * BN + ((uint32_t)(quad * 32) << 16) + half * (BN / 2);
+#pragma unroll
+                        for (int ch = 0; ch < BN / 64; ++ch) {
+                            float v[32];
+                            tm_ld32(t0 + ch * 32, v);
+                            tm_wait_ld(v);
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) sum[ch][j] = r0 == kb ? v[j] : sum[ch][j] + v[j];
+                        }
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&accempty[buf]);
+                    }
+                    if (!ok) break;
+#pragma unroll
+                    for (int ch = 0; ch < BN / 64; ++ch) finish(sum[ch], col0 + ch * 32);
+                } else {
+                    const uint32_t buf = acc & 1;
+                    ok = __all_sync(0xffffffffu, head_wait(&accfull[buf], (acc >> 1) & 1, a.wait_ns, gave_up));
+                    if (!ok) break;
+                    ++acc;
+                    tc_fence_after();
+                    const uint32_t t0 = tmem + buf * BN + ((uint32_t)(quad * 32) << 16) + half * (BN / 2);
+                    // the next 32 columns are on their way while these are worked on
+                    constexpr int kCh = BN / 64;
+                    float v[2][32];
+                    tm_ld32(t0, v[0]);
+                    tm_wait_ld(v[0]);
+#pragma unroll
+                    for (int ch = 0; ch < kCh; ++ch) {
+                        if (ch + 1 < kCh) tm_ld32(t0 + (ch + 1) * 32, v[(ch + 1) & 1]);
+                        finish(v[ch & 1], col0 + ch * 32);
+                        if (ch + 1 < kCh) tm_wait_ld(v[(ch + 1) & 1]);
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&accempty[buf]);
+                }
+            }
+            if (EPI == kEpiStats && ok && in)
+                a.part[row * (2 * a.nstrips) + 2 * split + half] =
+                    make_float2(run_m == -INFINITY ? -INFINITY : run_m * cr, run_s);
+        }
+    }
+    if (!ok) {
+        *gave_up = 1;
+        if (a.err) atomicOr(a.err, kErrTimeout);
+    }
+    __syncwarp();
+    __syncthreads();
+    if (*gave_up) {  // no copy and no MMA may still be running when the block ends
+        if (threadIdx.x == 0)
+            for (uint32_t i = it > S::kStages ? it - S::kStages : 0; i < it; ++i)
+                head_drain(&full[i % S::kStages], (i / S::kStages) & 1);
+        if (threadIdx.x == 32) {
+            tc_commit(&drain);
+            head_drain(&drain, 0);
+        }
+        __syncwarp();
+        __syncthreads();
+    }
+    tc_fence_after();
+    if (warp == 2) tc_dealloc(tmem, 2 * BN);
+}
+
+}  // namespace ttemb
