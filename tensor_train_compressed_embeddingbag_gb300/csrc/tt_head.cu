@@ -36,7 +36,7 @@
 namespace ttemb {
 
 constexpr int64_t kDzBytes = 256ll << 20;  // dz of one vocabulary piece
-constexpr int64_t kMaxBlocks = 1ll << 28;    // 32 x 32 blocks of targets (1 GB of list heads)
+constexpr int64_t kMaxBlocks = 1ll << 26;    // 32 x 32 blocks of targets (1 GB of them)
 constexpr int kMaxTeacher = TT_HEAD_MAX_TEACHER;
 
 // ---------------------------------------------------------------- rows and copies
@@ -220,11 +220,11 @@ __global__ void __launch_bounds__(kRowThreads) k_head_finish(HeadIn in, Target t
 // its packed copy (zeros for a row that does not count, so that nothing such a row
 // holds, infinities and NaN included, reaches dweight).  Entries of one row with the
 // same id hold the same value, of their summed q.  Target entries go to an array
-// (ids_out, dzt; k_head_fix) or, ents given, into lists by 32 x 32 block (k_head_fused).
+// (ids_out, dzt; k_head_fix) or, ents given, to their 32 x 32 blocks (k_head_fused).
 template <class T, bool DISTILL>
 __global__ void __launch_bounds__(kRowThreads)
     k_head_rows(HeadIn in, Target t, const float* lse, const float* grad, const uint32_t* amax, float2* rowc, int* ids_out,
-                float* dzt, int* heads, int nblocks, TargetEntry* ents, uint16_t* hp, int* err) {
+                float* dzt, TargetBlock* blocks, int nblocks, TargetEntry* ents, uint16_t* hp, int* err) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t n = blockIdx.x;
     const T* h = static_cast<const T*>(in.h) + n * in.ldh;
@@ -250,13 +250,19 @@ __global__ void __launch_bounds__(kRowThreads)
     for (int k = warp; k < t.K; k += 4) {
         const int64_t id = DISTILL ? (q[k] == 0.f ? -1 : ids[k]) : xid;
         float d = 0.f;
+        bool again = false;  // an earlier entry has the same id
         if (id >= 0) {
             float qs = 1.f;
             if (DISTILL) {
                 qs = 0.f;
+                bool earlier = false;
                 for (int j = lane; j < t.K; j += 32)
-                    if (ids[j] == id) qs += q[j];
+                    if (ids[j] == id && q[j] != 0.f) {
+                        qs += q[j];
+                        earlier |= j < k;
+                    }
                 qs = warp_sum(qs);
+                again = __any_sync(0xffffffffu, earlier);
             }
             const float z = warp_dot(h, w + id * in.ldw, in.D, in.vec, lane);
             d = (expf(z / t.T - l) - qs) * rs;
@@ -266,14 +272,8 @@ __global__ void __launch_bounds__(kRowThreads)
             if (!ents) {
                 ids_out[e] = (int)id;
                 dzt[e] = d;
-            } else if (id >= 0) {
-                // an element's entries all hold its value: their order in the list does not matter
-                TargetEntry x;
-                x.at = (int)(n & 31) | (int)(id & 31) << 5;
-                x.val = d;
-                x.pad = 0;
-                x.next = atomicExch(&heads[(id >> 5) * nblocks + (n >> 5)], (int)e);
-                ents[e] = x;
+            } else if (id >= 0 && !again) {
+                add_target(&blocks[(id >> 5) * nblocks + (n >> 5)], ents, (int)e, (int)(n & 31) | (int)(id & 31) << 5, d);
             }
         }
     }
@@ -541,11 +541,11 @@ bool run_fused(const Operand& X, const Operand& Y, FusedArgs a, int sms, cudaStr
     a.Y = Y.rows;
     a.xtiles = (int)cdiv(X.rows, 128);
     a.ytiles = (int)cdiv(Y.rows, S::BY);
-    a.units = (int64_t)a.xtiles * a.splits;
+    a.units = a.xtiles * a.splits;
     a.wait_ns = g_head_wait_ns;
     auto k = k_head_fused<DT, SPLIT, COLS>;
     if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem) != cudaSuccess) return false;
-    k<<<(unsigned)(a.units < sms ? a.units : sms), kFusedThreads, S::kSmem, st>>>(mx, my, a);
+    k<<<(unsigned)(a.units < sms ? a.units : sms), S::kThreads, S::kSmem, st>>>(mx, my, a);
     return cudaGetLastError() == cudaSuccess;
 }
 
@@ -631,7 +631,7 @@ tt_status make_plan(const tt_head* hd, int K, Plan* p) {
     // wide ones would leave blocks without work
     p->bn_s = !p->split && mt * cdiv(in.V, 256) >= 2 * p->sms ? 256 : 128;
     p->strip = choose_strip(mt, cdiv(in.V, p->bn_s), p->sms);
-    p->nparts = 2 * cdiv(cdiv(in.V, p->bn_s), p->strip);
+    p->nparts = kParts * cdiv(cdiv(in.V, p->bn_s), p->strip);
     // backward
     p->nblocks = cdiv(in.N, 32);
     p->vblocks = cdiv(in.V, 32);
@@ -686,7 +686,8 @@ struct BwdWs {
     uint32_t* amax;
     float2* rowc;
     float *dzt, *dh_part, *dw_part;
-    int *ids, *heads;
+    int* ids;
+    TargetBlock* blocks;
     TargetEntry* ents;
     uint16_t *hp, *wp, *dz;
 };
@@ -697,7 +698,7 @@ size_t bwd_ws(const Plan& p, int K, void* base, BwdWs* w) {
     w->rowc = a.get<float2>(p.in.N);
     w->ids = a.get<int>(p.fused ? 0 : nk);
     w->dzt = a.get<float>(p.fused ? 0 : nk);
-    w->heads = a.get<int>(p.fused ? p.nblocks * p.vblocks : 0);
+    w->blocks = a.get<TargetBlock>(p.fused ? p.nblocks * p.vblocks : 0);
     w->ents = a.get<TargetEntry>(p.fused ? nk : 0);
     w->hp = a.get<uint16_t>(pc * p.in.N * p.in.Dp);
     w->wp = a.get<uint16_t>(p.pack_w ? pc * p.in.V * p.in.Dp : 0);
@@ -786,12 +787,12 @@ tt_status head_backward(const Plan& p, const Target& t, const float* lse, const 
         if (!launch_ok()) return TT_ERR_CUDA;
     }
     TargetEntry* ents = p.fused ? w.ents : nullptr;
-    if (ents && cudaMemsetAsync(w.heads, 0xFF, (size_t)(p.nblocks * p.vblocks) * sizeof(int), st) != cudaSuccess) return TT_ERR_CUDA;
+    if (ents && cudaMemsetAsync(w.blocks, 0, (size_t)(p.nblocks * p.vblocks) * sizeof(TargetBlock), st) != cudaSuccess) return TT_ERR_CUDA;
     if (distill)
-        k_head_rows<T, true><<<(unsigned)in.N, kRowThreads, (size_t)t.K * 12, st>>>(in, t, lse, grad, amax, w.rowc, w.ids, w.dzt, w.heads,
+        k_head_rows<T, true><<<(unsigned)in.N, kRowThreads, (size_t)t.K * 12, st>>>(in, t, lse, grad, amax, w.rowc, w.ids, w.dzt, w.blocks,
                                                                                   (int)p.nblocks, ents, w.hp, err);
     else
-        k_head_rows<T, false><<<(unsigned)in.N, kRowThreads, 12, st>>>(in, t, lse, grad, amax, w.rowc, w.ids, w.dzt, w.heads, (int)p.nblocks,
+        k_head_rows<T, false><<<(unsigned)in.N, kRowThreads, 12, st>>>(in, t, lse, grad, amax, w.rowc, w.ids, w.dzt, w.blocks, (int)p.nblocks,
                                                                      ents, w.hp, err);
     if (!launch_ok()) return TT_ERR_CUDA;
     const uint32_t *ah = amax, *aw = amax ? amax + 1 : nullptr, *az = amax ? amax + 2 : nullptr;
@@ -823,7 +824,7 @@ tt_status head_backward(const Plan& p, const Target& t, const float* lse, const 
         a.amax_z = az;
         a.ctemp = kLog2e / t.T;
         a.rowc = w.rowc;
-        a.heads = w.heads;
+        a.blocks = w.blocks;
         a.ents = w.ents;
         a.nblocks = (int)p.nblocks;
         a.vblocks = (int)p.vblocks;

@@ -21,12 +21,6 @@ namespace ttemb {
 
 constexpr uint64_t kHeadWaitNs = 2000000000ull;  // default bound of a device wait (2 s)
 
-__device__ __forceinline__ uint64_t global_ns() {
-    uint64_t t;
-    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
-    return t;
-}
-
 __device__ __forceinline__ bool mbar_try(uint64_t* bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
@@ -37,22 +31,25 @@ __device__ __forceinline__ bool mbar_try(uint64_t* bar, uint32_t parity) {
     return ok != 0;
 }
 
-// Wait for the phase of the given parity for at most `ns` nanoseconds, or until
-// another role of the block gave up; false if the phase did not complete.
+// A warp's wait for the phase of the given parity, for at most `ns` nanoseconds (counted
+// as two SM cycles each, which is a little long) or until another role of the block gave
+// up; false if the phase did not complete.  The answer is the same in every lane, and
+// known to the compiler to be so: what the TMA and MMA warps compute between waits
+// stays in uniform registers, where the tensor instructions take their operands from.
 __device__ __forceinline__ bool head_wait(uint64_t* bar, uint32_t parity, uint64_t ns, volatile int* gave_up) {
-    if (mbar_try(bar, parity)) return true;
-    const uint64_t t0 = global_ns();
-    while (!mbar_try(bar, parity)) {
-        if (*gave_up || global_ns() - t0 >= ns) return false;
+    if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return true;
+    const int64_t t0 = clock64();
+    while (!__all_sync(0xffffffffu, mbar_try(bar, parity))) {
+        if (__any_sync(0xffffffffu, *gave_up || (uint64_t)(clock64() - t0) >= 2 * ns)) return false;
     }
     return true;
 }
 
 // The same wait without the early way out, for copies and MMAs in flight.
 __device__ __forceinline__ void head_drain(uint64_t* bar, uint32_t parity) {
-    const uint64_t t0 = global_ns();
+    const int64_t t0 = clock64();
     while (!mbar_try(bar, parity)) {
-        if (global_ns() - t0 >= kHeadWaitNs) return;
+        if ((uint64_t)(clock64() - t0) >= 2 * kHeadWaitNs) return;
     }
 }
 
@@ -70,12 +67,12 @@ __device__ __forceinline__ void tma_load3(uint32_t dst, const CUtensorMap* map, 
         : "memory");
 }
 
-// Shared-memory matrix descriptor of a 128-byte-swizzled operand; lbo: bytes between
-// the 64-index blocks of an MN-major operand.
-__device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, bool mn_major, uint32_t lbo) {
-    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(mn_major ? lbo >> 4 : 1u) << 16) | ((uint64_t)(1024u >> 4) << 32) |
-           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
-}
+// Shared-memory matrix descriptor of a 128-byte-swizzled operand, in two words: the
+// start address (moving along K or to another tile adds to it) with the leading byte
+// offset (lbo: bytes between the 64-index blocks of an MN-major operand), and the rest.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) { return (saddr >> 4) | (lbo >> 4 << 16); }
+constexpr uint32_t kDescHi = (1024u >> 4) | 1u << 14 | 2u << 29;  // stride 1,024 bytes, version, 128-byte swizzle
+constexpr uint32_t kNoLbo = 16;                                   // K-major: unused, written as 1
 
 // Instruction descriptor of kind::f16, fp32 accumulator; fmt 0: f16, 1: bf16.
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int fmt, bool a_mn, bool b_mn) {
@@ -83,22 +80,51 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int fmt, bool a_m
            ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-__device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                        bool accumulate) {
+// One MMA (K = 16), run by a whole warp and issued by the lane whose `lead` is set.
+__device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, bool accumulate, bool lead) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate)
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "mov.b64 da, {%1, %6};\n\tmov.b64 db, {%2, %6};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"((uint32_t)accumulate), "r"((uint32_t)lead), "r"(kDescHi)
         : "memory");
 }
 
 // The same with A in tensor memory (K-major: a row per lane, two 16-bit elements per column).
-__device__ __forceinline__ void mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, bool accumulate) {
+__device__ __forceinline__ void mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, bool accumulate, bool lead) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate)
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 db;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "mov.b64 db, {%2, %6};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"((uint32_t)accumulate), "r"((uint32_t)lead), "r"(kDescHi)
         : "memory");
+}
+
+// The mbarrier's phase completes when every MMA issued so far by the lead lane is done.
+__device__ __forceinline__ void mma_commit(uint64_t* bar, bool lead) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_addr(bar)),
+        "r"((uint32_t)lead)
+        : "memory");
+}
+
+// Two fp32 operations in one instruction, each rounded as the single one is.
+__device__ __forceinline__ void fma2(float& x, float& y, float ax, float ay, float bx, float by) {
+    asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\tmov.b64 c, {%4, %5};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "+f"(x), "+f"(y)
+        : "f"(ax), "f"(ay), "f"(bx), "f"(by));
+}
+__device__ __forceinline__ void mul2(float& x, float& y, float ax, float ay) {
+    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\tmul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "+f"(x), "+f"(y)
+        : "f"(ax), "f"(ay));
+}
+__device__ __forceinline__ void add2(float& x, float& y, float ax, float ay) {
+    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\tadd.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "+f"(x), "+f"(y)
+        : "f"(ax), "f"(ay));
 }
 
 // Start reading 32 consecutive fp32 columns of this warp's 32 lanes (lane i gets its
@@ -123,6 +149,16 @@ __device__ __forceinline__ void tm_wait_ld(float (&v)[32]) {
                    "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31])
                  :
                  : "memory");
+}
+// The same for 16 columns, waited for at once.
+__device__ __forceinline__ void tm_read16(uint32_t taddr, float (&v)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]),
+          "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+        : "r"(taddr)
+        : "memory");
 }
 // Write 16 columns of this warp's 32 lanes (32 16-bit elements of an A operand's row);
 // tm_wait_st makes all such writes done.

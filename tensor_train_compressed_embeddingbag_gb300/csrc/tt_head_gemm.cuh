@@ -6,8 +6,9 @@
 
 namespace ttemb {
 
-constexpr int kGemmThreads = 384;  // warp 0: TMA, 1: MMA, 2: tensor memory, 4..11: epilogue
-constexpr int kEpiWarps = 8;
+constexpr int kEpiWarps = 16;
+constexpr int kGemmThreads = (4 + kEpiWarps) * 32;  // warp 0: TMA, 1: MMA, 2: tensor memory, 4..: epilogue
+constexpr int kParts = kEpiWarps / 4;               // column parts of a tile, a warp per part and 32 rows
 constexpr int kBK = 64;            // K depth of a stage: one 128-byte swizzled row
 
 enum Epi { kEpiStats = 0, kEpiDz = 1, kEpiOut = 2 };
@@ -29,7 +30,7 @@ struct GemmArgs {
     const int* row_exp;  // per-row exponent of A (forward), else null
     float ctemp;         // log2(e) / T
     // kEpiStats
-    float2* part;        // [M][2 nstrips] (maximum in log2 units, sum)
+    float2* part;        // [M][nstrips][kParts] (maximum in log2 units, sum)
     // kEpiDz
     const float2* rowc;  // per row (lse in log2 units, scale)
     uint16_t* dz;        // [pieces][M][dz_pitch]
@@ -48,8 +49,8 @@ struct GemmShape {
 
 // C[m, n] = sum_k A[m, k] B[n, k] by 128 x BN tiles, a persistent block per SM: one
 // thread feeds a ring of stages by TMA, one issues the MMAs into one of two
-// accumulators in tensor memory, eight warps read the other out (warps 4..7 the
-// left half of its columns, 8..11 the right half, a row per lane).
+// accumulators in tensor memory, sixteen warps read the other out, a quarter of its
+// columns and 32 of its rows each, a row per lane.
 //
 // SPLIT (fp32 operands in two pieces).  The tensor core's fp32 accumulation cuts off
 // the bits below its accumulator instead of rounding them, so the error of a long sum
@@ -61,15 +62,17 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     k_head_gemm(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
                 const __grid_constant__ GemmArgs a) {
     using S = GemmShape<BN>;
-    static_assert(!SPLIT || BN <= 128, "the ranges' sums stay in registers");
+    static_assert(BN % (32 * kParts) == 0 && (!SPLIT || BN <= 128), "the ranges' sums stay in registers");
     constexpr int kSegs = SPLIT ? 3 : 1, kRange = 4;
+    constexpr int kCh = BN / kParts / 32;  // 32-column chunks of a part
     extern __shared__ uint8_t raw[];
     __shared__ uint64_t full[S::kStages], empty[S::kStages], accfull[2], accempty[2], drain;
     __shared__ uint32_t tmem_slot;
     __shared__ int gave_up_s;
     volatile int* gave_up = &gave_up_s;
     const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const bool lead = lane == 0;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::kStages; ++i) {
@@ -115,19 +118,19 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     };
 
     if (warp == 0) {
-        if (lane == 0) {
-            for (int64_t u = blockIdx.x; ok && u < a.units; u += gridDim.x) {
-                int m, n0, n1, kb, ke, split;
-                unit(u, m, n0, n1, kb, ke, split);
-                for (int n = n0; ok && n < n1; ++n)
-                    for (int r0 = kb; ok && r0 < ke; r0 += SPLIT ? kRange : ke - kb) {
-                        const int r1 = SPLIT ? min(r0 + kRange, ke) : ke;
-                        for (int seg = 0; ok && seg < kSegs; ++seg) {
-                            const int za = SPLIT && seg == 0, zb = SPLIT && seg == 1;
-                            for (int kc = r0; kc < r1; ++kc, ++it) {
-                                const uint32_t st = it % S::kStages;
-                                ok = head_wait(&empty[st], ((it / S::kStages) & 1) ^ 1, a.wait_ns, gave_up);
-                                if (!ok) break;
+        for (int64_t u = blockIdx.x; ok && u < a.units; u += gridDim.x) {
+            int m, n0, n1, kb, ke, split;
+            unit(u, m, n0, n1, kb, ke, split);
+            for (int n = n0; ok && n < n1; ++n)
+                for (int r0 = kb; ok && r0 < ke; r0 += SPLIT ? kRange : ke - kb) {
+                    const int r1 = SPLIT ? min(r0 + kRange, ke) : ke;
+                    for (int seg = 0; ok && seg < kSegs; ++seg) {
+                        const int za = SPLIT && seg == 0, zb = SPLIT && seg == 1;
+                        for (int kc = r0; kc < r1; ++kc, ++it) {
+                            const uint32_t st = it % S::kStages;
+                            ok = head_wait(&empty[st], ((it / S::kStages) & 1) ^ 1, a.wait_ns, gave_up);
+                            if (!ok) break;
+                            if (lead) {
                                 const uint32_t sa = base + st * S::kStage, sb = sa + S::kA;
                                 bulk_expect(&full[st], S::kStage);
                                 if (AMN) {
@@ -144,42 +147,40 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                                     tma_load3(sb, &mapB, kc * kBK, n * BN, zb, &full[st]);
                                 }
                             }
+                            __syncwarp();
                         }
                     }
-            }
+                }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            const uint32_t idesc = idesc_f16(128, BN, a.fmt, AMN, BMN);
-            for (int64_t u = blockIdx.x; ok && u < a.units; u += gridDim.x) {
-                int m, n0, n1, kb, ke, split;
-                unit(u, m, n0, n1, kb, ke, split);
-                for (int n = n0; ok && n < n1; ++n)
-                    for (int r0 = kb; ok && r0 < ke; r0 += SPLIT ? kRange : ke - kb, ++acc) {
-                        const int steps = (SPLIT ? min(kRange, ke - r0) : ke - kb) * kSegs;
-                        const uint32_t buf = acc & 1, d = tmem + buf * BN;
-                        ok = head_wait(&accempty[buf], ((acc >> 1) & 1) ^ 1, a.wait_ns, gave_up);
+        const uint32_t idesc = idesc_f16(128, BN, a.fmt, AMN, BMN);
+        const uint32_t da0 = desc_lo(base, AMN ? 8192 : kNoLbo), db0 = desc_lo(base + S::kA, BMN ? 8192 : kNoLbo);
+        for (int64_t u = blockIdx.x; ok && u < a.units; u += gridDim.x) {
+            int m, n0, n1, kb, ke, split;
+            unit(u, m, n0, n1, kb, ke, split);
+            for (int n = n0; ok && n < n1; ++n)
+                for (int r0 = kb; ok && r0 < ke; r0 += SPLIT ? kRange : ke - kb, ++acc) {
+                    const int steps = (SPLIT ? min(kRange, ke - r0) : ke - kb) * kSegs;
+                    const uint32_t buf = acc & 1, d = tmem + buf * BN;
+                    ok = head_wait(&accempty[buf], ((acc >> 1) & 1) ^ 1, a.wait_ns, gave_up);
+                    if (!ok) break;
+                    tc_fence_after();
+                    for (int c = 0; c < steps; ++c, ++it) {
+                        const uint32_t st = it % S::kStages;
+                        ok = head_wait(&full[st], (it / S::kStages) & 1, a.wait_ns, gave_up);
                         if (!ok) break;
                         tc_fence_after();
-                        for (int c = 0; c < steps; ++c, ++it) {
-                            const uint32_t st = it % S::kStages;
-                            ok = head_wait(&full[st], (it / S::kStages) & 1, a.wait_ns, gave_up);
-                            if (!ok) break;
-                            tc_fence_after();
-                            const uint32_t sa = base + st * S::kStage;
-                            const uint64_t da = desc_sw128(sa, AMN, 8192), db = desc_sw128(sa + S::kA, BMN, 8192);
+                        const uint32_t da = da0 + st * (S::kStage >> 4), db = db0 + st * (S::kStage >> 4);
 #pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                mma_f16(d, da + (uint64_t)(k * (AMN ? 2048 : 32) >> 4), db + (uint64_t)(k * (BMN ? 2048 : 32) >> 4),
-                                        idesc, c > 0 || k > 0);
-                            tc_commit(&empty[st]);
-                        }
-                        if (ok) tc_commit(&accfull[buf]);
+                        for (int k = 0; k < 4; ++k)
+                            mma_f16(d, da + k * ((AMN ? 2048 : 32) >> 4), db + k * ((BMN ? 2048 : 32) >> 4), idesc, c > 0 || k > 0, lead);
+                        mma_commit(&empty[st], lead);
                     }
-            }
+                    if (ok) mma_commit(&accfull[buf], lead);
+                }
         }
     } else if (warp >= 4) {
-        const int half = warp >= 8, quad = warp & 3;
+        const int part = (warp - 4) >> 2, quad = warp & 3;
         const int r = quad * 32 + lane;
         float c = 0.f, s1 = 1.f, s2 = 1.f;
         if (EPI == kEpiOut) {
@@ -198,7 +199,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             if (EPI == kEpiStats && a.row_exp && in) cr = c * exp2i(-a.row_exp[row]);
             if (EPI == kEpiDz && in) rc = a.rowc[row];
             for (int n = n0; ok && n < n1; ++n) {
-                const int64_t col0 = (int64_t)n * BN + half * (BN / 2);
+                const int64_t col0 = (int64_t)n * BN + part * (BN / kParts);
                 // 32 finished columns of this thread's row, the first of them `col`
                 auto finish = [&](float (&v)[32], int64_t col) {
                     if (EPI == kEpiStats) {
@@ -215,7 +216,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                         const float m2 = mn == -INFINITY ? 0.f : mn * cr;
                         float s[4] = {run_s * ex2(fmaf(run_m, cr, -m2)), 0.f, 0.f, 0.f};
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) s[j & 3] += ex2(fmaf(v[j], cr, -m2));
+                        for (int j = 0; j < 32; j += 4) {
+                            fma2(v[j], v[j + 1], cr, cr, -m2, -m2);
+                            fma2(v[j + 2], v[j + 3], cr, cr, -m2, -m2);
+                            add2(s[0], s[1], ex2(v[j]), ex2(v[j + 1]));
+                            add2(s[2], s[3], ex2(v[j + 2]), ex2(v[j + 3]));
+                        }
                         run_s = (s[0] + s[1]) + (s[2] + s[3]);
                         run_m = mn;
                     } else if (EPI == kEpiDz) {
@@ -245,15 +251,15 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     }
                 };
                 if (SPLIT) {
-                    float sum[BN / 64][32];
+                    float sum[kCh][32];
                     for (int r0 = kb; ok && r0 < ke; r0 += kRange, ++acc) {
                         const uint32_t buf = acc & 1;
-                        ok = __all_sync(0xffffffffu, head_wait(&accfull[buf], (acc >> 1) & 1, a.wait_ns, gave_up));
+                        ok = head_wait(&accfull[buf], (acc >> 1) & 1, a.wait_ns, gave_up);
                         if (!ok) break;
                         tc_fence_after();
-                        const uint32_t t0 = tmem + buf * BN + ((uint32_t)(quad * 32) << 16) + half * (BN / 2);
+                        const uint32_t t0 = tmem + buf * BN + ((uint32_t)(quad * 32) << 16) + part * (BN / kParts);
 #pragma unroll
-                        for (int ch = 0; ch < BN / 64; ++ch) {
+                        for (int ch = 0; ch < kCh; ++ch) {
                             float v[32];
                             tm_ld32(t0 + ch * 32, v);
                             tm_wait_ld(v);
@@ -266,16 +272,15 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     }
                     if (!ok) break;
 #pragma unroll
-                    for (int ch = 0; ch < BN / 64; ++ch) finish(sum[ch], col0 + ch * 32);
+                    for (int ch = 0; ch < kCh; ++ch) finish(sum[ch], col0 + ch * 32);
                 } else {
                     const uint32_t buf = acc & 1;
-                    ok = __all_sync(0xffffffffu, head_wait(&accfull[buf], (acc >> 1) & 1, a.wait_ns, gave_up));
+                    ok = head_wait(&accfull[buf], (acc >> 1) & 1, a.wait_ns, gave_up);
                     if (!ok) break;
                     ++acc;
                     tc_fence_after();
-                    const uint32_t t0 = tmem + buf * BN + ((uint32_t)(quad * 32) << 16) + half * (BN / 2);
+                    const uint32_t t0 = tmem + buf * BN + ((uint32_t)(quad * 32) << 16) + part * (BN / kParts);
                     // the next 32 columns are on their way while these are worked on
-                    constexpr int kCh = BN / 64;
                     float v[2][32];
                     tm_ld32(t0, v[0]);
                     tm_wait_ld(v[0]);
@@ -291,11 +296,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 }
             }
             if (EPI == kEpiStats && ok && in)
-                a.part[row * (2 * a.nstrips) + 2 * split + half] =
+                a.part[(row * a.nstrips + split) * kParts + part] =
                     make_float2(run_m == -INFINITY ? -INFINITY : run_m * cr, run_s);
         }
     }
-    if (!ok) {
+    if (!ok && lead) {
         *gave_up = 1;
         if (a.err) atomicOr(a.err, kErrTimeout);
     }
@@ -306,7 +311,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             for (uint32_t i = it > S::kStages ? it - S::kStages : 0; i < it; ++i)
                 head_drain(&full[i % S::kStages], (i / S::kStages) & 1);
         if (threadIdx.x == 32) {
-            tc_commit(&drain);
+            mma_commit(&drain, true);
             head_drain(&drain, 0);
         }
         __syncwarp();
