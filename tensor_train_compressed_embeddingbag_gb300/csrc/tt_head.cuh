@@ -198,6 +198,16 @@ __device__ __forceinline__ uint32_t pack16(float a, float b, int fmt) {
         asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
     return r;
 }
+// 32 floats rounded and packed; one branch on the type.
+__device__ __forceinline__ void pack32(const float (&p)[32], uint32_t (&q)[16], int fmt) {
+    if (fmt) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) q[j] = pack16(p[2 * j], p[2 * j + 1], 1);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) q[j] = pack16(p[2 * j], p[2 * j + 1], 0);
+    }
+}
 __device__ __forceinline__ float2 unpack_f16(uint32_t v) { return __half22float2(*reinterpret_cast<__half2*>(&v)); }
 
 // Power of two that brings a tensor whose largest magnitude has these fp32 bits

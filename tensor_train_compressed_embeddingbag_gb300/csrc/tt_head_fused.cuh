@@ -5,20 +5,20 @@
 //   dweight[v] = sum_n dz[n, v] hidden[n]        resident rows: weight, streamed: hidden
 //
 // One kernel for both: a block holds 128 resident rows X and streams tiles of BY rows
-// Y.  Per tile, S = X Y^T (tensor cores, K = D), a warp for every 32 columns and 32 rows
-// turns S into dz (one exponential an element) and writes it back to tensor memory in
-// 16 bits, where it is the A operand of OUT += dz Y (K = BY); the same bytes of Y in
-// shared memory are read K-major by the first product and MN-major by the second.  At these widths dz in
-// memory would cost more than forming S twice: 6 bytes of traffic an element (written
-// once, read twice) against 2 D FLOP and one exponential.
+// Y.  Per tile, S = X Y^T (tensor cores, K = D), warps turn S into dz (one exponential an
+// element) and write it back to tensor memory in 16 bits, where it is the A operand of
+// OUT += dz Y (K = BY); the same bytes of Y in shared memory are read K-major by the
+// first product and MN-major by the second.  At these widths dz in memory would cost
+// more than forming S twice: 6 bytes of traffic an element (written once, read twice)
+// against 2 D FLOP and one exponential.
 //
-// A tile's way through S, dz and OUT is long (each hand-over between the tensor cores
-// and the warps is a few hundred cycles), so three tiles are on their way at a time: S
-// has three buffers and the MMA warp queues S(i + 2) behind OUT(i).  What
-// the warps read of memory for a tile (lse and scale of its hidden rows, its targets)
-// is fetched a tile ahead.  X (but for fp32 at D > 64, where shared memory is full) and
-// OUT (but for 16-bit types at D > 64, where tensor memory is) have two buffers, and
-// eight further warps take OUT to memory, so units follow each other without a gap.
+// A tile's way through S, dz and OUT is long: every hand-over between the tensor cores
+// and the warps costs one to four hundred cycles.  So S and OUT are issued by a warp
+// each, S has three buffers and runs two tiles ahead, two sets of dz warps take tiles in
+// turn, and what a dz warp needs of memory (lse and scale of the hidden rows, targets)
+// is fetched while it works on the tile before.  X (but for fp32 at D > 64, where shared
+// memory is full) and OUT (where tensor memory has room) have two buffers, and eight
+// further warps take OUT to memory, so units follow each other without a gap.
 //
 // SPLIT (fp32: every operand as f16 hi + lo): three products each; OUT covers one tile
 // of Y at a time and its sums are kept in the storing warps' registers (k_head_gemm
@@ -88,7 +88,8 @@ struct FusedShape {
     static constexpr uint32_t kXBlock = 128 * 128, kYBlock = BY * 128;  // 64 columns of a tile
     static constexpr uint32_t kX = PC * DB * kXBlock, kY = PC * DB * kYBlock;
     static constexpr size_t kSmem = (size_t)XB * kX + (size_t)kStages * kY + 1024;
-    static constexpr int kDzWarps = BY / 8, kThreads = (12 + kDzWarps) * 32;  // warp 0: TMA, 1: MMA, 2: tensor memory, 4..11: OUT
+    // warp 0: TMA, 1: S, 2: tensor memory, 3: OUT product, 4..11: OUT to memory, 12..: dz
+    static constexpr int kDzSet = BY / 16, kDzWarps = 2 * kDzSet, kThreads = (12 + kDzWarps) * 32;
     // tensor memory: three S, then OUT (fp32 at D <= 64: hi hi and the two small products
     // in columns of their own)
     static constexpr int NS = 3, kOut = SPLIT && DT == 64 ? 128 : DT, OB = (512 - NS * BY) / kOut >= 2 ? 2 : 1;
@@ -104,9 +105,10 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
     using S = FusedShape<DT, SPLIT>;
     constexpr int BY = S::BY, NS = S::NS, OB = S::OB, kSegs = SPLIT ? 3 : 1;
     extern __shared__ uint8_t raw[];
-    __shared__ uint64_t xfull[S::XB], xempty[S::XB], yfull[S::kStages], yempty[S::kStages];
-    __shared__ uint64_t sfull[NS], pready[NS], pfree[NS], ofull[OB], oempty[OB], drain;
-    __shared__ float4 consts[COLS ? S::kDzWarps : 1][16];  // per dz warp: (lse, scale) of its columns
+    // odone: OUT of the tile in that stage is done (the stage and the tile's S are free)
+    __shared__ uint64_t xfull[S::XB], xempty[S::XB], yfull[S::kStages], odone[S::kStages];
+    __shared__ uint64_t sfull[NS], pready[NS], ofull[OB], oempty[OB], drain[2];
+    __shared__ float4 consts[COLS ? S::kDzWarps : 1][32];  // per dz warp: (lse, scale) of its columns
     __shared__ uint32_t tmem_slot;
     __shared__ int gave_up_s;
     volatile int* gave_up = &gave_up_s;
@@ -122,18 +124,18 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
         }
         for (int i = 0; i < S::kStages; ++i) {
             mbar_init(&yfull[i], 1);
-            mbar_init(&yempty[i], 1);
+            mbar_init(&odone[i], 1);
         }
         for (int i = 0; i < NS; ++i) {
             mbar_init(&sfull[i], 1);
-            mbar_init(&pready[i], S::kDzWarps);
-            mbar_init(&pfree[i], 1);
+            mbar_init(&pready[i], S::kDzSet);
         }
         for (int i = 0; i < OB; ++i) {
             mbar_init(&ofull[i], 1);
             mbar_init(&oempty[i], 8);
         }
-        mbar_init(&drain, 1);
+        mbar_init(&drain[0], 1);
+        mbar_init(&drain[1], 1);
         gave_up_s = 0;
     }
     if (warp == 2) tc_alloc(&tmem_slot, 512);
@@ -177,7 +179,7 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
                 ++xu;
             }
             const uint32_t st = g % S::kStages;
-            ok = head_wait(&yempty[st], ((g / S::kStages) & 1) ^ 1, a.wait_ns, gave_up);
+            ok = head_wait(&odone[st], ((g / S::kStages) & 1) ^ 1, a.wait_ns, gave_up);
             if (!ok) break;
             if (lead) {
                 bulk_expect(&yfull[st], S::kY);
@@ -187,20 +189,17 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
             __syncwarp();
         }
     } else if (warp == 1) {
-        const uint32_t id_s = idesc_f16(128, BY, a.fmt, false, false), id_o = idesc_f16(128, DT, a.fmt, false, true);
-        const uint32_t id_o2 = idesc_f16(128, 2 * DT, a.fmt, false, true);
+        const uint32_t idesc = idesc_f16(128, BY, a.fmt, false, false);
         const int ksteps = (a.D + 15) / 16;
-        uint32_t gs = 0, fl = 0;
-        Walk ws = w;
-        auto issue_s = [&]() {
-            const uint32_t b = xu % S::XB, st = gs % S::kStages, sb = gs % NS;
-            if (ws.y == ws.y0) {
-                ok = head_wait(&xfull[b], (xu / S::XB) & 1, a.wait_ns, gave_up);
-                if (!ok) return;
+        for (; w.u < a.units; ++g) {
+            const uint32_t b = xu % S::XB, st = g % S::kStages, sb = g % NS;
+            if (w.y == w.y0) ok = head_wait(&xfull[b], (xu / S::XB) & 1, a.wait_ns, gave_up);
+            ok = ok && head_wait(&yfull[st], (g / S::kStages) & 1, a.wait_ns, gave_up);
+            if (ok && g >= NS) {
+                const uint32_t o = g - NS;
+                ok = head_wait(&odone[o % S::kStages], (o / S::kStages) & 1, a.wait_ns, gave_up);
             }
-            ok = head_wait(&yfull[st], (gs / S::kStages) & 1, a.wait_ns, gave_up) &&
-                 head_wait(&pfree[sb], ((gs / NS) & 1) ^ 1, a.wait_ns, gave_up);
-            if (!ok) return;
+            if (!ok) break;
             tc_fence_after();
             const uint32_t d = tmem + sb * BY;
 #pragma unroll
@@ -211,23 +210,23 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
                 for (int k = 0; k < DT / 16; ++k)
                     if (k < ksteps)
                         mma_f16(d, sx + (((k >> 2) * S::kXBlock + (k & 3) * 32) >> 4), sy + (((k >> 2) * S::kYBlock + (k & 3) * 32) >> 4),
-                                id_s, seg > 0 || k > 0, lead);
+                                idesc, seg > 0 || k > 0, lead);
             }
             mma_commit(&sfull[sb], lead);
-            ++gs;
-            if (ws.y + 1 == ws.y1) {
+            if (w.y + 1 == w.y1) {
                 mma_commit(&xempty[b], lead);  // nothing but S reads X
                 ++xu;
             }
-            step(ws);
-        };
-        if (ws.u < a.units) issue_s();
-        if (ok && ws.u < a.units) issue_s();
-        for (; ok && w.u < a.units; step(w), ++g) {
+            step(w);
+        }
+    } else if (warp == 3) {
+        const uint32_t idesc = idesc_f16(128, DT, a.fmt, false, true), idesc2 = idesc_f16(128, 2 * DT, a.fmt, false, true);
+        uint32_t fl = 0;
+        for (; w.u < a.units; step(w), ++g) {
             const uint32_t st = g % S::kStages, sb = g % NS, ob = fl % OB;
             const bool first = SPLIT || w.y == w.y0, last = SPLIT || w.y + 1 == w.y1;
-            ok = head_wait(&pready[sb], (g / NS) & 1, a.wait_ns, gave_up);
-            if (ok && first) ok = head_wait(&oempty[ob], ((fl / OB) & 1) ^ 1, a.wait_ns, gave_up);
+            if (first) ok = head_wait(&oempty[ob], ((fl / OB) & 1) ^ 1, a.wait_ns, gave_up);
+            ok = ok && head_wait(&pready[sb], (g / NS) & 1, a.wait_ns, gave_up);
             if (!ok) break;
             tc_fence_after();
             const uint32_t d = tmem + S::kOutCol + ob * S::kOut, p = tmem + sb * BY;
@@ -238,114 +237,122 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
                 if (SPLIT && DT == 64) {
                     // the two pieces of Y lie one behind the other: hi [hi | lo] is one MMA of
                     // twice the columns, and the second half takes lo hi as well
-                    mma_f16_ta(d, pa, yb, id_o2, k > 0, lead);
-                    mma_f16_ta(d + DT, pa + 16, yb, id_o, true, lead);
+                    mma_f16_ta(d, pa, yb, idesc2, k > 0, lead);
+                    mma_f16_ta(d + DT, pa + 16, yb, idesc, true, lead);
                 } else if (SPLIT) {
                     const uint32_t yl = yb + (S::DB * S::kYBlock >> 4);
-                    mma_f16_ta(d, pa + 16, yb, id_o, k > 0, lead);
-                    mma_f16_ta(d, pa, yl, id_o, true, lead);
-                    mma_f16_ta(d, pa, yb, id_o, true, lead);
+                    mma_f16_ta(d, pa + 16, yb, idesc, k > 0, lead);
+                    mma_f16_ta(d, pa, yl, idesc, true, lead);
+                    mma_f16_ta(d, pa, yb, idesc, true, lead);
                 } else {
-                    mma_f16_ta(d, pa, yb, id_o, !first || k > 0, lead);
+                    mma_f16_ta(d, pa, yb, idesc, !first || k > 0, lead);
                 }
             }
-            mma_commit(&yempty[st], lead);
-            mma_commit(&pfree[sb], lead);
+            mma_commit(&odone[st], lead);
             if (last) {
                 mma_commit(&ofull[ob], lead);
                 ++fl;
             }
-            if (ws.u < a.units) issue_s();
         }
     } else if (warp >= 12) {
-        const int quad = warp & 3, part = (warp - 12) >> 2;  // its 32 rows and 32 columns
+        const int set = (warp - 12) / S::kDzSet, quad = warp & 3, part = (warp - 12) % S::kDzSet >> 2;  // its 32 rows and 64 columns
         const float c = a.ctemp * exp2i(-amax_exp(a.amax_h)) * exp2i(-amax_exp(a.amax_w));
         float4* my = consts[COLS ? warp - 12 : 0];
         // what a tile needs of memory, fetched while the tile before it is worked on
-        uint4 blk = make_uint4(0, 0, 0, 0);
-        float2 rc = make_float2(0.f, 0.f);
+        uint4 blk[2];
+        float2 rc[2];
         auto fetch = [&](const Walk& t) {
             if (t.u >= a.units) return;
-            const int xb = t.x * 4 + quad, yb = t.y * (BY / 32) + part;
-            const int nb = COLS ? yb : xb, vb = COLS ? xb : yb;
-            blk = nb < a.nblocks && vb < a.vblocks ? __ldg(reinterpret_cast<const uint4*>(a.blocks) + (int64_t)vb * a.nblocks + nb)
-                                                   : make_uint4(0, 0, 0, 0);
-            if (COLS || t.y == t.y0) {
-                const int64_t n = (int64_t)nb * 32 + lane;
-                rc = n < (COLS ? a.Y : a.X) ? __ldg(&a.rowc[n]) : make_float2(0.f, 0.f);
+#pragma unroll
+            for (int ch = 0; ch < 2; ++ch) {
+                const int xb = t.x * 4 + quad, yb = t.y * (BY / 32) + part * 2 + ch;
+                const int nb = COLS ? yb : xb, vb = COLS ? xb : yb;
+                blk[ch] = nb < a.nblocks && vb < a.vblocks ? __ldg(reinterpret_cast<const uint4*>(a.blocks) + (int64_t)vb * a.nblocks + nb)
+                                                           : make_uint4(0, 0, 0, 0);
+                if (COLS || ch == 0) {
+                    const int64_t n = (int64_t)nb * 32 + lane;
+                    rc[ch] = n < (COLS ? a.Y : a.X) ? __ldg(&a.rowc[n]) : make_float2(0.f, 0.f);
+                }
             }
         };
+        if (set && w.u < a.units) step(w);
         fetch(w);
-        for (; w.u < a.units; ++g) {
+        for (g = set; w.u < a.units; g += 2) {
             const uint32_t sb = g % NS;
-            const int64_t left = a.Y - ((int64_t)w.y * BY + part * 32);  // streamed rows from this warp's first column on
-            const uint4 b = blk;
-            const float2 r = rc;
+            const int64_t left = a.Y - ((int64_t)w.y * BY + part * 64);  // streamed rows from this warp's first column on
+            const uint4 b[2] = {blk[0], blk[1]};
+            const float2 r = rc[0];
             if (COLS) {
                 __syncwarp();
-                float* f = reinterpret_cast<float*>(my) + (lane >> 1) * 4 + (lane & 1);
-                f[0] = -r.x;
-                f[2] = r.y;
+#pragma unroll
+                for (int ch = 0; ch < 2; ++ch) {
+                    float* f = reinterpret_cast<float*>(my) + ch * 64 + (lane >> 1) * 4 + (lane & 1);
+                    f[0] = -rc[ch].x;
+                    f[2] = rc[ch].y;
+                }
                 __syncwarp();
             }
             step(w);
+            if (w.u < a.units) step(w);
             fetch(w);
             ok = head_wait(&sfull[sb], (g / NS) & 1, a.wait_ns, gave_up);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t t0 = tmem + ((uint32_t)(quad * 32) << 16) + sb * BY + part * 32;
-            float p[32];
-            tm_ld32(t0, p);
-            tm_wait_ld(p);
-            if (COLS) {
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const float4 k = my[j];  // -lse of columns 2 j and 2 j + 1, then their scales
-                    fma2(p[2 * j], p[2 * j + 1], c, c, k.x, k.y);
-                    p[2 * j] = ex2(p[2 * j]);
-                    p[2 * j + 1] = ex2(p[2 * j + 1]);
-                    mul2(p[2 * j], p[2 * j + 1], k.z, k.w);
+            for (int ch = 0; ch < 2; ++ch) {
+                const uint32_t t0 = tmem + ((uint32_t)(quad * 32) << 16) + sb * BY + part * 64 + ch * 32;
+                float p[32];
+                tm_ld32(t0, p);
+                tm_wait_ld(p);
+                if (COLS) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const float4 k = my[ch * 16 + j];  // -lse of columns 2 j and 2 j + 1, then their scales
+                        fma2(p[2 * j], p[2 * j + 1], c, c, k.x, k.y);
+                        p[2 * j] = ex2(p[2 * j]);
+                        p[2 * j + 1] = ex2(p[2 * j + 1]);
+                        mul2(p[2 * j], p[2 * j + 1], k.z, k.w);
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) {
+                        fma2(p[j], p[j + 1], c, c, -r.x, -r.x);
+                        p[j] = ex2(p[j]);
+                        p[j + 1] = ex2(p[j + 1]);
+                        mul2(p[j], p[j + 1], r.y, r.y);
+                    }
+                    if (left < ch * 32 + 32) {  // table rows past the last have no dz
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (ch * 32 + j >= left) p[j] = 0.f;
+                    }
                 }
-            } else {
+                if (b[ch].x) {
+                    auto put = [&](int at, float val) {
+                        const int tl = COLS ? at >> 5 : at & 31, tc = COLS ? at & 31 : at >> 5;
 #pragma unroll
-                for (int j = 0; j < 32; j += 2) {
-                    fma2(p[j], p[j + 1], c, c, -r.x, -r.x);
-                    p[j] = ex2(p[j]);
-                    p[j + 1] = ex2(p[j + 1]);
-                    mul2(p[j], p[j + 1], r.y, r.y);
+                        for (int j = 0; j < 32; ++j)
+                            if (j == tc && lane == tl) p[j] = val;
+                    };
+                    put(b[ch].x & 1023, __uint_as_float(b[ch].y));
+                    if (b[ch].x >> 21) put((b[ch].x >> 10) & 1023, __uint_as_float(b[ch].z));
+                    for (int e = (int)b[ch].w; e;) {
+                        const int4 t = __ldg(reinterpret_cast<const int4*>(a.ents + (e - 1)));
+                        put(t.x, __int_as_float(t.y));
+                        e = t.z;
+                    }
                 }
-                if (left < 32) {  // table rows past the last have no dz
+                uint32_t q[16];
+                pack32(p, q, SPLIT ? 0 : a.fmt);
+                tm_st16(t0, q);
+                if (SPLIT) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (j >= left) p[j] = 0.f;
+                    for (int j = 0; j < 16; ++j) {
+                        const float2 h = unpack_f16(q[j]);
+                        q[j] = pack16(p[2 * j] - h.x, p[2 * j + 1] - h.y, 0);
+                    }
+                    tm_st16(t0 + 16, q);
                 }
-            }
-            if (b.x) {
-                auto put = [&](int at, float val) {
-                    const int tl = COLS ? at >> 5 : at & 31, tc = COLS ? at & 31 : at >> 5;
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (j == tc && lane == tl) p[j] = val;
-                };
-                put(b.x & 1023, __uint_as_float(b.y));
-                if (b.x >> 21) put((b.x >> 10) & 1023, __uint_as_float(b.z));
-                for (int e = (int)b.w; e;) {
-                    const int4 t = __ldg(reinterpret_cast<const int4*>(a.ents + (e - 1)));
-                    put(t.x, __int_as_float(t.y));
-                    e = t.z;
-                }
-            }
-            uint32_t q[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) q[j] = pack16(p[2 * j], p[2 * j + 1], a.fmt);
-            tm_st16(t0, q);
-            if (SPLIT) {
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const float2 h = unpack_f16(q[j]);
-                    q[j] = pack16(p[2 * j] - h.x, p[2 * j + 1] - h.y, 0);
-                }
-                tm_st16(t0 + 16, q);
             }
             tm_wait_st();
             tc_fence_before();
@@ -424,9 +431,9 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
             for (uint32_t i = xu > S::XB ? xu - S::XB : 0; i < xu; ++i) head_drain(&xfull[i % S::XB], (i / S::XB) & 1);
             for (uint32_t i = g > S::kStages ? g - S::kStages : 0; i < g; ++i) head_drain(&yfull[i % S::kStages], (i / S::kStages) & 1);
         }
-        if (threadIdx.x == 32) {
-            mma_commit(&drain, true);
-            head_drain(&drain, 0);
+        if (threadIdx.x == 32 || threadIdx.x == 96) {
+            mma_commit(&drain[threadIdx.x == 96], true);
+            head_drain(&drain[threadIdx.x == 96], 0);
         }
         __syncwarp();
         __syncthreads();
