@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(kRowThreads) k_head_finish(HeadIn in, Target t
 // (ids_out, dzt; k_head_fix) or, ents given, to their 32 x 32 blocks (k_head_fused).
 template <class T, bool DISTILL>
 __global__ void __launch_bounds__(kRowThreads)
-    k_head_rows(HeadIn in, Target t, const float* lse, const float* grad, const uint32_t* amax, float2* rowc, int* ids_out,
+    k_head_rows(HeadIn in, Target t, const float* lse, const float* grad, const uint32_t* amax, float* nlse, float* scale, int* ids_out,
                 float* dzt, TargetBlock* blocks, int nblocks, TargetEntry* ents, uint16_t* hp, int* err) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t n = blockIdx.x;
@@ -245,8 +245,11 @@ __global__ void __launch_bounds__(kRowThreads)
     const int ez = amax ? scale_exp(amax[2]) : 0, eh = amax ? scale_exp(amax[0]) : 0;
     const float rs = any ? grad[n] * t.T * exp2i(ez) : 0.f;
     if (threadIdx.x == 0) {
-        rowc[n] = any ? make_float2(l * kLog2e, rs) : make_float2(0.f, 0.f);
+        nlse[n] = any ? -l * kLog2e : 0.f;
+        scale[n] = rs;
     }
+    if (n == in.N - 1)
+        for (int64_t i = in.N + threadIdx.x; i < (in.N + 127) / 128 * 128; i += kRowThreads) nlse[i] = scale[i] = 0.f;
     for (int k = warp; k < t.K; k += 4) {
         const int64_t id = DISTILL ? (q[k] == 0.f ? -1 : ids[k]) : xid;
         float d = 0.f;
@@ -531,7 +534,7 @@ bool out_gemm(bool split, const Operand& A, const Operand& B, const GemmArgs& a,
     return run_gemm<256, AMN, true, kEpiOut, false>(A, B, a, sms, st);
 }
 
-template <int DT, bool SPLIT, bool COLS>
+template <int DT, bool SPLIT, int MODE>
 bool run_fused(const Operand& X, const Operand& Y, FusedArgs a, int sms, cudaStream_t st) {
     using S = FusedShape<DT, SPLIT>;
     CUtensorMap mx, my;
@@ -543,16 +546,16 @@ bool run_fused(const Operand& X, const Operand& Y, FusedArgs a, int sms, cudaStr
     a.ytiles = (int)cdiv(Y.rows, S::BY);
     a.units = a.xtiles * a.splits;
     a.wait_ns = g_head_wait_ns;
-    auto k = k_head_fused<DT, SPLIT, COLS>;
+    auto k = k_head_fused<DT, SPLIT, MODE>;
     if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem) != cudaSuccess) return false;
     k<<<(unsigned)(a.units < sms ? a.units : sms), S::kThreads, S::kSmem, st>>>(mx, my, a);
     return cudaGetLastError() == cudaSuccess;
 }
 
-template <bool COLS>
+template <int MODE>
 bool fused(bool split, const Operand& X, const Operand& Y, const FusedArgs& a, int sms, cudaStream_t st) {
-    if (a.D <= 64) return split ? run_fused<64, true, COLS>(X, Y, a, sms, st) : run_fused<64, false, COLS>(X, Y, a, sms, st);
-    return split ? run_fused<128, true, COLS>(X, Y, a, sms, st) : run_fused<128, false, COLS>(X, Y, a, sms, st);
+    if (a.D <= 64) return split ? run_fused<64, true, MODE>(X, Y, a, sms, st) : run_fused<64, false, MODE>(X, Y, a, sms, st);
+    return split ? run_fused<128, true, MODE>(X, Y, a, sms, st) : run_fused<128, false, MODE>(X, Y, a, sms, st);
 }
 
 // Column tiles per strip: the fewest rounds of tiles over the blocks, and among the
@@ -587,7 +590,8 @@ struct Plan {
     bool pack_h, pack_w;
     int bn_s;                // column tile of the score products
     int strip;
-    int64_t nparts;
+    int64_t nparts;          // (maximum, sum) pairs per row
+    int lse_splits;          // D <= 128: ranges of the vocabulary (k_head_fused)
     bool fused;              // backward: dz stays on the chip (k_head_fused)
     int64_t nblocks, vblocks;  // its 32 x 32 blocks
     int64_t P;               // else: vocabulary piece
@@ -632,6 +636,11 @@ tt_status make_plan(const tt_head* hd, int K, Plan* p) {
     p->bn_s = !p->split && mt * cdiv(in.V, 256) >= 2 * p->sms ? 256 : 128;
     p->strip = choose_strip(mt, cdiv(in.V, p->bn_s), p->sms);
     p->nparts = kParts * cdiv(cdiv(in.V, p->bn_s), p->strip);
+    if (in.D <= 128) {
+        const int by = p->split && in.D > 64 ? 64 : 128;
+        p->lse_splits = choose_splits(mt, cdiv(in.V, by), p->sms);
+        p->nparts = (by == 64 ? 2 : 4) * p->lse_splits;
+    }
     // backward
     p->nblocks = cdiv(in.N, 32);
     p->vblocks = cdiv(in.V, 32);
@@ -684,8 +693,7 @@ size_t fwd_ws(const Plan& p, void* base, FwdWs* w) {
 
 struct BwdWs {
     uint32_t* amax;
-    float2* rowc;
-    float *dzt, *dh_part, *dw_part;
+    float *nlse, *scale, *dzt, *dh_part, *dw_part;
     int* ids;
     TargetBlock* blocks;
     TargetEntry* ents;
@@ -695,7 +703,8 @@ size_t bwd_ws(const Plan& p, int K, void* base, BwdWs* w) {
     Arena a(base);
     const int64_t pc = p.split ? 2 : 1, nk = p.in.N * K;
     w->amax = a.get<uint32_t>(4);
-    w->rowc = a.get<float2>(p.in.N);
+    w->nlse = a.get<float>(cdiv(p.in.N, 128) * 128);
+    w->scale = a.get<float>(cdiv(p.in.N, 128) * 128);
     w->ids = a.get<int>(p.fused ? 0 : nk);
     w->dzt = a.get<float>(p.fused ? 0 : nk);
     w->blocks = a.get<TargetBlock>(p.fused ? p.nblocks * p.vblocks : 0);
@@ -741,18 +750,35 @@ tt_status head_forward(const Plan& p, const Target& t, float* loss, float* lse, 
             in, w.amax, p.pack_w ? w.wp : nullptr, p.pack_h ? w.hp : nullptr, w.row_exp);
         if (!launch_ok()) return TT_ERR_CUDA;
     }
-    GemmArgs a = gemm_args(p, err);
-    a.M = in.N;
-    a.N = in.V;
-    a.strip = p.strip;
-    a.chunks = (int)cdiv(in.D, kBK);
-    a.amax_b = p.split ? w.amax + 1 : nullptr;
-    a.row_exp = p.split ? w.row_exp : nullptr;
-    a.ctemp = kLog2e / t.T;
-    a.part = w.part;
     const Operand H{p.pack_h ? w.hp : static_cast<const uint16_t*>(in.h), in.N, in.D, p.pack_h ? in.Dp : in.ldh, in.N * in.Dp};
     const Operand W{p.pack_w ? w.wp : static_cast<const uint16_t*>(in.w), in.V, in.D, p.pack_w ? in.Dp : in.ldw, in.V * in.Dp};
-    if (!score_gemm<kEpiStats>(p.bn_s, p.split, H, W, a, p.sms, st)) return TT_ERR_CUDA;
+    const uint32_t* amax_w = p.split ? w.amax + 1 : nullptr;
+    const int* row_exp = p.split ? w.row_exp : nullptr;
+    bool ok;
+    if (in.D <= 128) {
+        FusedArgs a{};
+        a.D = in.D;
+        a.splits = p.lse_splits;
+        a.fmt = p.fmt;
+        a.err = err;
+        a.amax_w = amax_w;
+        a.row_exp = row_exp;
+        a.ctemp = kLog2e / t.T;
+        a.part = w.part;
+        ok = fused<kLse>(p.split, H, W, a, p.sms, st);
+    } else {
+        GemmArgs a = gemm_args(p, err);
+        a.M = in.N;
+        a.N = in.V;
+        a.strip = p.strip;
+        a.chunks = (int)cdiv(in.D, kBK);
+        a.amax_b = amax_w;
+        a.row_exp = row_exp;
+        a.ctemp = kLog2e / t.T;
+        a.part = w.part;
+        ok = score_gemm<kEpiStats>(p.bn_s, p.split, H, W, a, p.sms, st);
+    }
+    if (!ok) return TT_ERR_CUDA;
     if (distill)
         k_head_finish<T, true><<<(unsigned)in.N, kRowThreads, (size_t)t.K * 12, st>>>(in, t, w.part, (int)p.nparts, loss, lse, err);
     else
@@ -789,10 +815,10 @@ tt_status head_backward(const Plan& p, const Target& t, const float* lse, const 
     TargetEntry* ents = p.fused ? w.ents : nullptr;
     if (ents && cudaMemsetAsync(w.blocks, 0, (size_t)(p.nblocks * p.vblocks) * sizeof(TargetBlock), st) != cudaSuccess) return TT_ERR_CUDA;
     if (distill)
-        k_head_rows<T, true><<<(unsigned)in.N, kRowThreads, (size_t)t.K * 12, st>>>(in, t, lse, grad, amax, w.rowc, w.ids, w.dzt, w.blocks,
+        k_head_rows<T, true><<<(unsigned)in.N, kRowThreads, (size_t)t.K * 12, st>>>(in, t, lse, grad, amax, w.nlse, w.scale, w.ids, w.dzt, w.blocks,
                                                                                   (int)p.nblocks, ents, w.hp, err);
     else
-        k_head_rows<T, false><<<(unsigned)in.N, kRowThreads, 12, st>>>(in, t, lse, grad, amax, w.rowc, w.ids, w.dzt, w.blocks, (int)p.nblocks,
+        k_head_rows<T, false><<<(unsigned)in.N, kRowThreads, 12, st>>>(in, t, lse, grad, amax, w.nlse, w.scale, w.ids, w.dzt, w.blocks, (int)p.nblocks,
                                                                      ents, w.hp, err);
     if (!launch_ok()) return TT_ERR_CUDA;
     const uint32_t *ah = amax, *aw = amax ? amax + 1 : nullptr, *az = amax ? amax + 2 : nullptr;
@@ -823,18 +849,19 @@ tt_status head_backward(const Plan& p, const Target& t, const float* lse, const 
         a.amax_w = aw;
         a.amax_z = az;
         a.ctemp = kLog2e / t.T;
-        a.rowc = w.rowc;
+        a.nlse = w.nlse;
+        a.scale = w.scale;
         a.blocks = w.blocks;
         a.ents = w.ents;
         a.nblocks = (int)p.nblocks;
         a.vblocks = (int)p.vblocks;
         a.splits = p.dw_splits;
         a.to = dest(p.dw_splits > 1 ? nullptr : dw, w.dw_part);
-        if (!fused<true>(p.split, W, H, a, p.sms, st)) return TT_ERR_CUDA;
+        if (!fused<kDweight>(p.split, W, H, a, p.sms, st)) return TT_ERR_CUDA;
         if (p.dw_splits > 1 && !reduce(w.dw_part, p.dw_splits, in.V, dw, ah)) return TT_ERR_CUDA;
         a.splits = p.dh_splits;
         a.to = dest(p.dh_direct ? dh : nullptr, w.dh_part);
-        if (!fused<false>(p.split, H, W, a, p.sms, st)) return TT_ERR_CUDA;
+        if (!fused<kDhidden>(p.split, H, W, a, p.sms, st)) return TT_ERR_CUDA;
         if (!p.dh_direct && !reduce(w.dh_part, p.dh_splits, in.N, dh, aw)) return TT_ERR_CUDA;
         return TT_OK;
     }
@@ -850,7 +877,8 @@ tt_status head_backward(const Plan& p, const Target& t, const float* lse, const 
         a.amax_a = ah;
         a.amax_b = aw;
         a.ctemp = kLog2e / t.T;
-        a.rowc = w.rowc;
+        a.nlse = w.nlse;
+        a.scale = w.scale;
         a.dz = w.dz;
         a.dz_pitch = p.pitch;
         a.dz_piece = dz_piece;

@@ -100,6 +100,13 @@ __device__ __forceinline__ void mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uin
         : "memory");
 }
 
+// 16 bytes from global to shared memory without a register (zeros if !have); done after
+// the thread's cp_wait.  What the other lanes of a warp copied is seen after a __syncwarp.
+__device__ __forceinline__ void cp16(void* dst, const void* src, bool have) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(have ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // The mbarrier's phase completes when every MMA issued so far by the lead lane is done.
 __device__ __forceinline__ void mma_commit(uint64_t* bar, bool lead) {
     asm volatile(
@@ -175,6 +182,31 @@ __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// Running maximum and sum of exp over one more 32 scores of a row, of which the first
+// `valid` count: v in units of which c makes log2 units (c > 0), the maximum in v's.
+__device__ __forceinline__ void take_scores(float (&v)[32], int64_t valid, float c, float& run_m, float& run_s) {
+    if (valid < 32) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (j >= valid) v[j] = -INFINITY;
+    }
+    float mx = v[0];
+#pragma unroll
+    for (int j = 1; j < 32; ++j) mx = fmaxf(mx, v[j]);
+    const float mn = fmaxf(run_m, mx);
+    const float m2 = mn == -INFINITY ? 0.f : mn * c;
+    float s[4] = {run_s * ex2(fmaf(run_m, c, -m2)), 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < 32; j += 4) {
+        fma2(v[j], v[j + 1], c, c, -m2, -m2);
+        fma2(v[j + 2], v[j + 3], c, c, -m2, -m2);
+        add2(s[0], s[1], ex2(v[j]), ex2(v[j + 1]));
+        add2(s[2], s[3], ex2(v[j + 2]), ex2(v[j + 3]));
+    }
+    run_s = (s[0] + s[1]) + (s[2] + s[3]);
+    run_m = mn;
 }
 
 constexpr float kLog2e = 1.4426950408889634f;

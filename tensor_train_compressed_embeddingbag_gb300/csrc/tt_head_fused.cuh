@@ -1,10 +1,11 @@
-// tt_head_fused.cuh -- the gradients of the vocabulary head for widths up to 128,
-// dz kept on the chip.
+// tt_head_fused.cuh -- the vocabulary head for widths up to 128: scores, and dz, never
+// leave the chip.
 //
-//   dhidden[n] = sum_v dz[n, v] weight[v]        resident rows: hidden, streamed: weight
-//   dweight[v] = sum_n dz[n, v] hidden[n]        resident rows: weight, streamed: hidden
+//   kLse      max and sum of exp of z[n, v]        resident rows: hidden, streamed: weight
+//   kDhidden  sum_v dz[n, v] weight[v]             resident rows: hidden, streamed: weight
+//   kDweight  sum_n dz[n, v] hidden[n]             resident rows: weight, streamed: hidden
 //
-// One kernel for both: a block holds 128 resident rows X and streams tiles of BY rows
+// One kernel for the three: a block holds 128 resident rows X and streams tiles of BY rows
 // Y.  Per tile, S = X Y^T (tensor cores, K = D), warps turn S into dz (one exponential an
 // element) and write it back to tensor memory in 16 bits, where it is the A operand of
 // OUT += dz Y (K = BY); the same bytes of Y in shared memory are read K-major by the
@@ -13,9 +14,9 @@
 // against 2 D FLOP and one exponential.
 //
 // A tile's way through S, dz and OUT is long: every hand-over between the tensor cores
-// and the warps costs one to four hundred cycles.  So S and OUT are issued by a warp
-// each, S has three buffers and runs two tiles ahead, two sets of dz warps take tiles in
-// turn, and what a dz warp needs of memory (lse and scale of the hidden rows, targets)
+// and the warps costs one to four hundred cycles, and so does what an issuing warp does
+// around a tile's MMAs (its waits and commits).  So two warps issue S, taking tiles in
+// turn, and one issues OUT; S has three buffers, two sets of dz warps take tiles in turn, and what a dz warp needs of memory (lse and scale of the hidden rows, targets)
 // is fetched while it works on the tile before.  X (but for fp32 at D > 64, where shared
 // memory is full) and OUT (where tensor memory has room) have two buffers, and eight
 // further warps take OUT to memory, so units follow each other without a gap.
@@ -71,13 +72,18 @@ struct FusedArgs {
     const uint32_t* amax_h;  // power-of-two scales of hidden, weight, dz (null: none)
     const uint32_t* amax_w;
     const uint32_t* amax_z;
+    const int* row_exp;      // kLse: per hidden row instead (null: amax_h)
     float ctemp;             // log2(e) / T
-    const float2* rowc;      // per hidden row (lse in log2 units, scale)
+    float2* part;            // kLse: [X][splits][kParts] (maximum in log2 units, sum)
+    const float* nlse;       // per hidden row -lse in log2 units, and its scale; zeros up to a
+    const float* scale;      //   multiple of 128 rows
     const TargetBlock* blocks;  // [vblocks][nblocks]
     const TargetEntry* ents;
     int nblocks, vblocks;
     OutArgs to;
 };
+
+enum FusedMode { kLse = 0, kDhidden = 1, kDweight = 2 };
 
 template <int DT, bool SPLIT>
 struct FusedShape {
@@ -88,8 +94,9 @@ struct FusedShape {
     static constexpr uint32_t kXBlock = 128 * 128, kYBlock = BY * 128;  // 64 columns of a tile
     static constexpr uint32_t kX = PC * DB * kXBlock, kY = PC * DB * kYBlock;
     static constexpr size_t kSmem = (size_t)XB * kX + (size_t)kStages * kY + 1024;
-    // warp 0: TMA, 1: S, 2: tensor memory, 3: OUT product, 4..11: OUT to memory, 12..: dz
+    // warp 0: TMA, 1 and 2: S, 3: OUT product, 4..11: OUT to memory, 12..: dz
     static constexpr int kDzSet = BY / 16, kDzWarps = 2 * kDzSet, kThreads = (12 + kDzWarps) * 32;
+    static constexpr int kParts = 2 * (BY / 64);  // kLse: pairs per row and unit, one of each dz warp of the row
     // tensor memory: three S, then OUT (fp32 at D <= 64: hi hi and the two small products
     // in columns of their own)
     static constexpr int NS = 3, kOut = SPLIT && DT == 64 ? 128 : DT, OB = (512 - NS * BY) / kOut >= 2 ? 2 : 1;
@@ -97,18 +104,25 @@ struct FusedShape {
     static_assert(NS * BY + OB * kOut <= 512, "tensor memory");
 };
 
-// COLS: the streamed rows are hidden rows (dweight), so lse and scale go by column.
-template <int DT, bool SPLIT, bool COLS>
+// kLse has no OUT: a tile's dz warps free its S, and its stage is free once S is formed.
+template <int DT, bool SPLIT, int MODE>
 __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
     k_head_fused(const __grid_constant__ CUtensorMap mapX, const __grid_constant__ CUtensorMap mapY,
                  const __grid_constant__ FusedArgs a) {
     using S = FusedShape<DT, SPLIT>;
+    constexpr bool COLS = MODE == kDweight;  // hidden rows are columns of S: lse and scale go by column
     constexpr int BY = S::BY, NS = S::NS, OB = S::OB, kSegs = SPLIT ? 3 : 1;
     extern __shared__ uint8_t raw[];
-    // odone: OUT of the tile in that stage is done (the stage and the tile's S are free)
-    __shared__ uint64_t xfull[S::XB], xempty[S::XB], yfull[S::kStages], odone[S::kStages];
-    __shared__ uint64_t sfull[NS], pready[NS], ofull[OB], oempty[OB], drain[2];
-    __shared__ float4 consts[COLS ? S::kDzWarps : 1][32];  // per dz warp: (lse, scale) of its columns
+    // by stage: sfull: S of the tile is formed; odone: its OUT is done (the stage and S are free)
+    __shared__ uint64_t xfull[S::XB], xempty[S::XB], yfull[S::kStages], sfull[S::kStages], odone[S::kStages];
+    __shared__ uint64_t pready[NS], ofull[OB], oempty[OB], drain[3];
+    // what a dz warp needs of memory for a tile, and for the next: -lse and scale of its
+    // columns (COLS) or rows, the targets of its two 32 x 32 blocks
+    struct Ahead {
+        float nlse[COLS ? 64 : 32], scale[COLS ? 64 : 32];
+        uint4 blk[2];
+    };
+    __shared__ __align__(16) Ahead ahead[S::kDzWarps][2];
     __shared__ uint32_t tmem_slot;
     __shared__ int gave_up_s;
     volatile int* gave_up = &gave_up_s;
@@ -120,22 +134,21 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::XB; ++i) {
             mbar_init(&xfull[i], 1);
-            mbar_init(&xempty[i], 1);
+            mbar_init(&xempty[i], 2);
         }
         for (int i = 0; i < S::kStages; ++i) {
             mbar_init(&yfull[i], 1);
+            mbar_init(&sfull[i], 1);
             mbar_init(&odone[i], 1);
         }
         for (int i = 0; i < NS; ++i) {
-            mbar_init(&sfull[i], 1);
             mbar_init(&pready[i], S::kDzSet);
         }
         for (int i = 0; i < OB; ++i) {
             mbar_init(&ofull[i], 1);
             mbar_init(&oempty[i], 8);
         }
-        mbar_init(&drain[0], 1);
-        mbar_init(&drain[1], 1);
+        for (int i = 0; i < 3; ++i) mbar_init(&drain[i], 1);
         gave_up_s = 0;
     }
     if (warp == 2) tc_alloc(&tmem_slot, 512);
@@ -179,7 +192,7 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
                 ++xu;
             }
             const uint32_t st = g % S::kStages;
-            ok = head_wait(&odone[st], ((g / S::kStages) & 1) ^ 1, a.wait_ns, gave_up);
+            ok = head_wait(MODE == kLse ? &sfull[st] : &odone[st], ((g / S::kStages) & 1) ^ 1, a.wait_ns, gave_up);
             if (!ok) break;
             if (lead) {
                 bulk_expect(&yfull[st], S::kY);
@@ -188,38 +201,44 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
             }
             __syncwarp();
         }
-    } else if (warp == 1) {
-        const uint32_t idesc = idesc_f16(128, BY, a.fmt, false, false);
+    } else if (warp == 1 || warp == 2) {
+        const uint32_t idesc = idesc_f16(128, BY, a.fmt, false, false), turn = warp - 1;
         const int ksteps = (a.D + 15) / 16;
         for (; w.u < a.units; ++g) {
             const uint32_t b = xu % S::XB, st = g % S::kStages, sb = g % NS;
-            if (w.y == w.y0) ok = head_wait(&xfull[b], (xu / S::XB) & 1, a.wait_ns, gave_up);
-            ok = ok && head_wait(&yfull[st], (g / S::kStages) & 1, a.wait_ns, gave_up);
-            if (ok && g >= NS) {
-                const uint32_t o = g - NS;
-                ok = head_wait(&odone[o % S::kStages], (o / S::kStages) & 1, a.wait_ns, gave_up);
+            if (w.y == w.y0) {
+                ok = head_wait(&xfull[b], (xu / S::XB) & 1, a.wait_ns, gave_up);
+                if (!ok) break;
             }
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t d = tmem + sb * BY;
+            if ((g & 1) == turn) {
+                if (g >= NS) {  // S of tile g - NS is done with
+                    const uint32_t o = g - NS;
+                    ok = MODE == kLse ? head_wait(&pready[sb], (o / NS) & 1, a.wait_ns, gave_up)
+                                      : head_wait(&odone[o % S::kStages], (o / S::kStages) & 1, a.wait_ns, gave_up);
+                }
+                ok = ok && head_wait(&yfull[st], (g / S::kStages) & 1, a.wait_ns, gave_up);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t d = tmem + sb * BY;
 #pragma unroll
-            for (int seg = 0; seg < kSegs; ++seg) {
-                const uint32_t sx = desc_lo(base + b * S::kX + (SPLIT && seg == 0 ? S::DB * S::kXBlock : 0), kNoLbo);
-                const uint32_t sy = desc_lo(ybase + st * S::kY + (SPLIT && seg == 1 ? S::DB * S::kYBlock : 0), kNoLbo);
+                for (int seg = 0; seg < kSegs; ++seg) {
+                    const uint32_t sx = desc_lo(base + b * S::kX + (SPLIT && seg == 0 ? S::DB * S::kXBlock : 0), kNoLbo);
+                    const uint32_t sy = desc_lo(ybase + st * S::kY + (SPLIT && seg == 1 ? S::DB * S::kYBlock : 0), kNoLbo);
 #pragma unroll
-                for (int k = 0; k < DT / 16; ++k)
-                    if (k < ksteps)
-                        mma_f16(d, sx + (((k >> 2) * S::kXBlock + (k & 3) * 32) >> 4), sy + (((k >> 2) * S::kYBlock + (k & 3) * 32) >> 4),
-                                idesc, seg > 0 || k > 0, lead);
+                    for (int k = 0; k < DT / 16; ++k)
+                        if (k < ksteps)
+                            mma_f16(d, sx + (((k >> 2) * S::kXBlock + (k & 3) * 32) >> 4),
+                                    sy + (((k >> 2) * S::kYBlock + (k & 3) * 32) >> 4), idesc, seg > 0 || k > 0, lead);
+                }
+                mma_commit(&sfull[st], lead);
             }
-            mma_commit(&sfull[sb], lead);
             if (w.y + 1 == w.y1) {
                 mma_commit(&xempty[b], lead);  // nothing but S reads X
                 ++xu;
             }
             step(w);
         }
-    } else if (warp == 3) {
+    } else if (MODE != kLse && warp == 3) {
         const uint32_t idesc = idesc_f16(128, DT, a.fmt, false, true), idesc2 = idesc_f16(128, 2 * DT, a.fmt, false, true);
         uint32_t fl = 0;
         for (; w.u < a.units; step(w), ++g) {
@@ -254,48 +273,73 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
                 ++fl;
             }
         }
-    } else if (warp >= 12) {
+    } else if (MODE == kLse && warp >= 12) {
+        const int set = (warp - 12) / S::kDzSet, quad = warp & 3, part = (warp - 12) % S::kDzSet >> 2;  // its 32 rows and 64 columns
+        const float c0 = a.ctemp * exp2i(-amax_exp(a.amax_h)) * exp2i(-amax_exp(a.amax_w));
+        float c = c0, run_m = -INFINITY, run_s = 0.f;
+        for (; w.u < a.units; ++g) {
+            const int64_t row = (int64_t)w.x * 128 + quad * 32 + lane;
+            if (w.y == w.y0) {
+                run_m = -INFINITY;
+                run_s = 0.f;
+                if (a.row_exp) c = row < a.X ? c0 * exp2i(-__ldg(&a.row_exp[row])) : c0;
+            }
+            if ((g & 1) == set) {
+                const uint32_t sb = g % NS;
+                const int64_t left = a.Y - ((int64_t)w.y * BY + part * 64);
+                ok = head_wait(&sfull[g % S::kStages], (g / S::kStages) & 1, a.wait_ns, gave_up);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int ch = 0; ch < 2; ++ch) {
+                    float v[32];
+                    tm_ld32(tmem + ((uint32_t)(quad * 32) << 16) + sb * BY + part * 64 + ch * 32, v);
+                    tm_wait_ld(v);
+                    if (ch == 1) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&pready[sb]);
+                    }
+                    take_scores(v, left - ch * 32, c, run_m, run_s);
+                }
+            }
+            if (w.y + 1 == w.y1 && row < a.X)
+                a.part[(row * a.splits + w.split) * S::kParts + set * (S::kParts / 2) + part] =
+                    make_float2(run_m == -INFINITY ? -INFINITY : run_m * c, run_s);
+            step(w);
+        }
+    } else if (MODE != kLse && warp >= 12) {
         const int set = (warp - 12) / S::kDzSet, quad = warp & 3, part = (warp - 12) % S::kDzSet >> 2;  // its 32 rows and 64 columns
         const float c = a.ctemp * exp2i(-amax_exp(a.amax_h)) * exp2i(-amax_exp(a.amax_w));
-        float4* my = consts[COLS ? warp - 12 : 0];
-        // what a tile needs of memory, fetched while the tile before it is worked on
-        uint4 blk[2];
-        float2 rc[2];
-        auto fetch = [&](const Walk& t) {
+        // fetched while the warp works on the tile before; by asynchronous copies, which
+        // hold no registers meanwhile
+        auto fetch = [&](const Walk& t, Ahead& to) {
             if (t.u >= a.units) return;
-#pragma unroll
-            for (int ch = 0; ch < 2; ++ch) {
-                const int xb = t.x * 4 + quad, yb = t.y * (BY / 32) + part * 2 + ch;
-                const int nb = COLS ? yb : xb, vb = COLS ? xb : yb;
-                blk[ch] = nb < a.nblocks && vb < a.vblocks ? __ldg(reinterpret_cast<const uint4*>(a.blocks) + (int64_t)vb * a.nblocks + nb)
-                                                           : make_uint4(0, 0, 0, 0);
-                if (COLS || ch == 0) {
-                    const int64_t n = (int64_t)nb * 32 + lane;
-                    rc[ch] = n < (COLS ? a.Y : a.X) ? __ldg(&a.rowc[n]) : make_float2(0.f, 0.f);
-                }
+            const int x32 = t.x * 4 + quad, y32 = t.y * (BY / 32) + part * 2;
+            constexpr int kHalf = COLS ? 16 : 8;  // lanes that copy each of the two rows of floats
+            if (lane < 2 * kHalf) {
+                const int64_t n = (int64_t)(COLS ? y32 : x32) * 32 + (lane % kHalf) * 4;
+                cp16((lane < kHalf ? to.nlse : to.scale) + (lane % kHalf) * 4, (lane < kHalf ? a.nlse : a.scale) + n, true);
+            }
+            if (lane < 2) {
+                const int nb = COLS ? y32 + lane : x32, vb = COLS ? x32 : y32 + lane;
+                const bool have = nb < a.nblocks && vb < a.vblocks;
+                cp16(&to.blk[lane], a.blocks + (have ? (int64_t)vb * a.nblocks + nb : 0), have);
             }
         };
         if (set && w.u < a.units) step(w);
-        fetch(w);
-        for (g = set; w.u < a.units; g += 2) {
+        int now = 0;
+        fetch(w, ahead[warp - 12][0]);
+        for (g = set; w.u < a.units; g += 2, now ^= 1) {
             const uint32_t sb = g % NS;
             const int64_t left = a.Y - ((int64_t)w.y * BY + part * 64);  // streamed rows from this warp's first column on
-            const uint4 b[2] = {blk[0], blk[1]};
-            const float2 r = rc[0];
-            if (COLS) {
-                __syncwarp();
-#pragma unroll
-                for (int ch = 0; ch < 2; ++ch) {
-                    float* f = reinterpret_cast<float*>(my) + ch * 64 + (lane >> 1) * 4 + (lane & 1);
-                    f[0] = -rc[ch].x;
-                    f[2] = rc[ch].y;
-                }
-                __syncwarp();
-            }
+            const Ahead& my = ahead[warp - 12][now];
+            cp_wait();
+            __syncwarp();
             step(w);
             if (w.u < a.units) step(w);
-            fetch(w);
-            ok = head_wait(&sfull[sb], (g / NS) & 1, a.wait_ns, gave_up);
+            fetch(w, ahead[warp - 12][now ^ 1]);
+            ok = head_wait(&sfull[g % S::kStages], (g / S::kStages) & 1, a.wait_ns, gave_up);
             if (!ok) break;
             tc_fence_after();
 #pragma unroll
@@ -306,20 +350,24 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
                 tm_wait_ld(p);
                 if (COLS) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const float4 k = my[ch * 16 + j];  // -lse of columns 2 j and 2 j + 1, then their scales
-                        fma2(p[2 * j], p[2 * j + 1], c, c, k.x, k.y);
-                        p[2 * j] = ex2(p[2 * j]);
-                        p[2 * j + 1] = ex2(p[2 * j + 1]);
-                        mul2(p[2 * j], p[2 * j + 1], k.z, k.w);
+                    for (int j = 0; j < 32; j += 4) {
+                        const float4 l = *reinterpret_cast<const float4*>(my.nlse + ch * 32 + j);
+                        const float4 r = *reinterpret_cast<const float4*>(my.scale + ch * 32 + j);
+                        fma2(p[j], p[j + 1], c, c, l.x, l.y);
+                        fma2(p[j + 2], p[j + 3], c, c, l.z, l.w);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) p[j + i] = ex2(p[j + i]);
+                        mul2(p[j], p[j + 1], r.x, r.y);
+                        mul2(p[j + 2], p[j + 3], r.z, r.w);
                     }
                 } else {
+                    const float l = my.nlse[lane], r = my.scale[lane];
 #pragma unroll
                     for (int j = 0; j < 32; j += 2) {
-                        fma2(p[j], p[j + 1], c, c, -r.x, -r.x);
+                        fma2(p[j], p[j + 1], c, c, l, l);
                         p[j] = ex2(p[j]);
                         p[j + 1] = ex2(p[j + 1]);
-                        mul2(p[j], p[j + 1], r.y, r.y);
+                        mul2(p[j], p[j + 1], r, r);
                     }
                     if (left < ch * 32 + 32) {  // table rows past the last have no dz
 #pragma unroll
@@ -327,16 +375,17 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
                             if (ch * 32 + j >= left) p[j] = 0.f;
                     }
                 }
-                if (b[ch].x) {
+                const uint4 b = my.blk[ch];
+                if (b.x) {
                     auto put = [&](int at, float val) {
                         const int tl = COLS ? at >> 5 : at & 31, tc = COLS ? at & 31 : at >> 5;
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
                             if (j == tc && lane == tl) p[j] = val;
                     };
-                    put(b[ch].x & 1023, __uint_as_float(b[ch].y));
-                    if (b[ch].x >> 21) put((b[ch].x >> 10) & 1023, __uint_as_float(b[ch].z));
-                    for (int e = (int)b[ch].w; e;) {
+                    put(b.x & 1023, __uint_as_float(b.y));
+                    if (b.x >> 21) put((b.x >> 10) & 1023, __uint_as_float(b.z));
+                    for (int e = (int)b.w; e;) {
                         const int4 t = __ldg(reinterpret_cast<const int4*>(a.ents + (e - 1)));
                         put(t.x, __int_as_float(t.y));
                         e = t.z;
@@ -359,7 +408,7 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&pready[sb]);
         }
-    } else if (warp >= 4) {
+    } else if (MODE != kLse && warp >= 4) {
         const int half = warp >= 8, quad = warp & 3;
         const float s1 = exp2i(-amax_exp(a.amax_z)), s2 = exp2i(-amax_exp(COLS ? a.amax_h : a.amax_w));
         constexpr int OC = DT / 64;  // 32-column chunks of this warp's half
@@ -431,9 +480,9 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
             for (uint32_t i = xu > S::XB ? xu - S::XB : 0; i < xu; ++i) head_drain(&xfull[i % S::XB], (i / S::XB) & 1);
             for (uint32_t i = g > S::kStages ? g - S::kStages : 0; i < g; ++i) head_drain(&yfull[i % S::kStages], (i / S::kStages) & 1);
         }
-        if (threadIdx.x == 32 || threadIdx.x == 96) {
-            mma_commit(&drain[threadIdx.x == 96], true);
-            head_drain(&drain[threadIdx.x == 96], 0);
+        if (lead && warp >= 1 && warp <= 3) {
+            mma_commit(&drain[warp - 1], true);
+            head_drain(&drain[warp - 1], 0);
         }
         __syncwarp();
         __syncthreads();

@@ -32,7 +32,8 @@ struct GemmArgs {
     // kEpiStats
     float2* part;        // [M][nstrips][kParts] (maximum in log2 units, sum)
     // kEpiDz
-    const float2* rowc;  // per row (lse in log2 units, scale)
+    const float* nlse;   // per row -lse in log2 units, and its scale
+    const float* scale;
     uint16_t* dz;        // [pieces][M][dz_pitch]
     int64_t dz_pitch, dz_piece;
     // kEpiOut
@@ -197,37 +198,17 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             float run_m = -INFINITY, run_s = 0.f, cr = c;
             float2 rc = make_float2(0.f, 0.f);
             if (EPI == kEpiStats && a.row_exp && in) cr = c * exp2i(-a.row_exp[row]);
-            if (EPI == kEpiDz && in) rc = a.rowc[row];
+            if (EPI == kEpiDz && in) rc = make_float2(a.nlse[row], a.scale[row]);
             for (int n = n0; ok && n < n1; ++n) {
                 const int64_t col0 = (int64_t)n * BN + part * (BN / kParts);
                 // 32 finished columns of this thread's row, the first of them `col`
                 auto finish = [&](float (&v)[32], int64_t col) {
                     if (EPI == kEpiStats) {
-                        const int valid = (int)max((int64_t)0, min((int64_t)32, a.N - col));
-                        if (valid < 32) {
-#pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                if (j >= valid) v[j] = -INFINITY;
-                        }
-                        float mx = v[0];
-#pragma unroll
-                        for (int j = 1; j < 32; ++j) mx = fmaxf(mx, v[j]);
-                        const float mn = fmaxf(run_m, mx);
-                        const float m2 = mn == -INFINITY ? 0.f : mn * cr;
-                        float s[4] = {run_s * ex2(fmaf(run_m, cr, -m2)), 0.f, 0.f, 0.f};
-#pragma unroll
-                        for (int j = 0; j < 32; j += 4) {
-                            fma2(v[j], v[j + 1], cr, cr, -m2, -m2);
-                            fma2(v[j + 2], v[j + 3], cr, cr, -m2, -m2);
-                            add2(s[0], s[1], ex2(v[j]), ex2(v[j + 1]));
-                            add2(s[2], s[3], ex2(v[j + 2]), ex2(v[j + 3]));
-                        }
-                        run_s = (s[0] + s[1]) + (s[2] + s[3]);
-                        run_m = mn;
+                        take_scores(v, a.N - col, cr, run_m, run_s);
                     } else if (EPI == kEpiDz) {
                         if (in && col < a.dz_pitch) {
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) v[j] = rc.y == 0.f ? 0.f : rc.y * ex2(fmaf(v[j], cr, -rc.x));
+                            for (int j = 0; j < 32; ++j) v[j] = rc.y == 0.f ? 0.f : rc.y * ex2(fmaf(v[j], cr, rc.x));
                             uint4* o = reinterpret_cast<uint4*>(a.dz + row * a.dz_pitch + col);
 #pragma unroll
                             for (int q = 0; q < 4; ++q) {
