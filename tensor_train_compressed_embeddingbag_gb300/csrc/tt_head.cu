@@ -169,17 +169,21 @@ __device__ bool teacher_row(const Target& t, int64_t n, int64_t V, float* q, flo
 // lse and loss of every row: the strips' pairs joined, the target scores as dot
 // products.  xent: a warp per row; distill: a block per row, a warp per entry.
 template <class T, bool DISTILL>
-__global__ void __launch_bounds__(kRowThreads) k_head_finish(HeadIn in, Target t, const float2* part, int nparts,
+__global__ void __launch_bounds__(kRowThreads) k_head_finish(HeadIn in, Target t, const float2* part, int slots, int per_slot, Runs runs,
                                                              float* loss, float* lse, int* err) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const T* h = static_cast<const T*>(in.h);
     const T* w = static_cast<const T*>(in.w);
+    const auto row_lse = [&](int64_t n) {  // of the slots, those that the row's runs filled
+        const int used = runs.blocks ? runs.last(n / 128) - runs.first(n / 128) + 1 : slots;
+        return join_parts(part + n * slots * per_slot, used * per_slot, lane);
+    };
     if (!DISTILL) {
         const int64_t n = (int64_t)blockIdx.x * 4 + warp;
         if (n >= in.N) return;
         const int64_t id = xent_id(t, n, in.V, lane == 0 ? err : nullptr);
         const float z = id >= 0 ? warp_dot(h + n * in.ldh, w + id * in.ldw, in.D, in.vec, lane) : 0.f;
-        const float l = join_parts(part + n * nparts, nparts, lane);
+        const float l = row_lse(n);
         if (lane == 0) {
             lse[n] = l;
             loss[n] = id >= 0 ? l - z : 0.f;
@@ -194,7 +198,7 @@ __global__ void __launch_bounds__(kRowThreads) k_head_finish(HeadIn in, Target t
         const int64_t n = blockIdx.x;
         const bool any = teacher_row(t, n, in.V, q, lq, ids, red, err);
         if (warp == 0) {
-            const float l = join_parts(part + n * nparts, nparts, lane);
+            const float l = row_lse(n);
             if (lane == 0) ls = l;
         }
         __syncthreads();
@@ -535,27 +539,36 @@ bool out_gemm(bool split, const Operand& A, const Operand& B, const GemmArgs& a,
 }
 
 template <int DT, bool SPLIT, int MODE>
-bool run_fused(const Operand& X, const Operand& Y, FusedArgs a, int sms, cudaStream_t st) {
+bool run_fused(const Operand& X, const Operand& Y, FusedArgs a, cudaStream_t st) {
     using S = FusedShape<DT, SPLIT>;
     CUtensorMap mx, my;
     if (!make_map(&mx, X.p, a.fmt, X.cols, X.rows, S::PC, X.pitch, X.piece, 128)) return false;
     if (!make_map(&my, Y.p, a.fmt, Y.cols, Y.rows, S::PC, Y.pitch, Y.piece, S::BY)) return false;
     a.X = X.rows;
     a.Y = Y.rows;
-    a.xtiles = (int)cdiv(X.rows, 128);
-    a.ytiles = (int)cdiv(Y.rows, S::BY);
-    a.units = a.xtiles * a.splits;
     a.wait_ns = g_head_wait_ns;
     auto k = k_head_fused<DT, SPLIT, MODE>;
     if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem) != cudaSuccess) return false;
-    k<<<(unsigned)(a.units < sms ? a.units : sms), S::kThreads, S::kSmem, st>>>(mx, my, a);
+    k<<<(unsigned)a.runs.blocks, S::kThreads, S::kSmem, st>>>(mx, my, a);
+    if (cudaGetLastError() != cudaSuccess) return false;
+    if (MODE == kLse || a.runs.blocks == 1) return true;
+    const bool by_boundary = a.runs.xtiles >= a.runs.blocks;
+    const unsigned gx = (unsigned)(by_boundary ? a.runs.blocks - 1 : a.runs.xtiles);
+    const unsigned gy = gx >= 256 ? 1 : (gx >= 64 ? 4 : (gx >= 16 ? 16 : 64));  // a block or more per SM
+    k_head_join<<<dim3(gx, gy), 128, 0, st>>>(a.runs, by_boundary, a.partial, a.to, a.X, a.D, a.amax_z, MODE == kDweight ? a.amax_h : a.amax_w);
     return cudaGetLastError() == cudaSuccess;
 }
 
 template <int MODE>
-bool fused(bool split, const Operand& X, const Operand& Y, const FusedArgs& a, int sms, cudaStream_t st) {
-    if (a.D <= 64) return split ? run_fused<64, true, MODE>(X, Y, a, sms, st) : run_fused<64, false, MODE>(X, Y, a, sms, st);
-    return split ? run_fused<128, true, MODE>(X, Y, a, sms, st) : run_fused<128, false, MODE>(X, Y, a, sms, st);
+bool fused(bool split, const Operand& X, const Operand& Y, const FusedArgs& a, cudaStream_t st) {
+    if (a.D <= 64) return split ? run_fused<64, true, MODE>(X, Y, a, st) : run_fused<64, false, MODE>(X, Y, a, st);
+    return split ? run_fused<128, true, MODE>(X, Y, a, st) : run_fused<128, false, MODE>(X, Y, a, st);
+}
+
+Runs make_runs(int64_t xrows, int64_t yrows, int by, int sms) {
+    Runs r{(int)cdiv(xrows, 128), (int)cdiv(yrows, by), 0};
+    r.blocks = (int)(r.total() < sms ? r.total() : sms);
+    return r;
 }
 
 // Column tiles per strip: the fewest rounds of tiles over the blocks, and among the
@@ -590,8 +603,9 @@ struct Plan {
     bool pack_h, pack_w;
     int bn_s;                // column tile of the score products
     int strip;
-    int64_t nparts;          // (maximum, sum) pairs per row
-    int lse_splits;          // D <= 128: ranges of the vocabulary (k_head_fused)
+    int slots, per_slot;     // (maximum, sum) pairs per row: slots of per_slot
+    bool fused_lse;          // scores by k_head_fused, its work shared as in
+    Runs runs_lse, runs_dw, runs_dh;
     bool fused;              // backward: dz stays on the chip (k_head_fused)
     int64_t nblocks, vblocks;  // its 32 x 32 blocks
     int64_t P;               // else: vocabulary piece
@@ -635,21 +649,32 @@ tt_status make_plan(const tt_head* hd, int K, Plan* p) {
     // wide ones would leave blocks without work
     p->bn_s = !p->split && mt * cdiv(in.V, 256) >= 2 * p->sms ? 256 : 128;
     p->strip = choose_strip(mt, cdiv(in.V, p->bn_s), p->sms);
-    p->nparts = kParts * cdiv(cdiv(in.V, p->bn_s), p->strip);
-    if (in.D <= 128) {
-        const int by = p->split && in.D > 64 ? 64 : 128;
-        p->lse_splits = choose_splits(mt, cdiv(in.V, by), p->sms);
-        p->nparts = (by == 64 ? 2 : 4) * p->lse_splits;
+    const int by = p->split && in.D > 64 ? 64 : 128;  // streamed rows per tile of k_head_fused
+    p->runs_lse = Runs{};
+    p->slots = (int)cdiv(cdiv(in.V, p->bn_s), p->strip);
+    p->per_slot = kParts;
+    // 16-bit types: with the hidden rows resident the scores are bound by the exponentials'
+    // warps either way, and the 256-column tiles of k_head_gemm feed them faster (4096 x
+    // 100003 x 64: 80 us, here 103); fp32 reads its two pieces of a tile once, not three
+    // times (208 us there, 129 here)
+    p->fused_lse = p->split && in.D <= 128 && mt * cdiv(in.V, by) < 1ll << 31;
+    if (p->fused_lse && in.N > 0) {
+        p->runs_lse = make_runs(in.N, in.V, by, p->sms);
+        p->slots = 1;
+        for (int64_t x = 0; x < mt; ++x) p->slots = max(p->slots, p->runs_lse.last(x) - p->runs_lse.first(x) + 1);
+        p->per_slot = 2 * (by / 64);
     }
     // backward
     p->nblocks = cdiv(in.N, 32);
     p->vblocks = cdiv(in.V, 32);
     p->fused = in.D <= 128 && p->nblocks * p->vblocks <= kMaxBlocks;
     if (p->fused) {
-        const int by = p->split && in.D > 64 ? 64 : 128;
-        p->dh_splits = choose_splits(mt, cdiv(in.V, by), p->sms);
-        p->dw_splits = choose_splits(cdiv(in.V, 128), cdiv(in.N, by), p->sms);
-        p->dh_direct = p->dh_splits == 1;
+        p->dh_splits = p->dw_splits = 1;
+        p->dh_direct = true;
+        if (in.N > 0) {
+            p->runs_dh = make_runs(in.N, in.V, by, p->sms);
+            p->runs_dw = make_runs(in.V, in.N, by, p->sms);
+        }
         p->P = in.V;
         p->pitch = 0;
     } else {
@@ -684,7 +709,7 @@ size_t fwd_ws(const Plan& p, void* base, FwdWs* w) {
     Arena a(base);
     const int64_t pc = p.split ? 2 : 1;
     w->amax = a.get<uint32_t>(4);
-    w->part = a.get<float2>(p.in.N * p.nparts);
+    w->part = a.get<float2>(p.in.N * p.slots * p.per_slot);
     w->row_exp = a.get<int>(p.split ? p.in.N : 0);
     w->hp = a.get<uint16_t>(p.pack_h ? pc * p.in.N * p.in.Dp : 0);
     w->wp = a.get<uint16_t>(p.pack_w ? pc * p.in.V * p.in.Dp : 0);
@@ -693,7 +718,7 @@ size_t fwd_ws(const Plan& p, void* base, FwdWs* w) {
 
 struct BwdWs {
     uint32_t* amax;
-    float *nlse, *scale, *dzt, *dh_part, *dw_part;
+    float *nlse, *scale, *joins, *dzt, *dh_part, *dw_part;
     int* ids;
     TargetBlock* blocks;
     TargetEntry* ents;
@@ -712,6 +737,7 @@ size_t bwd_ws(const Plan& p, int K, void* base, BwdWs* w) {
     w->hp = a.get<uint16_t>(pc * p.in.N * p.in.Dp);
     w->wp = a.get<uint16_t>(p.pack_w ? pc * p.in.V * p.in.Dp : 0);
     w->dz = a.get<uint16_t>(pc * p.in.N * p.pitch);
+    w->joins = a.get<float>(p.fused ? (int64_t)p.sms * 2 * 128 * p.pp : 0);
     w->dh_part = a.get<float>(p.dh_direct ? 0 : (int64_t)p.dh_splits * p.in.N * p.pp);
     w->dw_part = a.get<float>(p.dw_splits > 1 ? (int64_t)p.dw_splits * p.P * p.pp : 0);
     return a.used;
@@ -755,17 +781,18 @@ tt_status head_forward(const Plan& p, const Target& t, float* loss, float* lse, 
     const uint32_t* amax_w = p.split ? w.amax + 1 : nullptr;
     const int* row_exp = p.split ? w.row_exp : nullptr;
     bool ok;
-    if (in.D <= 128) {
+    if (p.fused_lse) {
         FusedArgs a{};
         a.D = in.D;
-        a.splits = p.lse_splits;
+        a.runs = p.runs_lse;
+        a.slots = p.slots;
         a.fmt = p.fmt;
         a.err = err;
         a.amax_w = amax_w;
         a.row_exp = row_exp;
         a.ctemp = kLog2e / t.T;
         a.part = w.part;
-        ok = fused<kLse>(p.split, H, W, a, p.sms, st);
+        ok = fused<kLse>(p.split, H, W, a, st);
     } else {
         GemmArgs a = gemm_args(p, err);
         a.M = in.N;
@@ -780,9 +807,9 @@ tt_status head_forward(const Plan& p, const Target& t, float* loss, float* lse, 
     }
     if (!ok) return TT_ERR_CUDA;
     if (distill)
-        k_head_finish<T, true><<<(unsigned)in.N, kRowThreads, (size_t)t.K * 12, st>>>(in, t, w.part, (int)p.nparts, loss, lse, err);
+        k_head_finish<T, true><<<(unsigned)in.N, kRowThreads, (size_t)t.K * 12, st>>>(in, t, w.part, p.slots, p.per_slot, p.runs_lse, loss, lse, err);
     else
-        k_head_finish<T, false><<<(unsigned)cdiv(in.N, 4), kRowThreads, 0, st>>>(in, t, w.part, (int)p.nparts, loss, lse, err);
+        k_head_finish<T, false><<<(unsigned)cdiv(in.N, 4), kRowThreads, 0, st>>>(in, t, w.part, p.slots, p.per_slot, p.runs_lse, loss, lse, err);
     return launch_ok() ? TT_OK : TT_ERR_CUDA;
 }
 
@@ -855,15 +882,13 @@ tt_status head_backward(const Plan& p, const Target& t, const float* lse, const 
         a.ents = w.ents;
         a.nblocks = (int)p.nblocks;
         a.vblocks = (int)p.vblocks;
-        a.splits = p.dw_splits;
-        a.to = dest(p.dw_splits > 1 ? nullptr : dw, w.dw_part);
-        if (!fused<kDweight>(p.split, W, H, a, p.sms, st)) return TT_ERR_CUDA;
-        if (p.dw_splits > 1 && !reduce(w.dw_part, p.dw_splits, in.V, dw, ah)) return TT_ERR_CUDA;
-        a.splits = p.dh_splits;
-        a.to = dest(p.dh_direct ? dh : nullptr, w.dh_part);
-        if (!fused<kDhidden>(p.split, H, W, a, p.sms, st)) return TT_ERR_CUDA;
-        if (!p.dh_direct && !reduce(w.dh_part, p.dh_splits, in.N, dh, aw)) return TT_ERR_CUDA;
-        return TT_OK;
+        a.partial = w.joins;
+        a.runs = p.runs_dw;
+        a.to = dest(dw, nullptr);
+        if (!fused<kDweight>(p.split, W, H, a, st)) return TT_ERR_CUDA;
+        a.runs = p.runs_dh;
+        a.to = dest(dh, nullptr);
+        return fused<kDhidden>(p.split, H, W, a, st) ? TT_OK : TT_ERR_CUDA;
     }
     const int64_t npieces = cdiv(in.V, p.P), dz_piece = in.N * p.pitch;
     for (int64_t i = 0; i < npieces; ++i) {

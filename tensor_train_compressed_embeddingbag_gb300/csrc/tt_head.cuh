@@ -192,10 +192,10 @@ __device__ __forceinline__ void take_scores(float (&v)[32], int64_t valid, float
         for (int j = 0; j < 32; ++j)
             if (j >= valid) v[j] = -INFINITY;
     }
-    float mx = v[0];
+    float mx[4] = {run_m, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-    for (int j = 1; j < 32; ++j) mx = fmaxf(mx, v[j]);
-    const float mn = fmaxf(run_m, mx);
+    for (int j = 0; j < 32; j += 2) mx[(j >> 1) & 3] = fmaxf(fmaxf(mx[(j >> 1) & 3], v[j]), v[j + 1]);
+    const float mn = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
     const float m2 = mn == -INFINITY ? 0.f : mn * c;
     float s[4] = {run_s * ex2(fmaf(run_m, c, -m2)), 0.f, 0.f, 0.f};
 #pragma unroll
@@ -254,6 +254,18 @@ __device__ __forceinline__ int scale_exp(uint32_t absmax_bits) {
 __device__ __forceinline__ float exp2i(int e) { return __int_as_float((e + 127) << 23); }
 
 __device__ __forceinline__ int amax_exp(const uint32_t* p) { return p ? scale_exp(*p) : 0; }
+
+// How the fused kernels share their work: the tiles (x, y), all y of one x before the
+// next x, are cut into `blocks` equal runs.  A run's tiles of one x are a segment; an x
+// whose tiles lie in one run is whole, others are joined from their runs' segments.
+struct Runs {
+    int xtiles, ytiles, blocks;
+    __host__ __device__ int64_t total() const { return (int64_t)xtiles * ytiles; }
+    __host__ __device__ int64_t begin(int b) const { return total() * b / blocks; }
+    __host__ __device__ int block_of(int64_t t) const { return (int)(((t + 1) * blocks - 1) / total()); }
+    __host__ __device__ int first(int64_t x) const { return block_of(x * ytiles); }
+    __host__ __device__ int last(int64_t x) const { return block_of(x * ytiles + ytiles - 1); }
+};
 
 // Where a product goes: converted rows of `out`, or (out null) fp32 partial sums, one
 // array per K range.

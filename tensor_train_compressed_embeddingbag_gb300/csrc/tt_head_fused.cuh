@@ -19,7 +19,7 @@
 // turn, and one issues OUT; S has three buffers, two sets of dz warps take tiles in turn, and what a dz warp needs of memory (lse and scale of the hidden rows, targets)
 // is fetched while it works on the tile before.  X (but for fp32 at D > 64, where shared
 // memory is full) and OUT (where tensor memory has room) have two buffers, and eight
-// further warps take OUT to memory, so units follow each other without a gap.
+// further warps take OUT to memory, so segments follow each other without a gap.
 //
 // SPLIT (fp32: every operand as f16 hi + lo): three products each; OUT covers one tile
 // of Y at a time and its sums are kept in the storing warps' registers (k_head_gemm
@@ -64,8 +64,7 @@ __device__ __forceinline__ void add_target(TargetBlock* b, TargetEntry* ents, in
 struct FusedArgs {
     int64_t X, Y;   // resident and streamed rows
     int D;
-    int xtiles, ytiles, splits;
-    int units;  // xtiles * splits
+    Runs runs;
     int fmt;
     uint64_t wait_ns;
     int* err;
@@ -74,13 +73,15 @@ struct FusedArgs {
     const uint32_t* amax_z;
     const int* row_exp;      // kLse: per hidden row instead (null: amax_h)
     float ctemp;             // log2(e) / T
-    float2* part;            // kLse: [X][splits][kParts] (maximum in log2 units, sum)
+    float2* part;            // kLse: [X][slots][kParts] (maximum in log2 units, sum), a slot per run
+    int slots;
     const float* nlse;       // per hidden row -lse in log2 units, and its scale; zeros up to a
     const float* scale;      //   multiple of 128 rows
     const TargetBlock* blocks;  // [vblocks][nblocks]
     const TargetEntry* ents;
     int nblocks, vblocks;
-    OutArgs to;
+    OutArgs to;              // whole segments; others as fp32 sums to
+    float* partial;          //   [blocks][2][128][to.pp]: the run's first segment, its last
 };
 
 enum FusedMode { kLse = 0, kDhidden = 1, kDweight = 2 };
@@ -157,28 +158,32 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
 
-    // The tiles of this block, in order: unit by unit, tile y of [y0, y1) of unit u.
+    // The tiles of this block, in order; y0 .. y1 is the segment that tile (x, y) is in.
     struct Walk {
-        int u, x, split, y, y0, y1;
+        int left, x, y, y0, y1;  // left: tiles to go, this one counted; 0: none
     };
-    auto start = [&](Walk& w, int u) {
-        w.u = u;
-        if (u >= a.units) return;
-        w.split = u / a.xtiles;
-        w.x = u - w.split * a.xtiles;
-        w.y0 = w.y = (int)((int64_t)a.ytiles * w.split / a.splits);
-        w.y1 = (int)((int64_t)a.ytiles * (w.split + 1) / a.splits);
-    };
+    auto seg_end = [&](Walk& w) { w.y1 = min(a.runs.ytiles, w.y0 + w.left); };
     auto step = [&](Walk& w) {
-        if (++w.y == w.y1) start(w, w.u + (int)gridDim.x);
+        --w.left;
+        if (++w.y == w.y1) {
+            ++w.x;
+            w.y0 = w.y = 0;
+            seg_end(w);
+        }
     };
     Walk w;
-    start(w, blockIdx.x);
+    {
+        const int64_t t0 = a.runs.begin(blockIdx.x);
+        w.left = (int)(a.runs.begin(blockIdx.x + 1) - t0);
+        w.x = (int)(t0 / a.runs.ytiles);
+        w.y0 = w.y = (int)(t0 - (int64_t)w.x * a.runs.ytiles);
+        seg_end(w);
+    }
     bool ok = true;
-    uint32_t g = 0, xu = 0;  // tiles and units fed (TMA thread) or taken (the others)
+    uint32_t g = 0, xu = 0;  // tiles and segments fed (TMA warp) or taken (the others)
 
     if (warp == 0) {
-        for (; w.u < a.units; step(w), ++g) {
+        for (; w.left; step(w), ++g) {
             if (w.y == w.y0) {
                 const uint32_t b = xu % S::XB;
                 ok = head_wait(&xempty[b], ((xu / S::XB) & 1) ^ 1, a.wait_ns, gave_up);
@@ -204,7 +209,7 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
     } else if (warp == 1 || warp == 2) {
         const uint32_t idesc = idesc_f16(128, BY, a.fmt, false, false), turn = warp - 1;
         const int ksteps = (a.D + 15) / 16;
-        for (; w.u < a.units; ++g) {
+        for (; w.left; ++g) {
             const uint32_t b = xu % S::XB, st = g % S::kStages, sb = g % NS;
             if (w.y == w.y0) {
                 ok = head_wait(&xfull[b], (xu / S::XB) & 1, a.wait_ns, gave_up);
@@ -241,7 +246,7 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
     } else if (MODE != kLse && warp == 3) {
         const uint32_t idesc = idesc_f16(128, DT, a.fmt, false, true), idesc2 = idesc_f16(128, 2 * DT, a.fmt, false, true);
         uint32_t fl = 0;
-        for (; w.u < a.units; step(w), ++g) {
+        for (; w.left; step(w), ++g) {
             const uint32_t st = g % S::kStages, sb = g % NS, ob = fl % OB;
             const bool first = SPLIT || w.y == w.y0, last = SPLIT || w.y + 1 == w.y1;
             if (first) ok = head_wait(&oempty[ob], ((fl / OB) & 1) ^ 1, a.wait_ns, gave_up);
@@ -277,7 +282,7 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
         const int set = (warp - 12) / S::kDzSet, quad = warp & 3, part = (warp - 12) % S::kDzSet >> 2;  // its 32 rows and 64 columns
         const float c0 = a.ctemp * exp2i(-amax_exp(a.amax_h)) * exp2i(-amax_exp(a.amax_w));
         float c = c0, run_m = -INFINITY, run_s = 0.f;
-        for (; w.u < a.units; ++g) {
+        for (; w.left; ++g) {
             const int64_t row = (int64_t)w.x * 128 + quad * 32 + lane;
             if (w.y == w.y0) {
                 run_m = -INFINITY;
@@ -304,7 +309,7 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
                 }
             }
             if (w.y + 1 == w.y1 && row < a.X)
-                a.part[(row * a.splits + w.split) * S::kParts + set * (S::kParts / 2) + part] =
+                a.part[(row * a.slots + ((int)blockIdx.x - a.runs.first(w.x))) * S::kParts + set * (S::kParts / 2) + part] =
                     make_float2(run_m == -INFINITY ? -INFINITY : run_m * c, run_s);
             step(w);
         }
@@ -314,7 +319,7 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
         // fetched while the warp works on the tile before; by asynchronous copies, which
         // hold no registers meanwhile
         auto fetch = [&](const Walk& t, Ahead& to) {
-            if (t.u >= a.units) return;
+            if (!t.left) return;
             const int x32 = t.x * 4 + quad, y32 = t.y * (BY / 32) + part * 2;
             constexpr int kHalf = COLS ? 16 : 8;  // lanes that copy each of the two rows of floats
             if (lane < 2 * kHalf) {
@@ -327,17 +332,17 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
                 cp16(&to.blk[lane], a.blocks + (have ? (int64_t)vb * a.nblocks + nb : 0), have);
             }
         };
-        if (set && w.u < a.units) step(w);
+        if (set && w.left) step(w);
         int now = 0;
         fetch(w, ahead[warp - 12][0]);
-        for (g = set; w.u < a.units; g += 2, now ^= 1) {
+        for (g = set; w.left; g += 2, now ^= 1) {
             const uint32_t sb = g % NS;
             const int64_t left = a.Y - ((int64_t)w.y * BY + part * 64);  // streamed rows from this warp's first column on
             const Ahead& my = ahead[warp - 12][now];
             cp_wait();
             __syncwarp();
             step(w);
-            if (w.u < a.units) step(w);
+            if (w.left) step(w);
             fetch(w, ahead[warp - 12][now ^ 1]);
             ok = head_wait(&sfull[g % S::kStages], (g / S::kStages) & 1, a.wait_ns, gave_up);
             if (!ok) break;
@@ -413,9 +418,22 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
         const float s1 = exp2i(-amax_exp(a.amax_z)), s2 = exp2i(-amax_exp(COLS ? a.amax_h : a.amax_w));
         constexpr int OC = DT / 64;  // 32-column chunks of this warp's half
         uint32_t fl = 0;
-        for (; ok && w.u < a.units; start(w, w.u + (int)gridDim.x)) {
+        bool first = true;
+        while (ok && w.left) {
             const int64_t row = (int64_t)w.x * 128 + quad * 32 + lane;
             const uint32_t l0 = tmem + ((uint32_t)(quad * 32) << 16) + S::kOutCol + half * (DT / 2);
+            const bool whole = w.y0 == 0 && w.y1 == a.runs.ytiles;
+            float* part = a.partial + (((int64_t)blockIdx.x * 2 + !first) * 128 + quad * 32 + lane) * a.to.pp;
+            auto put = [&](float(&v)[32], int col) {
+                if (row >= a.X || col >= a.D) return;
+                if (whole) {
+                    store_out(a.to, 0, row, col, a.X, a.D, v, s1, s2);
+                } else {
+                    float4* p = reinterpret_cast<float4*>(part + col);
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) p[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+                }
+            };
             if (SPLIT) {
                 float sum[OC][32];
 #pragma unroll
@@ -443,10 +461,7 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
                 }
                 if (!ok) break;
 #pragma unroll
-                for (int ch = 0; ch < OC; ++ch) {
-                    const int64_t col = half * (DT / 2) + ch * 32;
-                    if (row < a.X && col < a.D) store_out(a.to, w.split, row, col, a.X, a.D, sum[ch], s1, s2);
-                }
+                for (int ch = 0; ch < OC; ++ch) put(sum[ch], half * (DT / 2) + ch * 32);
             } else {
                 const uint32_t ob = fl % OB;
                 ok = head_wait(&ofull[ob], (fl / OB) & 1, a.wait_ns, gave_up);
@@ -455,7 +470,6 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
                 tc_fence_after();
 #pragma unroll
                 for (int ch = 0; ch < OC; ++ch) {
-                    const int64_t col = half * (DT / 2) + ch * 32;
                     float v[32];
                     tm_ld32(l0 + ob * S::kOut + ch * 32, v);
                     tm_wait_ld(v);
@@ -464,9 +478,14 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&oempty[ob]);
                     }
-                    if (row < a.X && col < a.D) store_out(a.to, w.split, row, col, a.X, a.D, v, s1, s2);
+                    put(v, half * (DT / 2) + ch * 32);
                 }
             }
+            first = false;
+            w.left -= w.y1 - w.y0;
+            ++w.x;
+            w.y0 = 0;
+            seg_end(w);
         }
     }
     if (!ok && lead) {
@@ -489,6 +508,59 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
     }
     tc_fence_after();
     if (warp == 2) tc_dealloc(tmem, 512);
+}
+
+// Rows of an x that more than one run has tiles of: their segments summed in run order,
+// 128 / gridDim.y rows per blockIdx.y.  blockIdx.x is the x, or (by_boundary: more x
+// than runs) the boundary between two runs that lies in it; the first boundary inside
+// an x takes it.
+__global__ void __launch_bounds__(128) k_head_join(Runs runs, int by_boundary, const float* partial, OutArgs to, int64_t X, int D,
+                                                   const uint32_t* amax_z, const uint32_t* amax_y) {
+    __shared__ int sh[4];
+    if (threadIdx.x == 0) {
+        int64_t x = blockIdx.x;
+        bool split = true;
+        int b = 0, last = 0, slot0 = 0;
+        if (by_boundary) {
+            const int64_t t = runs.begin(blockIdx.x + 1);
+            x = t / runs.ytiles;
+            split = x * runs.ytiles != t;
+        }
+        if (split) {
+            b = runs.first(x);
+            last = runs.last(x);
+            split = b != last && (!by_boundary || b == (int)blockIdx.x);
+            // in its first run x may come behind others (slot 1); every later run begins inside x
+            slot0 = runs.begin(b) < x * runs.ytiles;
+        }
+        sh[0] = split ? (int)x : -1;
+        sh[1] = b;
+        sh[2] = last - b;
+        sh[3] = slot0;
+    }
+    __syncthreads();
+    const int64_t x = sh[0];
+    if (x < 0) return;
+    const int more = sh[2], per_row = (int)to.pp / 4, rows = 128 / per_row, span = 128 / gridDim.y;
+    const int c = (int)threadIdx.x % per_row * 4, r0 = (int)threadIdx.x / per_row;
+    if (r0 >= rows || c >= D) return;
+    const float s1 = exp2i(-amax_exp(amax_z)), s2 = exp2i(-amax_exp(amax_y));
+    const int64_t step = 256 * to.pp;
+    for (int i = r0; i < span; i += rows) {
+        const int r = blockIdx.y * span + i;
+        if (x * 128 + r >= X) break;
+        const float* p = partial + ((int64_t)sh[1] * 256 + r) * to.pp + c;
+        float4 s = *reinterpret_cast<const float4*>(p + sh[3] * 128 * to.pp);
+#pragma unroll 4
+        for (int k = 1; k <= more; ++k) {
+            const float4 v = *reinterpret_cast<const float4*>(p + k * step);
+            s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
+        }
+        const float v[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (c + j < D) store_one(to.out, (x * 128 + r) * to.ldo + c + j, v[j] * s1 * s2, to.type);
+    }
 }
 
 }  // namespace ttemb
