@@ -21,7 +21,8 @@
 //
 // Types.  bf16 and f16 inputs go to the tensor cores as they are.  An fp32 input x
 // is split as x 2^e = hi + lo with hi, lo in f16 (e a power-of-two scale that puts
-// the largest magnitude near 2^14) and a product is taken as hi hi + hi lo + lo hi,
+// the largest magnitude near 2^14: of a hidden row in the forward pass, of 128 table
+// rows, of all hidden rows that count and of all of dz in the backward pass) and a product is taken as hi hi + hi lo + lo hi,
 // so 22 bits of each operand enter, with fp32 accumulation; lo lo (2^-22 of the
 // product and below) is dropped.  dz is rounded to the inputs' 16-bit type before
 // the two gradient products (relative 2^-9 or 2^-12 an entry, independent errors,
@@ -311,13 +312,11 @@ __global__ void k_head_fix(const int* ids, const float* dzt, int64_t total, int 
     if (split) dz[piece + at] = (uint16_t)pack16(dzt[i] - unpack_f16(w).x, 0.f, 0);
 }
 
-// Largest finite magnitudes: blockIdx.y = 0: |weight| -> amax[1]; 1: |hidden| over
-// the rows that count -> amax[0]; 2: |grad| T over the same rows -> amax[2].
-// A largest value is the same in whatever order the atomics arrive.
+// Largest finite magnitudes over the rows that count: blockIdx.y = 0: |grad| T ->
+// amax[2]; 1 (fp32): |hidden| -> amax[0].  A largest value is the same in whatever order
+// the atomics arrive.
 __global__ void __launch_bounds__(256) k_head_absmax(HeadIn in, Target t, const float* grad, int distill, uint32_t* amax) {
-    const int what = blockIdx.y == 0 ? 1 : (blockIdx.y == 1 ? 0 : 2);
     const int lane = threadIdx.x & 31;
-    const int64_t warp0 = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5), warps = (int64_t)gridDim.x * 8;
     uint32_t m = 0;
     auto take = [&](float x) {
         const uint32_t b = __float_as_uint(x) & 0x7FFFFFFFu;
@@ -329,70 +328,119 @@ __global__ void __launch_bounds__(256) k_head_absmax(HeadIn in, Target t, const 
             if (t.ids[n * t.K + k] >= 0) return true;
         return false;
     };
-    if (what == 2) {
+    if (blockIdx.y == 0) {
         for (int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x; n < in.N; n += (int64_t)gridDim.x * 256)
             if (counts(n)) take(grad[n] * t.T);
     } else {
-        const float* x = static_cast<const float*>(what == 1 ? in.w : in.h);
-        const int64_t rows = what == 1 ? in.V : in.N, ld = what == 1 ? in.ldw : in.ldh;
-        if (what == 1 && in.vec && ld == in.D) {
-            const float4* x4 = reinterpret_cast<const float4*>(x);
-            const int64_t n4 = rows * in.D / 4, step = (int64_t)gridDim.x * 256;
-#pragma unroll 4
-            for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n4; i += step) {
-                const float4 v = x4[i];
-                take(v.x);
-                take(v.y);
-                take(v.z);
-                take(v.w);
-            }
-        } else {
-            for (int64_t n = warp0; n < rows; n += warps) {
-                if (what == 0 && !counts(n)) continue;
-                for (int i = lane; i < in.D; i += 32) take(x[n * ld + i]);
-            }
-        }
+        const float* x = static_cast<const float*>(in.h);
+        for (int64_t n = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); n < in.N; n += (int64_t)gridDim.x * 8)
+            if (counts(n))
+                for (int i = lane; i < in.D; i += 32) take(x[n * in.ldh + i]);
     }
     m = __reduce_max_sync(0xffffffffu, m);
-    if (lane == 0 && m) atomicMax(&amax[what], m);
+    if (lane == 0 && m) atomicMax(&amax[blockIdx.y == 0 ? 2 : 0], m);
 }
 
-// Packed copies with rows of Dp 16-bit elements: blockIdx.y = 0: the table (fp32:
-// hi and lo pieces under one scale for the whole table); 1: the hidden rows, a warp
-// per row (fp32: a scale of each row's own, its exponent in row_exp).
-template <class T>
-__global__ void __launch_bounds__(256) k_head_pack(HeadIn in, const uint32_t* amax, uint16_t* wp, uint16_t* hp, int* row_exp) {
+// 8 elements of a row from column c on; columns past D are 0.
+__device__ __forceinline__ void load8(const HeadIn& in, const float* src, int c, float (&x)[8]) {
+    if (in.vec) {
+        *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(src);
+        *reinterpret_cast<float4*>(x + 4) = *(reinterpret_cast<const float4*>(src) + 1);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = c + j < in.D ? src[j] : 0.f;
+    }
+}
+__device__ __forceinline__ uint32_t absmax8(const float (&x)[8], uint32_t m) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const uint32_t b = __float_as_uint(x[j]) & 0x7FFFFFFFu;
+        if (b < 0x7F800000u) m = max(m, b);
+    }
+    return m;
+}
+__device__ __forceinline__ void split8(const float (&x)[8], float sc, uint16_t* hi_at, uint16_t* lo_at) {
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float a = x[2 * j] * sc, b = x[2 * j + 1] * sc;
+        hi[j] = pack16(a, b, 0);
+        const float2 h = unpack_f16(hi[j]);
+        lo[j] = pack16(a - h.x, b - h.y, 0);
+    }
+    *reinterpret_cast<uint4*>(hi_at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4*>(lo_at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+}
+
+// Packed copies with rows of Dp 16-bit elements: blockIdx.y = 0: the table (fp32: hi and
+// lo pieces, a scale per 128 rows, its exponent in wexp: the rows of a tile of the
+// products, so that a scale is one factor per tile; up to 128 columns a tile is read
+// once and kept in registers); 1: the hidden rows, a warp per row (fp32: a scale of each
+// row's own, its exponent in row_exp).
+template <class T, int TH, int Q>  // TH threads; Q (fp32): 8-element groups that a thread holds of a tile, 0: none
+__global__ void __launch_bounds__(TH, 1024 / TH) k_head_pack(HeadIn in, uint16_t* wp, int* wexp, uint16_t* hp, int* row_exp) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (blockIdx.y == 0) {
         if (!wp) return;
-        const T* w = static_cast<const T*>(in.w);
         const int g = in.Dp / 8;  // 8-element groups of a row
-        const int64_t total = in.V * g, piece = in.V * in.Dp;
-        const float sc = sizeof(T) == 4 ? exp2i(scale_exp(amax[1])) : 1.f;
-        for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-            const int64_t r = i / g;
-            const int c = (int)(i - r * g) * 8;
-            const T* src = w + r * in.ldw + c;
-            if (sizeof(T) == 4) {
-                float x[8];
-                if (in.vec) {
-                    *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(src);
-                    *reinterpret_cast<float4*>(x + 4) = *(reinterpret_cast<const float4*>(src) + 1);
+        const int64_t piece = in.V * in.Dp;
+        if constexpr (sizeof(T) == 4) {
+            __shared__ uint32_t red[TH / 32];
+            const float* w = static_cast<const float*>(in.w);
+            const int64_t tiles = (in.V + 127) / 128;
+            for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+                const int64_t v0 = tile * 128;
+                const int rows = (int)min((int64_t)128, in.V - v0), total = rows * g;
+                float x[Q ? Q : 1][8];
+                uint32_t m = 0;
+                if (Q) {
+                    const uint32_t inv = 65536u / g + 1;  // i / g for i < 2,048, g <= 16
+#pragma unroll
+                    for (int q = 0; q < Q; ++q) {
+                        const int i = threadIdx.x + q * TH, r = (int)(i * inv >> 16), c = (i - r * g) * 8;
+                        if (i < total) {
+                            load8(in, w + (v0 + r) * in.ldw + c, c, x[q]);
+                            m = absmax8(x[q], m);
+                        }
+                    }
                 } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) x[j] = c + j < in.D ? to_f32(src[j]) : 0.f;
+                    for (int i = threadIdx.x; i < total; i += TH) {
+                        const int r = i / g, c = (i - r * g) * 8;
+                        load8(in, w + (v0 + r) * in.ldw + c, c, x[0]);
+                        m = absmax8(x[0], m);
+                    }
                 }
-                uint32_t hi[4], lo[4];
+                m = __reduce_max_sync(0xffffffffu, m);
+                if (lane == 0) red[warp] = m;
+                __syncthreads();
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float a = x[2 * j] * sc, b = x[2 * j + 1] * sc;
-                    hi[j] = pack16(a, b, 0);
-                    const float2 h = unpack_f16(hi[j]);
-                    lo[j] = pack16(a - h.x, b - h.y, 0);
+                for (int q = 0; q < TH / 32; ++q) m = max(m, red[q]);
+                __syncthreads();
+                const int e = scale_exp(m);
+                const float sc = exp2i(e);
+                if (threadIdx.x == 0) wexp[tile] = e;
+                uint16_t* to = wp + v0 * in.Dp;
+                if (Q) {
+#pragma unroll
+                    for (int q = 0; q < Q; ++q) {
+                        const int i = threadIdx.x + q * TH;
+                        if (i < total) split8(x[q], sc, to + i * 8, to + piece + i * 8);
+                    }
+                } else {
+                    for (int i = threadIdx.x; i < total; i += TH) {
+                        const int r = i / g, c = (i - r * g) * 8;
+                        load8(in, w + (v0 + r) * in.ldw + c, c, x[0]);
+                        split8(x[0], sc, to + (int64_t)i * 8, to + piece + (int64_t)i * 8);
+                    }
                 }
-                *reinterpret_cast<uint4*>(wp + i * 8) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                *reinterpret_cast<uint4*>(wp + piece + i * 8) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-            } else {
-                const uint16_t* s = reinterpret_cast<const uint16_t*>(src);
+            }
+        } else {
+            const uint16_t* w = static_cast<const uint16_t*>(in.w);
+            const int64_t total = in.V * g;
+            for (int64_t i = (int64_t)blockIdx.x * TH + threadIdx.x; i < total; i += (int64_t)gridDim.x * TH) {
+                const int64_t r = i / g;
+                const int c = (int)(i - r * g) * 8;
+                const uint16_t* s = w + r * in.ldw + c;
                 uint16_t x[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) x[j] = c + j < in.D ? s[j] : (uint16_t)0;
@@ -401,9 +449,8 @@ __global__ void __launch_bounds__(256) k_head_pack(HeadIn in, const uint32_t* am
         }
     } else {
         if (!hp) return;
-        const int lane = threadIdx.x & 31;
         const int64_t piece = in.N * in.Dp;
-        for (int64_t n = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); n < in.N; n += (int64_t)gridDim.x * 8) {
+        for (int64_t n = (int64_t)blockIdx.x * (TH / 32) + warp; n < in.N; n += (int64_t)gridDim.x * (TH / 32)) {
             const T* h = static_cast<const T*>(in.h) + n * in.ldh;
             if (sizeof(T) == 4) {
                 uint32_t m = 0;
@@ -555,7 +602,7 @@ bool run_fused(const Operand& X, const Operand& Y, FusedArgs a, cudaStream_t st)
     const bool by_boundary = a.runs.xtiles >= a.runs.blocks;
     const unsigned gx = (unsigned)(by_boundary ? a.runs.blocks - 1 : a.runs.xtiles);
     const unsigned gy = gx >= 256 ? 1 : (gx >= 64 ? 4 : (gx >= 16 ? 16 : 64));  // a block or more per SM
-    k_head_join<<<dim3(gx, gy), 128, 0, st>>>(a.runs, by_boundary, a.partial, a.to, a.X, a.D, a.amax_z, MODE == kDweight ? a.amax_h : a.amax_w);
+    k_head_join<<<dim3(gx, gy), 128, 0, st>>>(a.runs, by_boundary, a.partial, a.to, a.X, a.D, a.amax_z, MODE == kDweight ? a.amax_h : nullptr);
     return cudaGetLastError() == cudaSuccess;
 }
 
@@ -702,13 +749,12 @@ tt_status make_plan(const tt_head* hd, int K, Plan* p) {
 struct FwdWs {
     float2* part;
     uint16_t *hp, *wp;
-    int* row_exp;
-    uint32_t* amax;
+    int *row_exp, *wexp;
 };
 size_t fwd_ws(const Plan& p, void* base, FwdWs* w) {
     Arena a(base);
     const int64_t pc = p.split ? 2 : 1;
-    w->amax = a.get<uint32_t>(4);
+    w->wexp = a.get<int>(p.split ? cdiv(p.in.V, 128) : 0);
     w->part = a.get<float2>(p.in.N * p.slots * p.per_slot);
     w->row_exp = a.get<int>(p.split ? p.in.N : 0);
     w->hp = a.get<uint16_t>(p.pack_h ? pc * p.in.N * p.in.Dp : 0);
@@ -719,7 +765,7 @@ size_t fwd_ws(const Plan& p, void* base, FwdWs* w) {
 struct BwdWs {
     uint32_t* amax;
     float *nlse, *scale, *joins, *dzt, *dh_part, *dw_part;
-    int* ids;
+    int *ids, *wexp;
     TargetBlock* blocks;
     TargetEntry* ents;
     uint16_t *hp, *wp, *dz;
@@ -728,6 +774,7 @@ size_t bwd_ws(const Plan& p, int K, void* base, BwdWs* w) {
     Arena a(base);
     const int64_t pc = p.split ? 2 : 1, nk = p.in.N * K;
     w->amax = a.get<uint32_t>(4);
+    w->wexp = a.get<int>(p.split ? cdiv(p.in.V, 128) : 0);
     w->nlse = a.get<float>(cdiv(p.in.N, 128) * 128);
     w->scale = a.get<float>(cdiv(p.in.N, 128) * 128);
     w->ids = a.get<int>(p.fused ? 0 : nk);
@@ -750,6 +797,19 @@ unsigned grid_of(int64_t items, int per_block, int sms, int per_sm) {
 
 bool launch_ok() { return cudaGetLastError() == cudaSuccess; }
 
+template <class T>
+bool launch_pack(const Plan& p, int64_t hidden_rows, uint16_t* wp, int* wexp, uint16_t* hp, int* row_exp, cudaStream_t st) {
+    const int64_t w = !wp ? 0 : (p.split ? cdiv(p.in.V, 128) : cdiv(p.in.V * (p.in.Dp / 8), 256)), h = cdiv(hidden_rows, 8);
+    const dim3 grid(grid_of(w > h ? w : h, 1, p.sms, 16), hp ? 2 : 1);
+    if (p.split && p.in.Dp <= 64)
+        k_head_pack<T, 256, 4><<<grid, 256, 0, st>>>(p.in, wp, wexp, hp, row_exp);
+    else if (p.split && p.in.Dp <= 128)
+        k_head_pack<T, 512, 4><<<grid, 512, 0, st>>>(p.in, wp, wexp, hp, row_exp);
+    else
+        k_head_pack<T, 256, 0><<<grid, 256, 0, st>>>(p.in, wp, wexp, hp, row_exp);
+    return launch_ok();
+}
+
 GemmArgs gemm_args(const Plan& p, int* err) {
     GemmArgs a{};
     a.strip = 1;
@@ -766,19 +826,11 @@ tt_status head_forward(const Plan& p, const Target& t, float* loss, float* lse, 
     if (fwd_ws(p, ws, &w) > ws_bytes) return TT_ERR_ARG;
     if (in.N == 0) return TT_OK;
     const bool distill = t.logits != nullptr;
-    if (p.split) {
-        if (cudaMemsetAsync(w.amax, 0, 16, st) != cudaSuccess) return TT_ERR_CUDA;
-        k_head_absmax<<<dim3(grid_of(in.V * in.D, 4096, p.sms, 8), 1), 256, 0, st>>>(in, t, nullptr, distill, w.amax);
-        if (!launch_ok()) return TT_ERR_CUDA;
-    }
     if (p.pack_h || p.pack_w) {
-        k_head_pack<T><<<dim3(grid_of(p.pack_w ? in.V * (in.Dp / 8) : in.N * 32, 256, p.sms, 8), 2), 256, 0, st>>>(
-            in, w.amax, p.pack_w ? w.wp : nullptr, p.pack_h ? w.hp : nullptr, w.row_exp);
-        if (!launch_ok()) return TT_ERR_CUDA;
+        if (!launch_pack<T>(p, in.N, p.pack_w ? w.wp : nullptr, w.wexp, p.pack_h ? w.hp : nullptr, w.row_exp, st)) return TT_ERR_CUDA;
     }
     const Operand H{p.pack_h ? w.hp : static_cast<const uint16_t*>(in.h), in.N, in.D, p.pack_h ? in.Dp : in.ldh, in.N * in.Dp};
     const Operand W{p.pack_w ? w.wp : static_cast<const uint16_t*>(in.w), in.V, in.D, p.pack_w ? in.Dp : in.ldw, in.V * in.Dp};
-    const uint32_t* amax_w = p.split ? w.amax + 1 : nullptr;
     const int* row_exp = p.split ? w.row_exp : nullptr;
     bool ok;
     if (p.fused_lse) {
@@ -788,7 +840,7 @@ tt_status head_forward(const Plan& p, const Target& t, float* loss, float* lse, 
         a.slots = p.slots;
         a.fmt = p.fmt;
         a.err = err;
-        a.amax_w = amax_w;
+        a.wexp = w.wexp;
         a.row_exp = row_exp;
         a.ctemp = kLog2e / t.T;
         a.part = w.part;
@@ -799,7 +851,7 @@ tt_status head_forward(const Plan& p, const Target& t, float* loss, float* lse, 
         a.N = in.V;
         a.strip = p.strip;
         a.chunks = (int)cdiv(in.D, kBK);
-        a.amax_b = amax_w;
+        a.wexp = w.wexp;
         a.row_exp = row_exp;
         a.ctemp = kLog2e / t.T;
         a.part = w.part;
@@ -824,20 +876,12 @@ tt_status head_backward(const Plan& p, const Target& t, const float* lse, const 
     const uint32_t* amax = p.fmt ? nullptr : w.amax;  // bf16 has fp32's range: dz needs no scale
     if (amax) {
         if (cudaMemsetAsync(w.amax, 0, 16, st) != cudaSuccess) return TT_ERR_CUDA;
-        // f16 inputs are taken as they are: only dz is scaled (blockIdx.y = 2)
-        if (p.split) {
-            k_head_absmax<<<dim3(grid_of(in.V * in.D, 4096, p.sms, 8), 3), 256, 0, st>>>(in, t, grad, distill, w.amax);
-        } else {
-            HeadIn none = in;
-            none.V = 0;
-            none.D = 0;
-            k_head_absmax<<<dim3(grid_of(in.N, 256, p.sms, 1), 3), 256, 0, st>>>(none, t, grad, distill, w.amax);
-        }
+        // f16 inputs are taken as they are: only dz is scaled
+        k_head_absmax<<<dim3(grid_of(in.N, p.split ? 16 : 256, p.sms, 4), p.split ? 2 : 1), 256, 0, st>>>(in, t, grad, distill, w.amax);
         if (!launch_ok()) return TT_ERR_CUDA;
     }
     if (p.pack_w) {
-        k_head_pack<T><<<dim3(grid_of(in.V * (in.Dp / 8), 256, p.sms, 16), 1), 256, 0, st>>>(in, w.amax, w.wp, nullptr, nullptr);
-        if (!launch_ok()) return TT_ERR_CUDA;
+        if (!launch_pack<T>(p, 0, w.wp, w.wexp, nullptr, nullptr, st)) return TT_ERR_CUDA;
     }
     TargetEntry* ents = p.fused ? w.ents : nullptr;
     if (ents && cudaMemsetAsync(w.blocks, 0, (size_t)(p.nblocks * p.vblocks) * sizeof(TargetBlock), st) != cudaSuccess) return TT_ERR_CUDA;
@@ -848,7 +892,7 @@ tt_status head_backward(const Plan& p, const Target& t, const float* lse, const 
         k_head_rows<T, false><<<(unsigned)in.N, kRowThreads, 12, st>>>(in, t, lse, grad, amax, w.nlse, w.scale, w.ids, w.dzt, w.blocks, (int)p.nblocks,
                                                                      ents, w.hp, err);
     if (!launch_ok()) return TT_ERR_CUDA;
-    const uint32_t *ah = amax, *aw = amax ? amax + 1 : nullptr, *az = amax ? amax + 2 : nullptr;
+    const uint32_t *ah = amax, *az = amax ? amax + 2 : nullptr;
     const int64_t wpitch = p.pack_w ? in.Dp : in.ldw;
     const uint16_t* w0 = p.pack_w ? w.wp : static_cast<const uint16_t*>(in.w);
     const Operand H{w.hp, in.N, in.D, in.Dp, in.N * in.Dp};
@@ -873,8 +917,8 @@ tt_status head_backward(const Plan& p, const Target& t, const float* lse, const 
         a.fmt = p.fmt;
         a.err = err;
         a.amax_h = ah;
-        a.amax_w = aw;
         a.amax_z = az;
+        a.wexp = w.wexp;
         a.ctemp = kLog2e / t.T;
         a.nlse = w.nlse;
         a.scale = w.scale;
@@ -900,7 +944,7 @@ tt_status head_backward(const Plan& p, const Target& t, const float* lse, const 
         a.N = P;
         a.chunks = (int)cdiv(in.D, kBK);
         a.amax_a = ah;
-        a.amax_b = aw;
+        a.wexp = w.wexp + v0 / 128;  // a piece begins at a multiple of 256 rows
         a.ctemp = kLog2e / t.T;
         a.nlse = w.nlse;
         a.scale = w.scale;
@@ -930,12 +974,12 @@ tt_status head_backward(const Plan& p, const Target& t, const float* lse, const 
         c.chunks = (int)cdiv(P, kBK);
         c.splits = p.dh_splits;
         c.amax_a = az;
-        c.amax_b = aw;
+        c.wexp = p.split ? w.wexp + v0 / 128 : nullptr;
         c.to = dest(p.dh_direct ? dh : nullptr, w.dh_part);
         c.to.accumulate = i > 0;
         if (!out_gemm<false>(p.split, Z, W, c, p.sms, st)) return TT_ERR_CUDA;
     }
-    if (!p.dh_direct && !reduce(w.dh_part, p.dh_splits, in.N, dh, aw)) return TT_ERR_CUDA;
+    if (!p.dh_direct && !reduce(w.dh_part, p.dh_splits, in.N, dh, nullptr)) return TT_ERR_CUDA;
     return TT_OK;
 }
 

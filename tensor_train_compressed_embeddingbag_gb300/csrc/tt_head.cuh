@@ -100,10 +100,20 @@ __device__ __forceinline__ void mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uin
         : "memory");
 }
 
+__device__ __forceinline__ void axpy2(float& x, float& y, float ax, float ay, float f) {
+    asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 c, {%0, %1};\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %4};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "+f"(x), "+f"(y)
+        : "f"(ax), "f"(ay), "f"(f));
+}
+
 // 16 bytes from global to shared memory without a register (zeros if !have); done after
 // the thread's cp_wait.  What the other lanes of a warp copied is seen after a __syncwarp.
 __device__ __forceinline__ void cp16(void* dst, const void* src, bool have) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(have ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp4(void* dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 

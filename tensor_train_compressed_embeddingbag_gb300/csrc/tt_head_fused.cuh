@@ -68,10 +68,10 @@ struct FusedArgs {
     int fmt;
     uint64_t wait_ns;
     int* err;
-    const uint32_t* amax_h;  // power-of-two scales of hidden, weight, dz (null: none)
-    const uint32_t* amax_w;
+    const uint32_t* amax_h;  // power-of-two scales of hidden and dz (null: none)
     const uint32_t* amax_z;
-    const int* row_exp;      // kLse: per hidden row instead (null: amax_h)
+    const int* row_exp;      // SPLIT, kLse: hidden's, per row instead
+    const int* wexp;         // SPLIT: weight's, per 128 rows
     float ctemp;             // log2(e) / T
     float2* part;            // kLse: [X][slots][kParts] (maximum in log2 units, sum), a slot per run
     int slots;
@@ -122,6 +122,7 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
     struct Ahead {
         float nlse[COLS ? 64 : 32], scale[COLS ? 64 : 32];
         uint4 blk[2];
+        int wexp[4];  // the first: scale of the tile's table rows
     };
     __shared__ __align__(16) Ahead ahead[S::kDzWarps][2];
     __shared__ uint32_t tmem_slot;
@@ -280,14 +281,19 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
         }
     } else if (MODE == kLse && warp >= 12) {
         const int set = (warp - 12) / S::kDzSet, quad = warp & 3, part = (warp - 12) % S::kDzSet >> 2;  // its 32 rows and 64 columns
-        const float c0 = a.ctemp * exp2i(-amax_exp(a.amax_h)) * exp2i(-amax_exp(a.amax_w));
-        float c = c0, run_m = -INFINITY, run_s = 0.f;
+        float cr = a.ctemp, c = cr, run_m = -INFINITY, run_s = 0.f;  // run_m in units of c
+        int we = 0, we_next = SPLIT && w.left ? __ldg(&a.wexp[w.y / (128 / BY)]) : 0;
         for (; w.left; ++g) {
             const int64_t row = (int64_t)w.x * 128 + quad * 32 + lane;
             if (w.y == w.y0) {
                 run_m = -INFINITY;
                 run_s = 0.f;
-                if (a.row_exp) c = row < a.X ? c0 * exp2i(-__ldg(&a.row_exp[row])) : c0;
+                if (SPLIT) cr = row < a.X ? a.ctemp * exp2i(-__ldg(&a.row_exp[row])) : a.ctemp;
+            }
+            if (SPLIT) {  // the tile's scale; the maximum so far in its units (a power of two between them)
+                if (w.y != w.y0) run_m *= exp2i(we_next - we);
+                we = we_next;
+                c = cr * exp2i(-we);
             }
             if ((g & 1) == set) {
                 const uint32_t sb = g % NS;
@@ -312,10 +318,11 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
                 a.part[(row * a.slots + ((int)blockIdx.x - a.runs.first(w.x))) * S::kParts + set * (S::kParts / 2) + part] =
                     make_float2(run_m == -INFINITY ? -INFINITY : run_m * c, run_s);
             step(w);
+            if (SPLIT && w.left) we_next = __ldg(&a.wexp[w.y / (128 / BY)]);
         }
     } else if (MODE != kLse && warp >= 12) {
         const int set = (warp - 12) / S::kDzSet, quad = warp & 3, part = (warp - 12) % S::kDzSet >> 2;  // its 32 rows and 64 columns
-        const float c = a.ctemp * exp2i(-amax_exp(a.amax_h)) * exp2i(-amax_exp(a.amax_w));
+        const float c0 = a.ctemp * exp2i(-amax_exp(a.amax_h));
         // fetched while the warp works on the tile before; by asynchronous copies, which
         // hold no registers meanwhile
         auto fetch = [&](const Walk& t, Ahead& to) {
@@ -330,6 +337,7 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
                 const int nb = COLS ? y32 + lane : x32, vb = COLS ? x32 : y32 + lane;
                 const bool have = nb < a.nblocks && vb < a.vblocks;
                 cp16(&to.blk[lane], a.blocks + (have ? (int64_t)vb * a.nblocks + nb : 0), have);
+                if (SPLIT && lane == 0) cp4(to.wexp, a.wexp + (COLS ? t.x : t.y / (128 / BY)));
             }
         };
         if (set && w.left) step(w);
@@ -344,6 +352,7 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
             step(w);
             if (w.left) step(w);
             fetch(w, ahead[warp - 12][now ^ 1]);
+            const float c = SPLIT ? c0 * exp2i(-my.wexp[0]) : c0;
             ok = head_wait(&sfull[g % S::kStages], (g / S::kStages) & 1, a.wait_ns, gave_up);
             if (!ok) break;
             tc_fence_after();
@@ -415,7 +424,7 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
         }
     } else if (MODE != kLse && warp >= 4) {
         const int half = warp >= 8, quad = warp & 3;
-        const float s1 = exp2i(-amax_exp(a.amax_z)), s2 = exp2i(-amax_exp(COLS ? a.amax_h : a.amax_w));
+        const float s1 = exp2i(-amax_exp(a.amax_z)), s2 = COLS ? exp2i(-amax_exp(a.amax_h)) : 1.f;
         constexpr int OC = DT / 64;  // 32-column chunks of this warp's half
         uint32_t fl = 0;
         bool first = true;
@@ -442,6 +451,7 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
                     for (int j = 0; j < 32; ++j) sum[ch][j] = 0.f;
                 for (int f = w.y0; f < w.y1; ++f, ++fl) {
                     const uint32_t ob = fl % OB;
+                    const float f1 = COLS ? 1.f : exp2i(-__ldg(&a.wexp[f / (128 / BY)]));
                     ok = head_wait(&ofull[ob], (fl / OB) & 1, a.wait_ns, gave_up);
                     if (!ok) break;
                     tc_fence_after();
@@ -452,7 +462,13 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
                         for (int part = S::kOut / DT - 1; part >= 0; --part) {  // small products first
                             tm_read16(l0 + ob * S::kOut + part * DT + ch * 16, v);
 #pragma unroll
-                            for (int j = 0; j < 16; j += 2) add2(sum[ch / 2][(ch & 1) * 16 + j], sum[ch / 2][(ch & 1) * 16 + j + 1], v[j], v[j + 1]);
+                            for (int j = 0; j < 16; j += 2) {
+                                float &x = sum[ch / 2][(ch & 1) * 16 + j], &y = sum[ch / 2][(ch & 1) * 16 + j + 1];
+                                if (COLS)
+                                    add2(x, y, v[j], v[j + 1]);
+                                else
+                                    axpy2(x, y, v[j], v[j + 1], f1);  // exact product: f1 is a power of two
+                            }
                         }
                     }
                     tc_fence_before();

@@ -28,6 +28,7 @@ struct GemmArgs {
     const uint32_t* amax_a;
     const uint32_t* amax_b;
     const int* row_exp;  // per-row exponent of A (forward), else null
+    const int* wexp;     // SPLIT: exponent per 128 table rows: of B's rows (scores), along K (dhidden), else null
     float ctemp;         // log2(e) / T
     // kEpiStats
     float2* part;        // [M][nstrips][kParts] (maximum in log2 units, sum)
@@ -64,7 +65,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 const __grid_constant__ GemmArgs a) {
     using S = GemmShape<BN>;
     static_assert(BN % (32 * kParts) == 0 && (!SPLIT || BN <= 128), "the ranges' sums stay in registers");
-    constexpr int kSegs = SPLIT ? 3 : 1, kRange = 4;
+    constexpr int kSegs = SPLIT ? 3 : 1, kRange = 2;  // a range: 128 of K
     constexpr int kCh = BN / kParts / 32;  // 32-column chunks of a part
     extern __shared__ uint8_t raw[];
     __shared__ uint64_t full[S::kStages], empty[S::kStages], accfull[2], accempty[2], drain;
@@ -123,8 +124,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             int m, n0, n1, kb, ke, split;
             unit(u, m, n0, n1, kb, ke, split);
             for (int n = n0; ok && n < n1; ++n)
-                for (int r0 = kb; ok && r0 < ke; r0 += SPLIT ? kRange : ke - kb) {
-                    const int r1 = SPLIT ? min(r0 + kRange, ke) : ke;
+                for (int r0 = kb; ok && r0 < ke; r0 = SPLIT ? (r0 / kRange + 1) * kRange : ke) {
+                    const int r1 = SPLIT ? min((r0 / kRange + 1) * kRange, ke) : ke;
                     for (int seg = 0; ok && seg < kSegs; ++seg) {
                         const int za = SPLIT && seg == 0, zb = SPLIT && seg == 1;
                         for (int kc = r0; kc < r1; ++kc, ++it) {
@@ -160,8 +161,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             int m, n0, n1, kb, ke, split;
             unit(u, m, n0, n1, kb, ke, split);
             for (int n = n0; ok && n < n1; ++n)
-                for (int r0 = kb; ok && r0 < ke; r0 += SPLIT ? kRange : ke - kb, ++acc) {
-                    const int steps = (SPLIT ? min(kRange, ke - r0) : ke - kb) * kSegs;
+                for (int r0 = kb; ok && r0 < ke; r0 = SPLIT ? (r0 / kRange + 1) * kRange : ke, ++acc) {
+                    const int steps = (SPLIT ? min((r0 / kRange + 1) * kRange, ke) - r0 : ke - kb) * kSegs;
                     const uint32_t buf = acc & 1, d = tmem + buf * BN;
                     ok = head_wait(&accempty[buf], ((acc >> 1) & 1) ^ 1, a.wait_ns, gave_up);
                     if (!ok) break;
@@ -195,12 +196,17 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             unit(u, m, n0, n1, kb, ke, split);
             const int64_t row = (int64_t)m * 128 + r;
             const bool in = row < a.M;
-            float run_m = -INFINITY, run_s = 0.f, cr = c;
+            float run_m = -INFINITY, run_s = 0.f, cr = c, cu = c;  // run_m in units of cr
             float2 rc = make_float2(0.f, 0.f);
-            if (EPI == kEpiStats && a.row_exp && in) cr = c * exp2i(-a.row_exp[row]);
+            if (EPI == kEpiStats && a.row_exp && in) cu = cr = c * exp2i(-a.row_exp[row]);
             if (EPI == kEpiDz && in) rc = make_float2(a.nlse[row], a.scale[row]);
             for (int n = n0; ok && n < n1; ++n) {
                 const int64_t col0 = (int64_t)n * BN + part * (BN / kParts);
+                if (SPLIT && EPI != kEpiOut) {  // the tile's scale; the maximum so far in its units
+                    const float next = cu * exp2i(-__ldg(&a.wexp[n]));
+                    if (EPI == kEpiStats && n != n0) run_m *= cr / next;  // powers of two apart
+                    cr = next;
+                }
                 // 32 finished columns of this thread's row, the first of them `col`
                 auto finish = [&](float (&v)[32], int64_t col) {
                     if (EPI == kEpiStats) {
@@ -233,19 +239,20 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 };
                 if (SPLIT) {
                     float sum[kCh][32];
-                    for (int r0 = kb; ok && r0 < ke; r0 += kRange, ++acc) {
+                    for (int r0 = kb; ok && r0 < ke; r0 = (r0 / kRange + 1) * kRange, ++acc) {
                         const uint32_t buf = acc & 1;
                         ok = head_wait(&accfull[buf], (acc >> 1) & 1, a.wait_ns, gave_up);
                         if (!ok) break;
                         tc_fence_after();
                         const uint32_t t0 = tmem + buf * BN + ((uint32_t)(quad * 32) << 16) + part * (BN / kParts);
+                        const float f = EPI == kEpiOut && a.wexp ? exp2i(-__ldg(&a.wexp[r0 / kRange])) : 1.f;
 #pragma unroll
                         for (int ch = 0; ch < kCh; ++ch) {
                             float v[32];
                             tm_ld32(t0 + ch * 32, v);
                             tm_wait_ld(v);
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) sum[ch][j] = r0 == kb ? v[j] : sum[ch][j] + v[j];
+                            for (int j = 0; j < 32; ++j) sum[ch][j] = r0 == kb ? v[j] * f : fmaf(v[j], f, sum[ch][j]);
                         }
                         tc_fence_before();
                         __syncwarp();
