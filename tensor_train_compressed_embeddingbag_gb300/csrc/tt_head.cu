@@ -526,14 +526,8 @@ bool make_map(CUtensorMap* m, const void* p, int fmt, int64_t cols, int64_t rows
 
 constexpr int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-int sm_count() {
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-        cudaGetLastError();
-        return 0;
-    }
-    return n;
-}
+template <int A, int B, int C, int D, int E>
+struct KernelTag {};
 
 // Workspace cut into 256-byte aligned blocks; with a null base only the size counts.
 struct Arena {
@@ -554,7 +548,7 @@ struct Operand {  // a 16-bit matrix the products read
 };
 
 template <int BN, bool AMN, bool BMN, int EPI, bool SPLIT>
-bool run_gemm(const Operand& A, const Operand& B, GemmArgs a, int sms, cudaStream_t st) {
+bool run_gemm(const Operand& A, const Operand& B, GemmArgs a, int sms, int dev, cudaStream_t st) {
     CUtensorMap ma, mb;
     const int pieces = SPLIT ? 2 : 1;
     if (!make_map(&ma, A.p, a.fmt, A.cols, A.rows, pieces, A.pitch, A.piece, AMN ? 64 : 128)) return false;
@@ -565,28 +559,28 @@ bool run_gemm(const Operand& A, const Operand& B, GemmArgs a, int sms, cudaStrea
     a.units = EPI == kEpiOut ? (int64_t)a.mtiles * a.ntiles * a.splits : (int64_t)a.mtiles * a.nstrips;
     a.wait_ns = g_head_wait_ns;
     auto k = k_head_gemm<BN, AMN, BMN, EPI, SPLIT>;
-    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)GemmShape<BN>::kSmem) != cudaSuccess) return false;
+    if (!allow_smem<KernelTag<BN, AMN, BMN, EPI, SPLIT>>(k, dev, GemmShape<BN>::kSmem)) return false;
     k<<<(unsigned)(a.units < sms ? a.units : sms), kGemmThreads, GemmShape<BN>::kSmem, st>>>(ma, mb, a);
     return cudaGetLastError() == cudaSuccess;
 }
 
 // Scores: 128-column tiles for fp32 (the ranges' sums stay in registers).
 template <int EPI>
-bool score_gemm(int bn, bool split, const Operand& A, const Operand& B, const GemmArgs& a, int sms, cudaStream_t st) {
-    if (split) return run_gemm<128, false, false, EPI, true>(A, B, a, sms, st);
-    if (bn == 128) return run_gemm<128, false, false, EPI, false>(A, B, a, sms, st);
-    return run_gemm<256, false, false, EPI, false>(A, B, a, sms, st);
+bool score_gemm(int bn, bool split, const Operand& A, const Operand& B, const GemmArgs& a, int sms, int dev, cudaStream_t st) {
+    if (split) return run_gemm<128, false, false, EPI, true>(A, B, a, sms, dev, st);
+    if (bn == 128) return run_gemm<128, false, false, EPI, false>(A, B, a, sms, dev, st);
+    return run_gemm<256, false, false, EPI, false>(A, B, a, sms, dev, st);
 }
 
 // Gradient products.  AMN: dweight = dz^T hidden; else dhidden = dz weight.
 template <bool AMN>
-bool out_gemm(bool split, const Operand& A, const Operand& B, const GemmArgs& a, int sms, cudaStream_t st) {
-    if (split) return run_gemm<128, AMN, true, kEpiOut, true>(A, B, a, sms, st);
-    return run_gemm<256, AMN, true, kEpiOut, false>(A, B, a, sms, st);
+bool out_gemm(bool split, const Operand& A, const Operand& B, const GemmArgs& a, int sms, int dev, cudaStream_t st) {
+    if (split) return run_gemm<128, AMN, true, kEpiOut, true>(A, B, a, sms, dev, st);
+    return run_gemm<256, AMN, true, kEpiOut, false>(A, B, a, sms, dev, st);
 }
 
 template <int DT, bool SPLIT, int MODE>
-bool run_fused(const Operand& X, const Operand& Y, FusedArgs a, cudaStream_t st) {
+bool run_fused(const Operand& X, const Operand& Y, FusedArgs a, int dev, cudaStream_t st) {
     using S = FusedShape<DT, SPLIT>;
     CUtensorMap mx, my;
     if (!make_map(&mx, X.p, a.fmt, X.cols, X.rows, S::PC, X.pitch, X.piece, 128)) return false;
@@ -595,7 +589,7 @@ bool run_fused(const Operand& X, const Operand& Y, FusedArgs a, cudaStream_t st)
     a.Y = Y.rows;
     a.wait_ns = g_head_wait_ns;
     auto k = k_head_fused<DT, SPLIT, MODE>;
-    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem) != cudaSuccess) return false;
+    if (!allow_smem<KernelTag<DT, SPLIT, MODE, 0, -1>>(k, dev, S::kSmem)) return false;
     k<<<(unsigned)a.runs.blocks, S::kThreads, S::kSmem, st>>>(mx, my, a);
     if (cudaGetLastError() != cudaSuccess) return false;
     if (MODE == kLse || a.runs.blocks == 1) return true;
@@ -607,9 +601,9 @@ bool run_fused(const Operand& X, const Operand& Y, FusedArgs a, cudaStream_t st)
 }
 
 template <int MODE>
-bool fused(bool split, const Operand& X, const Operand& Y, const FusedArgs& a, cudaStream_t st) {
-    if (a.D <= 64) return split ? run_fused<64, true, MODE>(X, Y, a, st) : run_fused<64, false, MODE>(X, Y, a, st);
-    return split ? run_fused<128, true, MODE>(X, Y, a, st) : run_fused<128, false, MODE>(X, Y, a, st);
+bool fused(bool split, const Operand& X, const Operand& Y, const FusedArgs& a, int dev, cudaStream_t st) {
+    if (a.D <= 64) return split ? run_fused<64, true, MODE>(X, Y, a, dev, st) : run_fused<64, false, MODE>(X, Y, a, dev, st);
+    return split ? run_fused<128, true, MODE>(X, Y, a, dev, st) : run_fused<128, false, MODE>(X, Y, a, dev, st);
 }
 
 Runs make_runs(int64_t xrows, int64_t yrows, int by, int sms) {
@@ -646,7 +640,7 @@ int choose_splits(int64_t tiles, int64_t chunks, int sms) {
 struct Plan {
     HeadIn in;
     int type, fmt, split;    // split: fp32 operands in hi and lo pieces
-    int esize, sms;
+    int esize, sms, device;
     bool pack_h, pack_w;
     int bn_s;                // column tile of the score products
     int strip;
@@ -675,7 +669,7 @@ tt_status make_plan(const tt_head* hd, int K, Plan* p) {
     p->fmt = hd->dtype == TT_BF16;
     p->split = hd->dtype == TT_F32;
     p->esize = hd->dtype == TT_F32 ? 4 : 2;
-    p->sms = sm_count();
+    p->sms = head_sms(&p->device);
     if (p->sms <= 0) return TT_ERR_CUDA;
     if (((uintptr_t)hd->hidden_dev | (uintptr_t)hd->weight_dev) % p->esize) return TT_ERR_ARG;
     HeadIn& in = p->in;
@@ -707,8 +701,8 @@ tt_status make_plan(const tt_head* hd, int K, Plan* p) {
     p->fused_lse = p->split && in.D <= 128 && mt * cdiv(in.V, by) < 1ll << 31;
     if (p->fused_lse && in.N > 0) {
         p->runs_lse = make_runs(in.N, in.V, by, p->sms);
-        p->slots = 1;
-        for (int64_t x = 0; x < mt; ++x) p->slots = max(p->slots, p->runs_lse.last(x) - p->runs_lse.first(x) + 1);
+        const int64_t shortest = p->runs_lse.total() / p->runs_lse.blocks;  // tiles of a run, rounded down
+        p->slots = (int)(cdiv(p->runs_lse.ytiles, shortest) + 1);           // most runs that an x is in
         p->per_slot = 2 * (by / 64);
     }
     // backward
@@ -844,7 +838,7 @@ tt_status head_forward(const Plan& p, const Target& t, float* loss, float* lse, 
         a.row_exp = row_exp;
         a.ctemp = kLog2e / t.T;
         a.part = w.part;
-        ok = fused<kLse>(p.split, H, W, a, st);
+        ok = fused<kLse>(p.split, H, W, a, p.device, st);
     } else {
         GemmArgs a = gemm_args(p, err);
         a.M = in.N;
@@ -855,7 +849,7 @@ tt_status head_forward(const Plan& p, const Target& t, float* loss, float* lse, 
         a.row_exp = row_exp;
         a.ctemp = kLog2e / t.T;
         a.part = w.part;
-        ok = score_gemm<kEpiStats>(p.bn_s, p.split, H, W, a, p.sms, st);
+        ok = score_gemm<kEpiStats>(p.bn_s, p.split, H, W, a, p.sms, p.device, st);
     }
     if (!ok) return TT_ERR_CUDA;
     if (distill)
@@ -929,10 +923,10 @@ tt_status head_backward(const Plan& p, const Target& t, const float* lse, const 
         a.partial = w.joins;
         a.runs = p.runs_dw;
         a.to = dest(dw, nullptr);
-        if (!fused<kDweight>(p.split, W, H, a, st)) return TT_ERR_CUDA;
+        if (!fused<kDweight>(p.split, W, H, a, p.device, st)) return TT_ERR_CUDA;
         a.runs = p.runs_dh;
         a.to = dest(dh, nullptr);
-        return fused<kDhidden>(p.split, H, W, a, st) ? TT_OK : TT_ERR_CUDA;
+        return fused<kDhidden>(p.split, H, W, a, p.device, st) ? TT_OK : TT_ERR_CUDA;
     }
     const int64_t npieces = cdiv(in.V, p.P), dz_piece = in.N * p.pitch;
     for (int64_t i = 0; i < npieces; ++i) {
@@ -951,7 +945,7 @@ tt_status head_backward(const Plan& p, const Target& t, const float* lse, const 
         a.dz = w.dz;
         a.dz_pitch = p.pitch;
         a.dz_piece = dz_piece;
-        if (!score_gemm<kEpiDz>(p.bn_s, p.split, H, W, a, p.sms, st)) return TT_ERR_CUDA;
+        if (!score_gemm<kEpiDz>(p.bn_s, p.split, H, W, a, p.sms, p.device, st)) return TT_ERR_CUDA;
         k_head_fix<<<(unsigned)cdiv(in.N * t.K, 256), 256, 0, st>>>(w.ids, w.dzt, in.N * t.K, t.K, (int)v0, (int)P, w.dz, p.pitch, dz_piece,
                                                                 p.fmt, p.split);
         if (!launch_ok()) return TT_ERR_CUDA;
@@ -965,7 +959,7 @@ tt_status head_backward(const Plan& p, const Target& t, const float* lse, const 
         b.amax_b = ah;
         void* dwp = static_cast<uint8_t*>(dw) + (size_t)v0 * in.D * p.esize;
         b.to = dest(p.dw_splits > 1 ? nullptr : dwp, w.dw_part);
-        if (!out_gemm<true>(p.split, Z, H, b, p.sms, st)) return TT_ERR_CUDA;
+        if (!out_gemm<true>(p.split, Z, H, b, p.sms, p.device, st)) return TT_ERR_CUDA;
         if (p.dw_splits > 1 && !reduce(w.dw_part, p.dw_splits, P, dwp, ah)) return TT_ERR_CUDA;
 
         GemmArgs c = gemm_args(p, err);  // the piece's share of dhidden: [N][D] += dz W
@@ -977,7 +971,7 @@ tt_status head_backward(const Plan& p, const Target& t, const float* lse, const 
         c.wexp = p.split ? w.wexp + v0 / 128 : nullptr;
         c.to = dest(p.dh_direct ? dh : nullptr, w.dh_part);
         c.to.accumulate = i > 0;
-        if (!out_gemm<false>(p.split, Z, W, c, p.sms, st)) return TT_ERR_CUDA;
+        if (!out_gemm<false>(p.split, Z, W, c, p.sms, p.device, st)) return TT_ERR_CUDA;
     }
     if (!p.dh_direct && !reduce(w.dh_part, p.dh_splits, in.N, dh, nullptr)) return TT_ERR_CUDA;
     return TT_OK;

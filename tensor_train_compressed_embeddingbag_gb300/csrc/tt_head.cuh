@@ -15,6 +15,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <atomic>
+
 #include "tt_tc.cuh"
 
 namespace ttemb {
@@ -340,6 +342,43 @@ __device__ __forceinline__ void store_out(const OutArgs& o, int split, int64_t r
             p[q] = x;
         }
     }
+}
+
+// ---------------------------------------------------------------- host
+
+constexpr int kMaxHeadDevices = 64;
+
+// Multiprocessors of the current device, 0 if there is none; asked once per device.
+inline int head_sms(int* device = nullptr) {
+    static std::atomic<int> known[kMaxHeadDevices];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxHeadDevices) {
+        cudaGetLastError();
+        return 0;
+    }
+    if (device) *device = dev;
+    n = known[dev].load(std::memory_order_relaxed);
+    if (n) return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    known[dev].store(n, std::memory_order_relaxed);
+    return n;
+}
+
+// A kernel's dynamic shared memory limit on the current device, set once per device
+// (K: a tag of the kernel's own).
+template <class K, class F>
+bool allow_smem(F* kernel, int device, size_t bytes) {
+    static std::atomic<bool> done[kMaxHeadDevices];
+    if (done[device].load(std::memory_order_relaxed)) return true;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
+    done[device].store(true, std::memory_order_relaxed);
+    return true;
 }
 
 }  // namespace ttemb

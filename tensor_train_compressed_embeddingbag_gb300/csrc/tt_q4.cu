@@ -292,17 +292,11 @@ tt_status q4_shape(int64_t V, int32_t D, int32_t G, int32_t dtype, Q4Shape* s) {
     return TT_OK;
 }
 
-int q4_sms() {
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-        cudaGetLastError();
-        return 0;
-    }
-    return n;
-}
+template <class T, int G, int NT>
+struct Q4Tag {};
 
 template <class T, int G, int NT>
-tt_status q4_launch(Q4Args a, int sms, cudaStream_t st) {
+tt_status q4_launch(Q4Args a, int sms, int dev, cudaStream_t st) {
     const int ng = a.g1 - a.g0;
     const size_t smem = (size_t)ng * (G / 32) * Q4Type<T>::pieces * NT * 512;
     const int64_t ntiles = (a.V + kQ4Rows - 1) / kQ4Rows;
@@ -312,13 +306,13 @@ tt_status q4_launch(Q4Args a, int sms, cudaStream_t st) {
     while (a.ksplit < kQ4Warps && ntiles * a.ksplit < 4ll * sms * 2 * kQ4Warps && ng >= 4 * a.ksplit) a.ksplit *= 2;
     const int64_t per = kQ4Warps / a.ksplit, rounds = (ntiles + per - 1) / per;
     auto k = k_q4_matvec<T, G, NT>;
-    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kQ4SmemBytes) != cudaSuccess) return TT_ERR_CUDA;
+    if (!allow_smem<Q4Tag<T, G, NT>>(k, dev, kQ4SmemBytes)) return TT_ERR_CUDA;
     k<<<(unsigned)(rounds < 2 * sms ? rounds : 2 * sms), kQ4Threads, smem, st>>>(a);
     return cudaGetLastError() == cudaSuccess ? TT_OK : TT_ERR_CUDA;
 }
 
 template <class T, int G>
-tt_status q4_rows(Q4Args a, int M, int sms, cudaStream_t st) {
+tt_status q4_rows(Q4Args a, int M, int sms, int dev, cudaStream_t st) {
     const int groups = a.groups;
     for (int m0 = 0; m0 < M; m0 += 32) {
         a.m0 = m0;
@@ -331,7 +325,7 @@ tt_status q4_rows(Q4Args a, int M, int sms, cudaStream_t st) {
             a.g0 = (int)((int64_t)groups * i / launches);
             a.g1 = (int)((int64_t)groups * (i + 1) / launches);
             a.accumulate = i > 0;
-            const tt_status s = nt == 1 ? q4_launch<T, G, 1>(a, sms, st) : (nt == 2 ? q4_launch<T, G, 2>(a, sms, st) : q4_launch<T, G, 4>(a, sms, st));
+            const tt_status s = nt == 1 ? q4_launch<T, G, 1>(a, sms, dev, st) : (nt == 2 ? q4_launch<T, G, 2>(a, sms, dev, st) : q4_launch<T, G, 4>(a, sms, dev, st));
             if (s != TT_OK) return s;
         }
     }
@@ -339,10 +333,10 @@ tt_status q4_rows(Q4Args a, int M, int sms, cudaStream_t st) {
 }
 
 template <class T>
-tt_status q4_type(const Q4Args& a, int M, int G, int sms, cudaStream_t st) {
-    if (G == 32) return q4_rows<T, 32>(a, M, sms, st);
-    if (G == 64) return q4_rows<T, 64>(a, M, sms, st);
-    return q4_rows<T, 128>(a, M, sms, st);
+tt_status q4_type(const Q4Args& a, int M, int G, int sms, int dev, cudaStream_t st) {
+    if (G == 32) return q4_rows<T, 32>(a, M, sms, dev, st);
+    if (G == 64) return q4_rows<T, 64>(a, M, sms, dev, st);
+    return q4_rows<T, 128>(a, M, sms, dev, st);
 }
 
 }  // namespace
@@ -360,7 +354,8 @@ tt_status tt_emb_q4_quantize(const void* weight_dev, int64_t weight_stride, int6
     if (weight_stride < dim) return TT_ERR_SHAPE;
     if (!weight_dev || !packed_dev || !scales_dev || (uintptr_t)packed_dev % 16 || (uintptr_t)scales_dev % 2) return TT_ERR_ARG;
     if ((uintptr_t)weight_dev % (dtype == TT_F32 ? 4 : 2)) return TT_ERR_ARG;
-    const int sms = q4_sms();
+    int dev = 0;
+    const int sms = head_sms(&dev);
     if (sms <= 0) return TT_ERR_CUDA;
     const int64_t total = vocab * s.groups * (group / 8);
     int64_t blocks = (total + 255) / 256;
@@ -389,7 +384,8 @@ tt_status tt_emb_q4_matvec(const void* x_dev, int64_t x_stride, int32_t rows, in
     if (!x_dev || !packed_dev || !scales_dev || !out_dev || (uintptr_t)packed_dev % 16 || (uintptr_t)scales_dev % 2 || (uintptr_t)out_dev % 4)
         return TT_ERR_ARG;
     if ((uintptr_t)x_dev % (dtype == TT_F32 ? 4 : 2)) return TT_ERR_ARG;
-    const int sms = q4_sms();
+    int dev = 0;
+    const int sms = head_sms(&dev);
     if (sms <= 0) return TT_ERR_CUDA;
     Q4Args a{};
     a.x = x_dev;
@@ -402,9 +398,9 @@ tt_status tt_emb_q4_matvec(const void* x_dev, int64_t x_stride, int32_t rows, in
     a.V = vocab;
     a.out = out_dev;
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-    if (dtype == TT_F32) return q4_type<float>(a, rows, group, sms, cs);
-    if (dtype == TT_BF16) return q4_type<__nv_bfloat16>(a, rows, group, sms, cs);
-    return q4_type<__half>(a, rows, group, sms, cs);
+    if (dtype == TT_F32) return q4_type<float>(a, rows, group, sms, dev, cs);
+    if (dtype == TT_BF16) return q4_type<__nv_bfloat16>(a, rows, group, sms, dev, cs);
+    return q4_type<__half>(a, rows, group, sms, dev, cs);
 }
 
 }  // extern "C"

@@ -23,7 +23,7 @@ from typing import Optional, Tuple
 
 import torch
 
-from . import TT_ERR_ARG, TT_ERR_SHAPE, TTError, _check, _ptr, _stream, load_library
+from . import TT_ERR_ARG, TT_ERR_SHAPE, TTError, _check, _stream, load_library
 
 __all__ = [
     "tt_emb_head_workspace",
@@ -60,51 +60,68 @@ def _refuse(code: int, what: str):
     raise TTError(code, what)
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_calls = {}  # name -> bound C function (looked up once: the calls below are short)
+
+
+def _c(name: str):
+    fn = _calls.get(name)
+    if fn is None:
+        fn = _calls[name] = getattr(load_library(), name)
+    return fn
+
+
+def _stream_now(device_index: int):
+    """The device's current stream as an address."""
+    return _raw_stream(device_index) if _raw_stream is not None else _stream(None)
+
+
 def _matrix(t: torch.Tensor, what: str) -> torch.Tensor:
     """A 2-D CUDA tensor of a supported type whose rows are contiguous (a copy where they are not)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in _DTYPES:
         _refuse(TT_ERR_ARG, f"{what} must be a float32, bfloat16 or float16 CUDA tensor")
     if t.dim() != 2 or t.shape[1] < 1:
         _refuse(TT_ERR_SHAPE, f"{what} must be [rows, dim] with dim >= 1")
+    if t.is_contiguous():
+        return t
     if t.shape[0] > 1 and t.stride(0) < t.shape[1] or t.shape[1] > 1 and t.stride(1) != 1:
-        t = t.contiguous()
+        return t.contiguous()
     return t
 
 
 def _row_stride(t: torch.Tensor) -> int:
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    rows, dim = t.shape
+    return t.stride(0) if rows > 1 else dim
 
 
 def _head(hidden: torch.Tensor, weight: torch.Tensor):
     h, w = _matrix(hidden, "hidden"), _matrix(weight, "weight")
     if h.dtype != w.dtype or h.device != w.device:
         _refuse(TT_ERR_ARG, "hidden and weight must have one type and one device")
-    if h.shape[1] != w.shape[1] or w.shape[0] < 1:
+    (rows, dim), (vocab, wdim) = h.shape, w.shape
+    if dim != wdim or vocab < 1:
         _refuse(TT_ERR_SHAPE, "hidden is [rows, dim] and weight [vocab, dim]")
-    d = _Head(h.data_ptr(), w.data_ptr(), h.shape[0], w.shape[0], _row_stride(h), _row_stride(w), h.shape[1], _DTYPES[h.dtype])
-    return h, w, d
+    return h, w, _Head(h.data_ptr(), w.data_ptr(), rows, vocab, _row_stride(h), _row_stride(w), dim, _DTYPES[h.dtype])
 
 
 def _vector(t: torch.Tensor, dtype, shape, device, what: str) -> torch.Tensor:
-    if not isinstance(t, torch.Tensor) or t.device != device or t.dtype != dtype:
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != device:
         _refuse(TT_ERR_ARG, f"{what} must be a {dtype} tensor on {device}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         _refuse(TT_ERR_SHAPE, f"{what} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    return t.contiguous()
+    return t if t.is_contiguous() else t.contiguous()
 
 
 def _err_word(err: Optional[torch.Tensor], device):
-    if err is not None and not (err.device == device and err.dtype == torch.int32 and err.numel() >= 1):
+    if err is None:
+        return None
+    if not (isinstance(err, torch.Tensor) and err.device == device and err.dtype == torch.int32 and err.numel() >= 1):
         _refuse(TT_ERR_ARG, "err must be an int32 tensor on the inputs' device")
-    return _ptr(err)
+    return err.data_ptr()
 
 
 @contextlib.contextmanager
-def _on(stream, device):
-    """The call's stream and device are current, so that what it allocates belongs to that stream."""
-    if stream is None and device.index == torch.cuda.current_device():
-        yield
-        return
+def _current(stream, device):
     with torch.cuda.device(device):
         if stream is None:
             yield
@@ -112,6 +129,14 @@ def _on(stream, device):
             s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=device)
             with torch.cuda.stream(s):
                 yield
+
+
+_here = contextlib.nullcontext()
+
+
+def _on(stream, device):
+    """The call's stream and device are current, so that what it allocates belongs to that stream."""
+    return _here if stream is None and device.index == torch.cuda.current_device() else _current(stream, device)
 
 
 def tt_emb_head_workspace(hidden: torch.Tensor, weight: torch.Tensor, teacher_k: int = 1, backward: bool = False) -> int:
@@ -122,38 +147,51 @@ def tt_emb_head_workspace(hidden: torch.Tensor, weight: torch.Tensor, teacher_k:
 
 
 def _workspace_bytes(d: _Head, k: int, backward: bool) -> int:
-    n = int(load_library().tt_emb_head_workspace(ctypes.byref(d), int(k), 1 if backward else 0))
+    n = _c("tt_emb_head_workspace")(ctypes.byref(d), k, backward)
     if n < 0:
         _refuse(TT_ERR_SHAPE, "tt_emb_head_workspace: sizes outside the limits")
     return n
 
 
-def _workspace(d: _Head, k: int, backward: bool, device) -> torch.Tensor:
-    return torch.empty(max(_workspace_bytes(d, k, backward), 256), dtype=torch.uint8, device=device)
-
-
-def _forward(name, hidden, weight, k, args, err, stream, keep):
+def _forward(name, hidden, weight, target, err, stream):
     h, w, d = _head(hidden, weight)
-    with _on(stream, h.device):
-        out = torch.empty((2, h.shape[0]), dtype=torch.float32, device=h.device)
-        ws = _workspace(d, k, False, h.device)
-        n = h.shape[0] * 4
-        _check(getattr(load_library(), name)(ctypes.byref(d), *args, out.data_ptr(), out.data_ptr() + n, _err_word(err, h.device),
-                                             ws.data_ptr(), ws.numel(), _stream(None)), name)
-    return out[0], out[1]
+    device, rows = h.device, d.rows
+    with _on(stream, device):
+        k, args, keep = target(rows, device)
+        n = _workspace_bytes(d, k, False)
+        loss = torch.empty(rows, dtype=torch.float32, device=device)
+        lse = torch.empty(rows, dtype=torch.float32, device=device)
+        ws = torch.empty(n, dtype=torch.uint8, device=device)
+        st = _c(name)(ctypes.byref(d), *args, loss.data_ptr(), lse.data_ptr(), _err_word(err, device), ws.data_ptr(), n,
+                      _stream_now(device.index))
+        if st:
+            _check(st, name)
+    return loss, lse
 
 
-def _backward(name, hidden, weight, k, args, lse, grad_loss, err, stream, keep):
+def _backward(name, hidden, weight, target, lse, grad_loss, err, stream):
     h, w, d = _head(hidden, weight)
-    with _on(stream, h.device):
-        lse = _vector(lse, torch.float32, (h.shape[0],), h.device, "lse")
-        grad_loss = _vector(grad_loss, torch.float32, (h.shape[0],), h.device, "grad_loss")
-        gh = torch.empty(h.shape, dtype=h.dtype, device=h.device)
-        gw = torch.empty(w.shape, dtype=w.dtype, device=w.device)
-        ws = _workspace(d, k, True, h.device)
-        _check(getattr(load_library(), name)(ctypes.byref(d), *args, lse.data_ptr(), grad_loss.data_ptr(), gh.data_ptr(), gw.data_ptr(),
-                                             _err_word(err, h.device), ws.data_ptr(), ws.numel(), _stream(None)), name)
+    device, rows = h.device, d.rows
+    with _on(stream, device):
+        k, args, keep = target(rows, device)
+        lse = _vector(lse, torch.float32, (rows,), device, "lse")
+        grad_loss = _vector(grad_loss, torch.float32, (rows,), device, "grad_loss")
+        n = _workspace_bytes(d, k, True)
+        gh = torch.empty(h.shape, dtype=h.dtype, device=device)
+        gw = torch.empty(w.shape, dtype=h.dtype, device=device)
+        ws = torch.empty(n, dtype=torch.uint8, device=device)
+        st = _c(name)(ctypes.byref(d), *args, lse.data_ptr(), grad_loss.data_ptr(), gh.data_ptr(), gw.data_ptr(), _err_word(err, device),
+                      ws.data_ptr(), n, _stream_now(device.index))
+        if st:
+            _check(st, name)
     return gh, gw
+
+
+def _ids(targets, ignore_index):
+    def target(rows, device):
+        t = _vector(targets, torch.int64, (rows,), device, "targets")
+        return 1, (t.data_ptr(), ignore_index), t
+    return target
 
 
 def tt_emb_xent_forward(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor, ignore_index: int = -100,
@@ -163,25 +201,27 @@ def tt_emb_xent_forward(hidden: torch.Tensor, weight: torch.Tensor, targets: tor
     hidden [rows, dim] and weight [vocab, dim] of one type (float32, bfloat16,
     float16), targets int64 [rows].  A row whose target is ignore_index has loss 0.  A
     target outside the table sets bit 1 of err (int32, optional) and counts as ignored."""
-    t = _vector(targets, torch.int64, (hidden.shape[0],), hidden.device, "targets")
-    return _forward("tt_emb_xent_forward", hidden, weight, 1, (t.data_ptr(), int(ignore_index)), err, stream, t)
+    return _forward("tt_emb_xent_forward", hidden, weight, _ids(targets, ignore_index), err, stream)
 
 
 def tt_emb_xent_backward(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor, lse: torch.Tensor, grad_loss: torch.Tensor,
                          ignore_index: int = -100, err: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """(grad_hidden, grad_weight) for lse of the forward call and the gradient of every row's loss."""
-    t = _vector(targets, torch.int64, (hidden.shape[0],), hidden.device, "targets")
-    return _backward("tt_emb_xent_backward", hidden, weight, 1, (t.data_ptr(), int(ignore_index)), lse, grad_loss, err, stream, t)
+    return _backward("tt_emb_xent_backward", hidden, weight, _ids(targets, ignore_index), lse, grad_loss, err, stream)
 
 
-def _teacher(hidden, teacher_ids, teacher_logits):
-    if not isinstance(teacher_ids, torch.Tensor) or teacher_ids.dim() != 2 or teacher_ids.shape[1] < 1:
-        _refuse(TT_ERR_SHAPE, "teacher_ids must be [rows, k] with k >= 1")
-    shape = (hidden.shape[0], teacher_ids.shape[1])
-    ids = _vector(teacher_ids, torch.int64, shape, hidden.device, "teacher_ids")
-    if isinstance(teacher_logits, torch.Tensor) and teacher_logits.dtype in (torch.bfloat16, torch.float16):
-        teacher_logits = teacher_logits.float()
-    return ids, _vector(teacher_logits, torch.float32, shape, hidden.device, "teacher_logits")
+def _teacher(teacher_ids, teacher_logits, temperature):
+    def target(rows, device):
+        if not isinstance(teacher_ids, torch.Tensor) or teacher_ids.dim() != 2 or teacher_ids.shape[1] < 1:
+            _refuse(TT_ERR_SHAPE, "teacher_ids must be [rows, k] with k >= 1")
+        k = teacher_ids.shape[1]
+        ids = _vector(teacher_ids, torch.int64, (rows, k), device, "teacher_ids")
+        logits = teacher_logits
+        if isinstance(logits, torch.Tensor) and logits.dtype in (torch.bfloat16, torch.float16):
+            logits = logits.float()
+        logits = _vector(logits, torch.float32, (rows, k), device, "teacher_logits")
+        return k, (ids.data_ptr(), logits.data_ptr(), k, temperature), (ids, logits)
+    return target
 
 
 def tt_emb_distill_forward(hidden: torch.Tensor, weight: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits: torch.Tensor,
@@ -189,22 +229,15 @@ def tt_emb_distill_forward(hidden: torch.Tensor, weight: torch.Tensor, teacher_i
     """(loss, lse), float32 [rows]: T^2 KL(teacher's renormalised top entries || student) and log sum_v exp(z / T).
 
     teacher_ids int64 [rows, k] (negative: no entry), teacher_logits [rows, k]."""
-    with _on(stream, hidden.device):
-        ids, logits = _teacher(hidden, teacher_ids, teacher_logits)
-    k = ids.shape[1]
-    return _forward("tt_emb_distill_forward", hidden, weight, k, (ids.data_ptr(), logits.data_ptr(), k, float(temperature)), err, stream,
-                    (ids, logits))
+    return _forward("tt_emb_distill_forward", hidden, weight, _teacher(teacher_ids, teacher_logits, temperature), err, stream)
 
 
 def tt_emb_distill_backward(hidden: torch.Tensor, weight: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits: torch.Tensor,
                             lse: torch.Tensor, grad_loss: torch.Tensor, temperature: float = 1.0, err: Optional[torch.Tensor] = None,
                             stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """(grad_hidden, grad_weight); the teacher gets no gradient."""
-    with _on(stream, hidden.device):
-        ids, logits = _teacher(hidden, teacher_ids, teacher_logits)
-    k = ids.shape[1]
-    return _backward("tt_emb_distill_backward", hidden, weight, k, (ids.data_ptr(), logits.data_ptr(), k, float(temperature)), lse,
-                     grad_loss, err, stream, (ids, logits))
+    return _backward("tt_emb_distill_backward", hidden, weight, _teacher(teacher_ids, teacher_logits, temperature), lse, grad_loss, err,
+                     stream)
 
 
 def tt_emb_head_set_wait_limit(ns: int):
@@ -224,8 +257,8 @@ def tt_emb_q4_quantize(weight: torch.Tensor, group: int = 64, stream=None) -> Tu
     with _on(stream, w.device):
         packed = torch.empty((V, (D + 31) // 32 * 16), dtype=torch.uint8, device=w.device)
         scales = torch.empty((V, (D + group - 1) // group), dtype=torch.bfloat16, device=w.device)
-        _check(load_library().tt_emb_q4_quantize(w.data_ptr(), _row_stride(w), V, D, _DTYPES[w.dtype], group, packed.data_ptr(),
-                                                 scales.data_ptr(), _stream(None)), "tt_emb_q4_quantize")
+        _check(_c("tt_emb_q4_quantize")(w.data_ptr(), _row_stride(w), V, D, _DTYPES[w.dtype], group, packed.data_ptr(), scales.data_ptr(),
+                                        _stream_now(w.device.index)), "tt_emb_q4_quantize")
     return packed, scales
 
 
@@ -233,22 +266,23 @@ def tt_emb_q4_matvec(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor
                      stream=None) -> torch.Tensor:
     """Scores float32 [rows, vocab] of the rows of x [rows, dim] (float32, bfloat16, float16) against a 4-bit table."""
     x = _matrix(x, "x")
-    M, D, group = x.shape[0], x.shape[1], int(group)
+    (M, D), device = x.shape, x.device
     if group not in (32, 64, 128):
         _refuse(TT_ERR_SHAPE, "group must be 32, 64 or 128")
-    for t, name, dtype, width in ((packed, "packed", torch.uint8, (D + 31) // 32 * 16), (scales, "scales", torch.bfloat16, (D + group - 1) // group)):
-        if not isinstance(t, torch.Tensor) or t.device != x.device or t.dtype != dtype or not t.is_contiguous():
-            _refuse(TT_ERR_ARG, f"{name} must be a contiguous {dtype} tensor on x's device")
-        if t.dim() != 2 or t.shape[1] != width or t.shape[0] != packed.shape[0] or t.shape[0] < 1:
-            _refuse(TT_ERR_SHAPE, f"{name} has shape {tuple(t.shape)}, expected [vocab, {width}]")
-    V = packed.shape[0]
-    with _on(stream, x.device):
+    V = packed.shape[0] if isinstance(packed, torch.Tensor) and packed.dim() == 2 else 0
+    if V < 1:
+        _refuse(TT_ERR_SHAPE, "packed must be [vocab, bytes] with vocab >= 1")
+    packed = _vector(packed, torch.uint8, (V, (D + 31) // 32 * 16), device, "packed")
+    scales = _vector(scales, torch.bfloat16, (V, (D + group - 1) // group), device, "scales")
+    with _on(stream, device):
         if out is None:
-            out = torch.empty((M, V), dtype=torch.float32, device=x.device)
-        elif out.shape != (M, V) or out.dtype != torch.float32 or out.device != x.device or not out.is_contiguous():
+            out = torch.empty((M, V), dtype=torch.float32, device=device)
+        elif out.shape != (M, V) or out.dtype != torch.float32 or out.device != device or not out.is_contiguous():
             _refuse(TT_ERR_ARG, "out must be a contiguous float32 [rows, vocab] tensor on x's device")
-        _check(load_library().tt_emb_q4_matvec(x.data_ptr(), _row_stride(x), M, _DTYPES[x.dtype], packed.data_ptr(), scales.data_ptr(),
-                                               V, D, group, out.data_ptr(), _stream(None)), "tt_emb_q4_matvec")
+        st = _c("tt_emb_q4_matvec")(x.data_ptr(), _row_stride(x), M, _DTYPES[x.dtype], packed.data_ptr(), scales.data_ptr(), V, D, group,
+                                    out.data_ptr(), _stream_now(device.index))
+        if st:
+            _check(st, "tt_emb_q4_matvec")
     return out
 
 
