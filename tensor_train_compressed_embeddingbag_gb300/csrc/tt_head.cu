@@ -121,6 +121,7 @@ __device__ __forceinline__ float join_parts(const float2* p, int n, int lane) {
 }
 
 constexpr int kRowThreads = 128;
+constexpr int kAmaxShares = 64;  // blocks that look for the largest magnitudes
 
 // The teacher's distribution of one row, a block per row: q[k] and log q[k] in
 // shared memory, ids as int (-1: not counted).  An id below 0 marks an entry that
@@ -228,7 +229,7 @@ __global__ void __launch_bounds__(kRowThreads) k_head_finish(HeadIn in, Target t
 // (ids_out, dzt; k_head_fix) or, ents given, to their 32 x 32 blocks (k_head_fused).
 template <class T, bool DISTILL>
 __global__ void __launch_bounds__(kRowThreads)
-    k_head_rows(HeadIn in, Target t, const float* lse, const float* grad, const uint32_t* amax, float* nlse, float* scale, int* ids_out,
+    k_head_rows(HeadIn in, Target t, const float* lse, const float* grad, const uint32_t* shares, uint32_t* amax, float* nlse, float* scale, int* ids_out,
                 float* dzt, TargetBlock* blocks, int nblocks, TargetEntry* ents, uint16_t* hp, int* err) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t n = blockIdx.x;
@@ -247,7 +248,21 @@ __global__ void __launch_bounds__(kRowThreads)
         xid = xent_id(t, n, in.V, threadIdx.x == 0 ? err : nullptr);
         any = xid >= 0;
     }
-    const int ez = amax ? scale_exp(amax[2]) : 0, eh = amax ? scale_exp(amax[0]) : 0;
+    int ez = 0, eh = 0;
+    if (amax) {  // the shares of the largest magnitudes joined: dz's by warps 0 and 1, hidden's by 2 and 3
+        __shared__ uint32_t most[4];
+        static_assert(kRowThreads == 2 * kAmaxShares, "a share per thread");
+        const uint32_t m = __reduce_max_sync(0xffffffffu, shares[threadIdx.x]);
+        if (lane == 0) most[warp] = m;
+        __syncthreads();
+        const uint32_t mz = max(most[0], most[1]), mh = max(most[2], most[3]);
+        ez = scale_exp(mz);
+        eh = scale_exp(mh);
+        if (n == 0 && threadIdx.x == 0) {
+            amax[0] = mh;
+            amax[2] = mz;
+        }
+    }
     const float rs = any ? grad[n] * t.T * exp2i(ez) : 0.f;
     if (threadIdx.x == 0) {
         nlse[n] = any ? -l * kLog2e : 0.f;
@@ -312,35 +327,6 @@ __global__ void k_head_fix(const int* ids, const float* dzt, int64_t total, int 
     if (split) dz[piece + at] = (uint16_t)pack16(dzt[i] - unpack_f16(w).x, 0.f, 0);
 }
 
-// Largest finite magnitudes over the rows that count: blockIdx.y = 0: |grad| T ->
-// amax[2]; 1 (fp32): |hidden| -> amax[0].  A largest value is the same in whatever order
-// the atomics arrive.
-__global__ void __launch_bounds__(256) k_head_absmax(HeadIn in, Target t, const float* grad, int distill, uint32_t* amax) {
-    const int lane = threadIdx.x & 31;
-    uint32_t m = 0;
-    auto take = [&](float x) {
-        const uint32_t b = __float_as_uint(x) & 0x7FFFFFFFu;
-        if (b < 0x7F800000u) m = max(m, b);
-    };
-    auto counts = [&](int64_t n) {
-        if (!distill) return t.ids[n] != t.ignore;
-        for (int k = 0; k < t.K; ++k)
-            if (t.ids[n * t.K + k] >= 0) return true;
-        return false;
-    };
-    if (blockIdx.y == 0) {
-        for (int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x; n < in.N; n += (int64_t)gridDim.x * 256)
-            if (counts(n)) take(grad[n] * t.T);
-    } else {
-        const float* x = static_cast<const float*>(in.h);
-        for (int64_t n = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); n < in.N; n += (int64_t)gridDim.x * 8)
-            if (counts(n))
-                for (int i = lane; i < in.D; i += 32) take(x[n * in.ldh + i]);
-    }
-    m = __reduce_max_sync(0xffffffffu, m);
-    if (lane == 0 && m) atomicMax(&amax[blockIdx.y == 0 ? 2 : 0], m);
-}
-
 // 8 elements of a row from column c on; columns past D are 0.
 __device__ __forceinline__ void load8(const HeadIn& in, const float* src, int c, float (&x)[8]) {
     if (in.vec) {
@@ -372,20 +358,41 @@ __device__ __forceinline__ void split8(const float (&x)[8], float sc, uint16_t* 
     *reinterpret_cast<uint4*>(lo_at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
 }
 
-// Packed copies with rows of Dp 16-bit elements: blockIdx.y = 0: the table (fp32: hi and
-// lo pieces, a scale per 128 rows, its exponent in wexp: the rows of a tile of the
-// products, so that a scale is one factor per tile; up to 128 columns a tile is read
-// once and kept in registers); 1: the hidden rows, a warp per row (fp32: a scale of each
-// row's own, its exponent in row_exp).
+// What a pass needs before its products, in one launch.
+//   blockIdx.y = 0  the table packed in rows of Dp 16-bit elements (fp32: hi and lo
+//                   pieces, a scale per 128 rows, its exponent in wexp: the rows of a tile
+//                   of the products, so that a scale is one factor per tile; up to 128
+//                   columns a tile is read once and kept in registers)
+//   blockIdx.y = 1  forward: the hidden rows packed, a warp per row (fp32: a scale of each
+//                   row's own, its exponent in row_exp); backward: the largest finite
+//                   |grad| T and (fp32) |hidden| over the rows that count, a share per block
+//   blockIdx.y = 2  backward, k_head_fused: the blocks of targets cleared
+struct PrepArgs {
+    HeadIn in;
+    uint16_t* wp;       // null: the table is read as it is
+    int* wexp;
+    uint16_t* hp;       // null: not packed
+    int* row_exp;
+    Target t;
+    int distill;
+    const float* grad;
+    uint32_t* shares;   // [2][kAmaxShares], |grad| T then |hidden|; null: no scales
+    uint4* clear;
+    int64_t nclear;
+};
+
 template <class T, int TH, int Q>  // TH threads; Q (fp32): 8-element groups that a thread holds of a tile, 0: none
-__global__ void __launch_bounds__(TH, 1024 / TH) k_head_pack(HeadIn in, uint16_t* wp, int* wexp, uint16_t* hp, int* row_exp) {
+__global__ void __launch_bounds__(TH, 1024 / TH) k_head_prep(const __grid_constant__ PrepArgs a) {
+    const HeadIn& in = a.in;
+    uint16_t* const wp = a.wp;
+    uint16_t* const hp = a.hp;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    __shared__ uint32_t red[2][TH / 32];
     if (blockIdx.y == 0) {
         if (!wp) return;
         const int g = in.Dp / 8;  // 8-element groups of a row
         const int64_t piece = in.V * in.Dp;
         if constexpr (sizeof(T) == 4) {
-            __shared__ uint32_t red[TH / 32];
             const float* w = static_cast<const float*>(in.w);
             const int64_t tiles = (in.V + 127) / 128;
             for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
@@ -411,14 +418,14 @@ __global__ void __launch_bounds__(TH, 1024 / TH) k_head_pack(HeadIn in, uint16_t
                     }
                 }
                 m = __reduce_max_sync(0xffffffffu, m);
-                if (lane == 0) red[warp] = m;
+                if (lane == 0) red[0][warp] = m;
                 __syncthreads();
 #pragma unroll
-                for (int q = 0; q < TH / 32; ++q) m = max(m, red[q]);
+                for (int q = 0; q < TH / 32; ++q) m = max(m, red[0][q]);
                 __syncthreads();
                 const int e = scale_exp(m);
                 const float sc = exp2i(e);
-                if (threadIdx.x == 0) wexp[tile] = e;
+                if (threadIdx.x == 0) a.wexp[tile] = e;
                 uint16_t* to = wp + v0 * in.Dp;
                 if (Q) {
 #pragma unroll
@@ -447,8 +454,7 @@ __global__ void __launch_bounds__(TH, 1024 / TH) k_head_pack(HeadIn in, uint16_t
                 *reinterpret_cast<uint4*>(wp + i * 8) = *reinterpret_cast<uint4*>(x);
             }
         }
-    } else {
-        if (!hp) return;
+    } else if (blockIdx.y == 1 && hp) {
         const int64_t piece = in.N * in.Dp;
         for (int64_t n = (int64_t)blockIdx.x * (TH / 32) + warp; n < in.N; n += (int64_t)gridDim.x * (TH / 32)) {
             const T* h = static_cast<const T*>(in.h) + n * in.ldh;
@@ -459,7 +465,7 @@ __global__ void __launch_bounds__(TH, 1024 / TH) k_head_pack(HeadIn in, uint16_t
                     if (b < 0x7F800000u) m = max(m, b);
                 }
                 const int e = scale_exp(__reduce_max_sync(0xffffffffu, m));
-                if (lane == 0) row_exp[n] = e;
+                if (lane == 0) a.row_exp[n] = e;
                 for (int i = lane; i < in.Dp; i += 32) {
                     const float x = i < in.D ? to_f32(h[i]) * exp2i(e) : 0.f;
                     const __half hi = __float2half_rn(x);
@@ -471,6 +477,44 @@ __global__ void __launch_bounds__(TH, 1024 / TH) k_head_pack(HeadIn in, uint16_t
                 for (int i = lane; i < in.Dp; i += 32) hp[n * in.Dp + i] = i < in.D ? s[i] : (uint16_t)0;
             }
         }
+    } else if (blockIdx.y == 1) {
+        if (!a.shares || blockIdx.x >= kAmaxShares) return;
+        const int share = blockIdx.x, shares = min((int)gridDim.x, kAmaxShares);
+        auto counts = [&](int64_t n) {
+            if (!a.distill) return a.t.ids[n] != a.t.ignore;
+            for (int k = 0; k < a.t.K; ++k)
+                if (a.t.ids[n * a.t.K + k] >= 0) return true;
+            return false;
+        };
+        uint32_t mz = 0, mh = 0;
+        auto take = [](uint32_t& m, float x) {
+            const uint32_t b = __float_as_uint(x) & 0x7FFFFFFFu;
+            if (b < 0x7F800000u) m = max(m, b);
+        };
+        for (int64_t n = (int64_t)share * TH + threadIdx.x; n < in.N; n += (int64_t)shares * TH)
+            if (counts(n)) take(mz, a.grad[n] * a.t.T);
+        if (sizeof(T) == 4)
+            for (int64_t n = (int64_t)share * (TH / 32) + warp; n < in.N; n += (int64_t)shares * (TH / 32))
+                if (counts(n)) {
+                    const float* h = static_cast<const float*>(in.h) + n * in.ldh;
+                    for (int i = lane; i < in.D; i += 32) take(mh, h[i]);
+                }
+        mz = __reduce_max_sync(0xffffffffu, mz);
+        mh = __reduce_max_sync(0xffffffffu, mh);
+        if (lane == 0) {
+            red[0][warp] = mz;
+            red[1][warp] = mh;
+        }
+        __syncthreads();
+        if (threadIdx.x < 2) {
+            uint32_t m = 0;
+            for (int q = 0; q < TH / 32; ++q) m = max(m, red[threadIdx.x][q]);
+            a.shares[threadIdx.x * kAmaxShares + share] = m;
+        }
+        if (share == 0)  // shares that no block has
+            for (int i = shares + threadIdx.x; i < kAmaxShares; i += TH) a.shares[i] = a.shares[kAmaxShares + i] = 0;
+    } else {
+        for (int64_t i = (int64_t)blockIdx.x * TH + threadIdx.x; i < a.nclear; i += (int64_t)gridDim.x * TH) a.clear[i] = make_uint4(0, 0, 0, 0);
     }
 }
 
@@ -757,7 +801,7 @@ size_t fwd_ws(const Plan& p, void* base, FwdWs* w) {
 }
 
 struct BwdWs {
-    uint32_t* amax;
+    uint32_t *amax, *shares;
     float *nlse, *scale, *joins, *dzt, *dh_part, *dw_part;
     int *ids, *wexp;
     TargetBlock* blocks;
@@ -768,6 +812,7 @@ size_t bwd_ws(const Plan& p, int K, void* base, BwdWs* w) {
     Arena a(base);
     const int64_t pc = p.split ? 2 : 1, nk = p.in.N * K;
     w->amax = a.get<uint32_t>(4);
+    w->shares = a.get<uint32_t>(2 * kAmaxShares);
     w->wexp = a.get<int>(p.split ? cdiv(p.in.V, 128) : 0);
     w->nlse = a.get<float>(cdiv(p.in.N, 128) * 128);
     w->scale = a.get<float>(cdiv(p.in.N, 128) * 128);
@@ -792,15 +837,17 @@ unsigned grid_of(int64_t items, int per_block, int sms, int per_sm) {
 bool launch_ok() { return cudaGetLastError() == cudaSuccess; }
 
 template <class T>
-bool launch_pack(const Plan& p, int64_t hidden_rows, uint16_t* wp, int* wexp, uint16_t* hp, int* row_exp, cudaStream_t st) {
-    const int64_t w = !wp ? 0 : (p.split ? cdiv(p.in.V, 128) : cdiv(p.in.V * (p.in.Dp / 8), 256)), h = cdiv(hidden_rows, 8);
-    const dim3 grid(grid_of(w > h ? w : h, 1, p.sms, 16), hp ? 2 : 1);
+bool launch_prep(const Plan& p, const PrepArgs& a, cudaStream_t st) {
+    const int64_t w = !a.wp ? 0 : (p.split ? cdiv(p.in.V, 128) : cdiv(p.in.V * (p.in.Dp / 8), 256));
+    const int64_t h = a.hp ? cdiv(p.in.N, 8) : (a.shares ? cdiv(p.in.N, 32) : 0), c = cdiv(a.nclear, 1024);
+    const int64_t most = w > h ? (w > c ? w : c) : (h > c ? h : c);
+    const dim3 grid(grid_of(most, 1, p.sms, 16), a.nclear ? 3 : (h ? 2 : 1));
     if (p.split && p.in.Dp <= 64)
-        k_head_pack<T, 256, 4><<<grid, 256, 0, st>>>(p.in, wp, wexp, hp, row_exp);
+        k_head_prep<T, 256, 4><<<grid, 256, 0, st>>>(a);
     else if (p.split && p.in.Dp <= 128)
-        k_head_pack<T, 512, 4><<<grid, 512, 0, st>>>(p.in, wp, wexp, hp, row_exp);
+        k_head_prep<T, 512, 4><<<grid, 512, 0, st>>>(a);
     else
-        k_head_pack<T, 256, 0><<<grid, 256, 0, st>>>(p.in, wp, wexp, hp, row_exp);
+        k_head_prep<T, 256, 0><<<grid, 256, 0, st>>>(a);
     return launch_ok();
 }
 
@@ -821,7 +868,13 @@ tt_status head_forward(const Plan& p, const Target& t, float* loss, float* lse, 
     if (in.N == 0) return TT_OK;
     const bool distill = t.logits != nullptr;
     if (p.pack_h || p.pack_w) {
-        if (!launch_pack<T>(p, in.N, p.pack_w ? w.wp : nullptr, w.wexp, p.pack_h ? w.hp : nullptr, w.row_exp, st)) return TT_ERR_CUDA;
+        PrepArgs a{};
+        a.in = in;
+        a.wp = p.pack_w ? w.wp : nullptr;
+        a.wexp = w.wexp;
+        a.hp = p.pack_h ? w.hp : nullptr;
+        a.row_exp = w.row_exp;
+        if (!launch_prep<T>(p, a, st)) return TT_ERR_CUDA;
     }
     const Operand H{p.pack_h ? w.hp : static_cast<const uint16_t*>(in.h), in.N, in.D, p.pack_h ? in.Dp : in.ldh, in.N * in.Dp};
     const Operand W{p.pack_w ? w.wp : static_cast<const uint16_t*>(in.w), in.V, in.D, p.pack_w ? in.Dp : in.ldw, in.V * in.Dp};
@@ -867,23 +920,26 @@ tt_status head_backward(const Plan& p, const Target& t, const float* lse, const 
     if (bwd_ws(p, t.K, ws, &w) > ws_bytes) return TT_ERR_ARG;
     if (in.N == 0) return cudaMemsetAsync(dw, 0, (size_t)in.V * in.D * p.esize, st) == cudaSuccess ? TT_OK : TT_ERR_CUDA;
     const bool distill = t.logits != nullptr;
-    const uint32_t* amax = p.fmt ? nullptr : w.amax;  // bf16 has fp32's range: dz needs no scale
-    if (amax) {
-        if (cudaMemsetAsync(w.amax, 0, 16, st) != cudaSuccess) return TT_ERR_CUDA;
-        // f16 inputs are taken as they are: only dz is scaled
-        k_head_absmax<<<dim3(grid_of(in.N, p.split ? 16 : 256, p.sms, 4), p.split ? 2 : 1), 256, 0, st>>>(in, t, grad, distill, w.amax);
-        if (!launch_ok()) return TT_ERR_CUDA;
-    }
-    if (p.pack_w) {
-        if (!launch_pack<T>(p, 0, w.wp, w.wexp, nullptr, nullptr, st)) return TT_ERR_CUDA;
-    }
+    uint32_t* amax = p.fmt ? nullptr : w.amax;  // bf16 has fp32's range: dz needs no scale
     TargetEntry* ents = p.fused ? w.ents : nullptr;
-    if (ents && cudaMemsetAsync(w.blocks, 0, (size_t)(p.nblocks * p.vblocks) * sizeof(TargetBlock), st) != cudaSuccess) return TT_ERR_CUDA;
+    if (amax || p.pack_w || ents) {
+        PrepArgs a{};
+        a.in = in;
+        a.wp = p.pack_w ? w.wp : nullptr;
+        a.wexp = w.wexp;
+        a.t = t;
+        a.distill = distill;
+        a.grad = grad;
+        a.shares = amax ? w.shares : nullptr;
+        a.clear = reinterpret_cast<uint4*>(w.blocks);
+        a.nclear = ents ? p.nblocks * p.vblocks : 0;
+        if (!launch_prep<T>(p, a, st)) return TT_ERR_CUDA;
+    }
     if (distill)
-        k_head_rows<T, true><<<(unsigned)in.N, kRowThreads, (size_t)t.K * 12, st>>>(in, t, lse, grad, amax, w.nlse, w.scale, w.ids, w.dzt, w.blocks,
+        k_head_rows<T, true><<<(unsigned)in.N, kRowThreads, (size_t)t.K * 12, st>>>(in, t, lse, grad, w.shares, amax, w.nlse, w.scale, w.ids, w.dzt, w.blocks,
                                                                                   (int)p.nblocks, ents, w.hp, err);
     else
-        k_head_rows<T, false><<<(unsigned)in.N, kRowThreads, 12, st>>>(in, t, lse, grad, amax, w.nlse, w.scale, w.ids, w.dzt, w.blocks, (int)p.nblocks,
+        k_head_rows<T, false><<<(unsigned)in.N, kRowThreads, 12, st>>>(in, t, lse, grad, w.shares, amax, w.nlse, w.scale, w.ids, w.dzt, w.blocks, (int)p.nblocks,
                                                                      ents, w.hp, err);
     if (!launch_ok()) return TT_ERR_CUDA;
     const uint32_t *ah = amax, *az = amax ? amax + 2 : nullptr;
