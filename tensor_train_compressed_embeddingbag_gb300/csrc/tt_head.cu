@@ -481,9 +481,9 @@ __global__ void __launch_bounds__(TH, 1024 / TH) k_head_prep(const __grid_consta
         if (!a.shares || blockIdx.x >= kAmaxShares) return;
         const int share = blockIdx.x, shares = min((int)gridDim.x, kAmaxShares);
         auto counts = [&](int64_t n) {
-            if (!a.distill) return a.t.ids[n] != a.t.ignore;
-            for (int k = 0; k < a.t.K; ++k)
-                if (a.t.ids[n * a.t.K + k] >= 0) return true;
+            if (!a.distill) return a.t.ids[n] != a.t.ignore && (uint64_t)a.t.ids[n] < (uint64_t)in.V;
+            for (int64_t k = n * a.t.K; k < (n + 1) * a.t.K; ++k)
+                if ((uint64_t)a.t.ids[k] < (uint64_t)in.V && a.t.logits[k] != -INFINITY) return true;
             return false;
         };
         uint32_t mz = 0, mh = 0;

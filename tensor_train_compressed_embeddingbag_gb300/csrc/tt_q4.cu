@@ -5,18 +5,25 @@
 // Codes are 4-bit, two to a byte (the even column in the low half), rows padded to a
 // multiple of 32 columns; one bf16 scale per group of 32, 64 or 128 columns.
 //
-// A call reads half a byte per weight and multiplies it by the few rows of x, so
-// reading the table bounds it.  What the kernel does per weight has to fit beside the
-// loads: codes become 16-bit floats two at a time (an OR puts a code into the low
-// mantissa bits of 128 (bf16) or 1024 (f16), one packed subtraction leaves code - 8,
-// exactly), and the products run on the warp-level tensor cores
-// (mma.sync.m16n8k16: 16 table rows x 8 rows of x), fp32 accumulation per group, one
-// fp32 multiply-add by the group's scale into the running sum.  bf16 and f16 x enter
-// as they are; an fp32 x as three bf16 pieces (8 + 8 + 8 bits of its significand), one
-// MMA each: every product is exact.  The order of k inside a group is free as long as
-// both operands use the same, so a thread's share of a group is one contiguous load of
-// group / 8 bytes per table row, and x is laid out in shared memory in the order in
-// which the fragments want it.
+// A call reads half a byte per weight and multiplies it by the few rows of x, so reading
+// the table is its floor.  What the kernel does per weight has to fit beside the loads:
+// codes become f16 two at a time (an OR puts two codes into the mantissas of 1024 or, at
+// the next higher nibble, of 1024 in steps of 16; one packed operation leaves code - 8,
+// exactly), and the products run on the warp-level tensor cores (mma.sync.m16n8k16: 16
+// table rows x 8 rows of x), fp32 accumulation per group, one fp32 multiply-add by the
+// group's scale into the running sum.
+//
+// x in f16: f16 rows as they are; bf16 and fp32 rows times a power of two that puts the
+// row's largest magnitude near 2^14.  A bf16 value is then an f16 value (its 8 bits fit;
+// values below 2^-31 of the row's largest lose bits, by at most 2^-39 of it), an fp32
+// value the sum of two (hi + lo, 22 bits), one MMA each.  So every product is exact.
+//
+// The order of k inside a group is free as long as both operands use the same: a thread's
+// share of a group is one contiguous load of group / 8 bytes per table row, and x lies in
+// shared memory in the order in which the fragments want it.  A warp takes 32 table rows
+// at a time and keeps the loads of the next groups, of this tile or the next, in flight.
+#include <type_traits>
+
 #include "tt_head.cuh"
 
 namespace ttemb {
@@ -40,47 +47,51 @@ struct Q4Args {
     float* out;             // [.][V]
     int accumulate;
     int ksplit;             // warps that share the groups of a table tile
+    int vec;                // rows of x are 16-byte aligned
+    uint32_t thousand;      // 0x64006400, not a literal in the kernel (and_or)
 };
 
-// (code - 8) of four columns as two 16-bit pairs: nibbles i and i + 4 of w.
-template <bool BF>
-__device__ __forceinline__ uint32_t q4_pair(uint32_t w, int i) {
-    const uint32_t c = ((w >> (4 * i)) & 0x000F000Fu) | (BF ? 0x43004300u : 0x64006400u);
+// (w & mask) | bits in one instruction, given that only one of the two is a literal.
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t bits) {
     uint32_t r;
-    if (BF)
-        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(c), "r"(0x43084308u));  // 136
-    else
-        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(c), "r"(0x64086408u));  // 1032
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "r"(mask), "r"(bits));
     return r;
 }
 
-template <bool BF>
-__device__ __forceinline__ void mma16816(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-    if (BF)
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-    else
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+// (code - 8) of columns i and i + 4 of the eight codes of w, i = 0 .. 3.  thousand: the
+// bits of two f16 1024s.
+__device__ __forceinline__ void q4_pairs(uint32_t w, uint32_t thousand, uint32_t (&f)[4]) {
+    const uint32_t h = w >> 8;
+    const uint32_t c0 = and_or(w, 0x000F000Fu, thousand), c1 = and_or(w, 0x00F000F0u, thousand);  // 1024 + q, 1024 + 16 q
+    const uint32_t c2 = and_or(h, 0x000F000Fu, thousand), c3 = and_or(h, 0x00F000F0u, thousand);
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(f[0]) : "r"(c0), "r"(0x64086408u));                          // - 1032
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(f[1]) : "r"(c1), "r"(0x2C002C00u), "r"(0xD480D480u));    // / 16 - 72
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(f[2]) : "r"(c2), "r"(0x64086408u));
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(f[3]) : "r"(c3), "r"(0x2C002C00u), "r"(0xD480D480u));
 }
 
-template <class T>
-struct Q4Type {
-    static constexpr bool bf = true;
-    static constexpr int pieces = 1;
-};
-template <>
-struct Q4Type<__half> {
-    static constexpr bool bf = false;
-    static constexpr int pieces = 1;
-};
-template <>
-struct Q4Type<float> {
-    static constexpr bool bf = true;
-    static constexpr int pieces = 3;
-};
+__device__ __forceinline__ void mma16816(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+template <int W>
+__device__ __forceinline__ void q4_load(const uint8_t* p, uint32_t (&q)[W]) {
+    if constexpr (W == 4) {
+        const uint4 u = __ldcs(reinterpret_cast<const uint4*>(p));
+        q[0] = u.x;
+        q[1] = u.y;
+        q[2] = u.z;
+        q[3] = u.w;
+    } else if constexpr (W == 2) {
+        const uint2 u = __ldcs(reinterpret_cast<const uint2*>(p));
+        q[0] = u.x;
+        q[1] = u.y;
+    } else {
+        q[0] = __ldcs(reinterpret_cast<const uint32_t*>(p));
+    }
+}
 
 // W = G / 32 words of 8 codes per thread, table row and group.  Shared memory:
 // x as [group][word][piece][n tile][32 lanes] x 16 bytes: lane (g, t) of an MMA (g =
@@ -88,34 +99,47 @@ struct Q4Type<float> {
 // holds in that word, in the order 0 4 1 5 2 6 3 7 of its nibbles.
 template <class T, int G, int NT>
 __global__ void __launch_bounds__(kQ4Threads, 2) k_q4_matvec(const __grid_constant__ Q4Args a) {
-    constexpr int W = G / 32, P = Q4Type<T>::pieces;
-    constexpr bool BF = Q4Type<T>::bf;
+    constexpr int W = G / 32, P = sizeof(T) == 4 ? 2 : 1;
     extern __shared__ uint4 xs[];
     __shared__ float red[kQ4Warps][kQ4Rows * 8];  // one n tile at a time
+    __shared__ float up[NT * 8], down[NT * 8];    // a row's power of two, and its inverse
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     const int ng = a.g1 - a.g0;
 
-    const T* x = static_cast<const T*>(a.x);
+    const T* x = static_cast<const T*>(a.x) + (int64_t)a.m0 * a.ldx;
+    for (int m = warp; m < NT * 8; m += kQ4Warps) {
+        uint32_t most = 0;
+        if (sizeof(T) != 2 || !std::is_same<T, __half>::value)
+            if (m < a.M)
+                for (int d = a.g0 * G + lane; d < min(a.g1 * G, a.D); d += 32) {
+                    const uint32_t b = __float_as_uint(to_f32(x[m * a.ldx + d])) & 0x7FFFFFFFu;
+                    if (b < 0x7F800000u) most = max(most, b);
+                }
+        const int e = scale_exp(__reduce_max_sync(0xffffffffu, most));
+        if (lane == 0) {
+            up[m] = exp2i(e);
+            down[m] = exp2i(-e);
+        }
+    }
+    __syncthreads();
     for (int i = threadIdx.x; i < ng * W * NT * 32; i += kQ4Threads) {
         const int l = i & 31, rest = i >> 5;
         const int nt = rest % NT, w = rest / NT % W, j = rest / NT / W;
         const int m = nt * 8 + (l >> 2), d0 = (a.g0 + j) * G + (l & 3) * (G / 4) + w * 8;
         uint16_t u[P][8];
+        __align__(16) T y[8];
+        const bool all = m < a.M && d0 + 8 <= a.D && a.vec;
+        if (all)
+#pragma unroll
+            for (int e = 0; e < (int)sizeof(T) / 2; ++e)
+                reinterpret_cast<uint4*>(y)[e] = __ldg(reinterpret_cast<const uint4*>(x + m * a.ldx + d0) + e);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const int d = d0 + (e >> 1) + (e & 1) * 4;
-            const bool in = m < a.M && d < a.D;
-            if (P == 1) {
-                u[0][e] = in ? reinterpret_cast<const uint16_t*>(x + (a.m0 + m) * a.ldx)[d] : (uint16_t)0;
-            } else {
-                float v = in ? to_f32(x[(a.m0 + m) * a.ldx + d]) : 0.f;
-#pragma unroll
-                for (int p = 0; p < P; ++p) {
-                    const __nv_bfloat16 b = __float2bfloat16_rn(v);
-                    u[p][e] = __bfloat16_as_ushort(b);
-                    v -= __bfloat162float(b);
-                }
-            }
+            const int k = (e >> 1) + (e & 1) * 4;
+            const float v = (all ? to_f32(y[k]) : (m < a.M && d0 + k < a.D ? to_f32(x[m * a.ldx + d0 + k]) : 0.f)) * up[m];
+            const __half hi = __float2half_rn(v);
+            u[0][e] = __half_as_ushort(hi);
+            if (P == 2) u[P - 1][e] = __half_as_ushort(__float2half_rn(v - __half2float(hi)));
         }
 #pragma unroll
         for (int p = 0; p < P; ++p) xs[(((j * W + w) * P + p) * NT + nt) * 32 + l] = *reinterpret_cast<uint4*>(u[p]);
@@ -127,119 +151,135 @@ __global__ void __launch_bounds__(kQ4Threads, 2) k_q4_matvec(const __grid_consta
     const int jb = ng * ks / a.ksplit, je = ng * (ks + 1) / a.ksplit;
     const int64_t ntiles = (a.V + kQ4Rows - 1) / kQ4Rows;
     const int64_t rounds = (ntiles + tiles_per_block - 1) / tiles_per_block;
-    for (int64_t rd = blockIdx.x; rd < rounds; rd += gridDim.x) {
-        const int64_t tile = rd * tiles_per_block + sub;
-        float tot[2][NT][4];
+
+    // the next group to load: round lr, group lj; four table rows per thread, tile * 32 +
+    // {0, 8, 16, 24} + g (rows past V read row V - 1)
+    int64_t lr = blockIdx.x;
+    int lj = jb;
+    const uint8_t* pr[4];
+    const __nv_bfloat16* sr[4];
+    auto at_tile = [&]() {
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) tot[r][n][e] = 0.f;
-        if (tile < ntiles) {
-            // four table rows per thread: tile * 32 + {0, 8, 16, 24} + g; rows past V read row V - 1
-            const uint8_t* pr[4];
-            const __nv_bfloat16* sr[4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                int64_t v = tile * kQ4Rows + r * 8 + g;
-                v = v < a.V ? v : a.V - 1;
-                pr[r] = a.packed + v * a.pitch + t * (G / 8);
-                sr[r] = a.scales + v * a.groups;
-            }
-            auto load = [&](int j, uint32_t (&q)[4][W], float (&s)[4]) {
-                const int64_t at = (int64_t)(a.g0 + j) * (G / 2);
-                const bool in = at + t * (G / 8) < a.pitch;
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    if (W == 4) {
-                        const uint4 u = in ? __ldcs(reinterpret_cast<const uint4*>(pr[r] + at))
-                                           : make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
-                        q[r][0] = u.x;
-                        q[r][1 % W] = u.y;
-                        q[r][2 % W] = u.z;
-                        q[r][3 % W] = u.w;
-                    } else if (W == 2) {
-                        const uint2 u = in ? __ldcs(reinterpret_cast<const uint2*>(pr[r] + at)) : make_uint2(0x88888888u, 0x88888888u);
-                        q[r][0] = u.x;
-                        q[r][1 % W] = u.y;
-                    } else {
-                        q[r][0] = in ? __ldcs(reinterpret_cast<const uint32_t*>(pr[r] + at)) : 0x88888888u;
-                    }
-                    s[r] = __bfloat162float(sr[r][a.g0 + j]);
-                }
-            };
-            constexpr int U = W == 4 ? 2 : 4;  // groups in flight
-            uint32_t q[U][4][W];
-            float s[U][4];
-#pragma unroll
-            for (int i = 0; i < U; ++i)
-                if (jb + i < je) load(jb + i, q[i], s[i]);
-            for (int j0 = jb; j0 < je; j0 += U) {
-#pragma unroll
-                for (int i = 0; i < U; ++i) {
-                    const int j = j0 + i;
-                    if (j >= je) break;
-                    float acc[2][NT][4];
-#pragma unroll
-                    for (int r = 0; r < 2; ++r)
-#pragma unroll
-                        for (int n = 0; n < NT; ++n)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) acc[r][n][e] = 0.f;
-#pragma unroll
-                    for (int w = 0; w < W; ++w) {
-                        uint32_t f[4][4];
-#pragma unroll
-                        for (int r = 0; r < 4; ++r)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) f[r][e] = q4_pair<BF>(q[i][r][w], e);
-#pragma unroll
-                        for (int p = 0; p < P; ++p)
-#pragma unroll
-                            for (int n = 0; n < NT; ++n) {
-                                const uint4 b = xs[(((j * W + w) * P + p) * NT + n) * 32 + lane];
-#pragma unroll
-                                for (int r = 0; r < 2; ++r) {
-                                    mma16816<BF>(acc[r][n], f[2 * r][0], f[2 * r + 1][0], f[2 * r][1], f[2 * r + 1][1], b.x, b.y);
-                                    mma16816<BF>(acc[r][n], f[2 * r][2], f[2 * r + 1][2], f[2 * r][3], f[2 * r + 1][3], b.z, b.w);
-                                }
-                            }
-                    }
-#pragma unroll
-                    for (int r = 0; r < 2; ++r)
-#pragma unroll
-                        for (int n = 0; n < NT; ++n)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                tot[r][n][e] = fmaf(s[i][2 * r + (e >> 1)], acc[r][n][e], tot[r][n][e]);
-                    if (j + U < je) load(j + U, q[i], s[i]);
-                }
-            }
+        for (int r = 0; r < 4; ++r) {
+            int64_t v = (lr * tiles_per_block + sub) * kQ4Rows + r * 8 + g;
+            v = v < a.V ? v : a.V - 1;
+            pr[r] = a.packed + v * a.pitch;
+            sr[r] = a.scales + v * a.groups;
         }
-        // join the warps that share the tile and write: element (row, m) of an n tile
+    };
+    at_tile();
+    auto load = [&](uint32_t (&q)[4][W], uint32_t (&s)[4]) {
+        if (lr >= rounds) return;
+        // a share past the row's end: any codes will do, x is 0 there
+        int at = (a.g0 + lj) * (G / 2) + t * (G / 8);
+        at = at < (int)a.pitch ? at : 0;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            if (n * 8 >= a.M) break;
-            if (a.ksplit > 1) __syncthreads();
-            float* my = red[warp];
+        for (int r = 0; r < 4; ++r) {
+            q4_load<W>(pr[r] + at, q[r]);
+            s[r] = *reinterpret_cast<const uint16_t*>(sr[r] + a.g0 + lj);
+        }
+        if (++lj == je) {
+            lj = jb;
+            lr += gridDim.x;
+            if (lr < rounds) at_tile();
+        }
+    };
+    constexpr int U = (W == 4 ? 2 : 4) / (NT == 4 ? 2 : 1);  // groups in flight, as registers allow
+    uint32_t q[U][4][W], s[U][4];
+#pragma unroll
+    for (int i = 0; i < U; ++i) load(q[i], s[i]);
+
+    float tot[2][NT][4];
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) tot[r][n][e] = 0.f;
+    int64_t rd = blockIdx.x;
+    int j = jb;
+    while (rd < rounds) {
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            if (rd >= rounds) break;
+            float acc[2][NT][4];
 #pragma unroll
             for (int r = 0; r < 2; ++r)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) my[(2 * t + (e & 1)) * kQ4Rows + r * 16 + (e >> 1) * 8 + g] = tot[r][n][e];
-            if (a.ksplit > 1)
-                __syncthreads();
-            else
-                __syncwarp();
-            const int64_t v = tile * kQ4Rows + lane;
-            for (int m = ks; m < 8; m += a.ksplit) {
-                if (n * 8 + m >= a.M || v >= a.V) continue;
-                float sum = 0.f;
-                for (int k = 0; k < a.ksplit; ++k) sum += red[sub * a.ksplit + k][m * kQ4Rows + lane];
-                float* o = a.out + (int64_t)(a.m0 + n * 8 + m) * a.V + v;
-                *o = a.accumulate ? *o + sum : sum;
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[r][n][e] = 0.f;
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+                uint32_t f[4][4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) q4_pairs(q[i][r][w], a.thousand, f[r]);
+#pragma unroll
+                for (int p = P - 1; p >= 0; --p)  // small products first
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        const uint4 b = xs[(((j * W + w) * P + p) * NT + n) * 32 + lane];
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            mma16816(acc[r][n], f[2 * r][0], f[2 * r + 1][0], f[2 * r][1], f[2 * r + 1][1], b.x, b.y);
+                            mma16816(acc[r][n], f[2 * r][2], f[2 * r + 1][2], f[2 * r][3], f[2 * r + 1][3], b.z, b.w);
+                        }
+                    }
             }
-            if (a.ksplit == 1) __syncwarp();
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) tot[r][n][e] = fmaf(__uint_as_float(s[i][2 * r + (e >> 1)] << 16), acc[r][n][e], tot[r][n][e]);
+            load(q[i], s[i]);
+            if (++j < je) continue;
+            // the tile's last group: element (row, m) of n tile n is tot[..][n][..]
+            const int64_t v0 = (rd * tiles_per_block + sub) * kQ4Rows;
+            if (a.ksplit == 1) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int m = n * 8 + 2 * t + e;
+                        if (m >= a.M) continue;
+                        float* o = a.out + (int64_t)(a.m0 + m) * a.V + v0 + g;
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            if (v0 + r * 8 + g >= a.V) continue;
+                            const float y = tot[r >> 1][n][(r & 1) * 2 + e] * down[m];
+                            o[r * 8] = a.accumulate ? o[r * 8] + y : y;
+                        }
+                    }
+            } else {  // joined with the other warps of the tile
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    if (n * 8 >= a.M) break;
+                    __syncthreads();
+#pragma unroll
+                    for (int r = 0; r < 2; ++r)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) red[warp][(2 * t + (e & 1)) * kQ4Rows + r * 16 + (e >> 1) * 8 + g] = tot[r][n][e];
+                    __syncthreads();
+                    const int64_t v = v0 + lane;
+                    for (int m = ks; m < 8; m += a.ksplit) {
+                        if (n * 8 + m >= a.M || v >= a.V) continue;
+                        float sum = 0.f;
+                        for (int k = 0; k < a.ksplit; ++k) sum += red[sub * a.ksplit + k][m * kQ4Rows + lane];
+                        sum *= down[n * 8 + m];
+                        float* o = a.out + (int64_t)(a.m0 + n * 8 + m) * a.V + v;
+                        *o = a.accumulate ? *o + sum : sum;
+                    }
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) tot[r][n][e] = 0.f;
+            j = jb;
+            rd += gridDim.x;
         }
     }
 }
@@ -295,10 +335,13 @@ tt_status q4_shape(int64_t V, int32_t D, int32_t G, int32_t dtype, Q4Shape* s) {
 template <class T, int G, int NT>
 struct Q4Tag {};
 
+template <class T>
+constexpr int q4_pieces() { return sizeof(T) == 4 ? 2 : 1; }
+
 template <class T, int G, int NT>
 tt_status q4_launch(Q4Args a, int sms, int dev, cudaStream_t st) {
     const int ng = a.g1 - a.g0;
-    const size_t smem = (size_t)ng * (G / 32) * Q4Type<T>::pieces * NT * 512;
+    const size_t smem = (size_t)ng * (G / 32) * q4_pieces<T>() * NT * 512;
     const int64_t ntiles = (a.V + kQ4Rows - 1) / kQ4Rows;
     // warps that share a tile's columns: more of them while the tiles alone would give
     // a warp slot fewer than 4, as long as each keeps two groups
@@ -319,7 +362,7 @@ tt_status q4_rows(Q4Args a, int M, int sms, int dev, cudaStream_t st) {
         a.M = M - m0 < 32 ? M - m0 : 32;
         const int nt = a.M <= 8 ? 1 : (a.M <= 16 ? 2 : 4);
         // x of as many groups as fit in shared memory at a time
-        int fit = (int)(kQ4SmemBytes / ((size_t)(G / 32) * Q4Type<T>::pieces * nt * 512));
+        int fit = (int)(kQ4SmemBytes / ((size_t)(G / 32) * q4_pieces<T>() * nt * 512));
         const int launches = (groups + fit - 1) / fit;
         for (int i = 0; i < launches; ++i) {
             a.g0 = (int)((int64_t)groups * i / launches);
@@ -390,6 +433,8 @@ tt_status tt_emb_q4_matvec(const void* x_dev, int64_t x_stride, int32_t rows, in
     Q4Args a{};
     a.x = x_dev;
     a.ldx = x_stride;
+    a.vec = (uintptr_t)x_dev % 16 == 0 && x_stride * (dtype == TT_F32 ? 4 : 2) % 16 == 0;
+    a.thousand = 0x64006400u;
     a.D = dim;
     a.packed = packed_dev;
     a.pitch = s.pitch;
