@@ -28,9 +28,11 @@
 // the two gradient products (relative 2^-9 or 2^-12 an entry, independent errors,
 // the size of the gradients' own final rounding), and split like an input for fp32.
 #include <math.h>
-#include <stdio.h>
+
+#include <type_traits>
 
 #include "tt_head.cuh"
+#include "tt_head_few.cuh"
 #include "tt_head_fused.cuh"
 #include "tt_head_gemm.cuh"
 
@@ -38,6 +40,7 @@ namespace ttemb {
 
 constexpr int64_t kDzBytes = 256ll << 20;  // dz of one vocabulary piece
 constexpr int64_t kMaxBlocks = 1ll << 26;    // 32 x 32 blocks of targets (1 GB of them)
+constexpr int kFewMinDim = 256;              // 16-bit rows: k_head_few from this width on
 constexpr int kMaxTeacher = TT_HEAD_MAX_TEACHER;
 
 // ---------------------------------------------------------------- rows and copies
@@ -685,10 +688,14 @@ struct Plan {
     HeadIn in;
     int type, fmt, split;    // split: fp32 operands in hi and lo pieces
     int esize, sms, device;
-    bool pack_h, pack_w;
+    bool pack_h, pack_w;          // 16-bit copies of hidden and weight
+    bool pack_h_fwd, pack_w_fwd;  // in the forward pass
     int bn_s;                // column tile of the score products
     int strip;
     int slots, per_slot;     // (maximum, sum) pairs per row: slots of per_slot
+    bool few;                // forward: scores by k_head_few, on few_blocks blocks
+    int few_blocks, few_ksplit;
+    size_t few_smem;
     bool fused_lse;          // scores by k_head_fused, its work shared as in
     Runs runs_lse, runs_dw, runs_dh;
     bool fused;              // backward: dz stays on the chip (k_head_fused)
@@ -729,6 +736,8 @@ tt_status make_plan(const tt_head* hd, int K, Plan* p) {
     in.vec = ah && aw && in.D % 8 == 0;
     p->pack_h = p->split || !ah;
     p->pack_w = p->split || !aw;
+    p->pack_h_fwd = p->pack_h;
+    p->pack_w_fwd = p->pack_w;
     const int64_t mt = cdiv(in.N, 128);
     // 256-column tiles read each operand row less often; 128-column tiles when the
     // wide ones would leave blocks without work
@@ -748,6 +757,30 @@ tt_status make_plan(const tt_head* hd, int K, Plan* p) {
         const int64_t shortest = p->runs_lse.total() / p->runs_lse.blocks;  // tiles of a run, rounded down
         p->slots = (int)(cdiv(p->runs_lse.ytiles, shortest) + 1);           // most runs that an x is in
         p->per_slot = 2 * (by / 64);
+    }
+    // few rows: a pass over the table as it is per eight of them, when its rows can be read
+    // 16 bytes at a time.  Measured against the other kernels, rows x table: bf16 4 x 131072
+    // x 4096 187 us (253), 8 x 131072 x 1024 59 (71), but 8 x 10^6 x 64 55 (38), where a tile's
+    // end outweighs its loads; fp32, which the others copy in pieces first, 8 x 131072 x 1024
+    // 109 (434), 16 rows in two passes 218 (484), 8 x 10^6 x 64 73 (144), 16 rows 146 (144).
+    const int64_t chunks = cdiv((int64_t)in.D * p->esize, 64);
+    p->few_smem = (size_t)(chunks * 512);
+    p->few = in.N > 0 && in.N <= (p->split ? 16 : 8) && (p->split || in.D >= kFewMinDim) && aw && (int64_t)in.D * p->esize % 16 == 0 &&
+             p->few_smem <= kFewSmem;
+    if (p->few) {
+        const int64_t tiles = cdiv(in.V, kFewRows), steps = cdiv(chunks, kFewStep);
+        const int blocks = (p->few_smem <= 100 * 1024 ? 2 : 1) * p->sms;
+        // warps share a tile's columns while the tiles alone would give a warp fewer than 4
+        // of them, as long as each keeps two steps
+        p->few_ksplit = 1;
+        while (p->few_ksplit < kFewWarps && tiles * p->few_ksplit < 4ll * blocks * kFewWarps && steps >= 4 * p->few_ksplit) p->few_ksplit *= 2;
+        const int64_t rounds = cdiv(tiles, kFewWarps / p->few_ksplit);
+        p->few_blocks = (int)(rounds < blocks ? rounds : blocks);
+        p->slots = p->few_blocks;
+        p->per_slot = 1;
+        p->fused_lse = false;
+        p->runs_lse = Runs{};
+        p->pack_h_fwd = p->pack_w_fwd = false;
     }
     // backward
     p->nblocks = cdiv(in.N, 32);
@@ -792,11 +825,11 @@ struct FwdWs {
 size_t fwd_ws(const Plan& p, void* base, FwdWs* w) {
     Arena a(base);
     const int64_t pc = p.split ? 2 : 1;
-    w->wexp = a.get<int>(p.split ? cdiv(p.in.V, 128) : 0);
+    w->wexp = a.get<int>(p.split && p.pack_w_fwd ? cdiv(p.in.V, 128) : 0);
     w->part = a.get<float2>(p.in.N * p.slots * p.per_slot);
-    w->row_exp = a.get<int>(p.split ? p.in.N : 0);
-    w->hp = a.get<uint16_t>(p.pack_h ? pc * p.in.N * p.in.Dp : 0);
-    w->wp = a.get<uint16_t>(p.pack_w ? pc * p.in.V * p.in.Dp : 0);
+    w->row_exp = a.get<int>(p.split && p.pack_h_fwd ? p.in.N : 0);
+    w->hp = a.get<uint16_t>(p.pack_h_fwd ? pc * p.in.N * p.in.Dp : 0);
+    w->wp = a.get<uint16_t>(p.pack_w_fwd ? pc * p.in.V * p.in.Dp : 0);
     return a.used;
 }
 
@@ -861,26 +894,54 @@ GemmArgs gemm_args(const Plan& p, int* err) {
 }
 
 template <class T>
+constexpr int type_of() { return sizeof(T) == 4 ? TT_F32 : (std::is_same<T, __half>::value ? TT_F16 : TT_BF16); }
+
+template <class T>
+bool run_few(const Plan& p, const FewArgs& a, cudaStream_t st) {
+    auto k = k_head_few<T, type_of<T>()>;
+    if (!allow_smem<KernelTag<type_of<T>(), 0, 0, 0, -2>>(k, p.device, kFewSmem)) return false;
+    k<<<(unsigned)p.few_blocks, kFewThreads, p.few_smem, st>>>(a);
+    return cudaGetLastError() == cudaSuccess;
+}
+
+template <class T>
 tt_status head_forward(const Plan& p, const Target& t, float* loss, float* lse, int* err, void* ws, size_t ws_bytes, cudaStream_t st) {
     const HeadIn& in = p.in;
     FwdWs w;
     if (fwd_ws(p, ws, &w) > ws_bytes) return TT_ERR_ARG;
     if (in.N == 0) return TT_OK;
     const bool distill = t.logits != nullptr;
-    if (p.pack_h || p.pack_w) {
+    if (p.pack_h_fwd || p.pack_w_fwd) {
         PrepArgs a{};
         a.in = in;
-        a.wp = p.pack_w ? w.wp : nullptr;
+        a.wp = p.pack_w_fwd ? w.wp : nullptr;
         a.wexp = w.wexp;
-        a.hp = p.pack_h ? w.hp : nullptr;
+        a.hp = p.pack_h_fwd ? w.hp : nullptr;
         a.row_exp = w.row_exp;
         if (!launch_prep<T>(p, a, st)) return TT_ERR_CUDA;
     }
-    const Operand H{p.pack_h ? w.hp : static_cast<const uint16_t*>(in.h), in.N, in.D, p.pack_h ? in.Dp : in.ldh, in.N * in.Dp};
-    const Operand W{p.pack_w ? w.wp : static_cast<const uint16_t*>(in.w), in.V, in.D, p.pack_w ? in.Dp : in.ldw, in.V * in.Dp};
+    const Operand H{p.pack_h_fwd ? w.hp : static_cast<const uint16_t*>(in.h), in.N, in.D, p.pack_h_fwd ? in.Dp : in.ldh, in.N * in.Dp};
+    const Operand W{p.pack_w_fwd ? w.wp : static_cast<const uint16_t*>(in.w), in.V, in.D, p.pack_w_fwd ? in.Dp : in.ldw, in.V * in.Dp};
     const int* row_exp = p.split ? w.row_exp : nullptr;
     bool ok;
-    if (p.fused_lse) {
+    if (p.few) {
+        FewArgs a{};
+        a.w = in.w;
+        a.ldh = in.ldh;
+        a.ldw = in.ldw;
+        a.V = in.V;
+        a.D = in.D;
+        a.chunks = (int)cdiv((int64_t)in.D * p.esize, 64);
+        a.ksplit = p.few_ksplit;
+        a.c = kLog2e / t.T;
+        ok = true;
+        for (int n0 = 0; ok && n0 < in.N; n0 += 8) {
+            a.h = static_cast<const T*>(in.h) + n0 * in.ldh;
+            a.N = (int)(in.N - n0 < 8 ? in.N - n0 : 8);
+            a.part = w.part + (int64_t)n0 * p.slots;
+            ok = run_few<T>(p, a, st);
+        }
+    } else if (p.fused_lse) {
         FusedArgs a{};
         a.D = in.D;
         a.runs = p.runs_lse;
