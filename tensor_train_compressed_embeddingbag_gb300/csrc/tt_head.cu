@@ -21,8 +21,8 @@
 //
 // Types.  bf16 and f16 inputs go to the tensor cores as they are.  An fp32 input x
 // is split as x 2^e = hi + lo with hi, lo in f16 (e a power-of-two scale that puts
-// the largest magnitude near 2^14: of a hidden row in the forward pass, of 128 table
-// rows, of all hidden rows that count and of all of dz in the backward pass) and a product is taken as hi hi + hi lo + lo hi,
+// the largest magnitude near 2^14: of a hidden row in the forward pass, of 128 x 128
+// elements of the table, of all hidden rows that count and of all of dz in the backward pass) and a product is taken as hi hi + hi lo + lo hi,
 // so 22 bits of each operand enter, with fp32 accumulation; lo lo (2^-22 of the
 // product and below) is dropped.  dz is rounded to the inputs' 16-bit type before
 // the two gradient products (relative 2^-9 or 2^-12 an entry, independent errors,
@@ -363,9 +363,9 @@ __device__ __forceinline__ void split8(const float (&x)[8], float sc, uint16_t* 
 
 // What a pass needs before its products, in one launch.
 //   blockIdx.y = 0  the table packed in rows of Dp 16-bit elements (fp32: hi and lo
-//                   pieces, a scale per 128 rows, its exponent in wexp: the rows of a tile
-//                   of the products, so that a scale is one factor per tile; up to 128
-//                   columns a tile is read once and kept in registers)
+//                   pieces, a scale per 128 x 128 block, its exponent in wexp: what a tile of
+//                   the products takes of the table between two read-outs, so that a scale is
+//                   one factor there; a block is read once and kept in registers)
 //   blockIdx.y = 1  forward: the hidden rows packed, a warp per row (fp32: a scale of each
 //                   row's own, its exponent in row_exp); backward: the largest finite
 //                   |grad| T and (fp32) |hidden| over the rows that count, a share per block
@@ -384,7 +384,7 @@ struct PrepArgs {
     int64_t nclear;
 };
 
-template <class T, int TH, int Q>  // TH threads; Q (fp32): 8-element groups that a thread holds of a tile, 0: none
+template <class T, int TH>  // TH threads; fp32: 4 groups of 8 elements a thread, 128 x 128 (512 threads) or 128 x 64
 __global__ void __launch_bounds__(TH, 1024 / TH) k_head_prep(const __grid_constant__ PrepArgs a) {
     const HeadIn& in = a.in;
     uint16_t* const wp = a.wp;
@@ -397,27 +397,21 @@ __global__ void __launch_bounds__(TH, 1024 / TH) k_head_prep(const __grid_consta
         const int64_t piece = in.V * in.Dp;
         if constexpr (sizeof(T) == 4) {
             const float* w = static_cast<const float*>(in.w);
-            const int64_t tiles = (in.V + 127) / 128;
-            for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-                const int64_t v0 = tile * 128;
-                const int rows = (int)min((int64_t)128, in.V - v0), total = rows * g;
-                float x[Q ? Q : 1][8];
+            const int cb = (in.D + 127) / 128;  // blocks to a row of blocks
+            const int64_t all = (in.V + 127) / 128 * cb;
+            for (int64_t blk = blockIdx.x; blk < all; blk += gridDim.x) {
+                const int64_t v0 = blk / cb * 128;
+                const int c0 = (int)(blk % cb) * 128;
+                const int rows = (int)min((int64_t)128, in.V - v0), bg = min(16, g - c0 / 8), total = rows * bg;
+                const uint32_t inv = 65536u / bg + 1;  // i / bg for i < 2,048, bg <= 16
+                float x[4][8];
                 uint32_t m = 0;
-                if (Q) {
-                    const uint32_t inv = 65536u / g + 1;  // i / g for i < 2,048, g <= 16
 #pragma unroll
-                    for (int q = 0; q < Q; ++q) {
-                        const int i = threadIdx.x + q * TH, r = (int)(i * inv >> 16), c = (i - r * g) * 8;
-                        if (i < total) {
-                            load8(in, w + (v0 + r) * in.ldw + c, c, x[q]);
-                            m = absmax8(x[q], m);
-                        }
-                    }
-                } else {
-                    for (int i = threadIdx.x; i < total; i += TH) {
-                        const int r = i / g, c = (i - r * g) * 8;
-                        load8(in, w + (v0 + r) * in.ldw + c, c, x[0]);
-                        m = absmax8(x[0], m);
+                for (int q = 0; q < 4; ++q) {
+                    const int i = threadIdx.x + q * TH, r = (int)(i * inv >> 16), c = c0 + (i - r * bg) * 8;
+                    if (i < total) {
+                        load8(in, w + (v0 + r) * in.ldw + c, c, x[q]);
+                        m = absmax8(x[q], m);
                     }
                 }
                 m = __reduce_max_sync(0xffffffffu, m);
@@ -428,20 +422,12 @@ __global__ void __launch_bounds__(TH, 1024 / TH) k_head_prep(const __grid_consta
                 __syncthreads();
                 const int e = scale_exp(m);
                 const float sc = exp2i(e);
-                if (threadIdx.x == 0) a.wexp[tile] = e;
-                uint16_t* to = wp + v0 * in.Dp;
-                if (Q) {
+                if (threadIdx.x == 0) a.wexp[blk] = e;
 #pragma unroll
-                    for (int q = 0; q < Q; ++q) {
-                        const int i = threadIdx.x + q * TH;
-                        if (i < total) split8(x[q], sc, to + i * 8, to + piece + i * 8);
-                    }
-                } else {
-                    for (int i = threadIdx.x; i < total; i += TH) {
-                        const int r = i / g, c = (i - r * g) * 8;
-                        load8(in, w + (v0 + r) * in.ldw + c, c, x[0]);
-                        split8(x[0], sc, to + (int64_t)i * 8, to + piece + (int64_t)i * 8);
-                    }
+                for (int q = 0; q < 4; ++q) {
+                    const int i = threadIdx.x + q * TH, r = (int)(i * inv >> 16), c = c0 + (i - r * bg) * 8;
+                    uint16_t* to = wp + (v0 + r) * in.Dp + c;
+                    if (i < total) split8(x[q], sc, to, to + piece);
                 }
             }
         } else {
@@ -825,7 +811,7 @@ struct FwdWs {
 size_t fwd_ws(const Plan& p, void* base, FwdWs* w) {
     Arena a(base);
     const int64_t pc = p.split ? 2 : 1;
-    w->wexp = a.get<int>(p.split && p.pack_w_fwd ? cdiv(p.in.V, 128) : 0);
+    w->wexp = a.get<int>(p.split && p.pack_w_fwd ? cdiv(p.in.V, 128) * cdiv(p.in.D, 128) : 0);
     w->part = a.get<float2>(p.in.N * p.slots * p.per_slot);
     w->row_exp = a.get<int>(p.split && p.pack_h_fwd ? p.in.N : 0);
     w->hp = a.get<uint16_t>(p.pack_h_fwd ? pc * p.in.N * p.in.Dp : 0);
@@ -846,7 +832,7 @@ size_t bwd_ws(const Plan& p, int K, void* base, BwdWs* w) {
     const int64_t pc = p.split ? 2 : 1, nk = p.in.N * K;
     w->amax = a.get<uint32_t>(4);
     w->shares = a.get<uint32_t>(2 * kAmaxShares);
-    w->wexp = a.get<int>(p.split ? cdiv(p.in.V, 128) : 0);
+    w->wexp = a.get<int>(p.split ? cdiv(p.in.V, 128) * cdiv(p.in.D, 128) : 0);
     w->nlse = a.get<float>(cdiv(p.in.N, 128) * 128);
     w->scale = a.get<float>(cdiv(p.in.N, 128) * 128);
     w->ids = a.get<int>(p.fused ? 0 : nk);
@@ -871,16 +857,14 @@ bool launch_ok() { return cudaGetLastError() == cudaSuccess; }
 
 template <class T>
 bool launch_prep(const Plan& p, const PrepArgs& a, cudaStream_t st) {
-    const int64_t w = !a.wp ? 0 : (p.split ? cdiv(p.in.V, 128) : cdiv(p.in.V * (p.in.Dp / 8), 256));
+    const int64_t w = !a.wp ? 0 : (p.split ? cdiv(p.in.V, 128) * cdiv(p.in.D, 128) : cdiv(p.in.V * (p.in.Dp / 8), 256));
     const int64_t h = a.hp ? cdiv(p.in.N, 8) : (a.shares ? cdiv(p.in.N, 32) : 0), c = cdiv(a.nclear, 1024);
     const int64_t most = w > h ? (w > c ? w : c) : (h > c ? h : c);
     const dim3 grid(grid_of(most, 1, p.sms, 16), a.nclear ? 3 : (h ? 2 : 1));
-    if (p.split && p.in.Dp <= 64)
-        k_head_prep<T, 256, 4><<<grid, 256, 0, st>>>(a);
-    else if (p.split && p.in.Dp <= 128)
-        k_head_prep<T, 512, 4><<<grid, 512, 0, st>>>(a);
+    if (p.split && p.in.Dp > 64)
+        k_head_prep<T, 512><<<grid, 512, 0, st>>>(a);
     else
-        k_head_prep<T, 256, 0><<<grid, 256, 0, st>>>(a);
+        k_head_prep<T, 256><<<grid, 256, 0, st>>>(a);
     return launch_ok();
 }
 
@@ -959,7 +943,8 @@ tt_status head_forward(const Plan& p, const Target& t, float* loss, float* lse, 
         a.N = in.V;
         a.strip = p.strip;
         a.chunks = (int)cdiv(in.D, kBK);
-        a.wexp = w.wexp;
+        a.wexp = p.split ? w.wexp : nullptr;
+        a.kb = (int)cdiv(in.D, 128);
         a.row_exp = row_exp;
         a.ctemp = kLog2e / t.T;
         a.part = w.part;
@@ -1055,7 +1040,8 @@ tt_status head_backward(const Plan& p, const Target& t, const float* lse, const 
         a.N = P;
         a.chunks = (int)cdiv(in.D, kBK);
         a.amax_a = ah;
-        a.wexp = w.wexp + v0 / 128;  // a piece begins at a multiple of 256 rows
+        a.kb = (int)cdiv(in.D, 128);
+        a.wexp = p.split ? w.wexp + v0 / 128 * a.kb : nullptr;  // a piece begins at a multiple of 256 rows
         a.ctemp = kLog2e / t.T;
         a.nlse = w.nlse;
         a.scale = w.scale;
@@ -1085,7 +1071,8 @@ tt_status head_backward(const Plan& p, const Target& t, const float* lse, const 
         c.chunks = (int)cdiv(P, kBK);
         c.splits = p.dh_splits;
         c.amax_a = az;
-        c.wexp = p.split ? w.wexp + v0 / 128 : nullptr;
+        c.kb = (int)cdiv(in.D, 128);
+        c.wexp = p.split ? w.wexp + v0 / 128 * c.kb : nullptr;
         c.to = dest(p.dh_direct ? dh : nullptr, w.dh_part);
         c.to.accumulate = i > 0;
         if (!out_gemm<false>(p.split, Z, W, c, p.sms, p.device, st)) return TT_ERR_CUDA;

@@ -291,22 +291,6 @@ struct OutArgs {
     int accumulate;  // add to what partial holds
 };
 
-__device__ __forceinline__ void store_vec(void* out, int64_t at, const float* v, int type) {
-    // 8 consecutive elements, 16-byte aligned
-    if (type == TT_F32) {
-        float4* o = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
-        o[0] = make_float4(v[0], v[1], v[2], v[3]);
-        o[1] = make_float4(v[4], v[5], v[6], v[7]);
-    } else {
-        const int fmt = type == TT_BF16;
-        uint4 u;
-        u.x = pack16(v[0], v[1], fmt);
-        u.y = pack16(v[2], v[3], fmt);
-        u.z = pack16(v[4], v[5], fmt);
-        u.w = pack16(v[6], v[7], fmt);
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at) = u;
-    }
-}
 __device__ __forceinline__ void store_one(void* out, int64_t at, float v, int type) {
     if (type == TT_F32)
         static_cast<float*>(out)[at] = v;
@@ -316,31 +300,73 @@ __device__ __forceinline__ void store_one(void* out, int64_t at, float v, int ty
         static_cast<__half*>(out)[at] = __float2half_rn(v);
 }
 
-// 32 consecutive columns [col, col + 32) of row `row`; col < N.
-__device__ __forceinline__ void store_out(const OutArgs& o, int split, int64_t row, int64_t col, int64_t M, int64_t N, float (&v)[32],
+// A warp's 32 rows x 64 bytes, a row per lane, written out through 2 KB of shared memory
+// so that four lanes write one row's 64 bytes and a store touches 8 rows, not 32.  base:
+// where the first row's bytes go; rows past `rows` are left alone.
+__device__ __forceinline__ void put_rows(uint4* buf, const uint4 (&mine)[4], uint8_t* base, int64_t pitch, int64_t rows) {
+    const int lane = threadIdx.x & 31;
+    __syncwarp();
+#pragma unroll
+    for (int c = 0; c < 4; ++c) buf[lane * 4 + (c ^ ((lane >> 1) & 3))] = mine[c];
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = i * 8 + (lane >> 2), c = lane & 3;
+        if (r < rows) *reinterpret_cast<uint4*>(base + r * pitch + c * 16) = buf[r * 4 + (c ^ ((r >> 1) & 3))];
+    }
+}
+__device__ __forceinline__ uint4 bits4(const float* v) {
+    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+}
+// The same for 32 fp32 columns (128 bytes a row).
+__device__ __forceinline__ void put_rows_f32(uint4* buf, const float (&v)[32], uint8_t* base, int64_t pitch, int64_t rows) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const uint4 mine[4] = {bits4(v + h * 16), bits4(v + h * 16 + 4), bits4(v + h * 16 + 8), bits4(v + h * 16 + 12)};
+        put_rows(buf, mine, base + h * 64, pitch, rows);
+    }
+}
+__device__ __forceinline__ void put_rows_16(uint4* buf, const float (&v)[32], uint8_t* base, int64_t pitch, int64_t rows, int fmt) {
+    uint32_t q[16];
+    pack32(v, q, fmt);
+    const uint4 mine[4] = {make_uint4(q[0], q[1], q[2], q[3]), make_uint4(q[4], q[5], q[6], q[7]), make_uint4(q[8], q[9], q[10], q[11]),
+                           make_uint4(q[12], q[13], q[14], q[15])};
+    put_rows(buf, mine, base, pitch, rows);
+}
+
+// Columns [col, col + 32), col < N, of a warp's 32 rows from row0 < M on, a row per lane.
+__device__ __forceinline__ void store_out(const OutArgs& o, uint4* buf, int split, int64_t row0, int64_t col, int64_t M, int64_t N, float (&v)[32],
                                           float s1, float s2) {
+    const int lane = threadIdx.x & 31;
+    const int64_t rows = M - row0;
     if (o.out) {
 #pragma unroll
         for (int j = 0; j < 32; ++j) v[j] = v[j] * s1 * s2;
+        const int64_t at = row0 * o.ldo + col;
         if (o.vec && col + 32 <= N) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) store_vec(o.out, row * o.ldo + col + q * 8, v + q * 8, o.type);
-        } else {
+            if (o.type == TT_F32)
+                put_rows_f32(buf, v, reinterpret_cast<uint8_t*>(static_cast<float*>(o.out) + at), o.ldo * 4, rows);
+            else
+                put_rows_16(buf, v, reinterpret_cast<uint8_t*>(static_cast<uint16_t*>(o.out) + at), o.ldo * 2, rows, o.type == TT_BF16);
+        } else if (lane < rows) {
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-                if (col + j < N) store_one(o.out, row * o.ldo + col + j, v[j], o.type);
+                if (col + j < N) store_one(o.out, at + lane * o.ldo + j, v[j], o.type);
         }
     } else {  // whole chunks: the columns past N hold zeros
-        float4* p = reinterpret_cast<float4*>(o.partial + ((int64_t)split * M + row) * o.pp + col);
+        float* p = o.partial + ((int64_t)split * M + row0) * o.pp + col;
+        if (o.accumulate && lane < rows) {
+            const float4* y4 = reinterpret_cast<const float4*>(p + lane * o.pp);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-            float4 x = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-            if (o.accumulate) {
-                const float4 y = p[q];
-                x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+            for (int q = 0; q < 8; ++q) {
+                const float4 y = y4[q];
+                v[4 * q] += y.x;
+                v[4 * q + 1] += y.y;
+                v[4 * q + 2] += y.z;
+                v[4 * q + 3] += y.w;
             }
-            p[q] = x;
         }
+        put_rows_f32(buf, v, reinterpret_cast<uint8_t*>(p), o.pp * 4, rows);
     }
 }
 

@@ -125,6 +125,7 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
         int wexp[4];  // the first: scale of the tile's table rows
     };
     __shared__ __align__(16) Ahead ahead[S::kDzWarps][2];
+    __shared__ uint4 rows_out[MODE == kLse ? 1 : 8][128];  // put_rows of the warps that store OUT
     __shared__ uint32_t tmem_slot;
     __shared__ int gave_up_s;
     volatile int* gave_up = &gave_up_s;
@@ -432,16 +433,13 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
             const int64_t row = (int64_t)w.x * 128 + quad * 32 + lane;
             const uint32_t l0 = tmem + ((uint32_t)(quad * 32) << 16) + S::kOutCol + half * (DT / 2);
             const bool whole = w.y0 == 0 && w.y1 == a.runs.ytiles;
-            float* part = a.partial + (((int64_t)blockIdx.x * 2 + !first) * 128 + quad * 32 + lane) * a.to.pp;
+            float* part = a.partial + (((int64_t)blockIdx.x * 2 + !first) * 128 + quad * 32) * a.to.pp;
             auto put = [&](float(&v)[32], int col) {
-                if (row >= a.X || col >= a.D) return;
-                if (whole) {
-                    store_out(a.to, 0, row, col, a.X, a.D, v, s1, s2);
-                } else {
-                    float4* p = reinterpret_cast<float4*>(part + col);
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) p[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-                }
+                if (row - lane >= a.X || col >= a.D) return;
+                if (whole)
+                    store_out(a.to, rows_out[warp - 4], 0, row - lane, col, a.X, a.D, v, s1, s2);
+                else
+                    put_rows_f32(rows_out[warp - 4], v, reinterpret_cast<uint8_t*>(part + col), a.to.pp * 4, 32);
             };
             if (SPLIT) {
                 float sum[OC][32];

@@ -28,7 +28,10 @@ struct GemmArgs {
     const uint32_t* amax_a;
     const uint32_t* amax_b;
     const int* row_exp;  // per-row exponent of A (forward), else null
-    const int* wexp;     // SPLIT: exponent per 128 table rows: of B's rows (scores), along K (dhidden), else null
+    // SPLIT: exponents of the table's 128 x 128 blocks, kb to a row of blocks: scores: B's
+    // rows by K; dhidden: K by columns; dweight: null
+    const int* wexp;
+    int kb;
     float ctemp;         // log2(e) / T
     // kEpiStats
     float2* part;        // [M][nstrips][kParts] (maximum in log2 units, sum)
@@ -46,7 +49,9 @@ struct GemmShape {
     static constexpr int kStages = BN == 256 ? 4 : (BN == 128 ? 6 : 8);
     static constexpr uint32_t kA = 128 * 128, kB = BN * 128;
     static constexpr uint32_t kStage = kA + kB;
-    static constexpr size_t kSmem = (size_t)kStages * kStage + 1024;
+    static constexpr uint32_t kRing = kStages * kStage;                     // then 2 KB per epilogue warp (put_rows)
+    static constexpr size_t kSmem = (size_t)kRing + kEpiWarps * 2048 + 1024;
+    static_assert(kSmem + 512 <= 227 * 1024, "shared memory");
 };
 
 // C[m, n] = sum_k A[m, k] B[n, k] by 128 x BN tiles, a persistent block per SM: one
@@ -184,6 +189,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     } else if (warp >= 4) {
         const int part = (warp - 4) >> 2, quad = warp & 3;
         const int r = quad * 32 + lane;
+        uint4* const buf = reinterpret_cast<uint4*>(raw + (base - smem_addr(raw)) + S::kRing + (warp - 4) * 2048);
         float c = 0.f, s1 = 1.f, s2 = 1.f;
         if (EPI == kEpiOut) {
             s1 = exp2i(-amax_exp(a.amax_a));
@@ -196,45 +202,30 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             unit(u, m, n0, n1, kb, ke, split);
             const int64_t row = (int64_t)m * 128 + r;
             const bool in = row < a.M;
-            float run_m = -INFINITY, run_s = 0.f, cr = c, cu = c;  // run_m in units of cr
+            float run_m = -INFINITY, run_s = 0.f, cr = c;
             float2 rc = make_float2(0.f, 0.f);
-            if (EPI == kEpiStats && a.row_exp && in) cu = cr = c * exp2i(-a.row_exp[row]);
+            if (EPI == kEpiStats && a.row_exp && in) cr = c * exp2i(-a.row_exp[row]);
             if (EPI == kEpiDz && in) rc = make_float2(a.nlse[row], a.scale[row]);
             for (int n = n0; ok && n < n1; ++n) {
                 const int64_t col0 = (int64_t)n * BN + part * (BN / kParts);
-                if (SPLIT && EPI != kEpiOut) {  // the tile's scale; the maximum so far in its units
-                    const float next = cu * exp2i(-__ldg(&a.wexp[n]));
-                    if (EPI == kEpiStats && n != n0) run_m *= cr / next;  // powers of two apart
-                    cr = next;
-                }
                 // 32 finished columns of this thread's row, the first of them `col`
                 auto finish = [&](float (&v)[32], int64_t col) {
                     if (EPI == kEpiStats) {
                         take_scores(v, a.N - col, cr, run_m, run_s);
                     } else if (EPI == kEpiDz) {
-                        if (in && col < a.dz_pitch) {
+                        if (col < a.dz_pitch && row - lane < a.M) {
 #pragma unroll
                             for (int j = 0; j < 32; ++j) v[j] = rc.y == 0.f ? 0.f : rc.y * ex2(fmaf(v[j], cr, rc.x));
-                            uint4* o = reinterpret_cast<uint4*>(a.dz + row * a.dz_pitch + col);
+                            uint16_t* to = a.dz + (row - lane) * a.dz_pitch + col;
+                            put_rows_16(buf, v, reinterpret_cast<uint8_t*>(to), a.dz_pitch * 2, a.M - (row - lane), SPLIT ? 0 : a.fmt);
+                            if (SPLIT) {
 #pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                uint32_t w[4];
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) w[i] = pack16(v[q * 8 + 2 * i], v[q * 8 + 2 * i + 1], a.fmt);
-                                o[q] = make_uint4(w[0], w[1], w[2], w[3]);
-                                if (SPLIT) {
-#pragma unroll
-                                    for (int i = 0; i < 4; ++i) {
-                                        const float2 h = unpack_f16(w[i]);
-                                        w[i] = pack16(v[q * 8 + 2 * i] - h.x, v[q * 8 + 2 * i + 1] - h.y, 0);
-                                    }
-                                    *(reinterpret_cast<uint4*>(a.dz + a.dz_piece + row * a.dz_pitch + col) + q) =
-                                        make_uint4(w[0], w[1], w[2], w[3]);
-                                }
+                                for (int j = 0; j < 32; ++j) v[j] -= __half2float(__float2half_rn(v[j]));
+                                put_rows_16(buf, v, reinterpret_cast<uint8_t*>(to + a.dz_piece), a.dz_pitch * 2, a.M - (row - lane), 0);
                             }
                         }
-                    } else if (in && col < a.N) {
-                        store_out(a.to, split, row, col, a.M, a.N, v, s1, s2);
+                    } else if (col < a.N && row - lane < a.M) {
+                        store_out(a.to, buf, split, row - lane, col, a.M, a.N, v, s1, s2);
                     }
                 };
                 if (SPLIT) {
@@ -245,7 +236,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                         if (!ok) break;
                         tc_fence_after();
                         const uint32_t t0 = tmem + buf * BN + ((uint32_t)(quad * 32) << 16) + part * (BN / kParts);
-                        const float f = EPI == kEpiOut && a.wexp ? exp2i(-__ldg(&a.wexp[r0 / kRange])) : 1.f;
+                        const float f = a.wexp ? exp2i(-__ldg(&a.wexp[EPI == kEpiOut ? (int64_t)(r0 / kRange) * a.kb + n : (int64_t)n * a.kb + r0 / kRange])) : 1.f;
 #pragma unroll
                         for (int ch = 0; ch < kCh; ++ch) {
                             float v[32];
