@@ -25,7 +25,7 @@
 // elements of the table, of all hidden rows that count and of all of dz in the backward pass) and a product is taken as hi hi + hi lo + lo hi,
 // so 22 bits of each operand enter, with fp32 accumulation; lo lo (2^-22 of the
 // product and below) is dropped.  dz is rounded to the inputs' 16-bit type before
-// the two gradient products (relative 2^-9 or 2^-12 an entry, independent errors,
+// the two gradient products (by at most 2^-8 or 2^-11 of an entry, independent errors,
 // the size of the gradients' own final rounding), and split like an input for fp32.
 #include <math.h>
 
@@ -510,13 +510,13 @@ __global__ void __launch_bounds__(TH, 1024 / TH) k_head_prep(const __grid_consta
 // out[m, n] = the splits' partial sums, in split order, unscaled and rounded once.
 __global__ void __launch_bounds__(256) k_head_reduce(const float* partial, int splits, int64_t M, int64_t N, int64_t pp, void* out,
                                                      int64_t ldo, int type, const uint32_t* amax_a, const uint32_t* amax_b) {
-    const float s1 = exp2i(-amax_exp(amax_a)), s2 = exp2i(-amax_exp(amax_b));
+    const Pow2 sc(-amax_exp(amax_a) - amax_exp(amax_b));
     const int64_t total = M * N;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
         const int64_t m = i / N, n = i - m * N;
         float s = 0.f;
         for (int k = 0; k < splits; ++k) s += partial[((int64_t)k * M + m) * pp + n];
-        store_one(out, m * ldo + n, s * s1 * s2, type);
+        store_one(out, m * ldo + n, sc(s), type);
     }
 }
 
@@ -629,7 +629,8 @@ bool run_fused(const Operand& X, const Operand& Y, FusedArgs a, int dev, cudaStr
     const bool by_boundary = a.runs.xtiles >= a.runs.blocks;
     const unsigned gx = (unsigned)(by_boundary ? a.runs.blocks - 1 : a.runs.xtiles);
     const unsigned gy = gx >= 256 ? 1 : (gx >= 64 ? 4 : (gx >= 16 ? 16 : 64));  // a block or more per SM
-    k_head_join<<<dim3(gx, gy), 128, 0, st>>>(a.runs, by_boundary, a.partial, a.to, a.X, a.D, a.amax_z, MODE == kDweight ? a.amax_h : nullptr);
+    k_head_join<<<dim3(gx, gy), 128, 0, st>>>(a.runs, by_boundary, a.partial, a.to, a.X, a.D, SPLIT && MODE == kDhidden ? nullptr : a.amax_z,
+                                              MODE == kDweight ? a.amax_h : nullptr);
     return cudaGetLastError() == cudaSuccess;
 }
 
@@ -695,7 +696,8 @@ struct Plan {
 
 bool aligned_rows(const void* p, int64_t ld, int esize) { return ((uintptr_t)p % 16 == 0) && (ld * esize % 16 == 0); }
 
-tt_status make_plan(const tt_head* hd, int K, Plan* p) {
+// buffers: whether the call's buffers are all there; host checks come before any CUDA call
+tt_status make_plan(const tt_head* hd, int K, bool buffers, Plan* p) {
     if (!hd) return TT_ERR_ARG;
     if (hd->dtype != TT_F32 && hd->dtype != TT_BF16 && hd->dtype != TT_F16) return TT_ERR_ARG;
     if (hd->rows < 0 || hd->dim < 1 || hd->vocab < 1 || K < 1 || K > kMaxTeacher) return TT_ERR_SHAPE;
@@ -706,9 +708,10 @@ tt_status make_plan(const tt_head* hd, int K, Plan* p) {
     p->fmt = hd->dtype == TT_BF16;
     p->split = hd->dtype == TT_F32;
     p->esize = hd->dtype == TT_F32 ? 4 : 2;
+    if (((uintptr_t)hd->hidden_dev | (uintptr_t)hd->weight_dev) % p->esize) return TT_ERR_ARG;
+    if (!buffers) return TT_ERR_ARG;
     p->sms = head_sms(&p->device);
     if (p->sms <= 0) return TT_ERR_CUDA;
-    if (((uintptr_t)hd->hidden_dev | (uintptr_t)hd->weight_dev) % p->esize) return TT_ERR_ARG;
     HeadIn& in = p->in;
     in.h = hd->hidden_dev;
     in.w = hd->weight_dev;
@@ -1003,7 +1006,9 @@ tt_status head_backward(const Plan& p, const Target& t, const float* lse, const 
         return o;
     };
     const auto reduce = [&](const float* partial, int splits, int64_t rows, void* out, const uint32_t* ay) {
-        k_head_reduce<<<grid_of(rows * in.D, 256, p.sms, 8), 256, 0, st>>>(partial, splits, rows, in.D, p.pp, out, in.D, p.type, az, ay);
+        // fp32's are in their own units already
+        k_head_reduce<<<grid_of(rows * in.D, 256, p.sms, 8), 256, 0, st>>>(partial, splits, rows, in.D, p.pp, out, in.D, p.type, p.split ? nullptr : az,
+                                                                           p.split ? nullptr : ay);
         return launch_ok();
     };
     if (p.fused) {
@@ -1083,10 +1088,9 @@ tt_status head_backward(const Plan& p, const Target& t, const float* lse, const 
 
 tt_status forward_any(const tt_head* hd, const Target& t, float* loss, float* lse, int* err, void* ws, size_t n, tt_stream s) {
     Plan p;
-    const tt_status st = make_plan(hd, t.K, &p);
+    const bool buffers = hd && (hd->rows == 0 || (hd->hidden_dev && t.ids && loss && lse)) && hd->weight_dev && ws && (uintptr_t)ws % 256 == 0;
+    const tt_status st = make_plan(hd, t.K, buffers, &p);
     if (st != TT_OK) return st;
-    if (hd->rows > 0 && (!hd->hidden_dev || !t.ids || !loss || !lse)) return TT_ERR_ARG;
-    if (!hd->weight_dev || !ws || (uintptr_t)ws % 256) return TT_ERR_ARG;
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(s);
     if (p.type == TT_F32) return head_forward<float>(p, t, loss, lse, err, ws, n, cs);
     if (p.type == TT_BF16) return head_forward<__nv_bfloat16>(p, t, loss, lse, err, ws, n, cs);
@@ -1096,11 +1100,10 @@ tt_status forward_any(const tt_head* hd, const Target& t, float* loss, float* ls
 tt_status backward_any(const tt_head* hd, const Target& t, const float* lse, const float* grad, void* dh, void* dw, int* err, void* ws,
                        size_t n, tt_stream s) {
     Plan p;
-    const tt_status st = make_plan(hd, t.K, &p);
+    const bool buffers = hd && (hd->rows == 0 || (hd->hidden_dev && t.ids && lse && grad && dh)) && hd->weight_dev && dw && ws &&
+                         (uintptr_t)ws % 256 == 0 && ((uintptr_t)dh | (uintptr_t)dw) % (hd->dtype == TT_F32 ? 4 : 2) == 0;
+    const tt_status st = make_plan(hd, t.K, buffers, &p);
     if (st != TT_OK) return st;
-    if (hd->rows > 0 && (!hd->hidden_dev || !t.ids || !lse || !grad || !dh)) return TT_ERR_ARG;
-    if (!hd->weight_dev || !dw || !ws || (uintptr_t)ws % 256) return TT_ERR_ARG;
-    if (((uintptr_t)dh | (uintptr_t)dw) % p.esize) return TT_ERR_ARG;
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(s);
     if (p.type == TT_F32) return head_backward<float>(p, t, lse, grad, dh, dw, err, ws, n, cs);
     if (p.type == TT_BF16) return head_backward<__nv_bfloat16>(p, t, lse, grad, dh, dw, err, ws, n, cs);
@@ -1118,7 +1121,7 @@ extern "C" {
 
 int64_t tt_emb_head_workspace(const tt_head* head, int32_t teacher_k, int32_t backward) {
     Plan p;
-    if (make_plan(head, teacher_k, &p) != TT_OK) return -1;
+    if (make_plan(head, teacher_k, true, &p) != TT_OK) return -1;
     if (backward) {
         BwdWs w;
         return (int64_t)bwd_ws(p, teacher_k, nullptr, &w);

@@ -33,12 +33,24 @@ __device__ __forceinline__ bool mbar_try(uint64_t* bar, uint32_t parity) {
     return ok != 0;
 }
 
+// The same without the moment's suspension that try_wait allows itself.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 // A warp's wait for the phase of the given parity, for at most `ns` nanoseconds (counted
 // as two SM cycles each, which is a little long) or until another role of the block gave
 // up; false if the phase did not complete.  The answer is the same in every lane, and
 // known to the compiler to be so: what the TMA and MMA warps compute between waits
 // stays in uniform registers, where the tensor instructions take their operands from.
 __device__ __forceinline__ bool head_wait(uint64_t* bar, uint32_t parity, uint64_t ns, volatile int* gave_up) {
+    if (ns == 0) return __all_sync(0xffffffffu, mbar_test(bar, parity));
     if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return true;
     const int64_t t0 = clock64();
     while (!__all_sync(0xffffffffu, mbar_try(bar, parity))) {
@@ -254,17 +266,21 @@ __device__ __forceinline__ void pack32(const float (&p)[32], uint32_t (&q)[16], 
 }
 __device__ __forceinline__ float2 unpack_f16(uint32_t v) { return __half22float2(*reinterpret_cast<__half2*>(&v)); }
 
-// Power of two that brings a tensor whose largest magnitude has these fp32 bits
-// just below 2^14 (the largest f16 is 65,504).  An all-zero tensor and one that
-// holds an infinity or a NaN are left alone.  |exponent| <= 60, so the product of
-// two such factors is a normal fp32 number.
+// Exponent of the power of two that brings a tensor whose largest finite magnitude has
+// these fp32 bits just below 2^14 (the largest f16 is 65,504); 0 for an all-zero one.
 __device__ __forceinline__ int scale_exp(uint32_t absmax_bits) {
     if (absmax_bits == 0 || absmax_bits >= 0x7F800000u) return 0;
-    const int e = 13 - ((int)(absmax_bits >> 23) - 127);
-    return e < -60 ? -60 : (e > 60 ? 60 : e);
+    return min(13 - ((int)(absmax_bits >> 23) - 127), 126);
 }
 __device__ __forceinline__ float exp2i(int e) { return __int_as_float((e + 127) << 23); }
-
+// The same for any e, held within fp32's normal range.
+__device__ __forceinline__ float exp2c(int e) { return exp2i(max(-126, min(127, e))); }
+// 2^e as a product, which undoes two scales of any size: b is 1 unless a alone falls short.
+struct Pow2 {
+    float a, b;
+    __device__ __forceinline__ explicit Pow2(int e) : a(exp2c(e)), b(exp2c(e - max(-126, min(127, e)))) {}
+    __device__ __forceinline__ float operator()(float x) const { return x * b * a; }
+};
 __device__ __forceinline__ int amax_exp(const uint32_t* p) { return p ? scale_exp(*p) : 0; }
 
 // How the fused kernels share their work: the tiles (x, y), all y of one x before the
@@ -336,12 +352,12 @@ __device__ __forceinline__ void put_rows_16(uint4* buf, const float (&v)[32], ui
 
 // Columns [col, col + 32), col < N, of a warp's 32 rows from row0 < M on, a row per lane.
 __device__ __forceinline__ void store_out(const OutArgs& o, uint4* buf, int split, int64_t row0, int64_t col, int64_t M, int64_t N, float (&v)[32],
-                                          float s1, float s2) {
+                                          Pow2 sc) {
     const int lane = threadIdx.x & 31;
     const int64_t rows = M - row0;
     if (o.out) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = v[j] * s1 * s2;
+        for (int j = 0; j < 32; ++j) v[j] = sc(v[j]);
         const int64_t at = row0 * o.ldo + col;
         if (o.vec && col + 32 <= N) {
             if (o.type == TT_F32)

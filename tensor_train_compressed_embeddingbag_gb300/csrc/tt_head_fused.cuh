@@ -282,19 +282,19 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
         }
     } else if (MODE == kLse && warp >= 12) {
         const int set = (warp - 12) / S::kDzSet, quad = warp & 3, part = (warp - 12) % S::kDzSet >> 2;  // its 32 rows and 64 columns
-        float cr = a.ctemp, c = cr, run_m = -INFINITY, run_s = 0.f;  // run_m in units of c
-        int we = 0, we_next = SPLIT && w.left ? __ldg(&a.wexp[w.y / (128 / BY)]) : 0;
+        float c = a.ctemp, run_m = -INFINITY, run_s = 0.f;  // run_m in units of c
+        int he = 0, we = 0, we_next = SPLIT && w.left ? __ldg(&a.wexp[w.y / (128 / BY)]) : 0;
         for (; w.left; ++g) {
             const int64_t row = (int64_t)w.x * 128 + quad * 32 + lane;
             if (w.y == w.y0) {
                 run_m = -INFINITY;
                 run_s = 0.f;
-                if (SPLIT) cr = row < a.X ? a.ctemp * exp2i(-__ldg(&a.row_exp[row])) : a.ctemp;
+                if (SPLIT) he = row < a.X ? __ldg(&a.row_exp[row]) : 0;
             }
             if (SPLIT) {  // the tile's scale; the maximum so far in its units (a power of two between them)
-                if (w.y != w.y0) run_m *= exp2i(we_next - we);
+                if (w.y != w.y0) run_m *= exp2c(we_next - we);
                 we = we_next;
-                c = cr * exp2i(-we);
+                c = fmaxf(a.ctemp * exp2c(-he - we), 1e-37f);  // never 0: -inf stays -inf
             }
             if ((g & 1) == set) {
                 const uint32_t sb = g % NS;
@@ -323,7 +323,7 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
         }
     } else if (MODE != kLse && warp >= 12) {
         const int set = (warp - 12) / S::kDzSet, quad = warp & 3, part = (warp - 12) % S::kDzSet >> 2;  // its 32 rows and 64 columns
-        const float c0 = a.ctemp * exp2i(-amax_exp(a.amax_h));
+        const int he = amax_exp(a.amax_h);
         // fetched while the warp works on the tile before; by asynchronous copies, which
         // hold no registers meanwhile
         auto fetch = [&](const Walk& t, Ahead& to) {
@@ -353,7 +353,7 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
             step(w);
             if (w.left) step(w);
             fetch(w, ahead[warp - 12][now ^ 1]);
-            const float c = SPLIT ? c0 * exp2i(-my.wexp[0]) : c0;
+            const float c = SPLIT ? a.ctemp * exp2c(-he - my.wexp[0]) : a.ctemp;
             ok = head_wait(&sfull[g % S::kStages], (g / S::kStages) & 1, a.wait_ns, gave_up);
             if (!ok) break;
             tc_fence_after();
@@ -425,7 +425,8 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
         }
     } else if (MODE != kLse && warp >= 4) {
         const int half = warp >= 8, quad = warp & 3;
-        const float s1 = exp2i(-amax_exp(a.amax_z)), s2 = COLS ? exp2i(-amax_exp(a.amax_h)) : 1.f;
+        const int ez = amax_exp(a.amax_z) + (COLS ? amax_exp(a.amax_h) : 0);
+        const Pow2 sc(SPLIT && !COLS ? 0 : -ez);  // SPLIT dhidden: freed of its scales tile by tile
         constexpr int OC = DT / 64;  // 32-column chunks of this warp's half
         uint32_t fl = 0;
         bool first = true;
@@ -437,7 +438,7 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
             auto put = [&](float(&v)[32], int col) {
                 if (row - lane >= a.X || col >= a.D) return;
                 if (whole)
-                    store_out(a.to, rows_out[warp - 4], 0, row - lane, col, a.X, a.D, v, s1, s2);
+                    store_out(a.to, rows_out[warp - 4], 0, row - lane, col, a.X, a.D, v, sc);
                 else
                     put_rows_f32(rows_out[warp - 4], v, reinterpret_cast<uint8_t*>(part + col), a.to.pp * 4, 32);
             };
@@ -449,7 +450,7 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
                     for (int j = 0; j < 32; ++j) sum[ch][j] = 0.f;
                 for (int f = w.y0; f < w.y1; ++f, ++fl) {
                     const uint32_t ob = fl % OB;
-                    const float f1 = COLS ? 1.f : exp2i(-__ldg(&a.wexp[f / (128 / BY)]));
+                    const Pow2 f1(COLS ? 0 : -ez - __ldg(&a.wexp[f / (128 / BY)]));
                     ok = head_wait(&ofull[ob], (fl / OB) & 1, a.wait_ns, gave_up);
                     if (!ok) break;
                     tc_fence_after();
@@ -461,11 +462,12 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
                             tm_read16(l0 + ob * S::kOut + part * DT + ch * 16, v);
 #pragma unroll
                             for (int j = 0; j < 16; j += 2) {
+                                if (!COLS && f1.b != 1.f) mul2(v[j], v[j + 1], f1.b, f1.b);
                                 float &x = sum[ch / 2][(ch & 1) * 16 + j], &y = sum[ch / 2][(ch & 1) * 16 + j + 1];
                                 if (COLS)
                                     add2(x, y, v[j], v[j + 1]);
                                 else
-                                    axpy2(x, y, v[j], v[j + 1], f1);  // exact product: f1 is a power of two
+                                    axpy2(x, y, v[j], v[j + 1], f1.a);  // exact products with powers of two
                             }
                         }
                     }
@@ -558,7 +560,7 @@ __global__ void __launch_bounds__(128) k_head_join(Runs runs, int by_boundary, c
     const int more = sh[2], per_row = (int)to.pp / 4, rows = 128 / per_row, span = 128 / gridDim.y;
     const int c = (int)threadIdx.x % per_row * 4, r0 = (int)threadIdx.x / per_row;
     if (r0 >= rows || c >= D) return;
-    const float s1 = exp2i(-amax_exp(amax_z)), s2 = exp2i(-amax_exp(amax_y));
+    const Pow2 sc(-amax_exp(amax_z) - amax_exp(amax_y));
     const int64_t step = 256 * to.pp;
     for (int i = r0; i < span; i += rows) {
         const int r = blockIdx.y * span + i;
@@ -573,7 +575,7 @@ __global__ void __launch_bounds__(128) k_head_join(Runs runs, int by_boundary, c
         const float v[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            if (c + j < D) store_one(to.out, (x * 128 + r) * to.ldo + c + j, v[j] * s1 * s2, to.type);
+            if (c + j < D) store_one(to.out, (x * 128 + r) * to.ldo + c + j, sc(v[j]), to.type);
     }
 }
 

@@ -190,32 +190,29 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         const int part = (warp - 4) >> 2, quad = warp & 3;
         const int r = quad * 32 + lane;
         uint4* const buf = reinterpret_cast<uint4*>(raw + (base - smem_addr(raw)) + S::kRing + (warp - 4) * 2048);
-        float c = 0.f, s1 = 1.f, s2 = 1.f;
-        if (EPI == kEpiOut) {
-            s1 = exp2i(-amax_exp(a.amax_a));
-            s2 = exp2i(-amax_exp(a.amax_b));
-        } else {
-            c = a.ctemp * exp2i(-amax_exp(a.amax_a)) * exp2i(-amax_exp(a.amax_b));
-        }
+        const int e = amax_exp(a.amax_a) + amax_exp(a.amax_b);
+        const float c = a.ctemp;
+        const Pow2 sc(SPLIT ? 0 : -e);
         for (int64_t u = blockIdx.x; ok && u < a.units; u += gridDim.x) {
             int m, n0, n1, kb, ke, split;
             unit(u, m, n0, n1, kb, ke, split);
             const int64_t row = (int64_t)m * 128 + r;
             const bool in = row < a.M;
-            float run_m = -INFINITY, run_s = 0.f, cr = c;
+            float run_m = -INFINITY, run_s = 0.f;
+            int er = e;  // SPLIT: the scales that the row's sums are freed of
             float2 rc = make_float2(0.f, 0.f);
-            if (EPI == kEpiStats && a.row_exp && in) cr = c * exp2i(-a.row_exp[row]);
+            if (SPLIT && EPI == kEpiStats && in) er = a.row_exp[row];
             if (EPI == kEpiDz && in) rc = make_float2(a.nlse[row], a.scale[row]);
             for (int n = n0; ok && n < n1; ++n) {
                 const int64_t col0 = (int64_t)n * BN + part * (BN / kParts);
                 // 32 finished columns of this thread's row, the first of them `col`
                 auto finish = [&](float (&v)[32], int64_t col) {
                     if (EPI == kEpiStats) {
-                        take_scores(v, a.N - col, cr, run_m, run_s);
+                        take_scores(v, a.N - col, c, run_m, run_s);
                     } else if (EPI == kEpiDz) {
                         if (col < a.dz_pitch && row - lane < a.M) {
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) v[j] = rc.y == 0.f ? 0.f : rc.y * ex2(fmaf(v[j], cr, rc.x));
+                            for (int j = 0; j < 32; ++j) v[j] = rc.y == 0.f ? 0.f : rc.y * ex2(fmaf(v[j], c, rc.x));
                             uint16_t* to = a.dz + (row - lane) * a.dz_pitch + col;
                             put_rows_16(buf, v, reinterpret_cast<uint8_t*>(to), a.dz_pitch * 2, a.M - (row - lane), SPLIT ? 0 : a.fmt);
                             if (SPLIT) {
@@ -225,7 +222,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                             }
                         }
                     } else if (col < a.N && row - lane < a.M) {
-                        store_out(a.to, buf, split, row - lane, col, a.M, a.N, v, s1, s2);
+                        store_out(a.to, buf, split, row - lane, col, a.M, a.N, v, sc);
                     }
                 };
                 if (SPLIT) {
@@ -236,14 +233,17 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                         if (!ok) break;
                         tc_fence_after();
                         const uint32_t t0 = tmem + buf * BN + ((uint32_t)(quad * 32) << 16) + part * (BN / kParts);
-                        const float f = a.wexp ? exp2i(-__ldg(&a.wexp[EPI == kEpiOut ? (int64_t)(r0 / kRange) * a.kb + n : (int64_t)n * a.kb + r0 / kRange])) : 1.f;
+                        const int we = a.wexp ? __ldg(&a.wexp[EPI == kEpiOut ? (int64_t)(r0 / kRange) * a.kb + n : (int64_t)n * a.kb + r0 / kRange]) : 0;
+                        const Pow2 f(-er - we);
 #pragma unroll
                         for (int ch = 0; ch < kCh; ++ch) {
                             float v[32];
                             tm_ld32(t0 + ch * 32, v);
                             tm_wait_ld(v);
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) sum[ch][j] = r0 == kb ? v[j] * f : fmaf(v[j], f, sum[ch][j]);
+                            for (int j = 0; j < 32; ++j) v[j] *= f.b;
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) sum[ch][j] = r0 == kb ? v[j] * f.a : fmaf(v[j], f.a, sum[ch][j]);
                         }
                         tc_fence_before();
                         __syncwarp();
@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             }
             if (EPI == kEpiStats && ok && in)
                 a.part[(row * a.nstrips + split) * kParts + part] =
-                    make_float2(run_m == -INFINITY ? -INFINITY : run_m * cr, run_s);
+                    make_float2(run_m == -INFINITY ? -INFINITY : run_m * c, run_s);
         }
     }
     if (!ok && lead) {
