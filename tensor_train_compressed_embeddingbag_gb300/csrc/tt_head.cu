@@ -89,7 +89,7 @@ __device__ __forceinline__ float warp_dot(const T* x, const T* y, int D, int vec
             for (int j = 0; j < E; ++j) s[j & 3] = fmaf(to_f32(pa[j]), to_f32(pb[j]), s[j & 3]);
         }
     } else {
-#pragma unroll 4
+#pragma unroll 16
         for (int i = lane; i < D; i += 32) s[0] = fmaf(to_f32(x[i]), to_f32(y[i]), s[0]);
     }
     float t = (s[0] + s[1]) + (s[2] + s[3]);
@@ -123,17 +123,19 @@ __device__ __forceinline__ float join_parts(const float2* p, int n, int lane) {
     return (b + log2f(s)) * kLn2;
 }
 
-constexpr int kRowThreads = 128;
+constexpr int kRowThreads = 128;  // per row or four rows; wide: per row, when rows are few and have many entries
+constexpr int kRowThreadsWide = 512;
 constexpr int kAmaxShares = 64;  // blocks that look for the largest magnitudes
 
-// The teacher's distribution of one row, a block per row: q[k] and log q[k] in
+// The teacher's distribution of one row, a block per row (red: two floats per warp): q[k] and log q[k] in
 // shared memory, ids as int (-1: not counted).  An id below 0 marks an entry that
 // does not count, whatever its logit holds; one past the table is recorded and does
 // not count either; so does an entry whose logit is -inf.  Returns whether any counts.
+template <int RT>
 __device__ bool teacher_row(const Target& t, int64_t n, int64_t V, float* q, float* logq, int* ids, float* red, int* err) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     float mx = -INFINITY;
-    for (int k = tid; k < t.K; k += kRowThreads) {
+    for (int k = tid; k < t.K; k += RT) {
         const int64_t id = t.ids[n * t.K + k];
         float x = -INFINITY;
         int got = -1;
@@ -152,17 +154,18 @@ __device__ bool teacher_row(const Target& t, int64_t n, int64_t V, float* q, flo
     mx = warp_max(mx);
     if (lane == 0) red[warp] = mx;
     __syncthreads();
-    mx = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+    for (int i = 0; i < RT / 32; ++i) mx = fmaxf(mx, red[i]);
     if (nan) mx = NAN;
     float s = 0.f;
-    for (int k = tid; k < t.K; k += kRowThreads)
+    for (int k = tid; k < t.K; k += RT)
         if (ids[k] >= 0) s += expf((logq[k] - mx) / t.T);
     s = warp_sum(s);
-    if (lane == 0) red[4 + warp] = s;
+    if (lane == 0) red[RT / 32 + warp] = s;
     const bool any = __syncthreads_or(mx != -INFINITY);
-    s = (red[4] + red[5]) + (red[6] + red[7]);
+    s = 0.f;
+    for (int i = 0; i < RT / 32; ++i) s += red[RT / 32 + i];
     const float ls = logf(s), inv = 1.f / s;
-    for (int k = tid; k < t.K; k += kRowThreads) {
+    for (int k = tid; k < t.K; k += RT) {
         const float d = (logq[k] - mx) / t.T;
         q[k] = ids[k] >= 0 ? expf(d) * inv : 0.f;
         logq[k] = ids[k] >= 0 ? d - ls : 0.f;
@@ -173,8 +176,8 @@ __device__ bool teacher_row(const Target& t, int64_t n, int64_t V, float* q, flo
 
 // lse and loss of every row: the strips' pairs joined, the target scores as dot
 // products.  xent: a warp per row; distill: a block per row, a warp per entry.
-template <class T, bool DISTILL>
-__global__ void __launch_bounds__(kRowThreads) k_head_finish(HeadIn in, Target t, const float2* part, int slots, int per_slot, Runs runs,
+template <class T, bool DISTILL, int RT>
+__global__ void __launch_bounds__(RT) k_head_finish(HeadIn in, Target t, const float2* part, int slots, int per_slot, Runs runs,
                                                              float* loss, float* lse, int* err) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const T* h = static_cast<const T*>(in.h);
@@ -184,7 +187,7 @@ __global__ void __launch_bounds__(kRowThreads) k_head_finish(HeadIn in, Target t
         return join_parts(part + n * slots * per_slot, used * per_slot, lane);
     };
     if (!DISTILL) {
-        const int64_t n = (int64_t)blockIdx.x * 4 + warp;
+        const int64_t n = (int64_t)blockIdx.x * (RT / 32) + warp;
         if (n >= in.N) return;
         const int64_t id = xent_id(t, n, in.V, lane == 0 ? err : nullptr);
         const float z = id >= 0 ? warp_dot(h + n * in.ldh, w + id * in.ldw, in.D, in.vec, lane) : 0.f;
@@ -198,10 +201,10 @@ __global__ void __launch_bounds__(kRowThreads) k_head_finish(HeadIn in, Target t
         float* q = sm;
         float* lq = sm + t.K;
         int* ids = reinterpret_cast<int*>(sm + 2 * t.K);
-        __shared__ float red[8];
+        __shared__ float red[RT / 16];
         __shared__ float ls;
         const int64_t n = blockIdx.x;
-        const bool any = teacher_row(t, n, in.V, q, lq, ids, red, err);
+        const bool any = teacher_row<RT>(t, n, in.V, q, lq, ids, red, err);
         if (warp == 0) {
             const float l = row_lse(n);
             if (lane == 0) ls = l;
@@ -209,7 +212,7 @@ __global__ void __launch_bounds__(kRowThreads) k_head_finish(HeadIn in, Target t
         __syncthreads();
         const float l = ls;
         float acc = 0.f;
-        for (int k = warp; k < t.K; k += 4) {
+        for (int k = warp; k < t.K; k += RT / 32) {
             if (q[k] == 0.f) continue;
             const float z = warp_dot(h + n * in.ldh, w + (int64_t)ids[k] * in.ldw, in.D, in.vec, lane);
             acc += q[k] * (lq[k] - z / t.T + l);
@@ -219,7 +222,9 @@ __global__ void __launch_bounds__(kRowThreads) k_head_finish(HeadIn in, Target t
         __syncthreads();
         if (threadIdx.x == 0) {
             lse[n] = l;
-            loss[n] = any ? t.T * t.T * ((red[0] + red[1]) + (red[2] + red[3])) : 0.f;
+            float sum = 0.f;
+            for (int i = 0; i < RT / 32; ++i) sum += red[i];
+            loss[n] = any ? t.T * t.T * sum : 0.f;
         }
     }
 }
@@ -230,8 +235,8 @@ __global__ void __launch_bounds__(kRowThreads) k_head_finish(HeadIn in, Target t
 // holds, infinities and NaN included, reaches dweight).  Entries of one row with the
 // same id hold the same value, of their summed q.  Target entries go to an array
 // (ids_out, dzt; k_head_fix) or, ents given, to their 32 x 32 blocks (k_head_fused).
-template <class T, bool DISTILL>
-__global__ void __launch_bounds__(kRowThreads)
+template <class T, bool DISTILL, int RT>
+__global__ void __launch_bounds__(RT)
     k_head_rows(HeadIn in, Target t, const float* lse, const float* grad, const uint32_t* shares, uint32_t* amax, float* nlse, float* scale, int* ids_out,
                 float* dzt, TargetBlock* blocks, int nblocks, TargetEntry* ents, uint16_t* hp, int* err) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -241,12 +246,12 @@ __global__ void __launch_bounds__(kRowThreads)
     const float l = lse[n];
     bool any;
     extern __shared__ float sm[];
-    __shared__ float red[8];
+    __shared__ float red[RT / 16];
     float* q = sm;
     int* ids = reinterpret_cast<int*>(sm + 2 * t.K);
     int64_t xid = -1;
     if (DISTILL) {
-        any = teacher_row(t, n, in.V, q, sm + t.K, ids, red, err);
+        any = teacher_row<RT>(t, n, in.V, q, sm + t.K, ids, red, err);
     } else {
         xid = xent_id(t, n, in.V, threadIdx.x == 0 ? err : nullptr);
         any = xid >= 0;
@@ -254,9 +259,11 @@ __global__ void __launch_bounds__(kRowThreads)
     int ez = 0, eh = 0;
     if (amax) {  // the shares of the largest magnitudes joined: dz's by warps 0 and 1, hidden's by 2 and 3
         __shared__ uint32_t most[4];
-        static_assert(kRowThreads == 2 * kAmaxShares, "a share per thread");
-        const uint32_t m = __reduce_max_sync(0xffffffffu, shares[threadIdx.x]);
-        if (lane == 0) most[warp] = m;
+        static_assert(kRowThreads == 2 * kAmaxShares, "a share per thread of the first four warps");
+        if (warp < 4) {
+            const uint32_t m = __reduce_max_sync(0xffffffffu, shares[threadIdx.x]);
+            if (lane == 0) most[warp] = m;
+        }
         __syncthreads();
         const uint32_t mz = max(most[0], most[1]), mh = max(most[2], most[3]);
         ez = scale_exp(mz);
@@ -272,8 +279,8 @@ __global__ void __launch_bounds__(kRowThreads)
         scale[n] = rs;
     }
     if (n == in.N - 1)
-        for (int64_t i = in.N + threadIdx.x; i < (in.N + 127) / 128 * 128; i += kRowThreads) nlse[i] = scale[i] = 0.f;
-    for (int k = warp; k < t.K; k += 4) {
+        for (int64_t i = in.N + threadIdx.x; i < (in.N + 127) / 128 * 128; i += RT) nlse[i] = scale[i] = 0.f;
+    for (int k = warp; k < t.K; k += RT / 32) {
         const int64_t id = DISTILL ? (q[k] == 0.f ? -1 : ids[k]) : xid;
         float d = 0.f;
         bool again = false;  // an earlier entry has the same id
@@ -304,7 +311,7 @@ __global__ void __launch_bounds__(kRowThreads)
         }
     }
     const int64_t piece = in.N * in.Dp;
-    for (int i = threadIdx.x; i < in.Dp; i += kRowThreads) {
+    for (int i = threadIdx.x; i < in.Dp; i += RT) {
         const int64_t at = n * in.Dp + i;
         if (sizeof(T) == 4) {
             const float x = any && i < in.D ? to_f32(h[i]) * exp2i(eh) : 0.f;
@@ -680,7 +687,7 @@ struct Plan {
     int bn_s;                // column tile of the score products
     int strip;
     int slots, per_slot;     // (maximum, sum) pairs per row: slots of per_slot
-    bool few;                // forward: scores by k_head_few, on few_blocks blocks
+    bool few, few_wide;      // forward: scores by k_head_few, on few_blocks blocks
     int few_blocks, few_ksplit;
     size_t few_smem;
     bool fused_lse;          // scores by k_head_fused, its work shared as in
@@ -748,14 +755,15 @@ tt_status make_plan(const tt_head* hd, int K, bool buffers, Plan* p) {
         p->per_slot = 2 * (by / 64);
     }
     // few rows: a pass over the table as it is per eight of them, when its rows can be read
-    // 16 bytes at a time.  Measured against the other kernels, rows x table: bf16 4 x 131072
+    // 4 bytes at a time.  Measured against the other kernels, rows x table: bf16 4 x 131072
     // x 4096 187 us (253), 8 x 131072 x 1024 59 (71), but 8 x 10^6 x 64 55 (38), where a tile's
     // end outweighs its loads; fp32, which the others copy in pieces first, 8 x 131072 x 1024
     // 109 (434), 16 rows in two passes 218 (484), 8 x 10^6 x 64 73 (144), 16 rows 146 (144).
     const int64_t chunks = cdiv((int64_t)in.D * p->esize, 64);
     p->few_smem = (size_t)(chunks * 512);
-    p->few = in.N > 0 && in.N <= (p->split ? 16 : 8) && (p->split || in.D >= kFewMinDim) && aw && (int64_t)in.D * p->esize % 16 == 0 &&
-             p->few_smem <= kFewSmem;
+    p->few = in.N > 0 && in.N <= (p->split ? 16 : 8) && (p->split || in.D >= kFewMinDim) && (uintptr_t)in.w % 4 == 0 &&
+             in.ldw * p->esize % 4 == 0 && (int64_t)in.D * p->esize % 4 == 0 && p->few_smem <= kFewSmem;
+    p->few_wide = aw && (int64_t)in.D * p->esize % 16 == 0;
     if (p->few) {
         const int64_t tiles = cdiv(in.V, kFewRows), steps = cdiv(chunks, kFewStep);
         const int blocks = (p->few_smem <= 100 * 1024 ? 2 : 1) * p->sms;
@@ -856,6 +864,10 @@ unsigned grid_of(int64_t items, int per_block, int sms, int per_sm) {
     return (unsigned)(b < 1 ? 1 : (b > (int64_t)sms * per_sm ? (int64_t)sms * per_sm : b));
 }
 
+// 16 warps to a row instead of 4: rows whose 4 warps would leave the SMs half empty, with
+// entries enough for more (6 rows x 102 entries of width 2811: 117 -> 33 us)
+bool wide_rows(const Plan& p, int K) { return K >= 16 && p.in.N < 4ll * p.sms; }
+
 bool launch_ok() { return cudaGetLastError() == cudaSuccess; }
 
 template <class T>
@@ -885,8 +897,10 @@ constexpr int type_of() { return sizeof(T) == 4 ? TT_F32 : (std::is_same<T, __ha
 
 template <class T>
 bool run_few(const Plan& p, const FewArgs& a, cudaStream_t st) {
-    auto k = k_head_few<T, type_of<T>()>;
-    if (!allow_smem<KernelTag<type_of<T>(), 0, 0, 0, -2>>(k, p.device, kFewSmem)) return false;
+    auto k = p.few_wide ? k_head_few<T, type_of<T>(), true> : k_head_few<T, type_of<T>(), false>;
+    if (!(p.few_wide ? allow_smem<KernelTag<type_of<T>(), 1, 0, 0, -2>>(k, p.device, kFewSmem)
+                     : allow_smem<KernelTag<type_of<T>(), 0, 0, 0, -2>>(k, p.device, kFewSmem)))
+        return false;
     k<<<(unsigned)p.few_blocks, kFewThreads, p.few_smem, st>>>(a);
     return cudaGetLastError() == cudaSuccess;
 }
@@ -954,10 +968,15 @@ tt_status head_forward(const Plan& p, const Target& t, float* loss, float* lse, 
         ok = score_gemm<kEpiStats>(p.bn_s, p.split, H, W, a, p.sms, p.device, st);
     }
     if (!ok) return TT_ERR_CUDA;
-    if (distill)
-        k_head_finish<T, true><<<(unsigned)in.N, kRowThreads, (size_t)t.K * 12, st>>>(in, t, w.part, p.slots, p.per_slot, p.runs_lse, loss, lse, err);
+    if (distill && wide_rows(p, t.K))
+        k_head_finish<T, true, kRowThreadsWide>
+            <<<(unsigned)in.N, kRowThreadsWide, (size_t)t.K * 12, st>>>(in, t, w.part, p.slots, p.per_slot, p.runs_lse, loss, lse, err);
+    else if (distill)
+        k_head_finish<T, true, kRowThreads>
+            <<<(unsigned)in.N, kRowThreads, (size_t)t.K * 12, st>>>(in, t, w.part, p.slots, p.per_slot, p.runs_lse, loss, lse, err);
     else
-        k_head_finish<T, false><<<(unsigned)cdiv(in.N, 4), kRowThreads, 0, st>>>(in, t, w.part, p.slots, p.per_slot, p.runs_lse, loss, lse, err);
+        k_head_finish<T, false, kRowThreads>
+            <<<(unsigned)cdiv(in.N, kRowThreads / 32), kRowThreads, 0, st>>>(in, t, w.part, p.slots, p.per_slot, p.runs_lse, loss, lse, err);
     return launch_ok() ? TT_OK : TT_ERR_CUDA;
 }
 
@@ -984,12 +1003,16 @@ tt_status head_backward(const Plan& p, const Target& t, const float* lse, const 
         a.nclear = ents ? p.nblocks * p.vblocks : 0;
         if (!launch_prep<T>(p, a, st)) return TT_ERR_CUDA;
     }
-    if (distill)
-        k_head_rows<T, true><<<(unsigned)in.N, kRowThreads, (size_t)t.K * 12, st>>>(in, t, lse, grad, w.shares, amax, w.nlse, w.scale, w.ids, w.dzt, w.blocks,
-                                                                                  (int)p.nblocks, ents, w.hp, err);
+    const auto rows = [&](auto kernel, int threads) {
+        kernel<<<(unsigned)in.N, threads, (size_t)t.K * 12, st>>>(in, t, lse, grad, w.shares, amax, w.nlse, w.scale, w.ids, w.dzt, w.blocks, (int)p.nblocks,
+                                                                ents, w.hp, err);
+    };
+    if (distill && wide_rows(p, t.K))
+        rows(k_head_rows<T, true, kRowThreadsWide>, kRowThreadsWide);
+    else if (distill)
+        rows(k_head_rows<T, true, kRowThreads>, kRowThreads);
     else
-        k_head_rows<T, false><<<(unsigned)in.N, kRowThreads, 12, st>>>(in, t, lse, grad, w.shares, amax, w.nlse, w.scale, w.ids, w.dzt, w.blocks, (int)p.nblocks,
-                                                                     ents, w.hp, err);
+        rows(k_head_rows<T, false, kRowThreads>, kRowThreads);
     if (!launch_ok()) return TT_ERR_CUDA;
     const uint32_t *ah = amax, *az = amax ? amax + 2 : nullptr;
     const int64_t wpitch = p.pack_w ? in.Dp : in.ldw;

@@ -350,6 +350,40 @@ __device__ __forceinline__ void put_rows_16(uint4* buf, const float (&v)[32], ui
     put_rows(buf, mine, base, pitch, rows);
 }
 
+// The same for rows that do not begin on 16-byte boundaries, and their last columns: lanes
+// along a row, element by element.  cols: how many of the 32 columns there are.
+__device__ __forceinline__ void put_elements(uint4* buf, const float (&v)[32], void* base, int64_t ld, int64_t rows, int64_t cols, int type) {
+    const int lane = threadIdx.x & 31;
+    if (type == TT_F32) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            __syncwarp();
+#pragma unroll
+            for (int c = 0; c < 4; ++c) buf[lane * 4 + (c ^ ((lane >> 1) & 3))] = bits4(v + h * 16 + c * 4);
+            __syncwarp();
+            const int k = lane & 15;
+#pragma unroll 4
+            for (int i = 0; i < 16; ++i) {
+                const int r = i * 2 + (lane >> 4);
+                const float x = reinterpret_cast<const float*>(buf)[r * 16 + ((k >> 2) ^ ((r >> 1) & 3)) * 4 + (k & 3)];
+                if (r < rows && h * 16 + k < cols) static_cast<float*>(base)[r * ld + h * 16 + k] = x;
+            }
+        }
+    } else {
+        uint32_t q[16];
+        pack32(v, q, type == TT_BF16);
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) buf[lane * 4 + (c ^ ((lane >> 1) & 3))] = make_uint4(q[4 * c], q[4 * c + 1], q[4 * c + 2], q[4 * c + 3]);
+        __syncwarp();
+#pragma unroll 4
+        for (int r = 0; r < 32; ++r) {
+            const uint16_t x = reinterpret_cast<const uint16_t*>(buf)[r * 32 + ((lane >> 3) ^ ((r >> 1) & 3)) * 8 + (lane & 7)];
+            if (r < rows && lane < cols) static_cast<uint16_t*>(base)[r * ld + lane] = x;
+        }
+    }
+}
+
 // Columns [col, col + 32), col < N, of a warp's 32 rows from row0 < M on, a row per lane.
 __device__ __forceinline__ void store_out(const OutArgs& o, uint4* buf, int split, int64_t row0, int64_t col, int64_t M, int64_t N, float (&v)[32],
                                           Pow2 sc) {
@@ -364,10 +398,8 @@ __device__ __forceinline__ void store_out(const OutArgs& o, uint4* buf, int spli
                 put_rows_f32(buf, v, reinterpret_cast<uint8_t*>(static_cast<float*>(o.out) + at), o.ldo * 4, rows);
             else
                 put_rows_16(buf, v, reinterpret_cast<uint8_t*>(static_cast<uint16_t*>(o.out) + at), o.ldo * 2, rows, o.type == TT_BF16);
-        } else if (lane < rows) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-                if (col + j < N) store_one(o.out, at + lane * o.ldo + j, v[j], o.type);
+        } else {
+            put_elements(buf, v, static_cast<uint8_t*>(o.out) + at * (o.type == TT_F32 ? 4 : 2), o.ldo, rows, N - col, o.type);
         }
     } else {  // whole chunks: the columns past N hold zeros
         float* p = o.partial + ((int64_t)split * M + row0) * o.pp + col;

@@ -7,7 +7,8 @@
 // run on the warp-level tensor cores with the table's rows as the long side
 // (mma.sync: 16 table rows x 8 hidden rows); fp32 as TF32 hi and lo parts, hi hi + hi lo +
 // lo hi, split on the fly.  The order of k is free as long as both operands use the same,
-// so a thread's part of a table row is one 16-byte load, and the hidden rows lie in shared
+// so a thread's part of a table row is 16 bytes in one load (four, where rows do not begin
+// on 16-byte boundaries), and the hidden rows lie in shared
 // memory as the fragments want them.  A warp takes 32 table rows at a time; where there
 // are too few of them, warps share a row's columns.  Sums over 64 bytes x 2 of a row are
 // added up in fp32 registers.  Each lane keeps the running maximum and sum of the table
@@ -49,14 +50,15 @@ __device__ __forceinline__ void mma_few(float* d, const uint32_t* a, const uint3
             : "r"(a[0]), "r"(a8[0]), "r"(a[1]), "r"(a8[1]), "r"(b[0]), "r"(b[1]));
 }
 
-// x as its TF32 part (cut, not rounded) and the rest, which is exact.
+// x as its TF32 part and the rest (exact), both rounded to nearest by adding half a unit:
+// the tensor core cuts what TF32 does not hold.
 __device__ __forceinline__ void few_split(uint32_t& x, uint32_t& lo) {
-    const uint32_t hi = x & 0xFFFFE000u;
-    lo = __float_as_uint(__uint_as_float(x) - __uint_as_float(hi));
+    const uint32_t hi = (x + 0x1000u) & 0xFFFFE000u;
+    lo = __float_as_uint(__uint_as_float(x) - __uint_as_float(hi)) + 0x1000u;
     x = hi;
 }
 
-template <class T, int TYPE>
+template <class T, int TYPE, bool WIDE>  // WIDE: table rows begin on 16-byte boundaries, else on 4-byte ones
 __global__ void __launch_bounds__(kFewThreads, 2) k_head_few(const __grid_constant__ FewArgs a) {
     constexpr int E = 16 / sizeof(T), C = kFewStep;
     constexpr bool TWO = TYPE == TT_F32;  // hi and lo parts
@@ -100,8 +102,15 @@ __global__ void __launch_bounds__(kFewThreads, 2) k_head_few(const __grid_consta
         for (int i = 0; i < C; ++i) {
             const int at = ((lj * C + i) * 4 + t) * 16;
 #pragma unroll
-            for (int r = 0; r < 4; ++r)  // past the row's end: 0, so that nothing not finite meets hidden's 0
-                q[r][i] = at < row_bytes ? __ldcs(reinterpret_cast<const uint4*>(pr[r] + at)) : make_uint4(0, 0, 0, 0);
+            for (int r = 0; r < 4; ++r) {  // past the row's end: 0, so that nothing not finite meets hidden's 0
+                if (WIDE) {
+                    q[r][i] = at < row_bytes ? __ldcs(reinterpret_cast<const uint4*>(pr[r] + at)) : make_uint4(0, 0, 0, 0);
+                } else {
+                    const uint32_t* p = reinterpret_cast<const uint32_t*>(pr[r] + at);
+                    q[r][i] = make_uint4(at < row_bytes ? __ldg(p) : 0, at + 4 < row_bytes ? __ldg(p + 1) : 0,
+                                         at + 8 < row_bytes ? __ldg(p + 2) : 0, at + 12 < row_bytes ? __ldg(p + 3) : 0);
+                }
+            }
         }
         if (++lj == je) {
             lj = jb;
