@@ -599,8 +599,8 @@ bool run_gemm(const Operand& A, const Operand& B, GemmArgs a, int sms, int dev, 
     a.units = EPI == kEpiOut ? (int64_t)a.mtiles * a.ntiles * a.splits : (int64_t)a.mtiles * a.nstrips;
     a.wait_ns = g_head_wait_ns;
     auto k = k_head_gemm<BN, AMN, BMN, EPI, SPLIT>;
-    if (!allow_smem<KernelTag<BN, AMN, BMN, EPI, SPLIT>>(k, dev, GemmShape<BN>::kSmem)) return false;
-    k<<<(unsigned)(a.units < sms ? a.units : sms), kGemmThreads, GemmShape<BN>::kSmem, st>>>(ma, mb, a);
+    if (!allow_smem<KernelTag<BN, AMN, BMN, EPI, SPLIT>>(k, dev, GemmShape<BN, SPLIT>::kSmem)) return false;
+    k<<<(unsigned)(a.units < sms ? a.units : sms), kGemmThreads, GemmShape<BN, SPLIT>::kSmem, st>>>(ma, mb, a);
     return cudaGetLastError() == cudaSuccess;
 }
 

@@ -44,14 +44,16 @@ struct GemmArgs {
     OutArgs to;
 };
 
-template <int BN>
+template <int BN, bool SPLIT>
 struct GemmShape {
-    static constexpr int kStages = BN == 256 ? 4 : (BN == 128 ? 6 : 8);
-    static constexpr uint32_t kA = 128 * 128, kB = BN * 128;
-    static constexpr uint32_t kStage = kA + kB;
-    static constexpr uint32_t kRing = kStages * kStage;                     // then 2 KB per epilogue warp (put_rows)
+    static constexpr int PC = SPLIT ? 2 : 1;
+    static constexpr uint32_t kA = 128 * 128, kB = BN * 128;  // a chunk of one piece
+    static constexpr uint32_t kStage = PC * (kA + kB);        // A hi, A lo, B hi, B lo
+    static constexpr int kStages = 192 * 1024 / kStage;
+    static constexpr uint32_t kRing = kStages * kStage;       // then 2 KB per epilogue warp (put_rows)
     static constexpr size_t kSmem = (size_t)kRing + kEpiWarps * 2048 + 1024;
-    static_assert(kSmem + 512 <= 227 * 1024, "shared memory");
+    static constexpr int kAcc = PC * BN;                      // tensor-memory columns of an accumulator
+    static_assert(kSmem + 512 <= 227 * 1024 && 2 * kAcc <= 512, "shared and tensor memory");
 };
 
 // C[m, n] = sum_k A[m, k] B[n, k] by 128 x BN tiles, a persistent block per SM: one
@@ -59,18 +61,19 @@ struct GemmShape {
 // accumulators in tensor memory, sixteen warps read the other out, a quarter of its
 // columns and 32 of its rows each, a row per lane.
 //
-// SPLIT (fp32 operands in two pieces).  The tensor core's fp32 accumulation cuts off
-// the bits below its accumulator instead of rounding them, so the error of a long sum
-// grows with its length and always in one direction.  An accumulator therefore holds
-// kRange K chunks only, its small products (lo hi, hi lo) first, and the epilogue adds
-// the ranges up in registers, rounding to nearest.
+// SPLIT (fp32 operands in two pieces).  The pieces of B lie one behind the other, so
+// A hi [B hi | B lo] is one MMA of twice the columns; A lo B hi adds to its second half,
+// which holds the small products.  The tensor core's fp32 accumulation cuts off the bits
+// below its accumulator instead of rounding them, so the error of a long sum grows with
+// its length and always in one direction.  An accumulator therefore holds kRange K chunks
+// only, and the epilogue adds the ranges up in registers, rounding to nearest.
 template <int BN, bool AMN, bool BMN, int EPI, bool SPLIT>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     k_head_gemm(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
                 const __grid_constant__ GemmArgs a) {
-    using S = GemmShape<BN>;
+    using S = GemmShape<BN, SPLIT>;
     static_assert(BN % (32 * kParts) == 0 && (!SPLIT || BN <= 128), "the ranges' sums stay in registers");
-    constexpr int kSegs = SPLIT ? 3 : 1, kRange = 2;  // a range: 128 of K
+    constexpr int kRange = 2;  // 128 of K
     constexpr int kCh = BN / kParts / 32;  // 32-column chunks of a part
     extern __shared__ uint8_t raw[];
     __shared__ uint64_t full[S::kStages], empty[S::kStages], accfull[2], accempty[2], drain;
@@ -93,7 +96,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         mbar_init(&drain, 1);
         gave_up_s = 0;
     }
-    if (warp == 2) tc_alloc(&tmem_slot, 2 * BN);
+    if (warp == 2) tc_alloc(&tmem_slot, 2 * S::kAcc);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -129,46 +132,43 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             int m, n0, n1, kb, ke, split;
             unit(u, m, n0, n1, kb, ke, split);
             for (int n = n0; ok && n < n1; ++n)
-                for (int r0 = kb; ok && r0 < ke; r0 = SPLIT ? (r0 / kRange + 1) * kRange : ke) {
-                    const int r1 = SPLIT ? min((r0 / kRange + 1) * kRange, ke) : ke;
-                    for (int seg = 0; ok && seg < kSegs; ++seg) {
-                        const int za = SPLIT && seg == 0, zb = SPLIT && seg == 1;
-                        for (int kc = r0; kc < r1; ++kc, ++it) {
-                            const uint32_t st = it % S::kStages;
-                            ok = head_wait(&empty[st], ((it / S::kStages) & 1) ^ 1, a.wait_ns, gave_up);
-                            if (!ok) break;
-                            if (lead) {
-                                const uint32_t sa = base + st * S::kStage, sb = sa + S::kA;
-                                bulk_expect(&full[st], S::kStage);
-                                if (AMN) {
-                                    tma_load3(sa, &mapA, m * 128, kc * kBK, za, &full[st]);
-                                    tma_load3(sa + 8192, &mapA, m * 128 + 64, kc * kBK, za, &full[st]);
-                                } else {
-                                    tma_load3(sa, &mapA, kc * kBK, m * 128, za, &full[st]);
-                                }
-                                if (BMN) {
+                for (int kc = kb; kc < ke; ++kc, ++it) {
+                    const uint32_t st = it % S::kStages;
+                    ok = head_wait(&empty[st], ((it / S::kStages) & 1) ^ 1, a.wait_ns, gave_up);
+                    if (!ok) break;
+                    if (lead) {
+                        const uint32_t sa = base + st * S::kStage, sb = sa + S::PC * S::kA;
+                        bulk_expect(&full[st], S::kStage);
 #pragma unroll
-                                    for (int j = 0; j < BN / 64; ++j)
-                                        tma_load3(sb + j * 8192, &mapB, n * BN + j * 64, kc * kBK, zb, &full[st]);
-                                } else {
-                                    tma_load3(sb, &mapB, kc * kBK, n * BN, zb, &full[st]);
-                                }
+                        for (int z = 0; z < S::PC; ++z) {
+                            if (AMN) {
+                                tma_load3(sa + z * S::kA, &mapA, m * 128, kc * kBK, z, &full[st]);
+                                tma_load3(sa + z * S::kA + 8192, &mapA, m * 128 + 64, kc * kBK, z, &full[st]);
+                            } else {
+                                tma_load3(sa + z * S::kA, &mapA, kc * kBK, m * 128, z, &full[st]);
                             }
-                            __syncwarp();
+                            if (BMN) {
+#pragma unroll
+                                for (int j = 0; j < BN / 64; ++j)
+                                    tma_load3(sb + z * S::kB + j * 8192, &mapB, n * BN + j * 64, kc * kBK, z, &full[st]);
+                            } else {
+                                tma_load3(sb + z * S::kB, &mapB, kc * kBK, n * BN, z, &full[st]);
+                            }
                         }
                     }
+                    __syncwarp();
                 }
         }
     } else if (warp == 1) {
-        const uint32_t idesc = idesc_f16(128, BN, a.fmt, AMN, BMN);
-        const uint32_t da0 = desc_lo(base, AMN ? 8192 : kNoLbo), db0 = desc_lo(base + S::kA, BMN ? 8192 : kNoLbo);
+        const uint32_t idesc = idesc_f16(128, BN, a.fmt, AMN, BMN), idesc2 = idesc_f16(128, S::PC * BN, a.fmt, AMN, BMN);
+        const uint32_t da0 = desc_lo(base, AMN ? 8192 : kNoLbo), db0 = desc_lo(base + S::PC * S::kA, BMN ? 8192 : kNoLbo);
         for (int64_t u = blockIdx.x; ok && u < a.units; u += gridDim.x) {
             int m, n0, n1, kb, ke, split;
             unit(u, m, n0, n1, kb, ke, split);
             for (int n = n0; ok && n < n1; ++n)
                 for (int r0 = kb; ok && r0 < ke; r0 = SPLIT ? (r0 / kRange + 1) * kRange : ke, ++acc) {
-                    const int steps = (SPLIT ? min((r0 / kRange + 1) * kRange, ke) - r0 : ke - kb) * kSegs;
-                    const uint32_t buf = acc & 1, d = tmem + buf * BN;
+                    const int steps = SPLIT ? min((r0 / kRange + 1) * kRange, ke) - r0 : ke - kb;
+                    const uint32_t buf = acc & 1, d = tmem + buf * S::kAcc;
                     ok = head_wait(&accempty[buf], ((acc >> 1) & 1) ^ 1, a.wait_ns, gave_up);
                     if (!ok) break;
                     tc_fence_after();
@@ -179,8 +179,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                         tc_fence_after();
                         const uint32_t da = da0 + st * (S::kStage >> 4), db = db0 + st * (S::kStage >> 4);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            mma_f16(d, da + k * ((AMN ? 2048 : 32) >> 4), db + k * ((BMN ? 2048 : 32) >> 4), idesc, c > 0 || k > 0, lead);
+                        for (int k = 0; k < 4; ++k) {
+                            const uint32_t ak = da + k * ((AMN ? 2048 : 32) >> 4), bk = db + k * ((BMN ? 2048 : 32) >> 4);
+                            mma_f16(d, ak, bk, idesc2, c > 0 || k > 0, lead);
+                            if (SPLIT) mma_f16(d + BN, ak + (S::kA >> 4), bk, idesc, true, lead);
+                        }
                         mma_commit(&empty[st], lead);
                     }
                     if (ok) mma_commit(&accfull[buf], lead);
@@ -232,14 +235,20 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                         ok = head_wait(&accfull[buf], (acc >> 1) & 1, a.wait_ns, gave_up);
                         if (!ok) break;
                         tc_fence_after();
-                        const uint32_t t0 = tmem + buf * BN + ((uint32_t)(quad * 32) << 16) + part * (BN / kParts);
+                        const uint32_t t0 = tmem + buf * S::kAcc + ((uint32_t)(quad * 32) << 16) + part * (BN / kParts);
                         const int we = a.wexp ? __ldg(&a.wexp[EPI == kEpiOut ? (int64_t)(r0 / kRange) * a.kb + n : (int64_t)n * a.kb + r0 / kRange]) : 0;
                         const Pow2 f(-er - we);
 #pragma unroll
                         for (int ch = 0; ch < kCh; ++ch) {
-                            float v[32];
+                            float v[32], small[16];
                             tm_ld32(t0 + ch * 32, v);
                             tm_wait_ld(v);
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                tm_read16(t0 + BN + ch * 32 + h * 16, small);
+#pragma unroll
+                                for (int j = 0; j < 16; ++j) v[h * 16 + j] += small[j];
+                            }
 #pragma unroll
                             for (int j = 0; j < 32; ++j) v[j] *= f.b;
 #pragma unroll
@@ -258,7 +267,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     if (!ok) break;
                     ++acc;
                     tc_fence_after();
-                    const uint32_t t0 = tmem + buf * BN + ((uint32_t)(quad * 32) << 16) + part * (BN / kParts);
+                    const uint32_t t0 = tmem + buf * S::kAcc + ((uint32_t)(quad * 32) << 16) + part * (BN / kParts);
                     // the next 32 columns are on their way while these are worked on
                     float v[2][32];
                     tm_ld32(t0, v[0]);
@@ -297,7 +306,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         __syncthreads();
     }
     tc_fence_after();
-    if (warp == 2) tc_dealloc(tmem, 2 * BN);
+    if (warp == 2) tc_dealloc(tmem, 2 * S::kAcc);
 }
 
 }  // namespace ttemb

@@ -111,6 +111,7 @@ __global__ void __launch_bounds__(kQ4Threads, 2) k_q4_matvec(const __grid_consta
         uint32_t most = 0;
         if (sizeof(T) != 2 || !std::is_same<T, __half>::value)
             if (m < a.M)
+#pragma unroll 16
                 for (int d = a.g0 * G + lane; d < min(a.g1 * G, a.D); d += 32) {
                     const uint32_t b = __float_as_uint(to_f32(x[m * a.ldx + d])) & 0x7FFFFFFFu;
                     if (b < 0x7F800000u) most = max(most, b);
