@@ -370,9 +370,10 @@ __device__ __forceinline__ void split8(const float (&x)[8], float sc, uint16_t* 
 
 // What a pass needs before its products, in one launch.
 //   blockIdx.y = 0  the table packed in rows of Dp 16-bit elements (fp32: hi and lo
-//                   pieces, a scale per 128 x 128 block, its exponent in wexp: what a tile of
-//                   the products takes of the table between two read-outs, so that a scale is
-//                   one factor there; a block is read once and kept in registers)
+//                   pieces, a scale per block of 128 x 128 (k_head_fused to D = 64: 256 rows), its
+//                   exponent in wexp: what the products take of the table between two
+//                   read-outs, so that a scale is one factor there; a block is read once and
+//                   kept in registers)
 //   blockIdx.y = 1  forward: the hidden rows packed, a warp per row (fp32: a scale of each
 //                   row's own, its exponent in row_exp); backward: the largest finite
 //                   |grad| T and (fp32) |hidden| over the rows that count, a share per block
@@ -380,6 +381,7 @@ __device__ __forceinline__ void split8(const float (&x)[8], float sc, uint16_t* 
 struct PrepArgs {
     HeadIn in;
     uint16_t* wp;       // null: the table is read as it is
+    int wrows;          // rows of a scale's block
     int* wexp;
     uint16_t* hp;       // null: not packed
     int* row_exp;
@@ -391,7 +393,7 @@ struct PrepArgs {
     int64_t nclear;
 };
 
-template <class T, int TH>  // TH threads; fp32: 4 groups of 8 elements a thread, 128 x 128 (512 threads) or 128 x 64
+template <class T, int TH>  // TH threads; fp32: 4 groups of 8 elements a thread: 128 x 128, 256 x 64 (512 threads) or 128 x 64
 __global__ void __launch_bounds__(TH, 1024 / TH) k_head_prep(const __grid_constant__ PrepArgs a) {
     const HeadIn& in = a.in;
     uint16_t* const wp = a.wp;
@@ -405,11 +407,12 @@ __global__ void __launch_bounds__(TH, 1024 / TH) k_head_prep(const __grid_consta
         if constexpr (sizeof(T) == 4) {
             const float* w = static_cast<const float*>(in.w);
             const int cb = (in.D + 127) / 128;  // blocks to a row of blocks
-            const int64_t all = (in.V + 127) / 128 * cb;
+            const int rb = a.wrows;
+            const int64_t all = (in.V + rb - 1) / rb * cb;
             for (int64_t blk = blockIdx.x; blk < all; blk += gridDim.x) {
-                const int64_t v0 = blk / cb * 128;
+                const int64_t v0 = blk / cb * rb;
                 const int c0 = (int)(blk % cb) * 128;
-                const int rows = (int)min((int64_t)128, in.V - v0), bg = min(16, g - c0 / 8), total = rows * bg;
+                const int rows = (int)min((int64_t)rb, in.V - v0), bg = min(16, g - c0 / 8), total = rows * bg;
                 const uint32_t inv = 65536u / bg + 1;  // i / bg for i < 2,048, bg <= 16
                 float x[4][8];
                 uint32_t m = 0;
@@ -514,17 +517,36 @@ __global__ void __launch_bounds__(TH, 1024 / TH) k_head_prep(const __grid_consta
     }
 }
 
-// out[m, n] = the splits' partial sums, in split order, unscaled and rounded once.
-__global__ void __launch_bounds__(256) k_head_reduce(const float* partial, int splits, int64_t M, int64_t N, int64_t pp, void* out,
-                                                     int64_t ldo, int type, const uint32_t* amax_a, const uint32_t* amax_b) {
+// out[m, n] = the splits' partial sums, in split order, unscaled and rounded once.  A
+// block takes 256 >> row_shift rows at a time, 1 << row_shift threads to a row, four
+// columns a thread.
+__global__ void __launch_bounds__(256) k_head_reduce(const float* partial, int splits, int64_t M, int64_t N, int64_t pp, OutArgs to, int row_shift,
+                                                     const uint32_t* amax_a, const uint32_t* amax_b) {
     const Pow2 sc(-amax_exp(amax_a) - amax_exp(amax_b));
-    const int64_t total = M * N;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-        const int64_t m = i / N, n = i - m * N;
-        float s = 0.f;
-        for (int k = 0; k < splits; ++k) s += partial[((int64_t)k * M + m) * pp + n];
-        store_one(out, m * ldo + n, sc(s), type);
-    }
+    const int per = 1 << row_shift, c0 = ((int)threadIdx.x & (per - 1)) * 4;
+    for (int64_t m = (int64_t)blockIdx.x * (256 >> row_shift) + (threadIdx.x >> row_shift); m < M; m += (int64_t)gridDim.x * (256 >> row_shift))
+        for (int64_t n = c0; n < N; n += per * 4) {
+            const float* p = partial + m * pp + n;
+            float4 s = *reinterpret_cast<const float4*>(p);
+#pragma unroll 4
+            for (int k = 1; k < splits; ++k) {
+                const float4 y = *reinterpret_cast<const float4*>(p + (int64_t)k * M * pp);
+                s = make_float4(s.x + y.x, s.y + y.y, s.z + y.z, s.w + y.w);
+            }
+            const float v[4] = {sc(s.x), sc(s.y), sc(s.z), sc(s.w)};
+            const int64_t at = m * to.ldo + n;
+            if (to.vec && n + 4 <= N) {
+                if (to.type == TT_F32)
+                    *reinterpret_cast<float4*>(static_cast<float*>(to.out) + at) = make_float4(v[0], v[1], v[2], v[3]);
+                else
+                    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(to.out) + at) =
+                        make_uint2(pack16(v[0], v[1], to.type == TT_BF16), pack16(v[2], v[3], to.type == TT_BF16));
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (n + j < N) store_one(to.out, at + j, v[j], to.type);
+            }
+        }
 }
 
 // ---------------------------------------------------------------- host
@@ -872,11 +894,11 @@ bool launch_ok() { return cudaGetLastError() == cudaSuccess; }
 
 template <class T>
 bool launch_prep(const Plan& p, const PrepArgs& a, cudaStream_t st) {
-    const int64_t w = !a.wp ? 0 : (p.split ? cdiv(p.in.V, 128) * cdiv(p.in.D, 128) : cdiv(p.in.V * (p.in.Dp / 8), 256));
+    const int64_t w = !a.wp ? 0 : (p.split ? cdiv(p.in.V, a.wrows) * cdiv(p.in.D, 128) : cdiv(p.in.V * (p.in.Dp / 8), 256));
     const int64_t h = a.hp ? cdiv(p.in.N, 8) : (a.shares ? cdiv(p.in.N, 32) : 0), c = cdiv(a.nclear, 1024);
     const int64_t most = w > h ? (w > c ? w : c) : (h > c ? h : c);
     const dim3 grid(grid_of(most, 1, p.sms, 16), a.nclear ? 3 : (h ? 2 : 1));
-    if (p.split && p.in.Dp > 64)
+    if (p.split && (p.in.Dp > 64 || a.wrows > 128))
         k_head_prep<T, 512><<<grid, 512, 0, st>>>(a);
     else
         k_head_prep<T, 256><<<grid, 256, 0, st>>>(a);
@@ -916,6 +938,7 @@ tt_status head_forward(const Plan& p, const Target& t, float* loss, float* lse, 
         PrepArgs a{};
         a.in = in;
         a.wp = p.pack_w_fwd ? w.wp : nullptr;
+        a.wrows = p.fused_lse && in.D <= 64 ? 256 : 128;
         a.wexp = w.wexp;
         a.hp = p.pack_h_fwd ? w.hp : nullptr;
         a.row_exp = w.row_exp;
@@ -994,6 +1017,7 @@ tt_status head_backward(const Plan& p, const Target& t, const float* lse, const 
         PrepArgs a{};
         a.in = in;
         a.wp = p.pack_w ? w.wp : nullptr;
+        a.wrows = p.fused && in.D <= 64 ? 256 : 128;
         a.wexp = w.wexp;
         a.t = t;
         a.distill = distill;
@@ -1029,9 +1053,11 @@ tt_status head_backward(const Plan& p, const Target& t, const float* lse, const 
         return o;
     };
     const auto reduce = [&](const float* partial, int splits, int64_t rows, void* out, const uint32_t* ay) {
+        int shift = 3;
+        while (shift < 8 && (4 << shift) < in.D) ++shift;
         // fp32's are in their own units already
-        k_head_reduce<<<grid_of(rows * in.D, 256, p.sms, 8), 256, 0, st>>>(partial, splits, rows, in.D, p.pp, out, in.D, p.type, p.split ? nullptr : az,
-                                                                           p.split ? nullptr : ay);
+        k_head_reduce<<<grid_of(rows, 256 >> shift, p.sms, 16), 256, 0, st>>>(partial, splits, rows, in.D, p.pp, dest(out, nullptr), shift,
+                                                                            p.split ? nullptr : az, p.split ? nullptr : ay);
         return launch_ok();
     };
     if (p.fused) {

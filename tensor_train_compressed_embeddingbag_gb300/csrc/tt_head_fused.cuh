@@ -21,9 +21,11 @@
 // memory is full) and OUT (where tensor memory has room) have two buffers, and eight
 // further warps take OUT to memory, so segments follow each other without a gap.
 //
-// SPLIT (fp32: every operand as f16 hi + lo): three products each; OUT covers one tile
-// of Y at a time and its sums are kept in the storing warps' registers (k_head_gemm
-// says why).
+// SPLIT (fp32: every operand as f16 hi + lo): three products each; OUT covers two tiles of
+// Y at a time, its small products in columns of their own where there is room, and its
+// sums are kept in the storing warps' registers (k_head_gemm says why).  A flush a tile
+// left the OUT product waiting for its single buffer to be read: 2,230 cycles a tile at
+// D <= 64.
 #pragma once
 
 #include "tt_head.cuh"
@@ -71,7 +73,7 @@ struct FusedArgs {
     const uint32_t* amax_h;  // power-of-two scales of hidden and dz (null: none)
     const uint32_t* amax_z;
     const int* row_exp;      // SPLIT, kLse: hidden's, per row instead
-    const int* wexp;         // SPLIT: weight's, per 128 rows
+    const int* wexp;         // SPLIT: weight's, per two streamed tiles (D <= 64: 256 rows, else 128)
     float ctemp;             // log2(e) / T
     float2* part;            // kLse: [X][slots][kParts] (maximum in log2 units, sum), a slot per run
     int slots;
@@ -250,7 +252,7 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
         uint32_t fl = 0;
         for (; w.left; step(w), ++g) {
             const uint32_t st = g % S::kStages, sb = g % NS, ob = fl % OB;
-            const bool first = SPLIT || w.y == w.y0, last = SPLIT || w.y + 1 == w.y1;
+            const bool first = w.y == w.y0 || (SPLIT && !(w.y & 1)), last = w.y + 1 == w.y1 || (SPLIT && (w.y & 1));
             if (first) ok = head_wait(&oempty[ob], ((fl / OB) & 1) ^ 1, a.wait_ns, gave_up);
             ok = ok && head_wait(&pready[sb], (g / NS) & 1, a.wait_ns, gave_up);
             if (!ok) break;
@@ -263,11 +265,11 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
                 if (SPLIT && DT == 64) {
                     // the two pieces of Y lie one behind the other: hi [hi | lo] is one MMA of
                     // twice the columns, and the second half takes lo hi as well
-                    mma_f16_ta(d, pa, yb, idesc2, k > 0, lead);
+                    mma_f16_ta(d, pa, yb, idesc2, !first || k > 0, lead);
                     mma_f16_ta(d + DT, pa + 16, yb, idesc, true, lead);
                 } else if (SPLIT) {
                     const uint32_t yl = yb + (S::DB * S::kYBlock >> 4);
-                    mma_f16_ta(d, pa + 16, yb, idesc, k > 0, lead);
+                    mma_f16_ta(d, pa + 16, yb, idesc, !first || k > 0, lead);
                     mma_f16_ta(d, pa, yl, idesc, true, lead);
                     mma_f16_ta(d, pa, yb, idesc, true, lead);
                 } else {
@@ -283,7 +285,7 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
     } else if (MODE == kLse && warp >= 12) {
         const int set = (warp - 12) / S::kDzSet, quad = warp & 3, part = (warp - 12) % S::kDzSet >> 2;  // its 32 rows and 64 columns
         float c = a.ctemp, run_m = -INFINITY, run_s = 0.f;  // run_m in units of c
-        int he = 0, we = 0, we_next = SPLIT && w.left ? __ldg(&a.wexp[w.y / (128 / BY)]) : 0;
+        int he = 0, we = 0, we_next = SPLIT && w.left ? __ldg(&a.wexp[w.y >> 1]) : 0;
         for (; w.left; ++g) {
             const int64_t row = (int64_t)w.x * 128 + quad * 32 + lane;
             if (w.y == w.y0) {
@@ -319,7 +321,7 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
                 a.part[(row * a.slots + ((int)blockIdx.x - a.runs.first(w.x))) * S::kParts + set * (S::kParts / 2) + part] =
                     make_float2(run_m == -INFINITY ? -INFINITY : run_m * c, run_s);
             step(w);
-            if (SPLIT && w.left) we_next = __ldg(&a.wexp[w.y / (128 / BY)]);
+            if (SPLIT && w.left) we_next = __ldg(&a.wexp[w.y >> 1]);
         }
     } else if (MODE != kLse && warp >= 12) {
         const int set = (warp - 12) / S::kDzSet, quad = warp & 3, part = (warp - 12) % S::kDzSet >> 2;  // its 32 rows and 64 columns
@@ -338,7 +340,7 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
                 const int nb = COLS ? y32 + lane : x32, vb = COLS ? x32 : y32 + lane;
                 const bool have = nb < a.nblocks && vb < a.vblocks;
                 cp16(&to.blk[lane], a.blocks + (have ? (int64_t)vb * a.nblocks + nb : 0), have);
-                if (SPLIT && lane == 0) cp4(to.wexp, a.wexp + (COLS ? t.x : t.y / (128 / BY)));
+                if (SPLIT && lane == 0) cp4(to.wexp, a.wexp + (COLS ? (DT == 64 ? t.x >> 1 : t.x) : t.y >> 1));
             }
         };
         if (set && w.left) step(w);
@@ -448,9 +450,9 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
                 for (int ch = 0; ch < OC; ++ch)
 #pragma unroll
                     for (int j = 0; j < 32; ++j) sum[ch][j] = 0.f;
-                for (int f = w.y0; f < w.y1; ++f, ++fl) {
+                for (int f = w.y0; f < w.y1; f = (f | 1) + 1, ++fl) {
                     const uint32_t ob = fl % OB;
-                    const Pow2 f1(COLS ? 0 : -ez - __ldg(&a.wexp[f / (128 / BY)]));
+                    const Pow2 f1(COLS ? 0 : -ez - __ldg(&a.wexp[f >> 1]));
                     ok = head_wait(&ofull[ob], (fl / OB) & 1, a.wait_ns, gave_up);
                     if (!ok) break;
                     tc_fence_after();
