@@ -486,17 +486,42 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
                 if (!ok) break;
                 ++fl;
                 tc_fence_after();
+                if (whole && a.to.vec && a.D == DT && a.to.type != TT_F32) {
+                    // OUT is let go before anything is written: the next segment's product waits for it
+                    uint32_t q[OC][16];
 #pragma unroll
-                for (int ch = 0; ch < OC; ++ch) {
-                    float v[32];
-                    tm_ld32(l0 + ob * S::kOut + ch * 32, v);
-                    tm_wait_ld(v);
-                    if (ch + 1 == OC) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&oempty[ob]);
+                    for (int ch = 0; ch < OC; ++ch) {
+                        float v[32];
+                        tm_ld32(l0 + ob * S::kOut + ch * 32, v);
+                        tm_wait_ld(v);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = sc(v[j]);
+                        pack32(v, q[ch], a.fmt);
                     }
-                    put(v, half * (DT / 2) + ch * 32);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&oempty[ob]);
+                    uint8_t* to = reinterpret_cast<uint8_t*>(static_cast<uint16_t*>(a.to.out) + (row - lane) * a.to.ldo + half * (DT / 2));
+#pragma unroll
+                    for (int ch = 0; ch < OC; ++ch) {
+                        const uint4 mine[4] = {make_uint4(q[ch][0], q[ch][1], q[ch][2], q[ch][3]), make_uint4(q[ch][4], q[ch][5], q[ch][6], q[ch][7]),
+                                               make_uint4(q[ch][8], q[ch][9], q[ch][10], q[ch][11]),
+                                               make_uint4(q[ch][12], q[ch][13], q[ch][14], q[ch][15])};
+                        put_rows(rows_out[warp - 4], mine, to + ch * 64, a.to.ldo * 2, a.X - (row - lane));
+                    }
+                } else {
+#pragma unroll
+                    for (int ch = 0; ch < OC; ++ch) {
+                        float v[32];
+                        tm_ld32(l0 + ob * S::kOut + ch * 32, v);
+                        tm_wait_ld(v);
+                        if (ch + 1 == OC) {
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&oempty[ob]);
+                        }
+                        put(v, half * (DT / 2) + ch * 32);
+                    }
                 }
             }
             first = false;
