@@ -233,8 +233,8 @@ __global__ void __launch_bounds__(RT) k_head_finish(HeadIn in, Target t, const f
 // a row that does not count), its lse in log2 units, dz of its target entries, and
 // its packed copy (zeros for a row that does not count, so that nothing such a row
 // holds, infinities and NaN included, reaches dweight).  Entries of one row with the
-// same id hold the same value, of their summed q.  Target entries go to an array
-// (ids_out, dzt; k_head_fix) or, ents given, to their 32 x 32 blocks (k_head_fused).
+// same id hold the same value, of their summed q.  Target entries go to arrays
+// [K][N] (ids_out, dzt) and, for k_head_fused, to their 32 x 32 blocks.
 template <class T, bool DISTILL, int RT>
 __global__ void __launch_bounds__(RT)
     k_head_rows(HeadIn in, Target t, const float* lse, const float* grad, const uint32_t* shares, uint32_t* amax, float* nlse, float* scale, int* ids_out,
@@ -301,13 +301,10 @@ __global__ void __launch_bounds__(RT)
             d = (expf(z / t.T - l) - qs) * rs;
         }
         if (lane == 0) {
-            const int64_t e = n * t.K + k;
-            if (!ents) {
-                ids_out[e] = (int)id;
-                dzt[e] = d;
-            } else if (id >= 0 && !again) {
-                add_target(&blocks[(id >> 5) * nblocks + (n >> 5)], ents, (int)e, (int)(n & 31) | (int)(id & 31) << 5, d);
-            }
+            ids_out[k * in.N + n] = (int)id;
+            dzt[k * in.N + n] = d;
+            if (blocks && id >= 0 && !again)
+                add_target(&blocks[(id >> 5) * nblocks + (n >> 5)], ents, (int)(n * t.K + k), (int)(n & 31) | (int)(id & 31) << 5, d);
         }
     }
     const int64_t piece = in.N * in.Dp;
@@ -325,13 +322,13 @@ __global__ void __launch_bounds__(RT)
 }
 
 // Target entries of dz in columns [v0, v0 + P) of the current piece.
-__global__ void k_head_fix(const int* ids, const float* dzt, int64_t total, int K, int v0, int P, uint16_t* dz,
+__global__ void k_head_fix(const int* ids, const float* dzt, int64_t total, int64_t rows, int v0, int P, uint16_t* dz,
                            int64_t pitch, int64_t piece, int fmt, int split) {
     const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     if (i >= total) return;
     const int id = ids[i];
     if (id < v0 || id >= v0 + P) return;
-    const int64_t at = (i / K) * pitch + (id - v0);
+    const int64_t at = (i % rows) * pitch + (id - v0);
     const uint32_t w = pack16(dzt[i], 0.f, fmt);
     dz[at] = (uint16_t)w;
     if (split) dz[piece + at] = (uint16_t)pack16(dzt[i] - unpack_f16(w).x, 0.f, 0);
@@ -868,8 +865,8 @@ size_t bwd_ws(const Plan& p, int K, void* base, BwdWs* w) {
     w->wexp = a.get<int>(p.split ? cdiv(p.in.V, 128) * cdiv(p.in.D, 128) : 0);
     w->nlse = a.get<float>(cdiv(p.in.N, 128) * 128);
     w->scale = a.get<float>(cdiv(p.in.N, 128) * 128);
-    w->ids = a.get<int>(p.fused ? 0 : nk);
-    w->dzt = a.get<float>(p.fused ? 0 : nk);
+    w->ids = a.get<int>(nk);
+    w->dzt = a.get<float>(nk);
     w->blocks = a.get<TargetBlock>(p.fused ? p.nblocks * p.vblocks : 0);
     w->ents = a.get<TargetEntry>(p.fused ? nk : 0);
     w->hp = a.get<uint16_t>(pc * p.in.N * p.in.Dp);
@@ -1012,8 +1009,8 @@ tt_status head_backward(const Plan& p, const Target& t, const float* lse, const 
     if (in.N == 0) return cudaMemsetAsync(dw, 0, (size_t)in.V * in.D * p.esize, st) == cudaSuccess ? TT_OK : TT_ERR_CUDA;
     const bool distill = t.logits != nullptr;
     uint32_t* amax = p.fmt ? nullptr : w.amax;  // bf16 has fp32's range: dz needs no scale
-    TargetEntry* ents = p.fused ? w.ents : nullptr;
-    if (amax || p.pack_w || ents) {
+    TargetBlock* blocks = p.fused ? w.blocks : nullptr;
+    if (amax || p.pack_w || blocks) {
         PrepArgs a{};
         a.in = in;
         a.wp = p.pack_w ? w.wp : nullptr;
@@ -1024,12 +1021,12 @@ tt_status head_backward(const Plan& p, const Target& t, const float* lse, const 
         a.grad = grad;
         a.shares = amax ? w.shares : nullptr;
         a.clear = reinterpret_cast<uint4*>(w.blocks);
-        a.nclear = ents ? p.nblocks * p.vblocks : 0;
+        a.nclear = blocks ? p.nblocks * p.vblocks : 0;
         if (!launch_prep<T>(p, a, st)) return TT_ERR_CUDA;
     }
     const auto rows = [&](auto kernel, int threads) {
-        kernel<<<(unsigned)in.N, threads, (size_t)t.K * 12, st>>>(in, t, lse, grad, w.shares, amax, w.nlse, w.scale, w.ids, w.dzt, w.blocks, (int)p.nblocks,
-                                                                ents, w.hp, err);
+        kernel<<<(unsigned)in.N, threads, (size_t)t.K * 12, st>>>(in, t, lse, grad, w.shares, amax, w.nlse, w.scale, w.ids, w.dzt, blocks, (int)p.nblocks,
+                                                                w.ents, w.hp, err);
     };
     if (distill && wide_rows(p, t.K))
         rows(k_head_rows<T, true, kRowThreadsWide>, kRowThreadsWide);
@@ -1074,6 +1071,10 @@ tt_status head_backward(const Plan& p, const Target& t, const float* lse, const 
         a.scale = w.scale;
         a.blocks = w.blocks;
         a.ents = w.ents;
+        a.ids = w.ids;
+        a.dzt = w.dzt;
+        a.K = t.K;
+        a.rows = in.N;
         a.nblocks = (int)p.nblocks;
         a.vblocks = (int)p.vblocks;
         a.partial = w.joins;
@@ -1103,7 +1104,7 @@ tt_status head_backward(const Plan& p, const Target& t, const float* lse, const 
         a.dz_pitch = p.pitch;
         a.dz_piece = dz_piece;
         if (!score_gemm<kEpiDz>(p.bn_s, p.split, H, W, a, p.sms, p.device, st)) return TT_ERR_CUDA;
-        k_head_fix<<<(unsigned)cdiv(in.N * t.K, 256), 256, 0, st>>>(w.ids, w.dzt, in.N * t.K, t.K, (int)v0, (int)P, w.dz, p.pitch, dz_piece,
+        k_head_fix<<<(unsigned)cdiv(in.N * t.K, 256), 256, 0, st>>>(w.ids, w.dzt, in.N * t.K, in.N, (int)v0, (int)P, w.dz, p.pitch, dz_piece,
                                                                 p.fmt, p.split);
         if (!launch_ok()) return TT_ERR_CUDA;
 

@@ -16,25 +16,35 @@
 // A tile's way through S, dz and OUT is long: every hand-over between the tensor cores
 // and the warps costs one to four hundred cycles, and so does what an issuing warp does
 // around a tile's MMAs (its waits and commits).  So two warps issue S, taking tiles in
-// turn, and one issues OUT; S has three buffers, two sets of dz warps take tiles in turn, and what a dz warp needs of memory (lse and scale of the hidden rows, targets)
-// is fetched while it works on the tile before.  X (but for fp32 at D > 64, where shared
+// turn, and one issues OUT; S has three buffers, two sets of dz warps take tiles in turn,
+// and what a dz warp needs of memory (lse and scale of the hidden rows, its block's first
+// targets) is fetched while it works on the tile before.  X (but for fp32 at D > 64, where shared
 // memory is full) and OUT (where tensor memory has room) have two buffers, and eight
 // further warps take OUT to memory, so segments follow each other without a gap.
 //
 // SPLIT (fp32: every operand as f16 hi + lo): three products each; OUT covers two tiles of
 // Y at a time, its small products in columns of their own where there is room, and its
-// sums are kept in the storing warps' registers (k_head_gemm says why).  A flush a tile
-// left the OUT product waiting for its single buffer to be read: 2,230 cycles a tile at
-// D <= 64.
+// sums are kept in the storing warps' registers (k_head_gemm says why).  Sums read
+// every tile instead of every second one: dweight of 512 x 1,000,000 x 64 took 315 us,
+// here 267.
+//
+// Measured, us and TFLOP/s of its 2 N V D (kLse) or 4 N V D products (SPLIT: x 3):
+// bf16 4096 x 100003 x 128 dhidden 118 (1770), dweight 144 (1460); fp32 512 x 1,000,000 x
+// 64 lse 143 (1380), dhidden 241 (1630), dweight 267 (1470).  The tensor pipe is 60 to 70%
+// busy and what bounds them; the rest is fill and drain of the tiles' way above.
 #pragma once
 
 #include "tt_head.cuh"
 
 namespace ttemb {
 
-// The elements of dz that have a target, by 32 x 32 block of (hidden row, table row):
-// a block holds two of them and the rest in a list.  An element's place in its block is
-// (n & 31) | (v & 31) << 5; its value is scaled like the others.  All zero: none.
+// The elements of dz that have a target, by 32 x 32 block of (hidden row, table row): a
+// block holds two of them, how many there are, and the rest in a list.  Where many rows of
+// a batch share popular items the list is long and every step of it a memory latency:
+// then the 32 rows' entries are gone through instead, a row per lane, four loads at a
+// time (a bf16 batch of 4096 over 25,003 items drawn by popularity, D = 128: dweight 59 us,
+// with lists alone 64; uniform ones change nothing).  An element's place in its block is (n & 31) | (v & 31) << 5; its value is scaled
+// like the others.  All zero: none.
 struct __align__(16) TargetBlock {
     uint32_t meta;  // places of the two (bits 0..9 and 10..19), bits 20..31: how many elements
     float val[2];
@@ -81,6 +91,10 @@ struct FusedArgs {
     const float* scale;      //   multiple of 128 rows
     const TargetBlock* blocks;  // [vblocks][nblocks]
     const TargetEntry* ents;
+    const int* ids;             // [K][hidden rows] the rows' entries (-1: none) and their elements of dz
+    const float* dzt;
+    int K;
+    int64_t rows;
     int nblocks, vblocks;
     OutArgs to;              // whole segments; others as fp32 sums to
     float* partial;          //   [blocks][2][128][to.pp]: the run's first segment, its last
@@ -106,6 +120,69 @@ struct FusedShape {
     static constexpr uint32_t kOutCol = NS * BY;
     static_assert(NS * BY + OB * kOut <= 512, "tensor memory");
 };
+
+// The target elements of a 32 x 32 block of dz, after its warp has written the block to
+// tensor memory from t0 on: each replaces one 16-bit half (SPLIT: and its lo part, 16
+// columns further) of one column.  nb, vb: which block; COLS: hidden rows are columns.
+template <bool SPLIT, bool COLS>
+__device__ __noinline__ void put_targets(const FusedArgs& a, uint32_t t0, uint4 b, int nb, int vb) {
+    const int lane = threadIdx.x & 31, count = (int)(b.x >> 20);
+    auto put = [&](int col, bool mine, float val) {
+        const uint32_t hi = pack16(val, 0.f, SPLIT ? 0 : a.fmt) & 0xFFFFu, sh = (uint32_t)(col & 1) * 16;
+        uint32_t w = tm_read1(t0 + (col >> 1));
+        if (mine) w = (w & ~(0xFFFFu << sh)) | hi << sh;
+        tm_write1(t0 + (col >> 1), w);
+        if (SPLIT) {
+            const uint32_t lo = pack16(val - unpack_f16(hi).x, 0.f, 0) & 0xFFFFu;
+            w = tm_read1(t0 + 16 + (col >> 1));
+            if (mine) w = (w & ~(0xFFFFu << sh)) | lo << sh;
+            tm_write1(t0 + 16 + (col >> 1), w);
+        }
+        tm_wait_st();  // the next may be in the same column
+    };
+    auto place = [&](int at, float val) {
+        const int n = at & 31, v = at >> 5;
+        put(COLS ? n : v, lane == (COLS ? v : n), val);
+    };
+    if (a.K >= 2 * (count - 2)) {  // count - 2 steps of the list, or K / 4 rounds of loads
+        place(b.x & 1023, __uint_as_float(b.y));
+        if (count > 1) place((b.x >> 10) & 1023, __uint_as_float(b.z));
+#pragma unroll 1
+        for (int e = (int)b.w; e;) {
+            const int4 t = __ldg(reinterpret_cast<const int4*>(a.ents + (e - 1)));
+            place(t.x, __int_as_float(t.y));
+            e = t.z;
+        }
+        return;
+    }
+    const int64_t n = (int64_t)nb * 32 + lane;
+#pragma unroll 1
+    for (int k0 = 0; k0 < a.K; k0 += 4) {
+        int off[4];
+        float val[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const bool in = n < a.rows && k0 + i < a.K;
+            off[i] = in ? __ldg(&a.ids[(k0 + i) * a.rows + n]) - vb * 32 : -1;
+            val[i] = in ? __ldg(&a.dzt[(k0 + i) * a.rows + n]) : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t m = __ballot_sync(0xffffffffu, (uint32_t)off[i] < 32u);
+            while (m) {
+                const int from = __ffs(m) - 1, o = __shfl_sync(0xffffffffu, off[i], from);
+                if (COLS) {
+                    const float x = __shfl_sync(0xffffffffu, val[i], from);
+                    put(from, lane == o, x);
+                    m &= m - 1;
+                } else {  // all rows with that column at once
+                    put(o, off[i] == o, val[i]);
+                    m &= ~__ballot_sync(0xffffffffu, off[i] == o);
+                }
+            }
+        }
+    }
+}
 
 // kLse has no OUT: a tile's dz warps free its S, and its stage is free once S is formed.
 template <int DT, bool SPLIT, int MODE>
@@ -350,12 +427,16 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
             const uint32_t sb = g % NS;
             const int64_t left = a.Y - ((int64_t)w.y * BY + part * 64);  // streamed rows from this warp's first column on
             const Ahead& my = ahead[warp - 12][now];
+            const struct {
+                int x32, y32;
+            } at = {w.x * 4 + quad, w.y * (BY / 32) + part * 2};  // its 32-row blocks
             cp_wait();
             __syncwarp();
             step(w);
             if (w.left) step(w);
             fetch(w, ahead[warp - 12][now ^ 1]);
             const float c = SPLIT ? a.ctemp * exp2c(-he - my.wexp[0]) : a.ctemp;
+            const float l = my.nlse[lane], r = my.scale[lane];  // of this lane's row (not COLS)
             ok = head_wait(&sfull[g % S::kStages], (g / S::kStages) & 1, a.wait_ns, gave_up);
             if (!ok) break;
             tc_fence_after();
@@ -378,7 +459,6 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
                         mul2(p[j + 2], p[j + 3], r.z, r.w);
                     }
                 } else {
-                    const float l = my.nlse[lane], r = my.scale[lane];
 #pragma unroll
                     for (int j = 0; j < 32; j += 2) {
                         fma2(p[j], p[j + 1], c, c, l, l);
@@ -392,22 +472,6 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
                             if (ch * 32 + j >= left) p[j] = 0.f;
                     }
                 }
-                const uint4 b = my.blk[ch];
-                if (b.x) {
-                    auto put = [&](int at, float val) {
-                        const int tl = COLS ? at >> 5 : at & 31, tc = COLS ? at & 31 : at >> 5;
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (j == tc && lane == tl) p[j] = val;
-                    };
-                    put(b.x & 1023, __uint_as_float(b.y));
-                    if (b.x >> 21) put((b.x >> 10) & 1023, __uint_as_float(b.z));
-                    for (int e = (int)b.w; e;) {
-                        const int4 t = __ldg(reinterpret_cast<const int4*>(a.ents + (e - 1)));
-                        put(t.x, __int_as_float(t.y));
-                        e = t.z;
-                    }
-                }
                 uint32_t q[16];
                 pack32(p, q, SPLIT ? 0 : a.fmt);
                 tm_st16(t0, q);
@@ -418,6 +482,11 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
                         q[j] = pack16(p[2 * j] - h.x, p[2 * j + 1] - h.y, 0);
                     }
                     tm_st16(t0 + 16, q);
+                }
+                const uint4 b = my.blk[ch];
+                if (b.x) {
+                    tm_wait_st();
+                    put_targets<SPLIT, COLS>(a, t0, b, COLS ? at.y32 + ch : at.x32, COLS ? at.x32 : at.y32 + ch);
                 }
             }
             tm_wait_st();
