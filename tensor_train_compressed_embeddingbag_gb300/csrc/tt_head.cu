@@ -75,27 +75,49 @@ __device__ __forceinline__ int64_t xent_id(const Target& t, int64_t n, int64_t V
     return id;
 }
 
-template <class T>
-__device__ __forceinline__ float warp_dot(const T* x, const T* y, int D, int vec, int lane) {
-    float s[4] = {0.f, 0.f, 0.f, 0.f};
+// The dot products of x with U rows y[.], side by side: their loads are in flight together.
+template <int U, class T>
+__device__ __forceinline__ void warp_dots(const T* x, const T* const (&y)[U], int D, int vec, int lane, float (&out)[U]) {
     constexpr int E = 16 / sizeof(T);
+    float s[U][2] = {};
     if (vec) {
-#pragma unroll 4
+#pragma unroll(U == 1 ? 4 : 2)
         for (int i = lane * E; i < D; i += 32 * E) {
-            const uint4 a = *reinterpret_cast<const uint4*>(x + i), b = *reinterpret_cast<const uint4*>(y + i);
-            const T* pa = reinterpret_cast<const T*>(&a);
-            const T* pb = reinterpret_cast<const T*>(&b);
+            const uint4 a = *reinterpret_cast<const uint4*>(x + i);
+            uint4 b[U];
 #pragma unroll
-            for (int j = 0; j < E; ++j) s[j & 3] = fmaf(to_f32(pa[j]), to_f32(pb[j]), s[j & 3]);
+            for (int u = 0; u < U; ++u) b[u] = *reinterpret_cast<const uint4*>(y[u] + i);
+            const T* pa = reinterpret_cast<const T*>(&a);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const T* pb = reinterpret_cast<const T*>(&b[u]);
+#pragma unroll
+                for (int j = 0; j < E; ++j) s[u][j & 1] = fmaf(to_f32(pa[j]), to_f32(pb[j]), s[u][j & 1]);
+            }
         }
     } else {
-#pragma unroll 16
-        for (int i = lane; i < D; i += 32) s[0] = fmaf(to_f32(x[i]), to_f32(y[i]), s[0]);
-    }
-    float t = (s[0] + s[1]) + (s[2] + s[3]);
+#pragma unroll(U == 1 ? 16 : 4)
+        for (int i = lane; i < D; i += 32) {
+            const float a = to_f32(x[i]);
 #pragma unroll
-    for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-    return t;
+            for (int u = 0; u < U; ++u) s[u][0] = fmaf(a, to_f32(y[u][i]), s[u][0]);
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) out[u] = s[u][0] + s[u][1];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) out[u] += __shfl_xor_sync(0xffffffffu, out[u], o);
+    }
+}
+
+template <class T>
+__device__ __forceinline__ float warp_dot(const T* x, const T* y, int D, int vec, int lane) {
+    const T* const rows[1] = {y};
+    float out[1];
+    warp_dots<1>(x, rows, D, vec, lane, out);
+    return out[0];
 }
 
 __device__ __forceinline__ float warp_max(float v) {
@@ -174,6 +196,35 @@ __device__ bool teacher_row(const Target& t, int64_t n, int64_t V, float* q, flo
     return any;
 }
 
+// Scores of a row's teacher entries (but those with q = 0), four to a warp at a time, one
+// where there are warps for that.  give(k, z) is called by one lane per entry.  The entries'
+// rows are scattered reads, bound by how many are in flight: bf16, 2048 rows x 64 entries of
+// width 1024, 268 MB, 45 us (6.0 TB/s); one entry at a time 66 to 80.
+template <int RT, class T, class F>
+__device__ __forceinline__ void entry_scores(const HeadIn& in, int64_t n, int K, const float* q, const int* ids, F give) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const T* h = static_cast<const T*>(in.h) + n * in.ldh;
+    const T* w = static_cast<const T*>(in.w);
+    constexpr int U = RT == kRowThreadsWide ? 1 : 4;
+    for (int k = warp * U; k < K; k += RT / 32 * U) {
+        const T* rows[U];
+        bool some = false;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {  // entries that are not there read the hidden row itself
+            const bool is = k + u < K && q[k + u] != 0.f;
+            rows[u] = is ? w + (int64_t)ids[k + u] * in.ldw : h;
+            some |= is;
+        }
+        if (!some) continue;
+        float z[U];
+        warp_dots<U>(h, rows, in.D, in.vec, lane, z);
+        float mine = z[0];
+#pragma unroll
+        for (int u = 1; u < U; ++u) mine = lane == u ? z[u] : mine;
+        if (lane < U && k + lane < K && q[k + lane] != 0.f) give(k + lane, mine);
+    }
+}
+
 // lse and loss of every row: the strips' pairs joined, the target scores as dot
 // products.  xent: a warp per row; distill: a block per row, a warp per entry.
 template <class T, bool DISTILL, int RT>
@@ -212,11 +263,8 @@ __global__ void __launch_bounds__(RT) k_head_finish(HeadIn in, Target t, const f
         __syncthreads();
         const float l = ls;
         float acc = 0.f;
-        for (int k = warp; k < t.K; k += RT / 32) {
-            if (q[k] == 0.f) continue;
-            const float z = warp_dot(h + n * in.ldh, w + (int64_t)ids[k] * in.ldw, in.D, in.vec, lane);
-            acc += q[k] * (lq[k] - z / t.T + l);
-        }
+        entry_scores<RT, T>(in, n, t.K, q, ids, [&](int k, float z) { acc += q[k] * (lq[k] - z / t.T + l); });
+        acc = warp_sum(acc);
         __syncthreads();
         if (lane == 0) red[warp] = acc;
         __syncthreads();
@@ -280,32 +328,31 @@ __global__ void __launch_bounds__(RT)
     }
     if (n == in.N - 1)
         for (int64_t i = in.N + threadIdx.x; i < (in.N + 127) / 128 * 128; i += RT) nlse[i] = scale[i] = 0.f;
-    for (int k = warp; k < t.K; k += RT / 32) {
-        const int64_t id = DISTILL ? (q[k] == 0.f ? -1 : ids[k]) : xid;
-        float d = 0.f;
-        bool again = false;  // an earlier entry has the same id
-        if (id >= 0) {
-            float qs = 1.f;
-            if (DISTILL) {
-                qs = 0.f;
-                bool earlier = false;
-                for (int j = lane; j < t.K; j += 32)
+    const auto put = [&](int k, int64_t id, float d, bool first) {
+        ids_out[k * in.N + n] = (int)id;
+        dzt[k * in.N + n] = d;
+        if (blocks && id >= 0 && first)
+            add_target(&blocks[(id >> 5) * nblocks + (n >> 5)], ents, (int)(n * t.K + k), (int)(n & 31) | (int)(id & 31) << 5, d);
+    };
+    if (DISTILL) {
+        float* z = sm + t.K;
+        entry_scores<RT, T>(in, n, t.K, q, ids, [&](int k, float x) { z[k] = x; });
+        __syncthreads();
+        for (int k = threadIdx.x; k < t.K; k += RT) {
+            const int id = q[k] == 0.f ? -1 : ids[k];
+            float qs = 0.f;
+            bool first = true;
+            if (id >= 0)
+                for (int j = 0; j < t.K; ++j)
                     if (ids[j] == id && q[j] != 0.f) {
                         qs += q[j];
-                        earlier |= j < k;
+                        first &= j >= k;
                     }
-                qs = warp_sum(qs);
-                again = __any_sync(0xffffffffu, earlier);
-            }
-            const float z = warp_dot(h, w + id * in.ldw, in.D, in.vec, lane);
-            d = (expf(z / t.T - l) - qs) * rs;
+            put(k, id, id >= 0 ? (expf(z[k] / t.T - l) - qs) * rs : 0.f, first);
         }
-        if (lane == 0) {
-            ids_out[k * in.N + n] = (int)id;
-            dzt[k * in.N + n] = d;
-            if (blocks && id >= 0 && !again)
-                add_target(&blocks[(id >> 5) * nblocks + (n >> 5)], ents, (int)(n * t.K + k), (int)(n & 31) | (int)(id & 31) << 5, d);
-        }
+    } else if (warp == 0) {
+        const float z = xid >= 0 ? warp_dot(h, w + xid * in.ldw, in.D, in.vec, lane) : 0.f;
+        if (lane == 0) put(0, xid, xid >= 0 ? (expf(z - l) - 1.f) * rs : 0.f, true);
     }
     const int64_t piece = in.N * in.Dp;
     for (int i = threadIdx.x; i < in.Dp; i += RT) {
@@ -883,9 +930,10 @@ unsigned grid_of(int64_t items, int per_block, int sms, int per_sm) {
     return (unsigned)(b < 1 ? 1 : (b > (int64_t)sms * per_sm ? (int64_t)sms * per_sm : b));
 }
 
-// 16 warps to a row instead of 4: rows whose 4 warps would leave the SMs half empty, with
-// entries enough for more (6 rows x 102 entries of width 2811: 117 -> 33 us)
-bool wide_rows(const Plan& p, int K) { return K >= 16 && p.in.N < 4ll * p.sms; }
+// 16 warps to a row instead of 4, an entry each: rows whose 4 warps would leave the SMs
+// half empty, with entries enough for more.  bf16, 64 entries of width 1024: 200 rows 11 us
+// a launch (4 warps: 14 to 20); fp32, 512 rows x 32 entries of width 128: 14 (4 warps: 9).
+bool wide_rows(const Plan& p, int K) { return K >= 16 && p.in.N < 2ll * p.sms; }
 
 bool launch_ok() { return cudaGetLastError() == cudaSuccess; }
 
