@@ -289,6 +289,16 @@ struct Pow2 {
     float a, b;
     __device__ __forceinline__ explicit Pow2(int e) : a(exp2c(e)), b(exp2c(e - max(-126, min(127, e)))) {}
     __device__ __forceinline__ float operator()(float x) const { return x * b * a; }
+    __device__ __forceinline__ void operator()(float (&v)[32]) const {  // the same in every lane
+        if (b != 1.f) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] *= b;
+        }
+        if (a != 1.f) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) mul2(v[j], v[j + 1], a, a);
+        }
+    }
 };
 __device__ __forceinline__ int amax_exp(const uint32_t* p) { return p ? scale_exp(*p) : 0; }
 
@@ -334,10 +344,16 @@ __device__ __forceinline__ void put_rows(uint4* buf, const uint4 (&mine)[4], uin
 #pragma unroll
     for (int c = 0; c < 4; ++c) buf[lane * 4 + (c ^ ((lane >> 1) & 3))] = mine[c];
     __syncwarp();
+    const int r0 = lane >> 2, c = lane & 3;
+    const uint4* from = buf + r0 * 4 + (c ^ ((r0 >> 1) & 3));  // 8 rows on, the swizzle is the same
+    uint8_t* to = base + r0 * pitch + c * 16;
+    if (rows >= 32) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = i * 8 + (lane >> 2), c = lane & 3;
-        if (r < rows) *reinterpret_cast<uint4*>(base + r * pitch + c * 16) = buf[r * 4 + (c ^ ((r >> 1) & 3))];
+        for (int i = 0; i < 4; ++i, to += 8 * pitch) *reinterpret_cast<uint4*>(to) = from[i * 32];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i, to += 8 * pitch)
+            if (r0 + i * 8 < rows) *reinterpret_cast<uint4*>(to) = from[i * 32];
     }
 }
 __device__ __forceinline__ uint4 bits4(const float* v) {
@@ -362,20 +378,20 @@ __device__ __forceinline__ void put_rows_16(uint4* buf, const float (&v)[32], ui
 // The same for rows that do not begin on 16-byte boundaries, and their last columns: lanes
 // along a row, element by element.  cols: how many of the 32 columns there are.
 __device__ __forceinline__ void put_elements(uint4* buf, const float (&v)[32], void* base, int64_t ld, int64_t rows, int64_t cols, int type) {
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, nrows = (int)min(rows, (int64_t)32), ncols = (int)min(cols, (int64_t)32);
     if (type == TT_F32) {
+        const int k = lane & 15, r0 = lane >> 4;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             __syncwarp();
 #pragma unroll
             for (int c = 0; c < 4; ++c) buf[lane * 4 + (c ^ ((lane >> 1) & 3))] = bits4(v + h * 16 + c * 4);
             __syncwarp();
-            const int k = lane & 15;
+            float* to = static_cast<float*>(base) + r0 * ld + h * 16 + k;
+            if (h * 16 + k < ncols) {
 #pragma unroll 4
-            for (int i = 0; i < 16; ++i) {
-                const int r = i * 2 + (lane >> 4);
-                const float x = reinterpret_cast<const float*>(buf)[r * 16 + ((k >> 2) ^ ((r >> 1) & 3)) * 4 + (k & 3)];
-                if (r < rows && h * 16 + k < cols) static_cast<float*>(base)[r * ld + h * 16 + k] = x;
+                for (int i = 0; i < 16; ++i, to += 2 * ld)
+                    if (i * 2 + r0 < nrows) *to = reinterpret_cast<const float*>(buf)[(i * 2 + r0) * 16 + ((k >> 2) ^ (i & 3)) * 4 + (k & 3)];
             }
         }
     } else {
@@ -385,10 +401,11 @@ __device__ __forceinline__ void put_elements(uint4* buf, const float (&v)[32], v
 #pragma unroll
         for (int c = 0; c < 4; ++c) buf[lane * 4 + (c ^ ((lane >> 1) & 3))] = make_uint4(q[4 * c], q[4 * c + 1], q[4 * c + 2], q[4 * c + 3]);
         __syncwarp();
-#pragma unroll 4
-        for (int r = 0; r < 32; ++r) {
-            const uint16_t x = reinterpret_cast<const uint16_t*>(buf)[r * 32 + ((lane >> 3) ^ ((r >> 1) & 3)) * 8 + (lane & 7)];
-            if (r < rows && lane < cols) static_cast<uint16_t*>(base)[r * ld + lane] = x;
+        uint16_t* to = static_cast<uint16_t*>(base) + lane;
+        if (lane < ncols) {
+#pragma unroll 8
+            for (int r = 0; r < 32; ++r, to += ld)
+                if (r < nrows) *to = reinterpret_cast<const uint16_t*>(buf)[r * 32 + ((lane >> 3) ^ ((r >> 1) & 3)) * 8 + (lane & 7)];
         }
     }
 }
@@ -399,8 +416,7 @@ __device__ __forceinline__ void store_out(const OutArgs& o, uint4* buf, int spli
     const int lane = threadIdx.x & 31;
     const int64_t rows = M - row0;
     if (o.out) {
-#pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = sc(v[j]);
+        sc(v);
         const int64_t at = row0 * o.ldo + col;
         if (o.vec && col + 32 <= N) {
             if (o.type == TT_F32)

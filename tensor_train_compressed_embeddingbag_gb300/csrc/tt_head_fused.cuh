@@ -563,8 +563,7 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
                         float v[32];
                         tm_ld32(l0 + ob * S::kOut + ch * 32, v);
                         tm_wait_ld(v);
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) v[j] = sc(v[j]);
+                        sc(v);
                         pack32(v, q[ch], a.fmt);
                     }
                     tc_fence_before();
