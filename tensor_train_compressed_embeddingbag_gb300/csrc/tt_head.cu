@@ -20,13 +20,14 @@
 // N x (vocabulary piece) is that dz (at most kDzBytes, or 1,024 columns).
 //
 // Types.  bf16 and f16 inputs go to the tensor cores as they are.  An fp32 input x
-// is split as x 2^e = hi + lo with hi, lo in f16 (e a power-of-two scale that puts
-// the largest magnitude near 2^14: of a hidden row in the forward pass, of 128 x 128
-// elements of the table, of all hidden rows that count and of all of dz in the backward pass) and a product is taken as hi hi + hi lo + lo hi,
-// so 22 bits of each operand enter, with fp32 accumulation; lo lo (2^-22 of the
-// product and below) is dropped.  dz is rounded to the inputs' 16-bit type before
-// the two gradient products (by at most 2^-8 or 2^-11 of an entry, independent errors,
-// the size of the gradients' own final rounding), and split like an input for fp32.
+// is split as x 2^e = hi + lo with hi, lo in f16 and a product is taken as hi hi + hi lo +
+// lo hi; e is a power-of-two scale that puts the largest magnitude near 2^14: of a hidden
+// row in the forward pass, of 128 x 128 elements of the table, of all hidden rows that
+// count and of all of dz in the backward pass.  So 22 bits of each operand enter, with
+// fp32 accumulation; lo lo (2^-22 of the product and below) is dropped.  dz is rounded to
+// the inputs' 16-bit type before the two gradient products (by at most 2^-8 or 2^-11 of an
+// entry, independent errors, the size of the gradients' own final rounding), and split
+// like an input for fp32.
 #include <math.h>
 
 #include <type_traits>
@@ -38,7 +39,7 @@
 
 namespace ttemb {
 
-constexpr int64_t kDzBytes = 256ll << 20;  // dz of one vocabulary piece
+constexpr int64_t kDzBytes = 256ll << 20;  // dz of one vocabulary piece: four pieces at 4096 x 131072, where a product fills the SMs many times over
 constexpr int64_t kMaxBlocks = 1ll << 26;    // 32 x 32 blocks of targets (1 GB of them)
 constexpr int kFewMinDim = 256;              // 16-bit rows: k_head_few from this width on
 constexpr int kMaxTeacher = TT_HEAD_MAX_TEACHER;
@@ -368,7 +369,8 @@ __global__ void __launch_bounds__(RT)
     }
 }
 
-// Target entries of dz in columns [v0, v0 + P) of the current piece.
+// Target entries of dz in columns [v0, v0 + P) of the current piece, a thread per entry (2 to
+// 3 us a piece, launch included: nothing to gain).
 __global__ void k_head_fix(const int* ids, const float* dzt, int64_t total, int64_t rows, int v0, int P, uint16_t* dz,
                            int64_t pitch, int64_t piece, int fmt, int split) {
     const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
@@ -417,7 +419,7 @@ __device__ __forceinline__ void split8(const float (&x)[8], float sc, uint16_t* 
 //                   pieces, a scale per block of 128 x 128 (k_head_fused to D = 64: 256 rows), its
 //                   exponent in wexp: what the products take of the table between two
 //                   read-outs, so that a scale is one factor there; a block is read once and
-//                   kept in registers)
+//                   kept in registers: 512 MB in and out for 10^6 x 64 in 89 us, 5.7 TB/s)
 //   blockIdx.y = 1  forward: the hidden rows packed, a warp per row (fp32: a scale of each
 //                   row's own, its exponent in row_exp); backward: the largest finite
 //                   |grad| T and (fp32) |hidden| over the rows that count, a share per block
@@ -822,9 +824,10 @@ tt_status make_plan(const tt_head* hd, int K, bool buffers, Plan* p) {
     }
     // few rows: a pass over the table as it is per eight of them, when its rows can be read
     // 4 bytes at a time.  Measured against the other kernels, rows x table: bf16 4 x 131072
-    // x 4096 187 us (253), 8 x 131072 x 1024 59 (71), but 8 x 10^6 x 64 55 (38), where a tile's
-    // end outweighs its loads; fp32, which the others copy in pieces first, 8 x 131072 x 1024
-    // 109 (434), 16 rows in two passes 218 (484), 8 x 10^6 x 64 73 (144), 16 rows 146 (144).
+    // x 4096 188 us (251), 8 x 131072 x 1024 61 (70), x 256 59 (59), but x 128 40 (34) and
+    // 8 x 10^6 x 64 55 (38), where a tile's end outweighs its loads; fp32, which the others
+    // copy in pieces first, 8 x 131072 x 1024 116 (432), 16 rows in two passes 227 (463),
+    // 8 x 10^6 x 64 71 (144), 16 rows 135 (144).
     const int64_t chunks = cdiv((int64_t)in.D * p->esize, 64);
     p->few_smem = (size_t)(chunks * 512);
     p->few = in.N > 0 && in.N <= (p->split ? 16 : 8) && (p->split || in.D >= kFewMinDim) && (uintptr_t)in.w % 4 == 0 &&

@@ -26,11 +26,11 @@
 // Y at a time, its small products in columns of their own where there is room, and its
 // sums are kept in the storing warps' registers (k_head_gemm says why).  Sums read
 // every tile instead of every second one: dweight of 512 x 1,000,000 x 64 took 315 us,
-// here 267.
+// here 256.
 //
 // Measured, us and TFLOP/s of its 2 N V D (kLse) or 4 N V D products (SPLIT: x 3):
-// bf16 4096 x 100003 x 128 dhidden 118 (1770), dweight 144 (1460); fp32 512 x 1,000,000 x
-// 64 lse 143 (1380), dhidden 241 (1630), dweight 267 (1470).  The tensor pipe is 60 to 70%
+// bf16 4096 x 100003 x 128 dhidden 118 (1770), dweight 142 (1480); fp32 512 x 1,000,000 x
+// 64 lse 140 (1400), dhidden 236 (1670), dweight 256 (1540).  The tensor pipe is 60 to 70%
 // busy and what bounds them; the rest is fill and drain of the tiles' way above.
 #pragma once
 

@@ -22,6 +22,12 @@
 // share of a group is one contiguous load of group / 8 bytes per table row, and x lies in
 // shared memory in the order in which the fragments want it.  A warp takes 32 table rows
 // at a time and keeps the loads of the next groups, of this tile or the next, in flight.
+//
+// Measured: 1 x 131072 x 4096, groups of 128, bf16 x: 277 MB in 63 us (4.4 TB/s; floor 41);
+// 8 x 1,000,000 x 64, groups of 32, fp32 x: 68 MB in 19.7 us (floor 10).  The ALU that
+// turns codes into f16 is 46 and 48% busy, half of all issue slots go, and a warp waits
+// mostly on its own last instruction: both bounds are near, neither is reached.  Codes as
+// f16 subnormals would spare the OR, but lose the scale's low bits.
 #include <type_traits>
 
 #include "tt_head.cuh"
