@@ -42,6 +42,10 @@ namespace ttemb {
 constexpr int64_t kDzBytes = 256ll << 20;  // dz of one vocabulary piece: four pieces at 4096 x 131072, where a product fills the SMs many times over
 constexpr int64_t kMaxBlocks = 1ll << 26;    // 32 x 32 blocks of targets (1 GB of them)
 constexpr int kFewMinDim = 256;              // 16-bit rows: k_head_few from this width on
+// 16-bit types, this many targets in all: their share of the gradients in fp32.  Error of the
+// gradients against their rounding alone (bf16, 2 x 90656 x 812; worst of six): 2.3 without,
+// 1.0 here; with more targets it is 1.4 to 1.5 and steady.  It costs a launch of 3 to 12 us.
+constexpr int kFewTargets = 64;
 constexpr int kMaxTeacher = TT_HEAD_MAX_TEACHER;
 
 // ---------------------------------------------------------------- rows and copies
@@ -563,11 +567,52 @@ __global__ void __launch_bounds__(TH, 1024 / TH) k_head_prep(const __grid_consta
     }
 }
 
+// Row id of dweight for every target id, from fp32 dz (Residue says why): a block per entry,
+// the first one with its id.
+template <class T>
+__global__ void __launch_bounds__(256) k_head_target_rows(HeadIn in, const int* ids, const float* dzt, int K, const float* nlse, const float* scale, float c,
+                                                          const uint32_t* amax_z, void* out, int type) {
+    __shared__ float dz[kFewTargets];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, N = (int)in.N;
+    const int id = ids[blockIdx.x];
+    if (id < 0) return;
+    static_assert(kFewTargets <= 256, "an entry per thread");
+    if (__syncthreads_or(threadIdx.x < blockIdx.x && ids[threadIdx.x] == id)) return;
+    const T* h = static_cast<const T*>(in.h);
+    const T* w = static_cast<const T*>(in.w) + (int64_t)id * in.ldw;
+    for (int n0 = warp * 4; n0 < N; n0 += 32) {
+        const T* rows[4];
+        float z[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) rows[u] = h + min(n0 + u, N - 1) * in.ldh;
+        warp_dots<4>(w, rows, in.D, in.vec, lane, z);
+        const float mine = lane & 2 ? (lane & 1 ? z[3] : z[2]) : (lane & 1 ? z[1] : z[0]);
+        const int n = n0 + lane;
+        if (lane < 4 && n < N) {
+            float d = scale[n] != 0.f ? scale[n] * ex2(fmaf(mine, c, nlse[n])) : 0.f;
+            for (int k = 0; k < K; ++k)
+                if (ids[k * N + n] == id) d = dzt[k * N + n];
+            dz[n] = d;
+        }
+    }
+    __syncthreads();
+    const Pow2 sc(-amax_exp(amax_z));
+    for (int i = threadIdx.x; i < in.D; i += 256) {
+        float s = 0.f;
+#pragma unroll 8
+        for (int n = 0; n < N; ++n) {
+            const float x = to_f32(h[n * in.ldh + i]);
+            s = dz[n] != 0.f ? fmaf(dz[n], x, s) : s;  // a row that does not count may hold anything
+        }
+        store_one(out, (int64_t)id * in.D + i, sc(s), type);
+    }
+}
+
 // out[m, n] = the splits' partial sums, in split order, unscaled and rounded once.  A
 // block takes 256 >> row_shift rows at a time, 1 << row_shift threads to a row, four
 // columns a thread.
 __global__ void __launch_bounds__(256) k_head_reduce(const float* partial, int splits, int64_t M, int64_t N, int64_t pp, OutArgs to, int row_shift,
-                                                     const uint32_t* amax_a, const uint32_t* amax_b) {
+                                                     const uint32_t* amax_a, const uint32_t* amax_b, Residue low) {
     const Pow2 sc(-amax_exp(amax_a) - amax_exp(amax_b));
     const int per = 1 << row_shift, c0 = ((int)threadIdx.x & (per - 1)) * 4;
     for (int64_t m = (int64_t)blockIdx.x * (256 >> row_shift) + (threadIdx.x >> row_shift); m < M; m += (int64_t)gridDim.x * (256 >> row_shift))
@@ -579,7 +624,12 @@ __global__ void __launch_bounds__(256) k_head_reduce(const float* partial, int s
                 const float4 y = *reinterpret_cast<const float4*>(p + (int64_t)k * M * pp);
                 s = make_float4(s.x + y.x, s.y + y.y, s.z + y.z, s.w + y.w);
             }
-            const float v[4] = {sc(s.x), sc(s.y), sc(s.z), sc(s.w)};
+            float v[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (low.K && n + j < N) v[j] += low(m, (int)n + j);
+                v[j] = sc(v[j]);
+            }
             const int64_t at = m * to.ldo + n;
             if (to.vec && n + 4 <= N) {
                 if (to.type == TT_F32)
@@ -705,7 +755,7 @@ bool run_fused(const Operand& X, const Operand& Y, FusedArgs a, int dev, cudaStr
     const unsigned gx = (unsigned)(by_boundary ? a.runs.blocks - 1 : a.runs.xtiles);
     const unsigned gy = gx >= 256 ? 1 : (gx >= 64 ? 4 : (gx >= 16 ? 16 : 64));  // a block or more per SM
     k_head_join<<<dim3(gx, gy), 128, 0, st>>>(a.runs, by_boundary, a.partial, a.to, a.X, a.D, SPLIT && MODE == kDhidden ? nullptr : a.amax_z,
-                                              MODE == kDweight ? a.amax_h : nullptr);
+                                              MODE == kDweight ? a.amax_h : nullptr, a.low);
     return cudaGetLastError() == cudaSuccess;
 }
 
@@ -770,6 +820,7 @@ struct Plan {
     int64_t pitch;           // its row pitch in dz
     int dh_splits, dw_splits;
     bool dh_direct;
+    bool few_targets;        // their elements of dz are not left at 16 bits
     int64_t pp;              // row pitch of partial sums
 };
 
@@ -853,6 +904,7 @@ tt_status make_plan(const tt_head* hd, int K, bool buffers, Plan* p) {
         p->pack_h_fwd = p->pack_w_fwd = false;
     }
     // backward
+    p->few_targets = !p->split && in.N * K <= kFewTargets;
     p->nblocks = cdiv(in.N, 32);
     p->vblocks = cdiv(in.V, 32);
     p->fused = in.D <= 128 && p->nblocks * p->vblocks <= kMaxBlocks;
@@ -880,7 +932,7 @@ tt_status make_plan(const tt_head* hd, int K, bool buffers, Plan* p) {
         const int bn = p->split ? 128 : 256;
         const int64_t nt = cdiv(in.D, bn), lastP = in.V - (cdiv(in.V, P) - 1) * P;
         p->dh_splits = choose_splits(mt * nt, cdiv(lastP, kBK), in.N * in.D, p->sms);
-        p->dh_direct = p->dh_splits == 1 && in.V <= P;
+        p->dh_direct = p->dh_splits == 1 && in.V <= P && !p->few_targets;
         p->dw_splits = choose_splits(cdiv(P, 128) * nt, cdiv(in.N, kBK), P * in.D, p->sms);
     }
     p->pp = cdiv(in.D, 32) * 32;
@@ -1104,12 +1156,20 @@ tt_status head_backward(const Plan& p, const Target& t, const float* lse, const 
         o.pp = p.pp;
         return o;
     };
-    const auto reduce = [&](const float* partial, int splits, int64_t rows, void* out, const uint32_t* ay) {
+    const Residue none{}, low = p.few_targets ? Residue{w.ids, w.dzt, in.w, in.ldw, in.N, t.K, p.fmt} : none;
+    // the rows of dweight that the few targets name, again (k_head_target_rows)
+    const auto target_rows = [&] {
+        if constexpr (sizeof(T) == 2)
+            if (p.few_targets)
+                k_head_target_rows<T><<<(unsigned)(in.N * t.K), 256, 0, st>>>(in, w.ids, w.dzt, t.K, w.nlse, w.scale, kLog2e / t.T, az, dw, p.type);
+        return launch_ok();
+    };
+    const auto reduce = [&](const float* partial, int splits, int64_t rows, void* out, const uint32_t* ay, const Residue& lw) {
         int shift = 3;
         while (shift < 8 && (4 << shift) < in.D) ++shift;
         // fp32's are in their own units already
         k_head_reduce<<<grid_of(rows, 256 >> shift, p.sms, 16), 256, 0, st>>>(partial, splits, rows, in.D, p.pp, dest(out, nullptr), shift,
-                                                                            p.split ? nullptr : az, p.split ? nullptr : ay);
+                                                                            p.split ? nullptr : az, p.split ? nullptr : ay, lw);
         return launch_ok();
     };
     if (p.fused) {
@@ -1138,7 +1198,8 @@ tt_status head_backward(const Plan& p, const Target& t, const float* lse, const 
         if (!fused<kDweight>(p.split, W, H, a, p.device, st)) return TT_ERR_CUDA;
         a.runs = p.runs_dh;
         a.to = dest(dh, nullptr);
-        return fused<kDhidden>(p.split, H, W, a, p.device, st) ? TT_OK : TT_ERR_CUDA;
+        a.low = low;
+        return fused<kDhidden>(p.split, H, W, a, p.device, st) && target_rows() ? TT_OK : TT_ERR_CUDA;
     }
     const int64_t npieces = cdiv(in.V, p.P), dz_piece = in.N * p.pitch;
     for (int64_t i = 0; i < npieces; ++i) {
@@ -1173,7 +1234,7 @@ tt_status head_backward(const Plan& p, const Target& t, const float* lse, const 
         void* dwp = static_cast<uint8_t*>(dw) + (size_t)v0 * in.D * p.esize;
         b.to = dest(p.dw_splits > 1 ? nullptr : dwp, w.dw_part);
         if (!out_gemm<true>(p.split, Z, H, b, p.sms, p.device, st)) return TT_ERR_CUDA;
-        if (p.dw_splits > 1 && !reduce(w.dw_part, p.dw_splits, P, dwp, ah)) return TT_ERR_CUDA;
+        if (p.dw_splits > 1 && !reduce(w.dw_part, p.dw_splits, P, dwp, ah, none)) return TT_ERR_CUDA;
 
         GemmArgs c = gemm_args(p, err);  // the piece's share of dhidden: [N][D] += dz W
         c.M = in.N;
@@ -1187,8 +1248,8 @@ tt_status head_backward(const Plan& p, const Target& t, const float* lse, const 
         c.to.accumulate = i > 0;
         if (!out_gemm<false>(p.split, Z, W, c, p.sms, p.device, st)) return TT_ERR_CUDA;
     }
-    if (!p.dh_direct && !reduce(w.dh_part, p.dh_splits, in.N, dh, nullptr)) return TT_ERR_CUDA;
-    return TT_OK;
+    if (!p.dh_direct && !reduce(w.dh_part, p.dh_splits, in.N, dh, nullptr, low)) return TT_ERR_CUDA;
+    return target_rows() ? TT_OK : TT_ERR_CUDA;
 }
 
 tt_status forward_any(const tt_head* hd, const Target& t, float* loss, float* lse, int* err, void* ws, size_t n, tt_stream s) {

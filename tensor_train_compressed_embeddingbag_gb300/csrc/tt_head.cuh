@@ -410,6 +410,33 @@ __device__ __forceinline__ void put_elements(uint4* buf, const float (&v)[32], v
     }
 }
 
+// The target elements of dz lose their low bits in 16 bits.  Over many rows these
+// roundings average out; with few targets in the whole batch the gradients carry each of
+// them whole (up to 2^-8 or 2^-11, where their own rounding is of that size at most), so
+// what they lost is added where dhidden's fp32 sums are joined.  K = 0: not done.
+struct Residue {
+    const int* ids;    // [K][rows]
+    const float* dzt;
+    const void* w;
+    int64_t ldw, rows;
+    int K, fmt;
+    // of dhidden[n][c]
+    __device__ __forceinline__ float operator()(int64_t n, int c) const {
+        float s = 0.f;
+        for (int k = 0; k < K; ++k) {
+            const int id = ids[k * rows + n];
+            bool first = id >= 0;  // the same id further on is the same element
+            for (int j = 0; j < k; ++j) first &= ids[j * rows + n] != id;
+            if (!first) continue;
+            const float x = dzt[k * rows + n];
+            const uint32_t b = pack16(x, 0.f, fmt) & 0xFFFFu;
+            const uint16_t y = static_cast<const uint16_t*>(w)[id * ldw + c];
+            s = fmaf(x - (fmt ? __uint_as_float(b << 16) : unpack_f16(b).x), fmt ? __uint_as_float((uint32_t)y << 16) : unpack_f16(y).x, s);
+        }
+        return s;
+    }
+};
+
 // Columns [col, col + 32), col < N, of a warp's 32 rows from row0 < M on, a row per lane.
 __device__ __forceinline__ void store_out(const OutArgs& o, uint4* buf, int split, int64_t row0, int64_t col, int64_t M, int64_t N, float (&v)[32],
                                           Pow2 sc) {

@@ -95,6 +95,7 @@ struct FusedArgs {
     const float* dzt;
     int K;
     int64_t rows;
+    Residue low;             // kDhidden: for k_head_join
     int nblocks, vblocks;
     OutArgs to;              // whole segments; others as fp32 sums to
     float* partial;          //   [blocks][2][128][to.pp]: the run's first segment, its last
@@ -626,7 +627,7 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
 // than runs) the boundary between two runs that lies in it; the first boundary inside
 // an x takes it.
 __global__ void __launch_bounds__(128) k_head_join(Runs runs, int by_boundary, const float* partial, OutArgs to, int64_t X, int D,
-                                                   const uint32_t* amax_z, const uint32_t* amax_y) {
+                                                   const uint32_t* amax_z, const uint32_t* amax_y, Residue low) {
     __shared__ int sh[4];
     if (threadIdx.x == 0) {
         int64_t x = blockIdx.x;
@@ -667,7 +668,10 @@ __global__ void __launch_bounds__(128) k_head_join(Runs runs, int by_boundary, c
             const float4 v = *reinterpret_cast<const float4*>(p + k * step);
             s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
         }
-        const float v[4] = {s.x, s.y, s.z, s.w};
+        float v[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (low.K && c + j < D) v[j] += low(x * 128 + r, c + j);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             if (c + j < D) store_one(to.out, (x * 128 + r) * to.ldo + c + j, sc(v[j]), to.type);

@@ -62,6 +62,35 @@ def test_xent(size, dtype):
     ref.check(run_xent(h, w, t, grad), ref.xent(h, w, t, grad=grad))
 
 
+@pytest.mark.parametrize("dtype", TYPES[1:])
+@pytest.mark.parametrize("size", [(1, 5000, 300), (3, 4000, 64), (4, 9000, 200), (31, 2000, 129), (64, 700, 72)])
+def test_few_targets_keep_their_low_bits(size, dtype):
+    """The bound of the gradients without the 16-bit rounding of dz at the targets: in dweight's
+    rows that a target names no entry of dz is rounded, in dhidden all others are."""
+    h, w, t, grad = inputs(*size, dtype, seed=21)
+    t[0], u = 7, ref.U[dtype]
+    t[-1] = t[0]
+    got = run_xent(h, w, t, grad)
+    z = ref.scores(h, w)
+    lse = torch.logsumexp(z, 1)
+    keep = t >= 0
+    q = torch.zeros_like(z)
+    q[keep.nonzero()[:, 0], t[keep]] = 1.0
+    g = torch.where(keep, grad.double(), torch.zeros_like(lse))[:, None]
+    dz = g * (torch.exp(z - lse[:, None]) - q)
+    ez, el = ref.bounds(h, w, lse)
+    off = (ez + el + 2.0 ** -20)[:, None] * g.abs() * (torch.exp(z - lse[:, None]) + q) + 2.0 ** -38 * grad.abs().max()
+    add = max(size) * 2.0 ** -27  # fp32 accumulation
+    hd, wd = h.double(), w.double()
+    want = dz.t() @ hd
+    bound = u * want.abs() + (off + add * dz.abs()).t() @ hd.abs() + 2.0 ** -25
+    rows = t[keep].unique()
+    assert ((got["grad_weight"].double() - want).abs() <= bound)[rows].all()
+    want = dz @ wd
+    bound = u * want.abs() + (off + (add + u * (1 - q)) * dz.abs()) @ wd.abs() + 2.0 ** -25
+    assert ((got["grad_hidden"].double() - want).abs() <= bound).all()
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("size,k,temp", [((1, 1, 1), 1, 1.0), ((8, 120, 8), 5, 1.0), ((63, 65, 16), 65, 2.0), ((130, 300, 64), 8, 2.0),
                                          ((129, 257, 65), 32, 4.0), ((140, 300, 129), 100, 0.5), ((7, 900, 256), 64, 2.0),
