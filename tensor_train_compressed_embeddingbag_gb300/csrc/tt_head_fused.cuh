@@ -35,6 +35,7 @@
 #pragma once
 
 #include "tt_head.cuh"
+#include "tt_head_pipe.cuh"
 
 namespace ttemb {
 
@@ -185,18 +186,19 @@ __device__ __noinline__ void put_targets(const FusedArgs& a, uint32_t t0, uint4 
     }
 }
 
-// kLse has no OUT: a tile's dz warps free its S, and its stage is free once S is formed.
+// kLse has no OUT: a tile's dz warps free its S, and its stage is free once S is formed (tt_head_pipe.cuh).
 template <int DT, bool SPLIT, int MODE>
 __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
     k_head_fused(const __grid_constant__ CUtensorMap mapX, const __grid_constant__ CUtensorMap mapY,
                  const __grid_constant__ FusedArgs a) {
     using S = FusedShape<DT, SPLIT>;
+    using Pipe = TilePipe<S::kStages, S::NS, MODE == kLse>;
     constexpr bool COLS = MODE == kDweight;  // hidden rows are columns of S: lse and scale go by column
     constexpr int BY = S::BY, NS = S::NS, OB = S::OB, kSegs = SPLIT ? 3 : 1;
     extern __shared__ uint8_t raw[];
-    // by stage: sfull: S of the tile is formed; odone: its OUT is done (the stage and S are free)
-    __shared__ uint64_t xfull[S::XB], xempty[S::XB], yfull[S::kStages], sfull[S::kStages], odone[S::kStages];
-    __shared__ uint64_t pready[NS], ofull[OB], oempty[OB], drain[3];
+    // of the tiles, as Pipe has them: loaded, formed, done, turned
+    __shared__ uint64_t xfull[S::XB], xempty[S::XB], yfull[S::kStages], sfull[Pipe::kFormed], odone[S::kStages];
+    __shared__ uint64_t pready[Pipe::kTurned], ofull[OB], oempty[OB], drain[3];
     // what a dz warp needs of memory for a tile, and for the next: -lse and scale of its
     // columns (COLS) or rows, the targets of its two 32 x 32 blocks
     struct Ahead {
@@ -209,6 +211,9 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
     __shared__ uint32_t tmem_slot;
     __shared__ int gave_up_s;
     volatile int* gave_up = &gave_up_s;
+    const auto formed = [&](uint32_t t) { return head_wait(&sfull[Pipe::formed(t).bar], Pipe::formed(t).n & 1, a.wait_ns, gave_up); };
+    const auto done = [&](uint32_t t) { return head_wait(&odone[Pipe::done(t).bar], Pipe::done(t).n & 1, a.wait_ns, gave_up); };
+    const auto turned = [&](uint32_t t) { return head_wait(&pready[Pipe::turned(t).bar], Pipe::turned(t).n & 1, a.wait_ns, gave_up); };
     const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
     const uint32_t ybase = base + S::XB * S::kX;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -221,12 +226,10 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
         }
         for (int i = 0; i < S::kStages; ++i) {
             mbar_init(&yfull[i], 1);
-            mbar_init(&sfull[i], 1);
             mbar_init(&odone[i], 1);
         }
-        for (int i = 0; i < NS; ++i) {
-            mbar_init(&pready[i], S::kDzSet);
-        }
+        for (int i = 0; i < Pipe::kFormed; ++i) mbar_init(&sfull[i], 1);
+        for (int i = 0; i < Pipe::kTurned; ++i) mbar_init(&pready[i], S::kDzSet);
         for (int i = 0; i < OB; ++i) {
             mbar_init(&ofull[i], 1);
             mbar_init(&oempty[i], 8);
@@ -279,7 +282,7 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
                 ++xu;
             }
             const uint32_t st = g % S::kStages;
-            ok = head_wait(MODE == kLse ? &sfull[st] : &odone[st], ((g / S::kStages) & 1) ^ 1, a.wait_ns, gave_up);
+            ok = g < S::kStages || done(g - S::kStages);
             if (!ok) break;
             if (lead) {
                 bulk_expect(&yfull[st], S::kY);
@@ -298,11 +301,7 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
                 if (!ok) break;
             }
             if ((g & 1) == turn) {
-                if (g >= NS) {  // S of tile g - NS is done with
-                    const uint32_t o = g - NS;
-                    ok = MODE == kLse ? head_wait(&pready[sb], (o / NS) & 1, a.wait_ns, gave_up)
-                                      : head_wait(&odone[o % S::kStages], (o / S::kStages) & 1, a.wait_ns, gave_up);
-                }
+                if (g >= NS) ok = MODE == kLse ? turned(g - NS) : done(g - NS);  // S of tile g - NS is done with
                 ok = ok && head_wait(&yfull[st], (g / S::kStages) & 1, a.wait_ns, gave_up);
                 if (!ok) break;
                 tc_fence_after();
@@ -317,7 +316,8 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
                             mma_f16(d, sx + (((k >> 2) * S::kXBlock + (k & 3) * 32) >> 4),
                                     sy + (((k >> 2) * S::kYBlock + (k & 3) * 32) >> 4), idesc, seg > 0 || k > 0, lead);
                 }
-                mma_commit(&sfull[st], lead);
+                mma_commit(&sfull[Pipe::formed(g).bar], lead);
+                if (MODE == kLse) mma_commit(&odone[st], lead);
             }
             if (w.y + 1 == w.y1) {
                 mma_commit(&xempty[b], lead);  // nothing but S reads X
@@ -332,7 +332,7 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
             const uint32_t st = g % S::kStages, sb = g % NS, ob = fl % OB;
             const bool first = w.y == w.y0 || (SPLIT && !(w.y & 1)), last = w.y + 1 == w.y1 || (SPLIT && (w.y & 1));
             if (first) ok = head_wait(&oempty[ob], ((fl / OB) & 1) ^ 1, a.wait_ns, gave_up);
-            ok = ok && head_wait(&pready[sb], (g / NS) & 1, a.wait_ns, gave_up);
+            ok = ok && turned(g);
             if (!ok) break;
             tc_fence_after();
             const uint32_t d = tmem + S::kOutCol + ob * S::kOut, p = tmem + sb * BY;
@@ -379,7 +379,7 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
             if ((g & 1) == set) {
                 const uint32_t sb = g % NS;
                 const int64_t left = a.Y - ((int64_t)w.y * BY + part * 64);
-                ok = head_wait(&sfull[g % S::kStages], (g / S::kStages) & 1, a.wait_ns, gave_up);
+                ok = formed(g);
                 if (!ok) break;
                 tc_fence_after();
 #pragma unroll
@@ -390,7 +390,7 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
                     if (ch == 1) {
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(&pready[sb]);
+                        if (lane == 0) mbar_arrive(&pready[Pipe::turned(g).bar]);
                     }
                     take_scores(v, left - ch * 32, c, run_m, run_s);
                 }
@@ -438,7 +438,7 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
             fetch(w, ahead[warp - 12][now ^ 1]);
             const float c = SPLIT ? a.ctemp * exp2c(-he - my.wexp[0]) : a.ctemp;
             const float l = my.nlse[lane], r = my.scale[lane];  // of this lane's row (not COLS)
-            ok = head_wait(&sfull[g % S::kStages], (g / S::kStages) & 1, a.wait_ns, gave_up);
+            ok = formed(g);
             if (!ok) break;
             tc_fence_after();
 #pragma unroll
@@ -493,7 +493,7 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
             tm_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&pready[sb]);
+            if (lane == 0) mbar_arrive(&pready[Pipe::turned(g).bar]);
         }
     } else if (MODE != kLse && warp >= 4) {
         const int half = warp >= 8, quad = warp & 3;
