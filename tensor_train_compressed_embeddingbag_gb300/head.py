@@ -76,10 +76,16 @@ def _stream_now(device_index: int):
     return _raw_stream(device_index) if _raw_stream is not None else _stream(None)
 
 
-def _matrix(t: torch.Tensor, what: str) -> torch.Tensor:
-    """A 2-D CUDA tensor of a supported type whose rows are contiguous (a copy where they are not)."""
+def _device(t: torch.Tensor, what: str) -> torch.device:
+    """The device of a CUDA tensor of a supported type."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in _DTYPES:
         _refuse(TT_ERR_ARG, f"{what} must be a float32, bfloat16 or float16 CUDA tensor")
+    return t.device
+
+
+def _matrix(t: torch.Tensor, what: str) -> torch.Tensor:
+    """A 2-D CUDA tensor of a supported type whose rows are contiguous (a copy where they are not)."""
+    _device(t, what)
     if t.dim() != 2 or t.shape[1] < 1:
         _refuse(TT_ERR_SHAPE, f"{what} must be [rows, dim] with dim >= 1")
     if t.is_contiguous():
@@ -135,14 +141,15 @@ _here = contextlib.nullcontext()
 
 
 def _on(stream, device):
-    """The call's stream and device are current, so that what it allocates belongs to that stream."""
+    """The call's stream and device are current: what it allocates belongs to that stream, and what it copies of its
+    arguments is copied there, before its kernels and with memory that no other stream takes meanwhile."""
     return _here if stream is None and device.index == torch.cuda.current_device() else _current(stream, device)
 
 
 def tt_emb_head_workspace(hidden: torch.Tensor, weight: torch.Tensor, teacher_k: int = 1, backward: bool = False) -> int:
     """Bytes of workspace that a forward or backward call on these tensors takes."""
-    h, w, d = _head(hidden, weight)
-    with _on(None, h.device):
+    with _on(None, _device(hidden, "hidden")):
+        h, w, d = _head(hidden, weight)
         return _workspace_bytes(d, teacher_k, backward)
 
 
@@ -154,9 +161,10 @@ def _workspace_bytes(d: _Head, k: int, backward: bool) -> int:
 
 
 def _forward(name, hidden, weight, target, err, stream):
-    h, w, d = _head(hidden, weight)
-    device, rows = h.device, d.rows
+    device = _device(hidden, "hidden")
     with _on(stream, device):
+        h, w, d = _head(hidden, weight)
+        rows = d.rows
         k, args, keep = target(rows, device)
         n = _workspace_bytes(d, k, False)
         loss = torch.empty(rows, dtype=torch.float32, device=device)
@@ -170,9 +178,10 @@ def _forward(name, hidden, weight, target, err, stream):
 
 
 def _backward(name, hidden, weight, target, lse, grad_loss, err, stream):
-    h, w, d = _head(hidden, weight)
-    device, rows = h.device, d.rows
+    device = _device(hidden, "hidden")
     with _on(stream, device):
+        h, w, d = _head(hidden, weight)
+        rows = d.rows
         k, args, keep = target(rows, device)
         lse = _vector(lse, torch.float32, (rows,), device, "lse")
         grad_loss = _vector(grad_loss, torch.float32, (rows,), device, "grad_loss")
@@ -250,11 +259,11 @@ def tt_emb_head_set_wait_limit(ns: int):
 
 def tt_emb_q4_quantize(weight: torch.Tensor, group: int = 64, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """(packed uint8 [vocab, ceil(dim / 32) * 16], scales bfloat16 [vocab, ceil(dim / group)]) of a dense table."""
-    w = _matrix(weight, "weight")
-    V, D, group = w.shape[0], w.shape[1], int(group)
-    if V < 1 or group not in (32, 64, 128):
-        _refuse(TT_ERR_SHAPE, "weight must have rows and group must be 32, 64 or 128")
-    with _on(stream, w.device):
+    with _on(stream, _device(weight, "weight")):
+        w = _matrix(weight, "weight")
+        V, D, group = w.shape[0], w.shape[1], int(group)
+        if V < 1 or group not in (32, 64, 128):
+            _refuse(TT_ERR_SHAPE, "weight must have rows and group must be 32, 64 or 128")
         packed = torch.empty((V, (D + 31) // 32 * 16), dtype=torch.uint8, device=w.device)
         scales = torch.empty((V, (D + group - 1) // group), dtype=torch.bfloat16, device=w.device)
         _check(_c("tt_emb_q4_quantize")(w.data_ptr(), _row_stride(w), V, D, _DTYPES[w.dtype], group, packed.data_ptr(), scales.data_ptr(),
@@ -265,16 +274,17 @@ def tt_emb_q4_quantize(weight: torch.Tensor, group: int = 64, stream=None) -> Tu
 def tt_emb_q4_matvec(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, group: int, out: Optional[torch.Tensor] = None,
                      stream=None) -> torch.Tensor:
     """Scores float32 [rows, vocab] of the rows of x [rows, dim] (float32, bfloat16, float16) against a 4-bit table."""
-    x = _matrix(x, "x")
-    (M, D), device = x.shape, x.device
-    if group not in (32, 64, 128):
-        _refuse(TT_ERR_SHAPE, "group must be 32, 64 or 128")
-    V = packed.shape[0] if isinstance(packed, torch.Tensor) and packed.dim() == 2 else 0
-    if V < 1:
-        _refuse(TT_ERR_SHAPE, "packed must be [vocab, bytes] with vocab >= 1")
-    packed = _vector(packed, torch.uint8, (V, (D + 31) // 32 * 16), device, "packed")
-    scales = _vector(scales, torch.bfloat16, (V, (D + group - 1) // group), device, "scales")
+    device = _device(x, "x")
     with _on(stream, device):
+        x = _matrix(x, "x")
+        M, D = x.shape
+        if group not in (32, 64, 128):
+            _refuse(TT_ERR_SHAPE, "group must be 32, 64 or 128")
+        V = packed.shape[0] if isinstance(packed, torch.Tensor) and packed.dim() == 2 else 0
+        if V < 1:
+            _refuse(TT_ERR_SHAPE, "packed must be [vocab, bytes] with vocab >= 1")
+        packed = _vector(packed, torch.uint8, (V, (D + 31) // 32 * 16), device, "packed")
+        scales = _vector(scales, torch.bfloat16, (V, (D + group - 1) // group), device, "scales")
         if out is None:
             out = torch.empty((M, V), dtype=torch.float32, device=device)
         elif out.shape != (M, V) or out.dtype != torch.float32 or out.device != device or not out.is_contiguous():
