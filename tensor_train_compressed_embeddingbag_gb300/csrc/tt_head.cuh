@@ -218,19 +218,20 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // Running maximum and sum of exp over one more 32 scores of a row, of which the first
-// `valid` count: v in units of which c makes log2 units (c > 0), the maximum in v's.
+// `valid` count.  v is in units of which c makes log2 units (c > 0); the maximum is kept in
+// log2 units, which are the same for every tile of the table whatever its scale.
 __device__ __forceinline__ void take_scores(float (&v)[32], int64_t valid, float c, float& run_m, float& run_s) {
     if (valid < 32) {
 #pragma unroll
         for (int j = 0; j < 32; ++j)
             if (j >= valid) v[j] = -INFINITY;
     }
-    float mx[4] = {run_m, -INFINITY, -INFINITY, -INFINITY};
+    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
     for (int j = 0; j < 32; j += 2) mx[(j >> 1) & 3] = fmaxf(fmaxf(mx[(j >> 1) & 3], v[j]), v[j + 1]);
-    const float mn = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-    const float m2 = mn == -INFINITY ? 0.f : mn * c;
-    float s[4] = {run_s * ex2(fmaf(run_m, c, -m2)), 0.f, 0.f, 0.f};
+    const float mn = fmaxf(run_m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c);
+    const float m2 = mn == -INFINITY ? 0.f : mn;
+    float s[4] = {run_s * ex2(run_m - m2), 0.f, 0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < 32; j += 4) {
         fma2(v[j], v[j + 1], c, c, -m2, -m2);

@@ -362,8 +362,8 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
         }
     } else if (MODE == kLse && warp >= 12) {
         const int set = (warp - 12) / S::kDzSet, quad = warp & 3, part = (warp - 12) % S::kDzSet >> 2;  // its 32 rows and 64 columns
-        float c = a.ctemp, run_m = -INFINITY, run_s = 0.f;  // run_m in units of c
-        int he = 0, we = 0, we_next = SPLIT && w.left ? __ldg(&a.wexp[w.y >> 1]) : 0;
+        float c = a.ctemp, run_m = -INFINITY, run_s = 0.f;
+        int he = 0, we_next = SPLIT && w.left ? __ldg(&a.wexp[w.y >> 1]) : 0;
         for (; w.left; ++g) {
             const int64_t row = (int64_t)w.x * 128 + quad * 32 + lane;
             if (w.y == w.y0) {
@@ -371,11 +371,8 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
                 run_s = 0.f;
                 if (SPLIT) he = row < a.X ? __ldg(&a.row_exp[row]) : 0;
             }
-            if (SPLIT) {  // the tile's scale; the maximum so far in its units (a power of two between them)
-                if (w.y != w.y0) run_m *= exp2c(we_next - we);
-                we = we_next;
-                c = fmaxf(a.ctemp * exp2c(-he - we), 1e-37f);  // never 0: -inf stays -inf
-            }
+            // the tile's scale, held within fp32's range (what it makes of the scores is next to 0 there) and never 0: -inf stays -inf
+            if (SPLIT) c = fmaxf(a.ctemp * exp2c(-he - we_next), 1e-37f);
             if ((g & 1) == set) {
                 const uint32_t sb = g % NS;
                 const int64_t left = a.Y - ((int64_t)w.y * BY + part * 64);
@@ -397,7 +394,7 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
             }
             if (w.y + 1 == w.y1 && row < a.X)
                 a.part[(row * a.slots + ((int)blockIdx.x - a.runs.first(w.x))) * S::kParts + set * (S::kParts / 2) + part] =
-                    make_float2(run_m == -INFINITY ? -INFINITY : run_m * c, run_s);
+                    make_float2(run_m, run_s);
             step(w);
             if (SPLIT && w.left) we_next = __ldg(&a.wexp[w.y >> 1]);
         }

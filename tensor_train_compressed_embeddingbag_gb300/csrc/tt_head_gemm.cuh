@@ -301,8 +301,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 }
             }
             if (EPI == kEpiStats && ok && in)
-                a.part[(row * a.nstrips + split) * kParts + part] =
-                    make_float2(run_m == -INFINITY ? -INFINITY : run_m * c, run_s);
+                a.part[(row * a.nstrips + split) * kParts + part] = make_float2(run_m, run_s);
         }
     }
     if (!ok && lead) {

@@ -558,3 +558,19 @@ def test_refusals():
     refused(tt.TT_ERR_ARG, q, h, packed.int(), scales, 32)
     refused(tt.TT_ERR_ARG, q, h, packed, scales, 32, out=torch.empty((4, 21), device="cuda"))
     refused(tt.TT_ERR_ARG, q, h.double(), packed, scales, 32)
+
+
+# ---------------------------------------------------------------- ranges of fp32
+
+
+@pytest.mark.parametrize("d", [64, 128, 200])
+@pytest.mark.parametrize("small", [1e-30, 1e-34, 1e-38, 3e-41])
+@pytest.mark.parametrize("first", [0, 1])
+def test_fp32_blocks_far_apart(d, small, first):
+    """Every second 256 rows of the table next to nothing (decayed or subnormal rows): scores of one size after scores of
+    another, in either order, many times in a block's run of tiles."""
+    n, v = 20, 80_000
+    h, w, t, grad = inputs(n, v, d, torch.float32, seed=36)
+    w = w * torch.where(torch.arange(v, device="cuda") // 256 % 2 == first, 1.0, small)[:, None]
+    got = run_xent(h, w, t, grad)
+    ref.check(got, ref.xent(h, w, t, grad=grad))
