@@ -23,11 +23,20 @@
 // is split as x 2^e = hi + lo with hi, lo in f16 and a product is taken as hi hi + hi lo +
 // lo hi; e is a power-of-two scale that puts the largest magnitude near 2^14: of a hidden
 // row in the forward pass, of 128 x 128 elements of the table, of all hidden rows that
-// count and of all of dz in the backward pass.  So 22 bits of each operand enter, with
-// fp32 accumulation; lo lo (2^-22 of the product and below) is dropped.  dz is rounded to
-// the inputs' 16-bit type before the two gradient products (by at most 2^-8 or 2^-11 of an
-// entry, independent errors, the size of the gradients' own final rounding), and split
-// like an input for fp32.
+// count in the backward pass.  So an element enters with 22 bits, or to 2^-39 of the largest
+// one under its scale where that is more; fp32 accumulation; lo lo (2^-22 of the product and
+// below) is dropped.
+//
+// dz is rounded to the inputs' 16-bit type before the two gradient products (by at most 2^-8
+// or 2^-11 of an entry, independent errors, the size of the gradients' own final rounding),
+// and split like an input for fp32.  For f16 and fp32 it is scaled as well, by a power of two that
+// puts |g T| just below 2^14: an element keeps its bits down to 2^-28 of |g T| (fp32's two
+// pieces: 22 bits down to 2^-16, to 2^-39 absolute below).  For dhidden that is the row's own
+// g (or 2^-100 of the largest, if that is more), as rows are independent of each other.  For
+// dweight, a sum over rows, the batch's largest |g T| is the measure: D > 128 has one dz for
+// both products, and the hidden rows that dweight multiplies it by take the factor between
+// the two scales; k_head_fused, whose hidden rows form the scores as well, scales dz, and
+// what lies below 2^-39 of the batch's largest |g T| is lost to dweight there.
 #include <math.h>
 
 #include <type_traits>
@@ -282,21 +291,38 @@ __global__ void __launch_bounds__(RT) k_head_finish(HeadIn in, Target t, const f
     }
 }
 
-// What the backward pass needs of every row, a block per row: its scale (g T, 0 for
-// a row that does not count), its lse in log2 units, dz of its target entries, and
-// its packed copy (zeros for a row that does not count, so that nothing such a row
-// holds, infinities and NaN included, reaches dweight).  Entries of one row with the
-// same id hold the same value, of their summed q.  Target entries go to arrays
-// [K][N] (ids_out, dzt) and, for k_head_fused, to their 32 x 32 blocks.
+// What the backward pass needs of every row, a block per row: its weight (g T, 0 for a
+// row that does not count) under its own scale and under the batch's, its lse in log2
+// units, dz of its target entries under the batch's, and its packed copy (zeros for a row
+// that does not count, so that nothing such a row holds, infinities and NaN included,
+// reaches dweight).  Entries of one row with the same id hold the same value, of their
+// summed q.  Target entries go to arrays [K][N] (ids, dzt) and, for k_head_fused, to their
+// 32 x 32 blocks.
+struct RowsArgs {
+    const float* lse;
+    const float* grad;
+    const uint32_t* shares;  // fp32, f16: the largest magnitudes, joined in
+    uint32_t* amax;          //   [0] hidden's, [2] |g T|'s; null: no scales
+    int* zexp;               //   exponent of the row's own scale over the batch's
+    float *nlse, *scale, *scale_batch;  // the last may be scale
+    float* to_own;  // from the batch's scale to the row's
+    int* ids;
+    float* dzt;
+    TargetBlock* blocks;
+    int nblocks;
+    TargetEntry* ents;
+    uint16_t* hp;
+    uint16_t* hq;  // null, or hidden rows under hidden's scale, less what the row's has over the batch's, for dweight
+    int* err;
+};
 template <class T, bool DISTILL, int RT>
 __global__ void __launch_bounds__(RT)
-    k_head_rows(HeadIn in, Target t, const float* lse, const float* grad, const uint32_t* shares, uint32_t* amax, float* nlse, float* scale, int* ids_out,
-                float* dzt, TargetBlock* blocks, int nblocks, TargetEntry* ents, uint16_t* hp, int* err) {
+    k_head_rows(HeadIn in, Target t, const __grid_constant__ RowsArgs a) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t n = blockIdx.x;
     const T* h = static_cast<const T*>(in.h) + n * in.ldh;
     const T* w = static_cast<const T*>(in.w);
-    const float l = lse[n];
+    const float l = a.lse[n];
     bool any;
     extern __shared__ float sm[];
     __shared__ float red[RT / 16];
@@ -304,40 +330,49 @@ __global__ void __launch_bounds__(RT)
     int* ids = reinterpret_cast<int*>(sm + 2 * t.K);
     int64_t xid = -1;
     if (DISTILL) {
-        any = teacher_row<RT>(t, n, in.V, q, sm + t.K, ids, red, err);
+        any = teacher_row<RT>(t, n, in.V, q, sm + t.K, ids, red, a.err);
     } else {
-        xid = xent_id(t, n, in.V, threadIdx.x == 0 ? err : nullptr);
+        xid = xent_id(t, n, in.V, threadIdx.x == 0 ? a.err : nullptr);
         any = xid >= 0;
     }
-    int ez = 0, eh = 0;
-    if (amax) {  // the shares of the largest magnitudes joined: dz's by warps 0 and 1, hidden's by 2 and 3
+    const float gt = any ? a.grad[n] * t.T : 0.f;
+    int ez = 0, eh = 0, own = 0;  // own: the row's scale over the batch's
+    if (a.amax) {  // the shares of the largest magnitudes joined: dz's by warps 0 and 1, hidden's by 2 and 3
         __shared__ uint32_t most[4];
         static_assert(kRowThreads == 2 * kAmaxShares, "a share per thread of the first four warps");
         if (warp < 4) {
-            const uint32_t m = __reduce_max_sync(0xffffffffu, shares[threadIdx.x]);
+            const uint32_t m = __reduce_max_sync(0xffffffffu, a.shares[threadIdx.x]);
             if (lane == 0) most[warp] = m;
         }
         __syncthreads();
         const uint32_t mz = max(most[0], most[1]), mh = max(most[2], most[3]);
-        ez = scale_exp(mz);
+        const uint32_t mine = __float_as_uint(gt) & 0x7FFFFFFFu;
+        const int eb = scale_exp(mz);
         eh = scale_exp(mh);
-        if (n == 0 && threadIdx.x == 0) {
-            amax[0] = mh;
-            amax[2] = mz;
+        ez = mine && mine < 0x7F800000u ? min(scale_exp(mine), eb + 100) : eb;
+        own = ez - eb;
+        if (threadIdx.x == 0) {
+            a.zexp[n] = own;
+            if (n == 0) {
+                a.amax[0] = mh;
+                a.amax[2] = mz;
+            }
         }
     }
-    const float rs = any ? grad[n] * t.T * exp2i(ez) : 0.f;
+    const float rs = gt * exp2i(ez), rb = rs * exp2i(-own);
     if (threadIdx.x == 0) {
-        nlse[n] = any ? -l * kLog2e : 0.f;
-        scale[n] = rs;
+        a.nlse[n] = any ? -l * kLog2e : 0.f;
+        a.scale[n] = rs;
+        a.scale_batch[n] = rb;
+        a.to_own[n] = exp2i(own);
     }
     if (n == in.N - 1)
-        for (int64_t i = in.N + threadIdx.x; i < (in.N + 127) / 128 * 128; i += RT) nlse[i] = scale[i] = 0.f;
+        for (int64_t i = in.N + threadIdx.x; i < (in.N + 127) / 128 * 128; i += RT) a.nlse[i] = a.scale[i] = a.scale_batch[i] = a.to_own[i] = 0.f;
     const auto put = [&](int k, int64_t id, float d, bool first) {
-        ids_out[k * in.N + n] = (int)id;
-        dzt[k * in.N + n] = d;
-        if (blocks && id >= 0 && first)
-            add_target(&blocks[(id >> 5) * nblocks + (n >> 5)], ents, (int)(n * t.K + k), (int)(n & 31) | (int)(id & 31) << 5, d);
+        a.ids[k * in.N + n] = (int)id;
+        a.dzt[k * in.N + n] = d;
+        if (a.blocks && id >= 0 && first)
+            add_target(&a.blocks[(id >> 5) * a.nblocks + (n >> 5)], a.ents, (int)(n * t.K + k), (int)(n & 31) | (int)(id & 31) << 5, d);
     };
     if (DISTILL) {
         float* z = sm + t.K;
@@ -353,38 +388,43 @@ __global__ void __launch_bounds__(RT)
                         qs += q[j];
                         first &= j >= k;
                     }
-            put(k, id, id >= 0 ? (expf(z[k] / t.T - l) - qs) * rs : 0.f, first);
+            put(k, id, id >= 0 ? (expf(z[k] / t.T - l) - qs) * rb : 0.f, first);
         }
     } else if (warp == 0) {
         const float z = xid >= 0 ? warp_dot(h, w + xid * in.ldw, in.D, in.vec, lane) : 0.f;
-        if (lane == 0) put(0, xid, xid >= 0 ? (expf(z - l) - 1.f) * rs : 0.f, true);
+        if (lane == 0) put(0, xid, xid >= 0 ? (expf(z - l) - 1.f) * rb : 0.f, true);
     }
     const int64_t piece = in.N * in.Dp;
     for (int i = threadIdx.x; i < in.Dp; i += RT) {
         const int64_t at = n * in.Dp + i;
-        if (sizeof(T) == 4) {
-            const float x = any && i < in.D ? to_f32(h[i]) * exp2i(eh) : 0.f;
-            const __half hi = __float2half_rn(x);
-            hp[at] = __half_as_ushort(hi);
-            hp[piece + at] = __half_as_ushort(__float2half_rn(x - __half2float(hi)));
-        } else {
-            hp[at] = any && i < in.D ? reinterpret_cast<const uint16_t*>(h)[i] : (uint16_t)0;
-        }
+        const bool is = any && i < in.D;
+        const float x = is && (sizeof(T) == 4 || a.hq) ? to_f32(h[i]) * exp2i(eh) : 0.f;
+        const auto scaled = [&](uint16_t* to, float y) {
+            const __half hi = __float2half_rn(y);
+            to[at] = __half_as_ushort(hi);
+            if (sizeof(T) == 4) to[piece + at] = __half_as_ushort(__float2half_rn(y - __half2float(hi)));
+        };
+        if (sizeof(T) == 4)
+            scaled(a.hp, x);
+        else
+            a.hp[at] = is ? reinterpret_cast<const uint16_t*>(h)[i] : (uint16_t)0;
+        if (a.hq) scaled(a.hq, x * exp2i(-own));
     }
 }
 
 // Target entries of dz in columns [v0, v0 + P) of the current piece, a thread per entry (2 to
 // 3 us a piece, launch included: nothing to gain).
-__global__ void k_head_fix(const int* ids, const float* dzt, int64_t total, int64_t rows, int v0, int P, uint16_t* dz,
+__global__ void k_head_fix(const int* ids, const float* dzt, const float* to_own, int64_t total, int64_t rows, int v0, int P, uint16_t* dz,
                            int64_t pitch, int64_t piece, int fmt, int split) {
     const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     if (i >= total) return;
     const int id = ids[i];
     if (id < v0 || id >= v0 + P) return;
-    const int64_t at = (i % rows) * pitch + (id - v0);
-    const uint32_t w = pack16(dzt[i], 0.f, fmt);
+    const int64_t n = i % rows, at = n * pitch + (id - v0);
+    const float d = dzt[i] * to_own[n];
+    const uint32_t w = pack16(d, 0.f, fmt);
     dz[at] = (uint16_t)w;
-    if (split) dz[piece + at] = (uint16_t)pack16(dzt[i] - unpack_f16(w).x, 0.f, 0);
+    if (split) dz[piece + at] = (uint16_t)pack16(d - unpack_f16(w).x, 0.f, 0);
 }
 
 // 8 elements of a row from column c on; columns past D are 0.
@@ -426,7 +466,7 @@ __device__ __forceinline__ void split8(const float (&x)[8], float sc, uint16_t* 
 //                   kept in registers: 512 MB in and out for 10^6 x 64 in 89 us, 5.7 TB/s)
 //   blockIdx.y = 1  forward: the hidden rows packed, a warp per row (fp32: a scale of each
 //                   row's own, its exponent in row_exp); backward: the largest finite
-//                   |grad| T and (fp32) |hidden| over the rows that count, a share per block
+//                   |grad| T and |hidden| over the rows that count, a share per block
 //   blockIdx.y = 2  backward, k_head_fused: the blocks of targets cleared
 struct PrepArgs {
     HeadIn in;
@@ -439,6 +479,7 @@ struct PrepArgs {
     int distill;
     const float* grad;
     uint32_t* shares;   // [2][kAmaxShares], |grad| T then |hidden|; null: no scales
+    int hidden_max;     // |hidden|'s are wanted, else 0
     uint4* clear;
     int64_t nclear;
 };
@@ -542,11 +583,11 @@ __global__ void __launch_bounds__(TH, 1024 / TH) k_head_prep(const __grid_consta
         };
         for (int64_t n = (int64_t)share * TH + threadIdx.x; n < in.N; n += (int64_t)shares * TH)
             if (counts(n)) take(mz, a.grad[n] * a.t.T);
-        if (sizeof(T) == 4)
+        if (a.hidden_max)
             for (int64_t n = (int64_t)share * (TH / 32) + warp; n < in.N; n += (int64_t)shares * (TH / 32))
                 if (counts(n)) {
-                    const float* h = static_cast<const float*>(in.h) + n * in.ldh;
-                    for (int i = lane; i < in.D; i += 32) take(mh, h[i]);
+                    const T* h = static_cast<const T*>(in.h) + n * in.ldh;
+                    for (int i = lane; i < in.D; i += 32) take(mh, to_f32(h[i]));
                 }
         mz = __reduce_max_sync(0xffffffffu, mz);
         mh = __reduce_max_sync(0xffffffffu, mh);
@@ -610,12 +651,13 @@ __global__ void __launch_bounds__(256) k_head_target_rows(HeadIn in, const int* 
 
 // out[m, n] = the splits' partial sums, in split order, unscaled and rounded once.  A
 // block takes 256 >> row_shift rows at a time, 1 << row_shift threads to a row, four
-// columns a thread.
+// columns a thread.  row_exp: exponents of the rows' scales, with those of amax_a and amax_b.
 __global__ void __launch_bounds__(256) k_head_reduce(const float* partial, int splits, int64_t M, int64_t N, int64_t pp, OutArgs to, int row_shift,
-                                                     const uint32_t* amax_a, const uint32_t* amax_b, Residue low) {
-    const Pow2 sc(-amax_exp(amax_a) - amax_exp(amax_b));
+                                                     const uint32_t* amax_a, const uint32_t* amax_b, const int* row_exp, Residue low) {
+    const int e = amax_exp(amax_a) + amax_exp(amax_b);
     const int per = 1 << row_shift, c0 = ((int)threadIdx.x & (per - 1)) * 4;
-    for (int64_t m = (int64_t)blockIdx.x * (256 >> row_shift) + (threadIdx.x >> row_shift); m < M; m += (int64_t)gridDim.x * (256 >> row_shift))
+    for (int64_t m = (int64_t)blockIdx.x * (256 >> row_shift) + (threadIdx.x >> row_shift); m < M; m += (int64_t)gridDim.x * (256 >> row_shift)) {
+        const Pow2 sc(-e - (row_exp ? __ldg(&row_exp[m]) : 0));
         for (int64_t n = c0; n < N; n += per * 4) {
             const float* p = partial + m * pp + n;
             float4 s = *reinterpret_cast<const float4*>(p);
@@ -643,6 +685,7 @@ __global__ void __launch_bounds__(256) k_head_reduce(const float* partial, int s
                     if (n + j < N) store_one(to.out, at + j, v[j], to.type);
             }
         }
+    }
 }
 
 // ---------------------------------------------------------------- host
@@ -754,8 +797,9 @@ bool run_fused(const Operand& X, const Operand& Y, FusedArgs a, int dev, cudaStr
     const bool by_boundary = a.runs.xtiles >= a.runs.blocks;
     const unsigned gx = (unsigned)(by_boundary ? a.runs.blocks - 1 : a.runs.xtiles);
     const unsigned gy = gx >= 256 ? 1 : (gx >= 64 ? 4 : (gx >= 16 ? 16 : 64));  // a block or more per SM
-    k_head_join<<<dim3(gx, gy), 128, 0, st>>>(a.runs, by_boundary, a.partial, a.to, a.X, a.D, SPLIT && MODE == kDhidden ? nullptr : a.amax_z,
-                                              MODE == kDweight ? a.amax_h : nullptr, a.low);
+    constexpr bool dw = MODE == kDweight;  // fp32 dhidden is freed of its scales but the rows' already
+    k_head_join<<<dim3(gx, gy), 128, 0, st>>>(a.runs, by_boundary, a.partial, a.to, a.X, a.D, SPLIT && !dw ? nullptr : a.amax_z,
+                                              dw ? a.amax_h : nullptr, dw ? nullptr : a.zexp, a.low);
     return cudaGetLastError() == cudaSuccess;
 }
 
@@ -803,6 +847,7 @@ int choose_splits(int64_t tiles, int64_t chunks, int64_t elements, int sms) {
 struct Plan {
     HeadIn in;
     int type, fmt, split;    // split: fp32 operands in hi and lo pieces
+    bool scaled;             // backward: dz is scaled (bf16 has fp32's range)
     int esize, sms, device;
     bool pack_h, pack_w;          // 16-bit copies of hidden and weight
     bool pack_h_fwd, pack_w_fwd;  // in the forward pass
@@ -837,6 +882,7 @@ tt_status make_plan(const tt_head* hd, int K, bool buffers, Plan* p) {
     p->type = hd->dtype;
     p->fmt = hd->dtype == TT_BF16;
     p->split = hd->dtype == TT_F32;
+    p->scaled = hd->dtype != TT_BF16;
     p->esize = hd->dtype == TT_F32 ? 4 : 2;
     if (((uintptr_t)hd->hidden_dev | (uintptr_t)hd->weight_dev) % p->esize) return TT_ERR_ARG;
     if (!buffers) return TT_ERR_ARG;
@@ -957,11 +1003,11 @@ size_t fwd_ws(const Plan& p, void* base, FwdWs* w) {
 
 struct BwdWs {
     uint32_t *amax, *shares;
-    float *nlse, *scale, *joins, *dzt, *dh_part, *dw_part;
-    int *ids, *wexp;
+    float *nlse, *scale, *scale_batch, *to_own, *joins, *dzt, *dh_part, *dw_part;
+    int *zexp, *ids, *wexp;
     TargetBlock* blocks;
     TargetEntry* ents;
-    uint16_t *hp, *wp, *dz;
+    uint16_t *hp, *hq, *wp, *dz;
 };
 size_t bwd_ws(const Plan& p, int K, void* base, BwdWs* w) {
     Arena a(base);
@@ -971,11 +1017,15 @@ size_t bwd_ws(const Plan& p, int K, void* base, BwdWs* w) {
     w->wexp = a.get<int>(p.split ? cdiv(p.in.V, 128) * cdiv(p.in.D, 128) : 0);
     w->nlse = a.get<float>(cdiv(p.in.N, 128) * 128);
     w->scale = a.get<float>(cdiv(p.in.N, 128) * 128);
+    w->scale_batch = p.scaled ? a.get<float>(cdiv(p.in.N, 128) * 128) : w->scale;
+    w->to_own = a.get<float>(cdiv(p.in.N, 128) * 128);
+    w->zexp = a.get<int>(p.scaled ? p.in.N : 0);
     w->ids = a.get<int>(nk);
     w->dzt = a.get<float>(nk);
     w->blocks = a.get<TargetBlock>(p.fused ? p.nblocks * p.vblocks : 0);
     w->ents = a.get<TargetEntry>(p.fused ? nk : 0);
     w->hp = a.get<uint16_t>(pc * p.in.N * p.in.Dp);
+    w->hq = a.get<uint16_t>(p.scaled && !p.fused ? pc * p.in.N * p.in.Dp : 0);
     w->wp = a.get<uint16_t>(p.pack_w ? pc * p.in.V * p.in.Dp : 0);
     w->dz = a.get<uint16_t>(pc * p.in.N * p.pitch);
     w->joins = a.get<float>(p.fused ? (int64_t)p.sms * 2 * 128 * p.pp : 0);
@@ -1115,7 +1165,9 @@ tt_status head_backward(const Plan& p, const Target& t, const float* lse, const 
     if (bwd_ws(p, t.K, ws, &w) > ws_bytes) return TT_ERR_ARG;
     if (in.N == 0) return cudaMemsetAsync(dw, 0, (size_t)in.V * in.D * p.esize, st) == cudaSuccess ? TT_OK : TT_ERR_CUDA;
     const bool distill = t.logits != nullptr;
-    uint32_t* amax = p.fmt ? nullptr : w.amax;  // bf16 has fp32's range: dz needs no scale
+    uint32_t* amax = p.scaled ? w.amax : nullptr;
+    const int* zexp = p.scaled ? w.zexp : nullptr;
+    const bool use_hq = p.scaled && !p.fused;
     TargetBlock* blocks = p.fused ? w.blocks : nullptr;
     if (amax || p.pack_w || blocks) {
         PrepArgs a{};
@@ -1127,14 +1179,14 @@ tt_status head_backward(const Plan& p, const Target& t, const float* lse, const 
         a.distill = distill;
         a.grad = grad;
         a.shares = amax ? w.shares : nullptr;
+        a.hidden_max = p.split || use_hq;
         a.clear = reinterpret_cast<uint4*>(w.blocks);
         a.nclear = blocks ? p.nblocks * p.vblocks : 0;
         if (!launch_prep<T>(p, a, st)) return TT_ERR_CUDA;
     }
-    const auto rows = [&](auto kernel, int threads) {
-        kernel<<<(unsigned)in.N, threads, (size_t)t.K * 12, st>>>(in, t, lse, grad, w.shares, amax, w.nlse, w.scale, w.ids, w.dzt, blocks, (int)p.nblocks,
-                                                                w.ents, w.hp, err);
-    };
+    const RowsArgs ra{lse,   grad,  w.shares, amax,           w.zexp, w.nlse, w.scale,                    w.scale_batch, w.to_own,
+                      w.ids, w.dzt, blocks,   (int)p.nblocks, w.ents, w.hp,   use_hq ? w.hq : nullptr, err};
+    const auto rows = [&](auto kernel, int threads) { kernel<<<(unsigned)in.N, threads, (size_t)t.K * 12, st>>>(in, t, ra); };
     if (distill && wide_rows(p, t.K))
         rows(k_head_rows<T, true, kRowThreadsWide>, kRowThreadsWide);
     else if (distill)
@@ -1156,20 +1208,23 @@ tt_status head_backward(const Plan& p, const Target& t, const float* lse, const 
         o.pp = p.pp;
         return o;
     };
-    const Residue none{}, low = p.few_targets ? Residue{w.ids, w.dzt, in.w, in.ldw, in.N, t.K, p.fmt} : none;
+    const Residue none{}, low = p.few_targets ? Residue{w.ids, w.dzt, w.to_own, in.w, in.ldw, in.N, t.K, p.fmt} : none;
     // the rows of dweight that the few targets name, again (k_head_target_rows)
     const auto target_rows = [&] {
         if constexpr (sizeof(T) == 2)
             if (p.few_targets)
-                k_head_target_rows<T><<<(unsigned)(in.N * t.K), 256, 0, st>>>(in, w.ids, w.dzt, t.K, w.nlse, w.scale, kLog2e / t.T, az, dw, p.type);
+                k_head_target_rows<T><<<(unsigned)(in.N * t.K), 256, 0, st>>>(in, w.ids, w.dzt, t.K, w.nlse, w.scale_batch, kLog2e / t.T, az, dw,
+                                                                              p.type);
         return launch_ok();
     };
-    const auto reduce = [&](const float* partial, int splits, int64_t rows, void* out, const uint32_t* ay, const Residue& lw) {
+    const auto reduce = [&](const float* partial, int splits, int64_t rows, void* out, const uint32_t* ay, const int* row_exp,
+                            const Residue& lw) {
         int shift = 3;
         while (shift < 8 && (4 << shift) < in.D) ++shift;
         // fp32's are in their own units already
         k_head_reduce<<<grid_of(rows, 256 >> shift, p.sms, 16), 256, 0, st>>>(partial, splits, rows, in.D, p.pp, dest(out, nullptr), shift,
-                                                                            p.split ? nullptr : az, p.split ? nullptr : ay, lw);
+                                                                            p.split ? nullptr : az, p.split ? nullptr : ay,
+                                                                            p.split ? nullptr : row_exp, lw);
         return launch_ok();
     };
     if (p.fused) {
@@ -1178,12 +1233,14 @@ tt_status head_backward(const Plan& p, const Target& t, const float* lse, const 
         a.D = in.D;
         a.fmt = p.fmt;
         a.err = err;
-        a.amax_h = ah;
+        a.amax_h = p.split ? ah : nullptr;
         a.amax_z = az;
+        a.zexp = zexp;
+        a.to_own = w.to_own;
         a.wexp = w.wexp;
         a.ctemp = kLog2e / t.T;
         a.nlse = w.nlse;
-        a.scale = w.scale;
+        a.scale = w.scale_batch;
         a.blocks = w.blocks;
         a.ents = w.ents;
         a.ids = w.ids;
@@ -1197,10 +1254,12 @@ tt_status head_backward(const Plan& p, const Target& t, const float* lse, const 
         a.to = dest(dw, nullptr);
         if (!fused<kDweight>(p.split, W, H, a, p.device, st)) return TT_ERR_CUDA;
         a.runs = p.runs_dh;
+        a.scale = w.scale;
         a.to = dest(dh, nullptr);
         a.low = low;
         return fused<kDhidden>(p.split, H, W, a, p.device, st) && target_rows() ? TT_OK : TT_ERR_CUDA;
     }
+    const Operand Hq{use_hq ? w.hq : w.hp, in.N, in.D, in.Dp, in.N * in.Dp};
     const int64_t npieces = cdiv(in.V, p.P), dz_piece = in.N * p.pitch;
     for (int64_t i = 0; i < npieces; ++i) {
         const int64_t v0 = i * p.P, P = in.V - v0 < p.P ? in.V - v0 : p.P;
@@ -1210,7 +1269,7 @@ tt_status head_backward(const Plan& p, const Target& t, const float* lse, const 
         a.M = in.N;
         a.N = P;
         a.chunks = (int)cdiv(in.D, kBK);
-        a.amax_a = ah;
+        a.amax_a = p.split ? ah : nullptr;
         a.kb = (int)cdiv(in.D, 128);
         a.wexp = p.split ? w.wexp + v0 / 128 * a.kb : nullptr;  // a piece begins at a multiple of 256 rows
         a.ctemp = kLog2e / t.T;
@@ -1220,11 +1279,11 @@ tt_status head_backward(const Plan& p, const Target& t, const float* lse, const 
         a.dz_pitch = p.pitch;
         a.dz_piece = dz_piece;
         if (!score_gemm<kEpiDz>(p.bn_s, p.split, H, W, a, p.sms, p.device, st)) return TT_ERR_CUDA;
-        k_head_fix<<<(unsigned)cdiv(in.N * t.K, 256), 256, 0, st>>>(w.ids, w.dzt, in.N * t.K, in.N, (int)v0, (int)P, w.dz, p.pitch, dz_piece,
+        k_head_fix<<<(unsigned)cdiv(in.N * t.K, 256), 256, 0, st>>>(w.ids, w.dzt, w.to_own, in.N * t.K, in.N, (int)v0, (int)P, w.dz, p.pitch, dz_piece,
                                                                 p.fmt, p.split);
         if (!launch_ok()) return TT_ERR_CUDA;
 
-        GemmArgs b = gemm_args(p, err);  // dweight of the piece: [P][D] = dz^T H
+        GemmArgs b = gemm_args(p, err);  // dweight of the piece: [P][D] = dz^T H, the rows' scales evened out in H
         b.M = P;
         b.N = in.D;
         b.chunks = (int)cdiv(in.N, kBK);
@@ -1233,8 +1292,8 @@ tt_status head_backward(const Plan& p, const Target& t, const float* lse, const 
         b.amax_b = ah;
         void* dwp = static_cast<uint8_t*>(dw) + (size_t)v0 * in.D * p.esize;
         b.to = dest(p.dw_splits > 1 ? nullptr : dwp, w.dw_part);
-        if (!out_gemm<true>(p.split, Z, H, b, p.sms, p.device, st)) return TT_ERR_CUDA;
-        if (p.dw_splits > 1 && !reduce(w.dw_part, p.dw_splits, P, dwp, ah, none)) return TT_ERR_CUDA;
+        if (!out_gemm<true>(p.split, Z, Hq, b, p.sms, p.device, st)) return TT_ERR_CUDA;
+        if (p.dw_splits > 1 && !reduce(w.dw_part, p.dw_splits, P, dwp, ah, nullptr, none)) return TT_ERR_CUDA;
 
         GemmArgs c = gemm_args(p, err);  // the piece's share of dhidden: [N][D] += dz W
         c.M = in.N;
@@ -1242,13 +1301,14 @@ tt_status head_backward(const Plan& p, const Target& t, const float* lse, const 
         c.chunks = (int)cdiv(P, kBK);
         c.splits = p.dh_splits;
         c.amax_a = az;
+        c.row_exp = zexp;
         c.kb = (int)cdiv(in.D, 128);
         c.wexp = p.split ? w.wexp + v0 / 128 * c.kb : nullptr;
         c.to = dest(p.dh_direct ? dh : nullptr, w.dh_part);
         c.to.accumulate = i > 0;
         if (!out_gemm<false>(p.split, Z, W, c, p.sms, p.device, st)) return TT_ERR_CUDA;
     }
-    if (!p.dh_direct && !reduce(w.dh_part, p.dh_splits, in.N, dh, nullptr, low)) return TT_ERR_CUDA;
+    if (!p.dh_direct && !reduce(w.dh_part, p.dh_splits, in.N, dh, nullptr, zexp, low)) return TT_ERR_CUDA;
     return target_rows() ? TT_OK : TT_ERR_CUDA;
 }
 

@@ -290,7 +290,7 @@ struct Pow2 {
     float a, b;
     __device__ __forceinline__ explicit Pow2(int e) : a(exp2c(e)), b(exp2c(e - max(-126, min(127, e)))) {}
     __device__ __forceinline__ float operator()(float x) const { return x * b * a; }
-    __device__ __forceinline__ void operator()(float (&v)[32]) const {  // the same in every lane
+    __device__ __forceinline__ void operator()(float (&v)[32]) const {
         if (b != 1.f) {
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] *= b;
@@ -417,7 +417,8 @@ __device__ __forceinline__ void put_elements(uint4* buf, const float (&v)[32], v
 // what they lost is added where dhidden's fp32 sums are joined.  K = 0: not done.
 struct Residue {
     const int* ids;    // [K][rows]
-    const float* dzt;
+    const float* dzt;  // times to_own: in dhidden's units
+    const float* to_own;
     const void* w;
     int64_t ldw, rows;
     int K, fmt;
@@ -429,7 +430,7 @@ struct Residue {
             bool first = id >= 0;  // the same id further on is the same element
             for (int j = 0; j < k; ++j) first &= ids[j * rows + n] != id;
             if (!first) continue;
-            const float x = dzt[k * rows + n];
+            const float x = dzt[k * rows + n] * to_own[n];
             const uint32_t b = pack16(x, 0.f, fmt) & 0xFFFFu;
             const uint16_t y = static_cast<const uint16_t*>(w)[id * ldw + c];
             s = fmaf(x - (fmt ? __uint_as_float(b << 16) : unpack_f16(b).x), fmt ? __uint_as_float((uint32_t)y << 16) : unpack_f16(y).x, s);

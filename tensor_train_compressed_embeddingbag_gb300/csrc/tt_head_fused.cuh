@@ -44,8 +44,8 @@ namespace ttemb {
 // a batch share popular items the list is long and every step of it a memory latency:
 // then the 32 rows' entries are gone through instead, a row per lane, four loads at a
 // time (a bf16 batch of 4096 over 25,003 items drawn by popularity, D = 128: dweight 59 us,
-// with lists alone 64; uniform ones change nothing).  An element's place in its block is (n & 31) | (v & 31) << 5; its value is scaled
-// like the others.  All zero: none.
+// with lists alone 64; uniform ones change nothing).  An element's place in its block is (n & 31) | (v & 31) << 5; its value
+// is under the batch's scale.  All zero: none.
 struct __align__(16) TargetBlock {
     uint32_t meta;  // places of the two (bits 0..9 and 10..19), bits 20..31: how many elements
     float val[2];
@@ -88,11 +88,13 @@ struct FusedArgs {
     float ctemp;             // log2(e) / T
     float2* part;            // kLse: [X][slots][kParts] (maximum in log2 units, sum), a slot per run
     int slots;
-    const float* nlse;       // per hidden row -lse in log2 units, and its scale; zeros up to a
-    const float* scale;      //   multiple of 128 rows
+    const float* nlse;       // per hidden row -lse in log2 units, and its scaled weight (kDhidden: by the
+    const float* scale;      //   row's own power of two, kDweight: by the batch's); zeros up to a multiple of 128 rows
+    const int* zexp;         // kDhidden: exponent of the row's own scale over the batch's (null: 0),
+    const float* to_own;     //   and what takes an element of dz from the batch's scale to it, as scale has it
     const TargetBlock* blocks;  // [vblocks][nblocks]
     const TargetEntry* ents;
-    const int* ids;             // [K][hidden rows] the rows' entries (-1: none) and their elements of dz
+    const int* ids;             // [K][hidden rows] the rows' entries (-1: none) and their elements of dz under the batch's scale
     const float* dzt;
     int K;
     int64_t rows;
@@ -125,11 +127,13 @@ struct FusedShape {
 
 // The target elements of a 32 x 32 block of dz, after its warp has written the block to
 // tensor memory from t0 on: each replaces one 16-bit half (SPLIT: and its lo part, 16
-// columns further) of one column.  nb, vb: which block; COLS: hidden rows are columns.
+// columns further) of one column.  nb, vb: which block; COLS: hidden rows are columns; else
+// to_own: from the batch's scale to that of this lane's row.
 template <bool SPLIT, bool COLS>
-__device__ __noinline__ void put_targets(const FusedArgs& a, uint32_t t0, uint4 b, int nb, int vb) {
+__device__ __noinline__ void put_targets(const FusedArgs& a, uint32_t t0, uint4 b, int nb, int vb, float to_own) {
     const int lane = threadIdx.x & 31, count = (int)(b.x >> 20);
     auto put = [&](int col, bool mine, float val) {
+        if (!COLS) val *= to_own;
         const uint32_t hi = pack16(val, 0.f, SPLIT ? 0 : a.fmt) & 0xFFFFu, sh = (uint32_t)(col & 1) * 16;
         uint32_t w = tm_read1(t0 + (col >> 1));
         if (mine) w = (w & ~(0xFFFFu << sh)) | hi << sh;
@@ -200,14 +204,15 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
     __shared__ uint64_t xfull[S::XB], xempty[S::XB], yfull[S::kStages], sfull[Pipe::kFormed], odone[S::kStages];
     __shared__ uint64_t pready[Pipe::kTurned], ofull[OB], oempty[OB], drain[3];
     // what a dz warp needs of memory for a tile, and for the next: -lse and scale of its
-    // columns (COLS) or rows, the targets of its two 32 x 32 blocks
+    // columns (COLS) or rows (and to_own), the targets of its two 32 x 32 blocks
     struct Ahead {
-        float nlse[COLS ? 64 : 32], scale[COLS ? 64 : 32];
+        float nlse[COLS ? 64 : 32], scale[64];  // not COLS: 32 scales, then 32 of to_own
         uint4 blk[2];
         int wexp[4];  // the first: scale of the tile's table rows
     };
     __shared__ __align__(16) Ahead ahead[S::kDzWarps][2];
     __shared__ uint4 rows_out[MODE == kLse ? 1 : 8][128];  // put_rows of the warps that store OUT
+    static_assert(S::kSmem + sizeof(ahead) + sizeof(rows_out) + 512 <= 227 * 1024, "shared memory");
     __shared__ uint32_t tmem_slot;
     __shared__ int gave_up_s;
     volatile int* gave_up = &gave_up_s;
@@ -406,10 +411,11 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
         auto fetch = [&](const Walk& t, Ahead& to) {
             if (!t.left) return;
             const int x32 = t.x * 4 + quad, y32 = t.y * (BY / 32) + part * 2;
-            constexpr int kHalf = COLS ? 16 : 8;  // lanes that copy each of the two rows of floats
-            if (lane < 2 * kHalf) {
-                const int64_t n = (int64_t)(COLS ? y32 : x32) * 32 + (lane % kHalf) * 4;
-                cp16((lane < kHalf ? to.nlse : to.scale) + (lane % kHalf) * 4, (lane < kHalf ? a.nlse : a.scale) + n, true);
+            constexpr int kEach = COLS ? 16 : 8;  // lanes that copy each of the two or three rows of floats
+            if (lane < (COLS ? 2 : 3) * kEach) {
+                const int which = lane / kEach, at = lane % kEach * 4;
+                const int64_t n = (int64_t)(COLS ? y32 : x32) * 32 + at;
+                cp16((which == 0 ? to.nlse : which == 1 ? to.scale : to.scale + 32) + at, (which == 0 ? a.nlse : which == 1 ? a.scale : a.to_own) + n, true);
             }
             if (lane < 2) {
                 const int nb = COLS ? y32 + lane : x32, vb = COLS ? x32 : y32 + lane;
@@ -484,7 +490,7 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
                 const uint4 b = my.blk[ch];
                 if (b.x) {
                     tm_wait_st();
-                    put_targets<SPLIT, COLS>(a, t0, b, COLS ? at.y32 + ch : at.x32, COLS ? at.x32 : at.y32 + ch);
+                    put_targets<SPLIT, COLS>(a, t0, b, COLS ? at.y32 + ch : at.x32, COLS ? at.x32 : at.y32 + ch, COLS ? 1.f : my.scale[32 + lane]);
                 }
             }
             tm_wait_st();
@@ -494,8 +500,7 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
         }
     } else if (MODE != kLse && warp >= 4) {
         const int half = warp >= 8, quad = warp & 3;
-        const int ez = amax_exp(a.amax_z) + (COLS ? amax_exp(a.amax_h) : 0);
-        const Pow2 sc(SPLIT && !COLS ? 0 : -ez);  // SPLIT dhidden: freed of its scales tile by tile
+        const int eb = amax_exp(a.amax_z) + (COLS ? amax_exp(a.amax_h) : 0);
         constexpr int OC = DT / 64;  // 32-column chunks of this warp's half
         uint32_t fl = 0;
         bool first = true;
@@ -503,11 +508,15 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
             const int64_t row = (int64_t)w.x * 128 + quad * 32 + lane;
             const uint32_t l0 = tmem + ((uint32_t)(quad * 32) << 16) + S::kOutCol + half * (DT / 2);
             const bool whole = w.y0 == 0 && w.y1 == a.runs.ytiles;
+            const auto scales = [&] {  // that the row's sums are still to be freed of; SPLIT dhidden: of its own only
+                const int own = !COLS && a.zexp && row < a.X ? __ldg(&a.zexp[row]) : 0;
+                return Pow2(SPLIT && !COLS ? -own : -eb - own);
+            };
             float* part = a.partial + (((int64_t)blockIdx.x * 2 + !first) * 128 + quad * 32) * a.to.pp;
             auto put = [&](float(&v)[32], int col) {
                 if (row - lane >= a.X || col >= a.D) return;
                 if (whole)
-                    store_out(a.to, rows_out[warp - 4], 0, row - lane, col, a.X, a.D, v, sc);
+                    store_out(a.to, rows_out[warp - 4], 0, row - lane, col, a.X, a.D, v, scales());
                 else
                     put_rows_f32(rows_out[warp - 4], v, reinterpret_cast<uint8_t*>(part + col), a.to.pp * 4, 32);
             };
@@ -519,7 +528,7 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
                     for (int j = 0; j < 32; ++j) sum[ch][j] = 0.f;
                 for (int f = w.y0; f < w.y1; f = (f | 1) + 1, ++fl) {
                     const uint32_t ob = fl % OB;
-                    const Pow2 f1(COLS ? 0 : -ez - __ldg(&a.wexp[f >> 1]));
+                    const Pow2 f1(COLS ? 0 : -eb - __ldg(&a.wexp[f >> 1]));
                     ok = head_wait(&ofull[ob], (fl / OB) & 1, a.wait_ns, gave_up);
                     if (!ok) break;
                     tc_fence_after();
@@ -555,6 +564,7 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
                 tc_fence_after();
                 if (whole && a.to.vec && a.D == DT && a.to.type != TT_F32) {
                     // OUT is let go before anything is written: the next segment's product waits for it
+                    const Pow2 sc = scales();
                     uint32_t q[OC][16];
 #pragma unroll
                     for (int ch = 0; ch < OC; ++ch) {
@@ -623,8 +633,9 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
 // 128 / gridDim.y rows per blockIdx.y.  blockIdx.x is the x, or (by_boundary: more x
 // than runs) the boundary between two runs that lies in it; the first boundary inside
 // an x takes it.
+// Sums are freed of the scales that amax_z, amax_y and (per row) zexp give.
 __global__ void __launch_bounds__(128) k_head_join(Runs runs, int by_boundary, const float* partial, OutArgs to, int64_t X, int D,
-                                                   const uint32_t* amax_z, const uint32_t* amax_y, Residue low) {
+                                                   const uint32_t* amax_z, const uint32_t* amax_y, const int* zexp, Residue low) {
     __shared__ int sh[4];
     if (threadIdx.x == 0) {
         int64_t x = blockIdx.x;
@@ -653,11 +664,12 @@ __global__ void __launch_bounds__(128) k_head_join(Runs runs, int by_boundary, c
     const int more = sh[2], per_row = (int)to.pp / 4, rows = 128 / per_row, span = 128 / gridDim.y;
     const int c = (int)threadIdx.x % per_row * 4, r0 = (int)threadIdx.x / per_row;
     if (r0 >= rows || c >= D) return;
-    const Pow2 sc(-amax_exp(amax_z) - amax_exp(amax_y));
+    const int e = amax_exp(amax_z) + amax_exp(amax_y);
     const int64_t step = 256 * to.pp;
     for (int i = r0; i < span; i += rows) {
         const int r = blockIdx.y * span + i;
         if (x * 128 + r >= X) break;
+        const Pow2 sc(-e - (zexp ? __ldg(&zexp[x * 128 + r]) : 0));
         const float* p = partial + ((int64_t)sh[1] * 256 + r) * to.pp + c;
         float4 s = *reinterpret_cast<const float4*>(p + sh[3] * 128 * to.pp);
 #pragma unroll 4

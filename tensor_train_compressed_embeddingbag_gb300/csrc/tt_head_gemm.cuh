@@ -27,7 +27,7 @@ struct GemmArgs {
     // scales: exponents of the operands' power-of-two scales come from these bits
     const uint32_t* amax_a;
     const uint32_t* amax_b;
-    const int* row_exp;  // per-row exponent of A (forward), else null
+    const int* row_exp;  // exponents of A's rows (with amax_a's), else null
     // SPLIT: exponents of the table's 128 x 128 blocks, kb to a row of blocks: scores: B's
     // rows by K; dhidden: K by columns; dweight: null
     const int* wexp;
@@ -203,16 +203,16 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         uint4* const buf = reinterpret_cast<uint4*>(raw + (base - smem_addr(raw)) + S::kRing + (warp - 4) * 2048);
         const int e = amax_exp(a.amax_a) + amax_exp(a.amax_b);
         const float c = a.ctemp;
-        const Pow2 sc(SPLIT ? 0 : -e);
         for (int64_t u = blockIdx.x; ok && u < a.units; u += gridDim.x) {
             int m, n0, n1, kb, ke, split;
             unit(u, m, n0, n1, kb, ke, split);
             const int64_t row = (int64_t)m * 128 + r;
             const bool in = row < a.M;
             float run_m = -INFINITY, run_s = 0.f;
-            int er = e;  // SPLIT: the scales that the row's sums are freed of
+            int er = e;  // the scales that the row's sums are freed of
             float2 rc = make_float2(0.f, 0.f);
-            if (SPLIT && EPI == kEpiStats && in) er = a.row_exp[row];
+            if ((SPLIT || EPI == kEpiOut) && a.row_exp && in) er += a.row_exp[row];
+            const Pow2 sc(SPLIT ? 0 : -er);
             if (EPI == kEpiDz && in) rc = make_float2(a.nlse[row], a.scale[row]);
             for (int n = n0; ok && n < n1; ++n) {
                 const int64_t col0 = (int64_t)n * BN + part * (BN / kParts);
