@@ -793,8 +793,9 @@ bool run_fused(const Operand& X, const Operand& Y, FusedArgs a, int dev, cudaStr
     if (!allow_smem<KernelTag<DT, SPLIT, MODE, 0, -1>>(k, dev, S::kSmem)) return false;
     k<<<(unsigned)a.runs.blocks, S::kThreads, S::kSmem, st>>>(mx, my, a);
     if (cudaGetLastError() != cudaSuccess) return false;
-    if (MODE == kLse || a.runs.blocks == 1) return true;
-    const bool by_boundary = a.runs.xtiles >= a.runs.blocks;
+    const bool join_all = MODE == kDhidden && a.low.K;  // few rows: one x
+    if (MODE == kLse || (a.runs.blocks == 1 && !join_all)) return true;
+    const bool by_boundary = a.runs.xtiles >= a.runs.blocks && !join_all;
     const unsigned gx = (unsigned)(by_boundary ? a.runs.blocks - 1 : a.runs.xtiles);
     const unsigned gy = gx >= 256 ? 1 : (gx >= 64 ? 4 : (gx >= 16 ? 16 : 64));  // a block or more per SM
     constexpr bool dw = MODE == kDweight;  // fp32 dhidden is freed of its scales but the rows' already

@@ -100,7 +100,7 @@ struct FusedArgs {
     int64_t rows;
     Residue low;             // kDhidden: for k_head_join
     int nblocks, vblocks;
-    OutArgs to;              // whole segments; others as fp32 sums to
+    OutArgs to;              // whole segments; others, and all with `low`, as fp32 sums to
     float* partial;          //   [blocks][2][128][to.pp]: the run's first segment, its last
 };
 
@@ -507,7 +507,7 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
         while (ok && w.left) {
             const int64_t row = (int64_t)w.x * 128 + quad * 32 + lane;
             const uint32_t l0 = tmem + ((uint32_t)(quad * 32) << 16) + S::kOutCol + half * (DT / 2);
-            const bool whole = w.y0 == 0 && w.y1 == a.runs.ytiles;
+            const bool whole = w.y0 == 0 && w.y1 == a.runs.ytiles && !(MODE == kDhidden && a.low.K);
             const auto scales = [&] {  // that the row's sums are still to be freed of; SPLIT dhidden: of its own only
                 const int own = !COLS && a.zexp && row < a.X ? __ldg(&a.zexp[row]) : 0;
                 return Pow2(SPLIT && !COLS ? -own : -eb - own);
@@ -633,7 +633,8 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
 // 128 / gridDim.y rows per blockIdx.y.  blockIdx.x is the x, or (by_boundary: more x
 // than runs) the boundary between two runs that lies in it; the first boundary inside
 // an x takes it.
-// Sums are freed of the scales that amax_z, amax_y and (per row) zexp give.
+// With `low` every x is joined, were it from one run.  Sums are freed of the scales that
+// amax_z, amax_y and (per row) zexp give.
 __global__ void __launch_bounds__(128) k_head_join(Runs runs, int by_boundary, const float* partial, OutArgs to, int64_t X, int D,
                                                    const uint32_t* amax_z, const uint32_t* amax_y, const int* zexp, Residue low) {
     __shared__ int sh[4];
@@ -649,7 +650,7 @@ __global__ void __launch_bounds__(128) k_head_join(Runs runs, int by_boundary, c
         if (split) {
             b = runs.first(x);
             last = runs.last(x);
-            split = b != last && (!by_boundary || b == (int)blockIdx.x);
+            split = (b != last || low.K) && (!by_boundary || b == (int)blockIdx.x);
             // in its first run x may come behind others (slot 1); every later run begins inside x
             slot0 = runs.begin(b) < x * runs.ytiles;
         }

@@ -574,3 +574,31 @@ def test_fp32_blocks_far_apart(d, small, first):
     w = w * torch.where(torch.arange(v, device="cuda") // 256 % 2 == first, 1.0, small)[:, None]
     got = run_xent(h, w, t, grad)
     ref.check(got, ref.xent(h, w, t, grad=grad))
+
+
+# ---------------------------------------------------------------- few targets
+
+
+@pytest.mark.parametrize("dtype", TYPES[1:])
+@pytest.mark.parametrize("size", [(1, 100, 64), (3, 128, 128), (31, 60, 72), (64, 128, 16), (8, 9, 33), (3, 300, 64), (20, 500, 200)])
+def test_few_targets_without_their_rounding(size, dtype):
+    """One target for all rows, whose table row alone is large in column 0 (where hidden is 0): that column of dhidden is
+    the target's dz times 91, rounded once.  Rounding is monotonic, so it lies between the roundings of the value less and plus
+    what fp32 may be off; with dz rounded as well it does not."""
+    n, v, d = size
+    h, w, _, _ = inputs(*size, dtype, seed=37)
+    h[:, 0], w[:, 0] = 0, w[:, 0] * 2.0 ** -10
+    w[7, 0] = 91.0
+    t = torch.full((n,), 7, device="cuda")
+    grad = torch.rand((n,), generator=gen(38), device="cuda") + 0.5
+    got = run_xent(h, w, t, grad)["grad_hidden"][:, 0].double()
+    want = ref.xent(h, w, t, grad=grad)["grad_hidden"][0][:, 0]
+    z = ref.scores(h, w)
+    lse = torch.logsumexp(z, 1)
+    ez, el = ref.bounds(h, w, lse)
+    p = torch.exp(z - lse[:, None])
+    off = grad.double() * 2 * (ez + el + 2.0 ** -20) * 91.0 + max(size) * 2.0 ** -27 * want.abs()
+    rest = (p * w.double()[:, 0].abs())[:, torch.arange(v, device="cuda") != 7].sum(1)  # the others' dz, rounded
+    off = off + ref.U[dtype] * grad.double() * rest
+    low, high = (want - off).to(dtype).double(), (want + off).to(dtype).double()
+    assert ((low <= got) & (got <= high)).all(), (got, low, high)
