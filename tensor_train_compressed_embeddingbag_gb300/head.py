@@ -304,14 +304,14 @@ class _XentFunction(torch.autograd.Function):
     def forward(ctx, hidden, weight, targets, ignore_index, err):
         loss, lse = tt_emb_xent_forward(hidden, weight, targets, ignore_index, err)
         ctx.save_for_backward(hidden, weight, targets, lse)
-        ctx.ignore_index = ignore_index
+        ctx.ignore_index, ctx.err = ignore_index, err
         return loss
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, grad):
         hidden, weight, targets, lse = ctx.saved_tensors
-        gh, gw = tt_emb_xent_backward(hidden, weight, targets, lse, grad, ctx.ignore_index)
+        gh, gw = tt_emb_xent_backward(hidden, weight, targets, lse, grad, ctx.ignore_index, ctx.err)
         return gh, gw, None, None, None
 
 
@@ -320,14 +320,14 @@ class _DistillFunction(torch.autograd.Function):
     def forward(ctx, hidden, weight, ids, logits, temperature, err):
         loss, lse = tt_emb_distill_forward(hidden, weight, ids, logits, temperature, err)
         ctx.save_for_backward(hidden, weight, ids, logits, lse)
-        ctx.temperature = temperature
+        ctx.temperature, ctx.err = temperature, err
         return loss
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, grad):
         hidden, weight, ids, logits, lse = ctx.saved_tensors
-        gh, gw = tt_emb_distill_backward(hidden, weight, ids, logits, lse, grad, ctx.temperature)
+        gh, gw = tt_emb_distill_backward(hidden, weight, ids, logits, lse, grad, ctx.temperature, ctx.err)
         return gh, gw, None, None, None, None
 
 
@@ -347,7 +347,9 @@ def vocab_cross_entropy(hidden: torch.Tensor, weight: torch.Tensor, targets: tor
                         reduction: str = "mean", err: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Softmax cross entropy of hidden [..., dim] against every row of weight [vocab, dim], differentiable in both.
 
-    reduction 'mean' divides by the rows whose target is not ignore_index (0 when there are none)."""
+    reduction 'mean' divides by the rows whose target is not ignore_index (0 when there are none).  err (int32, optional):
+    what the forward pass finds is ORed into it, and later what the backward pass does; without it nothing tells of a
+    target outside the table (a row that does not count) or of a device wait that gave up (results undefined)."""
     _check_reduction(reduction)
     t = targets.reshape(-1)
     loss = _XentFunction.apply(hidden.reshape(-1, hidden.shape[-1]), weight, t, int(ignore_index), err)
@@ -361,7 +363,7 @@ def vocab_distillation(hidden: torch.Tensor, weight: torch.Tensor, teacher_ids: 
     """T^2 KL(teacher's top entries || student) of hidden [..., dim] against weight [vocab, dim], differentiable in both.
 
     teacher_ids / teacher_logits [..., k]; negative ids are no entries.  reduction 'mean'
-    divides by the rows that have an entry (0 when there are none)."""
+    divides by the rows that have an entry (0 when there are none).  err: as in vocab_cross_entropy."""
     _check_reduction(reduction)
     k = teacher_ids.shape[-1]
     ids = teacher_ids.reshape(-1, k)

@@ -602,3 +602,23 @@ def test_few_targets_without_their_rounding(size, dtype):
     off = off + ref.U[dtype] * grad.double() * rest
     low, high = (want - off).to(dtype).double(), (want + off).to(dtype).double()
     assert ((low <= got) & (got <= high)).all(), (got, low, high)
+
+
+# ---------------------------------------------------------------- error words of the autograd functions
+
+
+@pytest.mark.parametrize("op", ["xent", "distill"])
+def test_a_backward_wait_that_gives_up_is_in_the_callers_err(op):
+    """The word given to the loss is the backward pass's too: cleared in between, it holds what that found."""
+    h, w, t, _ = inputs(130, 300, 64, torch.float32, seed=39)
+    ids, logits = entries(130, 300, 4)
+    h, w = h.requires_grad_(), w.requires_grad_()
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    loss = tt.vocab_cross_entropy(h, w, t, err=err) if op == "xent" else tt.vocab_distillation(h, w, ids, logits, err=err)
+    assert err.item() == 0
+    try:
+        tt.tt_emb_head_set_wait_limit(0)
+        loss.backward()
+        assert err.item() & 4
+    finally:
+        tt.tt_emb_head_set_wait_limit(2 * 10 ** 9)
