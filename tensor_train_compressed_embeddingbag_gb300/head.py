@@ -347,15 +347,18 @@ def vocab_cross_entropy(hidden: torch.Tensor, weight: torch.Tensor, targets: tor
                         reduction: str = "mean", err: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Softmax cross entropy of hidden [..., dim] against every row of weight [vocab, dim], differentiable in both.
 
-    reduction 'mean' divides by the rows whose target is not ignore_index (0 when there are none).  err (int32, optional):
-    what the forward pass finds is ORed into it, and later what the backward pass does; without it nothing tells of a
-    target outside the table (a row that does not count) or of a device wait that gave up (results undefined)."""
+    reduction 'mean' divides by the rows that count: a target in the table that is not ignore_index (0 when there are
+    none).  err (int32, optional): what the forward pass finds is ORed into it, and later what the backward pass does;
+    without it nothing tells of a target outside the table (a row that does not count) or of a device wait that gave up
+    (results undefined)."""
     _check_reduction(reduction)
     t = targets.reshape(-1)
     loss = _XentFunction.apply(hidden.reshape(-1, hidden.shape[-1]), weight, t, int(ignore_index), err)
     if reduction == "none":
         return loss.reshape(targets.shape)
-    return _reduce(loss, t != ignore_index, reduction)
+    vocab = weight.shape[0]
+    counts = t == t.clamp(0, vocab - 1)
+    return _reduce(loss, counts & (t != ignore_index) if 0 <= ignore_index < vocab else counts, reduction)
 
 
 def vocab_distillation(hidden: torch.Tensor, weight: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits: torch.Tensor,

@@ -622,3 +622,15 @@ def test_a_backward_wait_that_gives_up_is_in_the_callers_err(op):
         assert err.item() & 4
     finally:
         tt.tt_emb_head_set_wait_limit(2 * 10 ** 9)
+
+
+@pytest.mark.parametrize("ignore", [-100, 7])
+def test_mean_divides_by_the_rows_that_count(ignore):
+    """A target outside the table counts as ignored: in the mean's denominator too."""
+    h, w, t, _ = inputs(40, 100, 16, torch.float32, seed=40)
+    t = torch.where(t == -100, torch.full_like(t, ignore), t)
+    t[3], t[5], t[6], t[8] = 100, -1, 1 << 40, 7
+    valid = (t >= 0) & (t < 100) & (t != ignore)
+    got = tt.vocab_cross_entropy(h, w, t, ignore_index=ignore)
+    want = ref.xent(h, w, t, ignore=ignore)["loss"]
+    assert abs(got.item() - (want[0].sum() / valid.sum()).item()) <= (want[1].sum() / valid.sum()).item() + 2.0 ** -20 * got.item()
