@@ -338,6 +338,11 @@ def _reduce(loss, counts, reduction):
     return total if reduction == "sum" else total / counts.sum().clamp(min=1)
 
 
+def _same_rows(a, b):
+    """Shapes of the same rows in the same order: equal, or one of the two flattened."""
+    return a == b or (min(len(a), len(b)) == 1 and a.numel() == b.numel())
+
+
 def _check_reduction(reduction):
     if reduction not in ("none", "sum", "mean"):
         raise ValueError("reduction must be 'none', 'sum' or 'mean'")
@@ -352,6 +357,8 @@ def vocab_cross_entropy(hidden: torch.Tensor, weight: torch.Tensor, targets: tor
     without it nothing tells of a target outside the table (a row that does not count) or of a device wait that gave up
     (results undefined)."""
     _check_reduction(reduction)
+    if not _same_rows(hidden.shape[:-1], targets.shape):
+        _refuse(TT_ERR_SHAPE, f"targets have shape {tuple(targets.shape)}, expected {tuple(hidden.shape[:-1])}")
     t = targets.reshape(-1)
     loss = _XentFunction.apply(hidden.reshape(-1, hidden.shape[-1]), weight, t, int(ignore_index), err)
     if reduction == "none":
@@ -368,6 +375,9 @@ def vocab_distillation(hidden: torch.Tensor, weight: torch.Tensor, teacher_ids: 
     teacher_ids / teacher_logits [..., k]; negative ids are no entries.  reduction 'mean'
     divides by the rows that have an entry (0 when there are none).  err: as in vocab_cross_entropy."""
     _check_reduction(reduction)
+    if teacher_ids.dim() < 2 or not _same_rows(hidden.shape[:-1], teacher_ids.shape[:-1]) or teacher_logits.shape != teacher_ids.shape:
+        _refuse(TT_ERR_SHAPE, f"teacher_ids and teacher_logits have shapes {tuple(teacher_ids.shape)} and {tuple(teacher_logits.shape)}, "
+                              f"expected {tuple(hidden.shape[:-1])} + [k]")
     k = teacher_ids.shape[-1]
     ids = teacher_ids.reshape(-1, k)
     loss = _DistillFunction.apply(hidden.reshape(-1, hidden.shape[-1]), weight, ids, teacher_logits.reshape(-1, k), float(temperature), err)

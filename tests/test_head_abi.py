@@ -108,3 +108,27 @@ def test_wrong_tensors_are_refused_without_a_gpu():
     assert e.value.code == tt.TT_ERR_ARG
     with pytest.raises(tt.TTError):
         tt.tt_emb_q4_quantize(h)
+
+
+def _refused(code, call, *args):
+    with pytest.raises(tt.TTError) as e:
+        call(*args)
+    assert e.value.code == code
+
+
+def test_losses_refuse_shapes_that_do_not_match():
+    """Also those that hold the right number of elements."""
+    import torch
+
+    h, w = torch.zeros((4, 6, 8)), torch.zeros((5, 8))
+    t = torch.zeros((4, 6), dtype=torch.int64)
+    for bad in (t.t(), t.reshape(3, 8), t[:, :5], t[..., None], t.reshape(-1)[1:]):
+        _refused(tt.TT_ERR_SHAPE, tt.vocab_cross_entropy, h, w, bad)
+    ids, logits = torch.zeros((4, 6, 3), dtype=torch.int64), torch.zeros((4, 6, 3))
+    for bad_ids, bad_logits in ((ids.transpose(0, 1), logits.transpose(0, 1)), (ids, logits.transpose(1, 2)), (ids, logits.reshape(24, 3)), (ids.reshape(3, 8, 3), logits.reshape(3, 8, 3)),
+                                (ids[..., :2], logits), (ids[..., 0], logits[..., 0])):
+        _refused(tt.TT_ERR_SHAPE, tt.vocab_distillation, h, w, bad_ids, bad_logits)
+    # rows flattened on one side only are the same rows: these go on to the next check, which wants a GPU
+    for rows, ts in ((h, t.reshape(-1)), (h.reshape(24, 8), t)):
+        _refused(tt.TT_ERR_ARG, tt.vocab_cross_entropy, rows, w, ts)
+    _refused(tt.TT_ERR_ARG, tt.vocab_distillation, h, w, ids.reshape(24, 3), logits.reshape(24, 3))
