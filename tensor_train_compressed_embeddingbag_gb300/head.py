@@ -395,4 +395,6 @@ class Q4Table:
         self.packed, self.scales = tt_emb_q4_quantize(weight.detach(), group)
 
     def scores(self, x: torch.Tensor) -> torch.Tensor:
+        if x.dim() < 1 or x.shape[-1] != self.dim:
+            _refuse(TT_ERR_SHAPE, f"x has shape {tuple(x.shape)}, expected [..., {self.dim}]")
         return tt_emb_q4_matvec(x.reshape(-1, x.shape[-1]), self.packed, self.scales, self.group).reshape(*x.shape[:-1], self.vocab)

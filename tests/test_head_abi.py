@@ -132,3 +132,15 @@ def test_losses_refuse_shapes_that_do_not_match():
     for rows, ts in ((h, t.reshape(-1)), (h.reshape(24, 8), t)):
         _refused(tt.TT_ERR_ARG, tt.vocab_cross_entropy, rows, w, ts)
     _refused(tt.TT_ERR_ARG, tt.vocab_distillation, h, w, ids.reshape(24, 3), logits.reshape(24, 3))
+
+
+def test_a_4_bit_table_refuses_rows_of_another_width():
+    """Widths 33 to 64 have codes of one size: the table knows which is its own."""
+    import torch
+
+    table = tt.Q4Table.__new__(tt.Q4Table)
+    table.vocab, table.dim, table.group = 10, 64, 32
+    table.packed, table.scales = torch.zeros((10, 32), dtype=torch.uint8), torch.zeros((10, 2), dtype=torch.bfloat16)
+    for width in (33, 60, 65, 128):
+        _refused(tt.TT_ERR_SHAPE, table.scores, torch.zeros((2, width)))
+    _refused(tt.TT_ERR_SHAPE, table.scores, torch.zeros(()))
