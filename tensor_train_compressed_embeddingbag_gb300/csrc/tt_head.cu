@@ -1315,7 +1315,8 @@ tt_status head_backward(const Plan& p, const Target& t, const float* lse, const 
 
 tt_status forward_any(const tt_head* hd, const Target& t, float* loss, float* lse, int* err, void* ws, size_t n, tt_stream s) {
     Plan p;
-    const bool buffers = hd && (hd->rows == 0 || (hd->hidden_dev && t.ids && loss && lse)) && hd->weight_dev && ws && (uintptr_t)ws % 256 == 0;
+    const bool buffers = hd && (hd->rows == 0 || (hd->hidden_dev && t.ids && loss && lse)) && hd->weight_dev &&
+                         (ws || n == 0) && (uintptr_t)ws % 256 == 0;  // no rows may need no workspace
     const tt_status st = make_plan(hd, t.K, buffers, &p);
     if (st != TT_OK) return st;
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(s);

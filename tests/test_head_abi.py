@@ -144,3 +144,15 @@ def test_a_4_bit_table_refuses_rows_of_another_width():
     for width in (33, 60, 65, 128):
         _refused(tt.TT_ERR_SHAPE, table.scores, torch.zeros((2, width)))
     _refused(tt.TT_ERR_SHAPE, table.scores, torch.zeros(()))
+
+
+@pytest.mark.parametrize("dtype", [0, 1, 2])
+def test_no_rows_need_no_workspace(lib, dtype):
+    """16-bit types take no workspace for a forward pass of no rows: a null one of 0 bytes is right."""
+    h = head(rows=0, dtype=dtype, hidden_dev=None)
+    n = 1 << 20 if dtype == 0 else 0  # fp32 copies the table whatever the rows
+    for call in (lambda: lib.tt_emb_xent_forward(ctypes.byref(h), None, -100, None, None, None, 4096 if n else None, n, None),
+                 lambda: lib.tt_emb_distill_forward(ctypes.byref(h), None, None, 3, 1.0, None, None, None, 4096 if n else None, n, None)):
+        assert call() in (tt.TT_OK, tt.TT_ERR_CUDA)  # the latter without a GPU
+    if dtype:
+        assert forward(lib, head(dtype=dtype), ws=None) == tt.TT_ERR_ARG

@@ -634,3 +634,16 @@ def test_mean_divides_by_the_rows_that_count(ignore):
     got = tt.vocab_cross_entropy(h, w, t, ignore_index=ignore)
     want = ref.xent(h, w, t, ignore=ignore)["loss"]
     assert abs(got.item() - (want[0].sum() / valid.sum()).item()) <= (want[1].sum() / valid.sum()).item() + 2.0 ** -20 * got.item()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("d", [16, 200])
+def test_no_rows_of_any_type(dtype, d):
+    w = torch.randn((50, d), device="cuda").to(dtype)
+    h, t, grad = torch.empty((0, d), dtype=dtype, device="cuda"), torch.empty(0, dtype=torch.int64, device="cuda"), torch.empty(0, device="cuda")
+    ids, logits = torch.empty((0, 3), dtype=torch.int64, device="cuda"), torch.empty((0, 3), device="cuda")
+    for got in (run_xent(h, w, t, grad), run_distill(h, w, ids, logits, 2.0, grad)):
+        assert got["loss"].shape == got["lse"].shape == (0,) and got["grad_hidden"].shape == (0, d)
+        assert got["grad_weight"].shape == (50, d) and not got["grad_weight"].any()
+    assert tt.vocab_cross_entropy(h, w, t).item() == 0 and tt.vocab_distillation(h, w, ids, logits).item() == 0
+    assert tt.Q4Table(w, 32).scores(h).shape == (0, 50)
