@@ -928,8 +928,8 @@ tt_status make_plan(const tt_head* hd, int K, bool buffers, Plan* p) {
     // 4 bytes at a time.  Measured against the other kernels, rows x table: bf16 4 x 131072
     // x 4096 188 us (251), 8 x 131072 x 1024 61 (70), x 256 59 (59), but x 128 40 (34) and
     // 8 x 10^6 x 64 55 (38), where a tile's end outweighs its loads; fp32, which the others
-    // copy in pieces first, 8 x 131072 x 1024 116 (432), 16 rows in two passes 227 (463),
-    // 8 x 10^6 x 64 71 (144), 16 rows 135 (144).
+    // copy in pieces first, 8 x 131072 x 1024 99 (432), 16 rows in two passes 192 (463),
+    // 8 x 10^6 x 64 66 (144), 16 rows 125 (144).
     const int64_t chunks = cdiv((int64_t)in.D * p->esize, 64);
     p->few_smem = (size_t)(chunks * 512);
     p->few = in.N > 0 && in.N <= (p->split ? 16 : 8) && (p->split || in.D >= kFewMinDim) && (uintptr_t)in.w % 4 == 0 &&

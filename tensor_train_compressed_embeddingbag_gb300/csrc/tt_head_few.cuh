@@ -6,7 +6,8 @@
 // no copies in 16-bit pieces, and no 128-row tiles that are mostly padding.  The products
 // run on the warp-level tensor cores with the table's rows as the long side
 // (mma.sync: 16 table rows x 8 hidden rows); fp32 as TF32 hi and lo parts, hi hi + hi lo +
-// lo hi, split on the fly.  The order of k is free as long as both operands use the same,
+// lo hi, split on the fly (a step whose numbers are not all finite, or round to infinity, in
+// a slower way that keeps them what they are).  The order of k is free as long as both operands use the same,
 // so a thread's part of a table row is 16 bytes in one load (four, where rows do not begin
 // on 16-byte boundaries), and the hidden rows lie in shared
 // memory as the fragments want them.  A warp takes 32 table rows at a time; where there
@@ -14,10 +15,12 @@
 // added up in fp32 registers.  Each lane keeps the running maximum and sum of the table
 // row it holds; lanes, warps and blocks are joined at the end.
 //
-// Measured: bf16 4 x 131072 x 4096, 1.07 GB, 188 us (5.7 TB/s); fp32 8 x 131072 x 1024,
-// 0.54 GB, 116 us (4.6 TB/s).  What is left is latency: the loads of a step wait on the
-// registers of the one before, at 16 warps to an SM.
+// Measured: bf16 4 x 131072 x 4096, 1.07 GB, 190 us (5.6 TB/s); fp32 8 x 131072 x 1024,
+// 0.54 GB, 99 us (5.4 TB/s).  A step's loads go to the registers of the one before, which
+// bounds the bytes in flight at 16 warps to an SM; loads to shared memory are not tried.
 #pragma once
+
+#include <type_traits>
 
 #include "tt_head.cuh"
 
@@ -55,11 +58,27 @@ __device__ __forceinline__ void mma_few(float* d, const uint32_t* a, const uint3
 }
 
 // x as its TF32 part and the rest (exact), both rounded to nearest by adding half a unit:
-// the tensor core cuts what TF32 does not hold.
+// the tensor core cuts what TF32 does not hold.  Not for what that carries out of the finite
+// numbers, infinities and NaN.
 __device__ __forceinline__ void few_split(uint32_t& x, uint32_t& lo) {
     const uint32_t hi = (x + 0x1000u) & 0xFFFFE000u;
     lo = __float_as_uint(__uint_as_float(x) - __uint_as_float(hi)) + 0x1000u;
     x = hi;
+}
+// The same for any x (a quarter of the rate).  The rounding saturates: an infinity becomes the
+// largest number and an infinite rest, which meets the other operand's first part once, with
+// its sign; rounded to an infinity its rest would be NaN.  NaN stays NaN.
+__device__ __forceinline__ void few_split_any(uint32_t& x, uint32_t& lo) {
+    uint32_t hi;
+    asm("cvt.rna.satfinite.tf32.f32 %0, %1;" : "=r"(hi) : "f"(__uint_as_float(x)));
+    lo = __float_as_uint(__uint_as_float(x) - __uint_as_float(hi)) + 0x1000u;
+    x = hi;
+}
+constexpr float kFewMost = 3.401992698887923e38f;  // the largest number that few_split rounds down
+__device__ __forceinline__ float max_abs(float m, uint32_t a, uint32_t b) {  // NaN if any is
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(fabsf(__uint_as_float(a))), "f"(fabsf(__uint_as_float(b))));
+    return r;
 }
 
 template <class T, int TYPE, bool WIDE>  // WIDE: table rows begin on 16-byte boundaries, else on 4-byte ones
@@ -71,14 +90,17 @@ __global__ void __launch_bounds__(kFewThreads, 2) k_head_few(const __grid_consta
     __shared__ float2 parts[kFewWarps][8];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
 
+    float hmax = 0.f;
     for (int i = threadIdx.x; i < a.chunks * 32; i += kFewThreads) {
         const int l = i & 31, m = l >> 2, d0 = ((i >> 5) * 4 + (l & 3)) * E;
         __align__(16) T y[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) y[e] = m < a.N && d0 + e < a.D ? static_cast<const T*>(a.h)[m * a.ldh + d0 + e] : T(0.f);
-        xs[i] = *reinterpret_cast<uint4*>(y);
+        const uint4 u = *reinterpret_cast<uint4*>(y);
+        xs[i] = u;
+        if (TWO) hmax = max_abs(max_abs(hmax, u.x, u.y), u.z, u.w);
     }
-    __syncthreads();
+    const bool any_hidden = __syncthreads_or(TWO && !(hmax <= kFewMost));  // hidden rows that few_split is not for
 
     const int tiles_per_block = kFewWarps / a.ksplit, sub = warp / a.ksplit, ks = warp - sub * a.ksplit;
     const int steps = (a.chunks + C - 1) / C, jb = steps * ks / a.ksplit, je = steps * (ks + 1) / a.ksplit;
@@ -140,34 +162,50 @@ __global__ void __launch_bounds__(kFewThreads, 2) k_head_few(const __grid_consta
         for (int i = 0; i < U; ++i) {
             if (rd >= rounds) break;
             float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+            auto products = [&](auto any) {
+                auto split = [](uint32_t& x, uint32_t& lo) { decltype(any)::value ? few_split_any(x, lo) : few_split(x, lo); };
 #pragma unroll
-            for (int ch = 0; ch < C; ++ch) {
-                const int c = j * C + ch;
-                if (c >= a.chunks) break;
-                const uint4 bv = xs[c * 32 + lane];
-                uint32_t b[4] = {bv.x, bv.y, bv.z, bv.w}, bl[4];
-                if (TWO)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) few_split(b[e], bl[e]);
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const uint4 u0 = q[i][2 * r][ch], u8 = q[i][2 * r + 1][ch];
-                    uint32_t f0[4] = {u0.x, u0.y, u0.z, u0.w}, f8[4] = {u8.x, u8.y, u8.z, u8.w}, l0[4], l8[4];
+                for (int ch = 0; ch < C; ++ch) {
+                    const int c = j * C + ch;
+                    if (c >= a.chunks) break;
+                    const uint4 bv = xs[c * 32 + lane];
+                    uint32_t b[4] = {bv.x, bv.y, bv.z, bv.w}, bl[4];
                     if (TWO)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            few_split(f0[e], l0[e]);
-                            few_split(f8[e], l8[e]);
-                        }
+                        for (int e = 0; e < 4; ++e) split(b[e], bl[e]);
 #pragma unroll
-                    for (int k = 0; k < 4; k += 2) {
-                        if (TWO) {
-                            mma_few(acc[r], l0 + k, b + k, l8 + k, TYPE);
-                            mma_few(acc[r], f0 + k, bl + k, f8 + k, TYPE);
+                    for (int r = 0; r < 2; ++r) {
+                        const uint4 u0 = q[i][2 * r][ch], u8 = q[i][2 * r + 1][ch];
+                        uint32_t f0[4] = {u0.x, u0.y, u0.z, u0.w}, f8[4] = {u8.x, u8.y, u8.z, u8.w}, l0[4], l8[4];
+                        if (TWO)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                split(f0[e], l0[e]);
+                                split(f8[e], l8[e]);
+                            }
+#pragma unroll
+                        for (int k = 0; k < 4; k += 2) {
+                            if (TWO) {
+                                mma_few(acc[r], l0 + k, b + k, l8 + k, TYPE);
+                                mma_few(acc[r], f0 + k, bl + k, f8 + k, TYPE);
+                            }
+                            mma_few(acc[r], f0 + k, b + k, f8 + k, TYPE);
                         }
-                        mma_few(acc[r], f0 + k, b + k, f8 + k, TYPE);
                     }
                 }
+            };
+            if (TWO) {
+                float m = 0.f;
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+#pragma unroll
+                    for (int ch = 0; ch < C; ++ch) m = max_abs(max_abs(m, q[i][r][ch].x, q[i][r][ch].y), q[i][r][ch].z, q[i][r][ch].w);
+                if (__any_sync(0xffffffffu, any_hidden || !(m <= kFewMost)))
+                    products(std::true_type());
+                else
+                    products(std::false_type());
+            } else {
+                products(std::false_type());
             }
 #pragma unroll
             for (int r = 0; r < 2; ++r)

@@ -1,0 +1,83 @@
+"""Infinities and NaN that count: a table row that is scored -inf drops out, NaN is not lost.
+
+Rows are banned from a table as they are in practice: a column of biases, 0 or -inf, that hidden holds a 1 for.  Bounds are
+_head_ref.py's for the table without the banned rows."""
+import math
+
+import pytest
+import torch
+
+import tensor_train_compressed_embeddingbag_gb300 as tt
+
+import _head_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+TYPES = [torch.float32, torch.bfloat16, torch.float16]
+
+
+def banned_table(n, v, d, dtype, seed):
+    """hidden, table, targets, grad, banned: every third row and one whole tile of the table."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    h = torch.randn((n, d), generator=g, device="cuda").to(dtype)
+    w = (torch.randn((v, d), generator=g, device="cuda") * (2.0 / math.sqrt(d))).to(dtype)
+    banned = torch.arange(v, device="cuda") % 3 == 1
+    banned[256:384] = True
+    h[:, -1], w[:, -1] = 1.0, torch.where(banned, -float("inf"), 0.0)
+    free = (~banned).nonzero()[:, 0]
+    t = free[torch.randint(0, free.numel(), (n,), generator=g, device="cuda")]
+    if n > 2:
+        t[n // 2] = -100
+    return h, w, t, (torch.rand((n,), generator=g, device="cuda") + 0.5) / n, banned
+
+
+def without_banned(h, w, t, grad, banned):
+    """_head_ref's values and bounds over the rows that are not banned."""
+    at = torch.cumsum(~banned, 0) - 1
+    return ref.xent(h, w[~banned], torch.where(t >= 0, at[t.clamp(min=0)], t), grad=grad)
+
+
+def check_forward(n, v, d, dtype):
+    h, w, t, grad, banned = banned_table(n, v, d, dtype, 1)
+    loss, lse = tt.tt_emb_xent_forward(h, w, t)
+    ref.check({"loss": loss, "lse": lse}, without_banned(h, w, t, grad, banned))
+
+
+NANS = [0x7FC00000, 0x7FFFFFFF, -1]  # a library's, this GPU's, the same with a sign
+
+
+def check_nan(n, v, d, bits):
+    """fp32: a NaN of these bits in the table makes every row NaN, in one hidden row that row."""
+    h, w, t, _, _ = banned_table(n, v, d, torch.float32, 2)
+    w = w[:, :-1].contiguous()
+    h = h[:, :-1].contiguous()
+    bad = w.clone()
+    bad.view(torch.int32)[v // 2, 3] = bits
+    assert torch.isnan(tt.tt_emb_xent_forward(h, bad, t)[1]).all()
+    bad = h.clone()
+    bad.view(torch.int32)[n - 1, d // 2] = bits
+    lse = tt.tt_emb_xent_forward(bad, w, t)[1]
+    assert torch.isnan(lse[n - 1]) and not torch.isnan(lse[:n - 1]).any()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n,v,d", [(1, 1000, 256), (4, 1000, 64), (8, 3000, 320), (16, 2000, 300), (5, 700, 31)])
+def test_few_rows_forward(n, v, d, dtype):
+    check_forward(n, v, d, dtype)
+
+
+@pytest.mark.parametrize("bits", NANS)
+@pytest.mark.parametrize("n,v,d", [(1, 1000, 257), (8, 500, 65), (16, 2000, 301)])
+def test_nan_in_few_rows(n, v, d, bits):
+    check_nan(n, v, d, bits)
+
+
+def test_few_rows_of_the_largest_values():
+    """fp32's largest values are not rounded up to infinity."""
+    w = torch.zeros((40, 64), device="cuda")
+    w[3, 5], w[4, 5] = torch.finfo(torch.float32).max, torch.finfo(torch.float32).min
+    h = torch.full((2, 64), 2.0 ** -126, device="cuda")
+    lse = tt.tt_emb_xent_forward(h, w, torch.zeros(2, dtype=torch.int64, device="cuda"))[1]
+    want = torch.logsumexp(ref.scores(h, w), 1)  # a score of 4, one of -4, 38 of 0
+    assert ((lse.double() - want).abs() <= 2.0 ** -9 * 4).all()  # the largest values enter as TF32 holds them, cut: 2^-10
