@@ -159,6 +159,12 @@ __device__ __forceinline__ float join_parts(const float2* p, int n, int lane) {
     return (b + log2f(s)) * kLn2;
 }
 
+__device__ __forceinline__ void split1(float x, uint16_t& hi, uint16_t& lo) {
+    const uint32_t h = pack_hi(x, 0.f);
+    hi = (uint16_t)h;
+    lo = __half_as_ushort(__float2half_rn(x - unpack_f16(h).x));
+}
+
 constexpr int kRowThreads = 128;  // per row or four rows; wide: per row, when rows are few and have many entries
 constexpr int kRowThreadsWide = 512;
 constexpr int kAmaxShares = 64;  // blocks that look for the largest magnitudes
@@ -400,9 +406,10 @@ __global__ void __launch_bounds__(RT)
         const bool is = any && i < in.D;
         const float x = is && (sizeof(T) == 4 || a.hq) ? to_f32(h[i]) * exp2i(eh) : 0.f;
         const auto scaled = [&](uint16_t* to, float y) {
-            const __half hi = __float2half_rn(y);
-            to[at] = __half_as_ushort(hi);
-            if (sizeof(T) == 4) to[piece + at] = __half_as_ushort(__float2half_rn(y - __half2float(hi)));
+            if (sizeof(T) == 4)
+                split1(y, to[at], to[piece + at]);
+            else
+                to[at] = __half_as_ushort(__float2half_rn(y));
         };
         if (sizeof(T) == 4)
             scaled(a.hp, x);
@@ -450,7 +457,7 @@ __device__ __forceinline__ void split8(const float (&x)[8], float sc, uint16_t* 
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const float a = x[2 * j] * sc, b = x[2 * j + 1] * sc;
-        hi[j] = pack16(a, b, 0);
+        hi[j] = pack_hi(a, b);
         const float2 h = unpack_f16(hi[j]);
         lo[j] = pack16(a - h.x, b - h.y, 0);
     }
@@ -557,10 +564,7 @@ __global__ void __launch_bounds__(TH, 1024 / TH) k_head_prep(const __grid_consta
                 const int e = scale_exp(__reduce_max_sync(0xffffffffu, m));
                 if (lane == 0) a.row_exp[n] = e;
                 for (int i = lane; i < in.Dp; i += 32) {
-                    const float x = i < in.D ? to_f32(h[i]) * exp2i(e) : 0.f;
-                    const __half hi = __float2half_rn(x);
-                    hp[n * in.Dp + i] = __half_as_ushort(hi);
-                    hp[piece + n * in.Dp + i] = __half_as_ushort(__float2half_rn(x - __half2float(hi)));
+                    split1(i < in.D ? to_f32(h[i]) * exp2i(e) : 0.f, hp[n * in.Dp + i], hp[piece + n * in.Dp + i]);
                 }
             } else {
                 const uint16_t* s = reinterpret_cast<const uint16_t*>(h);

@@ -264,6 +264,14 @@ __device__ __forceinline__ uint32_t pack16(float a, float b, int fmt) {
         asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
     return r;
 }
+// The hi pieces of two fp32 operands: infinities become the largest f16, and what is left
+// of them, the lo piece, infinite.  So one product of an infinity (with the other operand's hi
+// piece, which has its sign) is infinite and none is inf - inf or infinity times a lo piece of 0.
+__device__ __forceinline__ uint32_t pack_hi(float a, float b) {
+    uint32_t r;
+    asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    return r;
+}
 // 32 floats rounded and packed; one branch on the type.
 __device__ __forceinline__ void pack32(const float (&p)[32], uint32_t (&q)[16], int fmt) {
     if (fmt) {

@@ -144,9 +144,13 @@ __global__ void __launch_bounds__(kQ4Threads, 2) k_q4_matvec(const __grid_consta
         for (int e = 0; e < 8; ++e) {
             const int k = (e >> 1) + (e & 1) * 4;
             const float v = (all ? to_f32(y[k]) : (m < a.M && d0 + k < a.D ? to_f32(x[m * a.ldx + d0 + k]) : 0.f)) * up[m];
-            const __half hi = __float2half_rn(v);
-            u[0][e] = __half_as_ushort(hi);
-            if (P == 2) u[P - 1][e] = __half_as_ushort(__float2half_rn(v - __half2float(hi)));
+            if (P == 2) {
+                const uint32_t hi = pack_hi(v, 0.f);
+                u[0][e] = (uint16_t)hi;
+                u[P - 1][e] = __half_as_ushort(__float2half_rn(v - unpack_f16(hi).x));
+            } else {
+                u[0][e] = __half_as_ushort(__float2half_rn(v));
+            }
         }
 #pragma unroll
         for (int p = 0; p < P; ++p) xs[(((j * W + w) * P + p) * NT + nt) * 32 + l] = *reinterpret_cast<uint4*>(u[p]);

@@ -81,3 +81,66 @@ def test_few_rows_of_the_largest_values():
     lse = tt.tt_emb_xent_forward(h, w, torch.zeros(2, dtype=torch.int64, device="cuda"))[1]
     want = torch.logsumexp(ref.scores(h, w), 1)  # a score of 4, one of -4, 38 of 0
     assert ((lse.double() - want).abs() <= 2.0 ** -9 * 4).all()  # the largest values enter as TF32 holds them, cut: 2^-10
+
+
+MANY = [(20, 1000, 64), (40, 3000, 128), (130, 2000, 100), (20, 1500, 300), (300, 2000, 200)]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n,v,d", MANY)
+def test_many_rows_forward(n, v, d, dtype):
+    check_forward(n, v, d, dtype)
+
+
+@pytest.mark.parametrize("bits", NANS)
+@pytest.mark.parametrize("n,v,d", [(20, 1000, 65), (40, 3000, 129), (20, 1500, 301)])
+def test_nan_in_many_rows(n, v, d, bits):
+    check_nan(n, v, d, bits)
+
+
+def check_gradients(h, w, t, grad, banned):
+    """The banned rows of dweight are 0, the column of biases aside (0 times -inf) dhidden is what it is without them."""
+    loss, lse = tt.tt_emb_xent_forward(h, w, t)
+    gh, gw = tt.tt_emb_xent_backward(h, w, t, lse, grad)
+    want = without_banned(h, w, t, grad, banned)
+    ref.check({"loss": loss, "lse": lse, "grad_weight": gw[~banned]}, want)
+    ref.check({"grad_hidden": gh[:, :-1]}, {"grad_hidden": [x[:, :-1] for x in want["grad_hidden"]]})
+    assert not gw[banned].any()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n,v,d", [(20, 1500, 300), (300, 2000, 200), (4, 600, 257)])
+def test_gradients(n, v, d, dtype):
+    h, w, t, grad, banned = banned_table(n, v, d, dtype, 3)
+    t[t < 0] = 0
+    check_gradients(h, w, t, grad, banned)
+
+
+def test_an_infinite_hidden_row_is_its_own():
+    """An infinity in one hidden row: scores of both infinities there, the others as they are."""
+    for n, v, d in MANY:
+        h, w, t, _, _ = banned_table(n, v, d, torch.float32, 4)
+        h, w = h[:, :-1].contiguous(), w[:, :-1].contiguous()
+        clean = tt.tt_emb_xent_forward(h, w, t)[1]
+        h[7, 3] = -float("inf")
+        lse = tt.tt_emb_xent_forward(h, w, t)[1]
+        others = torch.arange(n, device="cuda") != 7
+        assert not torch.isfinite(lse[7]) and torch.equal(lse[others], clean[others])
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("m", [1, 9, 40])
+def test_4_bit_scores_of_an_infinity(m, dtype):
+    """An infinity in x: the sign of its column's code where that is not 0, NaN where it is."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+    packed, scales = tt.tt_emb_q4_quantize(torch.randn((300, 96), generator=g, device="cuda"), 32)
+    x = torch.randn((m, 96), generator=g, device="cuda").to(dtype)
+    x[0, 40] = float("inf")
+    got = tt.tt_emb_q4_matvec(x, packed, scales, 32)
+    column = ref.unpack_q4(packed, scales, 96, 32)[:, 40]
+    assert torch.equal(got[0] == float("inf"), column > 0) and torch.equal(got[0] == -float("inf"), column < 0)
+    assert torch.equal(torch.isnan(got[0]), column == 0)
+    if m > 1:
+        want, bound = ref.q4(x[1:], packed, scales, 32)
+        assert ((got[1:].double() - want).abs() <= bound).all()
