@@ -299,9 +299,10 @@ __global__ void __launch_bounds__(RT) k_head_finish(HeadIn in, Target t, const f
 
 // What the backward pass needs of every row, a block per row: its weight (g T, 0 for a
 // row that does not count) under its own scale and under the batch's, its lse in log2
-// units, dz of its target entries under the batch's, and its packed copy (zeros for a row
-// that does not count, so that nothing such a row holds, infinities and NaN included,
-// reaches dweight).  Entries of one row with the same id hold the same value, of their
+// units, dz of its target entries under the batch's, and its packed copy.  A row that does
+// not count, and what fills up a tile of k_head_fused, is all ones with an lse that makes every
+// p 0: nothing that it holds, infinities and NaN included, reaches dweight, and a table row
+// that is scored -inf by a column of its own is so there too (zeros would make it NaN).  Entries of one row with the same id hold the same value, of their
 // summed q.  Target entries go to arrays [K][N] (ids, dzt) and, for k_head_fused, to their
 // 32 x 32 blocks.
 struct RowsArgs {
@@ -318,9 +319,12 @@ struct RowsArgs {
     int nblocks;
     TargetEntry* ents;
     uint16_t* hp;
+    int64_t hrows;  // rows of hp
     uint16_t* hq;  // null, or hidden rows under hidden's scale, less what the row's has over the batch's, for dweight
+    uint16_t one;  // 1 in hp's type
     int* err;
 };
+constexpr float kNoLse = -3e38f;  // -lse of a row that does not count
 template <class T, bool DISTILL, int RT>
 __global__ void __launch_bounds__(RT)
     k_head_rows(HeadIn in, Target t, const __grid_constant__ RowsArgs a) {
@@ -328,6 +332,17 @@ __global__ void __launch_bounds__(RT)
     const int64_t n = blockIdx.x;
     const T* h = static_cast<const T*>(in.h) + n * in.ldh;
     const T* w = static_cast<const T*>(in.w);
+    if (n >= in.N) {
+        if (threadIdx.x == 0) {
+            a.nlse[n] = kNoLse;
+            a.scale[n] = a.scale_batch[n] = a.to_own[n] = 0.f;
+        }
+        for (int i = threadIdx.x; i < in.Dp; i += RT) {
+            a.hp[n * in.Dp + i] = a.one;
+            if (sizeof(T) == 4) a.hp[(a.hrows + n) * in.Dp + i] = 0;
+        }
+        return;
+    }
     const float l = a.lse[n];
     bool any;
     extern __shared__ float sm[];
@@ -367,13 +382,11 @@ __global__ void __launch_bounds__(RT)
     }
     const float rs = gt * exp2i(ez), rb = rs * exp2i(-own);
     if (threadIdx.x == 0) {
-        a.nlse[n] = any ? -l * kLog2e : 0.f;
+        a.nlse[n] = any ? -l * kLog2e : kNoLse;
         a.scale[n] = rs;
         a.scale_batch[n] = rb;
         a.to_own[n] = exp2i(own);
     }
-    if (n == in.N - 1)
-        for (int64_t i = in.N + threadIdx.x; i < (in.N + 127) / 128 * 128; i += RT) a.nlse[i] = a.scale[i] = a.scale_batch[i] = a.to_own[i] = 0.f;
     const auto put = [&](int k, int64_t id, float d, bool first) {
         a.ids[k * in.N + n] = (int)id;
         a.dzt[k * in.N + n] = d;
@@ -400,22 +413,21 @@ __global__ void __launch_bounds__(RT)
         const float z = xid >= 0 ? warp_dot(h, w + xid * in.ldw, in.D, in.vec, lane) : 0.f;
         if (lane == 0) put(0, xid, xid >= 0 ? (expf(z - l) - 1.f) * rb : 0.f, true);
     }
-    const int64_t piece = in.N * in.Dp;
-    for (int i = threadIdx.x; i < in.Dp; i += RT) {
+    for (int i = threadIdx.x; i < in.Dp; i += RT) {  // columns past D are not read
         const int64_t at = n * in.Dp + i;
         const bool is = any && i < in.D;
         const float x = is && (sizeof(T) == 4 || a.hq) ? to_f32(h[i]) * exp2i(eh) : 0.f;
-        const auto scaled = [&](uint16_t* to, float y) {
+        const auto scaled = [&](uint16_t* to, int64_t rows, float y) {
             if (sizeof(T) == 4)
-                split1(y, to[at], to[piece + at]);
+                split1(y, to[at], to[rows * in.Dp + at]);
             else
                 to[at] = __half_as_ushort(__float2half_rn(y));
         };
         if (sizeof(T) == 4)
-            scaled(a.hp, x);
+            scaled(a.hp, a.hrows, any ? x : 1.f);
         else
-            a.hp[at] = is ? reinterpret_cast<const uint16_t*>(h)[i] : (uint16_t)0;
-        if (a.hq) scaled(a.hq, x * exp2i(-own));
+            a.hp[at] = is ? reinterpret_cast<const uint16_t*>(h)[i] : a.one;
+        if (a.hq) scaled(a.hq, in.N, x * exp2i(-own));
     }
 }
 
@@ -790,8 +802,6 @@ bool run_fused(const Operand& X, const Operand& Y, FusedArgs a, int dev, cudaStr
     CUtensorMap mx, my;
     if (!make_map(&mx, X.p, a.fmt, X.cols, X.rows, S::PC, X.pitch, X.piece, 128)) return false;
     if (!make_map(&my, Y.p, a.fmt, Y.cols, Y.rows, S::PC, Y.pitch, Y.piece, S::BY)) return false;
-    a.X = X.rows;
-    a.Y = Y.rows;
     a.wait_ns = g_head_wait_ns;
     auto k = k_head_fused<DT, SPLIT, MODE>;
     if (!allow_smem<KernelTag<DT, SPLIT, MODE, 0, -1>>(k, dev, S::kSmem)) return false;
@@ -866,6 +876,7 @@ struct Plan {
     Runs runs_lse, runs_dw, runs_dh;
     bool fused;              // backward: dz stays on the chip (k_head_fused)
     int64_t nblocks, vblocks;  // its 32 x 32 blocks
+    int64_t hrows;             // rows of hidden's copy
     int64_t P;               // else: vocabulary piece
     int64_t pitch;           // its row pitch in dz
     int dh_splits, dw_splits;
@@ -958,8 +969,10 @@ tt_status make_plan(const tt_head* hd, int K, bool buffers, Plan* p) {
     p->few_targets = !p->split && in.N * K <= kFewTargets;
     p->nblocks = cdiv(in.N, 32);
     p->vblocks = cdiv(in.V, 32);
+    p->hrows = in.N;
     p->fused = in.D <= 128 && p->nblocks * p->vblocks <= kMaxBlocks;
     if (p->fused) {
+        p->hrows = mt * 128;
         p->dh_splits = p->dw_splits = 1;
         p->dh_direct = true;
         if (in.N > 0) {
@@ -1029,7 +1042,7 @@ size_t bwd_ws(const Plan& p, int K, void* base, BwdWs* w) {
     w->dzt = a.get<float>(nk);
     w->blocks = a.get<TargetBlock>(p.fused ? p.nblocks * p.vblocks : 0);
     w->ents = a.get<TargetEntry>(p.fused ? nk : 0);
-    w->hp = a.get<uint16_t>(pc * p.in.N * p.in.Dp);
+    w->hp = a.get<uint16_t>(pc * p.hrows * p.in.Dp);
     w->hq = a.get<uint16_t>(p.scaled && !p.fused ? pc * p.in.N * p.in.Dp : 0);
     w->wp = a.get<uint16_t>(p.pack_w ? pc * p.in.V * p.in.Dp : 0);
     w->dz = a.get<uint16_t>(pc * p.in.N * p.pitch);
@@ -1126,6 +1139,8 @@ tt_status head_forward(const Plan& p, const Target& t, float* loss, float* lse, 
         }
     } else if (p.fused_lse) {
         FusedArgs a{};
+        a.X = in.N;
+        a.Y = in.V;
         a.D = in.D;
         a.runs = p.runs_lse;
         a.slots = p.slots;
@@ -1189,9 +1204,10 @@ tt_status head_backward(const Plan& p, const Target& t, const float* lse, const 
         a.nclear = blocks ? p.nblocks * p.vblocks : 0;
         if (!launch_prep<T>(p, a, st)) return TT_ERR_CUDA;
     }
-    const RowsArgs ra{lse,   grad,  w.shares, amax,           w.zexp, w.nlse, w.scale,                    w.scale_batch, w.to_own,
-                      w.ids, w.dzt, blocks,   (int)p.nblocks, w.ents, w.hp,   use_hq ? w.hq : nullptr, err};
-    const auto rows = [&](auto kernel, int threads) { kernel<<<(unsigned)in.N, threads, (size_t)t.K * 12, st>>>(in, t, ra); };
+    const uint16_t one = p.type == TT_BF16 ? 0x3F80 : 0x3C00;
+    const RowsArgs ra{lse,   grad,  w.shares, amax,           w.zexp, w.nlse, w.scale, w.scale_batch,             w.to_own,
+                      w.ids, w.dzt, blocks,   (int)p.nblocks, w.ents, w.hp,   p.hrows, use_hq ? w.hq : nullptr, one,     err};
+    const auto rows = [&](auto kernel, int threads) { kernel<<<(unsigned)p.hrows, threads, (size_t)t.K * 12, st>>>(in, t, ra); };
     if (distill && wide_rows(p, t.K))
         rows(k_head_rows<T, true, kRowThreadsWide>, kRowThreadsWide);
     else if (distill)
@@ -1202,7 +1218,7 @@ tt_status head_backward(const Plan& p, const Target& t, const float* lse, const 
     const uint32_t *ah = amax, *az = amax ? amax + 2 : nullptr;
     const int64_t wpitch = p.pack_w ? in.Dp : in.ldw;
     const uint16_t* w0 = p.pack_w ? w.wp : static_cast<const uint16_t*>(in.w);
-    const Operand H{w.hp, in.N, in.D, in.Dp, in.N * in.Dp};
+    const Operand H{w.hp, p.hrows, in.D, in.Dp, p.hrows * in.Dp};
     const auto dest = [&](void* out, float* partial) {
         OutArgs o{};
         o.out = out;
@@ -1255,16 +1271,20 @@ tt_status head_backward(const Plan& p, const Target& t, const float* lse, const 
         a.nblocks = (int)p.nblocks;
         a.vblocks = (int)p.vblocks;
         a.partial = w.joins;
+        a.X = in.V;
+        a.Y = in.N;
         a.runs = p.runs_dw;
         a.to = dest(dw, nullptr);
         if (!fused<kDweight>(p.split, W, H, a, p.device, st)) return TT_ERR_CUDA;
+        a.X = in.N;
+        a.Y = in.V;
         a.runs = p.runs_dh;
         a.scale = w.scale;
         a.to = dest(dh, nullptr);
         a.low = low;
         return fused<kDhidden>(p.split, H, W, a, p.device, st) && target_rows() ? TT_OK : TT_ERR_CUDA;
     }
-    const Operand Hq{use_hq ? w.hq : w.hp, in.N, in.D, in.Dp, in.N * in.Dp};
+    const Operand Hq{use_hq ? w.hq : w.hp, in.N, in.D, in.Dp, in.N * in.Dp};  // hrows is N here
     const int64_t npieces = cdiv(in.V, p.P), dz_piece = in.N * p.pitch;
     for (int64_t i = 0; i < npieces; ++i) {
         const int64_t v0 = i * p.P, P = in.V - v0 < p.P ? in.V - v0 : p.P;
@@ -1307,6 +1327,7 @@ tt_status head_backward(const Plan& p, const Target& t, const float* lse, const 
         c.splits = p.dh_splits;
         c.amax_a = az;
         c.row_exp = zexp;
+        c.scale = w.scale;
         c.kb = (int)cdiv(in.D, 128);
         c.wexp = p.split ? w.wexp + v0 / 128 * c.kb : nullptr;
         c.to = dest(p.dh_direct ? dh : nullptr, w.dh_part);

@@ -89,7 +89,7 @@ struct FusedArgs {
     float2* part;            // kLse: [X][slots][kParts] (maximum in log2 units, sum), a slot per run
     int slots;
     const float* nlse;       // per hidden row -lse in log2 units, and its scaled weight (kDhidden: by the
-    const float* scale;      //   row's own power of two, kDweight: by the batch's); zeros up to a multiple of 128 rows
+    const float* scale;      //   row's own power of two, kDweight: by the batch's); up to a multiple of 128 rows
     const int* zexp;         // kDhidden: exponent of the row's own scale over the batch's (null: 0),
     const float* to_own;     //   and what takes an element of dz from the batch's scale to it, as scale has it
     const TargetBlock* blocks;  // [vblocks][nblocks]
@@ -508,6 +508,7 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
             const int64_t row = (int64_t)w.x * 128 + quad * 32 + lane;
             const uint32_t l0 = tmem + ((uint32_t)(quad * 32) << 16) + S::kOutCol + half * (DT / 2);
             const bool whole = w.y0 == 0 && w.y1 == a.runs.ytiles && !(MODE == kDhidden && a.low.K);
+            const auto counts = [&] { return COLS || (row < a.X && __ldg(&a.scale[row]) != 0.f); };  // else dhidden is 0, whatever the table holds
             const auto scales = [&] {  // that the row's sums are still to be freed of; SPLIT dhidden: of its own only
                 const int own = !COLS && a.zexp && row < a.X ? __ldg(&a.zexp[row]) : 0;
                 return Pow2(SPLIT && !COLS ? -own : -eb - own);
@@ -515,6 +516,10 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
             float* part = a.partial + (((int64_t)blockIdx.x * 2 + !first) * 128 + quad * 32) * a.to.pp;
             auto put = [&](float(&v)[32], int col) {
                 if (row - lane >= a.X || col >= a.D) return;
+                if (!counts()) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = 0.f;
+                }
                 if (whole)
                     store_out(a.to, rows_out[warp - 4], 0, row - lane, col, a.X, a.D, v, scales());
                 else
@@ -573,6 +578,10 @@ __global__ void __launch_bounds__((FusedShape<DT, SPLIT>::kThreads), 1)
                         tm_wait_ld(v);
                         sc(v);
                         pack32(v, q[ch], a.fmt);
+                        if (!counts()) {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) q[ch][j] = 0;
+                        }
                     }
                     tc_fence_before();
                     __syncwarp();

@@ -36,7 +36,7 @@ struct GemmArgs {
     // kEpiStats
     float2* part;        // [M][nstrips][kParts] (maximum in log2 units, sum)
     // kEpiDz
-    const float* nlse;   // per row -lse in log2 units, and its scale
+    const float* nlse;   // per row -lse in log2 units, and its scale (kEpiOut: null, or 0 for rows that are 0)
     const float* scale;
     uint16_t* dz;        // [pieces][M][dz_pitch]
     int64_t dz_pitch, dz_piece;
@@ -214,6 +214,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             if ((SPLIT || EPI == kEpiOut) && a.row_exp && in) er += a.row_exp[row];
             const Pow2 sc(SPLIT ? 0 : -er);
             if (EPI == kEpiDz && in) rc = make_float2(a.nlse[row], a.scale[row]);
+            const bool zero = EPI == kEpiOut && a.scale && in && a.scale[row] == 0.f;
             for (int n = n0; ok && n < n1; ++n) {
                 const int64_t col0 = (int64_t)n * BN + part * (BN / kParts);
                 // 32 finished columns of this thread's row, the first of them `col`
@@ -233,6 +234,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                             }
                         }
                     } else if (col < a.N && row - lane < a.M) {
+                        if (zero) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) v[j] = 0.f;
+                        }
                         store_out(a.to, buf, split, row - lane, col, a.M, a.N, v, sc);
                     }
                 };

@@ -109,11 +109,32 @@ def check_gradients(h, w, t, grad, banned):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("n,v,d", [(20, 1500, 300), (300, 2000, 200), (4, 600, 257)])
+@pytest.mark.parametrize("n,v,d", MANY + [(5, 700, 32), (4, 600, 257), (128, 900, 48), (256, 384, 128)])
 def test_gradients(n, v, d, dtype):
     h, w, t, grad, banned = banned_table(n, v, d, dtype, 3)
     t[t < 0] = 0
     check_gradients(h, w, t, grad, banned)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n,v,d", MANY + [(5, 700, 32), (4, 600, 257), (128, 900, 48), (256, 384, 128)])
+def test_gradients_beside_rows_that_do_not_count(n, v, d, dtype):
+    """Rows that do not count, whatever they hold, get 0 in every column, that of the biases too, and give nothing; with none
+    that counts dweight is 0."""
+    h, w, t, grad, banned = banned_table(n, v, d, dtype, 6)
+    t[::3] = -100
+    ignored = t < 0
+    h[ignored] = torch.tensor([float("nan"), float("inf"), -float("inf"), 0.0], dtype=dtype, device="cuda")[torch.arange(n, device="cuda") % 4][ignored, None]
+    lse = tt.tt_emb_xent_forward(h, w, t)[1]
+    gh, gw = tt.tt_emb_xent_backward(h, w, t, lse, grad)
+    clean = torch.where(ignored[:, None], torch.zeros_like(h), h)
+    want = without_banned(clean, w, t, grad, banned)
+    assert not gh[ignored].any() and not gw[banned].any()
+    ref.check({"grad_weight": gw[~banned]}, want)
+    ref.check({"grad_hidden": gh[:, :-1]}, {"grad_hidden": [x[:, :-1] for x in want["grad_hidden"]]})
+    t[:] = -100
+    gh, gw = tt.tt_emb_xent_backward(h, w, t, tt.tt_emb_xent_forward(h, w, t)[1], grad)
+    assert not gh.any() and not gw.any()
 
 
 def test_an_infinite_hidden_row_is_its_own():
