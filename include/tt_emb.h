@@ -480,7 +480,8 @@ tt_status tt_emb_head_set_wait_limit(uint64_t ns);
  *
  * tt_emb_q4_quantize lays a dense table out so: per group scale = bf16(max |w| / 7),
  *   code = round(w / scale) held within [-8, 7], plus 8; an all-zero group gets scale
- *   0.  weight_dev [vocab][dim] of `dtype` (tt_dtype), rows weight_stride apart.
+ *   0.  A group with infinities gets an infinite scale and keeps only them (codes 7 and
+ *   9), so they outweigh it; one with a NaN gets a scale of NaN.  weight_dev [vocab][dim] of `dtype` (tt_dtype), rows weight_stride apart.
  * tt_emb_q4_matvec: x_dev [rows][dim] of `dtype`, rows x_stride apart; out_dev float
  *   [rows][vocab], written whole.  Every product is exact and sums are fp32.  Meant for
  *   few rows: each 32 of them read the table once.

@@ -296,7 +296,8 @@ __global__ void __launch_bounds__(kQ4Threads, 2) k_q4_matvec(const __grid_consta
 }
 
 // Codes and scales of a table: per group, scale = bf16(max |w| / 7), code = w / scale
-// rounded to nearest (ties to even), held within [-8, 7], plus 8.  A thread takes 8 columns.
+// rounded to nearest (ties to even), held within [-8, 7], plus 8.  A group that holds an
+// infinity has an infinite scale, one with a NaN a scale of NaN.  A thread takes 8 columns.
 template <class T>
 __global__ void __launch_bounds__(256) k_q4_quantize(const T* w, int64_t ldw, int64_t V, int D, int G, uint8_t* packed, int64_t pitch,
                                                      __nv_bfloat16* scales, int groups) {
@@ -306,19 +307,23 @@ __global__ void __launch_bounds__(256) k_q4_quantize(const T* w, int64_t ldw, in
         const bool live = i < total;
         const int64_t v = live ? i / per_row : 0;
         const int c = live ? (int)(i - v * per_row) : 0, d0 = c * 8;
-        float x[8], m = 0.f;
+        float x[8];
+        uint32_t most = 0;  // bits of the largest magnitude; infinities and NaN are above all others
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             x[j] = live && d0 + j < D ? to_f32(w[v * ldw + d0 + j]) : 0.f;
-            m = fmaxf(m, fabsf(x[j]));
+            most = max(most, __float_as_uint(x[j]) & 0x7FFFFFFFu);
         }
-        for (int o = tg / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        for (int o = tg / 2; o; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+        const float m = __uint_as_float(most);
         const __nv_bfloat16 sb = __float2bfloat16_rn(m / 7.f);
         const float s = __bfloat162float(sb);
         uint32_t q = 0;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const float r = s > 0.f ? fminf(fmaxf(rintf(x[j] / s), -8.f), 7.f) : 0.f;
+            // an infinite scale: its infinities are 1 and -1 of it
+            const float r = s == INFINITY ? (fabsf(x[j]) == INFINITY ? copysignf(1.f, x[j]) : 0.f)
+                                          : (s > 0.f ? fminf(fmaxf(rintf(x[j] / s), -8.f), 7.f) : 0.f);
             q |= (uint32_t)((int)r + 8) << (4 * j);
         }
         if (!live) continue;

@@ -165,3 +165,28 @@ def test_4_bit_scores_of_an_infinity(m, dtype):
     if m > 1:
         want, bound = ref.q4(x[1:], packed, scales, 32)
         assert ((got[1:].double() - want).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_4_bit_tables_of_infinities_and_nan(group, dtype):
+    """An infinite element keeps its sign and outweighs its group; a NaN makes its row's scores NaN; other rows are as they are."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(7)
+    w = torch.randn((200, 150), generator=g, device="cuda").to(dtype)
+    x = torch.randn((3, 150), generator=g, device="cuda").to(dtype)
+    packed, scales = tt.tt_emb_q4_quantize(w, group)
+    clean = tt.tt_emb_q4_matvec(x, packed, scales, group)
+    bad = w.clone()
+    bad[5, 149], bad[6, 0], bad[7, 70] = -float("inf"), float("inf"), float("nan")
+    bad[8, 3], bad[8, 149] = float("inf"), -float("inf")
+    packed, scales = tt.tt_emb_q4_quantize(bad, group)
+    got = tt.tt_emb_q4_matvec(x, packed, scales, group)
+    inf = torch.full((3,), float("inf"), device="cuda")
+    assert torch.equal(got[:, 5], torch.copysign(inf, -x[:, 149].float())) and torch.equal(got[:, 6], torch.copysign(inf, x[:, 0].float()))
+    assert torch.isnan(got[:, 7]).all()
+    both = torch.copysign(inf, x[:, 3].float()) + torch.copysign(inf, -x[:, 149].float())
+    assert torch.equal(torch.isnan(got[:, 8]), torch.isnan(both)) and torch.equal(got[:, 8].nan_to_num(0, 1, -1), both.nan_to_num(0, 1, -1))
+    others = torch.ones(200, dtype=torch.bool, device="cuda")
+    others[5:9] = False
+    assert torch.equal(got[:, others], clean[:, others])
