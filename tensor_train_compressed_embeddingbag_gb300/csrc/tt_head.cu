@@ -784,7 +784,8 @@ bool run_gemm(const Operand& A, const Operand& B, GemmArgs a, int sms, int dev, 
 // Scores: 128-column tiles for fp32 (the ranges' sums stay in registers).
 template <int EPI>
 bool score_gemm(int bn, bool split, const Operand& A, const Operand& B, const GemmArgs& a, int sms, int dev, cudaStream_t st) {
-    if (split) return run_gemm<128, false, false, EPI, true>(A, B, a, sms, dev, st);
+    if constexpr (EPI != kEpiStatsLong)
+        if (split) return run_gemm<128, false, false, EPI, true>(A, B, a, sms, dev, st);
     if (bn == 128) return run_gemm<128, false, false, EPI, false>(A, B, a, sms, dev, st);
     return run_gemm<256, false, false, EPI, false>(A, B, a, sms, dev, st);
 }
@@ -1162,7 +1163,8 @@ tt_status head_forward(const Plan& p, const Target& t, float* loss, float* lse, 
         a.row_exp = row_exp;
         a.ctemp = kLog2e / t.T;
         a.part = w.part;
-        ok = score_gemm<kEpiStats>(p.bn_s, p.split, H, W, a, p.sms, p.device, st);
+        ok = !p.split && a.chunks > kLongChunks ? score_gemm<kEpiStatsLong>(p.bn_s, false, H, W, a, p.sms, p.device, st)
+                                                : score_gemm<kEpiStats>(p.bn_s, p.split, H, W, a, p.sms, p.device, st);
     }
     if (!ok) return TT_ERR_CUDA;
     if (distill && wide_rows(p, t.K))

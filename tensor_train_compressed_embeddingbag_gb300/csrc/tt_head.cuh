@@ -191,6 +191,14 @@ __device__ __forceinline__ void tm_read16(uint32_t taddr, float (&v)[16]) {
         : "r"(taddr)
         : "memory");
 }
+__device__ __forceinline__ void tm_read8(uint32_t taddr, float (&v)[8]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+        : "r"(taddr)
+        : "memory");
+}
 // Write 16 columns of this warp's 32 lanes (32 16-bit elements of an A operand's row);
 // tm_wait_st makes all such writes done.
 __device__ __forceinline__ void tm_st16(uint32_t taddr, const uint32_t (&w)[16]) {

@@ -11,7 +11,8 @@ constexpr int kGemmThreads = (4 + kEpiWarps) * 32;  // warp 0: TMA, 1: MMA, 2: t
 constexpr int kParts = kEpiWarps / 4;               // column parts of a tile, a warp per part and 32 rows
 constexpr int kBK = 64;            // K depth of a stage: one 128-byte swizzled row
 
-enum Epi { kEpiStats = 0, kEpiDz = 1, kEpiOut = 2 };
+enum Epi { kEpiStats = 0, kEpiDz = 1, kEpiOut = 2, kEpiStatsLong = 3 };  // the last: 16-bit types, more than kLongChunks of K
+constexpr int kLongChunks = 8;  // 512 of K; 1,024 takes the same time and has twice the error
 
 struct GemmArgs {
     int64_t M, N;      // valid rows and columns of the product
@@ -63,10 +64,16 @@ struct GemmShape {
 //
 // SPLIT (fp32 operands in two pieces).  The pieces of B lie one behind the other, so
 // A hi [B hi | B lo] is one MMA of twice the columns; A lo B hi adds to its second half,
-// which holds the small products.  The tensor core's fp32 accumulation cuts off the bits
-// below its accumulator instead of rounding them, so the error of a long sum grows with
-// its length and always in one direction.  An accumulator therefore holds kRange K chunks
-// only, and the epilogue adds the ranges up in registers, rounding to nearest.
+// which holds the small products.
+//
+// Ranges.  The tensor core's fp32 accumulation cuts off the bits below its accumulator
+// instead of rounding them, so the error of a long sum grows with its length and always in
+// one direction.  Where the result is fp32 (fp32 operands; scores of 16-bit ones, whose lse
+// is) an accumulator therefore holds kRange K chunks only, and the epilogue adds the ranges up in
+// registers, rounding to nearest.  For 16-bit scores that is no slower, as the epilogue lets an
+// accumulator go before its exponentials: bf16 4096 x 131072 x 2048 1186 us (1217 in one range),
+// 300 x 20000 x 4096 83 (88); the error of lse falls from 5.8e-7 to 1.4e-7 and from 1.3e-6 to
+// 1.5e-7.  dz and the gradients of 16-bit types are rounded to 16 bits, far above that.
 //
 // Bound by the tensor cores from some hundred rows and columns on (their pipe 78% busy in
 // the scores of 2048 x 16384 x 2048 bf16, 70 in dz, 73 in dhidden, 62 in dweight).  Measured,
@@ -81,7 +88,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 const __grid_constant__ GemmArgs a) {
     using S = GemmShape<BN, SPLIT>;
     static_assert(BN % (32 * kParts) == 0 && (!SPLIT || BN <= 128), "the ranges' sums stay in registers");
-    constexpr int kRange = 2;  // 128 of K
+    constexpr bool STATS = EPI == kEpiStats || EPI == kEpiStatsLong;
+    constexpr bool RANGES = SPLIT || EPI == kEpiStatsLong;
+    constexpr int kRange = SPLIT ? 2 : kLongChunks;  // SPLIT: 128 of K
     constexpr int kCh = BN / kParts / 32;  // 32-column chunks of a part
     extern __shared__ uint8_t raw[];
     __shared__ uint64_t full[S::kStages], empty[S::kStages], accfull[2], accempty[2], drain;
@@ -174,8 +183,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             int m, n0, n1, kb, ke, split;
             unit(u, m, n0, n1, kb, ke, split);
             for (int n = n0; ok && n < n1; ++n)
-                for (int r0 = kb; ok && r0 < ke; r0 = SPLIT ? (r0 / kRange + 1) * kRange : ke, ++acc) {
-                    const int steps = SPLIT ? min((r0 / kRange + 1) * kRange, ke) - r0 : ke - kb;
+                for (int r0 = kb; ok && r0 < ke; r0 = RANGES ? (r0 / kRange + 1) * kRange : ke, ++acc) {
+                    const int steps = RANGES ? min((r0 / kRange + 1) * kRange, ke) - r0 : ke - kb;
                     const uint32_t buf = acc & 1, d = tmem + buf * S::kAcc;
                     ok = head_wait(&accempty[buf], ((acc >> 1) & 1) ^ 1, a.wait_ns, gave_up);
                     if (!ok) break;
@@ -219,7 +228,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 const int64_t col0 = (int64_t)n * BN + part * (BN / kParts);
                 // 32 finished columns of this thread's row, the first of them `col`
                 auto finish = [&](float (&v)[32], int64_t col) {
-                    if (EPI == kEpiStats) {
+                    if (STATS) {
                         take_scores(v, a.N - col, c, run_m, run_s);
                     } else if (EPI == kEpiDz) {
                         if (col < a.dz_pitch && row - lane < a.M) {
@@ -274,6 +283,33 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     if (!ok) break;
 #pragma unroll
                     for (int ch = 0; ch < kCh; ++ch) finish(sum[ch], col0 + ch * 32);
+                } else if (RANGES) {
+                    float sum[kCh][32];
+#pragma unroll
+                    for (int ch = 0; ch < kCh; ++ch)
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) sum[ch][j] = 0.f;
+#pragma unroll 1
+                    for (int r0 = kb; ok && r0 < ke; r0 += kRange, ++acc) {
+                        const uint32_t buf = acc & 1;
+                        ok = head_wait(&accfull[buf], (acc >> 1) & 1, a.wait_ns, gave_up);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t t0 = tmem + buf * S::kAcc + ((uint32_t)(quad * 32) << 16) + part * (BN / kParts);
+#pragma unroll
+                        for (int h = 0; h < 4 * kCh; ++h) {
+                            float v[8];
+                            tm_read8(t0 + h * 8, v);
+#pragma unroll
+                            for (int j = 0; j < 8; j += 2) add2(sum[h / 4][(h & 3) * 8 + j], sum[h / 4][(h & 3) * 8 + j + 1], v[j], v[j + 1]);
+                        }
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&accempty[buf]);
+                    }
+                    if (!ok) break;
+#pragma unroll
+                    for (int ch = 0; ch < kCh; ++ch) finish(sum[ch], col0 + ch * 32);
                 } else {
                     const uint32_t buf = acc & 1;
                     ok = head_wait(&accfull[buf], (acc >> 1) & 1, a.wait_ns, gave_up);
@@ -305,7 +341,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     if (lane == 0) mbar_arrive(&accempty[buf]);
                 }
             }
-            if (EPI == kEpiStats && ok && in)
+            if (STATS && ok && in)
                 a.part[(row * a.nstrips + split) * kParts + part] = make_float2(run_m, run_s);
         }
     }

@@ -647,3 +647,24 @@ def test_no_rows_of_any_type(dtype, d):
         assert got["grad_weight"].shape == (50, d) and not got["grad_weight"].any()
     assert tt.vocab_cross_entropy(h, w, t).item() == 0 and tt.vocab_distillation(h, w, ids, logits).item() == 0
     assert tt.Q4Table(w, 32).scores(h).shape == (0, 50)
+
+
+# ---------------------------------------------------------------- long rows
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n,v,d", [(40, 700, 1100), (200, 2000, 4096), (40, 20000, 8192), (150, 3000, 20001)])
+def test_wide_scores_of_one_sign(n, v, d, dtype):
+    """All products positive, so every addition of a score's sum is cut the same way where the accumulator cuts: at most one
+    unit (2^-23) of the sum per 16 columns within 512 of them, then one rounding (2^-24) per 512.  fp32 operands: 3 x 2^-22."""
+    g = gen(41)
+    h = torch.rand((n, d), generator=g, device="cuda").to(dtype)
+    w = (torch.rand((v, d), generator=g, device="cuda") * (32.0 / d)).to(dtype)
+    t = torch.randint(0, v, (n,), generator=g, device="cuda")
+    _, lse = tt.tt_emb_xent_forward(h, w, t)
+    z = ref.scores(h, w)
+    want = torch.logsumexp(z, 1)
+    unit = (3 * 2.0 ** -22 if dtype == torch.float32 else 0.0) + 32 * 2.0 ** -23 + (d / 512 + 1) * 2.0 ** -24
+    bound = unit * z.amax(1) + 2.0 ** -21 * (1 + want)
+    off = (lse.double() - want).abs()
+    assert (off <= bound).all(), (off.max().item(), bound.min().item())
