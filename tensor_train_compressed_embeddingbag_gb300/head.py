@@ -339,8 +339,8 @@ def _reduce(loss, counts, reduction):
 
 
 def _same_rows(a, b):
-    """Shapes of the same rows in the same order: equal, or one of the two flattened."""
-    return a == b or (min(len(a), len(b)) == 1 and a.numel() == b.numel())
+    """Shapes of the same rows in the same order: equal, or one of the two flattened (or the one row's, without a batch)."""
+    return a == b or (min(len(a), len(b)) <= 1 and a.numel() == b.numel())
 
 
 def _check_reduction(reduction):
@@ -375,7 +375,7 @@ def vocab_distillation(hidden: torch.Tensor, weight: torch.Tensor, teacher_ids: 
     teacher_ids / teacher_logits [..., k]; negative ids are no entries.  reduction 'mean'
     divides by the rows that have an entry (0 when there are none).  err: as in vocab_cross_entropy."""
     _check_reduction(reduction)
-    if teacher_ids.dim() < 2 or not _same_rows(hidden.shape[:-1], teacher_ids.shape[:-1]) or teacher_logits.shape != teacher_ids.shape:
+    if teacher_ids.dim() < 1 or not _same_rows(hidden.shape[:-1], teacher_ids.shape[:-1]) or teacher_logits.shape != teacher_ids.shape:
         _refuse(TT_ERR_SHAPE, f"teacher_ids and teacher_logits have shapes {tuple(teacher_ids.shape)} and {tuple(teacher_logits.shape)}, "
                               f"expected {tuple(hidden.shape[:-1])} + [k]")
     k = teacher_ids.shape[-1]

@@ -156,3 +156,17 @@ def test_no_rows_need_no_workspace(lib, dtype):
         assert call() in (tt.TT_OK, tt.TT_ERR_CUDA)  # the latter without a GPU
     if dtype:
         assert forward(lib, head(dtype=dtype), ws=None) == tt.TT_ERR_ARG
+
+
+def test_losses_take_one_row_without_a_batch():
+    """Shapes that go on to the next check, which wants a GPU."""
+    import torch
+
+    h, w = torch.zeros(8), torch.zeros((5, 8))
+    for rows, t in ((h, torch.tensor(1)), (h, torch.tensor([1])), (h[None], torch.tensor(1))):
+        _refused(tt.TT_ERR_ARG, tt.vocab_cross_entropy, rows, w, t)
+    ids, logits = torch.zeros(3, dtype=torch.int64), torch.zeros(3)
+    for rows, i, x in ((h, ids, logits), (h, ids[None], logits[None]), (h[None], ids, logits)):
+        _refused(tt.TT_ERR_ARG, tt.vocab_distillation, rows, w, i, x)
+    _refused(tt.TT_ERR_SHAPE, tt.vocab_cross_entropy, h, w, torch.tensor([1, 2]))
+    _refused(tt.TT_ERR_SHAPE, tt.vocab_distillation, h, w, torch.tensor(1), torch.tensor(1.0))
