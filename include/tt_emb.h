@@ -391,6 +391,29 @@ tt_status tt_emb_forward_noalloc(int64_t num_embeddings, const int64_t p[3], con
  */
 typedef enum { TT_F32 = 0, TT_BF16 = 1, TT_F16 = 2 } tt_dtype;
 
+/*
+ * What the numbers keep.  Losses, lse, softmax statistics and sums are fp32.
+ *   bf16, f16  enter the products as they are.  Scores for the losses are summed over 512
+ *              columns in the tensor cores and beyond that with rounding; dz (below) is
+ *              rounded to the type before the gradient products, whose sums run over a piece
+ *              of the vocabulary (grad_hidden) or the rows (grad_weight) in the tensor cores,
+ *              which cut low bits off: the gradients' error is some 1.4 times that of
+ *              their own final rounding.
+ *   fp32       an operand enters with 22 bits, or to 2^-39 of the largest finite magnitude
+ *              under its scale where that is more: a hidden row (grad_weight: all that
+ *              count), 128 x 128 elements of the table (dim <= 64: 256 rows), an x row of
+ *              the 4-bit scores.  So one very large number (-1e9 in a column of biases) costs its
+ *              neighbours bits; -inf does not.
+ *   dz         fp32 and f16 are scaled by a power of two: grad_hidden keeps elements down to
+ *              2^-28 (f16) or, with 22 bits, 2^-16 (fp32; 2^-39 absolute) of the row's own
+ *              |grad_loss| T, rows down to 2^-100 of the heaviest; grad_weight loses what lies below
+ *              2^-39 of the batch's largest |grad_loss| T.
+ * Infinities are kept in every type: a table row that scores -inf drops out of lse and
+ * grad_weight, as by a column of biases that hidden holds a 1 for; grad_hidden's column of
+ * it is 0 times -inf, NaN, for rows that count.  An infinity times an infinity at one place is
+ * NaN in fp32.  A score of +inf, and NaN, make lse NaN.
+ */
+
 #define TT_HEAD_MAX_ROWS 16777216    /* rows N */
 #define TT_HEAD_MAX_VOCAB 1073741824 /* table rows V */
 #define TT_HEAD_MAX_DIM 65536        /* width D */
@@ -418,7 +441,8 @@ int64_t tt_emb_head_workspace(const tt_head* head, int32_t teacher_k, int32_t ba
 /*
  * Softmax cross entropy.
  *   targets_dev  int64 [rows]; a row whose target is ignore_index has loss 0 and
- *                gives no gradient, whatever its hidden row and grad_loss hold
+ *                gives no gradient (grad_hidden 0), whatever its hidden row and
+ *                grad_loss hold
  *   loss_dev     float [rows]: lse[n] - z[n][targets[n]]
  *   lse_dev      float [rows]: log sum_v exp(z[n][v]), of every row
  *   err_dev      int32 or NULL; the call ORs in 1 for a target that is neither
@@ -466,7 +490,7 @@ tt_status tt_emb_distill_backward(const tt_head* head, const int64_t* ids_dev, c
 /*
  * Bound, in nanoseconds, of each wait inside the head's kernels (for their own
  * copies and MMAs; default 2e9).  Process-wide, from the next call on; 0 makes a wait
- * that is not already over give up (a test of that path).  A wait that gives up sets
+ * that is not already over give up, those of other threads' calls too (a test of that path).  A wait that gives up sets
  * 4 in err_dev; the call then ends with undefined results and leaves nothing running.
  */
 tt_status tt_emb_head_set_wait_limit(uint64_t ns);
@@ -483,8 +507,9 @@ tt_status tt_emb_head_set_wait_limit(uint64_t ns);
  *   0.  A group with infinities gets an infinite scale and keeps only them (codes 7 and
  *   9), so they outweigh it; one with a NaN gets a scale of NaN.  weight_dev [vocab][dim] of `dtype` (tt_dtype), rows weight_stride apart.
  * tt_emb_q4_matvec: x_dev [rows][dim] of `dtype`, rows x_stride apart; out_dev float
- *   [rows][vocab], written whole.  Every product is exact and sums are fp32.  Meant for
- *   few rows: each 32 of them read the table once.
+ *   [rows][vocab], written whole.  Products with f16 and bf16 x are exact (bf16 values
+ *   below 2^-31 of the row's largest lose bits), fp32 x enters with 22 bits; sums are
+ *   fp32.  Meant for few rows: each 32 of them read the table once.
  * Both are asynchronous on `stream` and allocate nothing.  Return TT_ERR_ARG (null or
  * misaligned pointers, unknown type), TT_ERR_SHAPE (limits, group, stride), TT_ERR_CUDA.
  */

@@ -302,9 +302,9 @@ __global__ void __launch_bounds__(RT) k_head_finish(HeadIn in, Target t, const f
 // units, dz of its target entries under the batch's, and its packed copy.  A row that does
 // not count, and what fills up a tile of k_head_fused, is all ones with an lse that makes every
 // p 0: nothing that it holds, infinities and NaN included, reaches dweight, and a table row
-// that is scored -inf by a column of its own is so there too (zeros would make it NaN).  Entries of one row with the same id hold the same value, of their
-// summed q.  Target entries go to arrays [K][N] (ids, dzt) and, for k_head_fused, to their
-// 32 x 32 blocks.
+// that is scored -inf by a column of its own is so there too (zeros would make it NaN).
+// Entries of one row with the same id hold the same value, of their summed q.  Target
+// entries go to arrays [K][N] (ids, dzt) and, for k_head_fused, to their 32 x 32 blocks.
 struct RowsArgs {
     const float* lse;
     const float* grad;

@@ -29,8 +29,8 @@
 // here 256.
 //
 // Measured, us and TFLOP/s of its 2 N V D (kLse) or 4 N V D products (SPLIT: x 3):
-// bf16 4096 x 100003 x 128 dhidden 118 (1770), dweight 142 (1480); fp32 512 x 1,000,000 x
-// 64 lse 140 (1400), dhidden 236 (1670), dweight 256 (1540).  The tensor pipe is 60 to 70%
+// bf16 4096 x 100003 x 128 dhidden 119 (1760), dweight 142 (1480); fp32 512 x 1,000,000 x
+// 64 lse 148 (1330), dhidden 241 (1630), dweight 261 (1510).  The tensor pipe is 60 to 70%
 // busy and what bounds them; the rest is fill and drain of the tiles' way above.
 #pragma once
 

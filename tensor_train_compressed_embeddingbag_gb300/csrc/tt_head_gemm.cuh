@@ -75,11 +75,11 @@ struct GemmShape {
 // 300 x 20000 x 4096 83 (88); the error of lse falls from 5.8e-7 to 1.4e-7 and from 1.3e-6 to
 // 1.5e-7.  dz and the gradients of 16-bit types are rounded to 16 bits, far above that.
 //
-// Bound by the tensor cores from some hundred rows and columns on (their pipe 78% busy in
-// the scores of 2048 x 16384 x 2048 bf16, 70 in dz, 73 in dhidden, 62 in dweight).  Measured,
-// bf16 4096 x 131072 x 2048, 2.2 TFLOP a product: scores 1187 us (1850 TFLOP/s), dz 1305
-// (1680), dhidden 1387 (1585), dweight 1425 (1540); f16 2047 x 50001 x 1024 scores 122 us
-// (1720); fp32 283 x 37955 x 1451 scores 91 us (340, three products each).  With few
+// Bound by the tensor cores from some hundred rows and columns on (their pipe 79% busy in
+// the scores of 2048 x 16384 x 2048 bf16, 71 in dz, 75 in dhidden, 64 in dweight).  Measured
+// within whole steps, bf16 4096 x 131072 x 2048, 2.2 TFLOP a product: scores 1215 us (1810
+// TFLOP/s), dz 1367 (1610), dhidden 1446 (1520), dweight 1486 (1480); f16 2047 x 50001 x 1024
+// scores 126 us (1660); fp32 283 x 37955 x 1451 scores 91 us (340, three products each).  With few
 // hidden rows it is a stream: bf16 8 x 200000 x 1024 reads the table for dhidden at 5.4 TB/s
 // (76 us) and writes dweight at 5.3 (78 us).
 template <int BN, bool AMN, bool BMN, int EPI, bool SPLIT>

@@ -9,14 +9,16 @@
 // the table is its floor.  What the kernel does per weight has to fit beside the loads:
 // codes become f16 two at a time (an OR puts two codes into the mantissas of 1024 or, at
 // the next higher nibble, of 1024 in steps of 16; one packed operation leaves code - 8,
-// exactly), and the products run on the warp-level tensor cores (mma.sync.m16n8k16: 16
-// table rows x 8 rows of x), fp32 accumulation per group, one fp32 multiply-add by the
-// group's scale into the running sum.
+// exactly: the conversion of Y. J. Kim et al., "Who Says Elephants Can't Run: Bringing Large
+// Scale MoE Models into Cloud Scale Production", 2022), and the products run on the
+// warp-level tensor cores (mma.sync.m16n8k16: 16 table rows x 8 rows of x), fp32
+// accumulation per group, one fp32 multiply-add by the group's scale into the running sum.
 //
 // x in f16: f16 rows as they are; bf16 and fp32 rows times a power of two that puts the
 // row's largest magnitude near 2^14.  A bf16 value is then an f16 value (its 8 bits fit;
 // values below 2^-31 of the row's largest lose bits, by at most 2^-39 of it), an fp32
-// value the sum of two (hi + lo, 22 bits), one MMA each.  So every product is exact.
+// value the sum of two (hi + lo, 22 bits), one MMA each.  So the products of what x enters
+// as are exact.
 //
 // The order of k inside a group is free as long as both operands use the same: a thread's
 // share of a group is one contiguous load of group / 8 bytes per table row, and x lies in
@@ -26,7 +28,9 @@
 // Measured: 1 x 131072 x 4096, groups of 128, bf16 x: 277 MB in 63 us (4.4 TB/s; floor 41);
 // 8 x 1,000,000 x 64, groups of 32, fp32 x: 68 MB in 19.7 us (floor 10).  The ALU that
 // turns codes into f16 is 46 and 48% busy, half of all issue slots go, and a warp waits
-// mostly on its own last instruction: both bounds are near, neither is reached.  Codes as
+// mostly on its own last instruction: neither bound is reached.  The table's bytes go to
+// registers (118 to 125 a thread at 16 warps to an SM), which holds how many are in flight;
+// copies to shared memory, which hold none, are not tried.  Codes as
 // f16 subnormals would spare the OR, but lose the scale's low bits.
 #include <type_traits>
 

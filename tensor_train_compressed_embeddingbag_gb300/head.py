@@ -12,8 +12,10 @@ dense table: an output projection, or the rows of a TT table themselves (a
   vocab_cross_entropy, vocab_distillation, Q4Table   the same for autograd and as
                                          an object
 
-Low-level functions carry the C ABI's names (``include/tt_emb.h``); outputs and the
-workspace are torch allocations on the call's stream.
+Low-level functions carry the C ABI's names (``include/tt_emb.h``, which also says what
+each type's numbers keep); outputs and the workspace are torch allocations on the call's
+stream, and so are copies of arguments whose rows are not contiguous.  Both gradients are
+always formed, whichever are wanted.
 """
 from __future__ import annotations
 
