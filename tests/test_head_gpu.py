@@ -668,3 +668,52 @@ def test_wide_scores_of_one_sign(n, v, d, dtype):
     bound = unit * z.amax(1) + 2.0 ** -21 * (1 + want)
     off = (lse.double() - want).abs()
     assert (off <= bound).all(), (off.max().item(), bound.min().item())
+
+
+@pytest.mark.parametrize("dtype,v,d", [(torch.float32, 35_000_000, 64), (torch.float16, 35_000_000, 64), (torch.bfloat16, 17_000_000, 136)])
+def test_gradients_past_32_bit_offsets(dtype, v, d):
+    """Both gradients of tables with more than 2^31 elements: dhidden whole, dweight at both ends, around 2^31 elements
+    and at the targets."""
+    n = 20
+    w = torch.empty((v, d), dtype=dtype, device="cuda")
+    w.normal_(0, 0.05, generator=gen(42))
+    h = torch.randn((n, d), generator=gen(43), device="cuda").to(dtype)
+    w[-n:] = h
+    t = torch.arange(v - n, v, device="cuda")
+    t[:5] = torch.tensor([0, 1, (1 << 31) // d, (1 << 31) // d + 1, v // 2], device="cuda")
+    grad = torch.rand((n,), generator=gen(44), device="cuda") + 0.5
+    _, lse = tt.tt_emb_xent_forward(h, w, t)
+    gh, gw = tt.tt_emb_xent_backward(h, w, t, lse, grad)
+    step = 1 << 21
+    z = torch.full((n,), -float("inf"), dtype=torch.float64, device="cuda")
+    a = torch.zeros_like(z)
+    for r in range(0, v, step):
+        part = w[r:r + step].double()
+        z = torch.logaddexp(z, torch.logsumexp(h.double() @ part.t(), 1))
+        a = torch.maximum(a, (h.double().abs() @ part.abs().t()).amax(1))
+    ez = (2.0 ** -20 + d * 2.0 ** -27) * a
+    el = ez + 2.0 ** -21 * (1 + z.abs())
+    assert ((lse.double() - z).abs() <= el).all()
+    u, g = ref.U[dtype], grad.double()[:, None]
+    want, size, off = (torch.zeros((n, d), dtype=torch.float64, device="cuda") for _ in range(3))
+
+    def dz_of(rows):  # dz of some table rows, how far it may be off
+        p = torch.exp(h.double() @ w[rows].double().t() - z[:, None])
+        q = (t[:, None] == rows[None]).double()
+        dz = g * (p - q)
+        return dz, g * (p * 2 * (ez + el)[:, None] + q * 2.0 ** -20) + (u if u else 2.0 ** -21) * dz.abs() + 2.0 ** -38 * g.max()
+    for r in range(0, v, step):
+        rows = torch.arange(r, min(v, r + step), device="cuda")
+        dz, e = dz_of(rows)
+        part = w[rows].double()
+        want += dz @ part
+        size += dz.abs() @ part.abs()
+        off += e @ part.abs()
+    bound = off + (3 * 2.0 ** -22 + v * 2.0 ** -27) * size + (u + 2.0 ** -23) * want.abs() + 2.0 ** -25
+    assert ((gh.double() - want).abs() <= bound).all()
+    edge = (1 << 31) // d
+    rows = torch.cat([torch.arange(0, 200, device="cuda"), torch.arange(edge - 200, edge + 200, device="cuda"), t, torch.arange(v - 200, v, device="cuda")])
+    dz, e = dz_of(rows)
+    want = dz.t() @ h.double()
+    bound = e.t() @ h.double().abs() + (3 * 2.0 ** -22 + n * 2.0 ** -27) * (dz.abs().t() @ h.double().abs()) + (u + 2.0 ** -23) * want.abs() + 2.0 ** -25
+    assert ((gw[rows].double() - want).abs() <= bound).all()
