@@ -178,7 +178,7 @@ def _plain_preference(s):
     else:
         u = (h - 0.5) / BETA
         loss, slope = u * u, 2.0 * u / BETA
-    out = {"loss": loss.float(), "rewards": rewards.float(), "counts": counts.to(torch.int32)}
+    out = {"loss": loss.float(), "margins": h.float(), "rewards": rewards.float(), "counts": counts.to(torch.int32)}
     if s["train"]:
         c = s["grad"] * slope * BETA
         each = q.spread((torch.cat([c, -c]) * share).float())
@@ -241,10 +241,10 @@ def run(state):
         return {"scores": tt.tt_emb_q8_scores(s["x"], s["codes"], s["scales"])}
     if s["op"] == "preference":
         how = dict(mask=s["mask"], offsets=s["offsets"], beta=BETA, kind=s["kind"], label_smoothing=s["smoothing"], average=s["average"])
-        loss, rewards, counts = tt.tt_emb_preference_forward(s["logp"], s["reference"], **how)
-        out = {"loss": loss, "rewards": rewards, "counts": counts}
+        loss, margins, rewards, counts = tt.tt_emb_preference_forward(s["logp"], s["reference"], **how)
+        out = {"loss": loss, "margins": margins, "rewards": rewards, "counts": counts}
         if s["train"]:
-            out["grad"] = tt.tt_emb_preference_backward(s["logp"], rewards, counts, s["grad"], **how)
+            out["grad"] = tt.tt_emb_preference_backward(s["logp"], margins, counts, s["grad"], **how)
         return out
     how = dict(reference=s["reference"], mask=s["mask"], offsets=s["offsets"], clip=CLIP, kl=s["kl"], kl_weight=s["kl_weight"], level=s["level"],
                average=s["average"])
@@ -267,7 +267,7 @@ def work(case):
         return {"bytes": m * d * _BYTES[case["type"]] + v * d + 4 * v + 4 * m * v, "flops": 2.0 * m * v * d}
     n = case["tokens"]
     if case["op"] == "preference":
-        return {"bytes": 9 * n + 44 * case["pairs"] + (4 * n if case["train"] else 0), "flops": 3.0 * n}
+        return {"bytes": 9 * n + 48 * case["pairs"] + (4 * n if case["train"] else 0), "flops": 3.0 * n}
     per_token = (17 if case["per_token"] else 13) * n
     return {"bytes": per_token + 32 * case["sequences"] + (4 * n if case["train"] else 0), "flops": 30.0 * n}
 
@@ -312,7 +312,7 @@ def exact(case, seed):
             loss = -(1 - e) * torch.nn.functional.logsigmoid(h) - e * torch.nn.functional.logsigmoid(-h)
         else:
             loss = torch.relu(1 - h) if case["kind"] == "hinge" else ((h - 0.5) / BETA) ** 2
-        out = {"loss": loss.detach(), "rewards": rewards.detach(), "counts": counts.to(torch.int32)}
+        out = {"loss": loss.detach(), "margins": h.detach(), "rewards": rewards.detach(), "counts": counts.to(torch.int32)}
     else:
         delta = logp - s["old"].reshape(-1).double()
         log_ratio = total(delta) / counts.clamp(min=1).double()
