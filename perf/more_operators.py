@@ -247,7 +247,7 @@ def run(state):
             out["grad"] = tt.tt_emb_preference_backward(s["logp"], margins, counts, s["grad"], **how)
         return out
     how = dict(reference=s["reference"], mask=s["mask"], offsets=s["offsets"], clip=CLIP, kl=s["kl"], kl_weight=s["kl_weight"], level=s["level"],
-               average=s["average"])
+               average=s["average"], per_token=s["per_token"])
     loss, kl, log_ratio, counts, clipped = tt.tt_emb_policy_forward(s["logp"], s["old"], s["advantages"], **how)
     out = {"loss": loss, "kl": kl, "log_ratio": log_ratio, "counts": counts, "clipped": clipped}
     if s["train"]:
