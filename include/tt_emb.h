@@ -521,6 +521,168 @@ tt_status tt_emb_q4_matvec(const void* x_dev, int64_t x_stride, int32_t rows, in
                            const uint8_t* packed_dev, const uint16_t* scales_dev, int64_t vocab, int32_t dim,
                            int32_t group, float* out_dev, tt_stream stream);
 
+/*
+ * Rows of a dense table by id, times a scale, and the table's gradient:
+ *     out[n][d] = scale weight[ids[n]][d]
+ *     grad_weight[v][d] = scale sum of grad_out[n][d] over the n with ids[n] = v != padding_idx
+ * The table is the kind that the vocabulary head scores (a tied table has both).  These
+ * calls need no handle; every buffer is the caller's, every call is asynchronous on
+ * `stream` and allocates nothing (so it may be captured in a CUDA graph).
+ *   ids_dev      int64 [rows].  An id outside [0, vocab) gives a row of zeros, no gradient,
+ *                and 1 in err_dev (int32 or NULL; the caller clears it)
+ *   padding_idx  rows with this id give no gradient (forward: like any other); -1: none
+ *   out          [rows][dim] of the table's type, rows out_stride elements apart; a product
+ *                by the fp32 scale, rounded once
+ *   grad_weight  [vocab][dim] of the table's type, rows grad_weight_stride apart.  accumulate
+ *                0: every row written (rows that no id names with zeros).  1: added to the rows that
+ *                are named, others neither read nor written: the gradient of a tied table, or,
+ *                with the table itself and scale = -(learning rate) scale, its step of gradient
+ *                descent.  Sums are fp32, rounded once, taken in an order that is fixed by
+ *                the ids: results repeat bit for bit.
+ * tt_emb_lookup_workspace: bytes of 256-byte aligned workspace that the backward call needs;
+ * it holds nothing between calls.  -1 for sizes that the calls refuse.
+ * Return TT_ERR_ARG (null or misaligned pointers, unknown type, short workspace),
+ * TT_ERR_SHAPE (limits, stride < dim), TT_ERR_CUDA.
+ */
+#define TT_LOOKUP_MAX_ROWS 134217728 /* rows of a call; table rows and width as for the head */
+
+typedef struct {
+    const void* weight_dev; /* [vocab][dim], rows weight_stride elements apart; the backward call takes NULL */
+    int64_t weight_stride;
+    const int64_t* ids_dev;
+    int64_t rows, vocab;
+    int64_t padding_idx;
+    int32_t dim;
+    int32_t dtype; /* tt_dtype of weight, out and their gradients */
+    float scale;
+} tt_lookup;
+
+int64_t tt_emb_lookup_workspace(int64_t rows, int64_t vocab, int32_t dim, int32_t dtype);
+tt_status tt_emb_lookup_forward(const tt_lookup* lookup, void* out_dev, int64_t out_stride, int32_t* err_dev,
+                                tt_stream stream);
+tt_status tt_emb_lookup_backward(const tt_lookup* lookup, const void* grad_out_dev, int64_t grad_out_stride,
+                                 void* grad_weight_dev, int64_t grad_weight_stride, int32_t accumulate,
+                                 int32_t* err_dev, void* ws_dev, size_t ws_bytes, tt_stream stream);
+
+/*
+ * Losses of answers (sequences of sampled tokens) from the log probabilities of their tokens,
+ * as the head gives them (minus its cross entropy), and the gradient of each of these.
+ * Tokens lie one behind the other; sequence s holds offsets[s] .. offsets[s + 1] - 1, or, without
+ * offsets, tokens / sequences tokens each (a padded batch).  A token whose mask is 0 does not
+ * count, whatever its numbers are.  m[t] is 1 for a token that counts, n[s] how many do.
+ * share[s] = 1 / n[s] if `average`, else 1 (a sequence without a token that counts: 0 for
+ * every sum).  Sums over tokens are taken in double.  Both need a workspace (256-byte aligned,
+ * nothing kept between calls) of tt_emb_answers_workspace bytes (-1: refused sizes) forward.
+ *
+ * Preference.  Sequences 0 .. P - 1 are chosen over sequences P .. 2 P - 1, pair by pair:
+ *   rewards[s] = beta share[s] sum_t m[t] (logp[t] - reference[t])     (no reference: 0)
+ *   margins[p] = h = rewards[p] - rewards[P + p] - margin
+ *   loss[p] = -(1 - smoothing) log sigma(h) - smoothing log sigma(-h)  TT_PREF_SIGMOID
+ *             max(0, 1 - h)                                            TT_PREF_HINGE
+ *             ((h - 1/2) / beta)^2                                     TT_PREF_SQUARED
+ *   (R. Rafailov et al., "Direct Preference Optimization", 2023; M. G. Azar et al., "A General
+ *   Theoretical Paradigm to Understand Learning from Human Preferences", 2023.)
+ *   Backward: grad_logp[t] = +-grad_loss[p] dloss/dh beta share[s] m[t]; reads margins and counts
+ *   of the forward call, and of the tokens only the mask.
+ *
+ * Policy.  With d[t] = logp[t] - old[t], log_ratio[s] the mean of d over the tokens of s that count,
+ * x[t] = log_ratio[s] (TT_POLICY_SEQUENCE) or d[t] (TT_POLICY_TOKEN), r = exp(x), advantage A
+ * of the token or of its sequence:
+ *   L[t] = -min(r A, clip(r, 1 - clip_low, 1 + clip_high) A), and at most -dual_clip A where A < 0
+ *          and dual_clip > 0
+ *   k[t] with y = reference[t] - logp[t]:  -y (TT_KL_1), y^2 / 2 (TT_KL_2), exp(y) - 1 - y (TT_KL_3)
+ *   kl[s] = share[s] sum_t m[t] k[t],  loss[s] = share[s] sum_t m[t] L[t] + kl_weight kl[s]
+ *   clipped[s]: how many tokens that count have a ratio beyond the bound that holds for the
+ *   sign of their A.  Whether it is is decided on x itself (d is not rounded for that).
+ *   No reference: k = 0.  TT_POLICY_SEQUENCE takes an advantage per sequence.
+ *   (J. Schulman et al., "Proximal Policy Optimization Algorithms", 2017; D. Ye et al., "Mastering
+ *   Complex Control in MOBA Games with Deep Reinforcement Learning", 2020: dual_clip; C. Zheng et al.,
+ *   "Group Sequence Policy Optimization", 2025.)
+ *   Backward: grad_logp[t] = grad_loss[s] share[s] m[t] (-A r [not clipped] + kl_weight dk/dlogp); reads
+ *   log_ratio and counts of the forward call.  old, reference and advantages get no gradient.
+ *
+ * grad_logp is written whole (0 for tokens that do not count or lie behind the last
+ * sequence).  err_dev (int32 or NULL; the caller clears it): 2 for offsets that do not begin
+ * with 0, decrease, pass `tokens` or hold 2^31 tokens or more in one sequence (results undefined; no access outside the buffers).
+ * Return TT_ERR_ARG (null or misaligned pointers, unknown kinds, numbers outside their ranges, short
+ * workspace), TT_ERR_SHAPE (limits; no offsets and tokens no multiple of sequences), TT_ERR_CUDA.
+ */
+#define TT_ANSWERS_MAX_TOKENS 1099511627776 /* 2^40 */
+#define TT_ANSWERS_MAX_SEQUENCES 16777216
+
+typedef enum { TT_PREF_SIGMOID = 0, TT_PREF_HINGE = 1, TT_PREF_SQUARED = 2 } tt_pref_kind;
+typedef enum { TT_POLICY_TOKEN = 0, TT_POLICY_SEQUENCE = 1 } tt_policy_level;
+typedef enum { TT_KL_1 = 1, TT_KL_2 = 2, TT_KL_3 = 3 } tt_kl_kind;
+
+typedef struct {
+    const float* logp_dev;      /* [tokens]; the preference's backward call takes NULL */
+    const float* reference_dev; /* [tokens] or NULL */
+    const uint8_t* mask_dev;    /* [tokens], 0 or 1, or NULL: every token counts */
+    const int64_t* offsets_dev; /* [sequences + 1] or NULL */
+    int64_t tokens, sequences;
+    int32_t average;
+} tt_answers;
+
+typedef struct {
+    int32_t kind;           /* tt_pref_kind */
+    double beta;            /* > 0 */
+    double label_smoothing; /* in [0, 1); TT_PREF_SIGMOID only, else 0 */
+    double margin;
+} tt_preference;
+
+typedef struct {
+    const float* old_dev;        /* [tokens] */
+    const float* advantages_dev; /* [tokens] if per_token, else [sequences] */
+    int32_t per_token;
+    int32_t level;     /* tt_policy_level */
+    int32_t kl;        /* tt_kl_kind */
+    double clip_low;   /* in [0, 1) */
+    double clip_high;  /* >= 0 */
+    double dual_clip;  /* 0 (none) or > 1 */
+    double kl_weight;  /* >= 0 */
+} tt_policy;
+
+int64_t tt_emb_answers_workspace(int64_t tokens, int64_t sequences);
+tt_status tt_emb_preference_forward(const tt_answers* answers, const tt_preference* how, float* loss_dev,
+                                    float* margins_dev, float* rewards_dev, int32_t* counts_dev,
+                                    int32_t* err_dev, void* ws_dev, size_t ws_bytes, tt_stream stream);
+tt_status tt_emb_preference_backward(const tt_answers* answers, const tt_preference* how,
+                                     const float* margins_dev, const int32_t* counts_dev,
+                                     const float* grad_loss_dev, float* grad_logp_dev, tt_stream stream);
+tt_status tt_emb_policy_forward(const tt_answers* answers, const tt_policy* how, float* loss_dev, float* kl_dev,
+                                float* log_ratio_dev, int32_t* counts_dev, int32_t* clipped_dev,
+                                int32_t* err_dev, void* ws_dev, size_t ws_bytes, tt_stream stream);
+tt_status tt_emb_policy_backward(const tt_answers* answers, const tt_policy* how, const float* log_ratio_dev,
+                                 const int32_t* counts_dev, const float* grad_loss_dev, float* grad_logp_dev,
+                                 tt_stream stream);
+
+/*
+ * Scores against a table held in 8-bit integers (serving, evaluation):
+ *   out[m][v] = xscale[m] scale[v] sum_d xcode[m][d] code[v][d]
+ * with a scale for each row of x and each row of the table.  codes_dev: int8 [vocab][pitch], pitch =
+ * ceil(dim / 16) * 16, 16-byte aligned; what padding columns hold does not matter.
+ *
+ * tt_emb_q8_quantize, of the rows of any matrix: scale = max |w| / 127 (fp32 division), code =
+ *   127 w / max |w| rounded to nearest, ties to even, as if the quotient were exact; a row of
+ *   zeros gets scale 0.  A row with infinities gets an infinite scale and keeps only them (codes 1
+ *   and -1); one with a NaN gets a scale of NaN and codes 0.  Padding columns get 0.
+ * tt_emb_q8_scores quantizes the rows of x in the same way, into its workspace, and multiplies.  The integer
+ *   sums are exact; each is rounded once to fp32 and multiplied by the product of the two
+ *   scales.  x_dev [rows][dim] of `dtype`, rows x_stride apart; out_dev float [rows][vocab], written whole.
+ *   err_dev (int32 or NULL; the caller clears it): 4 for a device wait that gave up (results
+ *   undefined; the bound is that of tt_emb_head_set_wait_limit).
+ * tt_emb_q8_workspace: bytes of the 256-byte aligned workspace that the scores need; it holds nothing between
+ * calls.  -1 for refused sizes.  All are asynchronous on `stream` and allocate nothing.  Return TT_ERR_ARG (null or
+ * misaligned pointers, unknown type, short workspace), TT_ERR_SHAPE (limits, stride), TT_ERR_CUDA.
+ */
+#define TT_Q8_MAX_ROWS 16777216
+int64_t tt_emb_q8_workspace(int64_t rows, int32_t dim);
+tt_status tt_emb_q8_quantize(const void* weight_dev, int64_t weight_stride, int64_t rows, int32_t dim,
+                             int32_t dtype, int8_t* codes_dev, float* scales_dev, tt_stream stream);
+tt_status tt_emb_q8_scores(const void* x_dev, int64_t x_stride, int64_t rows, int32_t dtype,
+                           const int8_t* codes_dev, const float* scales_dev, int64_t vocab, int32_t dim,
+                           float* out_dev, int32_t* err_dev, void* ws_dev, size_t ws_bytes, tt_stream stream);
+
 /* Static description of a status code; never NULL. */
 const char* tt_emb_status_string(tt_status s);
 

@@ -79,9 +79,24 @@ __all__ = [
     "tt_emb_head_set_wait_limit",
     "tt_emb_q4_quantize",
     "tt_emb_q4_matvec",
+    "tt_emb_lookup_workspace",
+    "tt_emb_lookup_forward",
+    "tt_emb_lookup_backward",
+    "tt_emb_answers_workspace",
+    "tt_emb_preference_forward",
+    "tt_emb_preference_backward",
+    "tt_emb_policy_forward",
+    "tt_emb_policy_backward",
+    "tt_emb_q8_workspace",
+    "tt_emb_q8_quantize",
+    "tt_emb_q8_scores",
     "vocab_cross_entropy",
     "vocab_distillation",
     "Q4Table",
+    "vocab_embedding",
+    "preference_loss",
+    "policy_loss",
+    "Q8Table",
 ]
 
 TT_OK, TT_ERR_ARG, TT_ERR_SHAPE, TT_ERR_INDEX, TT_ERR_CUDA, TT_ERR_STATE, TT_ERR_TIMEOUT, TT_ERR_NOMEM, TT_ERR_BOUNDS = range(9)
@@ -124,6 +139,17 @@ EXPORTED_SYMBOLS = (
     "tt_emb_head_set_wait_limit",
     "tt_emb_q4_quantize",
     "tt_emb_q4_matvec",
+    "tt_emb_lookup_workspace",
+    "tt_emb_lookup_forward",
+    "tt_emb_lookup_backward",
+    "tt_emb_answers_workspace",
+    "tt_emb_preference_forward",
+    "tt_emb_preference_backward",
+    "tt_emb_policy_forward",
+    "tt_emb_policy_backward",
+    "tt_emb_q8_workspace",
+    "tt_emb_q8_quantize",
+    "tt_emb_q8_scores",
 )
 
 
@@ -207,6 +233,17 @@ def load_library():
             "tt_emb_head_set_wait_limit": (ctypes.c_int, [ctypes.c_uint64]),
             "tt_emb_q4_quantize": (ctypes.c_int, [vp, i64, i64, i32, i32, i32, vp, vp, vp]),
             "tt_emb_q4_matvec": (ctypes.c_int, [vp, i64, i32, i32, vp, vp, i64, i32, i32, vp, vp]),
+            "tt_emb_lookup_workspace": (i64, [i64, i64, i32, i32]),
+            "tt_emb_lookup_forward": (ctypes.c_int, [vp, vp, i64, vp, vp]),
+            "tt_emb_lookup_backward": (ctypes.c_int, [vp, vp, i64, vp, i64, i32, vp, vp, ctypes.c_size_t, vp]),
+            "tt_emb_answers_workspace": (i64, [i64, i64]),
+            "tt_emb_preference_forward": (ctypes.c_int, [vp, vp, vp, vp, vp, vp, vp, vp, ctypes.c_size_t, vp]),
+            "tt_emb_preference_backward": (ctypes.c_int, [vp, vp, vp, vp, vp, vp, vp]),
+            "tt_emb_policy_forward": (ctypes.c_int, [vp, vp, vp, vp, vp, vp, vp, vp, vp, ctypes.c_size_t, vp]),
+            "tt_emb_policy_backward": (ctypes.c_int, [vp, vp, vp, vp, vp, vp, vp]),
+            "tt_emb_q8_workspace": (i64, [i64, i32]),
+            "tt_emb_q8_quantize": (ctypes.c_int, [vp, i64, i64, i32, i32, vp, vp, vp]),
+            "tt_emb_q8_scores": (ctypes.c_int, [vp, i64, i64, i32, vp, vp, i64, i32, vp, vp, vp, ctypes.c_size_t, vp]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)
@@ -826,3 +863,17 @@ from .head import (  # noqa: E402  (uses the names above)
     vocab_cross_entropy,
     vocab_distillation,
 )
+
+# ---------------------------------------------------------------- around the head: lookups, answers, 8-bit scores
+
+from .answers import (  # noqa: E402
+    policy_loss,
+    preference_loss,
+    tt_emb_answers_workspace,
+    tt_emb_policy_backward,
+    tt_emb_policy_forward,
+    tt_emb_preference_backward,
+    tt_emb_preference_forward,
+)
+from .lookup import tt_emb_lookup_backward, tt_emb_lookup_forward, tt_emb_lookup_workspace, vocab_embedding  # noqa: E402
+from .q8 import Q8Table, tt_emb_q8_quantize, tt_emb_q8_scores, tt_emb_q8_workspace  # noqa: E402

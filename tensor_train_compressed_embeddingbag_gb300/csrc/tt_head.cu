@@ -707,26 +707,12 @@ __global__ void __launch_bounds__(256) k_head_reduce(const float* partial, int s
 // ---------------------------------------------------------------- host
 
 namespace {
-
 std::atomic<uint64_t> g_head_wait_ns{kHeadWaitNs};  // of the process: calls of other threads read it meanwhile
+}  // namespace
 
-typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
-                                const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+uint64_t head_wait_limit() { return g_head_wait_ns.load(std::memory_order_relaxed); }
 
-EncodeTiled encode_tiled() {
-    static EncodeTiled fn = [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult r;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r) != cudaSuccess ||
-            r != cudaDriverEntryPointSuccess) {
-            cudaGetLastError();
-            p = nullptr;
-        }
-        return reinterpret_cast<EncodeTiled>(p);
-    }();
-    return fn;
-}
+namespace {
 
 // A [pieces][rows][cols] array of 16-bit elements, rows `pitch` elements apart, read
 // in boxes of 64 columns x box_rows rows; elements outside read as 0.
@@ -774,7 +760,7 @@ bool run_gemm(const Operand& A, const Operand& B, GemmArgs a, int sms, int dev, 
     a.ntiles = (int)cdiv(a.N, BN);
     a.nstrips = (int)cdiv(a.ntiles, a.strip);
     a.units = EPI == kEpiOut ? (int64_t)a.mtiles * a.ntiles * a.splits : (int64_t)a.mtiles * a.nstrips;
-    a.wait_ns = g_head_wait_ns.load(std::memory_order_relaxed);
+    a.wait_ns = head_wait_limit();
     auto k = k_head_gemm<BN, AMN, BMN, EPI, SPLIT>;
     if (!allow_smem<KernelTag<BN, AMN, BMN, EPI, SPLIT>>(k, dev, GemmShape<BN, SPLIT>::kSmem)) return false;
     k<<<(unsigned)(a.units < sms ? a.units : sms), kGemmThreads, GemmShape<BN, SPLIT>::kSmem, st>>>(ma, mb, a);
@@ -803,7 +789,7 @@ bool run_fused(const Operand& X, const Operand& Y, FusedArgs a, int dev, cudaStr
     CUtensorMap mx, my;
     if (!make_map(&mx, X.p, a.fmt, X.cols, X.rows, S::PC, X.pitch, X.piece, 128)) return false;
     if (!make_map(&my, Y.p, a.fmt, Y.cols, Y.rows, S::PC, Y.pitch, Y.piece, S::BY)) return false;
-    a.wait_ns = g_head_wait_ns.load(std::memory_order_relaxed);
+    a.wait_ns = head_wait_limit();
     auto k = k_head_fused<DT, SPLIT, MODE>;
     if (!allow_smem<KernelTag<DT, SPLIT, MODE, 0, -1>>(k, dev, S::kSmem)) return false;
     k<<<(unsigned)a.runs.blocks, S::kThreads, S::kSmem, st>>>(mx, my, a);

@@ -1,0 +1,821 @@
+// tt_lookup.cu -- rows of a dense table by id, times a scale, and the table's gradient.
+//
+// Forward: a copy with a multiplication, 8 bytes of id and 2 D elements of traffic a row.
+//
+// Backward: dweight[v] = scale * sum of the rows of grad_out whose id is v.  The dense gradient
+// is written whole, so N D elements are read and V D written.  Positions are sorted by
+// id (stable, so that a row's sum has one order), and the sorted positions are cut into
+// chunks of R: the threads of a chunk, one 16-byte unit of columns each, add up its rows in
+// fp32 registers, eight loads in flight whatever the ids are, and write a row where
+// the id changes.  Chunks are equal work however popular an id is; what an id has in several
+// chunks goes through fp32 partial sums, joined in order.  Rows that no id names are written
+// with zeros by blocks that find their range of the sorted ids by bisection.
+//
+// The sort is a radix sort by counting (digits of up to 11 bits): per chunk of kSortChunk
+// positions a histogram, scanned over the chunks of a digit by a warp, and a scatter by ranks
+// within the chunk (match masks per warp).  The scatter counts the next digit's histogram.
+//
+// Few lookups are not sorted: a block per lookup and column slice looks through all ids,
+// leaves if an earlier lookup has the same, and else sums those that have it: one launch.
+#include <algorithm>
+#include <type_traits>
+
+#include "tt_head.cuh"
+
+namespace ttemb {
+
+constexpr int kLkThreads = 256;
+constexpr int kLkRows = 4;             // rows of a thread in the forward pass
+constexpr int kSmallRows = 1024;       // lookups that are not sorted
+constexpr int kSortChunk = 2048;
+constexpr int kSortBlock = 256;
+constexpr int kSortW = kSortBlock / 32;
+constexpr int kDigitBits = 11;
+constexpr int kMaxPasses = 3;
+constexpr int kZeroRows = 2048;        // most table rows of a block that writes zeros
+constexpr int kChunkSlots = 4096;      // sorted positions staged by a block
+constexpr int kInFlight = 8;
+
+template <class T, int VEC>
+__device__ __forceinline__ void unpack_unit(const uint4& u, float (&v)[VEC]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (sizeof(T) == 4) {
+            v[i] = __uint_as_float(w[i]);
+        } else if constexpr (std::is_same<T, __half>::value) {
+            const float2 f = unpack_f16(w[i]);
+            v[2 * i] = f.x;
+            v[2 * i + 1] = f.y;
+        } else {
+            v[2 * i] = __uint_as_float(w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+    }
+}
+template <class T, int VEC>
+__device__ __forceinline__ uint4 pack_unit(const float (&v)[VEC]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (sizeof(T) == 4)
+            w[i] = __float_as_uint(v[i]);
+        else
+            w[i] = pack16(v[2 * i], v[2 * i + 1], !std::is_same<T, __half>::value);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The raw unit: 16 bytes, or one element.
+template <class T, int VEC>
+using Raw = typename std::conditional<VEC == 1, T, uint4>::type;
+
+template <class T, int VEC>
+__device__ __forceinline__ Raw<T, VEC> raw_zero() {
+    if constexpr (VEC == 1)
+        return T(0.f);
+    else
+        return make_uint4(0, 0, 0, 0);
+}
+template <class T, int VEC>
+__device__ __forceinline__ void unpack(const Raw<T, VEC>& r, float (&v)[VEC]) {
+    if constexpr (VEC == 1)
+        v[0] = to_f32(r);
+    else
+        unpack_unit<T, VEC>(r, v);
+}
+template <class T>
+__device__ __forceinline__ T from_f32(float x) {
+    if constexpr (sizeof(T) == 4)
+        return x;
+    else if constexpr (std::is_same<T, __half>::value)
+        return __float2half_rn(x);
+    else
+        return __float2bfloat16_rn(x);
+}
+template <class T, int VEC>
+__device__ __forceinline__ Raw<T, VEC> pack(const float (&v)[VEC]) {
+    if constexpr (VEC == 1)
+        return from_f32<T>(v[0]);
+    else
+        return pack_unit<T, VEC>(v);
+}
+template <class T, int VEC>
+__device__ __forceinline__ Raw<T, VEC>* unit_at(T* p, int64_t row, int64_t stride, int u) {
+    return reinterpret_cast<Raw<T, VEC>*>(p + row * stride) + u;
+}
+template <class T, int VEC>
+__device__ __forceinline__ const Raw<T, VEC>* unit_at(const T* p, int64_t row, int64_t stride, int u) {
+    return reinterpret_cast<const Raw<T, VEC>*>(p + row * stride) + u;
+}
+
+struct LookupArgs {
+    const void* in;   // weight (forward) or grad_out
+    int64_t in_ld;
+    void* out;        // out or grad_weight
+    int64_t out_ld;
+    const int64_t* ids;
+    int64_t N, V, pad;
+    int units;        // of a row
+    int D;
+    int lanes;        // threads of a row (a power of two, at most kLkThreads)
+    float scale;
+    int accumulate;
+    int* err;
+    // backward, sorted
+    int R;            // sorted positions of a chunk
+    int64_t chunks;
+    int64_t sum_blocks;  // then blocks that write zeros
+    int zero_rows;       // table rows of one of these
+    int slices;          // column slices of `lanes` units
+    const uint32_t* keys;  // [m] sorted ids
+    const uint32_t* pos;   // [m] their positions
+    const int* m;
+    float* head;           // [chunks][D] sum of a chunk's first id where it began before the chunk
+    float* tail;           // [chunks][D] of its last id where that began in the chunk and goes on
+};
+
+template <class T, int VEC>
+__global__ void __launch_bounds__(kLkThreads) k_lookup(const __grid_constant__ LookupArgs a) {
+    const int lane = threadIdx.x & (a.lanes - 1), sub = threadIdx.x / a.lanes, per = kLkThreads / a.lanes;
+    const int64_t n0 = (int64_t)blockIdx.x * per * kLkRows + sub;
+    const int u = blockIdx.y * a.lanes + lane;
+    if (u >= a.units) return;
+    int64_t id[kLkRows];
+#pragma unroll
+    for (int i = 0; i < kLkRows; ++i) {
+        const int64_t n = n0 + (int64_t)i * per;
+        id[i] = n < a.N ? __ldg(a.ids + n) : 0;
+    }
+    Raw<T, VEC> r[kLkRows];
+#pragma unroll
+    for (int i = 0; i < kLkRows; ++i) {
+        const int64_t n = n0 + (int64_t)i * per;
+        const bool ok = id[i] >= 0 && id[i] < a.V;
+        r[i] = raw_zero<T, VEC>();
+        if (ok && n < a.N) r[i] = __ldg(unit_at<T, VEC>(static_cast<const T*>(a.in), id[i], a.in_ld, u));
+        if (!ok && u == 0 && a.err) atomicOr(a.err, kErrIndex);
+        if (!ok) id[i] = -1;
+    }
+#pragma unroll
+    for (int i = 0; i < kLkRows; ++i) {
+        const int64_t n = n0 + (int64_t)i * per;
+        if (n >= a.N) break;
+        float v[VEC];
+        unpack<T, VEC>(r[i], v);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) v[j] = id[i] >= 0 ? v[j] * a.scale : 0.f;
+        *unit_at<T, VEC>(static_cast<T*>(a.out), n, a.out_ld, u) = pack<T, VEC>(v);
+    }
+}
+
+// ---------------------------------------------------------------- sort by id
+
+struct SortArgs {
+    const int64_t* ids;
+    int64_t N, V, pad;
+    int nch, passes, bits[kMaxPasses], bins[kMaxPasses];
+    int* H[kMaxPasses];      // [bins][nch], after its scan the sum over earlier chunks
+    int* total[kMaxPasses];  // [bins]
+    uint32_t* keys[2];
+    uint32_t* pos[2];
+    int* m;                  // ids that count
+    int* err;
+};
+
+__device__ __forceinline__ int64_t key_of(const SortArgs& a, int64_t n) {  // -1: does not count
+    const int64_t id = a.ids[n];
+    return id < 0 || id >= a.V || id == a.pad ? -1 : id;
+}
+
+__global__ void __launch_bounds__(kSortBlock) k_lookup_hist(const __grid_constant__ SortArgs a) {
+    extern __shared__ int bins_s[];
+    const int c = blockIdx.x;
+    for (int i = threadIdx.x; i < a.bins[0]; i += kSortBlock) bins_s[i] = 0;
+    for (int p = 1; p < a.passes; ++p)  // counted by the scatter before
+        for (int64_t i = (int64_t)c * kSortBlock + threadIdx.x; i < (int64_t)a.bins[p] * a.nch; i += (int64_t)a.nch * kSortBlock) a.H[p][i] = 0;
+    __syncthreads();
+    const int64_t lo = (int64_t)c * kSortChunk;
+#pragma unroll
+    for (int i = 0; i < kSortChunk / kSortBlock; ++i) {
+        const int64_t n = lo + i * kSortBlock + threadIdx.x;
+        if (n >= a.N) break;
+        const int64_t k = key_of(a, n);
+        if (k >= 0)
+            atomicAdd(&bins_s[(int)k & (a.bins[0] - 1)], 1);
+        else if (a.err && (a.ids[n] < 0 || a.ids[n] >= a.V))
+            atomicOr(a.err, kErrIndex);
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.bins[0]; i += kSortBlock) a.H[0][(int64_t)i * a.nch + c] = bins_s[i];
+}
+
+// A warp per digit: sums over earlier chunks, and over all.
+__global__ void __launch_bounds__(kSortBlock) k_lookup_scan(const __grid_constant__ SortArgs a, int p) {
+    const int b = blockIdx.x * kSortW + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (b >= a.bins[p]) return;
+    int* h = a.H[p] + (int64_t)b * a.nch;
+    int carry = 0;
+    for (int c0 = 0; c0 < a.nch; c0 += 32) {
+        const int c = c0 + lane, v = c < a.nch ? h[c] : 0;
+        int s = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) s += x;
+        }
+        if (c < a.nch) h[c] = carry + s - v;
+        carry += __shfl_sync(0xffffffffu, s, 31);
+    }
+    if (lane == 0) a.total[p][b] = carry;
+}
+
+// Exclusive scan of x over the block's threads; *total: the sum.
+__device__ __forceinline__ int block_scan(int x, int* sh, int* total) {
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    int s = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += y;
+    }
+    __syncthreads();
+    if (lane == 31) sh[w] = s;
+    __syncthreads();
+    int before = 0, all = 0;
+#pragma unroll
+    for (int i = 0; i < kSortW; ++i) {
+        before += i < w ? sh[i] : 0;
+        all += sh[i];
+    }
+    *total = all;
+    return before + s - x;
+}
+
+__global__ void __launch_bounds__(kSortBlock) k_lookup_scatter(const __grid_constant__ SortArgs a, int p) {
+    extern __shared__ int sm[];
+    __shared__ int sh[kSortW];
+    const int bins = a.bins[p], c = blockIdx.x, lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    int* base = sm;             // [bins]
+    int* cnt = sm + bins;       // [kSortW][bins]
+    int shift = 0;
+    for (int i = 0; i < p; ++i) shift += a.bits[i];
+    const int64_t count = p == 0 ? a.N : *a.m;
+    const int64_t lo = (int64_t)c * kSortChunk;
+    // where the digits begin
+    int carry = 0;
+    for (int b0 = 0; b0 < bins; b0 += kSortBlock) {
+        const int b = b0 + threadIdx.x, t = b < bins ? a.total[p][b] : 0;
+        int all;
+        const int before = block_scan(t, sh, &all);
+        if (b < bins) base[b] = carry + before + a.H[p][(int64_t)b * a.nch + c];
+        carry += all;
+    }
+    if (p == 0 && c == 0 && threadIdx.x == 0) *a.m = carry;
+    if (lo >= count) return;
+    for (int i = threadIdx.x; i < kSortW * bins; i += kSortBlock) cnt[i] = 0;
+    __syncthreads();
+    // a warp's positions are consecutive: 8 x 32
+    constexpr int kPer = kSortChunk / kSortBlock;
+    uint32_t key[kPer], at[kPer];
+    int digit[kPer], rank[kPer];
+    int* mine = cnt + w * bins;
+    const int64_t first = lo + w * (kSortChunk / kSortW);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int64_t n = first + i * 32 + lane;
+        digit[i] = -1;
+        key[i] = at[i] = 0;
+        if (n < count) {
+            if (p == 0) {
+                const int64_t k = key_of(a, n);
+                key[i] = (uint32_t)k;
+                at[i] = (uint32_t)n;
+                digit[i] = k >= 0 ? (int)k & (bins - 1) : -1;
+            } else {
+                key[i] = a.keys[(p - 1) & 1][n];
+                at[i] = a.pos[(p - 1) & 1][n];
+                digit[i] = (int)(key[i] >> shift) & (bins - 1);
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const unsigned m = __match_any_sync(0xffffffffu, digit[i]);
+        const int leader = __ffs(m) - 1;
+        int before = 0;
+        if (digit[i] >= 0 && lane == leader) {
+            before = mine[digit[i]];
+            mine[digit[i]] = before + __popc(m);
+        }
+        rank[i] = __shfl_sync(0xffffffffu, before, leader) + __popc(m & lanemask_lt());
+        __syncwarp();
+    }
+    __syncthreads();
+    for (int b = threadIdx.x; b < bins; b += kSortBlock) {
+        int run = base[b];
+#pragma unroll
+        for (int i = 0; i < kSortW; ++i) {
+            const int v = cnt[i * bins + b];
+            cnt[i * bins + b] = run;
+            run += v;
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        if (digit[i] < 0) continue;
+        const int to = mine[digit[i]] + rank[i];
+        a.keys[p & 1][to] = key[i];
+        a.pos[p & 1][to] = at[i];
+        if (p + 1 < a.passes) {
+            const int next = (int)(key[i] >> (shift + a.bits[p])) & (a.bins[p + 1] - 1);
+            atomicAdd(&a.H[p + 1][(int64_t)next * a.nch + to / kSortChunk], 1);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- sums
+
+// scale * v to a row of the gradient, or added to it.
+template <class T, int VEC>
+__device__ __forceinline__ void put_unit(const LookupArgs& a, int64_t row, int u, float (&v)[VEC]) {
+    Raw<T, VEC>* p = unit_at<T, VEC>(static_cast<T*>(a.out), row, a.out_ld, u);
+    if (a.accumulate) {
+        float o[VEC];
+        unpack<T, VEC>(*p, o);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) v[j] = fmaf(v[j], a.scale, o[j]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) v[j] *= a.scale;
+    }
+    *p = pack<T, VEC>(v);
+}
+
+// The first of keys[0, m) that is not below `key`; the whole warp, 32 probes a step.
+__device__ int first_not_below(const uint32_t* keys, int m, uint32_t key) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, hi = m;  // the answer is in [lo, hi]
+    while (lo < hi) {
+        const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+        const unsigned below = __ballot_sync(0xffffffffu, at < hi && __ldg(keys + at) < key);
+        const int n = __popc(below);  // sorted: the first n probes
+        if (n == 0) return lo;
+        hi = min(hi, lo + n * step);
+        lo += (n - 1) * step + 1;
+    }
+    return lo;
+}
+
+// Rows [r0, r0 + rows) that are not flagged, with zeros.
+template <class T, int VEC>
+__device__ void zero_rows(const LookupArgs& a, const uint8_t* named, int64_t r0, int rows) {
+    const int lane = threadIdx.x & (a.lanes - 1), sub = threadIdx.x / a.lanes, per = kLkThreads / a.lanes;
+    for (int r = sub; r < rows; r += per) {
+        if (named[r]) continue;
+        Raw<T, VEC>* p = unit_at<T, VEC>(static_cast<T*>(a.out), r0 + r, a.out_ld, 0);
+#pragma unroll 4
+        for (int u = lane; u < a.units; u += a.lanes) p[u] = raw_zero<T, VEC>();
+    }
+}
+
+template <class T, int VEC>
+__global__ void __launch_bounds__(kLkThreads) k_lookup_sums(const __grid_constant__ LookupArgs a) {
+    __shared__ uint32_t keys_s[kChunkSlots], pos_s[kChunkSlots];
+    const int m = *a.m;
+    if (blockIdx.x >= a.sum_blocks) {
+        uint8_t* named = reinterpret_cast<uint8_t*>(keys_s);
+        int* range = reinterpret_cast<int*>(pos_s);
+        const int64_t r0 = (blockIdx.x - a.sum_blocks) * a.zero_rows;
+        const int rows = (int)min((int64_t)a.zero_rows, a.V - r0);
+        for (int r = threadIdx.x; r < rows; r += kLkThreads) named[r] = 0;
+        const int w = threadIdx.x >> 5;
+        if (w < 2) {
+            const int at = first_not_below(a.keys, m, (uint32_t)(r0 + w * rows));
+            if ((threadIdx.x & 31) == 0) range[w] = at;
+        }
+        __syncthreads();
+        for (int i = range[0] + threadIdx.x; i < range[1]; i += kLkThreads) named[a.keys[i] - (uint32_t)r0] = 1;
+        __syncthreads();
+        zero_rows<T, VEC>(a, named, r0, rows);
+        return;
+    }
+    const int lane = threadIdx.x & (a.lanes - 1), sub = threadIdx.x / a.lanes, per = kLkThreads / a.lanes;
+    const int64_t block = blockIdx.x / a.slices;
+    const int u = (int)(blockIdx.x - block * a.slices) * a.lanes + lane;
+    const int64_t first = block * per * a.R;  // of the block's chunks
+    if (first >= m) return;
+    const int staged = (int)min((int64_t)per * a.R, m - first);
+    for (int i = threadIdx.x; i < staged; i += kLkThreads) {
+        keys_s[i] = a.keys[first + i];
+        pos_s[i] = a.pos[first + i];
+    }
+    __syncthreads();
+    const int64_t j = block * per + sub, b = j * a.R, e = min(b + a.R, (int64_t)m);
+    if (b >= m || u >= a.units) return;
+    const uint32_t* k = keys_s + sub * a.R;
+    const uint32_t* p = pos_s + sub * a.R;
+    const int n = (int)(e - b);
+    const bool goes_back = b > 0 && a.keys[b - 1] == k[0], goes_on = e < m && a.keys[e] == k[n - 1];
+    const T* in = static_cast<const T*>(a.in);
+    float acc[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) acc[i] = 0.f;
+    uint32_t cur = k[0];
+    bool whole = !goes_back;  // the current id began in this chunk
+    for (int t = 0; t < n; t += kInFlight) {
+        Raw<T, VEC> r[kInFlight];
+#pragma unroll
+        for (int i = 0; i < kInFlight; ++i)
+            if (t + i < n) r[i] = __ldcs(unit_at<T, VEC>(in, p[t + i], a.in_ld, u));
+#pragma unroll
+        for (int i = 0; i < kInFlight; ++i) {
+            if (t + i >= n) break;
+            const uint32_t key = k[t + i];
+            if (key != cur) {
+                if (whole) {
+                    put_unit<T, VEC>(a, cur, u, acc);
+                } else {
+#pragma unroll
+                    for (int q = 0; q < VEC; ++q) a.head[j * a.D + u * VEC + q] = acc[q];
+                }
+#pragma unroll
+                for (int q = 0; q < VEC; ++q) acc[q] = 0.f;
+                cur = key;
+                whole = true;
+            }
+            float v[VEC];
+            unpack<T, VEC>(r[i], v);
+#pragma unroll
+            for (int q = 0; q < VEC; ++q) acc[q] += v[q];
+        }
+    }
+    if (whole && !goes_on) {
+        put_unit<T, VEC>(a, cur, u, acc);
+    } else {
+        float* to = (whole ? a.tail : a.head) + j * a.D + u * VEC;
+#pragma unroll
+        for (int q = 0; q < VEC; ++q) to[q] = acc[q];
+    }
+}
+
+// The id that begins in chunk j and goes on: its partial sums, in order.  A block per chunk and
+// slice of 32 units; its 8 warps take the partial sums in turn.
+template <class T, int VEC>
+__global__ void __launch_bounds__(kLkThreads) k_lookup_join(const __grid_constant__ LookupArgs a) {
+    __shared__ float part[kLkThreads / 32][32 * VEC];
+    __shared__ int last_s;
+    const int m = *a.m, w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int slices = (a.units + 31) / 32;
+    const int64_t j = blockIdx.x / slices;
+    const int u = (int)(blockIdx.x - j * slices) * 32 + lane;
+    const int64_t b = j * a.R, e = b + a.R;
+    if (e >= m) return;
+    const uint32_t key = a.keys[e - 1];
+    if (a.keys[e] != key || (b > 0 && a.keys[b - 1] == key)) return;
+    if (w == 0) {
+        const int end = first_not_below(a.keys, m, key + 1);
+        if (lane == 0) last_s = (end - 1) / a.R;  // the last chunk that has it
+    }
+    __syncthreads();
+    const int64_t last = last_s;
+    float s[VEC];
+#pragma unroll
+    for (int q = 0; q < VEC; ++q) s[q] = 0.f;
+    if (u < a.units) {
+#pragma unroll 4
+        for (int64_t c = j + w; c <= last; c += kLkThreads / 32) {
+            const float* from = (c == j ? a.tail : a.head) + c * a.D + u * VEC;
+#pragma unroll
+            for (int q = 0; q < VEC; ++q) s[q] += from[q];
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < VEC; ++q) part[w][q * 32 + lane] = s[q];
+    __syncthreads();
+    if (w > 0 || u >= a.units) return;
+#pragma unroll
+    for (int q = 0; q < VEC; ++q)
+#pragma unroll
+        for (int i = 1; i < kLkThreads / 32; ++i) s[q] += part[i][q * 32 + lane];
+    put_unit<T, VEC>(a, key, u, s);
+}
+
+// Few lookups: a block per lookup and slice of `lanes` units, then blocks that write zeros.
+template <class T, int VEC>
+__global__ void __launch_bounds__(kLkThreads) k_lookup_few(const __grid_constant__ LookupArgs a) {
+    __shared__ int ids[kSmallRows];
+    __shared__ union {
+        int list[kSmallRows];
+        uint8_t named[kZeroRows];
+        float part[kLkThreads * 8];
+    } s;
+    __shared__ int sh[kSortW];
+    const int N = (int)a.N;
+    for (int n = threadIdx.x; n < N; n += kLkThreads) {
+        const int64_t id = a.ids[n];
+        const bool in = id >= 0 && id < a.V;
+        if (!in && a.err && blockIdx.x == 0) atomicOr(a.err, kErrIndex);
+        ids[n] = in && id != a.pad ? (int)id : -1;
+    }
+    __syncthreads();
+    if (blockIdx.x >= a.sum_blocks) {
+        const int64_t r0 = (blockIdx.x - a.sum_blocks) * a.zero_rows;
+        const int rows = (int)min((int64_t)a.zero_rows, a.V - r0);
+        for (int r = threadIdx.x; r < rows; r += kLkThreads) s.named[r] = 0;
+        __syncthreads();
+        for (int n = threadIdx.x; n < N; n += kLkThreads) {
+            const int64_t r = (int64_t)ids[n] - r0;
+            if (ids[n] >= 0 && r >= 0 && r < rows) s.named[r] = 1;
+        }
+        __syncthreads();
+        zero_rows<T, VEC>(a, s.named, r0, rows);
+        return;
+    }
+    const int n0 = (int)(blockIdx.x / a.slices), slice = (int)(blockIdx.x - (int64_t)n0 * a.slices);
+    const int id = ids[n0];
+    if (id < 0) return;
+    // the lookups with this id, in order; a thread's are consecutive
+    constexpr int kPer = kSmallRows / kLkThreads;
+    int mine[kPer], found = 0;
+    bool earlier = false;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int n = threadIdx.x * kPer + i;
+        if (n < N && ids[n] == id) {
+            earlier |= n < n0;
+            mine[found++] = n;
+        }
+    }
+    if (__syncthreads_or(earlier)) return;
+    int count;
+    const int at = block_scan(found, sh, &count);
+    for (int i = 0; i < found; ++i) s.list[at + i] = mine[i];
+    __syncthreads();
+    const int lane = threadIdx.x & (a.lanes - 1), sub = threadIdx.x / a.lanes, per = kLkThreads / a.lanes;
+    const int u = slice * a.lanes + lane;
+    const T* in = static_cast<const T*>(a.in);
+    float acc[VEC];
+#pragma unroll
+    for (int q = 0; q < VEC; ++q) acc[q] = 0.f;
+    const int b = (count * sub + per - 1) / per, e = (count * (sub + 1) + per - 1) / per;  // one lookup: the first share's
+    if (u < a.units) {
+        for (int t = b; t < e; t += kInFlight) {
+            Raw<T, VEC> r[kInFlight];
+#pragma unroll
+            for (int i = 0; i < kInFlight; ++i) r[i] = t + i < e ? __ldg(unit_at<T, VEC>(in, s.list[t + i], a.in_ld, u)) : raw_zero<T, VEC>();
+#pragma unroll
+            for (int i = 0; i < kInFlight; ++i) {
+                float v[VEC];
+                unpack<T, VEC>(r[i], v);
+                if (t + i < e) {
+#pragma unroll
+                    for (int q = 0; q < VEC; ++q) acc[q] += v[q];
+                }
+            }
+        }
+    }
+    if (count > 1 && per > 1) {  // the shares in order
+        __syncthreads();
+#pragma unroll
+        for (int q = 0; q < VEC; ++q) s.part[q * kLkThreads + threadIdx.x] = acc[q];
+        __syncthreads();
+        if (sub == 0)
+            for (int i = 1; i < per; ++i)
+#pragma unroll
+                for (int q = 0; q < VEC; ++q) acc[q] += s.part[q * kLkThreads + i * a.lanes + lane];
+    }
+    if (sub == 0 && u < a.units) put_unit<T, VEC>(a, id, u, acc);
+}
+
+// ---------------------------------------------------------------- host
+
+namespace {
+
+int pow2_at_least(int64_t x, int most) {
+    int p = 1;
+    while (p < x && p < most) p *= 2;
+    return p;
+}
+
+int esize(int dtype) { return dtype == TT_F32 ? 4 : 2; }
+
+tt_status lookup_sizes(int64_t rows, int64_t vocab, int64_t dim, int dtype) {
+    if (dtype != TT_F32 && dtype != TT_BF16 && dtype != TT_F16) return TT_ERR_ARG;
+    if (rows < 0 || rows > TT_LOOKUP_MAX_ROWS || vocab < 1 || vocab > TT_HEAD_MAX_VOCAB || dim < 1 || dim > TT_HEAD_MAX_DIM) return TT_ERR_SHAPE;
+    return TT_OK;
+}
+
+// How a backward pass sorts and cuts its lookups; sizes only, so that the workspace's are known.
+struct LookupPlan {
+    bool sorted;
+    int nch, passes, bits[kMaxPasses], bins[kMaxPasses], R;
+    int64_t chunks;
+    // the workspace's blocks
+    int* H[kMaxPasses];
+    int* total[kMaxPasses];
+    uint32_t* keys[2];
+    uint32_t* pos[2];
+    int* m;
+    float* head;
+    float* tail;
+    size_t bytes;
+};
+
+LookupPlan lookup_plan(int64_t N, int64_t V, int D, int dtype, void* ws) {
+    LookupPlan p{};
+    p.sorted = N > kSmallRows;
+    if (!p.sorted) return p;
+    int bits = 1;
+    while ((1ll << bits) < V) ++bits;
+    p.passes = (bits + kDigitBits - 1) / kDigitBits;
+    for (int i = 0; i < p.passes; ++i) {
+        p.bits[i] = (bits + p.passes - 1) / p.passes;
+        p.bins[i] = 1 << p.bits[i];
+    }
+    p.nch = (int)((N + kSortChunk - 1) / kSortChunk);
+    // long chunks leave fewer partial sums; short ones while the device would not be full
+    const int64_t units = ((int64_t)D * esize(dtype) + 15) / 16;
+    const int per = kLkThreads / pow2_at_least(units, kLkThreads);
+    p.R = std::min(256, kChunkSlots / per);
+    while (p.R > 16 && N / p.R * units < 262144) p.R /= 2;
+    p.chunks = (N + p.R - 1) / p.R;
+    uint8_t* base = static_cast<uint8_t*>(ws);
+    size_t used = 0;
+    auto get = [&](size_t n) {
+        uint8_t* at = base ? base + used : nullptr;
+        used += (n + 255) / 256 * 256;
+        return at;
+    };
+    for (int i = 0; i < p.passes; ++i) {
+        p.H[i] = reinterpret_cast<int*>(get((size_t)p.bins[i] * p.nch * 4));
+        p.total[i] = reinterpret_cast<int*>(get((size_t)p.bins[i] * 4));
+    }
+    for (int i = 0; i < 2; ++i) {
+        p.keys[i] = reinterpret_cast<uint32_t*>(get((size_t)N * 4));
+        p.pos[i] = reinterpret_cast<uint32_t*>(get((size_t)N * 4));
+    }
+    p.m = reinterpret_cast<int*>(get(4));
+    p.head = reinterpret_cast<float*>(get((size_t)p.chunks * D * 4));
+    p.tail = reinterpret_cast<float*>(get((size_t)p.chunks * D * 4));
+    p.bytes = used;
+    return p;
+}
+
+bool aligned(const void* p, int to) { return (uintptr_t)p % to == 0; }
+
+void set_units(LookupArgs* a, int vec, int most) {
+    a->units = a->D / vec;
+    a->lanes = pow2_at_least(a->units, most);
+    a->slices = (a->units + a->lanes - 1) / a->lanes;
+}
+
+template <class T, int VEC>
+tt_status forward_launch(LookupArgs a, cudaStream_t st) {
+    set_units(&a, VEC, kLkThreads);
+    const int per = kLkThreads / a.lanes * kLkRows;
+    k_lookup<T, VEC><<<dim3((unsigned)((a.N + per - 1) / per), (unsigned)a.slices), kLkThreads, 0, st>>>(a);
+    return cudaGetLastError() == cudaSuccess ? TT_OK : TT_ERR_CUDA;
+}
+
+template <class T, int VEC>
+tt_status backward_launch(LookupArgs a, const LookupPlan& p, const int64_t* ids, int dev, cudaStream_t st) {
+    // some 128 KB of table rows to a block that writes zeros
+    a.zero_rows = (int)std::max<int64_t>(1, std::min<int64_t>(kZeroRows, 131072 / ((int64_t)a.D * (int64_t)sizeof(T))));
+    const int64_t zero_blocks = a.accumulate ? 0 : (a.V + a.zero_rows - 1) / a.zero_rows;
+    if (!p.sorted) {
+        set_units(&a, VEC, 64);
+        a.sum_blocks = a.N * a.slices;
+        if (a.sum_blocks + zero_blocks == 0) return TT_OK;
+        k_lookup_few<T, VEC><<<(unsigned)(a.sum_blocks + zero_blocks), kLkThreads, 0, st>>>(a);
+        return cudaGetLastError() == cudaSuccess ? TT_OK : TT_ERR_CUDA;
+    }
+    SortArgs s{};
+    s.ids = ids;
+    s.N = a.N;
+    s.V = a.V;
+    s.pad = a.pad;
+    s.nch = p.nch;
+    s.passes = p.passes;
+    for (int i = 0; i < p.passes; ++i) {
+        s.bits[i] = p.bits[i];
+        s.bins[i] = p.bins[i];
+        s.H[i] = p.H[i];
+        s.total[i] = p.total[i];
+    }
+    for (int i = 0; i < 2; ++i) {
+        s.keys[i] = p.keys[i];
+        s.pos[i] = p.pos[i];
+    }
+    s.m = p.m;
+    s.err = a.err;
+    constexpr size_t kScatterSmem = sizeof(int) * (1 + kSortW) << kDigitBits;
+    struct Tag {};
+    if (!allow_smem<Tag>(k_lookup_scatter, dev, kScatterSmem)) return TT_ERR_CUDA;
+    k_lookup_hist<<<p.nch, kSortBlock, sizeof(int) * p.bins[0], st>>>(s);
+    for (int i = 0; i < p.passes; ++i) {
+        k_lookup_scan<<<(p.bins[i] + kSortW - 1) / kSortW, kSortBlock, 0, st>>>(s, i);
+        k_lookup_scatter<<<p.nch, kSortBlock, sizeof(int) * (1 + kSortW) * p.bins[i], st>>>(s, i);
+    }
+    set_units(&a, VEC, kLkThreads);
+    a.R = p.R;
+    a.chunks = p.chunks;
+    a.keys = p.keys[(p.passes - 1) & 1];
+    a.pos = p.pos[(p.passes - 1) & 1];
+    a.m = p.m;
+    a.head = p.head;
+    a.tail = p.tail;
+    const int per = kLkThreads / a.lanes;
+    a.sum_blocks = (p.chunks + per - 1) / per * a.slices;
+    k_lookup_sums<T, VEC><<<(unsigned)(a.sum_blocks + zero_blocks), kLkThreads, 0, st>>>(a);
+    k_lookup_join<T, VEC><<<(unsigned)(p.chunks * ((a.units + 31) / 32)), kLkThreads, 0, st>>>(a);
+    return cudaGetLastError() == cudaSuccess ? TT_OK : TT_ERR_CUDA;
+}
+
+template <class T>
+tt_status run_lookup(const LookupArgs& a, bool vec, const LookupPlan* plan, int dev, cudaStream_t st) {
+    constexpr int kVec = 16 / (int)sizeof(T);
+    if (!plan) return vec ? forward_launch<T, kVec>(a, st) : forward_launch<T, 1>(a, st);
+    return vec ? backward_launch<T, kVec>(a, *plan, a.ids, dev, st) : backward_launch<T, 1>(a, *plan, a.ids, dev, st);
+}
+
+tt_status dispatch(int dtype, const LookupArgs& a, const LookupPlan* plan, int dev, cudaStream_t st) {
+    const int e = esize(dtype);
+    const bool vec = a.D * e % 16 == 0 && aligned(a.in, 16) && aligned(a.out, 16) && a.in_ld * e % 16 == 0 && a.out_ld * e % 16 == 0;
+    if (dtype == TT_F32) return run_lookup<float>(a, vec, plan, dev, st);
+    if (dtype == TT_BF16) return run_lookup<__nv_bfloat16>(a, vec, plan, dev, st);
+    return run_lookup<__half>(a, vec, plan, dev, st);
+}
+
+}  // namespace
+}  // namespace ttemb
+
+using namespace ttemb;
+
+extern "C" {
+
+int64_t tt_emb_lookup_workspace(int64_t rows, int64_t vocab, int32_t dim, int32_t dtype) {
+    if (lookup_sizes(rows, vocab, dim, dtype) != TT_OK) return -1;
+    return (int64_t)lookup_plan(rows, vocab, dim, dtype, nullptr).bytes;
+}
+
+tt_status tt_emb_lookup_forward(const tt_lookup* lookup, void* out_dev, int64_t out_stride, int32_t* err_dev, tt_stream stream) {
+    if (!lookup) return TT_ERR_ARG;
+    const tt_lookup& l = *lookup;
+    const tt_status s = lookup_sizes(l.rows, l.vocab, l.dim, l.dtype);
+    if (s != TT_OK) return s;
+    if (l.weight_stride < l.dim || out_stride < l.dim) return TT_ERR_SHAPE;
+    if (!l.weight_dev || (l.rows && (!l.ids_dev || !out_dev))) return TT_ERR_ARG;
+    if (!aligned(l.weight_dev, esize(l.dtype)) || !aligned(out_dev, esize(l.dtype)) || !aligned(l.ids_dev, 8) || !aligned(err_dev, 4)) return TT_ERR_ARG;
+    if (l.rows == 0) return TT_OK;
+    int dev = 0;
+    if (head_sms(&dev) <= 0) return TT_ERR_CUDA;
+    LookupArgs a{};
+    a.in = l.weight_dev;
+    a.in_ld = l.weight_stride;
+    a.out = out_dev;
+    a.out_ld = out_stride;
+    a.ids = l.ids_dev;
+    a.N = l.rows;
+    a.V = l.vocab;
+    a.pad = -1;
+    a.D = l.dim;
+    a.scale = l.scale;
+    a.err = err_dev;
+    return dispatch(l.dtype, a, nullptr, dev, reinterpret_cast<cudaStream_t>(stream));
+}
+
+tt_status tt_emb_lookup_backward(const tt_lookup* lookup, const void* grad_out_dev, int64_t grad_out_stride, void* grad_weight_dev,
+                                 int64_t grad_weight_stride, int32_t accumulate, int32_t* err_dev, void* ws_dev, size_t ws_bytes,
+                                 tt_stream stream) {
+    if (!lookup) return TT_ERR_ARG;
+    const tt_lookup& l = *lookup;
+    const tt_status s = lookup_sizes(l.rows, l.vocab, l.dim, l.dtype);
+    if (s != TT_OK) return s;
+    if (grad_out_stride < l.dim || grad_weight_stride < l.dim) return TT_ERR_SHAPE;
+    if (!grad_weight_dev || (l.rows && (!l.ids_dev || !grad_out_dev))) return TT_ERR_ARG;
+    if (!aligned(grad_out_dev, esize(l.dtype)) || !aligned(grad_weight_dev, esize(l.dtype)) || !aligned(l.ids_dev, 8) || !aligned(err_dev, 4) ||
+        !aligned(ws_dev, 256))
+        return TT_ERR_ARG;
+    const LookupPlan p = lookup_plan(l.rows, l.vocab, l.dim, l.dtype, ws_dev);
+    if (ws_bytes < p.bytes || (p.bytes && !ws_dev)) return TT_ERR_ARG;
+    int dev = 0;
+    if (head_sms(&dev) <= 0) return TT_ERR_CUDA;
+    LookupArgs a{};
+    a.in = grad_out_dev;
+    a.in_ld = grad_out_stride;
+    a.out = grad_weight_dev;
+    a.out_ld = grad_weight_stride;
+    a.ids = l.ids_dev;
+    a.N = l.rows;
+    a.V = l.vocab;
+    a.pad = l.padding_idx;
+    a.D = l.dim;
+    a.scale = l.scale;
+    a.accumulate = accumulate != 0;
+    a.err = err_dev;
+    return dispatch(l.dtype, a, &p, dev, reinterpret_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"
