@@ -15,7 +15,7 @@
 // lane and step; pieces of one sequence are joined in their order, so results repeat.
 #include <cmath>
 
-#include "tt_head.cuh"
+#include "tt_units.cuh"
 
 namespace ttemb {
 
@@ -31,6 +31,24 @@ struct __align__(16) Sums {
 };
 constexpr int64_t kSumsBytes = sizeof(Sums);
 static_assert(sizeof(Sums) == 32, "layout of the workspace");
+
+// A sum in two floats, which keeps some 48 bits: every rounding of `hi` goes to `lo` (the exact
+// error of an addition: D. E. Knuth, "The Art of Computer Programming", vol. 2, 4.2.2).  Doubles
+// would cost more than all else here: the device adds two a cycle and multiprocessor.
+struct Long {
+    float hi = 0.f, lo = 0.f;
+    __device__ __forceinline__ void add(float x) {
+        const float s = hi + x, b = s - hi;
+        lo += (hi - (s - b)) + (x - b);
+        hi = s;
+    }
+    __device__ __forceinline__ void add_lanes(int apart) {
+        const float x = __shfl_xor_sync(0xffffffffu, hi, apart), y = __shfl_xor_sync(0xffffffffu, lo, apart);
+        add(x);
+        lo += y;
+    }
+    __device__ __forceinline__ double value() const { return isfinite(hi) ? (double)hi + (double)lo : (double)hi; }
+};
 
 struct Threshold {  // a number in two pieces: hi + lo
     float hi, lo;
@@ -119,14 +137,10 @@ __device__ __forceinline__ Piece piece_of(const AnswerArgs& a, int64_t u, bool w
     return p;
 }
 
-// x > t for x = p - q without the rounding of the difference (d is the rounded one).
-__device__ __forceinline__ bool above(float d, float p, float q, Threshold t) {
-    if (d != t.hi) return d > t.hi;
-    return (double)p - (double)q > (double)t.hi + (double)t.lo;
-}
-__device__ __forceinline__ bool below(float d, float p, float q, Threshold t) {
-    if (d != t.hi) return d < t.hi;
-    return (double)p - (double)q < (double)t.hi + (double)t.lo;
+// x against t for x = p - q without the rounding of the difference: -1, 0, 1.
+__device__ __noinline__ int side_of(float p, float q, Threshold t) {
+    const double x = (double)p - (double)q, y = (double)t.hi + (double)t.lo;
+    return x > y ? 1 : (x < y ? -1 : 0);
 }
 
 // exp(y) - 1 - y.  Where the three nearly cancel, its Taylor series (|y| <= 1: the first term
@@ -147,145 +161,187 @@ __device__ __forceinline__ float exp_less_line(float y) {
     return s * y * y;
 }
 
-// The clipped term of one token: whether its ratio is beyond the bound, L, and dL/dx.
+// The clipped term of one token, d = p - q rounded: whether its ratio is beyond the bound, L, and dL/dx.
+// The rounded d decides which side of a border x is on unless it is the rounded border itself.
 struct Clipped {
     bool over;
     float term, slope;
 };
 __device__ __forceinline__ Clipped clip_term(const AnswerArgs& a, float adv, float d, float p, float q) {
-    Clipped c;
-    float bound = a.high;
-    c.over = adv > 0.f && above(d, p, q, a.thigh);
-    if (adv < 0.f) {
-        if (below(d, p, q, a.tlow)) {
-            c.over = true;
-            bound = a.low;
-        } else if (a.dual > 0.f && above(d, p, q, a.tdual)) {
-            c.over = true;
-            bound = a.dual;
-        }
+    bool high = d > a.thigh.hi, low = d < a.tlow.hi, dual = d > a.tdual.hi;
+    if (d == a.thigh.hi || d == a.tlow.hi || d == a.tdual.hi) {
+        high = side_of(p, q, a.thigh) > 0;
+        low = side_of(p, q, a.tlow) < 0;
+        dual = side_of(p, q, a.tdual) > 0;
     }
-    c.term = -adv * (c.over ? bound : expf(d));
+    Clipped c;
+    c.over = adv > 0.f ? high : (adv < 0.f && (low || dual));
+    const float bound = adv > 0.f ? a.high : (low ? a.low : a.dual), r = expf(d);
+    c.term = -adv * (c.over ? bound : r);
     c.slope = c.over ? 0.f : c.term;
     return c;
 }
 
-// Four values from i on, i a multiple of 4; those at N and beyond are 0.
-__device__ __forceinline__ void load4(const float* p, int64_t i, int64_t N, int vec, float (&v)[4]) {
-    if (vec && i + 4 <= N) {
-        const float4 x = __ldg(reinterpret_cast<const float4*>(p + i));
-        v[0] = x.x;
-        v[1] = x.y;
-        v[2] = x.z;
-        v[3] = x.w;
+// k and dk/dlogp of y = reference - logp.
+__device__ __forceinline__ float kl_of(const AnswerArgs& a, float y) {
+    return a.kl == TT_KL_1 ? -y : (a.kl == TT_KL_2 ? 0.5f * y * y : exp_less_line(y));
+}
+__device__ __forceinline__ float kl_slope(const AnswerArgs& a, float y) {
+    if (a.kl != TT_KL_3) return a.kl == TT_KL_1 ? 1.f : -y;
+    return fabsf(y) > 1.f ? 1.f - expf(y) : -(exp_less_line(y) + y);  // 1 - exp(y)
+}
+
+// Four tokens of a piece, the first a multiple of 4.  A piece's tokens are counted from the last
+// multiple of 4 before it, so that all but its first and last four are loaded whole.
+struct Four {
+    float lp[4], rf[4], od[4], ad[4];
+    unsigned keep;  // bit 8 j + 7: token j is in the piece and counts
+};
+struct Span {
+    int64_t first;  // a multiple of 4
+    int b, e, lim;  // the piece, and the end of the arrays, from there
+    __device__ __forceinline__ explicit Span(const AnswerArgs& a, const Piece& p) {
+        first = p.b & ~3ll;
+        b = (int)(p.b - first);
+        e = (int)(p.e - first);
+        lim = (int)min(a.N - first, (int64_t)1 << 20);
+    }
+};
+__device__ __forceinline__ void load_four(const AnswerArgs& a, const Span& s, int at, bool lp, bool rf, bool od, bool ad, Four& f) {
+    f.keep = 0;
+    if (at >= s.e) return;
+    const int64_t i = s.first + at;
+    unsigned m = 0x01010101u;
+    if (a.vec && at + 4 <= s.lim) {
+        auto get = [&](const float* p, float (&v)[4]) {
+            const float4 x = __ldg(reinterpret_cast<const float4*>(p + i));
+            v[0] = x.x;
+            v[1] = x.y;
+            v[2] = x.z;
+            v[3] = x.w;
+        };
+        if (lp) get(a.logp, f.lp);
+        if (rf) get(a.ref, f.rf);
+        if (od) get(a.old, f.od);
+        if (ad) get(a.adv, f.ad);
+        if (a.mask) m = __ldg(reinterpret_cast<const unsigned*>(a.mask + i));
     } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = i + j < N ? __ldg(p + i + j) : 0.f;
+        for (int j = 0; j < 4; ++j) {
+            if (at + j >= s.lim) break;
+            if (lp) f.lp[j] = __ldg(a.logp + i + j);
+            if (rf) f.rf[j] = __ldg(a.ref + i + j);
+            if (od) f.od[j] = __ldg(a.old + i + j);
+            if (ad) f.ad[j] = __ldg(a.adv + i + j);
+            if (a.mask) m = (m & ~(255u << (8 * j))) | (unsigned)__ldg(a.mask + i + j) << (8 * j);
+        }
     }
+    f.keep = (((m & 0x7F7F7F7Fu) + 0x7F7F7F7Fu) | m) & 0x80808080u;  // bytes that are not 0
+    if (at < s.b) f.keep &= 0x80808080u << (8 * (s.b - at));
+    if (at + 4 > s.e) f.keep &= 0x80808080u >> (8 * (at + 4 - s.e));
 }
-__device__ __forceinline__ unsigned load_mask4(const uint8_t* p, int64_t i, int64_t N, int vec) {  // a byte each
-    if (!p) return 0x01010101u;
-    if (vec && i + 4 <= N) return __ldg(reinterpret_cast<const unsigned*>(p + i));
-    unsigned m = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-        if (i + j < N) m |= (unsigned)__ldg(p + i + j) << (8 * j);
-    return m;
-}
-__device__ __forceinline__ bool counts_at(const Piece& p, int64_t i, unsigned m, int j) {
-    return i + j >= p.b && i + j < p.e && (m >> (8 * j) & 255u);
-}
+__device__ __forceinline__ bool kept(const Four& f, int j) { return f.keep & (0x80u << (8 * j)); }
 
 template <bool POLICY>
 __device__ Sums sum_piece(const AnswerArgs& a, const Piece& p) {
     const int lane = threadIdx.x & 31;
     Sums s{0., 0., 0., 0, 0};
-    const float seq_adv = POLICY && !a.per_token && p.s < a.S ? a.adv[p.s] : 0.f;
-    for (int64_t base = p.b & ~3ll; base < p.e; base += 256) {
-        float lp[2][4], rf[2][4], od[2][4], ad[2][4];
-        unsigned m[2];
+    Long la, lb, lc;
+    if (p.b < p.e) {
+        const bool ref = a.ref != nullptr, per_token = POLICY && a.per_token, clip = POLICY && !a.sequence;
+        const float seq_adv = POLICY && !a.per_token ? __ldg(a.adv + p.s) : 0.f;
+        const Span span(a, p);
+        for (int base = lane * 4; base - lane * 4 < span.e; base += 256) {
+            Four f[2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int64_t i = base + h * 128 + lane * 4, end = i < p.e ? a.N : 0;  // beyond the piece nothing is read
-            load4(a.logp, i, end, a.vec, lp[h]);
-            if (a.ref) load4(a.ref, i, end, a.vec, rf[h]);
-            if (POLICY) load4(a.old, i, end, a.vec, od[h]);
-            if (POLICY && a.per_token) load4(a.adv, i, end, a.vec, ad[h]);
-            m[h] = load_mask4(a.mask, i, end, a.vec);
-        }
-        float fa = 0.f, fb = 0.f, fc = 0.f;
+            for (int h = 0; h < 2; ++h) load_four(a, span, base + h * 128, true, ref, POLICY, per_token, f[h]);
+            float fa = 0.f, fb = 0.f, fc = 0.f;
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+            for (int h = 0; h < 2; ++h) {
+                s.count += __popc(f[h].keep);
+                if constexpr (!POLICY) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if (!counts_at(p, base + h * 128 + lane * 4, m[h], j)) continue;
-                ++s.count;
-                if (!POLICY) {
-                    fa += a.ref ? lp[h][j] - rf[h][j] : lp[h][j];
-                    continue;
+                    for (int j = 0; j < 4; ++j) fa += kept(f[h], j) ? (ref ? f[h].lp[j] - f[h].rf[j] : f[h].lp[j]) : 0.f;
+                } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) fc += kept(f[h], j) ? f[h].lp[j] - f[h].od[j] : 0.f;
+                if (clip) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const Clipped c = clip_term(a, per_token ? f[h].ad[j] : seq_adv, f[h].lp[j] - f[h].od[j], f[h].lp[j], f[h].od[j]);
+                        fa += kept(f[h], j) ? c.term : 0.f;
+                        s.clipped += kept(f[h], j) && c.over;
+                    }
                 }
-                const float d = lp[h][j] - od[h][j];
-                fc += d;
-                if (!a.sequence) {
-                    const Clipped c = clip_term(a, a.per_token ? ad[h][j] : seq_adv, d, lp[h][j], od[h][j]);
-                    fa += c.term;
-                    s.clipped += c.over;
+                if (ref) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float k = kl_of(a, f[h].rf[j] - f[h].lp[j]);
+                        fb += kept(f[h], j) ? k : 0.f;
+                    }
                 }
-                if (a.ref) {
-                    const float y = rf[h][j] - lp[h][j];
-                    fb += a.kl == TT_KL_1 ? -y : (a.kl == TT_KL_2 ? 0.5f * y * y : exp_less_line(y));
                 }
             }
-        s.a += fa;
-        if (POLICY) {
-            s.b += fb;
-            s.c += fc;
+            la.add(fa);
+            if (POLICY) {
+                lb.add(fb);
+                lc.add(fc);
+            }
         }
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
-        s.a += __shfl_xor_sync(0xffffffffu, s.a, o);
+        la.add_lanes(o);
         if (POLICY) {
-            s.b += __shfl_xor_sync(0xffffffffu, s.b, o);
-            s.c += __shfl_xor_sync(0xffffffffu, s.c, o);
+            lb.add_lanes(o);
+            lc.add_lanes(o);
         }
     }
+    s.a = la.value();
+    s.b = lb.value();
+    s.c = lc.value();
     s.count = __reduce_add_sync(0xffffffffu, s.count);
     if (POLICY) s.clipped = __reduce_add_sync(0xffffffffu, s.clipped);
     return s;
 }
 
-// All pieces of sequence s; the whole warp, the same result in every lane.
-template <bool POLICY>
-__device__ Sums sum_sequence(const AnswerArgs& a, const Sums* part, int64_t s) {
+// All pieces of COUNT sequences (s, s + apart ..), by a warp; lane 0 has the result.
+template <int COUNT>
+__device__ __forceinline__ void sum_sequences(const AnswerArgs& a, const Sums* part, int64_t s, int64_t apart, Sums (&t)[COUNT]) {
     const int lane = threadIdx.x & 31;
-    const int64_t b = offset_at(a, s), e = offset_at(a, s + 1), c0 = b / a.K, c1 = e > b ? (e - 1) / a.K : c0;
-    Sums t{0., 0., 0., 0, 0};
-    for (int64_t c = c0 + lane; c <= c1; c += 32) {  // the piece of the sequence in [c K, (c + 1) K)
-        const Sums x = part[c == c0 ? s : a.S + c - 1];
-        t.a += x.a;
-        t.b += x.b;
-        t.c += x.c;
-        t.count += x.count;
-        t.clipped += x.clipped;
-    }
-    if (c1 == c0) {  // lane 0 has it all
-        t.a = __shfl_sync(0xffffffffu, t.a, 0);
-        t.b = __shfl_sync(0xffffffffu, t.b, 0);
-        t.c = __shfl_sync(0xffffffffu, t.c, 0);
-        t.count = __shfl_sync(0xffffffffu, t.count, 0);
-        t.clipped = __shfl_sync(0xffffffffu, t.clipped, 0);
-        return t;
-    }
+    int64_t b[COUNT], e[COUNT];
 #pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        t.a += __shfl_xor_sync(0xffffffffu, t.a, o);
-        t.b += __shfl_xor_sync(0xffffffffu, t.b, o);
-        t.c += __shfl_xor_sync(0xffffffffu, t.c, o);
+    for (int i = 0; i < COUNT; ++i) {
+        b[i] = offset_at(a, s + i * apart);
+        e[i] = offset_at(a, s + i * apart + 1);
     }
-    t.count = __reduce_add_sync(0xffffffffu, t.count);
-    t.clipped = __reduce_add_sync(0xffffffffu, t.clipped);
-    return t;
+    bool one = true;
+#pragma unroll
+    for (int i = 0; i < COUNT; ++i) {
+        const int64_t c0 = b[i] / a.K, c1 = e[i] > b[i] ? (e[i] - 1) / a.K : c0;
+        t[i] = Sums{0., 0., 0., 0, 0};
+        for (int64_t c = c0 + lane; c <= c1; c += 32) {  // the piece of the sequence in [c K, (c + 1) K)
+            const Sums x = part[c == c0 ? s + i * apart : a.S + c - 1];
+            t[i].a += x.a;
+            t[i].b += x.b;
+            t[i].c += x.c;
+            t[i].count += x.count;
+            t[i].clipped += x.clipped;
+        }
+        one = one && c1 == c0;
+    }
+    if (one) return;  // lane 0 has them whole, which is the lane that is asked
+#pragma unroll
+    for (int i = 0; i < COUNT; ++i) {
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            t[i].a += __shfl_xor_sync(0xffffffffu, t[i].a, o);
+            t[i].b += __shfl_xor_sync(0xffffffffu, t[i].b, o);
+            t[i].c += __shfl_xor_sync(0xffffffffu, t[i].c, o);
+        }
+        t[i].count = __reduce_add_sync(0xffffffffu, t[i].count);
+        t[i].clipped = __reduce_add_sync(0xffffffffu, t[i].clipped);
+    }
 }
 
 // dloss/dh of a pair.
@@ -300,7 +356,9 @@ template <bool POLICY>
 __device__ void finish_one(const AnswerArgs& a, const Sums* part, int64_t u) {
     const bool lead = (threadIdx.x & 31) == 0;
     if (POLICY) {
-        const Sums t = sum_sequence<true>(a, part, u);
+        Sums one[1];
+        sum_sequences<1>(a, part, u, 0, one);
+        const Sums& t = one[0];
         if (!lead) return;
         const double n = t.count > 0 ? (double)t.count : 1.0, share = a.average ? 1.0 / n : 1.0;
         const float x = (float)(t.c / n);
@@ -318,7 +376,9 @@ __device__ void finish_one(const AnswerArgs& a, const Sums* part, int64_t u) {
         a.counts_out[u] = t.count;
         a.clipped[u] = over;
     } else {
-        const Sums c = sum_sequence<false>(a, part, u), r = sum_sequence<false>(a, part, a.pairs + u);
+        Sums two[2];
+        sum_sequences<2>(a, part, u, a.pairs, two);
+        const Sums &c = two[0], &r = two[1];
         if (!lead) return;
         const double rc = a.dbeta * c.a / (a.average && c.count > 0 ? c.count : 1), rr = a.dbeta * r.a / (a.average && r.count > 0 ? r.count : 1);
         const float h = (float)(rc - rr - a.dmargin);
@@ -352,6 +412,7 @@ __device__ __forceinline__ void check_offsets(const AnswerArgs& a, int64_t u) { 
 template <bool POLICY>
 __global__ void __launch_bounds__(kAnswerWarps * 32) k_answer_sums(const __grid_constant__ AnswerArgs a) {
     const int64_t u = (int64_t)blockIdx.x * kAnswerWarps + (threadIdx.x >> 5);
+    pdl_launch_dependents();
     if (u >= a.S + a.chunks) return;
     const Sums s = sum_piece<POLICY>(a, piece_of(a, u, false));
     if ((threadIdx.x & 31) == 0) {
@@ -363,6 +424,7 @@ __global__ void __launch_bounds__(kAnswerWarps * 32) k_answer_sums(const __grid_
 template <bool POLICY>
 __global__ void __launch_bounds__(kAnswerWarps * 32) k_answer_finish(const __grid_constant__ AnswerArgs a) {
     const int64_t u = (int64_t)blockIdx.x * kAnswerWarps + (threadIdx.x >> 5);
+    pdl_wait();
     if (u < (POLICY ? a.S : a.pairs)) finish_one<POLICY>(a, a.part, u);
 }
 
@@ -408,47 +470,45 @@ __global__ void __launch_bounds__(kAnswerWarps * 32) k_answer_grad(const __grid_
         }
     }
     const bool kl = POLICY && in && a.ref && a.kl_weight != 0.f, ratio = POLICY && in && !a.sequence;
-    for (int64_t base = p.b & ~3ll; base < p.e; base += 256) {
-        float lp[2][4], rf[2][4], od[2][4], ad[2][4];
-        unsigned m[2];
+    const bool per_token = ratio && a.per_token;
+    const Span span(a, p);
+    for (int base = lane * 4; base - lane * 4 < span.e; base += 256) {
+        Four f[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int64_t i = base + h * 128 + lane * 4, end = i < p.e && in ? a.N : 0;
-            if (kl || ratio) load4(a.logp, i, end, a.vec, lp[h]);
-            if (kl) load4(a.ref, i, end, a.vec, rf[h]);
-            if (ratio) load4(a.old, i, end, a.vec, od[h]);
-            if (ratio && a.per_token) load4(a.adv, i, end, a.vec, ad[h]);
-            m[h] = load_mask4(a.mask, i, end, a.vec);
+            load_four(a, span, base + h * 128, kl || ratio, kl, ratio, per_token, f[h]);
+            if (!in) f[h].keep = 0;
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int64_t i = base + h * 128 + lane * 4;
-            if (i >= p.e) continue;
+            const int at = base + h * 128;
+            if (at >= span.e) continue;
             float v[4];
+            if (POLICY) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                v[j] = 0.f;
-                if (!in || !counts_at(p, i, m[h], j)) continue;
-                if (!POLICY) {
-                    v[j] = g;
-                    continue;
+                for (int j = 0; j < 4; ++j) v[j] = seq_slope;
+                if (ratio) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        v[j] = clip_term(a, per_token ? f[h].ad[j] : adv, f[h].lp[j] - f[h].od[j], f[h].lp[j], f[h].od[j]).slope;
                 }
-                float s = seq_slope;
-                if (ratio) s = clip_term(a, a.per_token ? ad[h][j] : adv, lp[h][j] - od[h][j], lp[h][j], od[h][j]).slope;
                 if (kl) {
-                    const float y = rf[h][j] - lp[h][j];
-                    // dk/dlogp; 1 - exp(y) from the series where it is one
-                    const float k = a.kl == TT_KL_1 ? 1.f : (a.kl == TT_KL_2 ? -y : (fabsf(y) > 1.f ? 1.f - expf(y) : -(exp_less_line(y) + y)));
-                    s = fmaf(a.kl_weight, k, s);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) v[j] = fmaf(a.kl_weight, kl_slope(a, f[h].rf[j] - f[h].lp[j]), v[j]);
                 }
-                v[j] = g * s;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[j] = kept(f[h], j) ? g * v[j] : 0.f;
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[j] = kept(f[h], j) ? g : 0.f;
             }
-            if (a.vec && i >= p.b && i + 4 <= p.e) {
-                *reinterpret_cast<float4*>(a.grad + i) = make_float4(v[0], v[1], v[2], v[3]);
+            float* to = a.grad + span.first + at;
+            if (a.vec && at >= span.b && at + 4 <= span.e) {
+                *reinterpret_cast<float4*>(to) = make_float4(v[0], v[1], v[2], v[3]);
             } else {
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    if (i + j >= p.b && i + j < p.e) a.grad[i + j] = v[j];
+                    if (at + j >= span.b && at + j < span.e) to[j] = v[j];
             }
         }
     }
@@ -487,8 +547,6 @@ tt_status fill_answers(const tt_answers* in, AnswerArgs* a) {
     if (!a->off && a->len > 0x7FFFFFFF) return TT_ERR_SHAPE;  // counts are int32
     return TT_OK;
 }
-
-bool aligned(const void* p, int to) { return (uintptr_t)p % to == 0; }
 
 tt_status fill_preference(const tt_preference* how, AnswerArgs* a) {
     if (!how || how->kind < TT_PREF_SIGMOID || how->kind > TT_PREF_SQUARED) return TT_ERR_ARG;
@@ -529,7 +587,7 @@ tt_status fill_policy(const tt_policy* how, AnswerArgs* a) {
     a->dual = (float)how->dual_clip;
     a->tlow = split(std::log1p(-how->clip_low));
     a->thigh = split(std::log1p(how->clip_high));
-    a->tdual = split(how->dual_clip > 0.0 ? std::log(how->dual_clip) : 0.0);
+    a->tdual = how->dual_clip > 0.0 ? split(std::log(how->dual_clip)) : Threshold{INFINITY, 0.f};
     a->kl_weight = (float)how->kl_weight;
     return TT_OK;
 }
@@ -554,7 +612,7 @@ tt_status run_forward(AnswerArgs a, void* ws, size_t bytes, cudaStream_t st) {
     } else {
         k_answer_sums<POLICY><<<(unsigned)((pieces + kAnswerWarps - 1) / kAnswerWarps), kAnswerWarps * 32, 0, st>>>(a);
         const int64_t out = POLICY ? a.S : a.pairs;
-        k_answer_finish<POLICY><<<(unsigned)((out + kAnswerWarps - 1) / kAnswerWarps), kAnswerWarps * 32, 0, st>>>(a);
+        if (!launch_ahead(k_answer_finish<POLICY>, dim3((unsigned)((out + kAnswerWarps - 1) / kAnswerWarps)), kAnswerWarps * 32, 0, st, a)) return TT_ERR_CUDA;
     }
     return cudaGetLastError() == cudaSuccess ? TT_OK : TT_ERR_CUDA;
 }

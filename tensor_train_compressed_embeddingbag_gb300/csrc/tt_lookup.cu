@@ -18,9 +18,8 @@
 // Few lookups are not sorted: a block per lookup and column slice looks through all ids,
 // leaves if an earlier lookup has the same, and else sums those that have it: one launch.
 #include <algorithm>
-#include <type_traits>
 
-#include "tt_head.cuh"
+#include "tt_units.cuh"
 
 namespace ttemb {
 
@@ -35,79 +34,6 @@ constexpr int kMaxPasses = 3;
 constexpr int kZeroRows = 2048;        // most table rows of a block that writes zeros
 constexpr int kChunkSlots = 4096;      // sorted positions staged by a block
 constexpr int kInFlight = 8;
-
-template <class T, int VEC>
-__device__ __forceinline__ void unpack_unit(const uint4& u, float (&v)[VEC]) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if constexpr (sizeof(T) == 4) {
-            v[i] = __uint_as_float(w[i]);
-        } else if constexpr (std::is_same<T, __half>::value) {
-            const float2 f = unpack_f16(w[i]);
-            v[2 * i] = f.x;
-            v[2 * i + 1] = f.y;
-        } else {
-            v[2 * i] = __uint_as_float(w[i] << 16);
-            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-        }
-    }
-}
-template <class T, int VEC>
-__device__ __forceinline__ uint4 pack_unit(const float (&v)[VEC]) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if constexpr (sizeof(T) == 4)
-            w[i] = __float_as_uint(v[i]);
-        else
-            w[i] = pack16(v[2 * i], v[2 * i + 1], !std::is_same<T, __half>::value);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-// The raw unit: 16 bytes, or one element.
-template <class T, int VEC>
-using Raw = typename std::conditional<VEC == 1, T, uint4>::type;
-
-template <class T, int VEC>
-__device__ __forceinline__ Raw<T, VEC> raw_zero() {
-    if constexpr (VEC == 1)
-        return T(0.f);
-    else
-        return make_uint4(0, 0, 0, 0);
-}
-template <class T, int VEC>
-__device__ __forceinline__ void unpack(const Raw<T, VEC>& r, float (&v)[VEC]) {
-    if constexpr (VEC == 1)
-        v[0] = to_f32(r);
-    else
-        unpack_unit<T, VEC>(r, v);
-}
-template <class T>
-__device__ __forceinline__ T from_f32(float x) {
-    if constexpr (sizeof(T) == 4)
-        return x;
-    else if constexpr (std::is_same<T, __half>::value)
-        return __float2half_rn(x);
-    else
-        return __float2bfloat16_rn(x);
-}
-template <class T, int VEC>
-__device__ __forceinline__ Raw<T, VEC> pack(const float (&v)[VEC]) {
-    if constexpr (VEC == 1)
-        return from_f32<T>(v[0]);
-    else
-        return pack_unit<T, VEC>(v);
-}
-template <class T, int VEC>
-__device__ __forceinline__ Raw<T, VEC>* unit_at(T* p, int64_t row, int64_t stride, int u) {
-    return reinterpret_cast<Raw<T, VEC>*>(p + row * stride) + u;
-}
-template <class T, int VEC>
-__device__ __forceinline__ const Raw<T, VEC>* unit_at(const T* p, int64_t row, int64_t stride, int u) {
-    return reinterpret_cast<const Raw<T, VEC>*>(p + row * stride) + u;
-}
 
 struct LookupArgs {
     const void* in;   // weight (forward) or grad_out
@@ -593,12 +519,6 @@ __global__ void __launch_bounds__(kLkThreads) k_lookup_few(const __grid_constant
 
 namespace {
 
-int pow2_at_least(int64_t x, int most) {
-    int p = 1;
-    while (p < x && p < most) p *= 2;
-    return p;
-}
-
 int esize(int dtype) { return dtype == TT_F32 ? 4 : 2; }
 
 tt_status lookup_sizes(int64_t rows, int64_t vocab, int64_t dim, int dtype) {
@@ -662,8 +582,6 @@ LookupPlan lookup_plan(int64_t N, int64_t V, int D, int dtype, void* ws) {
     p.bytes = used;
     return p;
 }
-
-bool aligned(const void* p, int to) { return (uintptr_t)p % to == 0; }
 
 void set_units(LookupArgs* a, int vec, int most) {
     a->units = a->D / vec;

@@ -16,25 +16,26 @@
 // the B operand.  So the accumulator's rows are table rows and its columns rows of x, and a
 // warp that stores 32 lanes of a column writes 128 consecutive bytes of a row of scores.
 #include <algorithm>
-#include <type_traits>
 
-#include "tt_head.cuh"
+#include "tt_units.cuh"
 
 namespace ttemb {
 
-constexpr int kQ8Threads = 512;   // warp 0: TMA, 1: MMA, 2: tensor memory, 4..7: codes to f16, 8..15: scores out
-constexpr int kQ8K = 128;         // columns of a stage
+constexpr int kQ8Threads = 640;   // warp 0: rows of x, 1: MMA, 2: tensor memory, 3: codes, 4..11: codes to f16, 12..19: scores out
+constexpr int kQ8K = 128;         // columns of a step
 constexpr int kQ8Range = 1024;    // columns that an accumulator takes (a multiple of kQ8K)
-constexpr int kQ8ACols = kQ8K / 2;  // tensor-memory columns of a stage's codes
+constexpr int kQ8ACols = kQ8K / 2;  // tensor-memory columns of a step's codes
 
 template <int BN>
 struct Q8Shape {
-    static constexpr uint32_t kA = 128 * kQ8K, kB = BN * kQ8K * 2, kStage = kA + kB;
-    static constexpr int kStages = (BN <= 32 ? 208 : 200) * 1024 / kStage;
-    static constexpr size_t kSmem = (size_t)kStages * kStage + 1024;
-    static constexpr int kAcc = BN < 32 ? 32 : BN;  // columns from one accumulator to the next
-    static constexpr int kAStages = 2;
-    static constexpr int kACol = 2 * kAcc;
+    // a step's codes leave shared memory early, its rows of x when its MMAs are done: a ring for each
+    static constexpr uint32_t kC = 128 * kQ8K, kX = BN * kQ8K * 2;
+    static constexpr int kXStages = BN > 128 ? 3 : (BN == 128 ? 4 : 6), kCStages = (220 * 1024 - kXStages * kX) / kC;
+    static constexpr size_t kSmem = (size_t)kXStages * kX + (size_t)kCStages * kC + 1024;
+    static constexpr int kAStages = BN > 128 ? 2 : 4;  // steps in tensor memory; every second one belongs to a set of four warps
+    static constexpr int kACol = 2 * BN;               // behind the two accumulators
+    // 192 columns take 96 sums a thread in the last eight warps: registers go there from the others
+    static constexpr bool kShift = BN > 128;
     static_assert(kACol + kAStages * kQ8ACols <= 512 && kSmem + 2048 <= 227 * 1024, "tensor and shared memory");
 };
 
@@ -72,6 +73,19 @@ __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t&
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(0x64806480u));
 }
 
+// Registers of a thread from here on, for all four warps of a group.  A launch has 640 x 96 of them; the
+// groups' shares add up to that: 48 + 2 x 88 + 2 x 128 = 5 x 96.
+constexpr int kQ8Regs = 96, kQ8RegsFeed = 48, kQ8RegsTurn = 88, kQ8RegsOut = 128;
+static_assert(kQ8RegsFeed + 2 * kQ8RegsTurn + 2 * kQ8RegsOut <= 5 * kQ8Regs, "more would never be there");
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void more_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // A unit is 128 table rows x BN rows of x; the tiles of x go fastest, so blocks that run together
 // share table rows.
 template <int BN>
@@ -79,24 +93,29 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
     k_q8_scores(const __grid_constant__ CUtensorMap map_codes, const __grid_constant__ CUtensorMap map_x, const __grid_constant__ Q8Args a) {
     using S = Q8Shape<BN>;
     constexpr int kHalf = BN / 2;        // columns of an epilogue warp
-    constexpr int kRangeChunks = kQ8Range / kQ8K;
+    constexpr int kRangeSteps = kQ8Range / kQ8K;
     extern __shared__ uint8_t raw[];
-    __shared__ uint64_t full[S::kStages], empty[S::kStages], turned[S::kAStages], used[S::kAStages], accfull[2], accempty[2], drain;
+    __shared__ uint64_t cfull[S::kCStages], cempty[S::kCStages], xfull[S::kXStages], xempty[S::kXStages];
+    __shared__ uint64_t turned[S::kAStages], used[S::kAStages], accfull[2], accempty[2], drain;
     __shared__ uint32_t tmem_slot;
     __shared__ int gave_up_s;
     volatile int* gave_up = &gave_up_s;
-    const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
+    const uint32_t xbase = (smem_addr(raw) + 1023u) & ~1023u, cbase = xbase + S::kXStages * S::kX;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const bool lead = lane == 0;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < S::kStages; ++i) {
-            mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 1);   // the stage's MMAs are done (its codes were read before they began)
+        for (int i = 0; i < S::kCStages; ++i) {
+            mbar_init(&cfull[i], 1);
+            mbar_init(&cempty[i], 4);  // the codes are in registers
+        }
+        for (int i = 0; i < S::kXStages; ++i) {
+            mbar_init(&xfull[i], 1);
+            mbar_init(&xempty[i], 1);  // the step's MMAs are done
         }
         for (int i = 0; i < S::kAStages; ++i) {
-            mbar_init(&turned[i], 4);  // codes are in tensor memory
-            mbar_init(&used[i], 1);    // the MMAs that read them are done
+            mbar_init(&turned[i], 4);  // codes are in tensor memory, rows of x in shared memory
+            mbar_init(&used[i], 1);    // the step's MMAs are done
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&accfull[i], 1);
@@ -109,102 +128,127 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = tmem_slot;
-    uint32_t it = 0;   // stages fed, turned or multiplied
+    // one value for the warp, known to the compiler to be so: the MMAs' addresses stay in uniform registers
+    const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
+    // steps of this block's units, one behind the other
+    const int64_t mine = a.units > blockIdx.x ? (a.units - 1 - blockIdx.x) / gridDim.x + 1 : 0, total = mine * a.chunks;
+    uint32_t it = 0;   // steps fed, turned or multiplied
     uint32_t acc = 0;  // accumulators filled or read
     bool ok = true;
 
-    if (warp == 0) {
-        for (int64_t u = blockIdx.x; ok && u < a.units; u += gridDim.x) {
-            const int v = (int)(u / a.mtiles), m = (int)(u - (int64_t)v * a.mtiles);
-            for (int c = 0; c < a.chunks; ++c, ++it) {
-                const uint32_t st = it % S::kStages;
-                ok = head_wait(&empty[st], ((it / S::kStages) & 1) ^ 1, a.wait_ns, gave_up);
-                if (!ok) break;
-                if (lead) {
-                    const uint32_t sa = base + st * S::kStage;
-                    bulk_expect(&full[st], S::kStage);
-                    tma_load2(sa, &map_codes, c * kQ8K, v * 128, &full[st]);
-                    tma_load2(sa + S::kA, &map_x, c * kQ8K, m * BN, &full[st]);
-                    tma_load2(sa + S::kA + S::kB / 2, &map_x, c * kQ8K + 64, m * BN, &full[st]);
+    if (warp < 4) {
+        if (S::kShift) fewer_registers<kQ8RegsFeed>();
+        if (warp == 0 || warp == 3) {
+            const bool x = warp == 0;
+            if (x) pdl_wait();  // x is being quantized; the codes need not wait for that
+            for (int64_t u = blockIdx.x; ok && u < a.units; u += gridDim.x) {
+                const int v = (int)(u / a.mtiles), m = (int)(u - (int64_t)v * a.mtiles);
+                for (int c = 0; c < a.chunks; ++c, ++it) {
+                    if (x) {
+                        const uint32_t st = it % S::kXStages, to = xbase + st * S::kX;
+                        ok = head_wait(&xempty[st], ((it / S::kXStages) & 1) ^ 1, a.wait_ns, gave_up);
+                        if (!ok) break;
+                        if (lead) {
+                            bulk_expect(&xfull[st], S::kX);
+                            tma_load2(to, &map_x, c * kQ8K, m * BN, &xfull[st]);
+                            tma_load2(to + S::kX / 2, &map_x, c * kQ8K + 64, m * BN, &xfull[st]);
+                        }
+                    } else {
+                        const uint32_t st = it % S::kCStages;
+                        ok = head_wait(&cempty[st], ((it / S::kCStages) & 1) ^ 1, a.wait_ns, gave_up);
+                        if (!ok) break;
+                        if (lead) {
+                            bulk_expect(&cfull[st], S::kC);
+                            tma_load2(cbase + st * S::kC, &map_codes, c * kQ8K, v * 128, &cfull[st]);
+                        }
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
             }
-        }
-    } else if (warp == 1) {
-        const uint32_t idesc = idesc_f16(128, BN, 0, false, false);
-        const uint32_t db0 = desc_lo(base + S::kA, kNoLbo);
-        for (int64_t u = blockIdx.x; ok && u < a.units; u += gridDim.x) {
-            for (int r0 = 0; ok && r0 < a.chunks; r0 += kRangeChunks, ++acc) {
-                const uint32_t buf = acc & 1, d = tmem + buf * S::kAcc;
-                ok = head_wait(&accempty[buf], ((acc >> 1) & 1) ^ 1, a.wait_ns, gave_up);
-                if (!ok) break;
-                tc_fence_after();
-                const int steps = min(kRangeChunks, a.chunks - r0);
-                for (int c = 0; c < steps; ++c, ++it) {
-                    const uint32_t st = it % S::kStages, ta = it % S::kAStages;
-                    ok = head_wait(&turned[ta], (it / S::kAStages) & 1, a.wait_ns, gave_up) &&
-                         head_wait(&full[st], (it / S::kStages) & 1, a.wait_ns, gave_up);
+        } else if (warp == 1) {
+            const uint32_t idesc = idesc_f16(128, BN, 0, false, false);
+            const uint32_t db0 = desc_lo(xbase, kNoLbo);
+            for (int64_t i = 0; ok && i < mine; ++i) {
+                for (int r0 = 0; ok && r0 < a.chunks; r0 += kRangeSteps, ++acc) {
+                    const uint32_t buf = acc & 1, d = tmem + buf * BN;
+                    ok = head_wait(&accempty[buf], ((acc >> 1) & 1) ^ 1, a.wait_ns, gave_up);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t pa = tmem + S::kACol + ta * kQ8ACols, db = db0 + st * (S::kStage >> 4);
+                    const int steps = min(kRangeSteps, a.chunks - r0);
+                    for (int c = 0; c < steps; ++c, ++it) {
+                        const uint32_t st = it % S::kXStages, ta = it % S::kAStages;
+                        // (the warps that turned the codes have waited for the rows of x)
+                        ok = head_wait(&turned[ta], (it / S::kAStages) & 1, a.wait_ns, gave_up);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t pa = tmem + S::kACol + ta * kQ8ACols, db = db0 + st * (S::kX >> 4);
 #pragma unroll
-                    for (int k = 0; k < kQ8K / 16; ++k)
-                        mma_f16_ta(d, pa + k * 8, db + (k >= 4 ? (S::kB / 2) >> 4 : 0) + (k & 3) * (32 >> 4), idesc, c > 0 || k > 0, lead);
-                    mma_commit(&empty[st], lead);
-                    mma_commit(&used[ta], lead);
-                }
-                if (ok) mma_commit(&accfull[buf], lead);
-            }
-        }
-    } else if (warp >= 4 && warp < 8) {
-        const int r = (warp - 4) * 32 + lane;
-        for (int64_t u = blockIdx.x; ok && u < a.units; u += gridDim.x) {
-            for (int c = 0; c < a.chunks; ++c, ++it) {
-                const uint32_t st = it % S::kStages, ta = it % S::kAStages;
-                ok = head_wait(&full[st], (it / S::kStages) & 1, a.wait_ns, gave_up) &&
-                     head_wait(&used[ta], ((it / S::kAStages) & 1) ^ 1, a.wait_ns, gave_up);
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t row = base + st * S::kStage + r * 128;
-                const uint32_t to = tmem + ((uint32_t)((warp - 4) * 32) << 16) + S::kACol + ta * kQ8ACols;
-#pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    uint32_t q[16];
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const uint4 w = lds16(row + (((h * 2 + x) ^ (r & 7)) << 4));  // 128-byte swizzle
-                        codes_to_f16(w.x, q[x * 8], q[x * 8 + 1]);
-                        codes_to_f16(w.y, q[x * 8 + 2], q[x * 8 + 3]);
-                        codes_to_f16(w.z, q[x * 8 + 4], q[x * 8 + 5]);
-                        codes_to_f16(w.w, q[x * 8 + 6], q[x * 8 + 7]);
+                        for (int k = 0; k < kQ8K / 16; ++k)
+                            mma_f16_ta(d, pa + k * 8, db + (k >= 4 ? (S::kX / 2) >> 4 : 0) + (k & 3) * (32 >> 4), idesc, c > 0 || k > 0, lead);
+                        mma_commit(&used[ta], lead);
+                        mma_commit(&xempty[st], lead);
                     }
-                    tm_st16(to + h * 16, q);
+                    if (ok) mma_commit(&accfull[buf], lead);
                 }
-                tm_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lead) mbar_arrive(&turned[ta]);
             }
         }
-    } else if (warp >= 8) {
-        const int half = (warp - 8) >> 2, quad = warp & 3;
+    } else if (warp < 12) {
+        if (S::kShift) fewer_registers<kQ8RegsTurn>();
+        const uint32_t set = (warp - 4) >> 2;
+        const int quad = warp & 3, r = quad * 32 + lane;
+        const uint32_t to = tmem + ((uint32_t)(quad * 32) << 16) + S::kACol;
+        for (int64_t i = set; i < total; i += 2) {
+            it = (uint32_t)i;
+            const uint32_t cs = it % S::kCStages, st = it % S::kXStages, ta = it % S::kAStages;
+            ok = head_wait(&cfull[cs], (it / S::kCStages) & 1, a.wait_ns, gave_up);
+            if (!ok) break;
+            // the codes are f16 in registers before the MMAs that still read this place are done
+            const uint32_t row = cbase + cs * S::kC + r * 128;
+            uint32_t q[4][16];
+#pragma unroll
+            for (int h = 0; h < 4; ++h)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const uint4 y = lds16(row + (((h * 2 + x) ^ (r & 7)) << 4));  // 128-byte swizzle
+                    codes_to_f16(y.x, q[h][x * 8], q[h][x * 8 + 1]);
+                    codes_to_f16(y.y, q[h][x * 8 + 2], q[h][x * 8 + 3]);
+                    codes_to_f16(y.z, q[h][x * 8 + 4], q[h][x * 8 + 5]);
+                    codes_to_f16(y.w, q[h][x * 8 + 6], q[h][x * 8 + 7]);
+                }
+            __syncwarp();
+            if (lead) mbar_arrive(&cempty[cs]);
+            ok = head_wait(&xfull[st], (it / S::kXStages) & 1, a.wait_ns, gave_up) &&
+                 head_wait(&used[ta], ((it / S::kAStages) & 1) ^ 1, a.wait_ns, gave_up);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int h = 0; h < 4; ++h) tm_st16(to + ta * kQ8ACols + h * 16, q[h]);
+            tm_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lead) mbar_arrive(&turned[ta]);
+        }
+    } else {
+        if (S::kShift) more_registers<kQ8RegsOut>();
+        pdl_wait();  // the scales of x
+        const int half = (warp - 12) >> 2, quad = warp & 3;
         for (int64_t u = blockIdx.x; ok && u < a.units; u += gridDim.x) {
             const int vt = (int)(u / a.mtiles), mt = (int)(u - (int64_t)vt * a.mtiles);
             const int64_t v = (int64_t)vt * 128 + quad * 32 + lane, m0 = (int64_t)mt * BN + half * kHalf;
             int sum[kHalf];
-            for (int r0 = 0; ok && r0 < a.chunks; r0 += kRangeChunks, ++acc) {
+#pragma unroll 1
+            for (int r0 = 0; ok && r0 < a.chunks; r0 += kRangeSteps, ++acc) {
                 const uint32_t buf = acc & 1;
                 ok = head_wait(&accfull[buf], (acc >> 1) & 1, a.wait_ns, gave_up);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t t0 = tmem + buf * S::kAcc + ((uint32_t)(quad * 32) << 16) + half * kHalf;
+                const uint32_t t0 = tmem + buf * BN + ((uint32_t)(quad * 32) << 16) + half * kHalf;
 #pragma unroll
-                for (int h = 0; h < kHalf; h += 8) {
-                    float x[8];
-                    tm_read8(t0 + h, x);
+                for (int h = 0; h < kHalf; h += 16) {
+                    float x[16];
+                    tm_read16(t0 + h, x);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
+                    for (int j = 0; j < 16; ++j) {
                         const int y = __float2int_rn(x[j]);
                         sum[h + j] = r0 == 0 ? y : sum[h + j] + y;
                     }
@@ -214,13 +258,17 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
                 if (lead) mbar_arrive(&accempty[buf]);
             }
             if (!ok) break;
-            if (v < a.V && m0 < a.M) {
-                const float s = a.scale[v];
-                float* o = a.out + m0 * a.V + v;
-                const int rows = (int)min((int64_t)kHalf, a.M - m0);
+            const int rows = (int)min((int64_t)kHalf, a.M - m0);  // may be below 1
+            const float s = v < a.V ? __ldg(a.scale + v) : 0.f;
+            float* o = a.out + m0 * a.V + v;
+            // a column's scale is in one lane and goes to all
 #pragma unroll
-                for (int j = 0; j < kHalf; ++j) {
-                    if (j < rows) *o = (float)sum[j] * (__ldg(a.xscale + m0 + j) * s);
+            for (int h = 0; h < kHalf; h += 32) {
+                const float xs = h + lane < rows ? __ldg(a.xscale + m0 + h + lane) : 0.f;
+#pragma unroll
+                for (int j = h; j < h + 32 && j < kHalf; ++j) {
+                    const float f = __shfl_sync(0xffffffffu, xs, j - h);
+                    if (j < rows && v < a.V) *o = (float)sum[j] * (f * s);
                     o += a.V;
                 }
             }
@@ -234,7 +282,9 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
     __syncthreads();
     if (*gave_up) {  // no copy and no MMA may still be running when the block ends
         if (threadIdx.x == 0)
-            for (uint32_t i = it > S::kStages ? it - S::kStages : 0; i < it; ++i) head_drain(&full[i % S::kStages], (i / S::kStages) & 1);
+            for (uint32_t i = it > S::kXStages ? it - S::kXStages : 0; i < it; ++i) head_drain(&xfull[i % S::kXStages], (i / S::kXStages) & 1);
+        if (threadIdx.x == 96)
+            for (uint32_t i = it > S::kCStages ? it - S::kCStages : 0; i < it; ++i) head_drain(&cfull[i % S::kCStages], (i / S::kCStages) & 1);
         if (threadIdx.x == 32) {
             mma_commit(&drain, true);
             head_drain(&drain, 0);
@@ -244,6 +294,176 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
     }
     tc_fence_after();
     if (warp == 2) tc_dealloc(tmem, 512);
+}
+
+// ---------------------------------------------------------------- few rows
+//
+// Up to 16 rows of x are a stream: the table's bytes are the floor.  Here a tile's way through shared
+// and tensor memory would cost more than its bytes (a step of the kernel above takes its issuing warp some
+// 700 cycles, whatever it multiplies), so the codes go from global memory to registers, 16 bytes of
+// a row to a thread, become f16 there and are multiplied by the warp-level tensor cores
+// (mma.sync.m16n8k16: 16 table rows x 8 rows of x).  The order of k is free as long as both operands use the
+// same: a thread's 16 columns of a row are the k of four MMAs, and x lies in memory in the order in which the
+// fragments want it.
+constexpr int kFewThreads = 256, kFewWarps8 = kFewThreads / 32;
+constexpr int kFewTile = 32;   // table rows of a warp
+constexpr int kFewK = 64;      // columns of a step
+
+// Where element d of row m is: [step][tile of 8 rows][half of a thread's 16 columns][row, quarter of 64 columns][8].
+__host__ __device__ __forceinline__ int64_t few_at(int64_t m, int d, int ntiles) {
+    return ((((int64_t)(d >> 6) * ntiles + (m >> 3)) * 2 + ((d >> 3) & 1)) * 32 + (m & 7) * 4 + ((d >> 4) & 3)) * 8 + (d & 7);
+}
+
+__device__ __forceinline__ void mma_codes(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+struct FewArgs8 {
+    const int8_t* codes;
+    int64_t pitch, V;
+    const float* scale;
+    const uint4* x;        // few_at
+    const float* xscale;
+    int M, steps;          // of kFewK columns
+    int ksplit;            // warps that share the columns of a table tile
+    float* out;
+};
+
+template <int NT>
+__global__ void __launch_bounds__(kFewThreads, 2) k_q8_few(const __grid_constant__ FewArgs8 a) {
+    constexpr int kAhead = NT == 1 ? 4 : 3;  // steps in flight, as registers allow
+    __shared__ int red[kFewWarps8][NT * 8 * kFewTile];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    const int per = kFewWarps8 / a.ksplit, sub = warp / a.ksplit, ks = warp - sub * a.ksplit;
+    const int jb = a.steps * ks / a.ksplit, je = a.steps * (ks + 1) / a.ksplit;
+    const int64_t tiles = (a.V + kFewTile - 1) / kFewTile, rounds = (tiles + per - 1) / per;
+    // the next step to load: four table rows per thread (rows past V read row V - 1)
+    int64_t lr = blockIdx.x;
+    int lj = jb;
+    const int8_t* row[4];
+    auto at_tile = [&]() {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int64_t v = (lr * per + sub) * kFewTile + r * 8 + g;
+            row[r] = a.codes + (v < a.V ? v : a.V - 1) * a.pitch;
+        }
+    };
+    at_tile();
+    uint4 q[kAhead][4];
+    auto load = [&](uint4 (&w)[4]) {
+        if (lr >= rounds) return;
+        const int64_t d = (int64_t)lj * kFewK + t * 16;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) w[r] = __ldcs(reinterpret_cast<const uint4*>(row[r] + (d < a.pitch ? d : 0)));  // past the end x is 0
+        if (++lj == je) {
+            lj = jb;
+            lr += gridDim.x;
+            if (lr < rounds) at_tile();
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) load(q[i]);
+    pdl_wait();  // x, and its scales
+    int sum[2][NT][4];
+    float acc[2][NT][4];
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                sum[r][n][e] = 0;
+                acc[r][n][e] = 0.f;
+            }
+    int in_range = 0;  // steps in acc: at most 1,024 columns, whose sums are exact
+    auto settle = [&]() {
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    sum[r][n][e] += __float2int_rn(acc[r][n][e]);
+                    acc[r][n][e] = 0.f;
+                }
+        in_range = 0;
+    };
+    int64_t rd = blockIdx.x;
+    int j = jb;
+    while (rd < rounds) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            if (rd >= rounds) break;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint4 x[NT];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) x[n] = __ldg(a.x + ((int64_t)(j * NT + n) * 2 + h) * 32 + lane);
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    uint32_t lo[4], hi[4];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const uint32_t c = h == 0 ? (w == 0 ? q[i][r].x : q[i][r].y) : (w == 0 ? q[i][r].z : q[i][r].w);
+                        codes_to_f16(c, lo[r], hi[r]);
+                    }
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        const uint32_t b0 = w == 0 ? x[n].x : x[n].z, b1 = w == 0 ? x[n].y : x[n].w;
+                        mma_codes(acc[0][n], lo[0], lo[1], hi[0], hi[1], b0, b1);
+                        mma_codes(acc[1][n], lo[2], lo[3], hi[2], hi[3], b0, b1);
+                    }
+                }
+            }
+            load(q[i]);
+            if (++in_range == kQ8Range / kFewK) settle();
+            if (++j < je) continue;
+            settle();
+            // element (row, m) of n tile n: row r * 16 + (e >> 1) * 8 + g, m = n * 8 + 2 t + (e & 1)
+            const int64_t v0 = (rd * per + sub) * kFewTile;
+            if (a.ksplit == 1) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int64_t v = v0 + r * 8 + g;
+                    if (v >= a.V) continue;
+                    const float s = __ldg(a.scale + v);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int m = n * 8 + 2 * t + e;
+                            if (m < a.M) a.out[(int64_t)m * a.V + v] = (float)sum[r >> 1][n][(r & 1) * 2 + e] * (a.xscale[m] * s);
+                        }
+                }
+            } else {  // joined with the other warps of the tile
+                __syncthreads();
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) red[warp][(n * 8 + 2 * t + (e & 1)) * kFewTile + r * 16 + (e >> 1) * 8 + g] = sum[r][n][e];
+                __syncthreads();
+                const int64_t v = v0 + lane;
+                for (int m = ks; m < a.M; m += a.ksplit) {
+                    if (v >= a.V) continue;
+                    int s = 0;
+                    for (int k = 0; k < a.ksplit; ++k) s += red[sub * a.ksplit + k][m * kFewTile + lane];
+                    a.out[(int64_t)m * a.V + v] = (float)s * (a.xscale[m] * __ldg(a.scale + v));
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sum[r][n][e] = 0;
+            j = jb;
+            rd += gridDim.x;
+        }
+    }
 }
 
 // 127 x / top rounded to nearest, ties to even, as if the quotient were exact: the fp32 product by
@@ -258,22 +478,37 @@ __device__ __forceinline__ float code_of(float x, float top, float inv) {
     return fmodf(lo, 2.f) == 0.f ? lo : lo + 1.f;
 }
 
-// Codes of the rows of a matrix: int8 (out8) or as f16 values (out16), columns up to `pitch` with 0.
-// `lanes` threads to a row.
-template <class T>
+// Codes of the rows of a matrix: int8 (out8) or as f16 values (out16), columns up to `pitch` with 0;
+// ntiles > 0: f16 in the order of few_at.
+// `lanes` threads to a row, which keep kQ8Held units each in registers and read what is beyond twice.
+constexpr int kQ8Held = 4;
+template <class T, int VEC>
 __global__ void __launch_bounds__(256) k_q8_rows(const T* x, int64_t ld, int64_t rows, int D, int lanes, int8_t* out8, __half* out16, int64_t pitch,
-                                                 float* scales) {
+                                                 int ntiles, float* scales) {
     __shared__ uint32_t top_s[8];
-    const int per = 256 / lanes, sub = threadIdx.x / lanes, lane = threadIdx.x & (lanes - 1);
+    const int per = 256 / lanes, sub = threadIdx.x / lanes, lane = threadIdx.x & (lanes - 1), units = D / VEC;
     const int64_t blocks = (rows + per - 1) / per;
+    pdl_launch_dependents();
     for (int64_t b = blockIdx.x; b < blocks; b += gridDim.x) {
         const int64_t r = b * per + sub;
         const bool live = r < rows;
-        const T* p = x + (live ? r : 0) * ld;
+        Raw<T, VEC> held[kQ8Held];
         uint32_t most = 0;  // bits of the largest magnitude; infinities and NaN are above all others
-        if (live)
-#pragma unroll 8
-            for (int d = lane; d < D; d += lanes) most = max(most, __float_as_uint(to_f32(p[d])) & 0x7FFFFFFFu);
+        auto take = [&](const Raw<T, VEC>& w) {
+            float y[VEC];
+            unpack<T, VEC>(w, y);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) most = max(most, __float_as_uint(y[j]) & 0x7FFFFFFFu);
+        };
+        if (live) {
+#pragma unroll
+            for (int i = 0; i < kQ8Held; ++i)
+                held[i] = lane + i * lanes < units ? __ldg(unit_at<T, VEC>(x, r, ld, lane + i * lanes)) : raw_zero<T, VEC>();
+#pragma unroll
+            for (int i = 0; i < kQ8Held; ++i) take(held[i]);
+#pragma unroll 4
+            for (int u = lane + kQ8Held * lanes; u < units; u += lanes) take(__ldg(unit_at<T, VEC>(x, r, ld, u)));
+        }
         for (int o = min(lanes, 32) / 2; o; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
         if (lanes > 32) {
             if ((threadIdx.x & 31) == 0) top_s[threadIdx.x >> 5] = most;
@@ -284,31 +519,51 @@ __global__ void __launch_bounds__(256) k_q8_rows(const T* x, int64_t ld, int64_t
         if (!live) continue;
         const float top = __uint_as_float(most);
         if (lane == 0) scales[r] = most > 0x7F800000u ? __int_as_float(0x7FC00000) : __fdiv_rn(top, 127.f);
-        const float inv = 127.f / top;
-        const bool plain = most > 0 && most < 0x7F800000u && inv < 3e38f;
-#pragma unroll 4
-        for (int d = lane; d < pitch; d += lanes) {
-            float k = 0.f;
-            if (d < D) {
-                const float y = to_f32(p[d]);
-                if (plain)
-                    k = code_of(y, top, inv);
-                else if (most == 0x7F800000u)
-                    k = fabsf(y) == INFINITY ? copysignf(1.f, y) : 0.f;
-                else if (most > 0 && most < 0x7F800000u)  // below 2^-120: 127 / top is infinite
-                    k = code_of(y * 0x1p100f, top * 0x1p100f, 127.f / (top * 0x1p100f));
+        const bool finite = most < 0x7F800000u && most > 0;
+        // 127 / top is infinite below 2^-120: both times 2^100, which changes no quotient
+        const float up = finite && most < 0x03800000u ? 0x1p100f : 1.f, big = top * up, inv = 127.f / big;
+        auto put = [&](int u, const Raw<T, VEC>& w) {
+            float y[VEC];
+            unpack<T, VEC>(w, y);
+            float k[VEC];
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                k[j] = finite ? code_of(y[j] * up, big, inv) : 0.f;
+                if (most == 0x7F800000u) k[j] = fabsf(y[j]) == INFINITY ? copysignf(1.f, y[j]) : 0.f;
             }
+            if constexpr (VEC == 1) {
+                if (out8)
+                    out8[r * pitch + u] = (int8_t)(int)k[0];
+                else
+                    out16[ntiles ? few_at(r, u, ntiles) : r * pitch + u] = __float2half_rn(k[0]);
+            } else if (out8) {
+#pragma unroll
+                for (int j = 0; j < VEC; j += 4) {
+                    const uint32_t q = ((uint32_t)(int)k[j] & 255u) | ((uint32_t)(int)k[j + 1] & 255u) << 8 | ((uint32_t)(int)k[j + 2] & 255u) << 16 |
+                                       (uint32_t)(int)k[j + 3] << 24;
+                    *reinterpret_cast<uint32_t*>(out8 + r * pitch + (int64_t)u * VEC + j) = q;
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < VEC; j += 4)
+                    *reinterpret_cast<uint2*>(out16 + (ntiles ? few_at(r, u * VEC + j, ntiles) : r * pitch + (int64_t)u * VEC + j)) =
+                        make_uint2(pack16(k[j], k[j + 1], 0), pack16(k[j + 2], k[j + 3], 0));
+            }
+        };
+#pragma unroll
+        for (int i = 0; i < kQ8Held; ++i)
+            if (lane + i * lanes < units) put(lane + i * lanes, held[i]);
+        for (int u = lane + kQ8Held * lanes; u < units; u += lanes) put(u, __ldg(unit_at<T, VEC>(x, r, ld, u)));
+        for (int64_t d = D + lane; d < pitch; d += lanes) {
             if (out8)
-                out8[r * pitch + d] = (int8_t)(int)k;
+                out8[r * pitch + d] = 0;
             else
-                out16[r * pitch + d] = __float2half_rn(k);
+                out16[ntiles ? few_at(r, (int)d, ntiles) : r * pitch + d] = __float2half_rn(0.f);
         }
     }
 }
 
 namespace {
-
-bool aligned(const void* p, int to) { return (uintptr_t)p % to == 0; }
 
 tt_status q8_sizes(int64_t rows, int64_t dim, int dtype) {
     if (dtype != TT_F32 && dtype != TT_BF16 && dtype != TT_F16) return TT_ERR_ARG;
@@ -319,34 +574,48 @@ tt_status q8_sizes(int64_t rows, int64_t dim, int dtype) {
 int64_t x_pitch(int64_t dim) { return (dim + 7) / 8 * 8; }
 int64_t code_pitch(int64_t dim) { return (dim + 15) / 16 * 16; }
 
+int64_t few_pitch(int64_t dim) { return (dim + kFewK - 1) / kFewK * kFewK; }
+int few_tiles(int64_t rows) { return rows > 16 ? 0 : (rows > 8 ? 2 : 1); }  // of 8 rows; 0: not few
+
 struct Q8Space {
     __half* x;
     float* xscale;
     size_t bytes;
 };
 Q8Space q8_space(int64_t rows, int64_t dim, void* ws) {
-    const size_t codes = ((size_t)rows * x_pitch(dim) * 2 + 255) / 256 * 256;
+    const int nt = few_tiles(rows);
+    const size_t codes = ((size_t)(nt ? (int64_t)nt * 8 * few_pitch(dim) : rows * x_pitch(dim)) * 2 + 255) / 256 * 256;
     uint8_t* p = static_cast<uint8_t*>(ws);
     return {reinterpret_cast<__half*>(p), reinterpret_cast<float*>(p ? p + codes : nullptr), codes + ((size_t)rows * 4 + 255) / 256 * 256};
 }
 
-template <class T>
-void rows_launch(const void* x, int64_t ld, int64_t rows, int D, int8_t* out8, __half* out16, int64_t pitch, float* scales, int sms, cudaStream_t st) {
-    // a row's threads: so many that each has some 8 elements
-    int lanes = 8;
-    while (lanes < 256 && lanes * 8 < D) lanes *= 2;
+template <class T, int VEC>
+void rows_launch(const void* x, int64_t ld, int64_t rows, int D, int8_t* out8, __half* out16, int64_t pitch, int ntiles, float* scales, int sms,
+                 cudaStream_t st) {
+    // two units a thread where there are threads enough, so that one row is quick too
+    const int lanes = std::max(8, pow2_at_least((D / VEC + 1) / 2, 256));
     const int64_t blocks = (rows * lanes + 255) / 256;
-    k_q8_rows<T><<<(unsigned)std::min<int64_t>(blocks, 16ll * sms), 256, 0, st>>>(static_cast<const T*>(x), ld, rows, D, lanes, out8, out16, pitch, scales);
+    k_q8_rows<T, VEC><<<(unsigned)std::min<int64_t>(blocks, 16ll * sms), 256, 0, st>>>(static_cast<const T*>(x), ld, rows, D, lanes, out8, out16, pitch,
+                                                                                     ntiles, scales);
+}
+template <class T>
+void rows_launch(const void* x, int64_t ld, int64_t rows, int D, int8_t* out8, __half* out16, int64_t pitch, int ntiles, float* scales, int sms,
+                 cudaStream_t st) {
+    constexpr int kVec = 16 / (int)sizeof(T);
+    if (D % kVec == 0 && aligned(x, 16) && ld % kVec == 0)
+        rows_launch<T, kVec>(x, ld, rows, D, out8, out16, pitch, ntiles, scales, sms, st);
+    else
+        rows_launch<T, 1>(x, ld, rows, D, out8, out16, pitch, ntiles, scales, sms, st);
 }
 
-void quantize_rows(const void* x, int64_t ld, int64_t rows, int D, int dtype, int8_t* out8, __half* out16, int64_t pitch, float* scales, int sms,
-                   cudaStream_t st) {
+void quantize_rows(const void* x, int64_t ld, int64_t rows, int D, int dtype, int8_t* out8, __half* out16, int64_t pitch, int ntiles, float* scales,
+                   int sms, cudaStream_t st) {
     if (dtype == TT_F32)
-        rows_launch<float>(x, ld, rows, D, out8, out16, pitch, scales, sms, st);
+        rows_launch<float>(x, ld, rows, D, out8, out16, pitch, ntiles, scales, sms, st);
     else if (dtype == TT_BF16)
-        rows_launch<__nv_bfloat16>(x, ld, rows, D, out8, out16, pitch, scales, sms, st);
+        rows_launch<__nv_bfloat16>(x, ld, rows, D, out8, out16, pitch, ntiles, scales, sms, st);
     else
-        rows_launch<__half>(x, ld, rows, D, out8, out16, pitch, scales, sms, st);
+        rows_launch<__half>(x, ld, rows, D, out8, out16, pitch, ntiles, scales, sms, st);
 }
 
 // [rows][cols] of bytes or f16, rows `pitch` bytes apart, in boxes of 128 bytes x box_rows; outside: 0.
@@ -360,6 +629,17 @@ bool make_map2(CUtensorMap* m, const void* p, bool f16, int64_t cols, int64_t ro
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+template <int NT>
+tt_status few_launch(FewArgs8 a, int sms, cudaStream_t st) {
+    // warps that share a tile's columns: more of them while the tiles alone would give a warp slot fewer
+    // than 4, as long as each keeps four steps
+    const int64_t tiles = (a.V + kFewTile - 1) / kFewTile;
+    a.ksplit = 1;
+    while (a.ksplit < kFewWarps8 && tiles * a.ksplit < 4ll * sms * 2 * kFewWarps8 && a.steps >= 8 * a.ksplit) a.ksplit *= 2;
+    const int64_t per = kFewWarps8 / a.ksplit, rounds = (tiles + per - 1) / per;
+    return launch_ahead(k_q8_few<NT>, dim3((unsigned)std::min<int64_t>(rounds, 2 * sms)), kFewThreads, 0, st, a) ? TT_OK : TT_ERR_CUDA;
+}
+
 template <int BN>
 struct Q8Tag {};
 
@@ -371,8 +651,15 @@ tt_status scores_launch(Q8Args a, const int8_t* codes, const __half* x, int D, i
     a.mtiles = (int)((a.M + BN - 1) / BN);
     a.units = (a.V + 127) / 128 * a.mtiles;
     if (!allow_smem<Q8Tag<BN>>(k_q8_scores<BN>, dev, Q8Shape<BN>::kSmem)) return TT_ERR_CUDA;
-    k_q8_scores<BN><<<(unsigned)std::min<int64_t>(a.units, sms), kQ8Threads, Q8Shape<BN>::kSmem, st>>>(mc, mx, a);
-    return cudaGetLastError() == cudaSuccess ? TT_OK : TT_ERR_CUDA;
+    if (Q8Shape<BN>::kShift) {  // the warps that take registers wait for them: they have to be there
+        static const bool enough = [] {
+            cudaFuncAttributes f;
+            return cudaFuncGetAttributes(&f, k_q8_scores<BN>) == cudaSuccess && f.numRegs >= kQ8Regs;
+        }();
+        if (!enough) return TT_ERR_CUDA;
+    }
+    return launch_ahead(k_q8_scores<BN>, dim3((unsigned)std::min<int64_t>(a.units, sms)), kQ8Threads, Q8Shape<BN>::kSmem, st, mc, mx, a) ? TT_OK
+                                                                                                                                         : TT_ERR_CUDA;
 }
 
 }  // namespace
@@ -397,7 +684,7 @@ tt_status tt_emb_q8_quantize(const void* weight_dev, int64_t weight_stride, int6
     if (rows == 0) return TT_OK;
     const int sms = head_sms();
     if (sms <= 0) return TT_ERR_CUDA;
-    quantize_rows(weight_dev, weight_stride, rows, dim, dtype, codes_dev, nullptr, code_pitch(dim), scales_dev, sms, reinterpret_cast<cudaStream_t>(stream));
+    quantize_rows(weight_dev, weight_stride, rows, dim, dtype, codes_dev, nullptr, code_pitch(dim), 0, scales_dev, sms, reinterpret_cast<cudaStream_t>(stream));
     return cudaGetLastError() == cudaSuccess ? TT_OK : TT_ERR_CUDA;
 }
 
@@ -417,7 +704,22 @@ tt_status tt_emb_q8_scores(const void* x_dev, int64_t x_stride, int64_t rows, in
     const int sms = head_sms(&dev);
     if (sms <= 0) return TT_ERR_CUDA;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    quantize_rows(x_dev, x_stride, rows, dim, dtype, nullptr, w.x, x_pitch(dim), w.xscale, sms, st);
+    const int nt = few_tiles(rows);
+    quantize_rows(x_dev, x_stride, rows, dim, dtype, nullptr, w.x, nt ? few_pitch(dim) : x_pitch(dim), nt, w.xscale, sms, st);
+    if (cudaGetLastError() != cudaSuccess) return TT_ERR_CUDA;
+    if (nt) {
+        FewArgs8 f{};
+        f.codes = codes_dev;
+        f.pitch = code_pitch(dim);
+        f.V = vocab;
+        f.scale = scales_dev;
+        f.x = reinterpret_cast<const uint4*>(w.x);
+        f.xscale = w.xscale;
+        f.M = (int)rows;
+        f.steps = (int)(few_pitch(dim) / kFewK);
+        f.out = out_dev;
+        return nt == 1 ? few_launch<1>(f, sms, st) : few_launch<2>(f, sms, st);
+    }
     Q8Args a{};
     a.M = rows;
     a.V = vocab;
@@ -428,7 +730,6 @@ tt_status tt_emb_q8_scores(const void* x_dev, int64_t x_stride, int64_t rows, in
     a.wait_ns = head_wait_limit();
     a.err = err_dev;
     // the narrowest tile that holds the rows; beyond 192 the width that pads less
-    if (rows <= 16) return scores_launch<16>(a, codes_dev, w.x, dim, sms, dev, st);
     if (rows <= 32) return scores_launch<32>(a, codes_dev, w.x, dim, sms, dev, st);
     if (rows <= 64) return scores_launch<64>(a, codes_dev, w.x, dim, sms, dev, st);
     if (rows <= 128) return scores_launch<128>(a, codes_dev, w.x, dim, sms, dev, st);
