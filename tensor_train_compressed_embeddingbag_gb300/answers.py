@@ -75,7 +75,7 @@ class _Policy(ctypes.Structure):
 
 def tt_emb_answers_workspace(tokens: int, sequences: int) -> int:
     """Bytes of workspace that a forward call on so many tokens and sequences takes."""
-    n = _c("tt_emb_answers_workspace")(int(tokens), int(sequences))
+    n = _c("tt_emb_answers_workspace")(tokens, sequences)
     if n < 0:
         _refuse(TT_ERR_SHAPE, "tt_emb_answers_workspace: sizes outside the limits")
     return n
@@ -112,14 +112,14 @@ def _answers(logp, reference, mask, offsets, average, read_logp=True):
     r = None if reference is None else _vector(reference, torch.float32, logp.shape, device, "reference")
     m = None if mask is None else _mask(mask, logp.shape, device)
     o = None if offsets is None else _vector(offsets, torch.int64, (count + 1,), device, "offsets")
-    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-    return _Answers(ptr(x), ptr(r), ptr(m), ptr(o), logp.numel(), count, int(bool(average))), count, (x, r, m, o)
+    keep = x, r, m, o
+    return _Answers(*[None if t is None else t.data_ptr() for t in keep], logp.numel(), count, bool(average)), count, keep
 
 
 def _preference(beta, kind, label_smoothing, margin):
     if kind not in _KINDS:
         _refuse(TT_ERR_ARG, f"kind must be one of {', '.join(_KINDS)}")
-    return _Preference(_KINDS[kind], float(beta), float(label_smoothing), float(margin))
+    return _Preference(_KINDS[kind], beta, label_smoothing, margin)
 
 
 def _policy(old_logp, advantages, logp, count, clip, dual_clip, kl, kl_weight, level, per_token):
@@ -133,8 +133,7 @@ def _policy(old_logp, advantages, logp, count, clip, dual_clip, kl, kl_weight, l
         if per_token and shape == (count,):
             _refuse(TT_ERR_ARG, "as many tokens as sequences: say by per_token which of the two the advantages belong to")
     adv = _vector(advantages, torch.float32, logp.shape if per_token else (count,), logp.device, "advantages")
-    return _Policy(old.data_ptr(), adv.data_ptr(), int(per_token), _LEVELS[level], _KLS[kl], float(low), float(high), float(dual_clip or 0.0),
-                   float(kl_weight)), (old, adv)
+    return _Policy(old.data_ptr(), adv.data_ptr(), per_token, _LEVELS[level], _KLS[kl], low, high, dual_clip or 0.0, kl_weight), (old, adv)
 
 
 def tt_emb_preference_forward(logp: torch.Tensor, reference: Optional[torch.Tensor] = None, mask: Optional[torch.Tensor] = None,
@@ -153,13 +152,14 @@ def tt_emb_preference_forward(logp: torch.Tensor, reference: Optional[torch.Tens
         if count % 2:
             _refuse(TT_ERR_SHAPE, "the number of sequences must be even: the chosen ones, then the rejected ones")
         n = tt_emb_answers_workspace(a.tokens, count)
-        out = torch.empty(2 * count, dtype=torch.float32, device=device)  # loss, margins, rewards
-        loss, margins, rewards = out[:count // 2], out[count // 2:count], out[count:]
-        counts = torch.empty(count, dtype=torch.int32, device=device)
-        ws = torch.empty(n, dtype=torch.uint8, device=device)
-        _check(_c("tt_emb_preference_forward")(ctypes.byref(a), ctypes.byref(how), loss.data_ptr(), margins.data_ptr(), rewards.data_ptr(),
-                                               counts.data_ptr(), _err_word(err, device), ws.data_ptr(), n, _stream_now(device.index)),
-               "tt_emb_preference_forward")
+        ws = torch.empty(n, dtype=torch.uint8, device=device) if n else None
+        pairs = count // 2
+        loss, margins, rewards, counts = torch.empty(3 * count, dtype=torch.float32, device=device).split((pairs, pairs, count, count))
+        counts = counts.view(torch.int32)
+        st = _c("tt_emb_preference_forward")(ctypes.byref(a), ctypes.byref(how), loss.data_ptr(), margins.data_ptr(), rewards.data_ptr(),
+                                             counts.data_ptr(), _err_word(err, device), ws.data_ptr() if n else None, n, _stream_now(device.index))
+        if st:
+            _check(st, "tt_emb_preference_forward")
     return loss, margins, rewards, counts
 
 
@@ -176,8 +176,10 @@ def tt_emb_preference_backward(logp: torch.Tensor, margins: torch.Tensor, counts
         counts = _vector(counts, torch.int32, (count,), device, "counts")
         grad_loss = _vector(grad_loss, torch.float32, (count // 2,), device, "grad_loss")
         grad = torch.empty(logp.shape, dtype=torch.float32, device=device)
-        _check(_c("tt_emb_preference_backward")(ctypes.byref(a), ctypes.byref(how), margins.data_ptr(), counts.data_ptr(), grad_loss.data_ptr(),
-                                                grad.data_ptr(), _stream_now(device.index)), "tt_emb_preference_backward")
+        st = _c("tt_emb_preference_backward")(ctypes.byref(a), ctypes.byref(how), margins.data_ptr(), counts.data_ptr(), grad_loss.data_ptr(),
+                                              grad.data_ptr(), _stream_now(device.index))
+        if st:
+            _check(st, "tt_emb_preference_backward")
     return grad
 
 
@@ -196,12 +198,14 @@ def tt_emb_policy_forward(logp: torch.Tensor, old_logp: torch.Tensor, advantages
         a, count, keep = _answers(logp, reference, mask, offsets, average)
         how, more = _policy(old_logp, advantages, logp, count, clip, dual_clip, kl, kl_weight, level, per_token)
         n = tt_emb_answers_workspace(a.tokens, count)
-        loss, kl_out, log_ratio = torch.empty((3, count), dtype=torch.float32, device=device).unbind(0)
-        counts, clipped = torch.empty((2, count), dtype=torch.int32, device=device).unbind(0)
-        ws = torch.empty(n, dtype=torch.uint8, device=device)
-        _check(_c("tt_emb_policy_forward")(ctypes.byref(a), ctypes.byref(how), loss.data_ptr(), kl_out.data_ptr(), log_ratio.data_ptr(),
-                                           counts.data_ptr(), clipped.data_ptr(), _err_word(err, device), ws.data_ptr(), n,
-                                           _stream_now(device.index)), "tt_emb_policy_forward")
+        ws = torch.empty(n, dtype=torch.uint8, device=device) if n else None
+        loss, kl_out, log_ratio, counts, clipped = torch.empty((5, count), dtype=torch.float32, device=device).unbind(0)
+        counts, clipped = counts.view(torch.int32), clipped.view(torch.int32)
+        st = _c("tt_emb_policy_forward")(ctypes.byref(a), ctypes.byref(how), loss.data_ptr(), kl_out.data_ptr(), log_ratio.data_ptr(),
+                                         counts.data_ptr(), clipped.data_ptr(), _err_word(err, device), ws.data_ptr() if n else None, n,
+                                         _stream_now(device.index))
+        if st:
+            _check(st, "tt_emb_policy_forward")
     return loss, kl_out, log_ratio, counts, clipped
 
 
@@ -220,8 +224,10 @@ def tt_emb_policy_backward(logp: torch.Tensor, old_logp: torch.Tensor, advantage
         counts = _vector(counts, torch.int32, (count,), device, "counts")
         grad_loss = _vector(grad_loss, torch.float32, (count,), device, "grad_loss")
         grad = torch.empty(logp.shape, dtype=torch.float32, device=device)
-        _check(_c("tt_emb_policy_backward")(ctypes.byref(a), ctypes.byref(how), log_ratio.data_ptr(), counts.data_ptr(), grad_loss.data_ptr(),
-                                            grad.data_ptr(), _stream_now(device.index)), "tt_emb_policy_backward")
+        st = _c("tt_emb_policy_backward")(ctypes.byref(a), ctypes.byref(how), log_ratio.data_ptr(), counts.data_ptr(), grad_loss.data_ptr(),
+                                          grad.data_ptr(), _stream_now(device.index))
+        if st:
+            _check(st, "tt_emb_policy_backward")
     return grad
 
 

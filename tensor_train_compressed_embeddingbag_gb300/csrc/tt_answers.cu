@@ -11,7 +11,7 @@
 // of K tokens, begins a piece, which ends where its sequence ends or at the next multiple of
 // K.  So there are at most S + N / K pieces, each in one sequence and at most K tokens
 // long, and piece u < S begins sequence u while piece S + c begins at token (c + 1) K (and is
-// empty where a sequence begins there or none is).  A warp takes a piece, eight tokens a
+// empty where a sequence begins there or none is).  A warp takes a piece, four tokens a
 // lane and step; pieces of one sequence are joined in their order, so results repeat.
 #include <cmath>
 
@@ -19,18 +19,10 @@
 
 namespace ttemb {
 
-constexpr int kPieceMin = 256, kPieceMax = 2048;  // tokens
+constexpr int kPieceMin = 8, kPieceMax = 11;  // log2 of K, tokens
 constexpr int kAnswerWarps = 8;                   // pieces of a block
 constexpr int kOneWarps = 32;                     // of the block that does a small call alone
 constexpr int64_t kOneTokens = 8192, kOnePieces = 320;
-
-// Sums over a piece, and over a sequence.
-struct __align__(16) Sums {
-    double a, b, c;  // preference: a = sum of log ratios; policy: L, k, d
-    int count, clipped;
-};
-constexpr int64_t kSumsBytes = sizeof(Sums);
-static_assert(sizeof(Sums) == 32, "layout of the workspace");
 
 // A sum in two floats, which keeps some 48 bits: every rounding of `hi` goes to `lo` (the exact
 // error of an addition: D. E. Knuth, "The Art of Computer Programming", vol. 2, 4.2.2).  Doubles
@@ -47,8 +39,20 @@ struct Long {
         add(x);
         lo += y;
     }
+    __device__ __forceinline__ void add(const Long& x) {
+        add(x.hi);
+        lo += x.lo;
+    }
     __device__ __forceinline__ double value() const { return isfinite(hi) ? (double)hi + (double)lo : (double)hi; }
 };
+
+// Sums over a piece, and over a sequence.
+struct __align__(16) Sums {
+    Long a, b, c;  // preference: a = sum of log ratios; policy: L, k, d
+    int count = 0, clipped = 0;
+};
+constexpr int64_t kSumsBytes = sizeof(Sums);
+static_assert(sizeof(Sums) == 32, "layout of the workspace");
 
 struct Threshold {  // a number in two pieces: hi + lo
     float hi, lo;
@@ -60,7 +64,7 @@ struct AnswerArgs {
     const uint8_t* mask;
     const int64_t* off;
     int64_t N, S, len;  // len: tokens of a sequence without offsets
-    int K;
+    int shift;          // log2 of K
     int64_t chunks;     // pieces that begin at a multiple of K
     int average, vec;
     Sums* part;         // [S + chunks]
@@ -91,6 +95,9 @@ struct AnswerArgs {
     const float* log_ratio_in;
 };
 
+// The warp's number in its block, known to the compiler to be one value for the warp.
+__device__ __forceinline__ int warp_id() { return __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0); }
+
 struct Piece {
     int64_t s, b, e;  // sequence (S: behind the last one, -1: nothing), tokens [b, e)
 };
@@ -103,7 +110,10 @@ __device__ __forceinline__ int64_t offset_at(const AnswerArgs& a, int64_t s) {
 
 // The sequence that holds token t, or S (behind the last one): the largest s with offset[s] <= t.
 __device__ int64_t sequence_of(const AnswerArgs& a, int64_t t) {
-    if (!a.off) return a.len ? t / a.len : a.S;
+    if (!a.off) {
+        if (a.len == 0) return a.S;
+        return a.N < 1ll << 31 ? (int64_t)((uint32_t)t / (uint32_t)a.len) : t / a.len;
+    }
     const int lane = threadIdx.x & 31;
     int64_t lo = 0, hi = a.S;
     while (hi > lo) {  // 32 probes a step
@@ -126,12 +136,12 @@ __device__ __forceinline__ Piece piece_of(const AnswerArgs& a, int64_t u, bool w
         p.s = u;
         p.b = offset_at(a, u);
         p.e = u < a.S ? offset_at(a, u + 1) : a.N;
-        p.e = min(p.e, (p.b / a.K + 1) * a.K);
+        p.e = min(p.e, ((p.b >> a.shift) + 1) << a.shift);
     } else {
-        p.b = (u - seqs + 1) * a.K;
+        p.b = (u - seqs + 1) << a.shift;
         p.s = sequence_of(a, p.b);
         p.e = p.s < a.S ? offset_at(a, p.s + 1) : (with_rest ? a.N : p.b);
-        p.e = min(p.e, p.b + a.K);
+        p.e = min(p.e, p.b + ((int64_t)1 << a.shift));
         if (offset_at(a, p.s) >= p.b) p.e = p.b;  // begins there: has a piece of its own
     }
     return p;
@@ -143,205 +153,255 @@ __device__ __noinline__ int side_of(float p, float q, Threshold t) {
     return x > y ? 1 : (x < y ? -1 : 0);
 }
 
-// exp(y) - 1 - y.  Where the three nearly cancel, its Taylor series (|y| <= 1: the first term
-// left out is below 2^-28 of the sum).
-__device__ __forceinline__ float exp_less_line(float y) {
-    if (fabsf(y) > 1.f) return y > 64.f ? expf(y) : expf(y) - 1.f - y;  // (infinite, not inf - inf)
-    float s = 1.f / 479001600.f;
-    s = fmaf(s, y, 1.f / 39916800.f);
-    s = fmaf(s, y, 1.f / 3628800.f);
-    s = fmaf(s, y, 1.f / 362880.f);
-    s = fmaf(s, y, 1.f / 40320.f);
-    s = fmaf(s, y, 1.f / 5040.f);
-    s = fmaf(s, y, 1.f / 720.f);
-    s = fmaf(s, y, 1.f / 120.f);
-    s = fmaf(s, y, 1.f / 24.f);
-    s = fmaf(s, y, 1.f / 6.f);
-    s = fmaf(s, y, 0.5f);
-    return s * y * y;
+// exp(y) - 1 - y = y^2 (1/2 + y/6 + ..) where the three nearly cancel, |y| <= 1: the first term left out is
+// below 2^-27 of the sum.  From the highest power down.
+constexpr int kTerms = 10;
+__device__ constexpr float kSeries[kTerms] = {1.f / 39916800.f, 1.f / 3628800.f, 1.f / 362880.f, 1.f / 40320.f, 1.f / 5040.f,
+                                              1.f / 720.f,      1.f / 120.f,     1.f / 24.f,     1.f / 6.f,     0.5f};
+__device__ __forceinline__ float series(float y) {
+    float s = kSeries[0];
+#pragma unroll
+    for (int i = 1; i < kTerms; ++i) s = fmaf(s, y, kSeries[i]);
+    return s * y;
 }
+__device__ __noinline__ float exp_less_line(float y) {
+    if (fabsf(y) <= 1.f) return series(y) * y;
+    return y > 64.f ? expf(y) : expf(y) - 1.f - y;  // (infinite, not inf - inf)
+}
+__device__ __noinline__ float one_less_exp(float y) { return fabsf(y) <= 1.f ? fmaf(series(y), -y, -y) : 1.f - expf(y); }
 
-// The clipped term of one token, d = p - q rounded: whether its ratio is beyond the bound, L, and dL/dx.
-// The rounded d decides which side of a border x is on unless it is the rounded border itself.
+// The clipped term of a token, x = p - q with d its rounded value: whether its ratio is beyond the bound, L, and dL/dx.
+// The rounded d decides which side of a border x is on unless it is the rounded border itself: on_border.
 struct Clipped {
     bool over;
     float term, slope;
 };
-__device__ __forceinline__ Clipped clip_term(const AnswerArgs& a, float adv, float d, float p, float q) {
-    bool high = d > a.thigh.hi, low = d < a.tlow.hi, dual = d > a.tdual.hi;
-    if (d == a.thigh.hi || d == a.tlow.hi || d == a.tdual.hi) {
-        high = side_of(p, q, a.thigh) > 0;
-        low = side_of(p, q, a.tlow) < 0;
-        dual = side_of(p, q, a.tdual) > 0;
+// Bit 0: beyond the border on the side that A's sign names; bit 1: A < 0 and beyond dual_clip.
+__device__ __noinline__ unsigned beyond_exactly(const AnswerArgs& a, bool up, float p, float q) {
+    if (up) return side_of(p, q, a.thigh) > 0;
+    return (side_of(p, q, a.tlow) < 0 ? 1u : 0u) | (side_of(p, q, a.tdual) > 0 ? 2u : 0u);
+}
+// A ratio: ex2.approx is good to 2 units, and rounding the product moves its exponent by 2^-24 |d|, as much
+// as the rounding of d itself; expf is no nearer and costs four times the instructions.
+__device__ __forceinline__ float ratio_of(float d) { return ex2(d * kLog2e); }
+
+// COUNT tokens at a time; one branch for the exact comparisons.
+template <int COUNT>
+__device__ __forceinline__ void clip_terms(const AnswerArgs& a, const float (&adv)[COUNT], const float (&d)[COUNT], const float (&p)[COUNT],
+                                           const float (&q)[COUNT], Clipped (&c)[COUNT]) {
+    bool border = false, dual[COUNT];
+#pragma unroll
+    for (int j = 0; j < COUNT; ++j) {
+        const bool up = adv[j] > 0.f;
+        const float past = up ? d[j] - a.thigh.hi : a.tlow.hi - d[j];
+        c[j].over = past > 0.f;
+        border = border || past == 0.f;
+        dual[j] = false;
     }
-    Clipped c;
-    c.over = adv > 0.f ? high : (adv < 0.f && (low || dual));
-    const float bound = adv > 0.f ? a.high : (low ? a.low : a.dual), r = expf(d);
-    c.term = -adv * (c.over ? bound : r);
-    c.slope = c.over ? 0.f : c.term;
-    return c;
+    if (a.dual > 0.f) {
+#pragma unroll
+        for (int j = 0; j < COUNT; ++j) {
+            dual[j] = !(adv[j] > 0.f) && d[j] > a.tdual.hi;
+            border = border || d[j] == a.tdual.hi;
+        }
+    }
+    if (border) {
+#pragma unroll
+        for (int j = 0; j < COUNT; ++j) {
+            const unsigned b = beyond_exactly(a, adv[j] > 0.f, p[j], q[j]);
+            c[j].over = b & 1;
+            dual[j] = b & 2;
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < COUNT; ++j) {
+        const float r = ratio_of(d[j]), bound = adv[j] > 0.f ? a.high : (c[j].over ? a.low : a.dual);
+        c[j].over = (c[j].over || dual[j]) && adv[j] != 0.f;
+        c[j].term = -adv[j] * (c[j].over ? bound : r);
+        c[j].slope = c[j].over ? 0.f : c[j].term;
+    }
+}
+__device__ __forceinline__ Clipped clip_term(const AnswerArgs& a, float adv, float d) {  // d as it is
+    const float av[1] = {adv}, x[1] = {d}, zero[1] = {0.f};
+    Clipped c[1];
+    clip_terms<1>(a, av, x, x, zero, c);
+    return c[0];
 }
 
-// k and dk/dlogp of y = reference - logp.
-__device__ __forceinline__ float kl_of(const AnswerArgs& a, float y) {
-    return a.kl == TT_KL_1 ? -y : (a.kl == TT_KL_2 ? 0.5f * y * y : exp_less_line(y));
-}
-__device__ __forceinline__ float kl_slope(const AnswerArgs& a, float y) {
-    if (a.kl != TT_KL_3) return a.kl == TT_KL_1 ? 1.f : -y;
-    return fabsf(y) > 1.f ? 1.f - expf(y) : -(exp_less_line(y) + y);  // 1 - exp(y)
+// k (slope: dk/dlogp) of two tokens' y = reference - logp.  The series of two at once.
+__device__ __forceinline__ void kl_two(const AnswerArgs& a, float y0, float y1, bool slope, float& k0, float& k1) {
+    if (a.kl != TT_KL_3) {
+        const bool one = a.kl == TT_KL_1;
+        k0 = one ? (slope ? 1.f : -y0) : (slope ? -y0 : 0.5f * y0 * y0);
+        k1 = one ? (slope ? 1.f : -y1) : (slope ? -y1 : 0.5f * y1 * y1);
+        return;
+    }
+    if (fmaxf(fabsf(y0), fabsf(y1)) <= 1.f) {
+        k0 = k1 = kSeries[0];
+#pragma unroll
+        for (int i = 1; i < kTerms; ++i) fma2(k0, k1, y0, y1, kSeries[i], kSeries[i]);
+        mul2(k0, k1, y0, y1);
+        if (slope) {  // 1 - exp(y) = -y - y^2 (1/2 + ..)
+            fma2(k0, k1, -y0, -y1, -y0, -y1);
+        } else {
+            mul2(k0, k1, y0, y1);
+        }
+    } else {
+        k0 = slope ? one_less_exp(y0) : exp_less_line(y0);
+        k1 = slope ? one_less_exp(y1) : exp_less_line(y1);
+    }
 }
 
-// Four tokens of a piece, the first a multiple of 4.  A piece's tokens are counted from the last
-// multiple of 4 before it, so that all but its first and last four are loaded whole.
+// Four tokens of a piece, the first a multiple of 4 in the arrays.
 struct Four {
     float lp[4], rf[4], od[4], ad[4];
     unsigned keep;  // bit 8 j + 7: token j is in the piece and counts
 };
-struct Span {
-    int64_t first;  // a multiple of 4
-    int b, e, lim;  // the piece, and the end of the arrays, from there
-    __device__ __forceinline__ explicit Span(const AnswerArgs& a, const Piece& p) {
-        first = p.b & ~3ll;
-        b = (int)(p.b - first);
-        e = (int)(p.e - first);
-        lim = (int)min(a.N - first, (int64_t)1 << 20);
-    }
+__device__ __forceinline__ bool kept(const Four& f, int j) { return f.keep & (0x80u << (8 * j)); }
+__device__ __forceinline__ unsigned nonzero_bytes(unsigned m) { return (((m & 0x7F7F7F7Fu) + 0x7F7F7F7Fu) | m) & 0x80808080u; }
+
+// What of the arrays a pass reads.
+struct Reads {
+    bool lp, rf, od, ad;
 };
-__device__ __forceinline__ void load_four(const AnswerArgs& a, const Span& s, int at, bool lp, bool rf, bool od, bool ad, Four& f) {
-    f.keep = 0;
-    if (at >= s.e) return;
-    const int64_t i = s.first + at;
-    unsigned m = 0x01010101u;
-    if (a.vec && at + 4 <= s.lim) {
-        auto get = [&](const float* p, float (&v)[4]) {
-            const float4 x = __ldg(reinterpret_cast<const float4*>(p + i));
-            v[0] = x.x;
-            v[1] = x.y;
-            v[2] = x.z;
-            v[3] = x.w;
-        };
-        if (lp) get(a.logp, f.lp);
-        if (rf) get(a.ref, f.rf);
-        if (od) get(a.old, f.od);
-        if (ad) get(a.adv, f.ad);
-        if (a.mask) m = __ldg(reinterpret_cast<const unsigned*>(a.mask + i));
-    } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (at + j >= s.lim) break;
-            if (lp) f.lp[j] = __ldg(a.logp + i + j);
-            if (rf) f.rf[j] = __ldg(a.ref + i + j);
-            if (od) f.od[j] = __ldg(a.old + i + j);
-            if (ad) f.ad[j] = __ldg(a.adv + i + j);
-            if (a.mask) m = (m & ~(255u << (8 * j))) | (unsigned)__ldg(a.mask + i + j) << (8 * j);
+
+// A group that is whole in the piece, at 16-byte boundaries.
+__device__ __forceinline__ void load_whole(const AnswerArgs& a, int64_t i, Reads r, Four& f) {
+    auto get = [&](const float* p, float (&v)[4]) {
+        const float4 x = __ldg(reinterpret_cast<const float4*>(p + i));
+        v[0] = x.x;
+        v[1] = x.y;
+        v[2] = x.z;
+        v[3] = x.w;
+    };
+    if (r.lp) get(a.logp, f.lp);
+    if (r.rf) get(a.ref, f.rf);
+    if (r.od) get(a.old, f.od);
+    if (r.ad) get(a.adv, f.ad);
+    f.keep = a.mask ? nonzero_bytes(__ldg(reinterpret_cast<const unsigned*>(a.mask + i))) : 0x80808080u;
+}
+// A piece's groups, a lane each at a time: those that are whole with the next one on its way, then the rest.
+// take(f, first token of f)
+template <class Take>
+__device__ __forceinline__ void walk(const AnswerArgs& a, const Piece& p, Reads r, Take take) {
+    const int lane = threadIdx.x & 31;
+    const int64_t from = a.vec ? (p.b + 3) & ~(int64_t)3 : p.e, to = a.vec ? p.e & ~(int64_t)3 : p.e;
+    if (from < to) {
+        const int n = (int)(to - from);
+        int at = lane * 4;
+        Four next;
+        if (at < n) load_whole(a, from + at, r, next);
+#pragma unroll 1
+        for (; at < n; at += 128) {
+            const Four f = next;
+            if (at + 128 < n) load_whole(a, from + at + 128, r, next);
+            take(f, from + at);
         }
     }
-    f.keep = (((m & 0x7F7F7F7Fu) + 0x7F7F7F7Fu) | m) & 0x80808080u;  // bytes that are not 0
-    if (at < s.b) f.keep &= 0x80808080u << (8 * (s.b - at));
-    if (at + 4 > s.e) f.keep &= 0x80808080u >> (8 * (at + 4 - s.e));
+    // groups that are not whole: all where the arrays are not aligned, else the first and the last
+    const int64_t first = p.b & ~(int64_t)3, last = (p.e - 1) & ~(int64_t)3;
+    for (int64_t i = a.vec ? (lane == 0 ? first : last) : first + lane * 4; i <= last; i += a.vec ? p.e : 128) {
+        if (i >= from && i + 4 <= to) break;
+        if (a.vec && (lane > 1 || (lane == 1 && first == last))) break;
+        Four f;
+        f.keep = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int64_t k = i + j;
+            if (k < p.b || k >= p.e) continue;
+            if (r.lp) f.lp[j] = __ldg(a.logp + k);
+            if (r.rf) f.rf[j] = __ldg(a.ref + k);
+            if (r.od) f.od[j] = __ldg(a.old + k);
+            if (r.ad) f.ad[j] = __ldg(a.adv + k);
+            if (!a.mask || __ldg(a.mask + k)) f.keep |= 0x80u << (8 * j);
+        }
+        take(f, i);
+    }
 }
-__device__ __forceinline__ bool kept(const Four& f, int j) { return f.keep & (0x80u << (8 * j)); }
 
 template <bool POLICY>
 __device__ Sums sum_piece(const AnswerArgs& a, const Piece& p) {
-    const int lane = threadIdx.x & 31;
-    Sums s{0., 0., 0., 0, 0};
-    Long la, lb, lc;
+    Sums s;
     if (p.b < p.e) {
         const bool ref = a.ref != nullptr, per_token = POLICY && a.per_token, clip = POLICY && !a.sequence;
         const float seq_adv = POLICY && !a.per_token ? __ldg(a.adv + p.s) : 0.f;
-        const Span span(a, p);
-        for (int base = lane * 4; base - lane * 4 < span.e; base += 256) {
-            Four f[2];
+        walk(a, p, Reads{true, ref, POLICY, per_token}, [&](const Four& f, int64_t) {
+            s.count += __popc(f.keep);
+            float x[4];
+            if constexpr (!POLICY) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) load_four(a, span, base + h * 128, true, ref, POLICY, per_token, f[h]);
-            float fa = 0.f, fb = 0.f, fc = 0.f;
+                for (int j = 0; j < 4; ++j) x[j] = kept(f, j) ? (ref ? f.lp[j] - f.rf[j] : f.lp[j]) : 0.f;
+                s.a.add((x[0] + x[1]) + (x[2] + x[3]));
+            } else {
+                float d[4], adv[4];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                s.count += __popc(f[h].keep);
-                if constexpr (!POLICY) {
+                for (int j = 0; j < 4; ++j) d[j] = f.lp[j] - f.od[j];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) fa += kept(f[h], j) ? (ref ? f[h].lp[j] - f[h].rf[j] : f[h].lp[j]) : 0.f;
-                } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) fc += kept(f[h], j) ? f[h].lp[j] - f[h].od[j] : 0.f;
+                for (int j = 0; j < 4; ++j) x[j] = kept(f, j) ? d[j] : 0.f;
+                s.c.add((x[0] + x[1]) + (x[2] + x[3]));
                 if (clip) {
 #pragma unroll
+                    for (int j = 0; j < 4; ++j) adv[j] = per_token ? f.ad[j] : seq_adv;
+                    Clipped c[4];
+                    clip_terms<4>(a, adv, d, f.lp, f.od, c);
+#pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const Clipped c = clip_term(a, per_token ? f[h].ad[j] : seq_adv, f[h].lp[j] - f[h].od[j], f[h].lp[j], f[h].od[j]);
-                        fa += kept(f[h], j) ? c.term : 0.f;
-                        s.clipped += kept(f[h], j) && c.over;
+                        x[j] = kept(f, j) ? c[j].term : 0.f;
+                        s.clipped += kept(f, j) && c[j].over;
                     }
+                    s.a.add((x[0] + x[1]) + (x[2] + x[3]));
                 }
                 if (ref) {
+                    kl_two(a, f.rf[0] - f.lp[0], f.rf[1] - f.lp[1], false, x[0], x[1]);
+                    kl_two(a, f.rf[2] - f.lp[2], f.rf[3] - f.lp[3], false, x[2], x[3]);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float k = kl_of(a, f[h].rf[j] - f[h].lp[j]);
-                        fb += kept(f[h], j) ? k : 0.f;
-                    }
-                }
+                    for (int j = 0; j < 4; ++j) x[j] = kept(f, j) ? x[j] : 0.f;
+                    s.b.add((x[0] + x[1]) + (x[2] + x[3]));
                 }
             }
-            la.add(fa);
-            if (POLICY) {
-                lb.add(fb);
-                lc.add(fc);
-            }
-        }
+        });
     }
+    __syncwarp();
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
-        la.add_lanes(o);
+        s.a.add_lanes(o);
         if (POLICY) {
-            lb.add_lanes(o);
-            lc.add_lanes(o);
+            s.b.add_lanes(o);
+            s.c.add_lanes(o);
         }
     }
-    s.a = la.value();
-    s.b = lb.value();
-    s.c = lc.value();
     s.count = __reduce_add_sync(0xffffffffu, s.count);
     if (POLICY) s.clipped = __reduce_add_sync(0xffffffffu, s.clipped);
     return s;
 }
 
-// All pieces of COUNT sequences (s, s + apart ..), by a warp; lane 0 has the result.
-template <int COUNT>
-__device__ __forceinline__ void sum_sequences(const AnswerArgs& a, const Sums* part, int64_t s, int64_t apart, Sums (&t)[COUNT]) {
-    const int lane = threadIdx.x & 31;
-    int64_t b[COUNT], e[COUNT];
-#pragma unroll
-    for (int i = 0; i < COUNT; ++i) {
-        b[i] = offset_at(a, s + i * apart);
-        e[i] = offset_at(a, s + i * apart + 1);
+// All pieces of sequence s, by half a warp; each of its lanes has the result.  (Both halves call it.)
+__device__ __forceinline__ Sums sum_sequence(const AnswerArgs& a, const Sums* part, int64_t s) {
+    const int64_t b = offset_at(a, s), e = offset_at(a, s + 1), c0 = b >> a.shift, c1 = e > b ? (e - 1) >> a.shift : c0;
+    Sums t;
+    for (int64_t c = c0 + (threadIdx.x & 15); c <= c1; c += 16) {  // the piece of the sequence in [c K, (c + 1) K)
+        const Sums x = part[c == c0 ? s : a.S + c - 1];
+        t.a.add(x.a);
+        t.b.add(x.b);
+        t.c.add(x.c);
+        t.count += x.count;
+        t.clipped += x.clipped;
     }
-    bool one = true;
 #pragma unroll
-    for (int i = 0; i < COUNT; ++i) {
-        const int64_t c0 = b[i] / a.K, c1 = e[i] > b[i] ? (e[i] - 1) / a.K : c0;
-        t[i] = Sums{0., 0., 0., 0, 0};
-        for (int64_t c = c0 + lane; c <= c1; c += 32) {  // the piece of the sequence in [c K, (c + 1) K)
-            const Sums x = part[c == c0 ? s + i * apart : a.S + c - 1];
-            t[i].a += x.a;
-            t[i].b += x.b;
-            t[i].c += x.c;
-            t[i].count += x.count;
-            t[i].clipped += x.clipped;
-        }
-        one = one && c1 == c0;
+    for (int o = 8; o; o >>= 1) {
+        t.a.add_lanes(o);
+        t.b.add_lanes(o);
+        t.c.add_lanes(o);
+        t.count += __shfl_xor_sync(0xffffffffu, t.count, o);
+        t.clipped += __shfl_xor_sync(0xffffffffu, t.clipped, o);
     }
-    if (one) return;  // lane 0 has them whole, which is the lane that is asked
-#pragma unroll
-    for (int i = 0; i < COUNT; ++i) {
-#pragma unroll
-        for (int o = 16; o; o >>= 1) {
-            t[i].a += __shfl_xor_sync(0xffffffffu, t[i].a, o);
-            t[i].b += __shfl_xor_sync(0xffffffffu, t[i].b, o);
-            t[i].c += __shfl_xor_sync(0xffffffffu, t[i].c, o);
-        }
-        t[i].count = __reduce_add_sync(0xffffffffu, t[i].count);
-        t[i].clipped = __reduce_add_sync(0xffffffffu, t[i].clipped);
-    }
+    return t;
+}
+
+// 1 / n (1 for none) to some 2^-48: a step of Newton's from the fp32 quotient costs two double operations, a division dozens.
+__device__ __forceinline__ double inverse_of(int n) {
+    const double d = n > 0 ? (double)n : 1.0, r = (double)(1.f / (float)(n > 0 ? n : 1));
+    return fma(r, fma(-d, r, 1.0), r);
 }
 
 // dloss/dh of a pair.
@@ -351,37 +411,37 @@ __device__ __forceinline__ float pref_slope(const AnswerArgs& a, float h) {
     return a.smoothing / (1.f + expf(-h)) - (1.f - a.smoothing) / (1.f + expf(h));
 }
 
-// The numbers of pair u (preference) or sequence u (policy), by a warp.
+// The numbers of pair u (preference: a half of the warp for each answer) or of sequences 2 u and 2 u + 1 (policy), by a warp.
 template <bool POLICY>
-__device__ void finish_one(const AnswerArgs& a, const Sums* part, int64_t u) {
-    const bool lead = (threadIdx.x & 31) == 0;
+__device__ void finish_two(const AnswerArgs& a, const Sums* part, int64_t u) {
+    const int half = (threadIdx.x >> 4) & 1;
+    const int64_t s = POLICY ? 2 * u + half : u + half * a.pairs;
+    const Sums t = sum_sequence(a, part, s < a.S ? s : a.S - 1);
+    const bool lead = (threadIdx.x & 15) == 0 && s < a.S;
     if (POLICY) {
-        Sums one[1];
-        sum_sequences<1>(a, part, u, 0, one);
-        const Sums& t = one[0];
         if (!lead) return;
-        const double n = t.count > 0 ? (double)t.count : 1.0, share = a.average ? 1.0 / n : 1.0;
-        const float x = (float)(t.c / n);
-        double term = t.a;
+        const double inverse = inverse_of(t.count), share = a.average ? inverse : 1.0;
+        const float x = (float)(t.c.value() * inverse);
+        double term = t.a.value();
         int over = t.clipped;
         if (a.sequence) {
-            const Clipped c = clip_term(a, a.adv[u], x, x, 0.f);
+            const Clipped c = clip_term(a, a.adv[s], x);
             term = t.count > 0 ? (double)c.term * t.count : 0.0;
             over = c.over ? t.count : 0;
         }
-        const double k = share * t.b;
-        a.log_ratio[u] = x;
-        a.kl_out[u] = (float)k;
-        a.loss[u] = (float)(share * term + (a.kl_weight != 0.f ? a.kl_weight * k : 0.0));
-        a.counts_out[u] = t.count;
-        a.clipped[u] = over;
+        const double k = share * t.b.value();
+        a.log_ratio[s] = x;
+        a.kl_out[s] = (float)k;
+        a.loss[s] = (float)(share * term + (a.kl_weight != 0.f ? a.kl_weight * k : 0.0));
+        a.counts_out[s] = t.count;
+        a.clipped[s] = over;
     } else {
-        Sums two[2];
-        sum_sequences<2>(a, part, u, a.pairs, two);
-        const Sums &c = two[0], &r = two[1];
+        const double mine = a.dbeta * t.a.value() * (a.average ? inverse_of(t.count) : 1.0), other = __shfl_xor_sync(0xffffffffu, mine, 16);
         if (!lead) return;
-        const double rc = a.dbeta * c.a / (a.average && c.count > 0 ? c.count : 1), rr = a.dbeta * r.a / (a.average && r.count > 0 ? r.count : 1);
-        const float h = (float)(rc - rr - a.dmargin);
+        a.rewards[s] = (float)mine;
+        a.counts_out[s] = t.count;
+        if (half) return;
+        const float h = (float)(mine - other - a.dmargin);
         float loss;
         if (a.kind == TT_PREF_SIGMOID) {
             const float soft = log1pf(expf(-fabsf(h)));  // log sigma(h) = min(h, 0) - soft
@@ -396,10 +456,6 @@ __device__ void finish_one(const AnswerArgs& a, const Sums* part, int64_t u) {
         }
         a.loss[u] = loss;
         a.margins[u] = h;
-        a.rewards[u] = (float)rc;
-        a.rewards[a.pairs + u] = (float)rr;
-        a.counts_out[u] = c.count;
-        a.counts_out[a.pairs + u] = r.count;
     }
 }
 
@@ -410,8 +466,8 @@ __device__ __forceinline__ void check_offsets(const AnswerArgs& a, int64_t u) { 
 }
 
 template <bool POLICY>
-__global__ void __launch_bounds__(kAnswerWarps * 32) k_answer_sums(const __grid_constant__ AnswerArgs a) {
-    const int64_t u = (int64_t)blockIdx.x * kAnswerWarps + (threadIdx.x >> 5);
+__global__ void __launch_bounds__(kAnswerWarps * 32, 4) k_answer_sums(const __grid_constant__ AnswerArgs a) {
+    const int64_t u = (int64_t)blockIdx.x * kAnswerWarps + warp_id();
     pdl_launch_dependents();
     if (u >= a.S + a.chunks) return;
     const Sums s = sum_piece<POLICY>(a, piece_of(a, u, false));
@@ -423,16 +479,17 @@ __global__ void __launch_bounds__(kAnswerWarps * 32) k_answer_sums(const __grid_
 
 template <bool POLICY>
 __global__ void __launch_bounds__(kAnswerWarps * 32) k_answer_finish(const __grid_constant__ AnswerArgs a) {
-    const int64_t u = (int64_t)blockIdx.x * kAnswerWarps + (threadIdx.x >> 5);
+    const int64_t u = (int64_t)blockIdx.x * kAnswerWarps + warp_id();
     pdl_wait();
-    if (u < (POLICY ? a.S : a.pairs)) finish_one<POLICY>(a, a.part, u);
+    if (u < (POLICY ? (a.S + 1) / 2 : a.pairs)) finish_two<POLICY>(a, a.part, u);
 }
 
 // A small call: both steps in one block.
 template <bool POLICY>
 __global__ void __launch_bounds__(kOneWarps * 32) k_answer_one(const __grid_constant__ AnswerArgs a) {
-    __shared__ Sums part[kOnePieces];
-    const int warp = threadIdx.x >> 5;
+    __shared__ __align__(16) uint8_t space[kOnePieces * sizeof(Sums)];
+    Sums* part = reinterpret_cast<Sums*>(space);
+    const int warp = warp_id();
     for (int64_t u = warp; u < a.S + a.chunks; u += kOneWarps) {
         const Sums s = sum_piece<POLICY>(a, piece_of(a, u, false));
         if ((threadIdx.x & 31) == 0) {
@@ -441,14 +498,13 @@ __global__ void __launch_bounds__(kOneWarps * 32) k_answer_one(const __grid_cons
         }
     }
     __syncthreads();
-    for (int64_t u = warp; u < (POLICY ? a.S : a.pairs); u += kOneWarps) finish_one<POLICY>(a, part, u);
+    for (int64_t u = warp; u < (POLICY ? (a.S + 1) / 2 : a.pairs); u += kOneWarps) finish_two<POLICY>(a, part, u);
 }
 
 template <bool POLICY>
-__global__ void __launch_bounds__(kAnswerWarps * 32) k_answer_grad(const __grid_constant__ AnswerArgs a) {
-    const int64_t u = (int64_t)blockIdx.x * kAnswerWarps + (threadIdx.x >> 5);
+__global__ void __launch_bounds__(kAnswerWarps * 32, 4) k_answer_grad(const __grid_constant__ AnswerArgs a) {
+    const int64_t u = (int64_t)blockIdx.x * kAnswerWarps + warp_id();
     if (u >= a.S + 1 + a.chunks) return;
-    const int lane = threadIdx.x & 31;
     const Piece p = piece_of(a, u, true);
     if (p.b >= p.e) return;
     const bool in = p.s < a.S;
@@ -460,7 +516,7 @@ __global__ void __launch_bounds__(kAnswerWarps * 32) k_answer_grad(const __grid_
             if (!a.per_token) adv = a.adv[p.s];
             if (a.sequence) {
                 const float x = a.log_ratio_in[p.s];
-                seq_slope = clip_term(a, adv, x, x, 0.f).slope;
+                seq_slope = clip_term(a, adv, x).slope;
             }
         } else {
             const bool chosen = p.s < a.pairs;
@@ -471,47 +527,40 @@ __global__ void __launch_bounds__(kAnswerWarps * 32) k_answer_grad(const __grid_
     }
     const bool kl = POLICY && in && a.ref && a.kl_weight != 0.f, ratio = POLICY && in && !a.sequence;
     const bool per_token = ratio && a.per_token;
-    const Span span(a, p);
-    for (int base = lane * 4; base - lane * 4 < span.e; base += 256) {
-        Four f[2];
+    walk(a, p, Reads{kl || ratio, kl, ratio, per_token}, [&](const Four& f, int64_t at) {
+        float v[4];
+        if (POLICY) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            load_four(a, span, base + h * 128, kl || ratio, kl, ratio, per_token, f[h]);
-            if (!in) f[h].keep = 0;
-        }
+            for (int j = 0; j < 4; ++j) v[j] = seq_slope;
+            if (ratio) {
+                float adv4[4], d[4];
+                Clipped c[4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int at = base + h * 128;
-            if (at >= span.e) continue;
-            float v[4];
-            if (POLICY) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) v[j] = seq_slope;
-                if (ratio) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        v[j] = clip_term(a, per_token ? f[h].ad[j] : adv, f[h].lp[j] - f[h].od[j], f[h].lp[j], f[h].od[j]).slope;
+                for (int j = 0; j < 4; ++j) {
+                    adv4[j] = per_token ? f.ad[j] : adv;
+                    d[j] = f.lp[j] - f.od[j];
                 }
-                if (kl) {
+                clip_terms<4>(a, adv4, d, f.lp, f.od, c);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) v[j] = fmaf(a.kl_weight, kl_slope(a, f[h].rf[j] - f[h].lp[j]), v[j]);
-                }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) v[j] = kept(f[h], j) ? g * v[j] : 0.f;
-            } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) v[j] = kept(f[h], j) ? g : 0.f;
+                for (int j = 0; j < 4; ++j) v[j] = c[j].slope;
             }
-            float* to = a.grad + span.first + at;
-            if (a.vec && at >= span.b && at + 4 <= span.e) {
-                *reinterpret_cast<float4*>(to) = make_float4(v[0], v[1], v[2], v[3]);
-            } else {
+            if (kl) {
+                float k[4];
+                kl_two(a, f.rf[0] - f.lp[0], f.rf[1] - f.lp[1], true, k[0], k[1]);
+                kl_two(a, f.rf[2] - f.lp[2], f.rf[3] - f.lp[3], true, k[2], k[3]);
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (at + j >= span.b && at + j < span.e) to[j] = v[j];
+                for (int j = 0; j < 4; ++j) v[j] = fmaf(a.kl_weight, k[j], v[j]);
             }
         }
-    }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = in && kept(f, j) ? (POLICY ? g * v[j] : g) : 0.f;
+        if (a.vec && at >= p.b && at + 4 <= p.e) {
+            *reinterpret_cast<float4*>(a.grad + at) = make_float4(v[0], v[1], v[2], v[3]);
+        } else {
+            for (int j = 0; j < 4; ++j)
+                if (at + j >= p.b && at + j < p.e) a.grad[at + j] = v[j];
+        }
+    });
 }
 
 namespace {
@@ -520,13 +569,16 @@ tt_status answer_sizes(int64_t tokens, int64_t sequences) {
     return tokens < 0 || sequences < 0 || tokens > TT_ANSWERS_MAX_TOKENS || sequences > TT_ANSWERS_MAX_SEQUENCES ? TT_ERR_SHAPE : TT_OK;
 }
 
-// Tokens of a piece: short ones while there are few for the device, to spread; long ones cost
+// log2 of the tokens of a piece: short ones while there are few for the device, to spread; long ones cost
 // fewer sums to write and join.
-int piece_tokens(int64_t tokens) {
+int piece_shift(int64_t tokens) {
     int k = kPieceMin;
-    while (k < kPieceMax && tokens / k > 8192) k *= 2;
+    while (k < kPieceMax && tokens >> k > 8192) ++k;
     return k;
 }
+
+// One launch, and no workspace, while a single block's reading costs less than a second launch.
+bool in_one_block(int64_t tokens, int64_t pieces) { return tokens <= kOneTokens && pieces <= kOnePieces; }
 
 tt_status fill_answers(const tt_answers* in, AnswerArgs* a) {
     if (!in) return TT_ERR_ARG;
@@ -541,8 +593,8 @@ tt_status fill_answers(const tt_answers* in, AnswerArgs* a) {
     a->N = in->tokens;
     a->S = in->sequences;
     a->len = in->sequences ? in->tokens / in->sequences : 0;
-    a->K = piece_tokens(in->tokens);
-    a->chunks = in->tokens > 0 ? (in->tokens - 1) / a->K : 0;
+    a->shift = piece_shift(in->tokens);
+    a->chunks = in->tokens > 0 ? (in->tokens - 1) >> a->shift : 0;
     a->average = in->average != 0;
     if (!a->off && a->len > 0x7FFFFFFF) return TT_ERR_SHAPE;  // counts are int32
     return TT_OK;
@@ -602,16 +654,16 @@ template <bool POLICY>
 tt_status run_forward(AnswerArgs a, void* ws, size_t bytes, cudaStream_t st) {
     if (a.S == 0) return TT_OK;
     const int64_t pieces = a.S + a.chunks;
-    if ((int64_t)bytes < pieces * kSumsBytes || !ws || !aligned(ws, 256)) return TT_ERR_ARG;
+    const bool one = in_one_block(a.N, pieces);
+    if (!aligned(ws, 256) || (!one && (!ws || (int64_t)bytes < pieces * kSumsBytes))) return TT_ERR_ARG;
     if (head_sms() <= 0) return TT_ERR_CUDA;
     a.part = static_cast<Sums*>(ws);
     a.vec = all_aligned(a);
-    // one launch while a single block's reading costs less than a second launch
-    if (a.N <= kOneTokens && pieces <= kOnePieces) {
+    if (one) {
         k_answer_one<POLICY><<<1, kOneWarps * 32, 0, st>>>(a);
     } else {
         k_answer_sums<POLICY><<<(unsigned)((pieces + kAnswerWarps - 1) / kAnswerWarps), kAnswerWarps * 32, 0, st>>>(a);
-        const int64_t out = POLICY ? a.S : a.pairs;
+        const int64_t out = POLICY ? (a.S + 1) / 2 : a.pairs;
         if (!launch_ahead(k_answer_finish<POLICY>, dim3((unsigned)((out + kAnswerWarps - 1) / kAnswerWarps)), kAnswerWarps * 32, 0, st, a)) return TT_ERR_CUDA;
     }
     return cudaGetLastError() == cudaSuccess ? TT_OK : TT_ERR_CUDA;
@@ -636,8 +688,8 @@ extern "C" {
 
 int64_t tt_emb_answers_workspace(int64_t tokens, int64_t sequences) {
     if (answer_sizes(tokens, sequences) != TT_OK) return -1;
-    const int64_t pieces = sequences + (tokens > 0 ? (tokens - 1) / piece_tokens(tokens) : 0);
-    return (pieces * kSumsBytes + 255) / 256 * 256;
+    const int64_t pieces = sequences + (tokens > 0 ? (tokens - 1) >> piece_shift(tokens) : 0);
+    return in_one_block(tokens, pieces) ? 0 : (pieces * kSumsBytes + 255) / 256 * 256;
 }
 
 tt_status tt_emb_preference_forward(const tt_answers* answers, const tt_preference* how, float* loss_dev, float* margins_dev, float* rewards_dev,

@@ -140,12 +140,13 @@ def _current(stream, device):
 
 
 _here = contextlib.nullcontext()
+_device_now = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)  # of tensors that are there: CUDA is up
 
 
 def _on(stream, device):
     """The call's stream and device are current: what it allocates belongs to that stream, and what it copies of its
     arguments is copied there, before its kernels and with memory that no other stream takes meanwhile."""
-    return _here if stream is None and device.index == torch.cuda.current_device() else _current(stream, device)
+    return _here if stream is None and device.index == _device_now() else _current(stream, device)
 
 
 def tt_emb_head_workspace(hidden: torch.Tensor, weight: torch.Tensor, teacher_k: int = 1, backward: bool = False) -> int:

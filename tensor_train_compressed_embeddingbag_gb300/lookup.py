@@ -91,10 +91,10 @@ def tt_emb_lookup_backward(grad_out: torch.Tensor, ids: torch.Tensor, vocab: int
             _refuse(TT_ERR_ARG, "grad_weight must have grad_out's type and device")
         elif out.shape != (vocab, dim) or (dim > 1 and out.stride(1) != 1) or (vocab > 1 and out.stride(0) < dim):
             _refuse(TT_ERR_SHAPE, f"grad_weight must be [{vocab}, {dim}] with contiguous rows that do not overlap")
-        ws = torch.empty(n, dtype=torch.uint8, device=device)
+        ws = torch.empty(n, dtype=torch.uint8, device=device) if n else None
         a = _Lookup(None, dim, ids.data_ptr(), rows, vocab, int(padding_idx), dim, _DTYPES[g.dtype], scale)
         st = _c("tt_emb_lookup_backward")(ctypes.byref(a), g.data_ptr(), _row_stride(g), out.data_ptr(), _row_stride(out),
-                                          int(grad_weight is not None), _err_word(err, device), ws.data_ptr(), n, _stream_now(device.index))
+                                          int(grad_weight is not None), _err_word(err, device), ws.data_ptr() if n else None, n, _stream_now(device.index))
         if st:
             _check(st, "tt_emb_lookup_backward")
     return out

@@ -3,7 +3,8 @@
 Error bounds, e = 2^-24 a rounding of fp32.
   d, y       differences of two fp32 numbers: e |d|
   sums       eight terms at a time in fp32, then double: 8 e sum |terms|, plus the terms' errors
-  exp        2 units (2^-22 of itself), and what an error of its argument makes of it
+  exp        2 units (2^-22 of itself), and what an error of its argument makes of it; the ratio's: that of
+             the difference, and e |x| of rounding x log2(e) (x log2(e) 2^-24 in the exponent of 2 is x 2^-24 in that of e)
   others     a few fp32 operations on numbers of one size: 2^-21 of it
 """
 import math
@@ -99,7 +100,7 @@ def policy(logp, old, adv, reference, mask, offsets, clip, dual_clip, kl, kl_wei
         over, bound = over | twice, torch.where(twice, torch.full_like(bound, dual_clip), bound)
     ratio = torch.exp(x)
     term = -a * torch.where(over, bound, ratio)
-    et = term.abs() * (torch.where(over, torch.zeros_like(ex), ex) + 2.0 ** -22)
+    et = term.abs() * (torch.where(over, torch.zeros_like(ex), ex + E * x.abs()) + 2.0 ** -22)
     slope, eslope = torch.where(over, torch.zeros_like(term), term), torch.where(over, torch.zeros_like(et), et)
     k, kslope, ek, ekslope = (torch.zeros_like(lp) for _ in range(4))
     if reference is not None:

@@ -96,7 +96,8 @@ def test_answers(lib):
         for i in range(many):
             assert call(lib, out=tuple(None if j == i else 4096 for j in range(many))) == tt.TT_ERR_ARG
             assert call(lib, out=tuple(4098 if j == i else 4096 for j in range(many))) == tt.TT_ERR_ARG
-        for bad in (dict(logp_dev=None), dict(logp_dev=4098), dict(reference_dev=4098), dict(ws=None), dict(ws=4096 + 128), dict(n=16)):
+        for bad in (dict(logp_dev=None), dict(logp_dev=4098), dict(reference_dev=4098), dict(ws=4096 + 128), dict(tokens=40000, ws=None),
+                    dict(tokens=40000, n=16)):
             assert call(lib, **bad) == tt.TT_ERR_ARG, bad
         assert call(lib, tokens=0, sequences=0, out=(None,) * many, ws=None, n=0) == tt.TT_OK
     for call in (_preference_backward, _policy_backward):
