@@ -13,7 +13,7 @@
 //
 // The sort is a radix sort by counting (digits of up to 11 bits): per chunk of kSortChunk
 // positions a histogram, scanned over the chunks of a digit by a warp, and a scatter by ranks
-// within the chunk (match masks per warp).  The scatter counts the next digit's histogram.
+// within the chunk (votes per warp).  The scatter counts the next digit's histogram.
 //
 // Few lookups are not sorted: a block per lookup and column slice looks through all ids,
 // leaves if an earlier lookup has the same, and else sums those that have it: one launch.
@@ -27,8 +27,9 @@ constexpr int kLkThreads = 256;
 constexpr int kLkRows = 4;             // rows of a thread in the forward pass
 constexpr int kSmallRows = 1024;       // lookups that are not sorted
 constexpr int kSortChunk = 2048;
-constexpr int kSortBlock = 256;
+constexpr int kSortBlock = 512;
 constexpr int kSortW = kSortBlock / 32;
+constexpr int kFoldChunks = 32;        // up to so many chunks a scatter sums the histograms itself
 constexpr int kDigitBits = 11;
 constexpr int kMaxPasses = 3;
 constexpr int kZeroRows = 2048;        // most table rows of a block that writes zeros
@@ -53,6 +54,7 @@ struct LookupArgs {
     int64_t chunks;
     int64_t sum_blocks;  // then blocks that write zeros
     int zero_rows;       // table rows of one of these
+    int64_t zero_first;  // the first row that the sort's launches have left to them
     int slices;          // column slices of `lanes` units
     const uint32_t* keys;  // [m] sorted ids
     const uint32_t* pos;   // [m] their positions
@@ -97,11 +99,40 @@ __global__ void __launch_bounds__(kLkThreads) k_lookup(const __grid_constant__ L
 
 // ---------------------------------------------------------------- sort by id
 
+// Rows of the gradient that a launch of the sort writes with zeros beside its own work: the sort is a chain of short
+// launches that leave most of the device idle, and zeros need no sorted ids.  Rows that are named are
+// written again by the sums.
+struct ZeroRows {
+    uint8_t* out;
+    int64_t row_bytes, pitch;  // of a row, and from row to row
+    int64_t rows;              // [0, rows)
+    int vec;                   // rows are 16-byte units
+};
+__device__ void write_zeros(const ZeroRows& z, int block, int blocks) {
+    const int64_t thread = (int64_t)block * blockDim.x + threadIdx.x, threads = (int64_t)blocks * blockDim.x;
+    if (z.vec && z.row_bytes == z.pitch) {
+        uint4* p = reinterpret_cast<uint4*>(z.out);
+        const int64_t n = z.rows * (z.row_bytes / 16);
+#pragma unroll 8
+        for (int64_t i = thread; i < n; i += threads) p[i] = make_uint4(0, 0, 0, 0);
+        return;
+    }
+    const int warps = blockDim.x / 32;
+    for (int64_t r = (int64_t)block * warps + (threadIdx.x >> 5); r < z.rows; r += (int64_t)blocks * warps) {
+        uint8_t* p = z.out + r * z.pitch;
+        if (z.vec) {
+            for (int64_t i = threadIdx.x & 31; i < z.row_bytes / 16; i += 32) reinterpret_cast<uint4*>(p)[i] = make_uint4(0, 0, 0, 0);
+        } else {
+            for (int64_t i = threadIdx.x & 31; i < z.row_bytes / 2; i += 32) reinterpret_cast<uint16_t*>(p)[i] = 0;
+        }
+    }
+}
+
 struct SortArgs {
     const int64_t* ids;
     int64_t N, V, pad;
     int nch, passes, bits[kMaxPasses], bins[kMaxPasses];
-    int* H[kMaxPasses];      // [bins][nch], after its scan the sum over earlier chunks
+    int* H[kMaxPasses];      // [nch][bins], after its scan the sum over earlier chunks
     int* total[kMaxPasses];  // [bins]
     uint32_t* keys[2];
     uint32_t* pos[2];
@@ -109,54 +140,74 @@ struct SortArgs {
     int* err;
 };
 
-__device__ __forceinline__ int64_t key_of(const SortArgs& a, int64_t n) {  // -1: does not count
-    const int64_t id = a.ids[n];
+__device__ __forceinline__ int64_t key_of(const SortArgs& a, int64_t id) {  // -1: does not count
     return id < 0 || id >= a.V || id == a.pad ? -1 : id;
 }
 
-__global__ void __launch_bounds__(kSortBlock) k_lookup_hist(const __grid_constant__ SortArgs a) {
+__global__ void __launch_bounds__(kSortBlock) k_lookup_hist(const __grid_constant__ SortArgs a, const __grid_constant__ ZeroRows z) {
     extern __shared__ int bins_s[];
     const int c = blockIdx.x;
+    pdl_launch_dependents();
+    if (c >= a.nch) {
+        write_zeros(z, c - a.nch, gridDim.x - a.nch);
+        return;
+    }
+    const int64_t lo = (int64_t)c * kSortChunk;
+    int64_t id[kSortChunk / kSortBlock];
+#pragma unroll
+    for (int i = 0; i < kSortChunk / kSortBlock; ++i) {
+        const int64_t n = lo + i * kSortBlock + threadIdx.x;
+        id[i] = n < a.N ? a.ids[n] : a.pad;
+    }
     for (int i = threadIdx.x; i < a.bins[0]; i += kSortBlock) bins_s[i] = 0;
     for (int p = 1; p < a.passes; ++p)  // counted by the scatter before
         for (int64_t i = (int64_t)c * kSortBlock + threadIdx.x; i < (int64_t)a.bins[p] * a.nch; i += (int64_t)a.nch * kSortBlock) a.H[p][i] = 0;
     __syncthreads();
-    const int64_t lo = (int64_t)c * kSortChunk;
 #pragma unroll
     for (int i = 0; i < kSortChunk / kSortBlock; ++i) {
         const int64_t n = lo + i * kSortBlock + threadIdx.x;
         if (n >= a.N) break;
-        const int64_t k = key_of(a, n);
+        const int64_t k = key_of(a, id[i]);
         if (k >= 0)
             atomicAdd(&bins_s[(int)k & (a.bins[0] - 1)], 1);
-        else if (a.err && (a.ids[n] < 0 || a.ids[n] >= a.V))
+        else if (a.err && (id[i] < 0 || id[i] >= a.V))
             atomicOr(a.err, kErrIndex);
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < a.bins[0]; i += kSortBlock) a.H[0][(int64_t)i * a.nch + c] = bins_s[i];
+    for (int i = threadIdx.x; i < a.bins[0]; i += kSortBlock) a.H[0][(int64_t)c * a.bins[0] + i] = bins_s[i];
 }
 
-// A warp per digit: sums over earlier chunks, and over all.
+// Sums over earlier chunks, and over all, of 32 digits: a digit to a lane, equal runs of chunks to the warps.
 __global__ void __launch_bounds__(kSortBlock) k_lookup_scan(const __grid_constant__ SortArgs a, int p) {
-    const int b = blockIdx.x * kSortW + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (b >= a.bins[p]) return;
-    int* h = a.H[p] + (int64_t)b * a.nch;
-    int carry = 0;
-    for (int c0 = 0; c0 < a.nch; c0 += 32) {
-        const int c = c0 + lane, v = c < a.nch ? h[c] : 0;
-        int s = v;
+    __shared__ int run_s[kSortW][32];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, b = blockIdx.x * 32 + lane, bins = a.bins[p];
+    pdl_entry();
+    const bool in = b < bins;
+    const int from = (int)((int64_t)a.nch * w / kSortW), to = (int)((int64_t)a.nch * (w + 1) / kSortW);
+    int* h = a.H[p] + (in ? b : 0);
+    int sum = 0;
+#pragma unroll 8
+    for (int c = from; c < to; ++c) sum += h[(int64_t)c * bins];
+    run_s[w][lane] = sum;
+    __syncthreads();
+    int before = 0, all = 0;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int x = __shfl_up_sync(0xffffffffu, s, o);
-            if (lane >= o) s += x;
-        }
-        if (c < a.nch) h[c] = carry + s - v;
-        carry += __shfl_sync(0xffffffffu, s, 31);
+    for (int i = 0; i < kSortW; ++i) {
+        before += i < w ? run_s[i][lane] : 0;
+        all += run_s[i][lane];
     }
-    if (lane == 0) a.total[p][b] = carry;
+    if (!in) return;
+#pragma unroll 8
+    for (int c = from; c < to; ++c) {
+        const int v = h[(int64_t)c * bins];
+        h[(int64_t)c * bins] = before;
+        before += v;
+    }
+    if (w == 0) a.total[p][b] = all;
 }
 
-// Exclusive scan of x over the block's threads; *total: the sum.
+// Exclusive scan of x over the block's WARPS warps; *total: the sum.
+template <int WARPS>
 __device__ __forceinline__ int block_scan(int x, int* sh, int* total) {
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     int s = x;
@@ -170,7 +221,7 @@ __device__ __forceinline__ int block_scan(int x, int* sh, int* total) {
     __syncthreads();
     int before = 0, all = 0;
 #pragma unroll
-    for (int i = 0; i < kSortW; ++i) {
+    for (int i = 0; i < WARPS; ++i) {
         before += i < w ? sh[i] : 0;
         all += sh[i];
     }
@@ -178,90 +229,165 @@ __device__ __forceinline__ int block_scan(int x, int* sh, int* total) {
     return before + s - x;
 }
 
-__global__ void __launch_bounds__(kSortBlock) k_lookup_scatter(const __grid_constant__ SortArgs a, int p) {
+__global__ void __launch_bounds__(kSortBlock) k_lookup_scatter(const __grid_constant__ SortArgs a, const __grid_constant__ ZeroRows z, int p) {
     extern __shared__ int sm[];
     __shared__ int sh[kSortW];
     const int bins = a.bins[p], c = blockIdx.x, lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    int* base = sm;             // [bins]
-    int* cnt = sm + bins;       // [kSortW][bins]
+    pdl_launch_dependents();
+    if (c >= a.nch) {
+        write_zeros(z, c - a.nch, gridDim.x - a.nch);
+        return;
+    }
+    int* base = sm;                                                // [bins]
+    uint16_t* cnt = reinterpret_cast<uint16_t*>(sm + bins);        // [kSortW][bins], at most kSortChunk each
+    uint32_t* cnt2 = reinterpret_cast<uint32_t*>(cnt);             // two bins at a time
+    for (int i = threadIdx.x; i < kSortW * bins / 2; i += kSortBlock) cnt2[i] = 0;
     int shift = 0;
     for (int i = 0; i < p; ++i) shift += a.bits[i];
-    const int64_t count = p == 0 ? a.N : *a.m;
     const int64_t lo = (int64_t)c * kSortChunk;
-    // where the digits begin
-    int carry = 0;
-    for (int b0 = 0; b0 < bins; b0 += kSortBlock) {
-        const int b = b0 + threadIdx.x, t = b < bins ? a.total[p][b] : 0;
-        int all;
-        const int before = block_scan(t, sh, &all);
-        if (b < bins) base[b] = carry + before + a.H[p][(int64_t)b * a.nch + c];
-        carry += all;
-    }
-    if (p == 0 && c == 0 && threadIdx.x == 0) *a.m = carry;
-    if (lo >= count) return;
-    for (int i = threadIdx.x; i < kSortW * bins; i += kSortBlock) cnt[i] = 0;
-    __syncthreads();
-    // a warp's positions are consecutive: 8 x 32
+    // a warp's positions are consecutive: 4 x 32
     constexpr int kPer = kSortChunk / kSortBlock;
     uint32_t key[kPer], at[kPer];
     int digit[kPer], rank[kPer];
-    int* mine = cnt + w * bins;
+    uint16_t* mine = cnt + w * bins;
     const int64_t first = lo + w * (kSortChunk / kSortW);
+    if (p == 0) {  // the ids need no wait
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int64_t n = first + i * 32 + lane;
-        digit[i] = -1;
-        key[i] = at[i] = 0;
-        if (n < count) {
-            if (p == 0) {
-                const int64_t k = key_of(a, n);
-                key[i] = (uint32_t)k;
-                at[i] = (uint32_t)n;
-                digit[i] = k >= 0 ? (int)k & (bins - 1) : -1;
-            } else {
+        for (int i = 0; i < kPer; ++i) {
+            const int64_t n = first + i * 32 + lane, k = n < a.N ? key_of(a, a.ids[n]) : -1;
+            key[i] = (uint32_t)k;
+            at[i] = (uint32_t)n;
+            digit[i] = k >= 0 ? (int)k & (bins - 1) : -1;
+        }
+    }
+    pdl_wait();
+    if (p > 0) {
+        const int64_t count = *a.m;
+        if (lo >= count) return;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int64_t n = first + i * 32 + lane;
+            digit[i] = -1;
+            key[i] = at[i] = 0;
+            if (n < count) {
                 key[i] = a.keys[(p - 1) & 1][n];
                 at[i] = a.pos[(p - 1) & 1][n];
                 digit[i] = (int)(key[i] >> shift) & (bins - 1);
             }
         }
     }
+    // where the digits begin: consecutive ones to a thread
+    constexpr int kMost = (1 << kDigitBits) / kSortBlock;
+    const int each = (bins + kSortBlock - 1) / kSortBlock;
+    int begin[kMost], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) {
+        const int b = threadIdx.x * each + i;
+        int all = 0, before = 0;
+        if (i < each && b < bins) {
+            const int* h = a.H[p] + b;
+            if (a.nch <= kFoldChunks) {
+#pragma unroll 32
+                for (int k = 0; k < a.nch; ++k) {
+                    const int v = h[k * bins];
+                    all += v;
+                    before += k < c ? v : 0;
+                }
+            } else {
+                all = a.total[p][b];
+                before = h[(int64_t)c * bins];
+            }
+        }
+        begin[i] = sum + before;
+        sum += all;
+    }
+    int carry;
+    const int thread_begin = block_scan<kSortW>(sum, sh, &carry);
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) {
+        const int b = threadIdx.x * each + i;
+        if (i < each && b < bins) base[b] = thread_begin + begin[i];
+    }
+    if (p == 0 && c == 0 && threadIdx.x == 0) *a.m = carry;
+    unsigned peers[kPer];  // lanes with the same digit
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) peers[i] = __ballot_sync(0xffffffffu, digit[i] >= 0);
+    for (int bit = 1; bit < bins; bit *= 2) {  // a vote for each bit costs a fraction of a match
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const unsigned with = __ballot_sync(0xffffffffu, digit[i] & bit);
+            peers[i] &= digit[i] & bit ? with : ~with;
+        }
+    }
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-        const unsigned m = __match_any_sync(0xffffffffu, digit[i]);
-        const int leader = __ffs(m) - 1;
+        const unsigned m = peers[i];
+        const int leader = digit[i] >= 0 ? __ffs(m) - 1 : lane;
         int before = 0;
         if (digit[i] >= 0 && lane == leader) {
             before = mine[digit[i]];
-            mine[digit[i]] = before + __popc(m);
+            mine[digit[i]] = (uint16_t)(before + __popc(m));
         }
         rank[i] = __shfl_sync(0xffffffffu, before, leader) + __popc(m & lanemask_lt());
         __syncwarp();
     }
     __syncthreads();
-    for (int b = threadIdx.x; b < bins; b += kSortBlock) {
-        int run = base[b];
+    for (int b = threadIdx.x; b < bins / 2; b += kSortBlock) {  // sums over earlier warps: no carry from bin to bin
+        uint32_t run = 0;
 #pragma unroll
         for (int i = 0; i < kSortW; ++i) {
-            const int v = cnt[i * bins + b];
-            cnt[i * bins + b] = run;
+            const uint32_t v = cnt2[i * (bins / 2) + b];
+            cnt2[i * (bins / 2) + b] = run;
             run += v;
         }
     }
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-        if (digit[i] < 0) continue;
-        const int to = mine[digit[i]] + rank[i];
-        a.keys[p & 1][to] = key[i];
-        a.pos[p & 1][to] = at[i];
+        const bool in = digit[i] >= 0;
+        const int to = in ? base[digit[i]] + mine[digit[i]] + rank[i] : 0;
+        if (in) {
+            a.keys[p & 1][to] = key[i];
+            a.pos[p & 1][to] = at[i];
+        }
         if (p + 1 < a.passes) {
-            const int next = (int)(key[i] >> (shift + a.bits[p])) & (a.bins[p + 1] - 1);
-            atomicAdd(&a.H[p + 1][(int64_t)next * a.nch + to / kSortChunk], 1);
+            // one addition for a popular id's lookups: those that go to one count with the digit's first
+            const int64_t next = (int64_t)(to / kSortChunk) * a.bins[p + 1] + ((key[i] >> (shift + a.bits[p])) & (a.bins[p + 1] - 1));
+            const int leader = in ? __ffs(peers[i]) - 1 : lane;
+            const bool follows = __shfl_sync(0xffffffffu, (int)next, leader) == (int)next;
+            const unsigned same = __ballot_sync(0xffffffffu, follows) & peers[i];
+            if (in && (lane == leader || !follows)) atomicAdd(&a.H[p + 1][next], lane == leader ? __popc(same) : 1);
         }
     }
 }
 
 // ---------------------------------------------------------------- sums
+
+// A unit of a row of partial sums.
+template <int VEC>
+__device__ __forceinline__ void put_part(float* to, const float (&v)[VEC]) {
+    if constexpr (VEC == 1) {
+        *to = v[0];
+    } else {
+#pragma unroll
+        for (int q = 0; q < VEC; q += 4) *reinterpret_cast<float4*>(to + q) = make_float4(v[q], v[q + 1], v[q + 2], v[q + 3]);
+    }
+}
+template <int VEC>
+__device__ __forceinline__ void add_part(const float* from, float (&v)[VEC]) {
+    if constexpr (VEC == 1) {
+        v[0] += *from;
+    } else {
+#pragma unroll
+        for (int q = 0; q < VEC; q += 4) {
+            const float4 x = *reinterpret_cast<const float4*>(from + q);
+            v[q] += x.x;
+            v[q + 1] += x.y;
+            v[q + 2] += x.z;
+            v[q + 3] += x.w;
+        }
+    }
+}
 
 // scale * v to a row of the gradient, or added to it.
 template <class T, int VEC>
@@ -309,11 +435,12 @@ __device__ void zero_rows(const LookupArgs& a, const uint8_t* named, int64_t r0,
 template <class T, int VEC>
 __global__ void __launch_bounds__(kLkThreads) k_lookup_sums(const __grid_constant__ LookupArgs a) {
     __shared__ uint32_t keys_s[kChunkSlots], pos_s[kChunkSlots];
+    pdl_entry();
     const int m = *a.m;
     if (blockIdx.x >= a.sum_blocks) {
         uint8_t* named = reinterpret_cast<uint8_t*>(keys_s);
         int* range = reinterpret_cast<int*>(pos_s);
-        const int64_t r0 = (blockIdx.x - a.sum_blocks) * a.zero_rows;
+        const int64_t r0 = a.zero_first + (blockIdx.x - a.sum_blocks) * a.zero_rows;
         const int rows = (int)min((int64_t)a.zero_rows, a.V - r0);
         for (int r = threadIdx.x; r < rows; r += kLkThreads) named[r] = 0;
         const int w = threadIdx.x >> 5;
@@ -363,8 +490,7 @@ __global__ void __launch_bounds__(kLkThreads) k_lookup_sums(const __grid_constan
                 if (whole) {
                     put_unit<T, VEC>(a, cur, u, acc);
                 } else {
-#pragma unroll
-                    for (int q = 0; q < VEC; ++q) a.head[j * a.D + u * VEC + q] = acc[q];
+                    put_part<VEC>(a.head + j * a.D + u * VEC, acc);
                 }
 #pragma unroll
                 for (int q = 0; q < VEC; ++q) acc[q] = 0.f;
@@ -380,52 +506,50 @@ __global__ void __launch_bounds__(kLkThreads) k_lookup_sums(const __grid_constan
     if (whole && !goes_on) {
         put_unit<T, VEC>(a, cur, u, acc);
     } else {
-        float* to = (whole ? a.tail : a.head) + j * a.D + u * VEC;
-#pragma unroll
-        for (int q = 0; q < VEC; ++q) to[q] = acc[q];
+        put_part<VEC>((whole ? a.tail : a.head) + j * a.D + u * VEC, acc);
     }
 }
 
-// The id that begins in chunk j and goes on: its partial sums, in order.  A block per chunk and
-// slice of 32 units; its 8 warps take the partial sums in turn.
+// The id that begins in chunk j and goes on: its partial sums, in order.  A block per chunk and slice of
+// `lanes` units; where these leave threads, they take the partial sums in turn.
 template <class T, int VEC>
 __global__ void __launch_bounds__(kLkThreads) k_lookup_join(const __grid_constant__ LookupArgs a) {
-    __shared__ float part[kLkThreads / 32][32 * VEC];
-    __shared__ int last_s;
-    const int m = *a.m, w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int slices = (a.units + 31) / 32;
-    const int64_t j = blockIdx.x / slices;
-    const int u = (int)(blockIdx.x - j * slices) * 32 + lane;
+    __shared__ float part[kLkThreads * VEC];
+    const int lane = threadIdx.x & (a.lanes - 1), sub = threadIdx.x / a.lanes, per = kLkThreads / a.lanes;
+    const int64_t j = blockIdx.x / a.slices;
+    const int u = (int)(blockIdx.x - j * a.slices) * a.lanes + lane;
     const int64_t b = j * a.R, e = b + a.R;
+    pdl_entry();
+    const int64_t m = *a.m;
     if (e >= m) return;
-    const uint32_t key = a.keys[e - 1];
-    if (a.keys[e] != key || (b > 0 && a.keys[b - 1] == key)) return;
-    if (w == 0) {
-        const int end = first_not_below(a.keys, m, key + 1);
-        if (lane == 0) last_s = (end - 1) / a.R;  // the last chunk that has it
+    const uint32_t key = a.keys[e - 1], after = a.keys[e], before = b > 0 ? a.keys[b - 1] : ~0u;  // ids are below 2^30
+    if (after != key || before == key) return;
+    int64_t last = j + 1;  // the last chunk that has it: those whose first position has it
+    for (bool more = true; more;) {
+        const int64_t at = (last + 1 + (threadIdx.x & 31)) * a.R;
+        const unsigned has = __ballot_sync(0xffffffffu, at < m && a.keys[at < m ? at : 0] == key);
+        last += __popc(has);
+        more = has == 0xffffffffu;
     }
-    __syncthreads();
-    const int64_t last = last_s;
     float s[VEC];
 #pragma unroll
     for (int q = 0; q < VEC; ++q) s[q] = 0.f;
     if (u < a.units) {
+        if (sub == 0) add_part<VEC>(a.tail + j * a.D + u * VEC, s);
+        const float* from = a.head + (int64_t)u * VEC;
 #pragma unroll 4
-        for (int64_t c = j + w; c <= last; c += kLkThreads / 32) {
-            const float* from = (c == j ? a.tail : a.head) + c * a.D + u * VEC;
-#pragma unroll
-            for (int q = 0; q < VEC; ++q) s[q] += from[q];
-        }
+        for (int64_t c = j + (sub ? sub : per); c <= last; c += per) add_part<VEC>(from + c * a.D, s);
     }
+    if (per > 1) {
 #pragma unroll
-    for (int q = 0; q < VEC; ++q) part[w][q * 32 + lane] = s[q];
-    __syncthreads();
-    if (w > 0 || u >= a.units) return;
+        for (int q = 0; q < VEC; ++q) part[q * kLkThreads + threadIdx.x] = s[q];
+        __syncthreads();
+        if (sub > 0) return;
+        for (int i = 1; i < per && j + i <= last; ++i)
 #pragma unroll
-    for (int q = 0; q < VEC; ++q)
-#pragma unroll
-        for (int i = 1; i < kLkThreads / 32; ++i) s[q] += part[i][q * 32 + lane];
-    put_unit<T, VEC>(a, key, u, s);
+            for (int q = 0; q < VEC; ++q) s[q] += part[q * kLkThreads + i * a.lanes + lane];
+    }
+    if (u < a.units) put_unit<T, VEC>(a, key, u, s);
 }
 
 // Few lookups: a block per lookup and slice of `lanes` units, then blocks that write zeros.
@@ -437,7 +561,7 @@ __global__ void __launch_bounds__(kLkThreads) k_lookup_few(const __grid_constant
         uint8_t named[kZeroRows];
         float part[kLkThreads * 8];
     } s;
-    __shared__ int sh[kSortW];
+    __shared__ int sh[kLkThreads / 32];
     const int N = (int)a.N;
     for (int n = threadIdx.x; n < N; n += kLkThreads) {
         const int64_t id = a.ids[n];
@@ -447,7 +571,7 @@ __global__ void __launch_bounds__(kLkThreads) k_lookup_few(const __grid_constant
     }
     __syncthreads();
     if (blockIdx.x >= a.sum_blocks) {
-        const int64_t r0 = (blockIdx.x - a.sum_blocks) * a.zero_rows;
+        const int64_t r0 = (blockIdx.x - a.sum_blocks) * a.zero_rows;  // (zero_first is 0)
         const int rows = (int)min((int64_t)a.zero_rows, a.V - r0);
         for (int r = threadIdx.x; r < rows; r += kLkThreads) s.named[r] = 0;
         __syncthreads();
@@ -476,7 +600,7 @@ __global__ void __launch_bounds__(kLkThreads) k_lookup_few(const __grid_constant
     }
     if (__syncthreads_or(earlier)) return;
     int count;
-    const int at = block_scan(found, sh, &count);
+    const int at = block_scan<kLkThreads / 32>(found, sh, &count);
     for (int i = 0; i < found; ++i) s.list[at + i] = mine[i];
     __syncthreads();
     const int lane = threadIdx.x & (a.lanes - 1), sub = threadIdx.x / a.lanes, per = kLkThreads / a.lanes;
@@ -559,7 +683,7 @@ LookupPlan lookup_plan(int64_t N, int64_t V, int D, int dtype, void* ws) {
     const int64_t units = ((int64_t)D * esize(dtype) + 15) / 16;
     const int per = kLkThreads / pow2_at_least(units, kLkThreads);
     p.R = std::min(256, kChunkSlots / per);
-    while (p.R > 16 && N / p.R * units < 262144) p.R /= 2;
+    while (p.R > 16 && N / p.R * units < 131072) p.R /= 2;
     p.chunks = (N + p.R - 1) / p.R;
     uint8_t* base = static_cast<uint8_t*>(ws);
     size_t used = 0;
@@ -598,11 +722,11 @@ tt_status forward_launch(LookupArgs a, cudaStream_t st) {
 }
 
 template <class T, int VEC>
-tt_status backward_launch(LookupArgs a, const LookupPlan& p, const int64_t* ids, int dev, cudaStream_t st) {
+tt_status backward_launch(LookupArgs a, const LookupPlan& p, const int64_t* ids, int sms, int dev, cudaStream_t st) {
     // some 128 KB of table rows to a block that writes zeros
     a.zero_rows = (int)std::max<int64_t>(1, std::min<int64_t>(kZeroRows, 131072 / ((int64_t)a.D * (int64_t)sizeof(T))));
-    const int64_t zero_blocks = a.accumulate ? 0 : (a.V + a.zero_rows - 1) / a.zero_rows;
     if (!p.sorted) {
+        const int64_t zero_blocks = a.accumulate ? 0 : (a.V + a.zero_rows - 1) / a.zero_rows;
         set_units(&a, VEC, 64);
         a.sum_blocks = a.N * a.slices;
         if (a.sum_blocks + zero_blocks == 0) return TT_OK;
@@ -628,13 +752,33 @@ tt_status backward_launch(LookupArgs a, const LookupPlan& p, const int64_t* ids,
     }
     s.m = p.m;
     s.err = a.err;
-    constexpr size_t kScatterSmem = sizeof(int) * (1 + kSortW) << kDigitBits;
+    // the rows that the sort's launches clear, in turn from the table's beginning
+    const int64_t row_bytes = (int64_t)a.D * (int64_t)sizeof(T), pitch = a.out_ld * (int64_t)sizeof(T);
+    const int64_t rows = a.accumulate ? 0 : a.V;
+    int64_t cleared = 0;
+    auto take = [&](int64_t bytes, int* blocks) {
+        ZeroRows z{static_cast<uint8_t*>(a.out) + cleared * pitch, row_bytes, pitch, std::min(rows - cleared, bytes / row_bytes), VEC > 1};
+        cleared += z.rows;
+        *blocks = z.rows ? (int)std::min<int64_t>(4 * sms, (z.rows * row_bytes + 65535) / 65536) : 0;
+        return z;
+    };
+    constexpr size_t kScatterSmem = (sizeof(int) + sizeof(uint16_t) * kSortW) << kDigitBits;
     struct Tag {};
     if (!allow_smem<Tag>(k_lookup_scatter, dev, kScatterSmem)) return TT_ERR_CUDA;
-    k_lookup_hist<<<p.nch, kSortBlock, sizeof(int) * p.bins[0], st>>>(s);
+    int extra;
+    // Where few rows can be named the sort's launches write all zeros, the histogram a share and each scatter
+    // two (10,240 lookups of 1,000,000 x 64 fp32, 256 MB of zeros: 62 us with a third of them there, 57 with all).  Where many can,
+    // the sums do it, which leave those out (65,521 of 50,001 x 2048 bf16: 182 with half of the table there, 178 without).
+    const bool all = a.N * 4 <= a.V;
+    const int64_t share = all ? rows * row_bytes / (2 * p.passes + 1) + row_bytes : 0;
+    const ZeroRows zh = take(share, &extra);
+    k_lookup_hist<<<p.nch + extra, kSortBlock, sizeof(int) * p.bins[0], st>>>(s, zh);
+    if (cudaGetLastError() != cudaSuccess) return TT_ERR_CUDA;
     for (int i = 0; i < p.passes; ++i) {
-        k_lookup_scan<<<(p.bins[i] + kSortW - 1) / kSortW, kSortBlock, 0, st>>>(s, i);
-        k_lookup_scatter<<<p.nch, kSortBlock, sizeof(int) * (1 + kSortW) * p.bins[i], st>>>(s, i);
+        if (p.nch > kFoldChunks && !launch_ahead(k_lookup_scan, dim3((p.bins[i] + 31) / 32), kSortBlock, 0, st, s, i)) return TT_ERR_CUDA;
+        const ZeroRows zs = take(all && i + 1 == p.passes ? rows * row_bytes : 2 * share, &extra);
+        const size_t smem = (sizeof(int) + sizeof(uint16_t) * kSortW) * p.bins[i];
+        if (!launch_ahead(k_lookup_scatter, dim3(p.nch + extra), kSortBlock, smem, st, s, zs, i)) return TT_ERR_CUDA;
     }
     set_units(&a, VEC, kLkThreads);
     a.R = p.R;
@@ -644,26 +788,28 @@ tt_status backward_launch(LookupArgs a, const LookupPlan& p, const int64_t* ids,
     a.m = p.m;
     a.head = p.head;
     a.tail = p.tail;
+    a.zero_first = cleared;
+    const int64_t zero_blocks = (rows - cleared + a.zero_rows - 1) / a.zero_rows;
     const int per = kLkThreads / a.lanes;
     a.sum_blocks = (p.chunks + per - 1) / per * a.slices;
-    k_lookup_sums<T, VEC><<<(unsigned)(a.sum_blocks + zero_blocks), kLkThreads, 0, st>>>(a);
-    k_lookup_join<T, VEC><<<(unsigned)(p.chunks * ((a.units + 31) / 32)), kLkThreads, 0, st>>>(a);
-    return cudaGetLastError() == cudaSuccess ? TT_OK : TT_ERR_CUDA;
+    if (!launch_ahead(k_lookup_sums<T, VEC>, dim3((unsigned)(a.sum_blocks + zero_blocks)), kLkThreads, 0, st, a)) return TT_ERR_CUDA;
+    set_units(&a, VEC, 64);  // a popular id has dozens of partial sums: at least four threads to each column
+    return launch_ahead(k_lookup_join<T, VEC>, dim3((unsigned)(p.chunks * a.slices)), kLkThreads, 0, st, a) ? TT_OK : TT_ERR_CUDA;
 }
 
 template <class T>
-tt_status run_lookup(const LookupArgs& a, bool vec, const LookupPlan* plan, int dev, cudaStream_t st) {
+tt_status run_lookup(const LookupArgs& a, bool vec, const LookupPlan* plan, int sms, int dev, cudaStream_t st) {
     constexpr int kVec = 16 / (int)sizeof(T);
     if (!plan) return vec ? forward_launch<T, kVec>(a, st) : forward_launch<T, 1>(a, st);
-    return vec ? backward_launch<T, kVec>(a, *plan, a.ids, dev, st) : backward_launch<T, 1>(a, *plan, a.ids, dev, st);
+    return vec ? backward_launch<T, kVec>(a, *plan, a.ids, sms, dev, st) : backward_launch<T, 1>(a, *plan, a.ids, sms, dev, st);
 }
 
-tt_status dispatch(int dtype, const LookupArgs& a, const LookupPlan* plan, int dev, cudaStream_t st) {
+tt_status dispatch(int dtype, const LookupArgs& a, const LookupPlan* plan, int sms, int dev, cudaStream_t st) {
     const int e = esize(dtype);
     const bool vec = a.D * e % 16 == 0 && aligned(a.in, 16) && aligned(a.out, 16) && a.in_ld * e % 16 == 0 && a.out_ld * e % 16 == 0;
-    if (dtype == TT_F32) return run_lookup<float>(a, vec, plan, dev, st);
-    if (dtype == TT_BF16) return run_lookup<__nv_bfloat16>(a, vec, plan, dev, st);
-    return run_lookup<__half>(a, vec, plan, dev, st);
+    if (dtype == TT_F32) return run_lookup<float>(a, vec, plan, sms, dev, st);
+    if (dtype == TT_BF16) return run_lookup<__nv_bfloat16>(a, vec, plan, sms, dev, st);
+    return run_lookup<__half>(a, vec, plan, sms, dev, st);
 }
 
 }  // namespace
@@ -688,7 +834,8 @@ tt_status tt_emb_lookup_forward(const tt_lookup* lookup, void* out_dev, int64_t 
     if (!aligned(l.weight_dev, esize(l.dtype)) || !aligned(out_dev, esize(l.dtype)) || !aligned(l.ids_dev, 8) || !aligned(err_dev, 4)) return TT_ERR_ARG;
     if (l.rows == 0) return TT_OK;
     int dev = 0;
-    if (head_sms(&dev) <= 0) return TT_ERR_CUDA;
+    const int sms = head_sms(&dev);
+    if (sms <= 0) return TT_ERR_CUDA;
     LookupArgs a{};
     a.in = l.weight_dev;
     a.in_ld = l.weight_stride;
@@ -701,7 +848,7 @@ tt_status tt_emb_lookup_forward(const tt_lookup* lookup, void* out_dev, int64_t 
     a.D = l.dim;
     a.scale = l.scale;
     a.err = err_dev;
-    return dispatch(l.dtype, a, nullptr, dev, reinterpret_cast<cudaStream_t>(stream));
+    return dispatch(l.dtype, a, nullptr, sms, dev, reinterpret_cast<cudaStream_t>(stream));
 }
 
 tt_status tt_emb_lookup_backward(const tt_lookup* lookup, const void* grad_out_dev, int64_t grad_out_stride, void* grad_weight_dev,
@@ -719,7 +866,8 @@ tt_status tt_emb_lookup_backward(const tt_lookup* lookup, const void* grad_out_d
     const LookupPlan p = lookup_plan(l.rows, l.vocab, l.dim, l.dtype, ws_dev);
     if (ws_bytes < p.bytes || (p.bytes && !ws_dev)) return TT_ERR_ARG;
     int dev = 0;
-    if (head_sms(&dev) <= 0) return TT_ERR_CUDA;
+    const int sms = head_sms(&dev);
+    if (sms <= 0) return TT_ERR_CUDA;
     LookupArgs a{};
     a.in = grad_out_dev;
     a.in_ld = grad_out_stride;
@@ -733,7 +881,7 @@ tt_status tt_emb_lookup_backward(const tt_lookup* lookup, const void* grad_out_d
     a.scale = l.scale;
     a.accumulate = accumulate != 0;
     a.err = err_dev;
-    return dispatch(l.dtype, a, &p, dev, reinterpret_cast<cudaStream_t>(stream));
+    return dispatch(l.dtype, a, &p, sms, dev, reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"
