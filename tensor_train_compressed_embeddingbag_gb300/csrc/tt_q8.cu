@@ -17,26 +17,38 @@
 // warp that stores 32 lanes of a column writes 128 consecutive bytes of a row of scores.
 #include <algorithm>
 
+#include "tt_q8_pipe.cuh"
 #include "tt_units.cuh"
 
 namespace ttemb {
 
-constexpr int kQ8Threads = 640;   // warp 0: rows of x, 1: MMA, 2: tensor memory, 3: codes, 4..11: codes to f16, 12..19: scores out
 constexpr int kQ8K = 128;         // columns of a step
 constexpr int kQ8Range = 1024;    // columns that an accumulator takes (a multiple of kQ8K)
 constexpr int kQ8ACols = kQ8K / 2;  // tensor-memory columns of a step's codes
 
+// Warps: 0 rows of x, 1 MMA, 2 tensor memory, 3 codes; then kSets x 4 codes to f16, kParts x 4 scores out (a part
+// of the columns each).
+//
+// What bounds a narrow tile is the warp that issues the MMAs: a step costs it some 190 cycles of waiting, 60 for each
+// of the eight MMAs and 90 for each commit, whatever their width.  So up to 64 rows of x two blocks share a
+// multiprocessor, each with half of its shared and tensor memory.
 template <int BN>
-struct Q8Shape {
+struct Q8Shape : Q8Pipe<BN> {
+    using Q8Pipe<BN>::kSets;
+    using Q8Pipe<BN>::kXStages;
+    using Q8Pipe<BN>::kCStages;
+    using Q8Pipe<BN>::kAStages;
+    static constexpr int kBlocks = BN > 64 ? 1 : 2;  // of a multiprocessor
+    static constexpr int kParts = BN > 64 ? 2 : 1, kCols = BN / kParts;
+    static constexpr int kThreads = (4 + 4 * kSets + 4 * kParts) * 32;
     // a step's codes leave shared memory early, its rows of x when its MMAs are done: a ring for each
     static constexpr uint32_t kC = 128 * kQ8K, kX = BN * kQ8K * 2;
-    static constexpr int kXStages = BN > 128 ? 3 : (BN == 128 ? 4 : 6), kCStages = (220 * 1024 - kXStages * kX) / kC;
     static constexpr size_t kSmem = (size_t)kXStages * kX + (size_t)kCStages * kC + 1024;
-    static constexpr int kAStages = BN > 128 ? 2 : 4;  // steps in tensor memory; every second one belongs to a set of four warps
-    static constexpr int kACol = 2 * BN;               // behind the two accumulators
+    static constexpr int kTmem = 512 / kBlocks;        // columns
+    static constexpr int kACol = 2 * BN;               // behind the two accumulators: kAStages steps
     // 192 columns take 96 sums a thread in the last eight warps: registers go there from the others
     static constexpr bool kShift = BN > 128;
-    static_assert(kACol + kAStages * kQ8ACols <= 512 && kSmem + 2048 <= 227 * 1024, "tensor and shared memory");
+    static_assert(kACol + kAStages * kQ8ACols <= kTmem && kBlocks * (kSmem + 2048) <= 228 * 1024, "tensor and shared memory");
 };
 
 struct Q8Args {
@@ -73,7 +85,7 @@ __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t&
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(0x64806480u));
 }
 
-// Registers of a thread from here on, for all four warps of a group.  A launch has 640 x 96 of them; the
+// Registers of a thread from here on, for all four warps of a group.  A launch of 640 threads has 640 x 96 of them; the
 // groups' shares add up to that: 48 + 2 x 88 + 2 x 128 = 5 x 96.
 constexpr int kQ8Regs = 96, kQ8RegsFeed = 48, kQ8RegsTurn = 88, kQ8RegsOut = 128;
 static_assert(kQ8RegsFeed + 2 * kQ8RegsTurn + 2 * kQ8RegsOut <= 5 * kQ8Regs, "more would never be there");
@@ -89,10 +101,11 @@ __device__ __forceinline__ void more_registers() {
 // A unit is 128 table rows x BN rows of x; the tiles of x go fastest, so blocks that run together
 // share table rows.
 template <int BN>
-__global__ void __launch_bounds__(kQ8Threads, 1)
+__global__ void __launch_bounds__(Q8Shape<BN>::kThreads, Q8Shape<BN>::kBlocks)
     k_q8_scores(const __grid_constant__ CUtensorMap map_codes, const __grid_constant__ CUtensorMap map_x, const __grid_constant__ Q8Args a) {
     using S = Q8Shape<BN>;
-    constexpr int kHalf = BN / 2;        // columns of an epilogue warp
+    constexpr int kCols = S::kCols;      // columns of an epilogue warp
+    constexpr int kOutWarp = 4 + 4 * S::kSets;
     constexpr int kRangeSteps = kQ8Range / kQ8K;
     extern __shared__ uint8_t raw[];
     __shared__ uint64_t cfull[S::kCStages], cempty[S::kCStages], xfull[S::kXStages], xempty[S::kXStages];
@@ -119,12 +132,12 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&accfull[i], 1);
-            mbar_init(&accempty[i], 8);
+            mbar_init(&accempty[i], 4 * S::kParts);
         }
         mbar_init(&drain, 1);
         gave_up_s = 0;
     }
-    if (warp == 2) tc_alloc(&tmem_slot, 512);
+    if (warp == 2) tc_alloc(&tmem_slot, S::kTmem);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -192,29 +205,36 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
                 }
             }
         }
-    } else if (warp < 12) {
+    } else if (warp < kOutWarp) {
         if (S::kShift) fewer_registers<kQ8RegsTurn>();
         const uint32_t set = (warp - 4) >> 2;
         const int quad = warp & 3, r = quad * 32 + lane;
         const uint32_t to = tmem + ((uint32_t)(quad * 32) << 16) + S::kACol;
-        for (int64_t i = set; i < total; i += 2) {
+        for (int64_t i = set; i < total; i += S::kSets) {
             it = (uint32_t)i;
             const uint32_t cs = it % S::kCStages, st = it % S::kXStages, ta = it % S::kAStages;
             ok = head_wait(&cfull[cs], (it / S::kCStages) & 1, a.wait_ns, gave_up);
             if (!ok) break;
-            // the codes are f16 in registers before the MMAs that still read this place are done
             const uint32_t row = cbase + cs * S::kC + r * 128;
-            uint32_t q[4][16];
+            uint4 w[8];
 #pragma unroll
-            for (int h = 0; h < 4; ++h)
+            for (int x = 0; x < 8; ++x) w[x] = lds16(row + ((x ^ (r & 7)) << 4));  // 128-byte swizzle
+            uint32_t q[4][16];
+            auto turn = [&](int h) {
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    const uint4 y = lds16(row + (((h * 2 + x) ^ (r & 7)) << 4));  // 128-byte swizzle
+                    const uint4 y = w[h * 2 + x];
                     codes_to_f16(y.x, q[h][x * 8], q[h][x * 8 + 1]);
                     codes_to_f16(y.y, q[h][x * 8 + 2], q[h][x * 8 + 3]);
                     codes_to_f16(y.z, q[h][x * 8 + 4], q[h][x * 8 + 5]);
                     codes_to_f16(y.w, q[h][x * 8 + 6], q[h][x * 8 + 7]);
                 }
+            };
+            // where there are registers, the codes are f16 before the MMAs that still read this place are done
+            constexpr bool kEarly = S::kBlocks == 1;
+            if (kEarly)
+#pragma unroll
+                for (int h = 0; h < 4; ++h) turn(h);
             __syncwarp();
             if (lead) mbar_arrive(&cempty[cs]);
             ok = head_wait(&xfull[st], (it / S::kXStages) & 1, a.wait_ns, gave_up) &&
@@ -222,7 +242,10 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
             if (!ok) break;
             tc_fence_after();
 #pragma unroll
-            for (int h = 0; h < 4; ++h) tm_st16(to + ta * kQ8ACols + h * 16, q[h]);
+            for (int h = 0; h < 4; ++h) {
+                if (!kEarly) turn(h);
+                tm_st16(to + ta * kQ8ACols + h * 16, q[h]);
+            }
             tm_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -231,20 +254,26 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
     } else {
         if (S::kShift) more_registers<kQ8RegsOut>();
         pdl_wait();  // the scales of x
-        const int half = (warp - 12) >> 2, quad = warp & 3;
+        const int part = (warp - kOutWarp) >> 2, quad = warp & 3;
         for (int64_t u = blockIdx.x; ok && u < a.units; u += gridDim.x) {
             const int vt = (int)(u / a.mtiles), mt = (int)(u - (int64_t)vt * a.mtiles);
-            const int64_t v = (int64_t)vt * 128 + quad * 32 + lane, m0 = (int64_t)mt * BN + half * kHalf;
-            int sum[kHalf];
+            const int64_t v = (int64_t)vt * 128 + quad * 32 + lane, m0 = (int64_t)mt * BN + part * kCols;
+            const int rows = (int)min((int64_t)kCols, a.M - m0);  // may be below 1
+            // the scales are on their way while the sums are formed; a column's is in one lane and goes to all
+            const float s = v < a.V ? __ldg(a.scale + v) : 0.f;
+            float xs[(kCols + 31) / 32];
+#pragma unroll
+            for (int h = 0; h < kCols; h += 32) xs[h / 32] = h + lane < rows ? __ldg(a.xscale + m0 + h + lane) : 0.f;
+            int sum[kCols];
 #pragma unroll 1
             for (int r0 = 0; ok && r0 < a.chunks; r0 += kRangeSteps, ++acc) {
                 const uint32_t buf = acc & 1;
                 ok = head_wait(&accfull[buf], (acc >> 1) & 1, a.wait_ns, gave_up);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t t0 = tmem + buf * BN + ((uint32_t)(quad * 32) << 16) + half * kHalf;
+                const uint32_t t0 = tmem + buf * BN + ((uint32_t)(quad * 32) << 16) + part * kCols;
 #pragma unroll
-                for (int h = 0; h < kHalf; h += 16) {
+                for (int h = 0; h < kCols; h += 16) {
                     float x[16];
                     tm_read16(t0 + h, x);
 #pragma unroll
@@ -258,19 +287,12 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
                 if (lead) mbar_arrive(&accempty[buf]);
             }
             if (!ok) break;
-            const int rows = (int)min((int64_t)kHalf, a.M - m0);  // may be below 1
-            const float s = v < a.V ? __ldg(a.scale + v) : 0.f;
             float* o = a.out + m0 * a.V + v;
-            // a column's scale is in one lane and goes to all
 #pragma unroll
-            for (int h = 0; h < kHalf; h += 32) {
-                const float xs = h + lane < rows ? __ldg(a.xscale + m0 + h + lane) : 0.f;
-#pragma unroll
-                for (int j = h; j < h + 32 && j < kHalf; ++j) {
-                    const float f = __shfl_sync(0xffffffffu, xs, j - h);
-                    if (j < rows && v < a.V) *o = (float)sum[j] * (f * s);
-                    o += a.V;
-                }
+            for (int j = 0; j < kCols; ++j) {
+                const float f = __shfl_sync(0xffffffffu, xs[j / 32], j & 31);
+                if (j < rows && v < a.V) *o = (float)sum[j] * (f * s);
+                o += a.V;
             }
         }
     }
@@ -293,7 +315,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
         __syncthreads();
     }
     tc_fence_after();
-    if (warp == 2) tc_dealloc(tmem, 512);
+    if (warp == 2) tc_dealloc(tmem, S::kTmem);
 }
 
 // ---------------------------------------------------------------- few rows
@@ -658,7 +680,7 @@ tt_status scores_launch(Q8Args a, const int8_t* codes, const __half* x, int D, i
         }();
         if (!enough) return TT_ERR_CUDA;
     }
-    return launch_ahead(k_q8_scores<BN>, dim3((unsigned)std::min<int64_t>(a.units, sms)), kQ8Threads, Q8Shape<BN>::kSmem, st, mc, mx, a) ? TT_OK
+    return launch_ahead(k_q8_scores<BN>, dim3((unsigned)std::min<int64_t>(a.units, sms * Q8Shape<BN>::kBlocks)), Q8Shape<BN>::kThreads, Q8Shape<BN>::kSmem, st, mc, mx, a) ? TT_OK
                                                                                                                                          : TT_ERR_CUDA;
 }
 
