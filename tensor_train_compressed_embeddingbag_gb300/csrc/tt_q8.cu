@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(Q8Shape<BN>::kThreads, Q8Shape<BN>::kBlocks)
 
 // ---------------------------------------------------------------- few rows
 //
-// Up to 16 rows of x are a stream: the table's bytes are the floor.  Here a tile's way through shared
+// Few rows of x are a stream: the table's bytes are the floor.  Here a tile's way through shared
 // and tensor memory would cost more than its bytes (a step of the kernel above takes its issuing warp some
 // 700 cycles, whatever it multiplies), so the codes go from global memory to registers, 16 bytes of
 // a row to a thread, become f16 there and are multiplied by the warp-level tensor cores
@@ -353,9 +353,11 @@ struct FewArgs8 {
     float* out;
 };
 
-template <int NT>
+// LONG: rows of the table are long: registers hold loads in flight; else a tile is soon over, and they hold the
+// scales of the next one (1 x 131072 x 4096: 92 us, 100 the other way; 1 x 1,000,000 x 64: 26 and 19).
+template <int NT, bool LONG>
 __global__ void __launch_bounds__(kFewThreads, 2) k_q8_few(const __grid_constant__ FewArgs8 a) {
-    constexpr int kAhead = NT == 1 ? 4 : 3;  // steps in flight, as registers allow
+    constexpr int kAhead = LONG ? 4 : 2;  // steps in flight
     __shared__ int red[kFewWarps8][NT * 8 * kFewTile];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     const int per = kFewWarps8 / a.ksplit, sub = warp / a.ksplit, ks = warp - sub * a.ksplit;
@@ -387,7 +389,21 @@ __global__ void __launch_bounds__(kFewThreads, 2) k_q8_few(const __grid_constant
     };
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) load(q[i]);
+    float s_now[4], s_next[4];  // not LONG: the scales of this tile's rows and of the next one's (with columns shared, the joining lanes read them)
+    auto scales = [&](int64_t round, float (&s)[4]) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int64_t v = (round * per + sub) * kFewTile + r * 8 + g;
+            s[r] = a.ksplit == 1 && v < a.V ? __ldg(a.scale + v) : 0.f;
+        }
+    };
+    if (!LONG) scales(blockIdx.x, s_now);
     pdl_wait();  // x, and its scales
+    float xs[NT][2];  // (LONG reads them again: no registers)
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) xs[n][e] = n * 8 + 2 * t + e < a.M ? a.xscale[n * 8 + 2 * t + e] : 0.f;
     int sum[2][NT][4];
     float acc[2][NT][4];
 #pragma unroll
@@ -418,6 +434,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) k_q8_few(const __grid_constant
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
             if (rd >= rounds) break;
+            if (!LONG && j == jb) scales(rd + gridDim.x, s_next);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 uint4 x[NT];
@@ -450,13 +467,13 @@ __global__ void __launch_bounds__(kFewThreads, 2) k_q8_few(const __grid_constant
                 for (int r = 0; r < 4; ++r) {
                     const int64_t v = v0 + r * 8 + g;
                     if (v >= a.V) continue;
-                    const float s = __ldg(a.scale + v);
+                    const float s = LONG ? __ldg(a.scale + v) : s_now[r];
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             const int m = n * 8 + 2 * t + e;
-                            if (m < a.M) a.out[(int64_t)m * a.V + v] = (float)sum[r >> 1][n][(r & 1) * 2 + e] * (a.xscale[m] * s);
+                            if (m < a.M) a.out[(int64_t)m * a.V + v] = (float)sum[r >> 1][n][(r & 1) * 2 + e] * ((LONG ? a.xscale[m] : xs[n][e]) * s);
                         }
                 }
             } else {  // joined with the other warps of the tile
@@ -482,6 +499,9 @@ __global__ void __launch_bounds__(kFewThreads, 2) k_q8_few(const __grid_constant
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) sum[r][n][e] = 0;
+            if (!LONG)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) s_now[r] = s_next[r];
             j = jb;
             rd += gridDim.x;
         }
@@ -597,7 +617,10 @@ int64_t x_pitch(int64_t dim) { return (dim + 7) / 8 * 8; }
 int64_t code_pitch(int64_t dim) { return (dim + 15) / 16 * 16; }
 
 int64_t few_pitch(int64_t dim) { return (dim + kFewK - 1) / kFewK * kFewK; }
-int few_tiles(int64_t rows) { return rows > 16 ? 0 : (rows > 8 ? 2 : 1); }  // of 8 rows; 0: not few
+// Tiles of 8 rows, 0: not few.  Up to 8 rows a stream is the fastest everywhere (8 x 131072 x 4096: 102 us, 106 the
+// other way); 9 to 16 cost it twice the multiplications, which it keeps up with only where rows of the table are short and the
+// other kernel has nothing to overlap its tiles' fill and drain with (16 rows: 1,000,000 x 64 38 us, 42 the other way; 131072 x 4096 128, 99).
+int few_tiles(int64_t rows, int64_t dim) { return rows <= 8 ? 1 : (rows <= 16 && dim <= 256 ? 2 : 0); }
 
 struct Q8Space {
     __half* x;
@@ -605,7 +628,7 @@ struct Q8Space {
     size_t bytes;
 };
 Q8Space q8_space(int64_t rows, int64_t dim, void* ws) {
-    const int nt = few_tiles(rows);
+    const int nt = few_tiles(rows, dim);
     const size_t codes = ((size_t)(nt ? (int64_t)nt * 8 * few_pitch(dim) : rows * x_pitch(dim)) * 2 + 255) / 256 * 256;
     uint8_t* p = static_cast<uint8_t*>(ws);
     return {reinterpret_cast<__half*>(p), reinterpret_cast<float*>(p ? p + codes : nullptr), codes + ((size_t)rows * 4 + 255) / 256 * 256};
@@ -651,7 +674,7 @@ bool make_map2(CUtensorMap* m, const void* p, bool f16, int64_t cols, int64_t ro
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int NT>
+template <int NT, bool LONG>
 tt_status few_launch(FewArgs8 a, int sms, cudaStream_t st) {
     // warps that share a tile's columns: more of them while the tiles alone would give a warp slot fewer
     // than 4, as long as each keeps four steps
@@ -659,7 +682,7 @@ tt_status few_launch(FewArgs8 a, int sms, cudaStream_t st) {
     a.ksplit = 1;
     while (a.ksplit < kFewWarps8 && tiles * a.ksplit < 4ll * sms * 2 * kFewWarps8 && a.steps >= 8 * a.ksplit) a.ksplit *= 2;
     const int64_t per = kFewWarps8 / a.ksplit, rounds = (tiles + per - 1) / per;
-    return launch_ahead(k_q8_few<NT>, dim3((unsigned)std::min<int64_t>(rounds, 2 * sms)), kFewThreads, 0, st, a) ? TT_OK : TT_ERR_CUDA;
+    return launch_ahead(k_q8_few<NT, LONG>, dim3((unsigned)std::min<int64_t>(rounds, 2 * sms)), kFewThreads, 0, st, a) ? TT_OK : TT_ERR_CUDA;
 }
 
 template <int BN>
@@ -726,7 +749,7 @@ tt_status tt_emb_q8_scores(const void* x_dev, int64_t x_stride, int64_t rows, in
     const int sms = head_sms(&dev);
     if (sms <= 0) return TT_ERR_CUDA;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    const int nt = few_tiles(rows);
+    const int nt = few_tiles(rows, dim);
     quantize_rows(x_dev, x_stride, rows, dim, dtype, nullptr, w.x, nt ? few_pitch(dim) : x_pitch(dim), nt, w.xscale, sms, st);
     if (cudaGetLastError() != cudaSuccess) return TT_ERR_CUDA;
     if (nt) {
@@ -740,7 +763,8 @@ tt_status tt_emb_q8_scores(const void* x_dev, int64_t x_stride, int64_t rows, in
         f.M = (int)rows;
         f.steps = (int)(few_pitch(dim) / kFewK);
         f.out = out_dev;
-        return nt == 1 ? few_launch<1>(f, sms, st) : few_launch<2>(f, sms, st);
+        if (nt == 2) return few_launch<2, false>(f, sms, st);
+        return dim > 256 ? few_launch<1, true>(f, sms, st) : few_launch<1, false>(f, sms, st);
     }
     Q8Args a{};
     a.M = rows;
