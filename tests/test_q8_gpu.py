@@ -95,7 +95,8 @@ def test_rows_that_are_not_finite(dtype):
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("m,v,d", [(1, 1, 1), (1, 129, 16), (2, 50, 33), (5, 1000, 257), (16, 300, 64), (17, 127, 130), (32, 77, 1024), (33, 200, 1025),
                                    (64, 640, 96), (65, 33, 4096), (128, 128, 128), (129, 500, 2050), (192, 257, 100), (193, 400, 1030), (600, 1000, 300),
-                                   (3, 20000, 40), (2, 40, 65536), (1000, 20011, 72)])
+                                   (3, 20000, 40), (2, 40, 65536), (1000, 20011, 72), (9, 700, 256), (16, 300, 257), (8, 30000, 256),
+                                   (12, 60000, 200), (40, 60000, 300), (100, 30000, 1100)])
 def test_scores(m, v, d, dtype):
     x = torch.randn((m, d), generator=gen(5), device="cuda").to(dtype)
     codes, scales = table(v, d)  # padding columns hold something
@@ -107,6 +108,17 @@ def test_scores(m, v, d, dtype):
     assert torch.equal(got, want)
     into = torch.full((m, v), float("nan"), device="cuda")
     assert tt.tt_emb_q8_scores(x, codes, scales, out=into) is into and torch.equal(into, want)
+
+
+@pytest.mark.parametrize("m", [4, 20, 50, 100, 129, 192])
+def test_long_rows_of_many_tiles(m):
+    """Every block takes many tiles of many steps: places of the rings are used hundreds of times."""
+    x = torch.randn((m, 4096), generator=gen(20), device="cuda")
+    codes, scales = table(60000, 4096)
+    xc, xs = quantized(x)
+    want = product(xc, xs, codes, scales)
+    for _ in range(3):
+        assert torch.equal(tt.tt_emb_q8_scores(x, codes, scales), want)
 
 
 @pytest.mark.parametrize("m", [1, 20, 200])
