@@ -22,7 +22,7 @@ namespace ttemb {
 constexpr int kPieceMin = 8, kPieceMax = 11;  // log2 of K, tokens
 constexpr int kAnswerWarps = 8;                   // pieces of a block
 constexpr int kOneWarps = 32;                     // of the block that does a small call alone
-constexpr int64_t kOneTokens = 8192, kOnePieces = 320;
+constexpr int64_t kOneTokens = 8192, kOnePieces = 64;
 
 // A sum in two floats, which keeps some 48 bits: every rounding of `hi` goes to `lo` (the exact
 // error of an addition: D. E. Knuth, "The Art of Computer Programming", vol. 2, 4.2.2).  Doubles

@@ -16,7 +16,7 @@
 // within the chunk (votes per warp).  The scatter counts the next digit's histogram.
 //
 // Few lookups are not sorted: a block per lookup and column slice looks through all ids,
-// leaves if an earlier lookup has the same, and else sums those that have it: one launch.
+// leaves if an earlier lookup has the same, and else sums those that have it.
 #include <algorithm>
 
 #include "tt_units.cuh"
@@ -106,26 +106,29 @@ struct ZeroRows {
     uint8_t* out;
     int64_t row_bytes, pitch;  // of a row, and from row to row
     int64_t rows;              // [0, rows)
-    int vec;                   // rows are 16-byte units
 };
 __device__ void write_zeros(const ZeroRows& z, int block, int blocks) {
     const int64_t thread = (int64_t)block * blockDim.x + threadIdx.x, threads = (int64_t)blocks * blockDim.x;
-    if (z.vec && z.row_bytes == z.pitch) {
-        uint4* p = reinterpret_cast<uint4*>(z.out);
-        const int64_t n = z.rows * (z.row_bytes / 16);
+    auto clear = [](uint8_t* p, int64_t bytes, int64_t first, int64_t step) {  // 16 bytes at a time, and what is left at both ends
+        const int64_t head = min(bytes, (int64_t)(-(intptr_t)p & 15)), n = (bytes - head) / 16;
+        uint4* q = reinterpret_cast<uint4*>(p + head);
 #pragma unroll 8
-        for (int64_t i = thread; i < n; i += threads) p[i] = make_uint4(0, 0, 0, 0);
+        for (int64_t i = first; i < n; i += step) q[i] = make_uint4(0, 0, 0, 0);
+        const int64_t tail = head + n * 16;
+        if (first * 2 < head) reinterpret_cast<uint16_t*>(p)[first] = 0;
+        if (first * 2 < bytes - tail) reinterpret_cast<uint16_t*>(p + tail)[first] = 0;
+    };
+    if (z.row_bytes == z.pitch || z.rows == 1) {
+        if (z.rows > 0) clear(z.out, z.rows * z.row_bytes, thread, threads);
         return;
     }
     const int warps = blockDim.x / 32;
-    for (int64_t r = (int64_t)block * warps + (threadIdx.x >> 5); r < z.rows; r += (int64_t)blocks * warps) {
-        uint8_t* p = z.out + r * z.pitch;
-        if (z.vec) {
-            for (int64_t i = threadIdx.x & 31; i < z.row_bytes / 16; i += 32) reinterpret_cast<uint4*>(p)[i] = make_uint4(0, 0, 0, 0);
-        } else {
-            for (int64_t i = threadIdx.x & 31; i < z.row_bytes / 2; i += 32) reinterpret_cast<uint16_t*>(p)[i] = 0;
-        }
-    }
+    for (int64_t r = (int64_t)block * warps + (threadIdx.x >> 5); r < z.rows; r += (int64_t)blocks * warps)
+        clear(z.out + r * z.pitch, z.row_bytes, threadIdx.x & 31, 32);
+}
+__global__ void __launch_bounds__(512) k_lookup_zero(const __grid_constant__ ZeroRows z) {
+    pdl_launch_dependents();
+    write_zeros(z, blockIdx.x, gridDim.x);
 }
 
 struct SortArgs {
@@ -366,8 +369,9 @@ __global__ void __launch_bounds__(kSortBlock) k_lookup_scatter(const __grid_cons
 // A unit of a row of partial sums.
 template <int VEC>
 __device__ __forceinline__ void put_part(float* to, const float (&v)[VEC]) {
-    if constexpr (VEC == 1) {
-        *to = v[0];
+    if constexpr (VEC < 4) {  // a row of an odd number of units does not begin on 16 bytes
+#pragma unroll
+        for (int q = 0; q < VEC; ++q) to[q] = v[q];
     } else {
 #pragma unroll
         for (int q = 0; q < VEC; q += 4) *reinterpret_cast<float4*>(to + q) = make_float4(v[q], v[q + 1], v[q + 2], v[q + 3]);
@@ -375,8 +379,9 @@ __device__ __forceinline__ void put_part(float* to, const float (&v)[VEC]) {
 }
 template <int VEC>
 __device__ __forceinline__ void add_part(const float* from, float (&v)[VEC]) {
-    if constexpr (VEC == 1) {
-        v[0] += *from;
+    if constexpr (VEC < 4) {
+#pragma unroll
+        for (int q = 0; q < VEC; ++q) v[q] += from[q];
     } else {
 #pragma unroll
         for (int q = 0; q < VEC; q += 4) {
@@ -552,14 +557,14 @@ __global__ void __launch_bounds__(kLkThreads) k_lookup_join(const __grid_constan
     if (u < a.units) put_unit<T, VEC>(a, key, u, s);
 }
 
-// Few lookups: a block per lookup and slice of `lanes` units, then blocks that write zeros.
+// Few lookups: a block per lookup and slice of `lanes` units.
 template <class T, int VEC>
 __global__ void __launch_bounds__(kLkThreads) k_lookup_few(const __grid_constant__ LookupArgs a) {
+    pdl_launch_dependents();
     __shared__ int ids[kSmallRows];
     __shared__ union {
         int list[kSmallRows];
-        uint8_t named[kZeroRows];
-        float part[kLkThreads * 8];
+        float part[kLkThreads * VEC];
     } s;
     __shared__ int sh[kLkThreads / 32];
     const int N = (int)a.N;
@@ -570,19 +575,6 @@ __global__ void __launch_bounds__(kLkThreads) k_lookup_few(const __grid_constant
         ids[n] = in && id != a.pad ? (int)id : -1;
     }
     __syncthreads();
-    if (blockIdx.x >= a.sum_blocks) {
-        const int64_t r0 = (blockIdx.x - a.sum_blocks) * a.zero_rows;  // (zero_first is 0)
-        const int rows = (int)min((int64_t)a.zero_rows, a.V - r0);
-        for (int r = threadIdx.x; r < rows; r += kLkThreads) s.named[r] = 0;
-        __syncthreads();
-        for (int n = threadIdx.x; n < N; n += kLkThreads) {
-            const int64_t r = (int64_t)ids[n] - r0;
-            if (ids[n] >= 0 && r >= 0 && r < rows) s.named[r] = 1;
-        }
-        __syncthreads();
-        zero_rows<T, VEC>(a, s.named, r0, rows);
-        return;
-    }
     const int n0 = (int)(blockIdx.x / a.slices), slice = (int)(blockIdx.x - (int64_t)n0 * a.slices);
     const int id = ids[n0];
     if (id < 0) return;
@@ -626,6 +618,7 @@ __global__ void __launch_bounds__(kLkThreads) k_lookup_few(const __grid_constant
             }
         }
     }
+    pdl_wait();  // the row may be zeros by now, and not later
     if (count > 1 && per > 1) {  // the shares in order
         __syncthreads();
 #pragma unroll
@@ -725,13 +718,26 @@ template <class T, int VEC>
 tt_status backward_launch(LookupArgs a, const LookupPlan& p, const int64_t* ids, int sms, int dev, cudaStream_t st) {
     // some 128 KB of table rows to a block that writes zeros
     a.zero_rows = (int)std::max<int64_t>(1, std::min<int64_t>(kZeroRows, 131072 / ((int64_t)a.D * (int64_t)sizeof(T))));
+    // the rows that other launches clear, in turn from the table's beginning
+    const int64_t row_bytes = (int64_t)a.D * (int64_t)sizeof(T), pitch = a.out_ld * (int64_t)sizeof(T);
+    const int64_t rows = a.accumulate ? 0 : a.V;
+    int64_t cleared = 0;
+    auto take = [&](int64_t bytes, int* blocks) {
+        ZeroRows z{static_cast<uint8_t*>(a.out) + cleared * pitch, row_bytes, pitch, std::min(rows - cleared, bytes / row_bytes)};
+        cleared += z.rows;
+        *blocks = z.rows ? (int)std::min<int64_t>(4 * sms, (z.rows * row_bytes + 65535) / 65536) : 0;
+        return z;
+    };
+    int extra;
     if (!p.sorted) {
-        const int64_t zero_blocks = a.accumulate ? 0 : (a.V + a.zero_rows - 1) / a.zero_rows;
         set_units(&a, VEC, 64);
-        a.sum_blocks = a.N * a.slices;
-        if (a.sum_blocks + zero_blocks == 0) return TT_OK;
-        k_lookup_few<T, VEC><<<(unsigned)(a.sum_blocks + zero_blocks), kLkThreads, 0, st>>>(a);
-        return cudaGetLastError() == cudaSuccess ? TT_OK : TT_ERR_CUDA;
+        const ZeroRows z = take(rows * row_bytes, &extra);
+        const dim3 grid((unsigned)(a.N * a.slices));
+        if (extra) k_lookup_zero<<<extra, 512, 0, st>>>(z);
+        else if (a.N) k_lookup_few<T, VEC><<<grid, kLkThreads, 0, st>>>(a);  // a call's first launch waits for what ran before
+        if (cudaGetLastError() != cudaSuccess) return TT_ERR_CUDA;
+        if (!extra || a.N == 0) return TT_OK;
+        return launch_ahead(k_lookup_few<T, VEC>, grid, kLkThreads, 0, st, a) ? TT_OK : TT_ERR_CUDA;
     }
     SortArgs s{};
     s.ids = ids;
@@ -752,24 +758,14 @@ tt_status backward_launch(LookupArgs a, const LookupPlan& p, const int64_t* ids,
     }
     s.m = p.m;
     s.err = a.err;
-    // the rows that the sort's launches clear, in turn from the table's beginning
-    const int64_t row_bytes = (int64_t)a.D * (int64_t)sizeof(T), pitch = a.out_ld * (int64_t)sizeof(T);
-    const int64_t rows = a.accumulate ? 0 : a.V;
-    int64_t cleared = 0;
-    auto take = [&](int64_t bytes, int* blocks) {
-        ZeroRows z{static_cast<uint8_t*>(a.out) + cleared * pitch, row_bytes, pitch, std::min(rows - cleared, bytes / row_bytes), VEC > 1};
-        cleared += z.rows;
-        *blocks = z.rows ? (int)std::min<int64_t>(4 * sms, (z.rows * row_bytes + 65535) / 65536) : 0;
-        return z;
-    };
     constexpr size_t kScatterSmem = (sizeof(int) + sizeof(uint16_t) * kSortW) << kDigitBits;
     struct Tag {};
     if (!allow_smem<Tag>(k_lookup_scatter, dev, kScatterSmem)) return TT_ERR_CUDA;
-    int extra;
     // Where few rows can be named the sort's launches write all zeros, the histogram a share and each scatter
     // two (10,240 lookups of 1,000,000 x 64 fp32, 256 MB of zeros: 62 us with a third of them there, 57 with all).  Where many can,
-    // the sums do it, which leave those out (65,521 of 50,001 x 2048 bf16: 182 with half of the table there, 178 without).
-    const bool all = a.N * 4 <= a.V;
+    // the sums do it, which leave those out (65,521 of 50,001 x 2048 bf16: 182 with half of the table there, 178 without), a row at a
+    // time: not where rows are not of whole 16 bytes.
+    const bool all = a.N * 4 <= a.V || VEC * sizeof(T) < 16;
     const int64_t share = all ? rows * row_bytes / (2 * p.passes + 1) + row_bytes : 0;
     const ZeroRows zh = take(share, &extra);
     k_lookup_hist<<<p.nch + extra, kSortBlock, sizeof(int) * p.bins[0], st>>>(s, zh);
@@ -797,19 +793,26 @@ tt_status backward_launch(LookupArgs a, const LookupPlan& p, const int64_t* ids,
     return launch_ahead(k_lookup_join<T, VEC>, dim3((unsigned)(p.chunks * a.slices)), kLkThreads, 0, st, a) ? TT_OK : TT_ERR_CUDA;
 }
 
+template <class T, int VEC>
+tt_status run_lookup(const LookupArgs& a, const LookupPlan* plan, int sms, int dev, cudaStream_t st) {
+    return plan ? backward_launch<T, VEC>(a, *plan, a.ids, sms, dev, st) : forward_launch<T, VEC>(a, st);
+}
+
+// The widest unit that divides the rows and on whose boundaries they begin.
 template <class T>
-tt_status run_lookup(const LookupArgs& a, bool vec, const LookupPlan* plan, int sms, int dev, cudaStream_t st) {
-    constexpr int kVec = 16 / (int)sizeof(T);
-    if (!plan) return vec ? forward_launch<T, kVec>(a, st) : forward_launch<T, 1>(a, st);
-    return vec ? backward_launch<T, kVec>(a, *plan, a.ids, sms, dev, st) : backward_launch<T, 1>(a, *plan, a.ids, sms, dev, st);
+tt_status run_lookup(const LookupArgs& a, const LookupPlan* plan, int sms, int dev, cudaStream_t st) {
+    constexpr int e = (int)sizeof(T);
+    auto fits = [&](int bytes) { return a.D * e % bytes == 0 && aligned(a.in, bytes) && aligned(a.out, bytes) && a.in_ld * e % bytes == 0 && a.out_ld * e % bytes == 0; };
+    if (fits(16)) return run_lookup<T, 16 / e>(a, plan, sms, dev, st);
+    if (fits(8)) return run_lookup<T, 8 / e>(a, plan, sms, dev, st);
+    if (e == 2 && fits(4)) return run_lookup<T, e == 2 ? 2 : 1>(a, plan, sms, dev, st);
+    return run_lookup<T, 1>(a, plan, sms, dev, st);
 }
 
 tt_status dispatch(int dtype, const LookupArgs& a, const LookupPlan* plan, int sms, int dev, cudaStream_t st) {
-    const int e = esize(dtype);
-    const bool vec = a.D * e % 16 == 0 && aligned(a.in, 16) && aligned(a.out, 16) && a.in_ld * e % 16 == 0 && a.out_ld * e % 16 == 0;
-    if (dtype == TT_F32) return run_lookup<float>(a, vec, plan, sms, dev, st);
-    if (dtype == TT_BF16) return run_lookup<__nv_bfloat16>(a, vec, plan, sms, dev, st);
-    return run_lookup<__half>(a, vec, plan, sms, dev, st);
+    if (dtype == TT_F32) return run_lookup<float>(a, plan, sms, dev, st);
+    if (dtype == TT_BF16) return run_lookup<__nv_bfloat16>(a, plan, sms, dev, st);
+    return run_lookup<__half>(a, plan, sms, dev, st);
 }
 
 }  // namespace

@@ -1,5 +1,5 @@
-// tt_units.cuh -- rows of the three types read and written a unit at a time: 16 bytes, or one
-// element where rows do not begin on 16-byte boundaries.
+// tt_units.cuh -- rows of the three types read and written a unit at a time: 16 bytes, or fewer where
+// rows do not begin on 16-byte boundaries, down to one element.
 #pragma once
 
 #include <type_traits>
@@ -8,53 +8,64 @@
 
 namespace ttemb {
 
+// The raw unit of VEC elements: 16, 8 or 4 bytes, or one element.
+template <int BYTES>
+struct RawBytes;
+template <>
+struct RawBytes<16> {
+    using type = uint4;
+};
+template <>
+struct RawBytes<8> {
+    using type = uint2;
+};
+template <>
+struct RawBytes<4> {
+    using type = uint32_t;
+};
 template <class T, int VEC>
-__device__ __forceinline__ void unpack_unit(const uint4& u, float (&v)[VEC]) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if constexpr (sizeof(T) == 4) {
-            v[i] = __uint_as_float(w[i]);
-        } else if constexpr (std::is_same<T, __half>::value) {
-            const float2 f = unpack_f16(w[i]);
-            v[2 * i] = f.x;
-            v[2 * i + 1] = f.y;
-        } else {
-            v[2 * i] = __uint_as_float(w[i] << 16);
-            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-        }
-    }
-}
+struct RawOf {
+    using type = typename RawBytes<VEC * (int)sizeof(T)>::type;
+};
+template <class T>
+struct RawOf<T, 1> {
+    using type = T;
+};
 template <class T, int VEC>
-__device__ __forceinline__ uint4 pack_unit(const float (&v)[VEC]) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if constexpr (sizeof(T) == 4)
-            w[i] = __float_as_uint(v[i]);
-        else
-            w[i] = pack16(v[2 * i], v[2 * i + 1], !std::is_same<T, __half>::value);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-// The raw unit: 16 bytes, or one element.
-template <class T, int VEC>
-using Raw = typename std::conditional<VEC == 1, T, uint4>::type;
+using Raw = typename RawOf<T, VEC>::type;
 
 template <class T, int VEC>
 __device__ __forceinline__ Raw<T, VEC> raw_zero() {
-    if constexpr (VEC == 1)
+    if constexpr (VEC == 1) {
         return T(0.f);
-    else
-        return make_uint4(0, 0, 0, 0);
+    } else {
+        Raw<T, VEC> r;
+        uint32_t* w = reinterpret_cast<uint32_t*>(&r);
+#pragma unroll
+        for (int i = 0; i < VEC * (int)sizeof(T) / 4; ++i) w[i] = 0;
+        return r;
+    }
 }
 template <class T, int VEC>
 __device__ __forceinline__ void unpack(const Raw<T, VEC>& r, float (&v)[VEC]) {
-    if constexpr (VEC == 1)
+    if constexpr (VEC == 1) {
         v[0] = to_f32(r);
-    else
-        unpack_unit<T, VEC>(r, v);
+    } else {
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(&r);
+#pragma unroll
+        for (int i = 0; i < VEC * (int)sizeof(T) / 4; ++i) {
+            if constexpr (sizeof(T) == 4) {
+                v[i] = __uint_as_float(w[i]);
+            } else if constexpr (std::is_same<T, __half>::value) {
+                const float2 f = unpack_f16(w[i]);
+                v[2 * i] = f.x;
+                v[2 * i + 1] = f.y;
+            } else {
+                v[2 * i] = __uint_as_float(w[i] << 16);
+                v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+            }
+        }
+    }
 }
 template <class T>
 __device__ __forceinline__ T from_f32(float x) {
@@ -67,10 +78,20 @@ __device__ __forceinline__ T from_f32(float x) {
 }
 template <class T, int VEC>
 __device__ __forceinline__ Raw<T, VEC> pack(const float (&v)[VEC]) {
-    if constexpr (VEC == 1)
+    if constexpr (VEC == 1) {
         return from_f32<T>(v[0]);
-    else
-        return pack_unit<T, VEC>(v);
+    } else {
+        Raw<T, VEC> r;
+        uint32_t* w = reinterpret_cast<uint32_t*>(&r);
+#pragma unroll
+        for (int i = 0; i < VEC * (int)sizeof(T) / 4; ++i) {
+            if constexpr (sizeof(T) == 4)
+                w[i] = __float_as_uint(v[i]);
+            else
+                w[i] = pack16(v[2 * i], v[2 * i + 1], !std::is_same<T, __half>::value);
+        }
+        return r;
+    }
 }
 template <class T, int VEC>
 __device__ __forceinline__ Raw<T, VEC>* unit_at(T* p, int64_t row, int64_t stride, int u) {
@@ -91,6 +112,7 @@ inline int pow2_at_least(int64_t x, int most) {
 }
 
 // A kernel that begins before the one ahead of it in the stream has ended, and waits for it in pdl_wait.
+// Not for a call's first: the one ahead of that is another call's, whose outputs may be its inputs.
 template <class... Params, class... Args>
 bool launch_ahead(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t st, Args... args) {
     cudaLaunchConfig_t cfg = {};

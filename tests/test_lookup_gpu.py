@@ -20,7 +20,8 @@ U = {torch.float32: 2.0 ** -24, torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 **
 TINY = {torch.float32: 2.0 ** -150, torch.bfloat16: 2.0 ** -134, torch.float16: 2.0 ** -25}
 # lookups, table, width: no lookups, one, a block's, few and sorted (from 1,025 on), one digit and two and three
 SIZES = [(0, 5, 8), (1, 1, 1), (2, 3, 5), (7, 120, 8), (8, 120, 3), (64, 50, 257), (1000, 70, 64), (1024, 4000, 40), (1025, 4000, 40),
-         (3000, 2048, 33), (2049, 2049, 64), (5000, 100, 520), (20000, 70000, 16), (4097, 5000000, 8), (40000, 300, 2)]
+         (3000, 2048, 33), (2049, 2049, 64), (5000, 100, 520), (20000, 70000, 16), (4097, 5000000, 8), (40000, 300, 2),
+         (90, 5000, 38), (1500, 900, 38), (300, 2000, 2031), (2500, 9000, 102), (12000, 3000, 34)]
 
 
 def gen(seed):
@@ -152,7 +153,7 @@ def test_strides(n, dtype):
     ids = popular(n, v, 13)
     want, grad = w[ids], tt.tt_emb_lookup_backward(g, ids, v)
     apart = ids.repeat_interleave(2)[::2]
-    for pad, at in ((8, 0), (13, 1), (8, 8)):
+    for pad, at in ((8, 0), (13, 1), (8, 8), (4, 4), (2, 2), (6, 0)):
         ww = torch.full((v, d + pad), float("nan"), dtype=dtype, device="cuda")
         ww[:, at:at + d] = w
         gg = torch.full((n, d + pad), float("nan"), dtype=dtype, device="cuda")
