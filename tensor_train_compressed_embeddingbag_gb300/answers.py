@@ -153,9 +153,8 @@ def tt_emb_preference_forward(logp: torch.Tensor, reference: Optional[torch.Tens
             _refuse(TT_ERR_SHAPE, "the number of sequences must be even: the chosen ones, then the rejected ones")
         n = tt_emb_answers_workspace(a.tokens, count)
         ws = torch.empty(n, dtype=torch.uint8, device=device) if n else None
-        pairs = count // 2
-        loss, margins, rewards, counts = torch.empty(3 * count, dtype=torch.float32, device=device).split((pairs, pairs, count, count))
-        counts = counts.view(torch.int32)
+        loss, rewards = torch.empty(count // 2, dtype=torch.float32, device=device), torch.empty(count, dtype=torch.float32, device=device)
+        margins, counts = torch.empty_like(loss), torch.empty(count, dtype=torch.int32, device=device)
         st = _c("tt_emb_preference_forward")(ctypes.byref(a), ctypes.byref(how), loss.data_ptr(), margins.data_ptr(), rewards.data_ptr(),
                                              counts.data_ptr(), _err_word(err, device), ws.data_ptr() if n else None, n, _stream_now(device.index))
         if st:
@@ -199,8 +198,8 @@ def tt_emb_policy_forward(logp: torch.Tensor, old_logp: torch.Tensor, advantages
         how, more = _policy(old_logp, advantages, logp, count, clip, dual_clip, kl, kl_weight, level, per_token)
         n = tt_emb_answers_workspace(a.tokens, count)
         ws = torch.empty(n, dtype=torch.uint8, device=device) if n else None
-        loss, kl_out, log_ratio, counts, clipped = torch.empty((5, count), dtype=torch.float32, device=device).unbind(0)
-        counts, clipped = counts.view(torch.int32), clipped.view(torch.int32)
+        loss, counts = torch.empty(count, dtype=torch.float32, device=device), torch.empty(count, dtype=torch.int32, device=device)
+        kl_out, log_ratio, clipped = torch.empty_like(loss), torch.empty_like(loss), torch.empty_like(counts)
         st = _c("tt_emb_policy_forward")(ctypes.byref(a), ctypes.byref(how), loss.data_ptr(), kl_out.data_ptr(), log_ratio.data_ptr(),
                                          counts.data_ptr(), clipped.data_ptr(), _err_word(err, device), ws.data_ptr() if n else None, n,
                                          _stream_now(device.index))
