@@ -33,6 +33,7 @@ constexpr int kFoldChunks = 32;        // up to so many chunks a scatter sums th
 constexpr int kDigitBits = 11;
 constexpr int kMaxPasses = 3;
 constexpr int kZeroRows = 2048;        // most table rows of a block that writes zeros
+constexpr int64_t kSmallTable = 1 << 20;  // bytes: a table that few lookups' own launch clears (beyond, a launch ahead of it, 16 bytes at a time)
 constexpr int kChunkSlots = 4096;      // sorted positions staged by a block
 constexpr int kInFlight = 8;
 
@@ -557,7 +558,7 @@ __global__ void __launch_bounds__(kLkThreads) k_lookup_join(const __grid_constan
     if (u < a.units) put_unit<T, VEC>(a, key, u, s);
 }
 
-// Few lookups: a block per lookup and slice of `lanes` units.
+// Few lookups: a block per lookup and slice of `lanes` units, then (small tables) blocks that write zeros.
 template <class T, int VEC>
 __global__ void __launch_bounds__(kLkThreads) k_lookup_few(const __grid_constant__ LookupArgs a) {
     pdl_launch_dependents();
@@ -565,6 +566,7 @@ __global__ void __launch_bounds__(kLkThreads) k_lookup_few(const __grid_constant
     __shared__ union {
         int list[kSmallRows];
         float part[kLkThreads * VEC];
+        uint8_t named[kZeroRows];
     } s;
     __shared__ int sh[kLkThreads / 32];
     const int N = (int)a.N;
@@ -575,6 +577,19 @@ __global__ void __launch_bounds__(kLkThreads) k_lookup_few(const __grid_constant
         ids[n] = in && id != a.pad ? (int)id : -1;
     }
     __syncthreads();
+    if (blockIdx.x >= a.sum_blocks) {
+        const int64_t r0 = (blockIdx.x - a.sum_blocks) * a.zero_rows;
+        const int rows = (int)min((int64_t)a.zero_rows, a.V - r0);
+        for (int r = threadIdx.x; r < rows; r += kLkThreads) s.named[r] = 0;
+        __syncthreads();
+        for (int n = threadIdx.x; n < N; n += kLkThreads) {
+            const int64_t r = (int64_t)ids[n] - r0;
+            if (ids[n] >= 0 && r >= 0 && r < rows) s.named[r] = 1;
+        }
+        __syncthreads();
+        zero_rows<T, VEC>(a, s.named, r0, rows);
+        return;
+    }
     const int n0 = (int)(blockIdx.x / a.slices), slice = (int)(blockIdx.x - (int64_t)n0 * a.slices);
     const int id = ids[n0];
     if (id < 0) return;
@@ -731,13 +746,19 @@ tt_status backward_launch(LookupArgs a, const LookupPlan& p, const int64_t* ids,
     int extra;
     if (!p.sorted) {
         set_units(&a, VEC, 64);
-        const ZeroRows z = take(rows * row_bytes, &extra);
-        const dim3 grid((unsigned)(a.N * a.slices));
-        if (extra) k_lookup_zero<<<extra, 512, 0, st>>>(z);
-        else if (a.N) k_lookup_few<T, VEC><<<grid, kLkThreads, 0, st>>>(a);  // a call's first launch waits for what ran before
-        if (cudaGetLastError() != cudaSuccess) return TT_ERR_CUDA;
-        if (!extra || a.N == 0) return TT_OK;
-        return launch_ahead(k_lookup_few<T, VEC>, grid, kLkThreads, 0, st, a) ? TT_OK : TT_ERR_CUDA;
+        a.sum_blocks = a.N * a.slices;
+        if (rows * row_bytes > kSmallTable) {
+            const ZeroRows z = take(rows * row_bytes, &extra);
+            k_lookup_zero<<<extra, 512, 0, st>>>(z);
+            if (cudaGetLastError() != cudaSuccess) return TT_ERR_CUDA;
+            if (a.N == 0) return TT_OK;
+            return launch_ahead(k_lookup_few<T, VEC>, dim3((unsigned)a.sum_blocks), kLkThreads, 0, st, a) ? TT_OK : TT_ERR_CUDA;
+        }
+        a.zero_rows = (int)std::max<int64_t>(1, std::min<int64_t>(kZeroRows, 8192 / row_bytes));
+        const int64_t blocks = a.sum_blocks + (rows + a.zero_rows - 1) / a.zero_rows;
+        if (blocks == 0) return TT_OK;
+        k_lookup_few<T, VEC><<<(unsigned)blocks, kLkThreads, 0, st>>>(a);  // a call's first launch waits for what ran before
+        return cudaGetLastError() == cudaSuccess ? TT_OK : TT_ERR_CUDA;
     }
     SortArgs s{};
     s.ids = ids;
