@@ -14,9 +14,9 @@
 // empty where a sequence begins there or none is).  A warp takes a piece, four tokens a
 // lane and step; pieces of one sequence are joined in their order, so results repeat.
 //
-// Measured: 1,024 x 8,192 tokens, k3, an advantage each: sums 28 us (143 MB, 5.1 TB/s), numbers of the sequences 5, gradient
-// 27; issue slots are some 60% busy, of 85 instructions a token a third the clipped term's.  1,024 pairs, 4.2 M packed
-// tokens: 23 us both ways (54 MB), bound by the way through a piece (its offsets, its first loads, its last votes), not by bytes.
+// Measured: 1,024 x 8,192 tokens, k3, an advantage each: 60 us both ways.  Under a profiler sums 30 us (143 MB; issue slots 65%
+// and memory 62% busy, 90 instructions a token), numbers of the sequences 6, gradient 30 (55%, 66%, 77).  1,024 pairs, 4.2 M
+// packed tokens: 23 us both ways where 55 MB take 8; which part of the way through a piece bounds it was not measured.
 #include <cmath>
 
 #include "tt_units.cuh"

@@ -17,6 +17,10 @@
 //
 // Few lookups are not sorted: a block per lookup and column slice looks through all ids,
 // leaves if an earlier lookup has the same, and else sums those that have it.
+//
+// Measured: 16,384 of 131,072 x 4096 bf16, forward: 40 us (269 MB, 6.7 TB/s).  65,521 of 50,001 x 2048 bf16: 160 us both
+// ways (947 MB, 5.9 TB/s), of which the sort's three launches, which keep few multiprocessors busy, some 19.  10,240 of 1,000,000 x 64
+// fp32: 54 us both ways, where the 256 MB of zeros alone need 38.  8 of 120 x 8: 5.5 us both ways.
 #include <algorithm>
 
 #include "tt_units.cuh"

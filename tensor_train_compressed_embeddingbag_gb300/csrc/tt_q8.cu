@@ -9,12 +9,15 @@
 // accumulation gives the exact integer for up to 1,024 columns.  Longer rows are added up in such
 // ranges as int32 in registers.
 //
-// The table stays in 8 bits until it is on the chip: TMA brings 128 rows x 128 columns of codes, four
-// warps turn them into f16 (one byte permutation puts a code, made unsigned, into the mantissa of 1024; one
+// The table stays in 8 bits until it is on the chip: TMA brings 128 rows x 128 columns of codes, one or two
+// sets of four warps turn them into f16 (one byte permutation puts a code, made unsigned, into the mantissa of 1024; one
 // packed subtraction leaves it) and write them to tensor memory, from where the MMA takes its A
 // operand.  The codes of x, few against the table's, are f16 in memory from the start and come by TMA as
 // the B operand.  So the accumulator's rows are table rows and its columns rows of x, and a
 // warp that stores 32 lanes of a column writes 128 consecutive bytes of a row of scores.
+//
+// Measured, rows of x by the table, quantizing included: 2048 x 131072 x 2048 707 to 720 us (1,530 to 1,555 TFLOP/s), 192 x 131072
+// x 4096 159 (1,294 TFLOP/s), 33 x 131072 x 4096 105 (5.3 TB/s), 1 x 131072 x 4096 95 (5.6 TB/s), 33 x 50001 x 1000 25.
 #include <algorithm>
 
 #include "tt_q8_pipe.cuh"
