@@ -103,9 +103,10 @@ def tt_emb_lookup_backward(grad_out: torch.Tensor, ids: torch.Tensor, vocab: int
 class _LookupFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, weight, ids, scale, padding_idx, err):
+        out = tt_emb_lookup_forward(weight, ids, scale, err)
         ctx.save_for_backward(ids)
         ctx.vocab, ctx.scale, ctx.padding_idx = weight.shape[0], scale, padding_idx
-        return tt_emb_lookup_forward(weight, ids, scale, err)
+        return out
 
     @staticmethod
     @torch.autograd.function.once_differentiable

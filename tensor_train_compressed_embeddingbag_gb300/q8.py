@@ -71,10 +71,12 @@ class Q8Table:
     """An 8-bit copy of a dense table: ``Q8Table(weight).scores(x)``, float32 [..., vocab]."""
 
     def __init__(self, weight: torch.Tensor):
+        self.codes, self.scales = tt_emb_q8_quantize(weight.detach() if isinstance(weight, torch.Tensor) else weight)
         self.vocab, self.dim = weight.shape
-        self.codes, self.scales = tt_emb_q8_quantize(weight.detach())
 
     def scores(self, x: torch.Tensor, err: Optional[torch.Tensor] = None) -> torch.Tensor:
+        if not isinstance(x, torch.Tensor):
+            _refuse(TT_ERR_ARG, "x must be a tensor")
         if x.dim() < 1 or x.shape[-1] != self.dim:
             _refuse(TT_ERR_SHAPE, f"x has shape {tuple(x.shape)}, expected [..., {self.dim}]")
         return tt_emb_q8_scores(x.reshape(-1, x.shape[-1]), self.codes, self.scales, err=err).reshape(*x.shape[:-1], self.vocab)

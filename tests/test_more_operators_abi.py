@@ -270,3 +270,18 @@ def test_wrong_8_bit_tables(here):
     for width in (33, 41, 48):
         _refused(s, served.scores, torch.zeros((2, width)))
     _refused(s, served.scores, torch.zeros(()))
+
+
+def test_what_is_no_table_is_refused_as_such(here):
+    ids = torch.zeros(4, dtype=torch.int64)
+    for bad in (None, [[1.0]], torch.zeros(2, 3)):
+        _refused(tt.TT_ERR_ARG, tt.vocab_embedding, ids, bad)
+        _refused(tt.TT_ERR_ARG, tt.Q8Table, bad)
+    _refused(tt.TT_ERR_SHAPE, tt.vocab_embedding, ids, cuda(8))
+    _refused(tt.TT_ERR_SHAPE, tt.vocab_embedding, ids, cuda(2, 3, 4))
+    _refused(tt.TT_ERR_SHAPE, tt.Q8Table, cuda(8))
+    _refused(tt.TT_ERR_SHAPE, tt.Q8Table, cuda(2, 3, 4))
+    served = tt.Q8Table.__new__(tt.Q8Table)
+    served.vocab, served.dim, served.codes, served.scales = 5, 40, None, None
+    for bad in (None, [1.0] * 40):
+        _refused(tt.TT_ERR_ARG, served.scores, bad)
