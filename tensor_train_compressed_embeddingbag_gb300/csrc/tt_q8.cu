@@ -101,6 +101,45 @@ __device__ __forceinline__ void more_registers() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// The block's barriers, and how the roles of tt_q8_pipe.cuh use them.
+template <int BN>
+struct Q8Barriers {
+    using S = Q8Pipe<BN>;
+    uint64_t cfull[S::kCStages], cempty[S::kCStages], xfull[S::kXStages], xempty[S::kXStages];
+    uint64_t turned[S::kAStages], used[S::kAStages], accfull[2], accempty[2], drain;
+    template <Q8Bar B>
+    __device__ __forceinline__ uint64_t* at(uint32_t place) {
+        if constexpr (B == kCfull) return &cfull[place];
+        if constexpr (B == kCempty) return &cempty[place];
+        if constexpr (B == kXfull) return &xfull[place];
+        if constexpr (B == kXempty) return &xempty[place];
+        if constexpr (B == kTurned) return &turned[place];
+        if constexpr (B == kUsed) return &used[place];
+        if constexpr (B == kAccFull) return &accfull[place];
+        if constexpr (B == kAccEmpty) return &accempty[place];
+    }
+};
+template <int BN>
+struct Q8Roles {
+    Q8Barriers<BN>& bars;
+    uint64_t wait_ns;
+    volatile int* gave_up;
+    bool lead;
+    template <Q8Bar B>
+    __device__ __forceinline__ bool wait(uint32_t place, uint32_t parity) {
+        return head_wait(bars.template at<B>(place), parity, wait_ns, gave_up);
+    }
+    template <Q8Bar B>
+    __device__ __forceinline__ void arrive(uint32_t place) {
+        __syncwarp();
+        if (lead) mbar_arrive(bars.template at<B>(place));
+    }
+    template <Q8Bar B>
+    __device__ __forceinline__ void commit(uint32_t place) {
+        mma_commit(bars.template at<B>(place), lead);
+    }
+};
+
 // A unit is 128 table rows x BN rows of x; the tiles of x go fastest, so blocks that run together
 // share table rows.
 template <int BN>
@@ -111,33 +150,34 @@ __global__ void __launch_bounds__(Q8Shape<BN>::kThreads, Q8Shape<BN>::kBlocks)
     constexpr int kOutWarp = 4 + 4 * S::kSets;
     constexpr int kRangeSteps = kQ8Range / kQ8K;
     extern __shared__ uint8_t raw[];
-    __shared__ uint64_t cfull[S::kCStages], cempty[S::kCStages], xfull[S::kXStages], xempty[S::kXStages];
-    __shared__ uint64_t turned[S::kAStages], used[S::kAStages], accfull[2], accempty[2], drain;
+    __shared__ Q8Barriers<BN> bars;
     __shared__ uint32_t tmem_slot;
     __shared__ int gave_up_s;
+    __shared__ volatile uint32_t taken[4 * S::kSets][32];  // never read
     volatile int* gave_up = &gave_up_s;
     const uint32_t xbase = (smem_addr(raw) + 1023u) & ~1023u, cbase = xbase + S::kXStages * S::kX;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const bool lead = lane == 0;
+    Q8Roles<BN> roles{bars, a.wait_ns, gave_up, lead};
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::kCStages; ++i) {
-            mbar_init(&cfull[i], 1);
-            mbar_init(&cempty[i], 4);  // the codes are in registers
+            mbar_init(&bars.cfull[i], 1);
+            mbar_init(&bars.cempty[i], 4);  // the warps of a set: their codes are in registers
         }
         for (int i = 0; i < S::kXStages; ++i) {
-            mbar_init(&xfull[i], 1);
-            mbar_init(&xempty[i], 1);  // the step's MMAs are done
+            mbar_init(&bars.xfull[i], 1);
+            mbar_init(&bars.xempty[i], 1);
         }
         for (int i = 0; i < S::kAStages; ++i) {
-            mbar_init(&turned[i], 4);  // codes are in tensor memory, rows of x in shared memory
-            mbar_init(&used[i], 1);    // the step's MMAs are done
+            mbar_init(&bars.turned[i], 4);  // codes are in tensor memory, rows of x in shared memory
+            mbar_init(&bars.used[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&accfull[i], 1);
-            mbar_init(&accempty[i], 4 * S::kParts);
+            mbar_init(&bars.accfull[i], 1);
+            mbar_init(&bars.accempty[i], 4 * S::kParts);
         }
-        mbar_init(&drain, 1);
+        mbar_init(&bars.drain, 1);
         gave_up_s = 0;
     }
     if (warp == 2) tc_alloc(&tmem_slot, S::kTmem);
@@ -148,7 +188,7 @@ __global__ void __launch_bounds__(Q8Shape<BN>::kThreads, Q8Shape<BN>::kBlocks)
     const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
     // steps of this block's units, one behind the other
     const int64_t mine = a.units > blockIdx.x ? (a.units - 1 - blockIdx.x) / gridDim.x + 1 : 0, total = mine * a.chunks;
-    uint32_t it = 0;   // steps fed, turned or multiplied
+    uint32_t it = 0;   // steps fed or multiplied
     uint32_t acc = 0;  // accumulators filled or read
     bool ok = true;
 
@@ -161,23 +201,22 @@ __global__ void __launch_bounds__(Q8Shape<BN>::kThreads, Q8Shape<BN>::kBlocks)
                 const int v = (int)(u / a.mtiles), m = (int)(u - (int64_t)v * a.mtiles);
                 for (int c = 0; c < a.chunks; ++c, ++it) {
                     if (x) {
-                        const uint32_t st = it % S::kXStages, to = xbase + st * S::kX;
-                        ok = head_wait(&xempty[st], ((it / S::kXStages) & 1) ^ 1, a.wait_ns, gave_up);
-                        if (!ok) break;
-                        if (lead) {
-                            bulk_expect(&xfull[st], S::kX);
-                            tma_load2(to, &map_x, c * kQ8K, m * BN, &xfull[st]);
-                            tma_load2(to + S::kX / 2, &map_x, c * kQ8K + 64, m * BN, &xfull[st]);
-                        }
+                        ok = q8_feed_x<BN>(roles, it, [&](uint32_t st) {
+                            if (!lead) return;
+                            const uint32_t to = xbase + st * S::kX;
+                            bulk_expect(&bars.xfull[st], S::kX);
+                            tma_load2(to, &map_x, c * kQ8K, m * BN, &bars.xfull[st]);
+                            tma_load2(to + S::kX / 2, &map_x, c * kQ8K + 64, m * BN, &bars.xfull[st]);
+                        });
                     } else {
-                        const uint32_t st = it % S::kCStages;
-                        ok = head_wait(&cempty[st], ((it / S::kCStages) & 1) ^ 1, a.wait_ns, gave_up);
-                        if (!ok) break;
-                        if (lead) {
-                            bulk_expect(&cfull[st], S::kC);
-                            tma_load2(cbase + st * S::kC, &map_codes, c * kQ8K, v * 128, &cfull[st]);
-                        }
+                        ok = q8_feed_codes<BN>(roles, it, [&](uint32_t st) {
+                            if (!lead) return;
+                            tc_fence_smem();  // the set's loads from this place before the copy into it
+                            bulk_expect(&bars.cfull[st], S::kC);
+                            tma_load2(cbase + st * S::kC, &map_codes, c * kQ8K, v * 128, &bars.cfull[st]);
+                        });
                     }
+                    if (!ok) break;
                     __syncwarp();
                 }
             }
@@ -186,25 +225,14 @@ __global__ void __launch_bounds__(Q8Shape<BN>::kThreads, Q8Shape<BN>::kBlocks)
             const uint32_t db0 = desc_lo(xbase, kNoLbo);
             for (int64_t i = 0; ok && i < mine; ++i) {
                 for (int r0 = 0; ok && r0 < a.chunks; r0 += kRangeSteps, ++acc) {
-                    const uint32_t buf = acc & 1, d = tmem + buf * BN;
-                    ok = head_wait(&accempty[buf], ((acc >> 1) & 1) ^ 1, a.wait_ns, gave_up);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const int steps = min(kRangeSteps, a.chunks - r0);
-                    for (int c = 0; c < steps; ++c, ++it) {
-                        const uint32_t st = it % S::kXStages, ta = it % S::kAStages;
-                        // (the warps that turned the codes have waited for the rows of x)
-                        ok = head_wait(&turned[ta], (it / S::kAStages) & 1, a.wait_ns, gave_up);
-                        if (!ok) break;
+                    // (the warps that turned the codes have waited for the rows of x)
+                    ok = q8_multiply<BN>(roles, acc, it, min(kRangeSteps, a.chunks - r0), [&](uint32_t buf, uint32_t st, uint32_t ta, int c) {
                         tc_fence_after();
-                        const uint32_t pa = tmem + S::kACol + ta * kQ8ACols, db = db0 + st * (S::kX >> 4);
+                        const uint32_t d = tmem + buf * BN, pa = tmem + S::kACol + ta * kQ8ACols, db = db0 + st * (S::kX >> 4);
 #pragma unroll
                         for (int k = 0; k < kQ8K / 16; ++k)
                             mma_f16_ta(d, pa + k * 8, db + (k >= 4 ? (S::kX / 2) >> 4 : 0) + (k & 3) * (32 >> 4), idesc, c > 0 || k > 0, lead);
-                        mma_commit(&used[ta], lead);
-                        mma_commit(&xempty[st], lead);
-                    }
-                    if (ok) mma_commit(&accfull[buf], lead);
+                    });
                 }
             }
         }
@@ -213,15 +241,8 @@ __global__ void __launch_bounds__(Q8Shape<BN>::kThreads, Q8Shape<BN>::kBlocks)
         const uint32_t set = (warp - 4) >> 2;
         const int quad = warp & 3, r = quad * 32 + lane;
         const uint32_t to = tmem + ((uint32_t)(quad * 32) << 16) + S::kACol;
-        for (int64_t i = set; i < total; i += S::kSets) {
-            it = (uint32_t)i;
-            const uint32_t cs = it % S::kCStages, st = it % S::kXStages, ta = it % S::kAStages;
-            ok = head_wait(&cfull[cs], (it / S::kCStages) & 1, a.wait_ns, gave_up);
-            if (!ok) break;
-            const uint32_t row = cbase + cs * S::kC + r * 128;
+        for (int64_t i = set; ok && i < total; i += S::kSets) {
             uint4 w[8];
-#pragma unroll
-            for (int x = 0; x < 8; ++x) w[x] = lds16(row + ((x ^ (r & 7)) << 4));  // 128-byte swizzle
             uint32_t q[4][16];
             auto turn = [&](int h) {
 #pragma unroll
@@ -235,24 +256,29 @@ __global__ void __launch_bounds__(Q8Shape<BN>::kThreads, Q8Shape<BN>::kBlocks)
             };
             // where there are registers, the codes are f16 before the MMAs that still read this place are done
             constexpr bool kEarly = S::kBlocks == 1;
-            if (kEarly)
+            ok = q8_turn<BN>(
+                roles, (uint32_t)i,
+                [&](uint32_t cs) {
+                    const uint32_t row = cbase + cs * S::kC + r * 128;
 #pragma unroll
-                for (int h = 0; h < 4; ++h) turn(h);
-            __syncwarp();
-            if (lead) mbar_arrive(&cempty[cs]);
-            ok = head_wait(&xfull[st], (it / S::kXStages) & 1, a.wait_ns, gave_up) &&
-                 head_wait(&used[ta], ((it / S::kAStages) & 1) ^ 1, a.wait_ns, gave_up);
-            if (!ok) break;
-            tc_fence_after();
+                    for (int x = 0; x < 8; ++x) w[x] = lds16(row + ((x ^ (r & 7)) << 4));  // 128-byte swizzle
+                    if (kEarly)
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
-                if (!kEarly) turn(h);
-                tm_st16(to + ta * kQ8ACols + h * 16, q[h]);
-            }
-            tm_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lead) mbar_arrive(&turned[ta]);
+                        for (int h = 0; h < 4; ++h) turn(h);
+                },
+                // A store of a word that takes one of each load: it waits for all of them, and the arrival, behind it, for it.  (Writing
+                // the codes to tensor memory first would do too: 2048 x 131072 x 2048 830 us, 723 this way.)
+                [&]() { taken[warp - 4][lane] = w[0].x ^ w[1].x ^ w[2].x ^ w[3].x ^ w[4].x ^ w[5].x ^ w[6].x ^ w[7].x; },
+                [&](uint32_t ta) {
+                    tc_fence_after();
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        if (!kEarly) turn(h);
+                        tm_st16(to + ta * kQ8ACols + h * 16, q[h]);
+                    }
+                    tm_wait_st();
+                    tc_fence_before();
+                });
         }
     } else {
         if (S::kShift) more_registers<kQ8RegsOut>();
@@ -269,26 +295,22 @@ __global__ void __launch_bounds__(Q8Shape<BN>::kThreads, Q8Shape<BN>::kBlocks)
             for (int h = 0; h < kCols; h += 32) xs[h / 32] = h + lane < rows ? __ldg(a.xscale + m0 + h + lane) : 0.f;
             int sum[kCols];
 #pragma unroll 1
-            for (int r0 = 0; ok && r0 < a.chunks; r0 += kRangeSteps, ++acc) {
-                const uint32_t buf = acc & 1;
-                ok = head_wait(&accfull[buf], (acc >> 1) & 1, a.wait_ns, gave_up);
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t t0 = tmem + buf * BN + ((uint32_t)(quad * 32) << 16) + part * kCols;
+            for (int r0 = 0; ok && r0 < a.chunks; r0 += kRangeSteps, ++acc)
+                ok = q8_take_sums<BN>(roles, acc, [&](uint32_t buf) {
+                    tc_fence_after();
+                    const uint32_t t0 = tmem + buf * BN + ((uint32_t)(quad * 32) << 16) + part * kCols;
 #pragma unroll
-                for (int h = 0; h < kCols; h += 16) {
-                    float x[16];
-                    tm_read16(t0 + h, x);
+                    for (int h = 0; h < kCols; h += 16) {
+                        float x[16];
+                        tm_read16(t0 + h, x);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const int y = __float2int_rn(x[j]);
-                        sum[h + j] = r0 == 0 ? y : sum[h + j] + y;
+                        for (int j = 0; j < 16; ++j) {
+                            const int y = __float2int_rn(x[j]);
+                            sum[h + j] = r0 == 0 ? y : sum[h + j] + y;
+                        }
                     }
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lead) mbar_arrive(&accempty[buf]);
-            }
+                    tc_fence_before();
+                });
             if (!ok) break;
             float* o = a.out + m0 * a.V + v;
 #pragma unroll
@@ -307,12 +329,12 @@ __global__ void __launch_bounds__(Q8Shape<BN>::kThreads, Q8Shape<BN>::kBlocks)
     __syncthreads();
     if (*gave_up) {  // no copy and no MMA may still be running when the block ends
         if (threadIdx.x == 0)
-            for (uint32_t i = it > S::kXStages ? it - S::kXStages : 0; i < it; ++i) head_drain(&xfull[i % S::kXStages], (i / S::kXStages) & 1);
+            for (uint32_t i = it > S::kXStages ? it - S::kXStages : 0; i < it; ++i) head_drain(&bars.xfull[i % S::kXStages], (i / S::kXStages) & 1);
         if (threadIdx.x == 96)
-            for (uint32_t i = it > S::kCStages ? it - S::kCStages : 0; i < it; ++i) head_drain(&cfull[i % S::kCStages], (i / S::kCStages) & 1);
+            for (uint32_t i = it > S::kCStages ? it - S::kCStages : 0; i < it; ++i) head_drain(&bars.cfull[i % S::kCStages], (i / S::kCStages) & 1);
         if (threadIdx.x == 32) {
-            mma_commit(&drain, true);
-            head_drain(&drain, 0);
+            mma_commit(&bars.drain, true);
+            head_drain(&bars.drain, 0);
         }
         __syncwarp();
         __syncthreads();
