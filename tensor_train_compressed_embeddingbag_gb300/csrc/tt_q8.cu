@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(Q8Shape<BN>::kThreads, Q8Shape<BN>::kBlocks)
             mbar_init(&bars.xempty[i], 1);
         }
         for (int i = 0; i < S::kAStages; ++i) {
-            mbar_init(&bars.turned[i], 4);  // codes are in tensor memory, rows of x in shared memory
+            mbar_init(&bars.turned[i], 4);  // a set's codes are in tensor memory
             mbar_init(&bars.used[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -225,7 +225,6 @@ __global__ void __launch_bounds__(Q8Shape<BN>::kThreads, Q8Shape<BN>::kBlocks)
             const uint32_t db0 = desc_lo(xbase, kNoLbo);
             for (int64_t i = 0; ok && i < mine; ++i) {
                 for (int r0 = 0; ok && r0 < a.chunks; r0 += kRangeSteps, ++acc) {
-                    // (the warps that turned the codes have waited for the rows of x)
                     ok = q8_multiply<BN>(roles, acc, it, min(kRangeSteps, a.chunks - r0), [&](uint32_t buf, uint32_t st, uint32_t ta, int c) {
                         tc_fence_after();
                         const uint32_t d = tmem + buf * BN, pa = tmem + S::kACol + ta * kQ8ACols, db = db0 + st * (S::kX >> 4);

@@ -3,8 +3,8 @@
 //
 //   codes     a step's table codes in shared memory.  kCfull: they are there; waited for by the set of warps that
 //             turns the step's codes.  kCempty: they are in that set's registers; waited for by the codes' TMA warp
-//   x         its rows of x.  kXfull: they are there; waited for by the same set, which tells the MMA warp by
-//             kTurned.  kXempty: the step's MMAs are done; waited for by x's TMA warp
+//   x         its rows of x.  kXfull: they are there; waited for by the MMA warp itself, so that no third party stands between
+//             the copy and the MMAs that read it.  kXempty: the step's MMAs are done; waited for by x's TMA warp
 //   tensor    its codes as f16 in tensor memory.  kTurned: they are there; waited for by the MMA warp.  kUsed: the step's
 //             MMAs are done; waited for by the set of the next step in this place
 //   sums      a range's accumulator, two of them.  kAccFull: its MMAs are done; waited for by the warps that write scores.
@@ -15,8 +15,9 @@
 //
 // A waiter tells phases apart by their parity only, so whoever waits for a phase has to have seen the
 // one before.  Sets take steps in turn: with two of them a place has to belong to one set, whose waits then see
-// every phase of it.  So the rings have even numbers of places (with three places for x, set 0 could ask for
-// step 6 while step 3, which set 1 waits for, is still on its way, and take step 0's phase for its own).
+// every phase of it.  So the rings of codes and of tensor memory have even numbers of places (with three places, set 0
+// could ask for step 6 while step 3, which set 1 waits for, is still on its way, and take step 0's phase for its own).  x's
+// ring has one waiter, which sees every phase; its places are even in number too.
 #pragma once
 
 #include <cstdint>
@@ -64,12 +65,12 @@ TT_Q8_ROLE bool q8_feed_x(P& p, uint32_t it, Load load) {
 // registers; put(place): writes them, as f16, to tensor memory, and returns when they are there.
 template <int BN, class P, class Read, class Held, class Put>
 TT_Q8_ROLE bool q8_turn(P& p, uint32_t it, Read read, Held held, Put put) {
-    constexpr uint32_t c = Q8Pipe<BN>::kCStages, x = Q8Pipe<BN>::kXStages, a = Q8Pipe<BN>::kAStages;
+    constexpr uint32_t c = Q8Pipe<BN>::kCStages, a = Q8Pipe<BN>::kAStages;
     if (!p.template wait<kCfull>(it % c, (it / c) & 1)) return false;
     read(it % c);
     held();
     p.template arrive<kCempty>(it % c);
-    if (!p.template wait<kXfull>(it % x, (it / x) & 1) || !p.template wait<kUsed>(it % a, ((it / a) & 1) ^ 1)) return false;
+    if (!p.template wait<kUsed>(it % a, ((it / a) & 1) ^ 1)) return false;
     put(it % a);
     p.template arrive<kTurned>(it % a);
     return true;
@@ -81,7 +82,7 @@ TT_Q8_ROLE bool q8_multiply(P& p, uint32_t acc, uint32_t& it, int steps, Issue i
     constexpr uint32_t x = Q8Pipe<BN>::kXStages, a = Q8Pipe<BN>::kAStages;
     if (!p.template wait<kAccEmpty>(acc & 1, ((acc >> 1) & 1) ^ 1)) return false;
     for (int c = 0; c < steps; ++c, ++it) {
-        if (!p.template wait<kTurned>(it % a, (it / a) & 1)) return false;
+        if (!p.template wait<kXfull>(it % x, (it / x) & 1) || !p.template wait<kTurned>(it % a, (it / a) & 1)) return false;
         issue(acc & 1, it % x, it % a, c);
         p.template commit<kUsed>(it % a);
         p.template commit<kXempty>(it % x);

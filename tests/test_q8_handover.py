@@ -196,8 +196,8 @@ def test_every_order_finds_what_it_means(written, bn):
 
 @pytest.mark.parametrize("bn", [32, 64, 128, 192])
 def test_the_walk_finds_places_that_are_let_go_too_early(written, bn):
-    """The walk itself: a place of codes that is free when its loads are issued, rows of x and
-    accumulators that nobody waits for."""
+    """The walk itself: a place of codes that is free when its loads are issued, codes written without a wait for the MMAs that
+    read their place, rows of x and accumulators that nobody waits for."""
     programs, sets = written(bn)
 
     def changed(role, change):
@@ -210,5 +210,20 @@ def test_the_walk_finds_places_that_are_let_go_too_early(written, bn):
         return lambda p: [e for e in p if not (e[0] == 0 and BARS[e[1]] in bars)]
 
     assert found(changed("set", early), sets, bn, "loads codes")
-    assert found(changed("set", without("xfull")), sets, bn, "rows of x")
+    assert found(changed("set", without("used")), sets, bn, "over those that MMAs still read", "find codes")
+    assert found(changed("mma", without("xfull")), sets, bn, "rows of x")
     assert found(changed("mma", without("accempty")), sets, bn, "sums of range")
+
+
+@pytest.mark.parametrize("bn", [32, 64, 128, 192])
+def test_the_warp_that_issues_mmas_has_waited_for_what_they_read(written, bn):
+    """For the copy of the step's rows of x and for its codes, itself: what a copy brings is there for those who waited
+    for the copy's own barrier."""
+    p = written(bn)[0]["mma"]
+    since = set()
+    for i, (kind, what, place, more) in enumerate(p):
+        if kind == 0:
+            since.add((BARS[what], place))
+        elif kind == 3 and p[i - 1][0] != 3:
+            assert {("xfull", place), ("turned", more)} <= since
+            since.clear()
