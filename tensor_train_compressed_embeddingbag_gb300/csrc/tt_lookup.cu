@@ -421,7 +421,7 @@ __device__ int first_not_below(const uint32_t* keys, int m, uint32_t key) {
     int lo = 0, hi = m;  // the answer is in [lo, hi]
     while (lo < hi) {
         const int step = (hi - lo + 31) / 32, at = lo + lane * step;
-        const unsigned below = __ballot_sync(0xffffffffu, at < hi && __ldg(keys + at) < key);
+        const unsigned below = __ballot_sync(0xffffffffu, at < hi && keys[at] < key);
         const int n = __popc(below);  // sorted: the first n probes
         if (n == 0) return lo;
         hi = min(hi, lo + n * step);

@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(Q8Shape<BN>::kThreads, Q8Shape<BN>::kBlocks)
             const float s = v < a.V ? __ldg(a.scale + v) : 0.f;
             float xs[(kCols + 31) / 32];
 #pragma unroll
-            for (int h = 0; h < kCols; h += 32) xs[h / 32] = h + lane < rows ? __ldg(a.xscale + m0 + h + lane) : 0.f;
+            for (int h = 0; h < kCols; h += 32) xs[h / 32] = h + lane < rows ? a.xscale[m0 + h + lane] : 0.f;
             int sum[kCols];
 #pragma unroll 1
             for (int r0 = 0; ok && r0 < a.chunks; r0 += kRangeSteps, ++acc)
@@ -463,7 +463,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) k_q8_few(const __grid_constant
             for (int h = 0; h < 2; ++h) {
                 uint4 x[NT];
 #pragma unroll
-                for (int n = 0; n < NT; ++n) x[n] = __ldg(a.x + ((int64_t)(j * NT + n) * 2 + h) * 32 + lane);
+                for (int n = 0; n < NT; ++n) x[n] = a.x[((int64_t)(j * NT + n) * 2 + h) * 32 + lane];
 #pragma unroll
                 for (int w = 0; w < 2; ++w) {
                     uint32_t lo[4], hi[4];

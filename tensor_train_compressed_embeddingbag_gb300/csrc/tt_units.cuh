@@ -111,7 +111,8 @@ inline int pow2_at_least(int64_t x, int most) {
     return p;
 }
 
-// A kernel that begins before the one ahead of it in the stream has ended, and waits for it in pdl_wait.
+// A kernel that begins before the one ahead of it in the stream has ended, and waits for it in pdl_wait.  What that one
+// writes it reads by ordinary loads: __ldg promises data that nobody writes while the kernel is there.
 // Not for a call's first: the one ahead of that is another call's, whose outputs may be its inputs.
 template <class... Params, class... Args>
 bool launch_ahead(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t st, Args... args) {
