@@ -119,6 +119,8 @@ def _answers(logp, reference, mask, offsets, average, read_logp=True):
 def _preference(beta, kind, label_smoothing, margin):
     if kind not in _KINDS:
         _refuse(TT_ERR_ARG, f"kind must be one of {', '.join(_KINDS)}")
+    if kind != "sigmoid" and 0.0 <= label_smoothing < 1.0:
+        label_smoothing = 0.0  # the other losses have no labels; the C ABI takes only 0 for them
     return _Preference(_KINDS[kind], beta, label_smoothing, margin)
 
 
@@ -143,7 +145,7 @@ def tt_emb_preference_forward(logp: torch.Tensor, reference: Optional[torch.Tens
     """(loss [pairs], margins [pairs], rewards [2 pairs], counts int32 [2 pairs]) of sequences 0 .. pairs - 1 chosen
     over sequences pairs .. 2 pairs - 1.
 
-    kind: "sigmoid", "hinge" or "squared".  average: rewards by the mean over an answer's tokens, not their
+    kind: "sigmoid", "hinge" or "squared".  label_smoothing, in [0, 1), belongs to the sigmoid loss; the others do not use it.  average: rewards by the mean over an answer's tokens, not their
     sum.  Malformed offsets set 2 in err (int32, optional)."""
     device = _device(logp)
     with _on(stream, device):
@@ -271,6 +273,7 @@ def preference_loss(logp: torch.Tensor, reference: Optional[torch.Tensor] = None
                     margin: float = 0.0, average: bool = False, reduction: str = "mean", err: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Loss of pairs of answers (the first half of the sequences chosen over the second), differentiable in logp.
 
+    label_smoothing, in [0, 1), belongs to kind "sigmoid"; "hinge" and "squared" do not use it.
     reduction 'mean' divides by the pairs that count: those with a token that counts in either answer (0 when
     there are none); pairs without one are in no sum."""
     _check_reduction(reduction)
