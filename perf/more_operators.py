@@ -240,8 +240,7 @@ def run(state):
     if s["op"] == "q8":
         return {"scores": tt.tt_emb_q8_scores(s["x"], s["codes"], s["scales"])}
     if s["op"] == "preference":
-        how = dict(mask=s["mask"], offsets=s["offsets"], beta=BETA, kind=s["kind"], average=s["average"],
-                   label_smoothing=s["smoothing"] if s["kind"] == "sigmoid" else 0.0)
+        how = dict(mask=s["mask"], offsets=s["offsets"], beta=BETA, kind=s["kind"], label_smoothing=s["smoothing"], average=s["average"])
         loss, margins, rewards, counts = tt.tt_emb_preference_forward(s["logp"], s["reference"], **how)
         out = {"loss": loss, "margins": margins, "rewards": rewards, "counts": counts}
         if s["train"]:
