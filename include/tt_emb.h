@@ -594,7 +594,7 @@ tt_status tt_emb_lookup_backward(const tt_lookup* lookup, const void* grad_out_d
  *   k[t] with y = reference[t] - logp[t]:  -y (TT_KL_1), y^2 / 2 (TT_KL_2), exp(y) - 1 - y (TT_KL_3)
  *   kl[s] = share[s] sum_t m[t] k[t],  loss[s] = share[s] sum_t m[t] L[t] + kl_weight kl[s]
  *   clipped[s]: how many tokens that count have a ratio beyond the bound that holds for the
- *   sign of their A.  Whether it is is decided on x itself (d is not rounded for that).
+ *   sign of their A (none without a sign: 0, NaN).  Whether it is is decided on x itself (d is not rounded for that).
  *   No reference: k = 0.  TT_POLICY_SEQUENCE takes an advantage per sequence.
  *   (J. Schulman et al., "Proximal Policy Optimization Algorithms", 2017; D. Ye et al., "Mastering
  *   Complex Control in MOBA Games with Deep Reinforcement Learning", 2020: dual_clip; C. Zheng et al.,

@@ -221,7 +221,7 @@ __device__ __forceinline__ void clip_terms(const AnswerArgs& a, const float (&ad
 #pragma unroll
     for (int j = 0; j < COUNT; ++j) {
         const float r = ratio_of(d[j]), bound = adv[j] > 0.f ? a.high : (c[j].over ? a.low : a.dual);
-        c[j].over = (c[j].over || dual[j]) && adv[j] != 0.f;
+        c[j].over = (c[j].over || dual[j]) && fabsf(adv[j]) > 0.f;  // no side without a sign: 0 (no bound), NaN (which stays in L and its slope)
         c[j].term = -adv[j] * (c[j].over ? bound : r);
         c[j].slope = c[j].over ? 0.f : c[j].term;
     }
