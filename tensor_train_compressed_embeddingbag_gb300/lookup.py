@@ -73,7 +73,7 @@ def tt_emb_lookup_backward(grad_out: torch.Tensor, ids: torch.Tensor, vocab: int
                            grad_weight: Optional[torch.Tensor] = None, err: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The gradient [vocab, dim] of a table, of grad_out's type: scale times the sums of the rows of grad_out by id.
 
-    Rows with padding_idx give none.  With grad_weight (rows of contiguous elements) the sums are added to
+    Rows with padding_idx give none (below 0: every id counts).  With grad_weight (rows of contiguous elements) the sums are added to
     the rows of it that ids name, the others stay as they are: a tied table's other gradient, or the table itself for
     a step of gradient descent (scale times minus the learning rate)."""
     device = _device(grad_out, "grad_out")
@@ -119,9 +119,15 @@ def vocab_embedding(ids: torch.Tensor, weight: torch.Tensor, scale: float = 1.0,
                     err: Optional[torch.Tensor] = None) -> torch.Tensor:
     """scale * weight[ids], [..., dim] for ids int64 [...], differentiable in weight [vocab, dim].
 
-    padding_idx: an id that gives no gradient (looked up as any other).  err: as in tt_emb_lookup_forward."""
+    padding_idx: an id that gives no gradient (looked up as any other), counted from the table's end if below 0; None: none.
+    err: as in tt_emb_lookup_forward."""
     if not isinstance(ids, torch.Tensor):
         _refuse(TT_ERR_ARG, "ids must be an int64 tensor")
     pad = -1 if padding_idx is None else int(padding_idx)
+    if padding_idx is not None and pad < 0:
+        _device(weight, "weight")
+        if weight.dim() != 2 or pad < -weight.shape[0]:
+            _refuse(TT_ERR_SHAPE, "padding_idx must not be below -vocab, of weight [vocab, dim]")
+        pad += weight.shape[0]
     out = _LookupFunction.apply(weight, ids.reshape(-1), float(scale), pad, err)
     return out.reshape(*ids.shape, weight.shape[1])
