@@ -105,14 +105,14 @@ class _LookupFunction(torch.autograd.Function):
     def forward(ctx, weight, ids, scale, padding_idx, err):
         out = tt_emb_lookup_forward(weight, ids, scale, err)
         ctx.save_for_backward(ids)
-        ctx.vocab, ctx.scale, ctx.padding_idx = weight.shape[0], scale, padding_idx
+        ctx.vocab, ctx.scale, ctx.padding_idx, ctx.err = weight.shape[0], scale, padding_idx, err
         return out
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, grad):
         ids, = ctx.saved_tensors
-        return tt_emb_lookup_backward(grad, ids, ctx.vocab, ctx.scale, ctx.padding_idx), None, None, None, None
+        return tt_emb_lookup_backward(grad, ids, ctx.vocab, ctx.scale, ctx.padding_idx, err=ctx.err), None, None, None, None
 
 
 def vocab_embedding(ids: torch.Tensor, weight: torch.Tensor, scale: float = 1.0, padding_idx: Optional[int] = None,
@@ -120,7 +120,7 @@ def vocab_embedding(ids: torch.Tensor, weight: torch.Tensor, scale: float = 1.0,
     """scale * weight[ids], [..., dim] for ids int64 [...], differentiable in weight [vocab, dim].
 
     padding_idx: an id that gives no gradient (looked up as any other), counted from the table's end if below 0; None: none.
-    err: as in tt_emb_lookup_forward."""
+    err (int32, optional): what the forward pass finds is ORed into it, and later what the backward pass does."""
     if not isinstance(ids, torch.Tensor):
         _refuse(TT_ERR_ARG, "ids must be an int64 tensor")
     pad = -1 if padding_idx is None else int(padding_idx)

@@ -22,3 +22,19 @@ def test_padding_below_zero_counts_from_the_end(n):
         w.grad = None
     tt.vocab_embedding(ids, w).backward(g)
     check_grad(w.grad, g, ids, 1.0)
+
+
+@pytest.mark.parametrize("n", [60, 3000])
+def test_the_backward_pass_reports_ids_outside_the_table(n):
+    """Into the caller's error word, as the head's losses do."""
+    w = torch.randn((40, 24), generator=gen(33), device="cuda").requires_grad_()
+    ids = popular(n, 40, 34)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    tt.vocab_embedding(ids, w, err=err).sum().backward()
+    assert err.item() == 0
+    ids[7] = 40
+    out = tt.vocab_embedding(ids, w, err=err)
+    assert err.item() == 1
+    err.zero_()
+    out.sum().backward()
+    assert err.item() == 1
