@@ -721,11 +721,16 @@ tt_status scores_launch(Q8Args a, const int8_t* codes, const __half* x, int D, i
     a.units = (a.V + 127) / 128 * a.mtiles;
     if (!allow_smem<Q8Tag<BN>>(k_q8_scores<BN>, dev, Q8Shape<BN>::kSmem)) return TT_ERR_CUDA;
     if (Q8Shape<BN>::kShift) {  // the warps that take registers wait for them: they have to be there
-        static const bool enough = [] {
-            cudaFuncAttributes f;
-            return cudaFuncGetAttributes(&f, k_q8_scores<BN>) == cudaSuccess && f.numRegs >= kQ8Regs;
-        }();
-        if (!enough) return TT_ERR_CUDA;
+        static std::atomic<bool> enough{false};
+        cudaFuncAttributes f;
+        if (!enough.load(std::memory_order_relaxed)) {
+            if (cudaFuncGetAttributes(&f, k_q8_scores<BN>) != cudaSuccess) {
+                cudaGetLastError();
+                return TT_ERR_CUDA;
+            }
+            if (f.numRegs < kQ8Regs) return TT_ERR_CUDA;
+            enough.store(true, std::memory_order_relaxed);
+        }
     }
     return launch_ahead(k_q8_scores<BN>, dim3((unsigned)std::min<int64_t>(a.units, sms * Q8Shape<BN>::kBlocks)), Q8Shape<BN>::kThreads, Q8Shape<BN>::kSmem, st, mc, mx, a) ? TT_OK
                                                                                                                                          : TT_ERR_CUDA;

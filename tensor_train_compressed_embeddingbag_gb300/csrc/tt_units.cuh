@@ -126,7 +126,9 @@ bool launch_ahead(void (*kernel)(Params...), dim3 grid, int threads, size_t smem
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess;
+    if (cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess) return true;
+    cudaGetLastError();  // this call's failure, not the next one's
+    return false;
 }
 
 }  // namespace ttemb
