@@ -571,9 +571,11 @@ tt_status tt_emb_lookup_backward(const tt_lookup* lookup, const void* grad_out_d
  * offsets, tokens / sequences tokens each (a padded batch).  A token whose mask is 0 does not
  * count, whatever its numbers are.  m[t] is 1 for a token that counts, n[s] how many do.
  * share[s] = 1 / n[s] if `average`, else 1 (a sequence without a token that counts: 0 for
- * every sum).  Sums over tokens are taken in two floats each (some 48 bits).  Both need a workspace (256-byte
- * aligned, nothing kept between calls) of tt_emb_answers_workspace bytes (-1: refused sizes) forward;
- * 0 bytes: none, NULL will do.
+ * every sum).  A token's terms are fp32 numbers; those of four neighbours (tokens 4 i .. 4 i + 3) are added in fp32, and
+ * such groups in two floats (some 48 bits), whatever their number: of sums of differences at most
+ * 3 x 2^-24 of the sum of their magnitudes is lost, and nothing of terms that are exact in groups of four.
+ * Both need a workspace (256-byte aligned, nothing kept between calls) of tt_emb_answers_workspace bytes (-1: refused
+ * sizes) forward; 0 bytes: none, NULL will do.
  *
  * Preference.  Sequences 0 .. P - 1 are chosen over sequences P .. 2 P - 1, pair by pair:
  *   rewards[s] = beta share[s] sum_t m[t] (logp[t] - reference[t])     (no reference: 0)

@@ -52,3 +52,60 @@ def test_advantages_that_are_not_a_number(level, per_token, dual_clip):
                 assert got["clipped"][row] == clean["clipped"][row] - int(over)
             else:
                 assert got["clipped"][row] == 0
+
+
+def exact_sums(shape, packed, seed):
+    """Values of tokens whose sums are known to the last bit: 2^24 and its negative, far apart, and between them multiples
+    of 2^-12 below 2^-9; a group of four has one of the large ones or four small, so its fp32 sum is exact, and the total of the
+    small ones keeps within 24 bits.  A sum in one fp32 number loses them next to 2^24."""
+    sequences, length = shape
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    x = torch.randint(1, 8, shape, generator=g, device="cuda").float() * 2.0 ** -12
+    x[:, :4] = 0
+    x[:, -4:] = 0
+    x[:, 1], x[:, -2] = 2.0 ** 24, -2.0 ** 24
+    want = x.double().sum(1)
+    assert torch.equal(want.float().double(), want)
+    offsets = torch.arange(sequences + 1, device="cuda") * length if packed else None
+    return (x.reshape(-1) if packed else x), want, offsets
+
+
+# one block, pieces of 256 to 2,048 tokens, a sequence of hundreds of pieces; the lengths are multiples of 4
+@pytest.mark.parametrize("shape", [(2, 400), (2, 4096), (4, 20000), (2, 400000), (200, 8192), (2, 3_000_000)])
+@pytest.mark.parametrize("packed", [False, True])
+def test_sums_keep_what_one_float_would_lose(shape, packed):
+    """2^24 and 2^-12 are 36 bits apart; the sums keep some 48."""
+    x, want, offsets = exact_sums(shape, packed, 50)
+    zero, n = torch.zeros_like(x), shape[1]
+    rewards = tt.tt_emb_preference_forward(x, zero, offsets=offsets, beta=1.0)[2]
+    assert torch.equal(rewards.double(), want)
+    # the difference of log probabilities: its mean; inverse counts are good to some 2^-48
+    none = torch.zeros(shape[0], device="cuda")
+    log_ratio = tt.tt_emb_policy_forward(x, zero, none, offsets=offsets, average=False, level="sequence")[2]
+    assert ((log_ratio.double() - want / n).abs() <= (2.0 ** -24 + 2.0 ** -40) * want / n).all()
+    # the divergence (k1: log probability less reference), and the clipped term: minus the advantages where all ratios are 1
+    loss, kl = tt.tt_emb_policy_forward(zero, zero, -x, reference=-x, offsets=offsets, average=False, kl="k1", kl_weight=1.0, per_token=True)[:2]
+    assert torch.equal(kl.double(), want)
+    assert ((loss.double() - 2 * want).abs() <= 2.0 ** -24 * 2 * want).all()
+
+
+@pytest.mark.parametrize("size", [(8, 777, True), (6, 6 * 257, False), (10, 100003, True), (2, 3000001, True), (64, 64 * 5000, False)])
+def test_sums_of_differences(size):
+    """A difference is rounded once (2^-24 of it), then twice within its group of four (2^-24 of partial sums that are at most the group's
+    magnitudes); the two floats and joins below 2^-40 of the magnitudes; the result is rounded to fp32."""
+    s = inputs(*size, seed=51)
+    got, pol = run_preference(s, beta=1.0), run_policy(s, kl="k1", average=False)
+    m = s["mask"].reshape(-1)
+    n = m.numel()
+    of = (torch.searchsorted(s["offsets"], torch.arange(n, device="cuda"), right=True) - 1 if size[2] else torch.arange(n, device="cuda") // (n // size[0]))[m]
+
+    def check(value, x, over=1.0):
+        x = x.reshape(-1)[m]
+        total, size_ = (torch.zeros(size[0], dtype=torch.float64, device="cuda").index_add_(0, of, y) / over for y in (x, x.abs()))
+        assert ((value.double() - total).abs() <= (3 * 2.0 ** -24 + 2.0 ** -40) * size_ + 1.01 * 2.0 ** -24 * total.abs()).all()
+
+    d = {k: s[k].double() for k in ("logp", "reference", "old")}
+    check(got["rewards"], d["logp"] - d["reference"])
+    check(pol["log_ratio"], d["logp"] - d["old"], pol["counts"].clamp(min=1).double())
+    check(pol["kl"], d["logp"] - d["reference"])
