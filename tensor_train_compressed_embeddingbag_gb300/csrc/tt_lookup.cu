@@ -596,7 +596,10 @@ __global__ void __launch_bounds__(kLkThreads) k_lookup_few(const __grid_constant
     }
     const int n0 = (int)(blockIdx.x / a.slices), slice = (int)(blockIdx.x - (int64_t)n0 * a.slices);
     const int id = ids[n0];
-    if (id < 0) return;
+    if (id < 0) {  // the zeros have to be there when this launch has ended, whatever the ids are
+        pdl_wait();
+        return;
+    }
     // the lookups with this id, in order; a thread's are consecutive
     constexpr int kPer = kSmallRows / kLkThreads;
     int mine[kPer], found = 0;
@@ -609,7 +612,7 @@ __global__ void __launch_bounds__(kLkThreads) k_lookup_few(const __grid_constant
             mine[found++] = n;
         }
     }
-    if (__syncthreads_or(earlier)) return;
+    if (__syncthreads_or(earlier)) return;  // (the block of the id's first lookup waits)
     int count;
     const int at = block_scan<kLkThreads / 32>(found, sh, &count);
     for (int i = 0; i < found; ++i) s.list[at + i] = mine[i];

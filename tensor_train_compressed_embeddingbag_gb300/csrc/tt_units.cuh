@@ -112,7 +112,9 @@ inline int pow2_at_least(int64_t x, int most) {
 }
 
 // A kernel that begins before the one ahead of it in the stream has ended, and waits for it in pdl_wait.  What that one
-// writes it reads by ordinary loads: __ldg promises data that nobody writes while the kernel is there.
+// writes it reads by ordinary loads: __ldg promises data that nobody writes while the kernel is there.  Some block of it has to
+// wait whatever the data are: the launch behind waits for this one only, so one that ended without waiting would let it run
+// beside the launch ahead.
 // Not for a call's first: the one ahead of that is another call's, whose outputs may be its inputs.
 template <class... Params, class... Args>
 bool launch_ahead(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t st, Args... args) {

@@ -65,3 +65,16 @@ def test_sorts_of_more_than_32_chunks(n, v, d, dtype):
     into = torch.randn((v, d), generator=gen(39), device="cuda").to(dtype)
     old = into.clone()
     check_grad(tt.tt_emb_lookup_backward(g, ids, v, padding_idx=pad, grad_weight=into), g, ids, 1.0, pad, old)
+
+
+@pytest.mark.parametrize("n", [1, 37, 1024])
+def test_a_large_gradient_that_no_id_names(n):
+    """All padding, or all outside: zeros, which the launch of the sums may not overtake."""
+    v, d = 1_000_003, 64
+    g = torch.randn((n, d), generator=gen(40), device="cuda")
+    ids = torch.full((n,), 9, device="cuda")
+    for i in range(30):
+        held = torch.full((v, d), float("nan"), device="cuda")
+        del held  # its memory is the gradient's next
+        got = tt.tt_emb_lookup_backward(g, ids, v, padding_idx=9) if i % 2 else tt.tt_emb_lookup_backward(g, ids + v, v)
+        assert not got.flip(0).any()
