@@ -629,15 +629,19 @@ tt_status answer_sizes(int64_t tokens, int64_t sequences) {
 }
 
 // log2 of the tokens of a piece.  Short ones spread over the device, and even out what its last blocks have to do; long
-// ones cost fewer sums to write and join.  The policy loss has more to do per token: 8.4 M tokens in pieces of 512 60 us, of 1,024 62,
-// of 2,048 69; preference of 4.2 M in pieces of 512 25, of 1,024 23.
+// ones cost fewer sums to write and join.  The policy loss has more to do per token.  Both ways, us, in pieces of 256 / 512 / 1,024 / 2,048 tokens:
+//   policy       2^20 tokens 14 / 14 / 16 / 14, 2^21 22 / 21 / 21 / 25, 2^22 37 / 34 / 35 / 35, 2^23 63 / 60 / 62 / 69, 2^25 226 / 197 / 197 / 202
+//   preference   2^20 9.7 / 8.3 / 8.5 / 8.2, 2^21 13 / 11 / 10 / 11, 2^22 23 / 20 / 20 / 17, 2^23 38 / 32 / 29 / 32, 2^25 134 / 109 / 101 / 103
+// The limits keep within a tenth of the best of these, the preference loss's within a fifth (2^20, 2^22).
 int piece_shift(int64_t tokens, bool policy) {
     int k = kPieceMin;
     while (k < kPieceMax && tokens >> k > (policy ? 16384 : 4096)) ++k;
     return k;
 }
 
-// One launch, and no workspace, while a single block's reading costs less than a second launch.
+// One launch, and no workspace: a forward call of 8,192 tokens takes 25 us of host time (policy; preference 21), in two launches 30 (26).
+// The device's time is below that: both ways, policy, 512 tokens 6.2 us (6.3 in two launches), 2,048 7.9 (7.2), 8,192 11.8 (7.2); preference 4.8 (5.5),
+// 5.2 (5.5), 7.2 (5.8).
 bool in_one_block(int64_t tokens, int64_t pieces) { return tokens <= kOneTokens && pieces <= kOnePieces; }
 
 tt_status fill_answers(const tt_answers* in, bool policy, AnswerArgs* a) {

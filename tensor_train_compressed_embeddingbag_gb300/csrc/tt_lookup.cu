@@ -29,11 +29,16 @@ namespace ttemb {
 
 constexpr int kLkThreads = 256;
 constexpr int kLkRows = 4;             // rows of a thread in the forward pass
-constexpr int kSmallRows = 1024;       // lookups that are not sorted
+// Lookups that are not sorted.  Each of their blocks looks through all ids, a block for 64 units of columns, so the limit lies
+// lower for wide rows.  bf16 gradients of 50,001 rows, us, this way and sorted: 64 wide, 300 lookups 6 and 15, 1,024 10 and 17, 2,048 20 and
+// 20; 2048 wide, 300 39 and 40, 600 46 and 41, 1,024 56 and 41 (added to a gradient: 9 and 18, 16 and 18, 26 and 19).
+constexpr int kSmallRows = 1024;
 constexpr int kSortChunk = 2048;
 constexpr int kSortBlock = 512;
 constexpr int kSortW = kSortBlock / 32;
-constexpr int kFoldChunks = 32;        // up to so many chunks a scatter sums the histograms itself
+// Up to so many chunks a scatter sums the histograms itself.  Gradients of 50,001 x 256, us, so and by a launch of its own: 2 chunks 22 and
+// 25, 8 chunks 27 and 27, 16 chunks 34 and 30, 32 chunks 39 and 36, 64 chunks 52 and 42.
+constexpr int kFoldChunks = 32;
 constexpr int kDigitBits = 11;
 constexpr int kMaxPasses = 3;
 constexpr int kZeroRows = 2048;        // most table rows of a block that writes zeros

@@ -16,8 +16,9 @@
 // the B operand.  So the accumulator's rows are table rows and its columns rows of x, and a
 // warp that stores 32 lanes of a column writes 128 consecutive bytes of a row of scores.
 //
-// Measured, rows of x by the table, quantizing included: 2048 x 131072 x 2048 707 to 720 us (1,530 to 1,555 TFLOP/s), 192 x 131072
-// x 4096 159 (1,294 TFLOP/s), 33 x 131072 x 4096 105 (5.3 TB/s), 1 x 131072 x 4096 95 (5.6 TB/s), 33 x 50001 x 1000 25.
+// Measured, rows of x by the table, quantizing included: 2048 x 131072 x 2048 722 to 739 us (1,490 to 1,520 TFLOP/s), 192 x 131072
+// x 4096 168 (1,227 TFLOP/s), 128 x 131072 x 4096 127 (4.8 TB/s), 33 x 131072 x 4096 100 (5.5 TB/s), 1 x 131072 x 4096 97 (5.5 TB/s),
+// 33 x 50001 x 1000 25.
 #include <algorithm>
 
 #include "tt_q8_pipe.cuh"
@@ -33,7 +34,7 @@ constexpr int kQ8ACols = kQ8K / 2;  // tensor-memory columns of a step's codes
 // of the columns each).
 //
 // What bounds a narrow tile is the warp that issues the MMAs: a step costs it some 190 cycles of waiting, 60 for each
-// of the eight MMAs and 90 for each commit, whatever their width.  So up to 64 rows of x two blocks share a
+// of the eight MMAs and 90 for each commit, whatever their width (clock stamps, taken before it waited for the rows of x itself).  So up to 64 rows of x two blocks share a
 // multiprocessor, each with half of its shared and tensor memory.
 template <int BN>
 struct Q8Shape : Q8Pipe<BN> {
@@ -804,7 +805,9 @@ tt_status tt_emb_q8_scores(const void* x_dev, int64_t x_stride, int64_t rows, in
     a.out = out_dev;
     a.wait_ns = head_wait_limit();
     a.err = err_dev;
-    // the narrowest tile that holds the rows; beyond 192 the width that pads less
+    // The narrowest tile that holds the rows, 192 beyond.  By 60000 x 4096, us: 32 rows 52 (the next wider tile 54), 64 rows 59 (narrower 81,
+    // wider 76), 65 rows 71 (84, 92), 128 rows 78 (91, 95), 192 rows 98 (125), 384 rows 158 (174 in tiles of 128), 512 rows 206 (226).
+    // 193 to 256 rows would be quicker in two tiles of 128 (256 rows 125, 149 this way).
     if (rows <= 32) return scores_launch<32>(a, codes_dev, w.x, dim, sms, dev, st);
     if (rows <= 64) return scores_launch<64>(a, codes_dev, w.x, dim, sms, dev, st);
     if (rows <= 128) return scores_launch<128>(a, codes_dev, w.x, dim, sms, dev, st);
