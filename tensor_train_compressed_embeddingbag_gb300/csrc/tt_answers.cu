@@ -61,7 +61,7 @@ struct __align__(16) Sums {
 constexpr int64_t kSumsBytes = sizeof(Sums);
 static_assert(sizeof(Sums) == 32, "layout of the workspace");
 
-struct Threshold {  // a number in two pieces: hi + lo
+struct Two {  // a number in two pieces: hi + lo, lo at most half a unit of hi
     float hi, lo;
 };
 
@@ -84,8 +84,8 @@ struct AnswerArgs {
     // preference
     int kind;
     int64_t pairs;
-    float beta, smoothing;
-    double dbeta, dmargin;
+    Two beta, smoothing, rest;  // rest: 1 - smoothing
+    double dbeta, dmargin, inverse_beta;
     float* margins;
     float* rewards;
     const float* margins_in;
@@ -94,7 +94,7 @@ struct AnswerArgs {
     const float* adv;
     int per_token, sequence, kl;
     float low, high, dual;        // 1 - clip_low, 1 + clip_high, dual_clip
-    Threshold tlow, thigh, tdual;  // their logarithms
+    Two tlow, thigh, tdual;  // their logarithms
     float kl_weight;
     float* kl_out;
     float* log_ratio;
@@ -155,7 +155,7 @@ __device__ __forceinline__ Piece piece_of(const AnswerArgs& a, int64_t u, bool w
 }
 
 // x against t for x = p - q without the rounding of the difference: -1, 0, 1.
-__device__ __noinline__ int side_of(float p, float q, Threshold t) {
+__device__ __noinline__ int side_of(float p, float q, Two t) {
     const double x = (double)p - (double)q, y = (double)t.hi + (double)t.lo;
     return x > y ? 1 : (x < y ? -1 : 0);
 }
@@ -460,12 +460,89 @@ __device__ __forceinline__ double inverse_of(int n) {
     return fma(r, fma(-d, r, 1.0), r);
 }
 
-// dloss/dh of a pair.  In fp32, as the margin is that the forward call wrote: the rounding of h moves the slope of the sigmoid by at
-// most 2^-24 |h| of itself, and the functions' own errors are a few units more.
-__device__ __forceinline__ float pref_slope(const AnswerArgs& a, float h) {
-    if (a.kind == TT_PREF_HINGE) return h < 1.f ? -1.f : 0.f;
-    if (a.kind == TT_PREF_SQUARED) return 2.f * ((h - 0.5f) / a.beta) / a.beta;
-    return a.smoothing / (1.f + expf(-h)) - (1.f - a.smoothing) / (1.f + expf(h));
+// Arithmetic of a pair's few numbers in two floats, so that its loss and its tokens' gradient are rounded once (sums and products with
+// their exact errors: T. J. Dekker, "A floating-point technique for extending the available precision", 1971).  Written so that no
+// product is fused with what is added to it, where the sum's own rounding is asked for.
+__device__ __forceinline__ Two two_sum(float a, float b) {
+    const float s = __fadd_rn(a, b), c = __fadd_rn(s, -a);
+    return {s, __fadd_rn(__fadd_rn(a, -__fadd_rn(s, -c)), __fadd_rn(b, -c))};
+}
+__device__ __forceinline__ Two two_norm(float hi, float lo) {  // |lo| is far below |hi|
+    const float s = __fadd_rn(hi, lo);
+    return {s, __fadd_rn(lo, -__fadd_rn(s, -hi))};
+}
+__device__ __forceinline__ Two two_add(Two a, Two b) {
+    const Two s = two_sum(a.hi, b.hi);
+    return two_norm(s.hi, s.lo + (a.lo + b.lo));
+}
+__device__ __forceinline__ Two two_mul(Two a, Two b) {
+    const float p = __fmul_rn(a.hi, b.hi);
+    return two_norm(p, fmaf(a.hi, b.lo, fmaf(a.lo, b.hi, fmaf(a.hi, b.hi, -p))));
+}
+__device__ __forceinline__ Two two_div(Two a, Two b) {
+    const float q = a.hi / b.hi, r = fmaf(-q, b.lo, fmaf(-q, b.hi, a.hi) + a.lo);
+    return two_norm(q, r / b.hi);
+}
+
+// exp(x), x <= 0, to some 2^-26: with x = n log 2 + r it is 2^n (1 + r + r^2 (1/2 + ..)), of which only the last term is a plain fp32 number.
+__device__ Two two_exp(float x) {
+    if (!(x > -80.f)) return {expf(x), 0.f};
+    constexpr double kLn2 = 0.69314718055994531;
+    constexpr float kHi = (float)kLn2, kLo = (float)(kLn2 - (double)kHi);
+    const float n = rintf(x * kLog2e), p = __fmul_rn(n, kHi);
+    const Two d = two_sum(x, -p), r = two_norm(d.hi, d.lo - fmaf(n, kLo, fmaf(n, kHi, -p)));
+    const Two s = two_sum(1.f, r.hi), e = two_norm(s.hi, s.lo + (r.lo + series(r.hi) * r.hi));
+    const float scale = __int_as_float((127 + (int)n) << 23);
+    return {e.hi * scale, e.lo * scale};
+}
+// log(1 + e), 0 <= e <= 1, as good: its series, or a step of Newton's from the fp32 function.
+__device__ Two two_log1p(Two e) {
+    if (!(e.hi > 0.0625f)) {
+        float q = 1.f / 9.f;
+#pragma unroll
+        for (int k = 8; k >= 2; --k) q = fmaf(-q, e.hi, 1.f / (float)k);
+        const Two s = two_sum(e.hi, __fmul_rn(__fmul_rn(-q, e.hi), e.hi));
+        return two_norm(s.hi, s.lo + e.lo);
+    }
+    const float y = log1pf(e.hi);
+    const Two d = two_sum(1.f, e.hi), p = two_mul({d.hi, d.lo + e.lo}, two_exp(-y));
+    return two_norm(y, (p.hi - 1.f) + p.lo);
+}
+
+// sigma(h) and sigma(-h).
+__device__ void sigmoids(float h, Two& up, Two& down) {
+    const Two e = two_exp(-fabsf(h)), s = two_sum(1.f, e.hi), d = {s.hi, s.lo + e.lo};
+    const Two large = two_div({1.f, 0.f}, d), small = two_div(e, d);
+    up = h < 0.f ? small : large;
+    down = h < 0.f ? large : small;
+}
+__device__ __forceinline__ Two sigmoid_slope(const AnswerArgs& a, Two up, Two down) {
+    const Two d = two_mul(a.rest, down);
+    return two_add(two_mul(a.smoothing, up), {-d.hi, -d.lo});
+}
+
+// g beta dloss/dh / n of a pair, of the margin that the forward call wrote.
+__device__ float pref_weight(const AnswerArgs& a, float g, float h, int n) {
+    const Two count = two_sum((float)(n & ~4095), (float)(n & 4095));
+    Two v;
+    float plain;  // where a number is not finite, two pieces of it are not
+    if (a.kind == TT_PREF_HINGE) {
+        const float slope = h < 1.f ? -1.f : 0.f;
+        v = two_mul(a.beta, {slope, 0.f});
+        plain = slope * a.beta.hi;
+    } else if (a.kind == TT_PREF_SQUARED) {
+        const Two s = two_sum(h, -0.5f);
+        v = two_div({2.f * s.hi, 2.f * s.lo}, a.beta);
+        plain = 2.f * (h - 0.5f) / a.beta.hi;
+    } else {
+        Two up, down;
+        sigmoids(h, up, down);
+        const Two slope = sigmoid_slope(a, up, down);
+        v = two_mul(slope, a.beta);
+        plain = slope.hi * a.beta.hi;
+    }
+    v = two_div(two_mul(v, {g, 0.f}), count);
+    return isfinite(v.hi) ? v.hi : g * plain / (float)n;
 }
 
 // The numbers of pair u (preference: a half of the warp for each answer) or of sequences 2 u and 2 u + 1 (policy), by a warp.
@@ -498,18 +575,24 @@ __device__ void finish_two(const AnswerArgs& a, const Sums* part, int64_t u) {
         a.rewards[s] = (float)mine;
         a.counts_out[s] = t.count;
         if (half) return;
-        const float h = (float)(mine - other - a.dmargin);
-        float loss;  // of the rounded margin, which the backward call takes too, in fp32
+        const double margin = mine - other - a.dmargin;
+        const float h = (float)margin;
+        float loss;
         if (a.kind == TT_PREF_SIGMOID) {
-            const float soft = log1pf(expf(-fabsf(h)));  // log sigma(h) = min(h, 0) - soft
-            loss = (1.f - a.smoothing) * (soft - fminf(h, 0.f));
-            if (a.smoothing != 0.f) loss += a.smoothing * (soft + fmaxf(h, 0.f));
-            if (isnan(h)) loss = h;
+            // -log sigma(h) = log(1 + exp(-|h|)) + max(-h, 0); of h's first piece, and the slope times the second
+            if (isfinite(h)) {
+                Two up, down, s = two_log1p(two_exp(-fabsf(h)));
+                s = two_add(s, two_mul(h < 0.f ? a.rest : a.smoothing, {fabsf(h), 0.f}));
+                sigmoids(h, up, down);
+                loss = s.hi + fmaf(sigmoid_slope(a, up, down).hi, (float)(margin - (double)h), s.lo);
+            } else {
+                loss = isnan(h) ? h : (h < 0.f || a.smoothing.hi > 0.f ? INFINITY : 0.f);
+            }
         } else if (a.kind == TT_PREF_HINGE) {
-            loss = isnan(h) ? h : fmaxf(1.f - h, 0.f);
+            loss = isnan(h) ? h : (float)fmax(1.0 - margin, 0.0);
         } else {
-            const float v = (h - 0.5f) / a.beta;
-            loss = v * v;
+            const double v = margin - 0.5;
+            loss = (float)(v * a.inverse_beta * (v * a.inverse_beta));
         }
         a.loss[u] = loss;
         a.margins[u] = h;
@@ -580,7 +663,7 @@ __global__ void __launch_bounds__(kAnswerWarps * 32, kAnswerBlocks) k_answer_gra
         } else {
             const bool chosen = p.s < a.pairs;
             const int64_t pair = chosen ? p.s : p.s - a.pairs;
-            g = a.grad_loss[pair] * pref_slope(a, a.margins_in[pair]) * a.beta / (float)n;
+            g = pref_weight(a, a.grad_loss[pair], a.margins_in[pair], n);
             if (!chosen) g = -g;
         }
     }
@@ -664,6 +747,11 @@ tt_status fill_answers(const tt_answers* in, bool policy, AnswerArgs* a) {
     return TT_OK;
 }
 
+Two split(double x) {
+    const float hi = (float)x;
+    return {hi, (float)(x - hi)};
+}
+
 tt_status fill_preference(const tt_preference* how, AnswerArgs* a) {
     if (!how || how->kind < TT_PREF_SIGMOID || how->kind > TT_PREF_SQUARED) return TT_ERR_ARG;
     if (!(how->beta > 0.0 && how->beta <= 1e6) || !(how->label_smoothing >= 0.0 && how->label_smoothing < 1.0) || !std::isfinite(how->margin))
@@ -672,16 +760,13 @@ tt_status fill_preference(const tt_preference* how, AnswerArgs* a) {
     if (a->S % 2) return TT_ERR_SHAPE;
     a->kind = how->kind;
     a->pairs = a->S / 2;
-    a->beta = (float)how->beta;
+    a->beta = split(how->beta);
     a->dbeta = how->beta;
-    a->smoothing = (float)how->label_smoothing;
+    a->smoothing = split(how->label_smoothing);
+    a->rest = split(1.0 - how->label_smoothing);
     a->dmargin = how->margin;
+    a->inverse_beta = 1.0 / how->beta;
     return TT_OK;
-}
-
-Threshold split(double x) {
-    const float hi = (float)x;
-    return {hi, (float)(x - hi)};
 }
 
 tt_status fill_policy(const tt_policy* how, AnswerArgs* a) {
@@ -702,7 +787,7 @@ tt_status fill_policy(const tt_policy* how, AnswerArgs* a) {
     a->dual = (float)how->dual_clip;
     a->tlow = split(std::log1p(-how->clip_low));
     a->thigh = split(std::log1p(how->clip_high));
-    a->tdual = how->dual_clip > 0.0 ? split(std::log(how->dual_clip)) : Threshold{INFINITY, 0.f};
+    a->tdual = how->dual_clip > 0.0 ? split(std::log(how->dual_clip)) : Two{INFINITY, 0.f};
     a->kl_weight = (float)how->kl_weight;
     return TT_OK;
 }

@@ -109,3 +109,52 @@ def test_sums_of_differences(size):
     check(got["rewards"], d["logp"] - d["reference"])
     check(pol["log_ratio"], d["logp"] - d["old"], pol["counts"].clamp(min=1).double())
     check(pol["kl"], d["logp"] - d["reference"])
+
+
+@pytest.mark.parametrize("smoothing", [0.0, 0.1, 0.45])
+@pytest.mark.parametrize("kind", ["sigmoid", "hinge", "squared"])
+def test_pairs_are_rounded_once(kind, smoothing):
+    """Answers of one token, whose rewards are exact but for one product: the loss and the gradient of a pair.
+
+    Two floats keep what leads to them, but for one term of exp: some 2.5 roundings of a number that is at most a
+    fifteenth of the result (0.7 for the smallest), 2^-26, and for as much in the logarithm: 2^-25 with the result's own 2^-24
+    is a bound for both.  Where the two parts of a smoothed slope cancel, what they lose is of their own size.  The gradient is that
+    of the margin which the forward call gave."""
+    if kind != "sigmoid" and smoothing:
+        pytest.skip("one loss without labels")
+    n, beta = 20000, 0.1
+    g = torch.Generator(device="cuda")
+    g.manual_seed(52)
+    size = 10.0 ** torch.linspace(-6, 2.9, n, device="cuda")
+    h = size * torch.where(torch.rand((n,), generator=g, device="cuda") < 0.5, -1.0, 1.0)
+    logp = torch.cat([h, torch.zeros_like(h)])[:, None]
+    how = dict(beta=beta, kind=kind, label_smoothing=smoothing)
+    loss, margins, rewards, counts = tt.tt_emb_preference_forward(logp, **how)
+    x = beta * h.double()
+    assert ((margins.double() - x).abs() <= 1.001 * 2.0 ** -24 * x.abs()).all()
+    soft = torch.nn.functional.softplus
+    want = {"sigmoid": (1 - smoothing) * soft(-x, threshold=1000.0) + smoothing * soft(x, threshold=1000.0), "hinge": (1 - x).clamp(min=0),
+            "squared": ((x - 0.5) / beta) ** 2}[kind]
+    # (a difference from 1 or 1/2 of a product that is itself rounded to 2^-47: of the numbers' size)
+    assert ((loss.double() - want).abs() <= (2.0 ** -24 + 2.0 ** -25) * want + 2.0 ** -40 * (1 + x.abs()) / (beta if kind == "squared" else 1) ** 2 * (kind != "sigmoid")).all()
+    grad = torch.rand((n,), generator=g, device="cuda") + 0.5
+    got = tt.tt_emb_preference_backward(logp, margins, counts, grad, **how)[:, 0].double()
+    m = margins.double()
+    up, down = torch.sigmoid(m), torch.sigmoid(-m)
+    slope = {"sigmoid": smoothing * up - (1 - smoothing) * down, "hinge": -(m < 1).double(), "squared": 2 * (m - 0.5) / beta ** 2}[kind]
+    parts = (smoothing * up + (1 - smoothing) * down) if kind == "sigmoid" else slope.abs()
+    c = grad.double() * beta
+    off = c * (1.001 * 2.0 ** -24 * slope.abs() + 2.0 ** -25 * parts) + 2.0 ** -149
+    assert ((got[:n] - c * slope).abs() <= off).all() and torch.equal(got[n:], -got[:n])
+
+
+def test_gradients_of_long_answers_are_rounded_once():
+    """A share of one over a number of tokens that is no fp32 number, and a beta that is none."""
+    n = 16777217 + 2
+    logp = torch.zeros((2, n), device="cuda")
+    for beta in (0.1, 0.3, 7.7):
+        _, margins, _, counts = tt.tt_emb_preference_forward(logp, beta=beta, average=True)
+        assert counts.tolist() == [n, n]
+        got = tt.tt_emb_preference_backward(logp, margins, counts, torch.ones(1, device="cuda"), beta=beta, average=True)
+        want = -0.5 * beta / n
+        assert (got[0] == got[0, 0]).all() and abs(got[0, 0].item() - want) <= (2.0 ** -24 + 2.0 ** -40) * abs(want) and torch.equal(got[1], -got[0])
