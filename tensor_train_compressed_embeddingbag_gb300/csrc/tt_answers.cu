@@ -16,7 +16,7 @@
 //
 // Measured: 1,024 x 8,192 tokens, k3, an advantage each: 60 us both ways.  Under a profiler sums 30 us (143 MB; issue slots 65%
 // and memory 62% busy, 90 instructions a token), numbers of the sequences 6, gradient 30 (55%, 66%, 77).  1,024 pairs, 4.2 M
-// packed tokens: 23 us both ways where 55 MB take 8; which part of the way through a piece bounds it was not measured.
+// packed tokens: 25 us both ways where 55 MB take 8; which part of the way through a piece bounds it was not measured.
 #include <cmath>
 
 #include "tt_units.cuh"
