@@ -527,7 +527,7 @@ __device__ float pref_weight(const AnswerArgs& a, float g, float h, int n) {
     Two v;
     float plain;  // where a number is not finite, two pieces of it are not
     if (a.kind == TT_PREF_HINGE) {
-        const float slope = h < 1.f ? -1.f : 0.f;
+        const float slope = isnan(h) ? h : (h < 1.f ? -1.f : 0.f);  // a NaN stays in the gradient too
         v = two_mul(a.beta, {slope, 0.f});
         plain = slope * a.beta.hi;
     } else if (a.kind == TT_PREF_SQUARED) {

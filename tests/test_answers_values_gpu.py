@@ -158,3 +158,18 @@ def test_gradients_of_long_answers_are_rounded_once():
         got = tt.tt_emb_preference_backward(logp, margins, counts, torch.ones(1, device="cuda"), beta=beta, average=True)
         want = -0.5 * beta / n
         assert (got[0] == got[0, 0]).all() and abs(got[0, 0].item() - want) <= (2.0 ** -24 + 2.0 ** -40) * abs(want) and torch.equal(got[1], -got[0])
+
+
+@pytest.mark.parametrize("kind", ["sigmoid", "hinge", "squared"])
+def test_margins_that_are_not_a_number(kind):
+    """The loss and the gradient of such a pair are NaN, others are as they were."""
+    s = inputs(8, 8 * 30, False, seed=53)
+    s["mask"][:] = True
+    s["grad"] = s["grad"].abs() + 0.5
+    clean = run_preference(s, kind=kind)
+    s["logp"][5, 7] = float("nan")  # of the second pair
+    got = run_preference(s, kind=kind)
+    assert got["loss"].isnan().tolist() == [False, True, False, False] and got["margins"][1].isnan()
+    hit = torch.zeros((8, 30), dtype=torch.bool, device="cuda")
+    hit[1], hit[5] = True, True
+    assert torch.equal(got["grad"].isnan(), hit) and torch.equal(got["grad"][~hit], clean["grad"][~hit])
